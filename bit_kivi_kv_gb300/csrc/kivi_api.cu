@@ -81,6 +81,8 @@ kivi_status ensure_device(kivi_cache_t c) {
 // the new token takes (a fused append-and-decode leaves that to its decode
 // kernel).  *wrote: a kernel that writes quantized blocks was launched.
 static kivi_status queue_before_append(kivi_cache* c, cudaStream_t st, bool pop, bool* wrote);
+// Flush rule of the default residual: when it is full, its R rows become blocks.
+static kivi_status flush_if_full(kivi_cache* c, cudaStream_t st);
 
 namespace kivi {
 
@@ -254,19 +256,52 @@ kivi_status kivi_append(kivi_cache_t c, const void* k, const void* v, kivi_strea
         c->n_resid += 1;
         return ok();
     }
-    if (c->n_resid == g.R) {
-        const __half* rk = reinterpret_cast<const __half*>(c->buf + g.k_resid_off);
-        const __half* rv = reinterpret_cast<const __half*>(c->buf + g.v_resid_off);
-        const cudaError_t e = kivi::launch_quantize_blocks(g, c->buf, rk, rv, (long long)g.R * g.D,
-                                                           c->n_quant / g.G, g.R / g.G, st);
-        if (e != cudaSuccess) return cuda_fail(e, "residual flush launch");
-        g_launches++;
-        c->n_quant += g.R;
-        c->n_resid = 0;
-    }
+    const kivi_status sf = flush_if_full(c, st);
+    if (sf != KIVI_OK) return sf;
     const cudaError_t e = kivi::launch_copy_rows(g, c->buf, static_cast<const __half*>(k),
                                                  static_cast<const __half*>(v), g.D, (int)c->n_resid, 1, st);
     if (e != cudaSuccess) return cuda_fail(e, "append copy launch");
+    g_launches++;
+    c->n_resid += 1;
+    return ok();
+}
+
+kivi_status kivi_append_qkv(kivi_cache_t c, const kivi_qkv* a, kivi_stream_t stream) {
+    if (!c) return fail(KIVI_ERR_INVALID_ARG, "null handle");
+    const kivi_status sa = kivi::check_qkv(a);
+    if (sa != KIVI_OK) return sa;
+    const kivi::Geometry& g = c->geo;
+    if (!a->k || !a->v) return fail(KIVI_ERR_INVALID_ARG, "null k or v");
+    if (a->q && !a->q_out) return fail(KIVI_ERR_INVALID_ARG, "q without q_out");
+    if (!aligned(a->q_out, 16)) return fail(KIVI_ERR_INVALID_ARG, "q_out must be 16-byte aligned");
+    if (a->batch != g.B || a->n_kv_heads != g.Hkv || a->n_q_heads != g.Hq || a->head_dim != g.D || a->n_tokens != 1)
+        return fail(KIVI_ERR_INVALID_ARG, "the cache takes one token of %d rows, %d query and %d kv heads of %d channels",
+                    g.B, g.Hq, g.Hkv, g.D);
+    if (c->n_quant + c->n_resid + 1 > g.max_tokens)
+        return fail(KIVI_ERR_CAPACITY, "cache already holds max_tokens (%lld) tokens", g.max_tokens);
+    const kivi_status sdev = ensure_device(c);
+    if (sdev != KIVI_OK) return sdev;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    long long v_row = 0;
+    if (c->value_queue) {
+        bool unused;
+        const kivi_status sq = queue_before_append(c, st, true, &unused);
+        if (sq != KIVI_OK) return sq;
+        v_row = (c->n_quant + c->n_resid) % g.R;
+    } else {
+        const kivi_status sf = flush_if_full(c, st);
+        if (sf != KIVI_OK) return sf;
+        v_row = c->n_resid;
+    }
+    // the kernel stores the new rows straight into the residual
+    kivi::QkvDest d;
+    d.q = static_cast<__half*>(a->q_out);
+    d.k = reinterpret_cast<__half*>(c->buf + g.k_resid_off) + c->n_resid * g.D;
+    d.v = reinterpret_cast<__half*>(c->buf + g.v_resid_off) + v_row * g.D;
+    d.q_slot = g.D;
+    d.k_slot = d.v_slot = (long long)g.R * g.D;
+    const cudaError_t e = kivi::launch_qk_norm_rope(*a, d, st);
+    if (e != cudaSuccess) return cuda_fail(e, "append norm and rotation launch");
     g_launches++;
     c->n_resid += 1;
     return ok();
@@ -383,14 +418,8 @@ kivi_status kivi_append_decode(kivi_cache_t c, const void* k, const void* v, con
         return ok();
     }
     if (c->n_resid == g.R) {
-        const __half* rk = reinterpret_cast<const __half*>(c->buf + g.k_resid_off);
-        const __half* rv = reinterpret_cast<const __half*>(c->buf + g.v_resid_off);
-        const cudaError_t e = kivi::launch_quantize_blocks(g, c->buf, rk, rv, (long long)g.R * g.D,
-                                                           c->n_quant / g.G, g.R / g.G, sp);
-        if (e != cudaSuccess) return cuda_fail(e, "residual flush launch");
-        g_launches++;
-        c->n_quant += g.R;
-        c->n_resid = 0;
+        const kivi_status sf = flush_if_full(c, sp);
+        if (sf != KIVI_OK) return sf;
         flushed = true;
     }
     kivi::FusedAppend fa;
@@ -450,12 +479,30 @@ void count_launches(int n) { g_launches += (unsigned long long)n; }
 
 kivi_status cache_device(kivi_cache* c) { return ensure_device(c); }
 
+CacheView cache_view(const kivi_cache* c) {
+    return CacheView{&c->geo, c->buf, c->n_quant, c->n_resid, c->value_queue, c->num_sms};
+}
+
 size_t decode_workspace_need(const kivi_cache* c) {
     const Geometry& g = c->geo;
     return (size_t)g.B * g.Hq * kPartialSlots * partial_stride(g.D) * sizeof(float);
 }
 
 }  // namespace kivi
+
+static kivi_status flush_if_full(kivi_cache* c, cudaStream_t st) {
+    const kivi::Geometry& g = c->geo;
+    if (c->n_resid != g.R) return KIVI_OK;
+    const __half* rk = reinterpret_cast<const __half*>(c->buf + g.k_resid_off);
+    const __half* rv = reinterpret_cast<const __half*>(c->buf + g.v_resid_off);
+    const cudaError_t e = kivi::launch_quantize_blocks(g, c->buf, rk, rv, (long long)g.R * g.D, c->n_quant / g.G,
+                                                       g.R / g.G, st);
+    if (e != cudaSuccess) return cuda_fail(e, "residual flush launch");
+    g_launches++;
+    c->n_quant += g.R;
+    c->n_resid = 0;
+    return KIVI_OK;
+}
 
 static kivi_status queue_before_append(kivi_cache* c, cudaStream_t st, bool pop, bool* wrote) {
     const kivi::Geometry& g = c->geo;

@@ -1,0 +1,500 @@
+// Decode over chosen blocks (include/kivi.h): the block scores, the selection,
+// the launch of attention over the listed blocks, and the dense cache's calls.
+#include <math.h>
+#include <stdarg.h>
+#include <stdio.h>
+
+#include "kivi_decode_blocks.cuh"
+
+namespace kivi {
+
+cudaError_t launch_decode_blocks_d128(const blocks_detail::Args& a, int bits, int nq, int G, long long rows,
+                                      long long units, int num_sms, cudaStream_t st);
+cudaError_t launch_decode_blocks_d64(const blocks_detail::Args& a, int bits, int nq, int G, long long rows,
+                                     long long units, int num_sms, cudaStream_t st);
+cudaError_t launch_decode_blocks_d128p(const blocks_detail::PagedArgs& a, int bits, int nq, int G, long long rows,
+                                       long long units, int num_sms, cudaStream_t st);
+cudaError_t launch_decode_blocks_d64p(const blocks_detail::PagedArgs& a, int bits, int nq, int G, long long rows,
+                                      long long units, int num_sms, cudaStream_t st);
+
+namespace {
+
+using mma_detail::griddepcontrol_launch_dependents;
+using mma_detail::griddepcontrol_wait;
+using mma_detail::kFull;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+kivi_status failf(kivi_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+kivi_status failf(kivi_status st, const char* fmt, ...) {
+    char msg[400];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(msg, sizeof msg, fmt, ap);
+    va_end(ap);
+    return report_error(st, msg);
+}
+
+kivi_status launched(cudaError_t e, const char* what) {
+    if (e != cudaSuccess) return failf(KIVI_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+    count_launches(1);
+    return report_error(KIVI_OK, "");
+}
+
+// ---- block scores ----
+//
+// A key block's entries give, per channel, its least dequantized key z_c and
+// its largest z_c + L s_c (L = 2^b - 1), so
+//
+//   u = sum_c q_c z_c + L sum_c max(q_c, 0) s_c
+//
+// is at least every logit q . k_hat_t of the block.  A lane holds 8 channels'
+// steps or 8 channels' zeros of a block (one 16-byte load) and multiplies them
+// with its 8 coefficients, L scale max(q_c, 0) or scale q_c, held in registers
+// for the whole row; D / 4 lanes share a block.  Eight loads are in flight per
+// lane, and the eight sums are reduced together by halving: each step adds
+// the half of the sums that the partner lane drops.
+constexpr int kScoreWarps = 8;
+constexpr int kScoreLoads = 8;       // 16-byte loads in flight per lane
+
+struct ScoreArgs {
+    const uint8_t* cache;
+    const __half* q;
+    float* scores;
+    long long ld, part_bytes, slot_bytes, entries_off;
+    int Hq, Hkv, n_blocks;
+    int iters;                       // groups of blocks a warp takes
+    float scale, levels;
+};
+struct PagedScoreArgs : ScoreArgs {
+    const int* table;
+    int max_blocks, n_pages;
+    RowSeq seqs[kMaxCallSeqs];
+};
+template <bool PAGED>
+struct ScoreArgsOf { using type = ScoreArgs; };
+template <>
+struct ScoreArgsOf<true> { using type = PagedScoreArgs; };
+
+template <int D, int NQ, bool PAGED>
+__global__ void __launch_bounds__(32 * kScoreWarps)
+    block_scores_kernel(const __grid_constant__ typename ScoreArgsOf<PAGED>::type a) {
+    constexpr int LPB = D / 4;                // lanes per block
+    constexpr int BPL = 32 / LPB;             // blocks a warp-wide load covers
+    constexpr int BPI = kScoreLoads * BPL;    // blocks per iteration
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lb = lane % LPB, sub = lane / LPB;
+    const long long row = blockIdx.y;
+    const int b = (int)(row / a.Hkv), hk = (int)(row % a.Hkv);
+    int nblk = a.n_blocks;
+    if constexpr (PAGED) nblk = a.seqs[b].n_blocks;
+    griddepcontrol_wait();
+    griddepcontrol_launch_dependents();
+    // the lane's coefficients: channels 8 (lb % (D/8)) .. of steps (first half of the lanes) or zeros
+    const bool steps = lb < LPB / 2;
+    float coef[NQ][8];
+#pragma unroll
+    for (int h = 0; h < NQ; ++h) {
+        const uint4 x = *reinterpret_cast<const uint4*>(a.q + ((long long)b * a.Hq + hk * NQ + h) * D + 8 * (lb % (D / 8)));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = mma_detail::unpack_f16x2(w[j]);
+            coef[h][2 * j] = steps ? fmaxf(f.x, 0.f) * a.levels * a.scale : f.x * a.scale;
+            coef[h][2 * j + 1] = steps ? fmaxf(f.y, 0.f) * a.levels * a.scale : f.y * a.scale;
+        }
+    }
+    float* out = a.scores + row * a.ld;
+    const long long n0 = ((long long)blockIdx.x * kScoreWarps + warp) * a.iters * BPI;
+    for (int it = 0; it < a.iters; ++it) {
+        const long long first = n0 + (long long)it * BPI;
+        if (first >= a.ld) break;
+        uint4 x[kScoreLoads];
+        bool bad[kScoreLoads];
+#pragma unroll
+        for (int u = 0; u < kScoreLoads; ++u) {
+            const long long n = first + u * BPL + sub;
+            x[u] = make_uint4(0, 0, 0, 0);
+            bad[u] = false;
+            if (n < nblk) {
+                const uint8_t* kp;
+                if constexpr (PAGED) {
+                    const int pg = __ldg(a.table + (long long)a.seqs[b].seq * a.max_blocks + n);
+                    bad[u] = (unsigned)pg >= (unsigned)a.n_pages;
+                    kp = a.cache + ((long long)(bad[u] ? 0 : pg) * a.Hkv + hk) * 2 * a.part_bytes;
+                } else {
+                    kp = a.cache + row * a.slot_bytes + n * a.part_bytes;
+                }
+                x[u] = mma_detail::ldg_stream(kp + a.entries_off + 16 * lb);
+            }
+        }
+        float best = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < NQ; ++h) {
+            float s[kScoreLoads];
+#pragma unroll
+            for (int u = 0; u < kScoreLoads; ++u) {
+                const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                float t = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = mma_detail::unpack_f16x2(w[j]);
+                    t = fmaf(coef[h][2 * j], f.x, fmaf(coef[h][2 * j + 1], f.y, t));
+                }
+                s[u] = PAGED && bad[u] ? NAN : t;
+            }
+            // sums over the block's LPB lanes; lane bits LPB/2, LPB/4, LPB/8 pick the load
+#pragma unroll
+            for (int n = kScoreLoads / 2, o = LPB / 2; n >= 1; n /= 2, o /= 2) {
+                const bool up = (lane & o) != 0;
+#pragma unroll
+                for (int u = 0; u < n; ++u) {
+                    const float keep = up ? s[u + n] : s[u], give = up ? s[u] : s[u + n];
+                    s[u] = keep + __shfl_xor_sync(kFull, give, o);
+                }
+            }
+#pragma unroll
+            for (int o = LPB / 16; o >= 1; o /= 2) s[0] += __shfl_xor_sync(kFull, s[0], o);
+            best = s[0] != s[0] || best != best ? NAN : fmaxf(best, s[0]);
+        }
+        const int u = lb / (LPB / 8);
+        const long long n = first + u * BPL + sub;
+        if (lb % (LPB / 8) == 0 && n < a.ld) out[n] = n < nblk ? best : -INFINITY;
+    }
+}
+
+template <int D, int NQ, bool PAGED>
+cudaError_t launch_scores_t(typename ScoreArgsOf<PAGED>::type& a, long long rows, int num_sms, cudaStream_t st) {
+    constexpr int BPI = kScoreLoads * 128 / D;
+    // a warp's coefficients cost about one group of blocks: more groups a warp
+    // only when the grid still gives every SM several CTAs
+    const long long groups = (a.ld + (long long)kScoreWarps * BPI - 1) / (kScoreWarps * BPI);
+    long long iters = groups * rows / (8LL * (num_sms > 0 ? num_sms : 1));
+    iters = iters < 1 ? 1 : iters > 4 ? 4 : iters;
+    a.iters = (int)iters;
+    const long long ctas = (groups + iters - 1) / iters;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+    return launch_dependent(block_scores_kernel<D, NQ, PAGED>, dim3((unsigned)ctas, (unsigned)rows), 32 * kScoreWarps,
+                            st, a);
+}
+
+template <bool PAGED>
+cudaError_t launch_scores(typename ScoreArgsOf<PAGED>::type& a, const BlockRows& r, cudaStream_t st) {
+    const int nq = r.g->Hq / r.g->Hkv;
+    const long long rows = (long long)r.n * r.g->Hkv;
+#define KIVI_S(DD, NN) \
+    if (r.g->D == DD && nq == NN) return launch_scores_t<DD, NN, PAGED>(a, rows, r.num_sms, st);
+    KIVI_S(128, 1) KIVI_S(128, 2) KIVI_S(128, 4) KIVI_S(64, 1) KIVI_S(64, 2) KIVI_S(64, 4)
+#undef KIVI_S
+    return cudaErrorInvalidValue;
+}
+
+// ---- selection ----
+//
+// A score as an unsigned key in the same order: 0 for -inf and NaN (never
+// chosen), all ones for a column that is always kept.  -0 and +0 are equal.
+__device__ __forceinline__ uint32_t score_key(float x, bool always) {
+    if (!(x > -INFINITY)) return 0u;
+    if (always) return 0xffffffffu;
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);   // -FLT_MAX -> 0x00800000 > 0; +inf -> 0xff800000
+}
+
+constexpr int kSelectThreads = 1024;
+constexpr int kSelectItems = 8;
+
+// One CTA per row.  The K-th largest key is found by bisection on its bits,
+// highest first, each step one count over the CTA; the row's keys stay in
+// registers (rows of more than 8192 columns are read again at each step).
+// Then every key above it is taken and, of the keys equal to it, the first
+// ones in index order; warps own consecutive columns, so a scan of the warps'
+// counts gives each chosen column its place.
+struct SelectArgs {
+    const float* scores;
+    long long cols, ld;
+    int n_keep, keep_first;
+    int* blocks;
+};
+
+__global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(const SelectArgs a) {
+    constexpr int kW = kSelectThreads / 32;
+    __shared__ int red[2][kW];
+    __shared__ int above_s[kW], equal_s[kW];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nw = blockDim.x / 32;
+    griddepcontrol_wait();
+    griddepcontrol_launch_dependents();
+    const float* row = a.scores + (long long)blockIdx.x * a.ld;
+    int* out = a.blocks + (long long)blockIdx.x * a.n_keep;
+    // columns of this warp: [c0, c0 + 32 * items), lane-strided
+    const long long items = (a.cols + blockDim.x - 1) / blockDim.x;
+    const long long c0 = warp * items * 32 + lane;
+    const bool held = items <= kSelectItems;
+    auto load = [&](long long c) {
+        return c < a.cols ? score_key(row[c], c < a.keep_first) : 0u;
+    };
+    uint32_t key[kSelectItems];
+#pragma unroll
+    for (int j = 0; j < kSelectItems; ++j) key[j] = j < items ? load(c0 + 32 * j) : 0u;
+    int flip = 0;
+    // columns of the row whose key is at least t
+    auto count = [&](uint32_t t) {
+        int n = 0;
+        if (held) {
+#pragma unroll
+            for (int j = 0; j < kSelectItems; ++j) n += key[j] >= t;
+        } else {
+            for (long long j = 0; j < items; ++j) n += load(c0 + 32 * j) >= t;
+        }
+        n = __reduce_add_sync(kFull, n);
+        if (lane == 0) red[flip][warp] = n;
+        __syncthreads();
+        int s = lane < nw ? red[flip][lane] : 0;
+        s = __reduce_add_sync(kFull, s);
+        flip ^= 1;                 // the next count writes the other half: no second barrier
+        return s;
+    };
+    const int K = a.n_keep;
+    uint32_t t = 1u;               // least key taken
+    const int valid = count(1u);
+    int take = valid < K ? valid : K;
+    if (valid > K) {
+        t = 0u;
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t c = t | (1u << bit);
+            const int n = count(c);
+            if (n >= K) {
+                t = c;
+                if (n == K) break;
+            }
+        }
+    }
+    // every key above t is taken, and of those equal to t the first `ties`
+    auto key_at = [&](long long j) { return held ? 0u : load(c0 + 32 * j); };
+    int na = 0, ne = 0;
+    auto tally = [&](uint32_t k) {
+        na += __popc(__ballot_sync(kFull, k > t));
+        ne += __popc(__ballot_sync(kFull, k == t));
+    };
+    if (held) {
+#pragma unroll
+        for (int j = 0; j < kSelectItems; ++j) tally(key[j]);
+    } else {
+        for (long long j = 0; j < items; ++j) tally(key_at(j));
+    }
+    if (lane == 0) {
+        above_s[warp] = na;
+        equal_s[warp] = ne;
+    }
+    __syncthreads();
+    const int wa = lane < nw ? above_s[lane] : 0, we = lane < nw ? equal_s[lane] : 0;
+    const int total_above = __reduce_add_sync(kFull, wa);
+    const int ties = take - total_above;
+    int before_a = __reduce_add_sync(kFull, lane < warp ? wa : 0);
+    int before_e = __reduce_add_sync(kFull, lane < warp ? we : 0);
+    const uint32_t below = (1u << lane) - 1u;
+    auto place = [&](uint32_t k, long long c) {
+        const uint32_t ma = __ballot_sync(kFull, k > t), me = __ballot_sync(kFull, k == t && t != 0u);
+        const int ra = before_a + __popc(ma & below), re = before_e + __popc(me & below);
+        if (k > t || (k == t && t != 0u && re < ties)) out[ra + min(re, ties)] = (int)c;
+        before_a += __popc(ma);
+        before_e += __popc(me);
+    };
+    if (held) {
+#pragma unroll
+        for (int j = 0; j < kSelectItems; ++j) place(key[j], c0 + 32 * j);
+    } else {
+        for (long long j = 0; j < items; ++j) place(key_at(j), c0 + 32 * j);
+    }
+    for (int j = take + tid; j < K; j += blockDim.x) out[j] = -1;
+}
+
+// A token appended to each of n sequences: residual rows of keys and values.
+struct AppendArgs {
+    uint8_t* buf;
+    const __half* k;
+    const __half* v;
+    long long k_resid_off, v_resid_off;
+    int Hkv, R, D;
+    AppendRow rows[kMaxCallSeqs];
+};
+__global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant__ AppendArgs a) {
+    griddepcontrol_wait();
+    griddepcontrol_launch_dependents();
+    const AppendRow r = a.rows[blockIdx.x];
+    const int cpr = a.D / 8;        // 16-byte chunks per row
+    const uint4* sk = reinterpret_cast<const uint4*>(a.k) + (long long)blockIdx.x * a.Hkv * cpr;
+    const uint4* sv = reinterpret_cast<const uint4*>(a.v) + (long long)blockIdx.x * a.Hkv * cpr;
+    uint4* dk = reinterpret_cast<uint4*>(a.buf + a.k_resid_off);
+    uint4* dv = reinterpret_cast<uint4*>(a.buf + a.v_resid_off);
+    for (int x = threadIdx.x; x < a.Hkv * cpr; x += blockDim.x) {
+        const long long at = (((long long)r.seq * a.Hkv + x / cpr) * a.R + r.row) * cpr + x % cpr;
+        dk[at] = sk[x];
+        dv[at] = sv[x];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_block_scores(const BlockRows& r, const __half* q, float scale, float* scores, long long ld,
+                                cudaStream_t st) {
+    const Geometry& g = *r.g;
+    const ScoreArgs base{r.buf, q, scores, ld, g.part_bytes, g.slot_bytes, (g.G / 16) * g.tile_bytes,
+                         g.Hq, g.Hkv, r.n_blocks, 1, scale, (float)((1 << g.bits) - 1)};
+    if (!r.table) {
+        ScoreArgs a = base;
+        return launch_scores<false>(a, r, st);
+    }
+    PagedScoreArgs a;
+    static_cast<ScoreArgs&>(a) = base;
+    a.table = r.table;
+    a.max_blocks = (int)g.NB;
+    a.n_pages = (int)r.n_pages;
+    for (int i = 0; i < r.n; ++i) a.seqs[i] = r.seqs[i];
+    return launch_scores<true>(a, r, st);
+}
+
+cudaError_t launch_select_blocks(const float* scores, long long rows, long long cols, long long ld, int n_keep,
+                                 int keep_first, int* blocks, cudaStream_t st) {
+    const long long warps = (cols + 31) / 32;
+    const int threads = warps >= kSelectThreads / 32 ? kSelectThreads : warps < 1 ? 32 : (int)warps * 32;
+    const SelectArgs a{scores, cols, ld, n_keep, keep_first, blocks};
+    return launch_dependent(select_blocks_kernel, dim3((unsigned)rows), threads, st, a);
+}
+
+cudaError_t launch_decode_blocks(const BlockRows& r, const __half* q, const int* list, int n_list, float scale_log2,
+                                 __half* out, cudaStream_t st) {
+    const Geometry& g = *r.g;
+    const int nq = g.Hq / g.Hkv;
+    const long long rows = (long long)r.n * g.Hkv;
+    // weights as in the dense decode: bytes of a quantized pair / 32, and 80 D
+    // bytes for a residual pair
+    const blocks_detail::Args base{r.buf, q, out, list, g.NB, g.part_bytes, g.slot_bytes, g.tile_bytes,
+                                   g.k_resid_off, g.v_resid_off, g.R, g.Hq, g.Hkv, n_list, r.n_blocks, r.n_resid,
+                                   g.D * g.bits / 4 + 8 * g.D / g.G, 5 * g.D / 2, scale_log2};
+    auto units = [&](int nblk, int nres) {
+        return (long long)(n_list < nblk ? n_list : nblk) * (g.G / 32) + (nres + 31) / 32;
+    };
+    if (!r.table) {
+        const long long u = units(r.n_blocks, r.n_resid);
+        return (g.D == 128 ? launch_decode_blocks_d128 : launch_decode_blocks_d64)(base, g.bits, nq, g.G, rows, u,
+                                                                                  r.num_sms, st);
+    }
+    blocks_detail::PagedArgs a;
+    static_cast<blocks_detail::Args&>(a) = base;
+    a.table = r.table;
+    a.max_blocks = (int)g.NB;
+    a.n_pages = (int)r.n_pages;
+    long long u = 0;
+    for (int i = 0; i < r.n; ++i) {
+        a.seqs[i] = r.seqs[i];
+        const long long ui = units(r.seqs[i].n_blocks, r.seqs[i].n_resid);
+        if (ui > u) u = ui;
+    }
+    return (g.D == 128 ? launch_decode_blocks_d128p : launch_decode_blocks_d64p)(a, g.bits, nq, g.G, rows, u,
+                                                                                r.num_sms, st);
+}
+
+cudaError_t launch_append_rows(const Geometry& g, uint8_t* buf, const AppendRow* rows, int n, const __half* new_k,
+                               const __half* new_v, cudaStream_t st) {
+    AppendArgs a;
+    a.buf = buf;
+    a.k = new_k;
+    a.v = new_v;
+    a.k_resid_off = g.k_resid_off;
+    a.v_resid_off = g.v_resid_off;
+    a.Hkv = g.Hkv;
+    a.R = g.R;
+    a.D = g.D;
+    for (int i = 0; i < n; ++i) a.rows[i] = rows[i];
+    return launch_dependent(append_rows_kernel, dim3((unsigned)n), 128, st, a);
+}
+
+kivi_status block_scores_call(const BlockRows& r, const void* q, float softmax_scale, float* scores, long long ld,
+                              kivi_stream_t stream) {
+    const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)r.g->D);
+    return launched(launch_block_scores(r, static_cast<const __half*>(q), scale, scores, ld,
+                                        reinterpret_cast<cudaStream_t>(stream)), "block scores launch");
+}
+
+kivi_status decode_blocks_call(const BlockRows& r, const void* q, const int* blocks, int n_list, void* out,
+                               float softmax_scale, kivi_stream_t stream) {
+    const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)r.g->D);
+    return launched(launch_decode_blocks(r, static_cast<const __half*>(q), blocks, n_list,
+                                         scale * 1.4426950408889634f, static_cast<__half*>(out),
+                                         reinterpret_cast<cudaStream_t>(stream)), "block decode launch");
+}
+
+kivi_status check_scores_args(const void* q, float softmax_scale, const float* scores, long long ld) {
+    if (!q || (!scores && ld != 0)) return failf(KIVI_ERR_INVALID_ARG, "null q or scores");
+    if (!aligned(q, 16)) return failf(KIVI_ERR_INVALID_ARG, "q must be 16-byte aligned");
+    if (!aligned(scores, 4)) return failf(KIVI_ERR_INVALID_ARG, "scores must be 4-byte aligned");
+    if (ld < 0) return failf(KIVI_ERR_INVALID_ARG, "negative column count");
+    if (!(softmax_scale == softmax_scale) || isinf(softmax_scale))
+        return failf(KIVI_ERR_INVALID_ARG, "softmax_scale must be finite");
+    return KIVI_OK;
+}
+
+kivi_status check_decode_blocks_args(const void* q, const int* blocks, int n_list, const void* out, float softmax_scale) {
+    if (!q || !out) return failf(KIVI_ERR_INVALID_ARG, "null q or out");
+    if (n_list < 0) return failf(KIVI_ERR_INVALID_ARG, "negative list length");
+    if (n_list > 0 && !blocks) return failf(KIVI_ERR_INVALID_ARG, "null block list");
+    if (!aligned(q, 16) || !aligned(out, 16)) return failf(KIVI_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+    if (!aligned(blocks, 4)) return failf(KIVI_ERR_INVALID_ARG, "blocks must be 4-byte aligned");
+    if (!(softmax_scale == softmax_scale) || isinf(softmax_scale))
+        return failf(KIVI_ERR_INVALID_ARG, "softmax_scale must be finite");
+    return KIVI_OK;
+}
+
+}  // namespace kivi
+
+extern "C" {
+
+kivi_status kivi_block_scores(kivi_cache_t c, const void* q, float softmax_scale, float* scores, long long ld,
+                              kivi_stream_t stream) {
+    using namespace kivi;
+    if (!c) return failf(KIVI_ERR_INVALID_ARG, "null handle");
+    const kivi_status sa = check_scores_args(q, softmax_scale, scores, ld);
+    if (sa != KIVI_OK) return sa;
+    CacheView v = cache_view(c);
+    BlockRows r{v.g, v.buf, v.g->B, (int)(v.n_quant / v.g->G), (int)v.n_resid, nullptr, 0, nullptr, 0};
+    if (ld < r.n_blocks)
+        return failf(KIVI_ERR_CAPACITY, "scores have %lld columns, the cache holds %d blocks", ld, r.n_blocks);
+    if (ld == 0) return report_error(KIVI_OK, "");
+    const kivi_status sd = cache_device(c);
+    if (sd != KIVI_OK) return sd;
+    r.num_sms = cache_view(c).num_sms;
+    return block_scores_call(r, q, softmax_scale, scores, ld, stream);
+}
+
+kivi_status kivi_select_blocks(const float* scores, long long rows, long long cols, long long ld, int n_keep,
+                               int keep_first, int* blocks, kivi_stream_t stream) {
+    using namespace kivi;
+    if (rows < 0 || cols < 0 || n_keep < 0 || keep_first < 0) return failf(KIVI_ERR_INVALID_ARG, "negative size");
+    if (ld < cols) return failf(KIVI_ERR_INVALID_ARG, "ld must be at least cols");
+    if (keep_first > n_keep) return failf(KIVI_ERR_INVALID_ARG, "keep_first must be at most n_keep");
+    if (rows > 0x7fffffffLL || cols > (1LL << 30)) return failf(KIVI_ERR_UNSUPPORTED, "rows must be < 2^31 and cols <= 2^30");
+    if (rows == 0 || n_keep == 0) return report_error(KIVI_OK, "");
+    if (!blocks || (!scores && cols > 0)) return failf(KIVI_ERR_INVALID_ARG, "null scores or blocks");
+    if (!aligned(scores, 4) || !aligned(blocks, 4)) return failf(KIVI_ERR_INVALID_ARG, "scores and blocks must be 4-byte aligned");
+    return launched(launch_select_blocks(scores, rows, cols, ld, n_keep, keep_first, blocks,
+                                         reinterpret_cast<cudaStream_t>(stream)), "block selection launch");
+}
+
+kivi_status kivi_decode_blocks(kivi_cache_t c, const void* q, const int* blocks, int n_list, void* out,
+                               float softmax_scale, kivi_stream_t stream) {
+    using namespace kivi;
+    if (!c) return failf(KIVI_ERR_INVALID_ARG, "null handle");
+    const kivi_status sa = check_decode_blocks_args(q, blocks, n_list, out, softmax_scale);
+    if (sa != KIVI_OK) return sa;
+    CacheView v = cache_view(c);
+    if (v.value_queue) return failf(KIVI_ERR_UNSUPPORTED, "the value queue has no decode over chosen blocks");
+    if (v.n_quant + v.n_resid == 0) return failf(KIVI_ERR_STATE, "decode on an empty cache");
+    const kivi_status sd = cache_device(c);
+    if (sd != KIVI_OK) return sd;
+    v = cache_view(c);
+    const BlockRows r{v.g, v.buf, v.g->B, (int)(v.n_quant / v.g->G), (int)v.n_resid, nullptr, 0, nullptr, v.num_sms};
+    return decode_blocks_call(r, q, blocks, n_list, out, softmax_scale, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,559 @@
+// Decode attention over a list of blocks per (query row, kv head) and the fp16
+// residual.
+//
+//   o = sum_t softmax_t(scale * q . k_hat_t) * v_hat_t,   t in the listed
+//   blocks' tokens and the residual rows,
+//
+// with the key and value arithmetic of the dense decode kernel
+// (kivi_decode_mma.cuh: codes as fp16 subnormals in mma.sync, steps folded into
+// the query and the probabilities, zero points on the side, online softmax in
+// the log2 domain, everything summed in fp32).
+//
+// What differs is the shape of the work: a list has tens of blocks, so a call
+// reads little and its latency counts.  One thread-block cluster takes one
+// row; its warps split the row's tile pairs (32 tokens) and residual pairs by
+// weight, stage their partial results (m, l, o) in shared memory, and merge
+// them through distributed shared memory: one launch, no workspace, no second
+// kernel.  The blocks' addresses come from the list (paged: through the block
+// table), which each warp turns into byte offsets in shared memory, a part of
+// the list at a time.
+#pragma once
+
+#include "kivi_decode_mma.cuh"
+
+namespace kivi {
+namespace blocks_detail {
+
+using namespace mma_detail;
+
+constexpr int kListCache = 64;      // list entries a warp keeps as byte offsets
+constexpr int kMaxCluster = 8;      // CTAs that share a row, at most (the portable cluster size)
+static_assert(kMaxCluster * kWarps <= 32, "the merge holds one partial a lane");
+
+struct Args {
+    const uint8_t* cache;
+    const __half* q;
+    __half* out;
+    const int* list;                // [rows][n_list] block numbers; negative: no block
+    long long NB, part_bytes, slot_bytes, tile_bytes, k_resid_off, v_resid_off;
+    int R, Hq, Hkv;
+    int n_list;
+    int n_blocks, n_resid;          // dense: quantized blocks and residual rows of every row
+    int wq, wr;                     // weights of a tile pair and of a residual pair
+    float scale_log2;
+};
+
+struct PagedArgs : Args {
+    const int* table;
+    int max_blocks, n_pages;
+    RowSeq seqs[kMaxCallSeqs];
+};
+
+template <bool PAGED>
+struct ArgsOf { using type = Args; };
+template <>
+struct ArgsOf<true> { using type = PagedArgs; };
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// the address of this CTA's shared variable at `a` in the cluster's CTA `rank`
+__device__ __forceinline__ uint32_t cluster_map(uint32_t a, uint32_t rank) {
+    uint32_t d;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
+    return d;
+}
+__device__ __forceinline__ float4 ldc128(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float2 ldc64(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void mbar_arrive_u32(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The MMAs of one 16-token tile, A fragments from the lane's words w, B
+// fragments from bfrag(t): keys sum every k-step into acc[0], values m-tile t
+// into acc[t].
+template <int BITS, bool VALUES, int W, int KS, int N, typename B>
+__device__ __forceinline__ void tile_mma(const uint32_t (&w)[W], const B& bfrag, float (&acc)[N][4]) {
+    uint32_t w8[W];
+    if constexpr (BITS != 8) {
+#pragma unroll
+        for (int x = 0; x < W; ++x) w8[x] = w[x] >> 8;
+    }
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+        uint32_t fa[4];
+        if constexpr (BITS == 8) a_frag_inline<BITS, VALUES, W>(w, t, fa);
+        else a_frag<BITS, VALUES, W>(w, w8, t, fa);
+        const uint2 bq = bfrag(t);
+        mma16816(acc[VALUES ? t : 0], fa, bq.x, bq.y);
+    }
+}
+
+template <int D, int BITS, int NQ, int G, bool PAGED>
+__global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
+    decode_blocks_kernel(const __grid_constant__ typename ArgsOf<PAGED>::type a) {
+    using C = Cfg<D, BITS, NQ, G>;
+    constexpr int KS = C::KSTEPS, W = C::W, NGRP = C::NGRP, GB = C::GB, NBF = C::NBF;
+    constexpr int PPB = C::TPB / 2;                   // tile pairs per block
+    // the row's scaled query (fp32) and the fp16 hi / lo parts of it times the
+    // code scale 2^-(BITS*pos), shared by the CTA's warps
+    __shared__ __align__(16) float qf[NQ][D];
+    __shared__ uint32_t qhc_s[NQ][D / 2], qlc_s[NQ][D / 2];
+    __shared__ __align__(16) uint32_t qfrag_all[kWarps][32 * C::QSTRIDE];
+    __shared__ __align__(8) uint64_t full_bar[kWarps][C::STAGES];
+    __shared__ long long off_all[kWarps][kListCache];
+    __shared__ __align__(16) float4 head_s[kWarps][NQ];   // a warp's (m, l, status) per query head
+    __shared__ float wgt_s[NQ][32];                       // the merge's weights
+    // per warp: the copy ring, then the warp's value sums [NQ][D] fp32
+    extern __shared__ __align__(128) uint8_t dyn_smem[];
+    static_assert(NQ * D * 4 <= C::STAGES * C::STAGE_BYTES, "the value sums reuse the copy ring");
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, i = lane & 3;
+    const uint32_t crank = cluster_rank(), csize = cluster_size();
+    const long long row = blockIdx.x / csize;
+    const int b = (int)(row / a.Hkv), hk = (int)(row % a.Hkv);
+    uint32_t* qfrag = qfrag_all[warp];
+    uint8_t* ring = dyn_smem + warp * C::STAGES * C::STAGE_BYTES;
+    uint64_t* bars = full_bar[warp];
+    long long* offs = off_all[warp];
+    for (int idx = lane; idx < 32 * C::QSTRIDE; idx += 32) qfrag[idx] = 0u;   // unused columns stay 0
+    if (lane == 0) {
+#pragma unroll
+        for (int st = 0; st < C::STAGES; ++st) mbar_init(&bars[st], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    int qoff[D / 64];     // this lane's Qt table offsets (channel pairs (D/64)*lane + j)
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+        const int cp = (D / 64) * lane + j, cc = (2 * cp) & 15;
+        qoff[j] = ((cc & 7) >> 1) * C::QSTRIDE + 2 * (cp >> 3) + (cc >> 3);
+    }
+    const uint32_t ring_u32 = smem_u32(ring), bars_u32 = smem_u32(bars);
+    const long long vdelta = PAGED ? a.part_bytes : a.NB * a.part_bytes;   // key part -> value part of a block
+    const int colP = g >> 1, hP = colP / GB, jP = colP % GB;   // this lane's B column for the values
+    const bool lo_col = (g & 1) != 0;
+    const bool col_ok = hP < NQ;
+    const int hO = i / GB, jO = i % GB;                        // this lane's output columns (2i, 2i+1)
+    const uint32_t eoff = 32u * jP + 8u * i;
+    const long long tiles_bytes = (long long)C::TPB * a.tile_bytes;
+
+    // ---- this warp's share of the row: units [u0, u1) of P quantized pairs, then PR residual pairs ----
+    int nblk, n_res;
+    long long rslot;
+    if constexpr (PAGED) {
+        const RowSeq& sq = a.seqs[b];
+        nblk = sq.n_blocks;
+        n_res = sq.n_resid;
+        rslot = (long long)sq.seq * a.Hkv + hk;
+    } else {
+        nblk = a.n_blocks;
+        n_res = a.n_resid;
+        rslot = row;
+    }
+    WorkMap wm{};
+    wm.P = (long long)min(a.n_list, nblk) * PPB;
+    wm.PR = (n_res + 31) / 32;
+    wm.wq = a.wq;
+    wm.wr = a.wr;
+    wm.Wt = wm.Ws = slot_weight(wm, wm.P, 0, wm.PR);
+    wm.n = csize * kWarps;
+    const long long worker = crank * kWarps + warp;
+    const int u0 = (int)first_unit_at(wm, map_begin(wm, worker)), u1 = (int)first_unit_at(wm, map_begin(wm, worker + 1));
+    const int wb = min(u0, (int)wm.P), we = min(u1, (int)wm.P);
+    const int rb = u0 - wb, re = u1 - we;
+
+    // everything below reads what earlier kernels on the stream may have written
+    griddepcontrol_wait();
+    griddepcontrol_launch_dependents();
+
+    const int* list = a.list + row * a.n_list;
+    uint32_t status = 0;       // 1: a bulk copy did not complete in time; 2: an entry outside the cache
+    // entries [j0, j0 + n) of the list as byte offsets of the blocks' key parts; -1: no block
+    auto fill = [&](int j0, int n) {
+        for (int j = lane; j < n; j += 32) {
+            const int e = __ldg(list + j0 + j);
+            long long off = -1;
+            if (e >= nblk) {
+                status |= 2u;
+            } else if (e >= 0) {
+                if constexpr (PAGED) {
+                    const int pg = __ldg(a.table + (long long)a.seqs[b].seq * a.max_blocks + e);
+                    if ((unsigned)pg < (unsigned)a.n_pages)
+                        off = ((long long)pg * a.Hkv + hk) * 2 * a.part_bytes;
+                    else
+                        status |= 2u;
+                } else {
+                    off = row * a.slot_bytes + (long long)e * a.part_bytes;
+                }
+            }
+            offs[j] = off;
+        }
+        __syncwarp();
+    };
+    int k = wb;                // next pair to process
+    int j0 = 0, kend = wb;     // the part of the list in offs: entries from j0, pairs below kend
+    uint32_t item = 0;         // ring item of pair k
+    auto issue = [&](int kk, uint32_t it) {       // lane 0: pair kk -> ring stage of item it
+        const uint32_t st = it % C::STAGES;
+        const uint32_t dst = ring_u32 + st * C::STAGE_BYTES, bar = bars_u32 + 8 * st;
+        const long long off = offs[kk / PPB - j0];
+        if (off < 0) {                            // no block: nothing to wait for
+            mbar_arrive_u32(bar);
+            return;
+        }
+        const uint8_t* kp = a.cache + off;
+        const uint8_t* vp = kp + vdelta;
+        if constexpr (C::WHOLE) {
+            mbar_expect_tx_u32(bar, C::STAGE_BYTES);
+            tma_1d_u32(dst + C::KT, kp, 2 * C::TILE + C::KSZ, bar);
+            tma_1d_u32(dst + C::VT, vp, 2 * C::TILE + 2 * C::ENT, bar);
+        } else {
+            const int t = 2 * (kk % PPB);         // the pair's first tile in the block
+            const bool kz = t == 0 || kk == wb;
+            mbar_expect_tx_u32(bar, 4 * C::TILE + 2 * C::ENT + (kz ? C::KSZ : 0));
+            tma_1d_u32(dst + C::KT, kp + t * C::TILE, 2 * C::TILE, bar);
+            if (kz) tma_1d_u32(dst + C::KE, kp + tiles_bytes, C::KSZ, bar);
+            tma_1d_u32(dst + C::VT, vp + t * C::TILE, 2 * C::TILE, bar);
+            tma_1d_u32(dst + C::VE, vp + tiles_bytes + t * C::ENT, 2 * C::ENT, bar);
+        }
+    };
+    // the list from pair k on into offs, and the first copies of that part
+    auto begin_part = [&]() {
+        j0 = k / PPB;
+        const int n = min((we - 1) / PPB - j0 + 1, kListCache);
+        kend = min(we, (j0 + n) * PPB);
+        fill(j0, n);
+        if (lane == 0) {
+            fence_proxy_async();
+            for (int u = 0; u < C::STAGES && k + u < kend; ++u) issue(k + u, item + u);
+        }
+        __syncwarp();
+    };
+    if (k < we) begin_part();
+    const __half* kr = reinterpret_cast<const __half*>(a.cache + a.k_resid_off) + rslot * a.R * D;
+    const __half* vr = reinterpret_cast<const __half*>(a.cache + a.v_resid_off) + rslot * a.R * D;
+    if (lane == 0 && rb < re) {                   // the residual rows into L2 ahead of their plain loads
+        const int n = min(32 * re, n_res) - 32 * rb;
+        prefetch_l2(kr + 32LL * rb * D, (uint32_t)(n * D * 2));
+        prefetch_l2(vr + 32LL * rb * D, (uint32_t)(n * D * 2));
+    }
+    for (int idx = tid; idx < NQ * D / 2; idx += kThreads) {
+        const int j = idx / (D / 2), cp = idx % (D / 2);
+        const float2 qv = __half22float2(
+            *reinterpret_cast<const __half2*>(a.q + ((long long)b * a.Hq + hk * NQ + j) * D + 2 * cp));
+        const float x0 = qv.x * a.scale_log2, x1 = qv.y * a.scale_log2;
+        qf[j][2 * cp] = x0;
+        qf[j][2 * cp + 1] = x1;
+        const float cs = pow2i(-BITS * ((cp >> 2) % (8 / BITS)));
+        const float y0 = x0 * cs, y1 = x1 * cs;
+        const uint32_t hic = pack_f16x2(y0, y1);
+        const float2 hcf = unpack_f16x2(hic);
+        qhc_s[j][cp] = hic;
+        qlc_s[j][cp] = pack_f16x2(y0 - hcf.x, y1 - hcf.y);
+    }
+    __syncthreads();
+
+    float m = -INFINITY, l = 0.f;
+    bool fresh = true;                            // no tile counted yet
+    float o[KS][4];
+    float zeta[NBF];
+#pragma unroll
+    for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+#pragma unroll
+    for (int f = 0; f < NBF; ++f) zeta[f] = 0.f;
+    constexpr bool QB_REGS = NQ > 1;
+    uint32_t qb[2 * KS] = {};
+    auto qbk = [&](const int kk) -> uint2 {       // the key B fragment of k-step kk (see build_q_frags)
+        if constexpr (QB_REGS)
+            return make_uint2(qb[2 * kk], qb[2 * kk + 1]);
+        else
+            return *reinterpret_cast<const uint2*>(qfrag + lane * C::QSTRIDE + 2 * kk);
+    };
+    float beta = 0.f;
+
+    // Online softmax step over two tiles: sc * unit = logits of tokens g, g+8
+    // of tile A and of tile B (head i); p receives their probabilities.
+    auto softmax = [&](const float (&sc)[4], float (&p)[4], float unit) {
+        float mt = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 4));
+        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 8));
+        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 16));
+        const float mn = fmaxf(m, mt * unit);
+        if (fresh) {
+            m = mn;
+            fresh = false;
+        } else if (__any_sync(kFull, mn > m)) {
+            const float alpha = fast_exp2(m - mn);
+            l *= alpha;
+            const float ao = __shfl_sync(kFull, alpha, (lane & ~3) | (hO < NQ ? hO : 0));
+#pragma unroll
+            for (int t = 0; t < KS; ++t) { o[t][0] *= ao; o[t][1] *= ao; o[t][2] *= ao; o[t][3] *= ao; }
+            const float az = __shfl_sync(kFull, alpha, col_ok ? hP : 0);
+#pragma unroll
+            for (int f = 0; f < NBF; ++f) zeta[f] *= az;
+            m = mn;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = fast_exp2(fmaf(sc[j], unit, -m));
+        l += (p[0] + p[1]) + (p[2] + p[3]);
+    };
+    // probabilities of tokens 2i, 2i+1, 2i+8, 2i+9 of head hP, and their fp16 hi / lo parts
+    auto gather = [&](float p0, float p1, float (&pr)[4]) {
+        const int src = 8 * i + (col_ok ? hP : 0);
+        pr[0] = __shfl_sync(kFull, p0, src);
+        pr[1] = __shfl_sync(kFull, p0, src + 4);
+        pr[2] = __shfl_sync(kFull, p1, src);
+        pr[3] = __shfl_sync(kFull, p1, src + 4);
+        if (!col_ok) pr[0] = pr[1] = pr[2] = pr[3] = 0.f;
+    };
+    auto split_p = [&](const float (&pr)[4], uint32_t& ph01, uint32_t& ph89, uint32_t& pl01, uint32_t& pl89) {
+        ph01 = pack_f16x2(pr[0], pr[1]);
+        ph89 = pack_f16x2(pr[2], pr[3]);
+        const float2 f01 = unpack_f16x2(ph01), f89 = unpack_f16x2(ph89);
+        pl01 = pack_f16x2(pr[0] - f01.x, pr[1] - f01.y);
+        pl89 = pack_f16x2(pr[2] - f89.x, pr[3] - f89.y);
+    };
+    const uint32_t lane_words = (uint32_t)(lane * W * 4);
+    auto lds_words = [&](uint32_t src, uint32_t (&w)[W]) {   // this lane's words of a tile at src
+        if constexpr (W % 4 == 0) {
+#pragma unroll
+            for (int v = 0; v < W / 4; ++v) {
+                const uint4 x = lds128(src + lane_words + 16 * v);
+                w[4 * v] = x.x; w[4 * v + 1] = x.y; w[4 * v + 2] = x.z; w[4 * v + 3] = x.w;
+            }
+        } else {
+            const uint2 x = lds64(src + lane_words);
+            w[0] = x.x; w[1] = x.y;
+        }
+    };
+    // ---- the listed blocks ----
+    while (k < we) {
+        if (k >= kend) begin_part();
+        bool failed = false;
+        bool skip = offs[k / PPB - j0] < 0;
+        for (; k < kend; ++k, ++item) {
+            const uint32_t st = item % C::STAGES;
+            if (!__all_sync(kFull, mbar_wait(&bars[st], (item / C::STAGES) & 1u))) { failed = true; break; }
+            const uint8_t* stage = ring + st * C::STAGE_BYTES;
+            const uint32_t stage_u32 = ring_u32 + st * C::STAGE_BYTES;
+            const bool first_of_block = k % PPB == 0 || k == wb;
+            if (first_of_block) skip = offs[k / PPB - j0] < 0;
+            if (!skip) {
+                if (first_of_block)
+                    build_q_frags<C, D, NQ, QB_REGS>(stage + C::KE, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);
+                float ca[1][4] = {{0.f, 0.f, 0.f, 0.f}}, cb[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+                uint32_t wa[W], wc[W];
+                lds_words(stage_u32 + C::KT, wa);
+                if constexpr (BITS != 8) lds_words(stage_u32 + C::KT + C::TILE, wc);
+                tile_mma<BITS, false, W, KS>(wa, qbk, ca);
+                if constexpr (BITS == 8) lds_words(stage_u32 + C::KT + C::TILE, wc);
+                tile_mma<BITS, false, W, KS>(wc, qbk, cb);
+                const float sc[4] = {ca[0][0] + (ca[0][1] + beta), ca[0][2] + (ca[0][3] + beta),
+                                     cb[0][0] + (cb[0][1] + beta), cb[0][2] + (cb[0][3] + beta)};
+                constexpr bool HOIST = BITS != 8 && W <= 4;   // as in the dense kernel
+                uint32_t wvh[2][W];
+                if constexpr (HOIST) {
+                    lds_words(stage_u32 + C::VT, wvh[0]);
+                    lds_words(stage_u32 + C::VT + C::TILE, wvh[1]);
+                }
+                float p[4];
+                softmax(sc, p, 0x1p24f);                       // scores are in units of 2^-24
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    float prb[4];
+                    gather(p[2 * t], p[2 * t + 1], prb);
+                    uint32_t ph01, ph89, pl01, pl89;
+                    split_p(prb, ph01, ph89, pl01, pl89);
+                    const uint32_t ve = stage_u32 + C::VE + t * C::ENT + eoff;
+                    uint32_t pb[NBF][2];
+#pragma unroll
+                    for (int f = 0; f < NBF; ++f) {            // B fragments of p * step, and p . zero
+                        const uint2 sv = lds64(ve + 32u * GB * f), zv = lds64(ve + 32u * (NGRP + GB * f));
+                        const uint32_t h01 = hmul2(ph01, sv.x), h89 = hmul2(ph89, sv.y);
+                        const uint32_t l01 = hfma2(pl01, sv.x, hfma2(ph01, sv.x, neg_f16x2(h01)));
+                        const uint32_t l89 = hfma2(pl89, sv.y, hfma2(ph89, sv.y, neg_f16x2(h89)));
+                        pb[f][0] = lo_col ? l01 : h01;
+                        pb[f][1] = lo_col ? l89 : h89;
+                        const float2 z01 = unpack_f16x2(zv.x), z89 = unpack_f16x2(zv.y);
+                        zeta[f] = fmaf(prb[0], z01.x, fmaf(prb[1], z01.y, fmaf(prb[2], z89.x, fmaf(prb[3], z89.y, zeta[f]))));
+                    }
+                    uint32_t wv[W];
+                    if constexpr (HOIST) {
+#pragma unroll
+                        for (int x = 0; x < W; ++x) wv[x] = wvh[t][x];
+                    } else {
+                        lds_words(stage_u32 + C::VT + t * C::TILE, wv);
+                    }
+                    auto pbk = [&](int mt) { return make_uint2(pb[(16 * mt / G) / GB][0], pb[(16 * mt / G) / GB][1]); };
+                    tile_mma<BITS, true, W, KS>(wv, pbk, o);
+                }
+            }
+            __syncwarp();                                      // every lane is done with this stage
+            if (lane == 0 && k + C::STAGES < kend) {
+                fence_proxy_async();
+                issue(k + C::STAGES, item + C::STAGES);
+            }
+        }
+        if (failed) {
+            // a copy timed out: wait (bounded) for the copies in flight, issue no more
+            status |= 1u;
+            for (int u = 0; u < C::STAGES && k + u < kend; ++u)
+                mbar_wait(&bars[(item + u) % C::STAGES], ((item + u) / C::STAGES) & 1u);
+            break;
+        }
+    }
+    // the quantized tiles' value sums are in units of 2^(BITS*pos - 24),
+    // pos = (channel / 8) % (8 / BITS): rows g and g+8 of m-tile mt have
+    // classes 2mt and 2mt+1
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt) {
+        const float s0 = pow2i(24 - BITS * ((2 * mt) % (8 / BITS)));
+        const float s1 = pow2i(24 - BITS * ((2 * mt + 1) % (8 / BITS)));
+        o[mt][0] *= s0; o[mt][1] *= s0; o[mt][2] *= s1; o[mt][3] *= s1;
+    }
+    // ---- the residual pairs: 32 fp16 rows each, A operands straight from memory ----
+    if (rb < re) {
+        build_q_frags<C, D, NQ, QB_REGS>(nullptr, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);   // step 1, zero 0
+        for (int rp = rb; rp < re; ++rp) {
+            float sc[4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int rw = 32 * rp + 16 * t;
+                const bool okg = rw + g < n_res, okg8 = rw + g + 8 < n_res;
+                const __half* kg = kr + (long long)(rw + g) * D;
+                const __half* kg8 = kg + 8 * D;
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    const int ch = 16 * kk + 2 * i;
+                    uint32_t af[4];
+                    af[0] = okg ? *reinterpret_cast<const uint32_t*>(kg + ch) : 0u;
+                    af[1] = okg8 ? *reinterpret_cast<const uint32_t*>(kg8 + ch) : 0u;
+                    af[2] = okg ? *reinterpret_cast<const uint32_t*>(kg + ch + 8) : 0u;
+                    af[3] = okg8 ? *reinterpret_cast<const uint32_t*>(kg8 + ch + 8) : 0u;
+                    const uint2 bq = qbk(kk);
+                    mma16816(c, af, bq.x, bq.y);
+                }
+                sc[2 * t] = okg ? c[0] + c[1] : -INFINITY;
+                sc[2 * t + 1] = okg8 ? c[2] + c[3] : -INFINITY;
+            }
+            float p[4];
+            softmax(sc, p, 1.f);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                float prb[4];
+                gather(p[2 * t], p[2 * t + 1], prb);
+                uint32_t ph01, ph89, pl01, pl89;
+                split_p(prb, ph01, ph89, pl01, pl89);
+                const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
+                const int rw = 32 * rp + 16 * t;
+                const __half* vg = vr + (long long)(rw + g) * D;
+#pragma unroll
+                for (int mt = 0; mt < KS; ++mt) {
+                    uint32_t af[4];
+                    vt_frag_rows<D>(vg, vg + 8 * D, rw + g < n_res, rw + g + 8 < n_res, mt, i, af);
+                    mma16816(o[mt], af, pb0, pb1);
+                }
+            }
+        }
+    }
+
+    // ---- this warp's partial result ----
+    const uint32_t st_all = __reduce_or_sync(kFull, status);
+#pragma unroll
+    for (int f = 0; f < NBF; ++f) {
+        zeta[f] += __shfl_xor_sync(kFull, zeta[f], 1);
+        zeta[f] += __shfl_xor_sync(kFull, zeta[f], 2);
+    }
+    float lt = l;
+    lt += __shfl_xor_sync(kFull, lt, 4);
+    lt += __shfl_xor_sync(kFull, lt, 8);
+    lt += __shfl_xor_sync(kFull, lt, 16);
+    float zo[NBF];
+#pragma unroll
+    for (int f = 0; f < NBF; ++f) zo[f] = __shfl_sync(kFull, zeta[f], 8 * i);
+    float* sums = reinterpret_cast<float*>(ring);
+    if (hO < NQ) {
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+            const int gr = 16 * mt / G;
+            if (gr % GB == jO) {
+                const float z = zo[gr / GB];
+                sums[hO * D + 16 * mt + g] = o[mt][0] + o[mt][1] + z;
+                sums[hO * D + 16 * mt + g + 8] = o[mt][2] + o[mt][3] + z;
+            }
+        }
+    }
+    if (g == 0 && i < NQ) head_s[warp][i] = make_float4(m, lt, (float)st_all, 0.f);
+
+    // ---- the log-sum-exp merge over the cluster's warps ----
+    __syncwarp();
+    if (csize > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    const int parts = (int)csize * kWarps;
+    static_assert(NQ <= kWarps, "one warp per query head in the merge");
+    if (warp < NQ) {
+        float mj = -INFINITY, lj = 0.f;
+        bool bad = false;
+        if (lane < parts) {
+            const float4 x = ldc128(cluster_map(smem_u32(&head_s[lane % kWarps][warp]), lane / kWarps));
+            mj = x.x;
+            lj = x.y;
+            bad = x.z != 0.f;
+        }
+        float M = mj;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, s));
+        const float e = mj == -INFINITY ? 0.f : fast_exp2(mj - M);
+        float L = lj * e;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(kFull, L, s);
+        bad = __any_sync(kFull, bad);
+        wgt_s[warp][lane] = bad ? NAN : e / L;    // (a row of one warp's worth of work: e is 0 or 1, L is l)
+    }
+    __syncthreads();
+    for (int idx = (int)crank * kThreads + tid; idx < NQ * D / 2; idx += (int)csize * kThreads) {
+        const int h = idx / (D / 2), c = 2 * (idx % (D / 2));
+        float s0 = 0.f, s1 = 0.f;
+        for (int j = 0; j < parts; ++j) {
+            const float w = wgt_s[h][j];
+            if (w == 0.f) continue;               // a partial without tokens
+            const uint32_t at = smem_u32(dyn_smem + (j % kWarps) * C::STAGES * C::STAGE_BYTES) + (h * D + c) * 4;
+            const float2 v = ldc64(cluster_map(at, j / kWarps));
+            s0 = fmaf(v.x, w, s0);
+            s1 = fmaf(v.y, w, s1);
+        }
+        *reinterpret_cast<__half2*>(a.out + ((long long)b * a.Hq + hk * NQ + h) * D + c) = __floats2half2_rn(s0, s1);
+    }
+    __syncwarp();
+    if (csize > 1) {                              // no CTA leaves while another reads its shared memory
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+}  // namespace blocks_detail
+}  // namespace kivi

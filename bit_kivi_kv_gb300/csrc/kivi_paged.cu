@@ -117,6 +117,100 @@ bool live_seq(const kivi_paged* c, int s) {
     return s >= 0 && s < (int)c->seqs.size() && c->seqs[s].live;
 }
 
+// The call's sequences are live and distinct.
+kivi_status mark_seqs(kivi_paged* c, const int* seqs, int n) {
+    if (++c->stamp == 0) {   // stamp wrapped: clear the marks
+        c->mark.assign(c->mark.size(), 0u);
+        c->stamp = 1;
+    }
+    for (int i = 0; i < n; ++i) {
+        const int s = seqs[i];
+        if (!live_seq(c, s)) return failf(KIVI_ERR_INVALID_ARG, "sequence %d (entry %d) is not live", s, i);
+        if (c->mark[(size_t)s] == c->stamp) return failf(KIVI_ERR_INVALID_ARG, "sequence %d is listed twice", s);
+        c->mark[(size_t)s] = c->stamp;
+    }
+    return KIVI_OK;
+}
+
+// The flushes of an append to the n sequences: how many pages they need, and
+// whether the sequences and the pool have room.
+kivi_status flush_room(const kivi_paged* c, const int* seqs, int n, long long* pages) {
+    const kivi::Geometry& g = c->pg.g;
+    *pages = 0;
+    for (int i = 0; i < n; ++i) {
+        const SeqState& sq = c->seqs[(size_t)seqs[i]];
+        if (sq.n_resid != g.R) continue;
+        if (sq.n_quant / g.G + g.R / g.G > g.NB)
+            return failf(KIVI_ERR_CAPACITY, "sequence %d is full (%lld tokens)", seqs[i], sq.n_quant + sq.n_resid);
+        *pages += g.R / g.G;
+    }
+    if (*pages > (long long)c->free_pages.size())
+        return failf(KIVI_ERR_CAPACITY, "flushes need %lld pages, %zu are free", *pages, c->free_pages.size());
+    return KIVI_OK;
+}
+
+// Launch the flushes (the R residual rows of each full sequence become R / G
+// blocks in the next free pages).
+cudaError_t launch_flushes(kivi_paged* c, const int* seqs, int n, long long pages, cudaStream_t st) {
+    const kivi::Geometry& g = c->pg.g;
+    std::vector<kivi::QJob> jobs;
+    jobs.reserve((size_t)pages);
+    size_t taken = 0;
+    for (int i = 0; i < n; ++i) {
+        const int s = seqs[i];
+        SeqState& sq = c->seqs[(size_t)s];
+        if (sq.n_resid != g.R) continue;
+        // room in the page list now, so that take_flushed cannot fail after the launch
+        const size_t need = sq.pages.size() + (size_t)(g.R / g.G);
+        if (sq.pages.capacity() < need) sq.pages.reserve(need > 2 * sq.pages.size() ? need : 2 * sq.pages.size());
+        for (int jj = 0; jj < g.R / g.G; ++jj) {
+            const int page = c->free_pages[c->free_pages.size() - 1 - taken++];
+            jobs.push_back(kivi::QJob{(long long)s * g.Hkv * g.R * g.D + (long long)jj * g.G * g.D, page,
+                                      (int)((long long)s * g.NB + sq.n_quant / g.G + jj)});
+        }
+    }
+    const __half* rk = reinterpret_cast<const __half*>(c->buf + g.k_resid_off);
+    const __half* rv = reinterpret_cast<const __half*>(c->buf + g.v_resid_off);
+    int nl = 0;
+    const cudaError_t e = kivi::launch_quantize_pages(c->pg, c->buf, rk, rv, (long long)g.R * g.D, jobs.data(),
+                                                      (int)jobs.size(), st, &nl);
+    kivi::count_launches(nl);
+    return e;
+}
+
+// The enqueued flushes' pages belong to their sequences.
+void take_flushed(kivi_paged* c, const int* seqs, int n) {
+    const kivi::Geometry& g = c->pg.g;
+    size_t used = 0;
+    for (int i = 0; i < n; ++i) {
+        SeqState& sq = c->seqs[(size_t)seqs[i]];
+        if (sq.n_resid != g.R) continue;
+        for (int jj = 0; jj < g.R / g.G; ++jj) sq.pages.push_back(c->free_pages[c->free_pages.size() - 1 - used++]);
+        sq.n_quant += g.R;
+        sq.n_resid = 0;
+    }
+    c->free_pages.resize(c->free_pages.size() - used);
+}
+
+// The rows of a call that only reads the cache: n distinct live sequences,
+// each holding a token.
+kivi_status read_rows(kivi_paged* c, const int* seqs, int n, kivi::RowSeq* out, kivi::BlockRows* r) {
+    if (!seqs) return failf(KIVI_ERR_INVALID_ARG, "null sequence list");
+    if (n < 1 || n > kivi::kMaxCallSeqs) return failf(KIVI_ERR_INVALID_ARG, "n must be in [1, %d]", kivi::kMaxCallSeqs);
+    const kivi_status sm = mark_seqs(c, seqs, n);
+    if (sm != KIVI_OK) return sm;
+    const kivi::Geometry& g = c->pg.g;
+    for (int i = 0; i < n; ++i) {
+        const SeqState& sq = c->seqs[(size_t)seqs[i]];
+        if (sq.n_quant + sq.n_resid == 0)
+            return failf(KIVI_ERR_STATE, "decode of sequence %d, which holds no token", seqs[i]);
+        out[i] = kivi::RowSeq{seqs[i], (int)(sq.n_quant / g.G), sq.n_resid};
+    }
+    *r = kivi::BlockRows{&g, c->buf, n, 0, 0, reinterpret_cast<const int*>(c->buf + c->pg.table_off),
+                         c->pg.n_pages, out, c->num_sms};
+    return KIVI_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -336,27 +430,9 @@ kivi_status kivi_paged_append_decode(kivi_paged_t c, const int* seqs, int n, con
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
 
     // flushes: the R residual rows of each full sequence become R / G blocks in new pages
-    std::vector<kivi::QJob> jobs;
     std::vector<kivi::PagedSeq> call((size_t)n);
-    size_t taken = 0;
     if (flush_pages) {
-        jobs.reserve((size_t)flush_pages);
-        for (int i = 0; i < n; ++i) {
-            const int s = seqs[i];
-            const SeqState& sq = c->seqs[(size_t)s];
-            if (!(append && sq.n_resid == g.R)) continue;
-            for (int jj = 0; jj < g.R / g.G; ++jj) {
-                const int page = c->free_pages[c->free_pages.size() - 1 - taken++];
-                jobs.push_back(kivi::QJob{(long long)s * g.Hkv * g.R * g.D + (long long)jj * g.G * g.D, page,
-                                          (int)((long long)s * g.NB + sq.n_quant / g.G + jj)});
-            }
-        }
-        const __half* rk = reinterpret_cast<const __half*>(c->buf + g.k_resid_off);
-        const __half* rv = reinterpret_cast<const __half*>(c->buf + g.v_resid_off);
-        int nl = 0;
-        const cudaError_t e = kivi::launch_quantize_pages(c->pg, c->buf, rk, rv, (long long)g.R * g.D, jobs.data(),
-                                                          (int)jobs.size(), st, &nl);
-        kivi::count_launches(nl);
+        const cudaError_t e = launch_flushes(c, seqs, n, flush_pages, st);
         if (e != cudaSuccess) return cuda_fail(e, "residual flush launch");
     }
     for (int i = 0; i < n; ++i) {
@@ -374,19 +450,80 @@ kivi_status kivi_paged_append_decode(kivi_paged_t c, const int* seqs, int n, con
         static_cast<const __half*>(v), flush_pages ? 0 : 1, c->num_sms, c->max_ctas, st, &nl);
     kivi::count_launches(nl);
     // the flushes were enqueued: their pages belong to the sequences whatever the decode launch did
-    size_t used = 0;
-    for (int i = 0; i < n && flush_pages; ++i) {
-        SeqState& sq = c->seqs[(size_t)seqs[i]];
-        if (!(append && sq.n_resid == g.R)) continue;
-        for (int jj = 0; jj < g.R / g.G; ++jj) sq.pages.push_back(c->free_pages[c->free_pages.size() - 1 - used++]);
-        sq.n_quant += g.R;
-        sq.n_resid = 0;
-    }
-    c->free_pages.resize(c->free_pages.size() - used);
+    if (flush_pages) take_flushed(c, seqs, n);
     if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
     if (append)
         for (int i = 0; i < n; ++i) c->seqs[(size_t)seqs[i]].n_resid += 1;
     return ok();
+}
+
+kivi_status kivi_paged_append(kivi_paged_t c, const int* seqs, int n, const void* k, const void* v,
+                              kivi_stream_t stream) {
+    if (!c) return failf(KIVI_ERR_INVALID_ARG, "null handle");
+    if (!seqs) return failf(KIVI_ERR_INVALID_ARG, "null sequence list");
+    if (n < 1 || n > kivi::kMaxCallSeqs) return failf(KIVI_ERR_INVALID_ARG, "n must be in [1, %d]", kivi::kMaxCallSeqs);
+    if (!k || !v) return failf(KIVI_ERR_INVALID_ARG, "null k or v");
+    if (!aligned(k, 16) || !aligned(v, 16)) return failf(KIVI_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+    const kivi_status sm = mark_seqs(c, seqs, n);
+    if (sm != KIVI_OK) return sm;
+    long long pages = 0;
+    const kivi_status sf = flush_room(c, seqs, n, &pages);
+    if (sf != KIVI_OK) return sf;
+    const kivi_status sdev = paged_device(c);
+    if (sdev != KIVI_OK) return sdev;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    try {
+        if (pages) {
+            const cudaError_t e = launch_flushes(c, seqs, n, pages, st);
+            if (e != cudaSuccess) return cuda_fail(e, "residual flush launch");
+            take_flushed(c, seqs, n);
+        }
+    } catch (const std::bad_alloc&) {
+        return failf(KIVI_ERR_INVALID_ARG, "out of host memory");
+    }
+    kivi::AppendRow rows[kivi::kMaxCallSeqs];
+    for (int i = 0; i < n; ++i) rows[i] = kivi::AppendRow{seqs[i], c->seqs[(size_t)seqs[i]].n_resid};
+    const cudaError_t e = kivi::launch_append_rows(c->pg.g, c->buf, rows, n, static_cast<const __half*>(k),
+                                                   static_cast<const __half*>(v), st);
+    if (e != cudaSuccess) return cuda_fail(e, "append copy launch");
+    kivi::count_launches(1);
+    for (int i = 0; i < n; ++i) c->seqs[(size_t)seqs[i]].n_resid += 1;
+    return ok();
+}
+
+kivi_status kivi_paged_block_scores(kivi_paged_t c, const int* seqs, int n, const void* q, float softmax_scale,
+                                    float* scores, long long ld, kivi_stream_t stream) {
+    if (!c) return failf(KIVI_ERR_INVALID_ARG, "null handle");
+    const kivi_status sa = kivi::check_scores_args(q, softmax_scale, scores, ld);
+    if (sa != KIVI_OK) return sa;
+    kivi::RowSeq rows[kivi::kMaxCallSeqs];
+    kivi::BlockRows r;
+    const kivi_status sr = read_rows(c, seqs, n, rows, &r);
+    if (sr != KIVI_OK) return sr;
+    for (int i = 0; i < n; ++i)
+        if (ld < rows[i].n_blocks)
+            return failf(KIVI_ERR_CAPACITY, "scores have %lld columns, sequence %d holds %d blocks", ld, seqs[i],
+                         rows[i].n_blocks);
+    if (ld == 0) return ok();
+    const kivi_status sdev = paged_device(c);
+    if (sdev != KIVI_OK) return sdev;
+    r.num_sms = c->num_sms;
+    return kivi::block_scores_call(r, q, softmax_scale, scores, ld, stream);
+}
+
+kivi_status kivi_paged_decode_blocks(kivi_paged_t c, const int* seqs, int n, const void* q, const int* blocks,
+                                     int n_list, void* out, float softmax_scale, kivi_stream_t stream) {
+    if (!c) return failf(KIVI_ERR_INVALID_ARG, "null handle");
+    const kivi_status sa = kivi::check_decode_blocks_args(q, blocks, n_list, out, softmax_scale);
+    if (sa != KIVI_OK) return sa;
+    kivi::RowSeq rows[kivi::kMaxCallSeqs];
+    kivi::BlockRows r;
+    const kivi_status sr = read_rows(c, seqs, n, rows, &r);
+    if (sr != KIVI_OK) return sr;
+    const kivi_status sdev = paged_device(c);
+    if (sdev != KIVI_OK) return sdev;
+    r.num_sms = c->num_sms;
+    return kivi::decode_blocks_call(r, q, blocks, n_list, out, softmax_scale, stream);
 }
 
 }  // extern "C"

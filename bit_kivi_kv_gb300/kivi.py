@@ -44,7 +44,20 @@ class kivi_paged_layout(ctypes.Structure):
                 ("resid_seq_bytes", ctypes.c_size_t), ("table_offset", ctypes.c_size_t)]
 
 
+class kivi_qkv(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("n_q_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("n_tokens", ctypes.c_longlong), ("dtype", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_longlong * 3), ("k_stride", ctypes.c_longlong * 3),
+                ("v_stride", ctypes.c_longlong * 3), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("cos_sin", ctypes.c_void_p), ("n_positions", ctypes.c_longlong),
+                ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("positions", ctypes.c_void_p),
+                ("positions_64bit", ctypes.c_int), ("first_position", ctypes.c_longlong),
+                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p)]
+
+
 KIVI_PAGED_MAX_CALL_SEQS = 512
+KIVI_F16, KIVI_BF16, KIVI_F32 = 0, 1, 2
 
 
 class KiviError(RuntimeError):
@@ -92,6 +105,14 @@ def _load():
         "kivi_paged_workspace_bytes": (SZ, [pcfgp, I]),
         "kivi_paged_set_max_ctas": (I, [P, I]),
         "kivi_paged_append_decode": (I, [P, IP, I, P, P, P, P, F, P, SZ, P]),
+        "kivi_block_scores": (I, [P, P, F, P, LL, P]),
+        "kivi_select_blocks": (I, [P, LL, LL, LL, I, I, P, P]),
+        "kivi_decode_blocks": (I, [P, P, P, I, P, F, P]),
+        "kivi_paged_block_scores": (I, [P, IP, I, P, F, P, LL, P]),
+        "kivi_paged_decode_blocks": (I, [P, IP, I, P, P, I, P, F, P]),
+        "kivi_paged_append": (I, [P, IP, I, P, P, P]),
+        "kivi_qk_norm_rope": (I, [ctypes.POINTER(kivi_qkv), P]),
+        "kivi_append_qkv": (I, [P, ctypes.POINTER(kivi_qkv), P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -264,6 +285,47 @@ def kivi_paged_append_decode(h: int, seqs, k: int, v: int, q: int, out: int, sof
                                         stream))
 
 
+# ---- decode over chosen blocks ------------------------------------------------------
+def kivi_block_scores(h: int, q: int, softmax_scale: float, scores: int, ld: int, stream: int):
+    _check(lib.kivi_block_scores(h, q, softmax_scale, scores, ld, stream))
+
+
+def kivi_select_blocks(scores: int, rows: int, cols: int, ld: int, n_keep: int, keep_first: int, blocks: int,
+                       stream: int):
+    _check(lib.kivi_select_blocks(scores, rows, cols, ld, n_keep, keep_first, blocks, stream))
+
+
+def kivi_decode_blocks(h: int, q: int, blocks: int, n_list: int, out: int, softmax_scale: float, stream: int):
+    _check(lib.kivi_decode_blocks(h, q, blocks, n_list, out, softmax_scale, stream))
+
+
+def _seq_array(seqs):
+    return (ctypes.c_int * max(len(seqs), 1))(*seqs)
+
+
+def kivi_paged_block_scores(h: int, seqs, q: int, softmax_scale: float, scores: int, ld: int, stream: int):
+    _check(lib.kivi_paged_block_scores(h, _seq_array(seqs), len(seqs), q, softmax_scale, scores, ld, stream))
+
+
+def kivi_paged_decode_blocks(h: int, seqs, q: int, blocks: int, n_list: int, out: int, softmax_scale: float,
+                             stream: int):
+    _check(lib.kivi_paged_decode_blocks(h, _seq_array(seqs), len(seqs), q, blocks, n_list, out, softmax_scale,
+                                        stream))
+
+
+def kivi_paged_append(h: int, seqs, k: int, v: int, stream: int):
+    _check(lib.kivi_paged_append(h, _seq_array(seqs), len(seqs), k, v, stream))
+
+
+# ---- norm and rotation of queries and keys -----------------------------------------
+def kivi_qk_norm_rope(args: kivi_qkv, stream: int):
+    _check(lib.kivi_qk_norm_rope(ctypes.byref(args), stream))
+
+
+def kivi_append_qkv(h: int, args: kivi_qkv, stream: int):
+    _check(lib.kivi_append_qkv(h, ctypes.byref(args), stream))
+
+
 def kivi_last_error_string() -> str:
     return lib.kivi_last_error_string().decode()
 
@@ -273,6 +335,141 @@ def kivi_launch_count() -> int:
 
 
 # ---- torch convenience wrapper -----------------------------------------------
+def _expect(t, what, dtype, shape, device=None):
+    """Raise KIVI_ERR_INVALID_ARG unless t is a dense CUDA tensor of this type and
+    shape on the current device (the one the kernels run on)."""
+    import torch
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+        raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be a contiguous CUDA {dtype} tensor of shape "
+                                              f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current device")
+
+
+def _raw_stream(stream):
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def select_blocks(scores, n_keep, keep_first=0, out=None, stream=None):
+    """The n_keep best columns of each row of scores (fp32 [..., cols], rows dense or
+    evenly strided), as int32 [..., n_keep] in ascending order with -1 behind; the
+    first keep_first columns always among them (kivi_select_blocks)."""
+    import torch
+    cols, lead = scores.shape[-1], tuple(scores.shape[:-1])
+    if scores.dtype != torch.float32 or not scores.is_cuda:
+        raise KiviError(KIVI_ERR_INVALID_ARG, "scores must be a CUDA float32 tensor")
+    if scores.device.index != torch.cuda.current_device():
+        raise KiviError(KIVI_ERR_INVALID_ARG, f"scores are on {scores.device}, not on the current device")
+    if scores.is_contiguous():
+        ld = cols
+    elif scores.dim() == 2 and scores.stride(1) == 1:
+        ld = scores.stride(0)
+    else:
+        raise KiviError(KIVI_ERR_INVALID_ARG, "scores must be contiguous, or a matrix with dense rows")
+    rows = 1
+    for n in lead:
+        rows *= n
+    if out is None:
+        out = torch.empty(lead + (n_keep,), dtype=torch.int32, device=scores.device)
+    else:
+        _expect(out, "out", torch.int32, lead + (n_keep,))
+    kivi_select_blocks(scores.data_ptr(), rows, cols, ld, n_keep, keep_first, out.data_ptr(), _raw_stream(stream))
+    return out
+
+
+def rope_table(n_positions, rot_dim, base=10000.0, device="cuda"):
+    """The cosines and sines of a rotation as QKNormRope takes them: fp32
+    [n_positions][rot_dim], pair j at position p turned by p * base^(-2j / rot_dim),
+    the angles in fp64 (their error in fp32 grows with the position)."""
+    import torch
+    freq = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    angle = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], dim=1).float().contiguous()
+
+
+class QKNormRope:
+    """The norm of every query and key head, the position rotation and the change to
+    the cache's fp16 head-major layout, in one pass (kivi_qk_norm_rope).
+
+    q_weight, k_weight: fp32 [head_dim], None: no norm.  cos_sin: fp32
+    [n_positions][rot_dim] (see rope_table), None: no rotation."""
+
+    def __init__(self, n_q_heads, n_kv_heads, head_dim, q_weight=None, k_weight=None, cos_sin=None, eps=1e-6,
+                 interleaved=False):
+        import torch
+        for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                _expect(w, what, torch.float32, (head_dim,))
+        a = kivi_qkv()
+        a.n_q_heads, a.n_kv_heads, a.head_dim, a.eps = n_q_heads, n_kv_heads, head_dim, eps
+        a.q_weight = w.data_ptr() if (w := q_weight) is not None else None
+        a.k_weight = w.data_ptr() if (w := k_weight) is not None else None
+        if cos_sin is not None:
+            _expect(cos_sin, "cos_sin", torch.float32, cos_sin.shape[:1] + cos_sin.shape[1:2])
+            a.cos_sin, (a.n_positions, a.rot_dim) = cos_sin.data_ptr(), cos_sin.shape
+        a.interleaved = bool(interleaved)
+        self._fixed = bytes(a)
+        self._keep = (q_weight, k_weight, cos_sin)
+        given = [t for t in self._keep if t is not None]
+        self._device = given[0].device.index if given else None
+        self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
+        self._dtypes = {torch.float16: KIVI_F16, torch.bfloat16: KIVI_BF16, torch.float32: KIVI_F32}
+
+    def _args(self, q, k, v, positions, first_position):
+        """The C call's arguments for inputs [batch, tokens, heads, head_dim] (or
+        [batch, heads, head_dim]: one token a row), without the outputs."""
+        import torch
+        a = kivi_qkv.from_buffer_copy(self._fixed)
+        lead = q.shape[:-2]
+        one = len(lead) == 1
+        if not one and len(lead) != 2:
+            raise KiviError(KIVI_ERR_INVALID_ARG, "q, k and v have 3 or 4 dimensions")
+        code = self._dtypes.get(q.dtype)
+        if code is None:
+            raise KiviError(KIVI_ERR_INVALID_ARG, f"no input type {q.dtype}")
+        device = torch.cuda.current_device()
+        if self._device not in (None, device):
+            raise KiviError(KIVI_ERR_INVALID_ARG, f"the weights are on cuda:{self._device}, not on the current device")
+        a.batch, a.n_tokens, a.dtype = lead[0], 1 if one else lead[1], code
+        for x, heads, ptr, stride in ((q, self.n_q_heads, "q", a.q_stride), (k, self.n_kv_heads, "k", a.k_stride),
+                                      (v, self.n_kv_heads, "v", a.v_stride)):
+            if x.dtype != q.dtype or not x.is_cuda or x.device.index != device:
+                raise KiviError(KIVI_ERR_INVALID_ARG, f"{ptr} must be of q's type and on the current device")
+            if x.shape[:-2] != lead or x.shape[-2] != heads or x.shape[-1] != self.head_dim or x.stride(-1) != 1:
+                raise KiviError(KIVI_ERR_INVALID_ARG, f"{ptr} must be [..., {heads}, {self.head_dim}] with dense "
+                                                      f"channels and q's leading sizes, got {tuple(x.shape)}")
+            s = x.stride()
+            stride[0], stride[1], stride[2] = s[0], 0 if one else s[1], s[-2]
+            setattr(a, ptr, x.data_ptr())
+        if positions is not None:
+            if positions.dtype not in (torch.int32, torch.int64):
+                raise KiviError(KIVI_ERR_INVALID_ARG, "positions must be int32 or int64")
+            _expect(positions, "positions", positions.dtype, lead)
+            a.positions, a.positions_64bit = positions.data_ptr(), positions.dtype == torch.int64
+        a.first_position = first_position
+        return a, one
+
+    def __call__(self, q, k, v, positions=None, first_position=0, out=None, stream=None):
+        """q [B, L, Hq, D], k and v [B, L, Hkv, D] (fp16, bf16 or fp32; any strides with
+        dense channels, e.g. parts of one projection's output; without L: one token
+        a row), positions [B, L] int32 or int64 (None: first_position + token).
+        Returns fp16 (q [B, Hq, L, D], k [B, Hkv, L, D], v), without L where the
+        inputs have none."""
+        import torch
+        a, one = self._args(q, k, v, positions, first_position)
+        shapes = [(a.batch, h, self.head_dim) if one else (a.batch, h, a.n_tokens, self.head_dim)
+                  for h in (self.n_q_heads, self.n_kv_heads, self.n_kv_heads)]
+        if out is None:
+            out = tuple(torch.empty(s, dtype=torch.float16, device=q.device) for s in shapes)
+        else:
+            for t, s, what in zip(out, shapes, ("out[0]", "out[1]", "out[2]")):
+                _expect(t, what, torch.float16, s)
+        a.q_out, a.k_out, a.v_out = (t.data_ptr() for t in out)
+        kivi_qk_norm_rope(a, _raw_stream(stream))
+        return out
+
+
 class KiviCache:
     """One layer's cache: a torch-owned device buffer plus the library handle."""
 
@@ -347,6 +544,60 @@ class KiviCache:
         return out
 
 
+    def append_qkv(self, norm_rope, q, k, v, positions=None, first_position=0, q_out=None, stream=None):
+        """Append one token a row from a projection's output: norm and rotation by
+        norm_rope (QKNormRope), k and v stored in the cache by the same kernel.
+        q [B, Hq, D], k, v [B, Hkv, D]; returns the query, fp16 [B, Hq, D]."""
+        import torch
+        a, one = norm_rope._args(q, k, v, positions, first_position)
+        if q_out is None:
+            q_out = torch.empty(a.batch, a.n_q_heads, a.head_dim, dtype=torch.float16, device=q.device)
+        else:
+            _expect(q_out, "q_out", torch.float16, (a.batch, a.n_q_heads, a.head_dim))
+        a.q_out = q_out.data_ptr()
+        kivi_append_qkv(self.handle, a, self._stream(stream))
+        return q_out
+
+    def block_scores(self, q, out=None, softmax_scale=0.0, stream=None):
+        """A bound on the logits of each quantized block for q [B, Hq, D]: fp32
+        [B, Hkv, blocks] (kivi_block_scores); out may have more columns (-inf there)."""
+        import torch
+        c = self.cfg
+        _expect(q, "q", torch.float16, (c.batch, c.n_q_heads, c.head_dim))
+        if out is None:
+            out = torch.empty(c.batch, c.n_kv_heads, self.counts()[0] // c.group, dtype=torch.float32, device=q.device)
+        else:
+            _expect(out, "out", torch.float32, (c.batch, c.n_kv_heads, out.shape[-1]))
+        kivi_block_scores(self.handle, q.data_ptr(), softmax_scale, out.data_ptr(), out.shape[-1], self._stream(stream))
+        return out
+
+    def decode_blocks(self, q, blocks, out=None, softmax_scale=0.0, stream=None):
+        """Decode attention of q [B, Hq, D] over the listed blocks (int32
+        [B, Hkv, n], negative: none) and the residual (kivi_decode_blocks)."""
+        import torch
+        c = self.cfg
+        _expect(q, "q", torch.float16, (c.batch, c.n_q_heads, c.head_dim))
+        _expect(blocks, "blocks", torch.int32, (c.batch, c.n_kv_heads, blocks.shape[-1]))
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _expect(out, "out", torch.float16, q.shape)
+        kivi_decode_blocks(self.handle, q.data_ptr(), blocks.data_ptr(), blocks.shape[-1], out.data_ptr(),
+                           softmax_scale, self._stream(stream))
+        return out
+
+    def sparse_decode(self, q, n_keep, keep_first=1, out=None, softmax_scale=0.0, stream=None):
+        """Decode attention over the n_keep blocks of the largest scores (the first
+        keep_first always) and the residual: block_scores, select_blocks and
+        decode_blocks in sequence."""
+        import torch
+        with torch.cuda.stream(stream):
+            scores = self.block_scores(q, softmax_scale=softmax_scale)
+            n_keep = min(n_keep, scores.shape[-1])
+            blocks = select_blocks(scores, n_keep, min(keep_first, n_keep))
+            return self.decode_blocks(q, blocks, out, softmax_scale)
+
+
 class KiviPagedCache:
     """A paged cache for ragged sequences: a torch-owned device buffer (page pool,
     residual rows, block table) plus the library handle."""
@@ -405,3 +656,50 @@ class KiviPagedCache:
                                  softmax_scale, self.workspace.data_ptr(), self.workspace.numel(),
                                  KiviCache._stream(stream))
         return out
+
+    def append(self, seqs, k, v, stream=None):
+        """For each listed sequence: append k[i], v[i] ([n][Hkv][D])."""
+        import torch
+        c, seqs = self.cfg, list(seqs)
+        _expect(k, "k", torch.float16, (len(seqs), c.n_kv_heads, c.head_dim))
+        _expect(v, "v", torch.float16, (len(seqs), c.n_kv_heads, c.head_dim))
+        kivi_paged_append(self.handle, seqs, k.data_ptr(), v.data_ptr(), KiviCache._stream(stream))
+
+    def block_scores(self, seqs, q, out=None, softmax_scale=0.0, stream=None):
+        """KiviCache.block_scores for the listed sequences: q [n, Hq, D] -> fp32
+        [n, Hkv, the longest sequence's blocks], -inf behind a sequence's last."""
+        import torch
+        c, seqs = self.cfg, list(seqs)
+        _expect(q, "q", torch.float16, (len(seqs), c.n_q_heads, c.head_dim))
+        if out is None:
+            cols = max((self.counts(s)[0] // c.group for s in seqs), default=0)
+            out = torch.empty(len(seqs), c.n_kv_heads, cols, dtype=torch.float32, device=q.device)
+        else:
+            _expect(out, "out", torch.float32, (len(seqs), c.n_kv_heads, out.shape[-1]))
+        kivi_paged_block_scores(self.handle, seqs, q.data_ptr(), softmax_scale, out.data_ptr(), out.shape[-1],
+                                KiviCache._stream(stream))
+        return out
+
+    def decode_blocks(self, seqs, q, blocks, out=None, softmax_scale=0.0, stream=None):
+        """KiviCache.decode_blocks for the listed sequences: blocks int32 [n, Hkv, m]."""
+        import torch
+        c, seqs = self.cfg, list(seqs)
+        _expect(q, "q", torch.float16, (len(seqs), c.n_q_heads, c.head_dim))
+        _expect(blocks, "blocks", torch.int32, (len(seqs), c.n_kv_heads, blocks.shape[-1]))
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _expect(out, "out", torch.float16, q.shape)
+        kivi_paged_decode_blocks(self.handle, seqs, q.data_ptr(), blocks.data_ptr(), blocks.shape[-1], out.data_ptr(),
+                                 softmax_scale, KiviCache._stream(stream))
+        return out
+
+    def sparse_decode(self, seqs, q, n_keep, keep_first=1, out=None, softmax_scale=0.0, stream=None):
+        """KiviCache.sparse_decode for the listed sequences."""
+        import torch
+        seqs = list(seqs)
+        with torch.cuda.stream(stream):
+            scores = self.block_scores(seqs, q, softmax_scale=softmax_scale)
+            n_keep = min(n_keep, scores.shape[-1])
+            blocks = select_blocks(scores, n_keep, min(keep_first, n_keep))
+            return self.decode_blocks(seqs, q, blocks, out, softmax_scale)

@@ -437,6 +437,156 @@ kivi_status kivi_paged_append_decode(kivi_paged_t cache, const int* seqs, int n,
                                      const void* v, const void* q, void* out, float softmax_scale,
                                      void* workspace, size_t ws_bytes, kivi_stream_t stream);
 
+/* ===================== Decode over chosen blocks =====================
+ *
+ * A decode call above reads every cached token.  The calls here read only the
+ * quantized blocks that matter for the query, and always the fp16 residual:
+ *
+ *     kivi_block_scores   a bound on every logit of each block, from the
+ *                         block's key steps and zeros alone
+ *     kivi_select_blocks  the blocks with the largest scores of each row
+ *     kivi_decode_blocks  decode attention over the listed blocks and the
+ *                         residual
+ *
+ * A row is one (query row, kv head) pair, query row = batch row or listed
+ * sequence; the query heads of one kv head share the row's blocks.  Rows are
+ * [query row][kv head], dense.  The three calls need no workspace, write
+ * nothing but their outputs and leave the cache as it is, so several may run
+ * at once on different streams, each with outputs of its own.  The method's
+ * description has no counterpart.
+ *
+ * A caller may use scores or lists of its own: each call only reads what it is
+ * given.
+ */
+
+/*
+ * Block scores.  A key block stores, per channel, its least dequantized key
+ * z_c and the step s_c, and its largest is z_c + (2^B - 1) s_c, so
+ *
+ *     u_h(n) = scale * (sum_c q_c z_c + (2^B - 1) sum_c max(q_c, 0) s_c)
+ *
+ * is at least (up to fp32 rounding) every logit scale * q_h . k_hat_t of block
+ * n's tokens.  scores[row][n] = max over the row's query heads h of u_h(n) for
+ * the blocks n < Lq / G of the row's sequence, and -inf for the columns from
+ * there to ld.  q: fp16 [query rows][Hq][D]; scores: fp32 [rows][ld], 4-byte
+ * aligned; softmax_scale <= 0 selects 1/sqrt(D).  fp32 sums in a fixed order:
+ * equal blocks get equal scores.  KIVI_ERR_CAPACITY when ld is less than the
+ * longest row's block count; ld == 0 does nothing.
+ */
+kivi_status kivi_block_scores(kivi_cache_t cache, const void* q, float softmax_scale, float* scores, long long ld,
+                              kivi_stream_t stream);
+
+/*
+ * Selection.  For each of rows rows of cols scores (row r at scores + r * ld,
+ * fp32): the n_keep columns with the largest scores, equal scores by the lowest
+ * index; columns below keep_first (<= n_keep) come before all others, whatever
+ * their scores (the first blocks, where attention sinks sit).  -inf and NaN
+ * are never chosen, not in those columns either; every other value is.
+ * blocks: int32 [rows][n_keep], each row its chosen columns in ascending
+ * order, then -1 for the places that no column fills.  cols may be 0.  Runs on
+ * the current device; scores and blocks need only their natural alignment.
+ */
+kivi_status kivi_select_blocks(const float* scores, long long rows, long long cols, long long ld, int n_keep,
+                               int keep_first, int* blocks, kivi_stream_t stream);
+
+/*
+ * Decode attention over chosen blocks: as kivi_decode_attn, over the tokens of
+ * each row's listed blocks and all residual rows.  blocks: int32
+ * [rows][n_list], 4-byte aligned, on the device.  Of a row's entries the
+ * first min(n_list, Lq / G) are read; a negative entry is no block (so a
+ * selection's -1 may stand anywhere), the order has no meaning beyond fp32
+ * summation, and a block listed twice counts twice.  An entry of Lq / G or
+ * more (or, paged, whose page lies outside the pool) is not read from; it makes
+ * the outputs of the row's heads NaN, as a copy that times out does.
+ * n_list may be 0 (the residual alone).  One launch, no workspace.
+ * KIVI_ERR_STATE on an empty cache; KIVI_ERR_UNSUPPORTED with the value queue.
+ */
+kivi_status kivi_decode_blocks(kivi_cache_t cache, const void* q, const int* blocks, int n_list, void* out,
+                               float softmax_scale, kivi_stream_t stream);
+
+/* The same on the paged cache, for the n distinct live sequences seqs[0..n-1]
+ * (host array, each holding a token): q and out fp16 [n][Hq][D], rows
+ * [n][Hkv].  Decode only: append with kivi_paged_append before. */
+kivi_status kivi_paged_block_scores(kivi_paged_t cache, const int* seqs, int n, const void* q, float softmax_scale,
+                                    float* scores, long long ld, kivi_stream_t stream);
+kivi_status kivi_paged_decode_blocks(kivi_paged_t cache, const int* seqs, int n, const void* q, const int* blocks,
+                                     int n_list, void* out, float softmax_scale, kivi_stream_t stream);
+
+/*
+ * Append token k[i], v[i] (fp16 [n][Hkv][D]) to each of the n distinct live
+ * sequences seqs[i], without a decode: the append half of
+ * kivi_paged_append_decode, with its flush rule and errors.
+ */
+kivi_status kivi_paged_append(kivi_paged_t cache, const int* seqs, int n, const void* k, const void* v,
+                              kivi_stream_t stream);
+
+/* ===================== Norm and rotation of queries and keys =====================
+ *
+ * From a projection's output to the cache's inputs in one pass: each head row
+ * x of q and k ([D] channels of one token) becomes
+ *
+ *     y  = x / sqrt(mean(x^2) + eps) * weight        (no weight: y = x)
+ *     (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)
+ *                                  for the rot_dim / 2 pairs (a, b) of the
+ *                                  first rot_dim channels (no table: none)
+ *     output = fp16(y),
+ *
+ * and each head row of v becomes fp16(x).  fp32 throughout, rounded once;
+ * results beyond fp16's range become infinite.  Pairs are (j, j + rot_dim / 2)
+ * or, interleaved, (2j, 2j + 1).
+ */
+typedef enum {
+    KIVI_F16 = 0,
+    KIVI_BF16 = 1,
+    KIVI_F32 = 2
+} kivi_dtype;
+
+typedef struct {
+    int batch;
+    int n_q_heads;
+    int n_kv_heads;
+    int head_dim;             /* 64 or 128 */
+    long long n_tokens;       /* per batch row */
+    int dtype;                /* kivi_dtype of q, k and v */
+    /* Inputs [batch][n_tokens][heads][head_dim] with any strides (elements;
+     * multiples of 16 bytes; batch, token, head) and dense channels, 16-byte
+     * aligned; they may be parts of one packed tensor.  Null: left out, with
+     * its output; not all three. */
+    const void *q, *k, *v;
+    long long q_stride[3], k_stride[3], v_stride[3];
+    const float *q_weight, *k_weight;   /* [head_dim], or null: no norm */
+    float eps;
+    /* cos_sin fp32 [n_positions][rot_dim]: a position's rot_dim / 2 cosines,
+     * then its sines; null: no rotation.  rot_dim: a multiple of 8, at most
+     * head_dim.  positions: [batch][n_tokens] int32 (positions_64bit: int64),
+     * dense; null: token t is at first_position + t.  A position outside
+     * [0, n_positions) reads no table row; it makes the rotated channels of
+     * its token's q and k heads NaN. */
+    const float* cos_sin;
+    long long n_positions;
+    int rot_dim;
+    int interleaved;
+    const void* positions;
+    int positions_64bit;
+    long long first_position;
+    /* fp16 [batch][heads][n_tokens][head_dim], dense, 16-byte aligned: the
+     * layout of kivi_prefill (n_tokens == 1: of kivi_append and the decode
+     * calls).  No output may overlap an input. */
+    void *q_out, *k_out, *v_out;
+} kivi_qkv;
+
+/* Runs on the current device.  batch or n_tokens 0: nothing. */
+kivi_status kivi_qk_norm_rope(const kivi_qkv* args, kivi_stream_t stream);
+
+/*
+ * kivi_qk_norm_rope of one token per batch row, its k and v stored as the
+ * cache's newest residual row by the same kernel: the result of
+ * kivi_qk_norm_rope followed by kivi_append, one launch fewer.  The shape in
+ * args must be the cache's, with n_tokens == 1; k and v are required, k_out and
+ * v_out ignored, q optional.  Errors as for those two calls.
+ */
+kivi_status kivi_append_qkv(kivi_cache_t cache, const kivi_qkv* args, kivi_stream_t stream);
+
 /*
  * Failure detection.  Every wait of the tensor-core decode kernel on its bulk
  * copies is bounded (about 2 s); a copy that does not complete in time marks
