@@ -367,13 +367,12 @@ cudaError_t launch_decode_blocks(const BlockRows& r, const __half* q, const int*
     const Geometry& g = *r.g;
     const int nq = g.Hq / g.Hkv;
     const long long rows = (long long)r.n * g.Hkv;
-    // weights as in the dense decode: bytes of a quantized pair / 32, and 80 D
-    // bytes for a residual pair
+    // weights: bytes of a quantized pair / 32, and 40 D bytes / 32 for a residual tile
     const blocks_detail::Args base{r.buf, q, out, list, g.NB, g.part_bytes, g.slot_bytes, g.tile_bytes,
                                    g.k_resid_off, g.v_resid_off, g.R, g.Hq, g.Hkv, n_list, r.n_blocks, r.n_resid,
-                                   g.D * g.bits / 4 + 8 * g.D / g.G, 5 * g.D / 2, scale_log2};
+                                   g.D * g.bits / 4 + 8 * g.D / g.G, 5 * g.D / 4, scale_log2};
     auto units = [&](int nblk, int nres) {
-        return (long long)(n_list < nblk ? n_list : nblk) * (g.G / 32) + (nres + 31) / 32;
+        return (long long)(n_list < nblk ? n_list : nblk) * (g.G / 32) + (nres + 15) / 16;
     };
     if (!r.table) {
         const long long u = units(r.n_blocks, r.n_resid);

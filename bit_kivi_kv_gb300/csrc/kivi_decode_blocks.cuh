@@ -28,7 +28,6 @@ using namespace mma_detail;
 
 constexpr int kListCache = 64;      // list entries a warp keeps as byte offsets
 constexpr int kMaxCluster = 8;      // CTAs that share a row, at most (the portable cluster size)
-static_assert(kMaxCluster * kWarps <= 32, "the merge holds one partial a lane");
 
 struct Args {
     const uint8_t* cache;
@@ -39,7 +38,7 @@ struct Args {
     int R, Hq, Hkv;
     int n_list;
     int n_blocks, n_resid;          // dense: quantized blocks and residual rows of every row
-    int wq, wr;                     // weights of a tile pair and of a residual pair
+    int wq, wr;                     // weights of a tile pair and of a residual tile
     float scale_log2;
 };
 
@@ -77,9 +76,9 @@ __device__ __forceinline__ float4 ldc128(uint32_t a) {
     asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
     return v;
 }
-__device__ __forceinline__ float2 ldc64(uint32_t a) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+__device__ __forceinline__ float ldc32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ void mbar_arrive_u32(uint32_t bar) {
@@ -119,9 +118,16 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
     __shared__ __align__(16) uint32_t qfrag_all[kWarps][32 * C::QSTRIDE];
     __shared__ __align__(8) uint64_t full_bar[kWarps][C::STAGES];
     __shared__ long long off_all[kWarps][kListCache];
-    __shared__ __align__(16) float4 head_s[kWarps][NQ];   // a warp's (m, l, status) per query head
-    __shared__ float wgt_s[NQ][32];                       // the merge's weights
-    // per warp: the copy ring, then the warp's value sums [NQ][D] fp32
+    // the residual's query: fp16 hi and lo parts of each head, a padded row each
+    __shared__ __align__(16) __half qres[2 * NQ][D + 8];
+    // partial results: (m, l, status) per query head of each warp's residual
+    // tiles and of its listed blocks, the residual tiles' value sums, and the
+    // CTA's merged heads (its merged value sums take the place of rsum[0])
+    __shared__ __align__(16) float4 head_s[2 * kWarps][NQ];
+    __shared__ __align__(16) float rsum[kWarps][NQ * D];
+    __shared__ float wgt_s[NQ][2 * kWarps];
+    __shared__ __align__(16) float4 cta_head[NQ];
+    // per warp: the copy ring, then the listed blocks' value sums [NQ][D] fp32
     extern __shared__ __align__(128) uint8_t dyn_smem[];
     static_assert(NQ * D * 4 <= C::STAGES * C::STAGE_BYTES, "the value sums reuse the copy ring");
 
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
     const uint32_t eoff = 32u * jP + 8u * i;
     const long long tiles_bytes = (long long)C::TPB * a.tile_bytes;
 
-    // ---- this warp's share of the row: units [u0, u1) of P quantized pairs, then PR residual pairs ----
+    // ---- this warp's share of the row by weight: residual tiles (16 rows), then listed pairs ----
     int nblk, n_res;
     long long rslot;
     if constexpr (PAGED) {
@@ -169,22 +175,52 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
         n_res = a.n_resid;
         rslot = row;
     }
-    WorkMap wm{};
-    wm.P = (long long)min(a.n_list, nblk) * PPB;
-    wm.PR = (n_res + 31) / 32;
-    wm.wq = a.wq;
-    wm.wr = a.wr;
-    wm.Wt = wm.Ws = slot_weight(wm, wm.P, 0, wm.PR);
-    wm.n = csize * kWarps;
-    const long long worker = crank * kWarps + warp;
-    const int u0 = (int)first_unit_at(wm, map_begin(wm, worker)), u1 = (int)first_unit_at(wm, map_begin(wm, worker + 1));
-    const int wb = min(u0, (int)wm.P), we = min(u1, (int)wm.P);
-    const int rb = u0 - wb, re = u1 - we;
+    const int P = min(a.n_list, nblk) * PPB, T = (n_res + 15) / 16;
+    const long long wt = (long long)T * a.wr + (long long)P * a.wq;
+    auto ceil_div = [](long long x, int y) {      // (64-bit division only for very long lists)
+        return x < (1LL << 30) ? (int)(((unsigned)x + (unsigned)y - 1u) / (unsigned)y) : (int)((x + y - 1) / y);
+    };
+    auto tile_at = [&](long long y) { return min(T, ceil_div(y, a.wr)); };            // first tile starting at or after y
+    auto pair_at = [&](long long y) { return ceil_div(max(0LL, y - (long long)T * a.wr), a.wq); };
+    const int worker = (int)crank * kWarps + warp, workers = (int)csize * kWarps;     // (workers: a power of two)
+    const long long y0 = worker * wt / workers, y1 = (worker + 1) * wt / workers;
+    const int tb = tile_at(y0), te = tile_at(y1);
+    const int wb = pair_at(y0), we = pair_at(y1);
 
     // everything below reads what earlier kernels on the stream may have written
     griddepcontrol_wait();
     griddepcontrol_launch_dependents();
 
+    // the first residual tile's rows and the query are on their way while the
+    // list is read: lane (g, i) holds channels 32 j + 8 i .. + 7 of rows g, g + 8
+    constexpr int DJ = D / 32;
+    const __half* kr = reinterpret_cast<const __half*>(a.cache + a.k_resid_off) + rslot * a.R * D;
+    const __half* vr = reinterpret_cast<const __half*>(a.cache + a.v_resid_off) + rslot * a.R * D;
+    uint4 kx[2][DJ], vx[2][DJ];
+    auto load_rows = [&](int tile) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int r = 16 * tile + g + 8 * s;
+#pragma unroll
+            for (int j = 0; j < DJ; ++j) {
+                kx[s][j] = vx[s][j] = make_uint4(0, 0, 0, 0);
+                if (r < n_res) {
+                    kx[s][j] = ldg_stream(kr + (long long)r * D + 32 * j + 8 * i);
+                    vx[s][j] = ldg_stream(vr + (long long)r * D + 32 * j + 8 * i);
+                }
+            }
+        }
+    };
+    constexpr int QPT = (NQ * D / 2 + kThreads - 1) / kThreads;     // query channel pairs per thread
+    __half2 qv[QPT];
+#pragma unroll
+    for (int x = 0; x < QPT; ++x) {
+        const int idx = tid + x * kThreads;
+        qv[x] = __half2half2(__ushort_as_half(0));
+        if (idx < NQ * D / 2)
+            qv[x] = *reinterpret_cast<const __half2*>(a.q + ((long long)b * a.Hq + hk * NQ) * D + 2 * idx);
+    }
+    if (tb < te) load_rows(tb);
     const int* list = a.list + row * a.n_list;
     uint32_t status = 0;       // 1: a bulk copy did not complete in time; 2: an entry outside the cache
     // entries [j0, j0 + n) of the list as byte offsets of the blocks' key parts; -1: no block
@@ -249,26 +285,27 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
         __syncwarp();
     };
     if (k < we) begin_part();
-    const __half* kr = reinterpret_cast<const __half*>(a.cache + a.k_resid_off) + rslot * a.R * D;
-    const __half* vr = reinterpret_cast<const __half*>(a.cache + a.v_resid_off) + rslot * a.R * D;
-    if (lane == 0 && rb < re) {                   // the residual rows into L2 ahead of their plain loads
-        const int n = min(32 * re, n_res) - 32 * rb;
-        prefetch_l2(kr + 32LL * rb * D, (uint32_t)(n * D * 2));
-        prefetch_l2(vr + 32LL * rb * D, (uint32_t)(n * D * 2));
-    }
-    for (int idx = tid; idx < NQ * D / 2; idx += kThreads) {
-        const int j = idx / (D / 2), cp = idx % (D / 2);
-        const float2 qv = __half22float2(
-            *reinterpret_cast<const __half2*>(a.q + ((long long)b * a.Hq + hk * NQ + j) * D + 2 * cp));
-        const float x0 = qv.x * a.scale_log2, x1 = qv.y * a.scale_log2;
-        qf[j][2 * cp] = x0;
-        qf[j][2 * cp + 1] = x1;
-        const float cs = pow2i(-BITS * ((cp >> 2) % (8 / BITS)));
-        const float y0 = x0 * cs, y1 = x1 * cs;
-        const uint32_t hic = pack_f16x2(y0, y1);
-        const float2 hcf = unpack_f16x2(hic);
-        qhc_s[j][cp] = hic;
-        qlc_s[j][cp] = pack_f16x2(y0 - hcf.x, y1 - hcf.y);
+#pragma unroll
+    for (int x = 0; x < QPT; ++x) {
+        const int idx = tid + x * kThreads;
+        if (idx < NQ * D / 2) {
+            const int j = idx / (D / 2), cp = idx % (D / 2);
+            const float2 f = __half22float2(qv[x]);
+            const float x0 = f.x * a.scale_log2, x1 = f.y * a.scale_log2;
+            qf[j][2 * cp] = x0;
+            qf[j][2 * cp + 1] = x1;
+            const uint32_t hi = pack_f16x2(x0, x1);
+            const float2 hf = unpack_f16x2(hi);
+            *reinterpret_cast<uint32_t*>(&qres[2 * j][2 * cp]) = hi;
+            *reinterpret_cast<uint32_t*>(&qres[2 * j + 1][2 * cp]) = pack_f16x2(x0 - hf.x, x1 - hf.y);
+            // channels 2cp, 2cp+1 have class cp / 4: their codes read as code * 2^(BITS*pos - 24)
+            const float cs = pow2i(-BITS * ((cp >> 2) % (8 / BITS)));
+            const float y0 = x0 * cs, y1 = x1 * cs;
+            const uint32_t hic = pack_f16x2(y0, y1);
+            const float2 hcf = unpack_f16x2(hic);
+            qhc_s[j][cp] = hic;
+            qlc_s[j][cp] = pack_f16x2(y0 - hcf.x, y1 - hcf.y);
+        }
     }
     __syncthreads();
 
@@ -345,6 +382,69 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
             w[0] = x.x; w[1] = x.y;
         }
     };
+    // ---- the residual tiles: 16 fp16 rows each, straight from memory.  The
+    // 16-byte loads hand lane i eight consecutive channels, so the MMAs' k
+    // (keys) and m (values) indices run over the channels in another order than
+    // the tiles': k-steps 2j, 2j+1 hold channels 32 j + 8 i + 0..3, + 4..7, and
+    // m-tile 2j+u has row g at channel 32 j + 8 (g / 2) + 4 u + g % 2, row g + 8
+    // two further.  The partial result is kept apart from the blocks'. ----
+    for (int tile = tb; tile < te; ++tile) {
+        if (tile > tb) load_rows(tile);
+        const bool okg = 16 * tile + g < n_res, okg8 = 16 * tile + g + 8 < n_res;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < DJ; ++j) {
+            uint4 bq = make_uint4(0, 0, 0, 0);
+            if (g < 2 * NQ) bq = *reinterpret_cast<const uint4*>(&qres[g < 2 * NQ ? g : 0][32 * j + 8 * i]);
+            const uint32_t f0[4] = {kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y};
+            const uint32_t f1[4] = {kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w};
+            mma16816(c, f0, bq.x, bq.y);
+            mma16816(c, f1, bq.z, bq.w);
+        }
+        const float sc[4] = {okg ? c[0] + c[1] : -INFINITY, okg8 ? c[2] + c[3] : -INFINITY, -INFINITY, -INFINITY};
+        float p[4];
+        softmax(sc, p, 1.f);
+        float prb[4];
+        gather(p[0], p[1], prb);
+        uint32_t ph01, ph89, pl01, pl89;
+        split_p(prb, ph01, ph89, pl01, pl89);
+        const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
+#pragma unroll
+        for (int j = 0; j < DJ; ++j) {
+            const uint32_t f0[4] = {movmatrix_trans(vx[0][j].x), movmatrix_trans(vx[0][j].y),
+                                    movmatrix_trans(vx[1][j].x), movmatrix_trans(vx[1][j].y)};
+            mma16816(o[2 * j], f0, pb0, pb1);
+            const uint32_t f1[4] = {movmatrix_trans(vx[0][j].z), movmatrix_trans(vx[0][j].w),
+                                    movmatrix_trans(vx[1][j].z), movmatrix_trans(vx[1][j].w)};
+            mma16816(o[2 * j + 1], f1, pb0, pb1);
+        }
+    }
+    auto sum_l = [&]() {                          // l over the lanes of a head
+        float lt = l;
+        lt += __shfl_xor_sync(kFull, lt, 4);
+        lt += __shfl_xor_sync(kFull, lt, 8);
+        lt += __shfl_xor_sync(kFull, lt, 16);
+        return lt;
+    };
+    {
+        const float lt = sum_l();
+        if (g == 0 && i < NQ) head_s[warp][i] = make_float4(m, lt, 0.f, 0.f);
+        if (tb < te && hO < NQ) {                 // every group slot's columns hold the same sums: each writes some
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+                if (mt % GB != jO) continue;
+                const int ch = 32 * (mt / 2) + 8 * (g / 2) + 4 * (mt % 2) + g % 2;
+                rsum[warp][hO * D + ch] = o[mt][0] + o[mt][1];
+                rsum[warp][hO * D + ch + 2] = o[mt][2] + o[mt][3];
+            }
+        }
+        m = -INFINITY;
+        l = 0.f;
+        fresh = true;
+#pragma unroll
+        for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    }
+
     // ---- the listed blocks ----
     while (k < we) {
         if (k >= kend) begin_part();
@@ -430,53 +530,6 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
         const float s1 = pow2i(24 - BITS * ((2 * mt + 1) % (8 / BITS)));
         o[mt][0] *= s0; o[mt][1] *= s0; o[mt][2] *= s1; o[mt][3] *= s1;
     }
-    // ---- the residual pairs: 32 fp16 rows each, A operands straight from memory ----
-    if (rb < re) {
-        build_q_frags<C, D, NQ, QB_REGS>(nullptr, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);   // step 1, zero 0
-        for (int rp = rb; rp < re; ++rp) {
-            float sc[4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int rw = 32 * rp + 16 * t;
-                const bool okg = rw + g < n_res, okg8 = rw + g + 8 < n_res;
-                const __half* kg = kr + (long long)(rw + g) * D;
-                const __half* kg8 = kg + 8 * D;
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    const int ch = 16 * kk + 2 * i;
-                    uint32_t af[4];
-                    af[0] = okg ? *reinterpret_cast<const uint32_t*>(kg + ch) : 0u;
-                    af[1] = okg8 ? *reinterpret_cast<const uint32_t*>(kg8 + ch) : 0u;
-                    af[2] = okg ? *reinterpret_cast<const uint32_t*>(kg + ch + 8) : 0u;
-                    af[3] = okg8 ? *reinterpret_cast<const uint32_t*>(kg8 + ch + 8) : 0u;
-                    const uint2 bq = qbk(kk);
-                    mma16816(c, af, bq.x, bq.y);
-                }
-                sc[2 * t] = okg ? c[0] + c[1] : -INFINITY;
-                sc[2 * t + 1] = okg8 ? c[2] + c[3] : -INFINITY;
-            }
-            float p[4];
-            softmax(sc, p, 1.f);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float prb[4];
-                gather(p[2 * t], p[2 * t + 1], prb);
-                uint32_t ph01, ph89, pl01, pl89;
-                split_p(prb, ph01, ph89, pl01, pl89);
-                const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
-                const int rw = 32 * rp + 16 * t;
-                const __half* vg = vr + (long long)(rw + g) * D;
-#pragma unroll
-                for (int mt = 0; mt < KS; ++mt) {
-                    uint32_t af[4];
-                    vt_frag_rows<D>(vg, vg + 8 * D, rw + g < n_res, rw + g + 8 < n_res, mt, i, af);
-                    mma16816(o[mt], af, pb0, pb1);
-                }
-            }
-        }
-    }
-
     // ---- this warp's partial result ----
     const uint32_t st_all = __reduce_or_sync(kFull, status);
 #pragma unroll
@@ -484,10 +537,7 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
         zeta[f] += __shfl_xor_sync(kFull, zeta[f], 1);
         zeta[f] += __shfl_xor_sync(kFull, zeta[f], 2);
     }
-    float lt = l;
-    lt += __shfl_xor_sync(kFull, lt, 4);
-    lt += __shfl_xor_sync(kFull, lt, 8);
-    lt += __shfl_xor_sync(kFull, lt, 16);
+    const float lt = sum_l();
     float zo[NBF];
 #pragma unroll
     for (int f = 0; f < NBF; ++f) zo[f] = __shfl_sync(kFull, zeta[f], 8 * i);
@@ -503,56 +553,76 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
             }
         }
     }
-    if (g == 0 && i < NQ) head_s[warp][i] = make_float4(m, lt, (float)st_all, 0.f);
+    if (g == 0 && i < NQ) head_s[kWarps + warp][i] = make_float4(m, lt, (float)st_all, 0.f);
 
-    // ---- the log-sum-exp merge over the cluster's warps ----
-    __syncwarp();
-    if (csize > 1) {
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
-    }
-    const int parts = (int)csize * kWarps;
+    // ---- the log-sum-exp merge: the CTA's partials, then the cluster's CTAs ----
     static_assert(NQ <= kWarps, "one warp per query head in the merge");
-    if (warp < NQ) {
-        float mj = -INFINITY, lj = 0.f;
-        bool bad = false;
-        if (lane < parts) {
-            const float4 x = ldc128(cluster_map(smem_u32(&head_s[lane % kWarps][warp]), lane / kWarps));
-            mj = x.x;
-            lj = x.y;
-            bad = x.z != 0.f;
-        }
-        float M = mj;
+    // weights 2^(m - M) and the sum L of head `warp` from each lane's (m, l, status)
+    auto weigh = [&](float4 x, float& M, float& L, bool& bad) {
+        M = x.x;
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, s));
-        const float e = mj == -INFINITY ? 0.f : fast_exp2(mj - M);
-        float L = lj * e;
+        const float e = x.x == -INFINITY ? 0.f : fast_exp2(x.x - M);
+        L = x.y * e;
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(kFull, L, s);
-        bad = __any_sync(kFull, bad);
-        wgt_s[warp][lane] = bad ? NAN : e / L;    // (a row of one warp's worth of work: e is 0 or 1, L is l)
+        bad = __any_sync(kFull, x.z != 0.f);
+        return e;
+    };
+    const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    __syncthreads();
+    if (warp < NQ) {
+        float M, L;
+        bool bad;
+        const float e = weigh(lane < 2 * kWarps ? head_s[lane][warp] : none, M, L, bad);
+        if (lane < 2 * kWarps) wgt_s[warp][lane] = csize > 1 ? e : bad ? NAN : e / L;
+        if (lane == 0) cta_head[warp] = make_float4(M, L, bad ? 1.f : 0.f, 0.f);
     }
     __syncthreads();
-    for (int idx = (int)crank * kThreads + tid; idx < NQ * D / 2; idx += (int)csize * kThreads) {
-        const int h = idx / (D / 2), c = 2 * (idx % (D / 2));
-        float s0 = 0.f, s1 = 0.f;
-        for (int j = 0; j < parts; ++j) {
+    __half* out = a.out + ((long long)b * a.Hq + hk * NQ) * D;
+    for (int idx = tid; idx < NQ * D; idx += kThreads) {
+        const int h = idx / D;
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2 * kWarps; ++j) {
             const float w = wgt_s[h][j];
-            if (w == 0.f) continue;               // a partial without tokens
-            const uint32_t at = smem_u32(dyn_smem + (j % kWarps) * C::STAGES * C::STAGE_BYTES) + (h * D + c) * 4;
-            const float2 v = ldc64(cluster_map(at, j / kWarps));
-            s0 = fmaf(v.x, w, s0);
-            s1 = fmaf(v.y, w, s1);
+            // (a partial without tokens has weight 0 and, of the residual, no sums)
+            const float v = j < kWarps ? rsum[j][idx]
+                                       : reinterpret_cast<const float*>(dyn_smem + (j - kWarps) * C::STAGES * C::STAGE_BYTES)[idx];
+            s = w == 0.f ? s : fmaf(v, w, s);
         }
-        *reinterpret_cast<__half2*>(a.out + ((long long)b * a.Hq + hk * NQ + h) * D + c) = __floats2half2_rn(s0, s1);
+        if (csize > 1) rsum[0][idx] = s;
+        else out[idx] = __float2half_rn(s);
+    }
+    if (csize == 1) return;
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (warp < NQ) {
+        float M, L;
+        bool bad;
+        const float4 x = lane < (int)csize ? ldc128(cluster_map(smem_u32(&cta_head[warp]), lane)) : none;
+        const float e = weigh(x, M, L, bad);
+        if (lane < (int)csize) wgt_s[warp][lane] = bad ? NAN : e / L;
+    }
+    __syncthreads();
+    const int span = NQ * D / (int)csize;         // this CTA's share of the output
+    for (int at = tid; at < span; at += kThreads) {
+        const int idx = (int)crank * span + at;
+        const uint32_t base = smem_u32(&rsum[0][idx]);
+        float v[kMaxCluster], s = 0.f;
+#pragma unroll
+        for (int j = 0; j < kMaxCluster; ++j) v[j] = j < (int)csize ? ldc32(cluster_map(base, j)) : 0.f;
+#pragma unroll
+        for (int j = 0; j < kMaxCluster; ++j) {
+            const float w = j < (int)csize ? wgt_s[idx / D][j] : 0.f;
+            s = w == 0.f ? s : fmaf(v[j], w, s);
+        }
+        out[idx] = __float2half_rn(s);
     }
     __syncwarp();
-    if (csize > 1) {                              // no CTA leaves while another reads its shared memory
-        cluster_arrive();
-        cluster_wait();
-    }
+    cluster_arrive();                             // no CTA leaves while another reads its shared memory
+    cluster_wait();
 }
 
 }  // namespace blocks_detail
