@@ -10,11 +10,11 @@
 // the log2 domain, everything summed in fp32).
 //
 // What differs is the shape of the work: a list has tens of blocks, so a call
-// reads little and its latency counts.  One thread-block cluster takes one
-// row; its warps split the row's tile pairs (32 tokens) and residual pairs by
-// weight, stage their partial results (m, l, o) in shared memory, and merge
-// them through distributed shared memory: one launch, no workspace, no second
-// kernel.  The blocks' addresses come from the list (paged: through the block
+// reads little and its latency counts.  One CTA, or a thread-block cluster of
+// them, takes one row; its warps split the row's residual tiles (16 rows) and
+// tile pairs (32 tokens) by weight, stage their partial results (m, l, o) in
+// shared memory, and merge them there (a cluster through distributed shared
+// memory): one launch, no workspace, no second kernel.  The blocks' addresses come from the list (paged: through the block
 // table), which each warp turns into byte offsets in shared memory, a part of
 // the list at a time.
 #pragma once
@@ -28,6 +28,12 @@ using namespace mma_detail;
 
 constexpr int kListCache = 64;      // list entries a warp keeps as byte offsets
 constexpr int kMaxCluster = 8;      // CTAs that share a row, at most (the portable cluster size)
+constexpr int kMaxRowWarps = 16;    // warps of a CTA, at most: two partials each, one a lane in the merge
+
+// Registers a thread may have: 128 (16 warps an SM), and at head_dim 128 with
+// four query heads per kv head 168 (12 warps an SM).
+template <int D, int NQ>
+constexpr int kCtaWarps = (D == 128 && NQ == 4) ? 12 : kMaxRowWarps;
 
 struct Args {
     const uint8_t* cache;
@@ -71,25 +77,48 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t a, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
     return d;
 }
-__device__ __forceinline__ float4 ldc128(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-    return v;
+__device__ __forceinline__ void stc128(uint32_t a, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
 }
-__device__ __forceinline__ float ldc32(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
-    return v;
+__device__ __forceinline__ void stc32(uint32_t a, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_u32(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The MMAs of one 16-token tile, A fragments from the lane's words w, B
-// fragments from bfrag(t): keys sum every k-step into acc[0], values m-tile t
+// The MMAs of 16-token tiles, A fragments from the lane's words w, B fragments
+// from bfrag(t): a key tile sums every k-step into acc, a value tile m-tile t
 // into acc[t].
-template <int BITS, bool VALUES, int W, int KS, int N, typename B>
-__device__ __forceinline__ void tile_mma(const uint32_t (&w)[W], const B& bfrag, float (&acc)[N][4]) {
+template <int BITS, int W, int KS, typename B>
+__device__ __forceinline__ void key_mma(const uint32_t (&w)[W], const B& bfrag, float (&acc)[4]) {
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+        uint32_t fa[4];
+        a_frag_inline<BITS, false, W>(w, t, fa);
+        const uint2 bq = bfrag(t);
+        mma16816(acc, fa, bq.x, bq.y);
+    }
+}
+template <int BITS, int W, int KS, typename B>
+__device__ __forceinline__ void key_mma2(const uint32_t (&w)[W], const uint32_t (&v)[W], const B& bfrag,
+                                         float (&acc)[4], float (&acc2)[4]) {
+    uint32_t w8[W], v8[W];
+#pragma unroll
+    for (int x = 0; x < W; ++x) { w8[x] = w[x] >> 8; v8[x] = v[x] >> 8; }
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+        uint32_t fa[4], fb[4];
+        a_frag<BITS, false, W>(w, w8, t, fa);
+        a_frag<BITS, false, W>(v, v8, t, fb);
+        const uint2 bq = bfrag(t);
+        mma16816(acc, fa, bq.x, bq.y);
+        mma16816(acc2, fb, bq.x, bq.y);
+    }
+}
+template <int BITS, int W, int KS, typename B>
+__device__ __forceinline__ void value_mma(const uint32_t (&w)[W], const B& bfrag, float (&acc)[KS][4]) {
     uint32_t w8[W];
     if constexpr (BITS != 8) {
 #pragma unroll
@@ -98,48 +127,59 @@ __device__ __forceinline__ void tile_mma(const uint32_t (&w)[W], const B& bfrag,
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
         uint32_t fa[4];
-        if constexpr (BITS == 8) a_frag_inline<BITS, VALUES, W>(w, t, fa);
-        else a_frag<BITS, VALUES, W>(w, w8, t, fa);
+        if constexpr (BITS == 8) a_frag_inline<BITS, true, W>(w, t, fa);
+        else a_frag<BITS, true, W>(w, w8, t, fa);
         const uint2 bq = bfrag(t);
-        mma16816(acc[VALUES ? t : 0], fa, bq.x, bq.y);
+        mma16816(acc[t], fa, bq.x, bq.y);
     }
 }
 
+// Dynamic shared memory of a CTA: per warp its copy ring (which later takes the
+// listed blocks' value sums [NQ][D] fp32), the key fragment table, the list's
+// offsets and the residual tiles' value sums [NQ][D] fp32.
+template <int D, int BITS, int NQ, int G>
+struct Smem {
+    using C = Cfg<D, BITS, NQ, G>;
+    static constexpr int RING = C::STAGES * C::STAGE_BYTES;
+    static constexpr int FRAG = RING, OFFS = FRAG + 32 * C::QSTRIDE * 4, SUMS = OFFS + kListCache * 8;
+    static constexpr int WARP = (SUMS + NQ * D * 4 + 127) / 128 * 128;
+    static_assert(NQ * D * 4 <= RING, "the value sums reuse the copy ring");
+};
+
 template <int D, int BITS, int NQ, int G, bool PAGED>
-__global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
+__global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     decode_blocks_kernel(const __grid_constant__ typename ArgsOf<PAGED>::type a) {
     using C = Cfg<D, BITS, NQ, G>;
+    using S = Smem<D, BITS, NQ, G>;
     constexpr int KS = C::KSTEPS, W = C::W, NGRP = C::NGRP, GB = C::GB, NBF = C::NBF;
     constexpr int PPB = C::TPB / 2;                   // tile pairs per block
     // the row's scaled query (fp32) and the fp16 hi / lo parts of it times the
     // code scale 2^-(BITS*pos), shared by the CTA's warps
     __shared__ __align__(16) float qf[NQ][D];
     __shared__ uint32_t qhc_s[NQ][D / 2], qlc_s[NQ][D / 2];
-    __shared__ __align__(16) uint32_t qfrag_all[kWarps][32 * C::QSTRIDE];
-    __shared__ __align__(8) uint64_t full_bar[kWarps][C::STAGES];
-    __shared__ long long off_all[kWarps][kListCache];
+    __shared__ __align__(8) uint64_t full_bar[kMaxRowWarps][C::STAGES];
     // the residual's query: fp16 hi and lo parts of each head, a padded row each
     __shared__ __align__(16) __half qres[2 * NQ][D + 8];
     // partial results: (m, l, status) per query head of each warp's residual
-    // tiles and of its listed blocks, the residual tiles' value sums, and the
-    // CTA's merged heads (its merged value sums take the place of rsum[0])
-    __shared__ __align__(16) float4 head_s[2 * kWarps][NQ];
-    __shared__ __align__(16) float rsum[kWarps][NQ * D];
-    __shared__ float wgt_s[NQ][2 * kWarps];
+    // tiles and of its listed blocks, the merge's weights, the CTA's merged heads
+    __shared__ __align__(16) float4 head_s[2 * kMaxRowWarps][NQ];
+    __shared__ float wgt_s[NQ][2 * kMaxRowWarps];
     __shared__ __align__(16) float4 cta_head[NQ];
-    // per warp: the copy ring, then the listed blocks' value sums [NQ][D] fp32
+    // from the cluster's CTAs: their value sums of this CTA's outputs, and their heads
+    __shared__ __align__(16) float recv_s[NQ * D];
+    __shared__ __align__(16) float4 recv_head[kMaxCluster][NQ];
     extern __shared__ __align__(128) uint8_t dyn_smem[];
-    static_assert(NQ * D * 4 <= C::STAGES * C::STAGE_BYTES, "the value sums reuse the copy ring");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, i = lane & 3;
+    const int warps = blockDim.x >> 5;
     const uint32_t crank = cluster_rank(), csize = cluster_size();
     const long long row = blockIdx.x / csize;
     const int b = (int)(row / a.Hkv), hk = (int)(row % a.Hkv);
-    uint32_t* qfrag = qfrag_all[warp];
-    uint8_t* ring = dyn_smem + warp * C::STAGES * C::STAGE_BYTES;
+    uint8_t* ring = dyn_smem + warp * S::WARP;
+    uint32_t* qfrag = reinterpret_cast<uint32_t*>(ring + S::FRAG);
+    long long* offs = reinterpret_cast<long long*>(ring + S::OFFS);
     uint64_t* bars = full_bar[warp];
-    long long* offs = off_all[warp];
     for (int idx = lane; idx < 32 * C::QSTRIDE; idx += 32) qfrag[idx] = 0u;   // unused columns stay 0
     if (lane == 0) {
 #pragma unroll
@@ -147,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
         fence_mbar_init();
     }
     __syncwarp();
+    if (csize > 1) cluster_arrive();              // waited for before the merge writes to the other CTAs
     int qoff[D / 64];     // this lane's Qt table offsets (channel pairs (D/64)*lane + j)
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
@@ -175,24 +216,31 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
         n_res = a.n_resid;
         rslot = row;
     }
+    // Every worker (a warp) gets its share of the tiles, and pairs up to its
+    // share of the weight: tiles [w T / n, (w + 1) T / n), pairs from
+    // pairs_before(w), the largest count that the weight position of a worker up
+    // to w leaves beside the tiles before it.
     const int P = min(a.n_list, nblk) * PPB, T = (n_res + 15) / 16;
+    const int workers = (int)csize * warps, worker = (int)crank * warps + warp;
+    const int tb = (int)((long long)worker * T / workers), te = (int)((long long)(worker + 1) * T / workers);
     const long long wt = (long long)T * a.wr + (long long)P * a.wq;
-    auto ceil_div = [](long long x, int y) {      // (64-bit division only for very long lists)
-        return x < (1LL << 30) ? (int)(((unsigned)x + (unsigned)y - 1u) / (unsigned)y) : (int)((x + y - 1) / y);
+    auto pairs_upto = [&](auto w) {
+        using I = decltype(w);                    // 32-bit unless the list is very long
+        int most = 0;
+        for (I v = lane; v <= w; v += 32) {
+            const I y = v * (I)wt / (I)workers - v * (I)T / (I)workers * (I)a.wr;
+            most = max(most, (int)min((I)P, (max((I)0, y) + (I)a.wq - 1) / (I)a.wq));
+        }
+        return __reduce_max_sync(kFull, most);
     };
-    auto tile_at = [&](long long y) { return min(T, ceil_div(y, a.wr)); };            // first tile starting at or after y
-    auto pair_at = [&](long long y) { return ceil_div(max(0LL, y - (long long)T * a.wr), a.wq); };
-    const int worker = (int)crank * kWarps + warp, workers = (int)csize * kWarps;     // (workers: a power of two)
-    const long long y0 = worker * wt / workers, y1 = (worker + 1) * wt / workers;
-    const int tb = tile_at(y0), te = tile_at(y1);
-    const int wb = pair_at(y0), we = pair_at(y1);
+    auto pairs_before = [&](int w) { return wt < (1 << 22) ? pairs_upto(w) : pairs_upto((long long)w); };
+    const int wb = pairs_before(worker), we = worker + 1 == workers ? P : pairs_before(worker + 1);
 
     // everything below reads what earlier kernels on the stream may have written
     griddepcontrol_wait();
     griddepcontrol_launch_dependents();
 
-    // the first residual tile's rows and the query are on their way while the
-    // list is read: lane (g, i) holds channels 32 j + 8 i .. + 7 of rows g, g + 8
+    // a residual tile's rows: lane (g, i) holds channels 32 j + 8 i .. + 7 of rows g, g + 8
     constexpr int DJ = D / 32;
     const __half* kr = reinterpret_cast<const __half*>(a.cache + a.k_resid_off) + rslot * a.R * D;
     const __half* vr = reinterpret_cast<const __half*>(a.cache + a.v_resid_off) + rslot * a.R * D;
@@ -211,39 +259,31 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
             }
         }
     };
-    constexpr int QPT = (NQ * D / 2 + kThreads - 1) / kThreads;     // query channel pairs per thread
-    __half2 qv[QPT];
-#pragma unroll
-    for (int x = 0; x < QPT; ++x) {
-        const int idx = tid + x * kThreads;
-        qv[x] = __half2half2(__ushort_as_half(0));
-        if (idx < NQ * D / 2)
-            qv[x] = *reinterpret_cast<const __half2*>(a.q + ((long long)b * a.Hq + hk * NQ) * D + 2 * idx);
-    }
-    if (tb < te) load_rows(tb);
     const int* list = a.list + row * a.n_list;
     uint32_t status = 0;       // 1: a bulk copy did not complete in time; 2: an entry outside the cache
-    // entries [j0, j0 + n) of the list as byte offsets of the blocks' key parts; -1: no block
-    auto fill = [&](int j0, int n) {
-        for (int j = lane; j < n; j += 32) {
-            const int e = __ldg(list + j0 + j);
-            long long off = -1;
-            if (e >= nblk) {
-                status |= 2u;
-            } else if (e >= 0) {
-                if constexpr (PAGED) {
-                    const int pg = __ldg(a.table + (long long)a.seqs[b].seq * a.max_blocks + e);
-                    if ((unsigned)pg < (unsigned)a.n_pages)
-                        off = ((long long)pg * a.Hkv + hk) * 2 * a.part_bytes;
-                    else
-                        status |= 2u;
-                } else {
-                    off = row * a.slot_bytes + (long long)e * a.part_bytes;
-                }
+    // entries j0 + lane, j0 + 32 + lane of the n entries from j0 on (as `none` past them)
+    auto list_entry = [&](int j, int n) {
+        int e = -1;                               // (volatile: not moved behind the loads that follow it)
+        if (j < n) asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(e) : "l"(list + j));
+        return e;
+    };
+    // entry e as the byte offset of its block's key part; -1: no block
+    auto offset_of = [&](int e) {
+        long long off = -1;
+        if (e >= nblk) {
+            status |= 2u;
+        } else if (e >= 0) {
+            if constexpr (PAGED) {
+                const int pg = __ldg(a.table + (long long)a.seqs[b].seq * a.max_blocks + e);
+                if ((unsigned)pg < (unsigned)a.n_pages)
+                    off = ((long long)pg * a.Hkv + hk) * 2 * a.part_bytes;
+                else
+                    status |= 2u;
+            } else {
+                off = row * a.slot_bytes + (long long)e * a.part_bytes;
             }
-            offs[j] = off;
         }
-        __syncwarp();
+        return off;
     };
     int k = wb;                // next pair to process
     int j0 = 0, kend = wb;     // the part of the list in offs: entries from j0, pairs below kend
@@ -272,40 +312,54 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
             tma_1d_u32(dst + C::VE, vp + tiles_bytes + t * C::ENT, 2 * C::ENT, bar);
         }
     };
-    // the list from pair k on into offs, and the first copies of that part
-    auto begin_part = [&]() {
+    // the part of the list from pair k on: its entries (two a lane), ...
+    static_assert(kListCache == 64, "two entries a lane");
+    int e0 = -1, e1 = -1;
+    auto read_part = [&]() {
         j0 = k / PPB;
-        const int n = min((we - 1) / PPB - j0 + 1, kListCache);
-        kend = min(we, (j0 + n) * PPB);
-        fill(j0, n);
+        const int end = min((we - 1) / PPB + 1, j0 + kListCache);
+        kend = min(we, end * PPB);
+        e0 = list_entry(j0 + lane, end);
+        e1 = list_entry(j0 + 32 + lane, end);
+    };
+    // ... then their offsets, and the part's first copies
+    auto begin_part = [&]() {
+        offs[lane] = offset_of(e0);
+        offs[32 + lane] = offset_of(e1);
+        __syncwarp();
         if (lane == 0) {
             fence_proxy_async();
             for (int u = 0; u < C::STAGES && k + u < kend; ++u) issue(k + u, item + u);
         }
         __syncwarp();
     };
+    if (k < we) read_part();
+    __half2 qv = __half2half2(__ushort_as_half(0));                // a channel pair of the query
+    const __half2* qp = reinterpret_cast<const __half2*>(a.q + ((long long)b * a.Hq + hk * NQ) * D);
+    if (tid < NQ * D / 2) qv = qp[tid];
     if (k < we) begin_part();
-#pragma unroll
-    for (int x = 0; x < QPT; ++x) {
-        const int idx = tid + x * kThreads;
-        if (idx < NQ * D / 2) {
-            const int j = idx / (D / 2), cp = idx % (D / 2);
-            const float2 f = __half22float2(qv[x]);
-            const float x0 = f.x * a.scale_log2, x1 = f.y * a.scale_log2;
-            qf[j][2 * cp] = x0;
-            qf[j][2 * cp + 1] = x1;
-            const uint32_t hi = pack_f16x2(x0, x1);
-            const float2 hf = unpack_f16x2(hi);
-            *reinterpret_cast<uint32_t*>(&qres[2 * j][2 * cp]) = hi;
-            *reinterpret_cast<uint32_t*>(&qres[2 * j + 1][2 * cp]) = pack_f16x2(x0 - hf.x, x1 - hf.y);
-            // channels 2cp, 2cp+1 have class cp / 4: their codes read as code * 2^(BITS*pos - 24)
-            const float cs = pow2i(-BITS * ((cp >> 2) % (8 / BITS)));
-            const float y0 = x0 * cs, y1 = x1 * cs;
-            const uint32_t hic = pack_f16x2(y0, y1);
-            const float2 hcf = unpack_f16x2(hic);
-            qhc_s[j][cp] = hic;
-            qlc_s[j][cp] = pack_f16x2(y0 - hcf.x, y1 - hcf.y);
-        }
+    if (lane == 0 && tb < te) {                   // the residual rows into L2 behind the first copies
+        const uint32_t bytes = (uint32_t)((min(16 * te, n_res) - 16 * tb) * D * 2);
+        prefetch_l2(kr + 16LL * tb * D, bytes);
+        prefetch_l2(vr + 16LL * tb * D, bytes);
+    }
+    for (int idx = tid; idx < NQ * D / 2; idx += blockDim.x) {
+        const int j = idx / (D / 2), cp = idx % (D / 2);
+        const float2 f = __half22float2(idx == tid ? qv : qp[idx]);
+        const float x0 = f.x * a.scale_log2, x1 = f.y * a.scale_log2;
+        qf[j][2 * cp] = x0;
+        qf[j][2 * cp + 1] = x1;
+        const uint32_t hi = pack_f16x2(x0, x1);
+        const float2 hf = unpack_f16x2(hi);
+        *reinterpret_cast<uint32_t*>(&qres[2 * j][2 * cp]) = hi;
+        *reinterpret_cast<uint32_t*>(&qres[2 * j + 1][2 * cp]) = pack_f16x2(x0 - hf.x, x1 - hf.y);
+        // channels 2cp, 2cp+1 have class cp / 4: their codes read as code * 2^(BITS*pos - 24)
+        const float cs = pow2i(-BITS * ((cp >> 2) % (8 / BITS)));
+        const float y0 = x0 * cs, y1 = x1 * cs;
+        const uint32_t hic = pack_f16x2(y0, y1);
+        const float2 hcf = unpack_f16x2(hic);
+        qhc_s[j][cp] = hic;
+        qlc_s[j][cp] = pack_f16x2(y0 - hcf.x, y1 - hcf.y);
     }
     __syncthreads();
 
@@ -382,72 +436,12 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
             w[0] = x.x; w[1] = x.y;
         }
     };
-    // ---- the residual tiles: 16 fp16 rows each, straight from memory.  The
-    // 16-byte loads hand lane i eight consecutive channels, so the MMAs' k
-    // (keys) and m (values) indices run over the channels in another order than
-    // the tiles': k-steps 2j, 2j+1 hold channels 32 j + 8 i + 0..3, + 4..7, and
-    // m-tile 2j+u has row g at channel 32 j + 8 (g / 2) + 4 u + g % 2, row g + 8
-    // two further.  The partial result is kept apart from the blocks'. ----
-    for (int tile = tb; tile < te; ++tile) {
-        if (tile > tb) load_rows(tile);
-        const bool okg = 16 * tile + g < n_res, okg8 = 16 * tile + g + 8 < n_res;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < DJ; ++j) {
-            uint4 bq = make_uint4(0, 0, 0, 0);
-            if (g < 2 * NQ) bq = *reinterpret_cast<const uint4*>(&qres[g < 2 * NQ ? g : 0][32 * j + 8 * i]);
-            const uint32_t f0[4] = {kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y};
-            const uint32_t f1[4] = {kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w};
-            mma16816(c, f0, bq.x, bq.y);
-            mma16816(c, f1, bq.z, bq.w);
-        }
-        const float sc[4] = {okg ? c[0] + c[1] : -INFINITY, okg8 ? c[2] + c[3] : -INFINITY, -INFINITY, -INFINITY};
-        float p[4];
-        softmax(sc, p, 1.f);
-        float prb[4];
-        gather(p[0], p[1], prb);
-        uint32_t ph01, ph89, pl01, pl89;
-        split_p(prb, ph01, ph89, pl01, pl89);
-        const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
-#pragma unroll
-        for (int j = 0; j < DJ; ++j) {
-            const uint32_t f0[4] = {movmatrix_trans(vx[0][j].x), movmatrix_trans(vx[0][j].y),
-                                    movmatrix_trans(vx[1][j].x), movmatrix_trans(vx[1][j].y)};
-            mma16816(o[2 * j], f0, pb0, pb1);
-            const uint32_t f1[4] = {movmatrix_trans(vx[0][j].z), movmatrix_trans(vx[0][j].w),
-                                    movmatrix_trans(vx[1][j].z), movmatrix_trans(vx[1][j].w)};
-            mma16816(o[2 * j + 1], f1, pb0, pb1);
-        }
-    }
-    auto sum_l = [&]() {                          // l over the lanes of a head
-        float lt = l;
-        lt += __shfl_xor_sync(kFull, lt, 4);
-        lt += __shfl_xor_sync(kFull, lt, 8);
-        lt += __shfl_xor_sync(kFull, lt, 16);
-        return lt;
-    };
-    {
-        const float lt = sum_l();
-        if (g == 0 && i < NQ) head_s[warp][i] = make_float4(m, lt, 0.f, 0.f);
-        if (tb < te && hO < NQ) {                 // every group slot's columns hold the same sums: each writes some
-#pragma unroll
-            for (int mt = 0; mt < KS; ++mt) {
-                if (mt % GB != jO) continue;
-                const int ch = 32 * (mt / 2) + 8 * (g / 2) + 4 * (mt % 2) + g % 2;
-                rsum[warp][hO * D + ch] = o[mt][0] + o[mt][1];
-                rsum[warp][hO * D + ch + 2] = o[mt][2] + o[mt][3];
-            }
-        }
-        m = -INFINITY;
-        l = 0.f;
-        fresh = true;
-#pragma unroll
-        for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-    }
-
     // ---- the listed blocks ----
     while (k < we) {
-        if (k >= kend) begin_part();
+        if (k >= kend) {
+            read_part();
+            begin_part();
+        }
         bool failed = false;
         bool skip = offs[k / PPB - j0] < 0;
         for (; k < kend; ++k, ++item) {
@@ -460,15 +454,19 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
             if (!skip) {
                 if (first_of_block)
                     build_q_frags<C, D, NQ, QB_REGS>(stage + C::KE, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);
-                float ca[1][4] = {{0.f, 0.f, 0.f, 0.f}}, cb[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+                float ca[4] = {0.f, 0.f, 0.f, 0.f}, cb[4] = {0.f, 0.f, 0.f, 0.f};
                 uint32_t wa[W], wc[W];
                 lds_words(stage_u32 + C::KT, wa);
-                if constexpr (BITS != 8) lds_words(stage_u32 + C::KT + C::TILE, wc);
-                tile_mma<BITS, false, W, KS>(wa, qbk, ca);
-                if constexpr (BITS == 8) lds_words(stage_u32 + C::KT + C::TILE, wc);
-                tile_mma<BITS, false, W, KS>(wc, qbk, cb);
-                const float sc[4] = {ca[0][0] + (ca[0][1] + beta), ca[0][2] + (ca[0][3] + beta),
-                                     cb[0][0] + (cb[0][1] + beta), cb[0][2] + (cb[0][3] + beta)};
+                if constexpr (BITS == 8) {                     // one tile at a time: the words of two do not fit
+                    key_mma<BITS, W, KS>(wa, qbk, ca);
+                    lds_words(stage_u32 + C::KT + C::TILE, wc);
+                    key_mma<BITS, W, KS>(wc, qbk, cb);
+                } else {                                       // two chains of sums side by side
+                    lds_words(stage_u32 + C::KT + C::TILE, wc);
+                    key_mma2<BITS, W, KS>(wa, wc, qbk, ca, cb);
+                }
+                const float sc[4] = {ca[0] + (ca[1] + beta), ca[2] + (ca[3] + beta), cb[0] + (cb[1] + beta),
+                                     cb[2] + (cb[3] + beta)};
                 constexpr bool HOIST = BITS != 8 && W <= 4;   // as in the dense kernel
                 uint32_t wvh[2][W];
                 if constexpr (HOIST) {
@@ -504,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
                         lds_words(stage_u32 + C::VT + t * C::TILE, wv);
                     }
                     auto pbk = [&](int mt) { return make_uint2(pb[(16 * mt / G) / GB][0], pb[(16 * mt / G) / GB][1]); };
-                    tile_mma<BITS, true, W, KS>(wv, pbk, o);
+                    value_mma<BITS, W, KS>(wv, pbk, o);
                 }
             }
             __syncwarp();                                      // every lane is done with this stage
@@ -530,14 +528,19 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
         const float s1 = pow2i(24 - BITS * ((2 * mt + 1) % (8 / BITS)));
         o[mt][0] *= s0; o[mt][1] *= s0; o[mt][2] *= s1; o[mt][3] *= s1;
     }
-    // ---- this warp's partial result ----
-    const uint32_t st_all = __reduce_or_sync(kFull, status);
+    auto sum_l = [&]() {                          // l over the lanes of a head
+        float lt = l;
+        lt += __shfl_xor_sync(kFull, lt, 4);
+        lt += __shfl_xor_sync(kFull, lt, 8);
+        lt += __shfl_xor_sync(kFull, lt, 16);
+        return lt;
+    };
+    // ---- the listed blocks' partial result ----
 #pragma unroll
     for (int f = 0; f < NBF; ++f) {
         zeta[f] += __shfl_xor_sync(kFull, zeta[f], 1);
         zeta[f] += __shfl_xor_sync(kFull, zeta[f], 2);
     }
-    const float lt = sum_l();
     float zo[NBF];
 #pragma unroll
     for (int f = 0; f < NBF; ++f) zo[f] = __shfl_sync(kFull, zeta[f], 8 * i);
@@ -553,11 +556,71 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
             }
         }
     }
-    if (g == 0 && i < NQ) head_s[kWarps + warp][i] = make_float4(m, lt, (float)st_all, 0.f);
+    {
+        const uint32_t st_all = __reduce_or_sync(kFull, status);
+        const float lt = sum_l();
+        if (g == 0 && i < NQ) head_s[warps + warp][i] = make_float4(m, lt, (float)st_all, 0.f);
+    }
+
+    // ---- the residual tiles: 16 fp16 rows each, straight from memory.  The
+    // 16-byte loads hand lane i eight consecutive channels, so the MMAs' k
+    // (keys) and m (values) indices run over the channels in another order than
+    // the tiles': k-steps 2j, 2j+1 hold channels 32 j + 8 i + 0..3, + 4..7, and
+    // m-tile 2j+u has row g at channel 32 j + 8 (g / 2) + 4 u + g % 2, row g + 8
+    // two further.  Their partial result is kept apart from the blocks'. ----
+    m = -INFINITY;
+    l = 0.f;
+    fresh = true;
+#pragma unroll
+    for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    for (int tile = tb; tile < te; ++tile) {
+        load_rows(tile);
+        const bool okg = 16 * tile + g < n_res, okg8 = 16 * tile + g + 8 < n_res;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < DJ; ++j) {
+            uint4 bq = make_uint4(0, 0, 0, 0);
+            if (g < 2 * NQ) bq = *reinterpret_cast<const uint4*>(&qres[g < 2 * NQ ? g : 0][32 * j + 8 * i]);
+            const uint32_t f0[4] = {kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y};
+            const uint32_t f1[4] = {kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w};
+            mma16816(c, f0, bq.x, bq.y);
+            mma16816(c, f1, bq.z, bq.w);
+        }
+        const float sc[4] = {okg ? c[0] + c[1] : -INFINITY, okg8 ? c[2] + c[3] : -INFINITY, -INFINITY, -INFINITY};
+        float p[4];
+        softmax(sc, p, 1.f);
+        float prb[4];
+        gather(p[0], p[1], prb);
+        uint32_t ph01, ph89, pl01, pl89;
+        split_p(prb, ph01, ph89, pl01, pl89);
+        const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
+#pragma unroll
+        for (int j = 0; j < DJ; ++j) {
+            const uint32_t f0[4] = {movmatrix_trans(vx[0][j].x), movmatrix_trans(vx[0][j].y),
+                                    movmatrix_trans(vx[1][j].x), movmatrix_trans(vx[1][j].y)};
+            mma16816(o[2 * j], f0, pb0, pb1);
+            const uint32_t f1[4] = {movmatrix_trans(vx[0][j].z), movmatrix_trans(vx[0][j].w),
+                                    movmatrix_trans(vx[1][j].z), movmatrix_trans(vx[1][j].w)};
+            mma16816(o[2 * j + 1], f1, pb0, pb1);
+        }
+    }
+    {
+        float* rsum = reinterpret_cast<float*>(ring + S::SUMS);
+        const float lt = sum_l();
+        if (g == 0 && i < NQ) head_s[warp][i] = make_float4(m, lt, 0.f, 0.f);
+        if (tb < te && hO < NQ) {                 // every group slot's columns hold the same sums: each writes some
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+                if (mt % GB != jO) continue;
+                const int ch = 32 * (mt / 2) + 8 * (g / 2) + 4 * (mt % 2) + g % 2;
+                rsum[hO * D + ch] = o[mt][0] + o[mt][1];
+                rsum[hO * D + ch + 2] = o[mt][2] + o[mt][3];
+            }
+        }
+    }
 
     // ---- the log-sum-exp merge: the CTA's partials, then the cluster's CTAs ----
-    static_assert(NQ <= kWarps, "one warp per query head in the merge");
-    // weights 2^(m - M) and the sum L of head `warp` from each lane's (m, l, status)
+    // weights 2^(m - M) and the sum L over the lanes' (m, l, status)
     auto weigh = [&](float4 x, float& M, float& L, bool& bad) {
         M = x.x;
 #pragma unroll
@@ -571,58 +634,53 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
     };
     const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f);
     __syncthreads();
-    if (warp < NQ) {
+    for (int h = warp; h < NQ; h += warps) {
         float M, L;
         bool bad;
-        const float e = weigh(lane < 2 * kWarps ? head_s[lane][warp] : none, M, L, bad);
-        if (lane < 2 * kWarps) wgt_s[warp][lane] = csize > 1 ? e : bad ? NAN : e / L;
-        if (lane == 0) cta_head[warp] = make_float4(M, L, bad ? 1.f : 0.f, 0.f);
+        const float e = weigh(lane < 2 * warps ? head_s[lane][h] : none, M, L, bad);
+        if (lane < 2 * warps) wgt_s[h][lane] = csize > 1 ? e : bad ? NAN : e / L;
+        if (lane == 0) cta_head[h] = make_float4(M, L, bad ? 1.f : 0.f, 0.f);
     }
     __syncthreads();
+    // a warp's value sums: of its residual tiles and of its blocks; a partial
+    // without tokens has weight 0 (and, of the residual, no sums)
     __half* out = a.out + ((long long)b * a.Hq + hk * NQ) * D;
-    for (int idx = tid; idx < NQ * D; idx += kThreads) {
-        const int h = idx / D;
+    const int span = NQ * D / (int)csize;         // the outputs a CTA of the cluster writes
+    if (csize > 1) cluster_wait();                // (every CTA has started: its shared memory may be written)
+    for (int idx = tid; idx < NQ * D; idx += blockDim.x) {
+        const float* w = wgt_s[idx / D];
         float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < 2 * kWarps; ++j) {
-            const float w = wgt_s[h][j];
-            // (a partial without tokens has weight 0 and, of the residual, no sums)
-            const float v = j < kWarps ? rsum[j][idx]
-                                       : reinterpret_cast<const float*>(dyn_smem + (j - kWarps) * C::STAGES * C::STAGE_BYTES)[idx];
-            s = w == 0.f ? s : fmaf(v, w, s);
+#pragma unroll 4
+        for (int j = 0; j < warps; ++j) {
+            const float* mine = reinterpret_cast<const float*>(dyn_smem + j * S::WARP) + idx;
+            const float vr = mine[S::SUMS / 4], vb = mine[0], er = w[j], eb = w[warps + j];
+            s = er == 0.f ? s : fmaf(vr, er, s);
+            s = eb == 0.f ? s : fmaf(vb, eb, s);
         }
-        if (csize > 1) rsum[0][idx] = s;
+        if (csize > 1) stc32(cluster_map(smem_u32(&recv_s[(int)crank * span + idx % span]), idx / span), s);
         else out[idx] = __float2half_rn(s);
     }
     if (csize == 1) return;
+    // each CTA has sent the owner of every output its sum, and all of them its
+    // heads' (M, L, status); nothing is read from afar, so a CTA may leave first
+    for (int idx = tid; idx < NQ * (int)csize; idx += blockDim.x)
+        stc128(cluster_map(smem_u32(&recv_head[crank][idx % NQ]), idx / NQ), cta_head[idx % NQ]);
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-    if (warp < NQ) {
-        float M, L;
-        bool bad;
-        const float4 x = lane < (int)csize ? ldc128(cluster_map(smem_u32(&cta_head[warp]), lane)) : none;
-        const float e = weigh(x, M, L, bad);
-        if (lane < (int)csize) wgt_s[warp][lane] = bad ? NAN : e / L;
-    }
-    __syncthreads();
-    const int span = NQ * D / (int)csize;         // this CTA's share of the output
-    for (int at = tid; at < span; at += kThreads) {
-        const int idx = (int)crank * span + at;
-        const uint32_t base = smem_u32(&rsum[0][idx]);
-        float v[kMaxCluster], s = 0.f;
-#pragma unroll
-        for (int j = 0; j < kMaxCluster; ++j) v[j] = j < (int)csize ? ldc32(cluster_map(base, j)) : 0.f;
-#pragma unroll
-        for (int j = 0; j < kMaxCluster; ++j) {
-            const float w = j < (int)csize ? wgt_s[idx / D][j] : 0.f;
-            s = w == 0.f ? s : fmaf(v[j], w, s);
+    for (int at = tid; at < span; at += blockDim.x) {
+        const int idx = (int)crank * span + at, h = idx / D;
+        float M = -INFINITY, L = 0.f, s = 0.f, bad = 0.f;
+        for (int j = 0; j < (int)csize; ++j) M = fmaxf(M, recv_head[j][h].x);
+        for (int j = 0; j < (int)csize; ++j) {
+            const float4 x = recv_head[j][h];
+            const float e = x.x == -INFINITY ? 0.f : fast_exp2(x.x - M);
+            L = fmaf(x.y, e, L);
+            s = e == 0.f ? s : fmaf(recv_s[j * span + at], e, s);
+            bad += x.z;
         }
-        out[idx] = __float2half_rn(s);
+        out[idx] = __float2half_rn(bad != 0.f ? NAN : s / L);
     }
-    __syncwarp();
-    cluster_arrive();                             // no CTA leaves while another reads its shared memory
-    cluster_wait();
 }
 
 }  // namespace blocks_detail

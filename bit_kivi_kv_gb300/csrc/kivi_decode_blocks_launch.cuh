@@ -12,50 +12,81 @@ namespace blocks_launch {
 constexpr int kMaxDevices = 64;
 
 // Per-device set-up of one instance: the opt-in to its dynamic shared memory
-// and its resident CTAs per SM.
+// and what an SM holds of its warps and CTAs.
+struct SmRoom {
+    int reg_warps = 0;                   // warps by registers; 0: not set up on that device yet
+    int sm_bytes = 0, cta_bytes = 0;     // shared memory of an SM; of a CTA, most
+    int fixed = 0, per_warp = 0;         // shared memory of a CTA: fixed, and per warp
+    // warps of each of n CTAs on one SM
+    int warps(long long n) const {
+        if (n > reg_warps) return 0;
+        const long long by_smem = (min2(sm_bytes / n, cta_bytes + 1024) - 1024 - fixed) / per_warp;
+        const long long w = min2(reg_warps / n, by_smem);
+        return w < 0 ? 0 : (int)w;
+    }
+    static long long min2(long long x, long long y) { return x < y ? x : y; }
+};
 struct InstanceSetup {
     std::mutex mu;
-    int per_sm[kMaxDevices] = {};        // 0: not set up on that device yet
+    SmRoom room[kMaxDevices];
 };
 
-// CTAs that share a row: the most (a power of two, at most 8) whose whole grid
-// is resident at once and whose warps each get a unit of work.
-inline int cluster_ctas(long long rows, long long units, long long resident) {
-    int c = 1;
-    while (c < blocks_detail::kMaxCluster && rows * c * 2 <= resident && 2LL * c * mma_detail::kWarps <= units) c *= 2;
-    return c;
+// A row's CTAs (a power of two, at most 8: a cluster) and their warps: the shape
+// with the most warps per row among those whose whole grid is resident at
+// once, a larger cluster only for at least half as many warps again.  Where
+// none gives a row two warps, CTAs of four warps in several waves.
+struct Shape { int ctas, warps; };
+inline Shape row_shape(long long rows, long long units, int num_sms, const SmRoom& room) {
+    Shape best{1, 0};
+    for (int c = 1; c <= blocks_detail::kMaxCluster; c *= 2) {
+        long long w = room.warps((rows * c + num_sms - 1) / num_sms);
+        if (w * c > units) w = (units + c - 1) / c;
+        if (w >= 1 && (best.warps == 0 || 2 * w * c >= 3LL * best.ctas * best.warps)) best = Shape{c, (int)w};
+    }
+    if (best.ctas * best.warps < 2 && units >= 2)
+        best = Shape{1, (int)SmRoom::min2(SmRoom::min2(units, 4), room.warps(1))};
+    return best;
 }
 
 template <int D, int BB, int NN, int GG, bool PAGED>
 cudaError_t launch_one(const typename blocks_detail::ArgsOf<PAGED>::type& a, long long rows, long long units,
                        int num_sms, cudaStream_t st) {
     using namespace blocks_detail;
-    using C = Cfg<D, BB, NN, GG>;
     static InstanceSetup setup;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    int per_sm;
+    using S = Smem<D, BB, NN, GG>;
+    auto kernel = decode_blocks_kernel<D, BB, NN, GG, PAGED>;
+    SmRoom room;
     {
         std::lock_guard<std::mutex> lock(setup.mu);
-        per_sm = setup.per_sm[dev];
-        if (per_sm == 0) {
-            e = cudaFuncSetAttribute(decode_blocks_kernel<D, BB, NN, GG, PAGED>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::DYN_SMEM);
+        SmRoom& r = setup.room[dev];
+        if (r.reg_warps == 0) {
+            SmRoom n;
+            cudaFuncAttributes fa;
+            e = cudaFuncGetAttributes(&fa, kernel);
+            if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n.cta_bytes, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+            if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n.sm_bytes, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+            n.fixed = (int)fa.sharedSizeBytes;
+            n.per_warp = S::WARP;
+            n.reg_warps = kCtaWarps<D, NN>;
+            const int most = n.warps(1);
+            if (e == cudaSuccess && most < 1) e = cudaErrorInvalidConfiguration;
             if (e == cudaSuccess)
-                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                    &per_sm, decode_blocks_kernel<D, BB, NN, GG, PAGED>, kThreads, C::DYN_SMEM);
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most * S::WARP);
             if (e != cudaSuccess) return e;
-            if (per_sm < 1) per_sm = 1;
-            setup.per_sm[dev] = per_sm;
+            r = n;
         }
+        room = r;
     }
-    const int c = cluster_ctas(rows, units, (long long)num_sms * per_sm);
+    const Shape sh = row_shape(rows, units, num_sms, room);
+    const int c = sh.ctas;
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3((unsigned)(rows * c));
-    lc.blockDim = dim3(kThreads);
-    lc.dynamicSmemBytes = C::DYN_SMEM;
+    lc.blockDim = dim3(32 * sh.warps);
+    lc.dynamicSmemBytes = sh.warps * S::WARP;
     lc.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -66,7 +97,7 @@ cudaError_t launch_one(const typename blocks_detail::ArgsOf<PAGED>::type& a, lon
     attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = c > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&lc, decode_blocks_kernel<D, BB, NN, GG, PAGED>, a);
+    return cudaLaunchKernelEx(&lc, kernel, a);
 }
 
 // every (bits, q heads per kv head, G) instance of head_dim D
