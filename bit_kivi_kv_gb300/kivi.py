@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkivi.so")
 
@@ -55,6 +56,9 @@ class kivi_qkv(ctypes.Structure):
                 ("positions_64bit", ctypes.c_int), ("first_position", ctypes.c_longlong),
                 ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p)]
 
+
+_QKV = struct.Struct("@iiiiqiPPPqqqqqqqqqPPfPqiiPiqPPP")   # kivi_qkv, field by field
+assert _QKV.size == ctypes.sizeof(kivi_qkv)
 
 KIVI_PAGED_MAX_CALL_SEQS = 512
 KIVI_F16, KIVI_BF16, KIVI_F32 = 0, 1, 2
@@ -337,18 +341,26 @@ def kivi_launch_count() -> int:
 # ---- torch convenience wrapper -----------------------------------------------
 def _expect(t, what, dtype, shape, device=None):
     """Raise KIVI_ERR_INVALID_ARG unless t is a dense CUDA tensor of this type and
-    shape on the current device (the one the kernels run on)."""
+    shape on the current device (the one the kernels run on; given by a caller
+    that has asked for it already)."""
     import torch
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+    if device is None:
+        device = torch.cuda.current_device()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be a contiguous CUDA {dtype} tensor of shape "
                                               f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current device")
+    raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current device")
 
 
 def _raw_stream(stream):
+    """The handle of stream (None: the current one)."""
     import torch
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # (what torch.cuda.current_stream().cuda_stream is, without the stream object: 0.1 against 2.9 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def select_blocks(scores, n_keep, keep_first=0, out=None, stream=None):
@@ -401,54 +413,59 @@ class QKNormRope:
         for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
             if w is not None:
                 _expect(w, what, torch.float32, (head_dim,))
-        a = kivi_qkv()
-        a.n_q_heads, a.n_kv_heads, a.head_dim, a.eps = n_q_heads, n_kv_heads, head_dim, eps
-        a.q_weight = w.data_ptr() if (w := q_weight) is not None else None
-        a.k_weight = w.data_ptr() if (w := k_weight) is not None else None
+        rot_dim = n_positions = table = 0
         if cos_sin is not None:
-            _expect(cos_sin, "cos_sin", torch.float32, cos_sin.shape[:1] + cos_sin.shape[1:2])
-            a.cos_sin, (a.n_positions, a.rot_dim) = cos_sin.data_ptr(), cos_sin.shape
-        a.interleaved = bool(interleaved)
-        self._fixed = bytes(a)
+            if cos_sin.dim() != 2:
+                raise KiviError(KIVI_ERR_INVALID_ARG, "cos_sin must be [n_positions, rot_dim]")
+            _expect(cos_sin, "cos_sin", torch.float32, cos_sin.shape)
+            table, (n_positions, rot_dim) = cos_sin.data_ptr(), cos_sin.shape
         self._keep = (q_weight, k_weight, cos_sin)
-        given = [t for t in self._keep if t is not None]
-        self._device = given[0].device.index if given else None
+        self._device = next((t.get_device() for t in self._keep if t is not None), None)
         self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
+        self._fixed = (q_weight.data_ptr() if q_weight is not None else 0, k_weight.data_ptr() if k_weight is not None
+                       else 0, eps, table, n_positions, rot_dim, bool(interleaved))
         self._dtypes = {torch.float16: KIVI_F16, torch.bfloat16: KIVI_BF16, torch.float32: KIVI_F32}
+        self._positions = {torch.int32: 0, torch.int64: 1}
 
-    def _args(self, q, k, v, positions, first_position):
+    def _args(self, q, k, v, positions, first_position, outs):
         """The C call's arguments for inputs [batch, tokens, heads, head_dim] (or
-        [batch, heads, head_dim]: one token a row), without the outputs."""
+        [batch, heads, head_dim]: one token a row); outs(batch, tokens or None, device) gives
+        the outputs and the addresses of the three."""
         import torch
-        a = kivi_qkv.from_buffer_copy(self._fixed)
         lead = q.shape[:-2]
-        one = len(lead) == 1
-        if not one and len(lead) != 2:
+        n = len(lead)
+        if n != 1 and n != 2:
             raise KiviError(KIVI_ERR_INVALID_ARG, "q, k and v have 3 or 4 dimensions")
         code = self._dtypes.get(q.dtype)
         if code is None:
             raise KiviError(KIVI_ERR_INVALID_ARG, f"no input type {q.dtype}")
         device = torch.cuda.current_device()
-        if self._device not in (None, device):
+        if self._device is not None and self._device != device:
             raise KiviError(KIVI_ERR_INVALID_ARG, f"the weights are on cuda:{self._device}, not on the current device")
-        a.batch, a.n_tokens, a.dtype = lead[0], 1 if one else lead[1], code
-        for x, heads, ptr, stride in ((q, self.n_q_heads, "q", a.q_stride), (k, self.n_kv_heads, "k", a.k_stride),
-                                      (v, self.n_kv_heads, "v", a.v_stride)):
-            if x.dtype != q.dtype or not x.is_cuda or x.device.index != device:
-                raise KiviError(KIVI_ERR_INVALID_ARG, f"{ptr} must be of q's type and on the current device")
-            if x.shape[:-2] != lead or x.shape[-2] != heads or x.shape[-1] != self.head_dim or x.stride(-1) != 1:
-                raise KiviError(KIVI_ERR_INVALID_ARG, f"{ptr} must be [..., {heads}, {self.head_dim}] with dense "
-                                                      f"channels and q's leading sizes, got {tuple(x.shape)}")
+        strides, D = [], self.head_dim
+        for x, heads, what in ((q, self.n_q_heads, "q"), (k, self.n_kv_heads, "k"), (v, self.n_kv_heads, "v")):
+            if x.dtype is not q.dtype or x.get_device() != device:
+                raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be of q's type and on the current device")
             s = x.stride()
-            stride[0], stride[1], stride[2] = s[0], 0 if one else s[1], s[-2]
-            setattr(a, ptr, x.data_ptr())
+            if x.shape != lead + (heads, D) or s[-1] != 1:
+                raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be [..., {heads}, {D}] with dense channels and "
+                                                      f"q's leading sizes, got {tuple(x.shape)}")
+            strides += (s[0], 0, s[1]) if n == 1 else s[:3]
+        wide, pos = 0, 0
         if positions is not None:
-            if positions.dtype not in (torch.int32, torch.int64):
+            wide = self._positions.get(positions.dtype)
+            if wide is None:
                 raise KiviError(KIVI_ERR_INVALID_ARG, "positions must be int32 or int64")
-            _expect(positions, "positions", positions.dtype, lead)
-            a.positions, a.positions_64bit = positions.data_ptr(), positions.dtype == torch.int64
-        a.first_position = first_position
-        return a, one
+            _expect(positions, "positions", positions.dtype, lead, device)
+            pos = positions.data_ptr()
+        tokens = 1 if n == 1 else lead[1]
+        out, ptrs = outs(lead[0], None if n == 1 else tokens, device)
+        qw, kw, eps, table, n_positions, rot_dim, interleaved = self._fixed
+        # (the fields of kivi_qkv in order, packed at once: a few times faster than one by one)
+        a = kivi_qkv.from_buffer_copy(_QKV.pack(
+            lead[0], self.n_q_heads, self.n_kv_heads, D, tokens, code, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            *strides, qw, kw, eps, table, n_positions, rot_dim, interleaved, pos, wide, first_position, *ptrs))
+        return a, out
 
     def __call__(self, q, k, v, positions=None, first_position=0, out=None, stream=None):
         """q [B, L, Hq, D], k and v [B, L, Hkv, D] (fp16, bf16 or fp32; any strides with
@@ -457,15 +474,19 @@ class QKNormRope:
         Returns fp16 (q [B, Hq, L, D], k [B, Hkv, L, D], v), without L where the
         inputs have none."""
         import torch
-        a, one = self._args(q, k, v, positions, first_position)
-        shapes = [(a.batch, h, self.head_dim) if one else (a.batch, h, a.n_tokens, self.head_dim)
-                  for h in (self.n_q_heads, self.n_kv_heads, self.n_kv_heads)]
-        if out is None:
-            out = tuple(torch.empty(s, dtype=torch.float16, device=q.device) for s in shapes)
-        else:
-            for t, s, what in zip(out, shapes, ("out[0]", "out[1]", "out[2]")):
-                _expect(t, what, torch.float16, s)
-        a.q_out, a.k_out, a.v_out = (t.data_ptr() for t in out)
+
+        def outs(B, L, device):
+            shapes = [(B, h, self.head_dim) if L is None else (B, h, L, self.head_dim)
+                      for h in (self.n_q_heads, self.n_kv_heads, self.n_kv_heads)]
+            if out is None:
+                o = tuple(torch.empty(s, dtype=torch.float16, device=q.device) for s in shapes)
+            else:
+                o = out
+                for t, s, what in zip(o, shapes, ("out[0]", "out[1]", "out[2]")):
+                    _expect(t, what, torch.float16, s, device)
+            return o, [t.data_ptr() for t in o]
+
+        a, out = self._args(q, k, v, positions, first_position, outs)
         kivi_qk_norm_rope(a, _raw_stream(stream))
         return out
 
@@ -549,13 +570,18 @@ class KiviCache:
         norm_rope (QKNormRope), k and v stored in the cache by the same kernel.
         q [B, Hq, D], k, v [B, Hkv, D]; returns the query, fp16 [B, Hq, D]."""
         import torch
-        a, one = norm_rope._args(q, k, v, positions, first_position)
-        if q_out is None:
-            q_out = torch.empty(a.batch, a.n_q_heads, a.head_dim, dtype=torch.float16, device=q.device)
-        else:
-            _expect(q_out, "q_out", torch.float16, (a.batch, a.n_q_heads, a.head_dim))
-        a.q_out = q_out.data_ptr()
-        kivi_append_qkv(self.handle, a, self._stream(stream))
+
+        def outs(B, L, device):
+            shape = (B, norm_rope.n_q_heads, norm_rope.head_dim)
+            o = q_out
+            if o is None:
+                o = torch.empty(shape, dtype=torch.float16, device=q.device)
+            else:
+                _expect(o, "q_out", torch.float16, shape, device)
+            return o, (o.data_ptr(), 0, 0)
+
+        a, q_out = norm_rope._args(q, k, v, positions, first_position, outs)
+        kivi_append_qkv(self.handle, a, _raw_stream(stream))
         return q_out
 
     def block_scores(self, q, out=None, softmax_scale=0.0, stream=None):
@@ -568,7 +594,7 @@ class KiviCache:
             out = torch.empty(c.batch, c.n_kv_heads, self.counts()[0] // c.group, dtype=torch.float32, device=q.device)
         else:
             _expect(out, "out", torch.float32, (c.batch, c.n_kv_heads, out.shape[-1]))
-        kivi_block_scores(self.handle, q.data_ptr(), softmax_scale, out.data_ptr(), out.shape[-1], self._stream(stream))
+        kivi_block_scores(self.handle, q.data_ptr(), softmax_scale, out.data_ptr(), out.shape[-1], _raw_stream(stream))
         return out
 
     def decode_blocks(self, q, blocks, out=None, softmax_scale=0.0, stream=None):
@@ -583,7 +609,7 @@ class KiviCache:
         else:
             _expect(out, "out", torch.float16, q.shape)
         kivi_decode_blocks(self.handle, q.data_ptr(), blocks.data_ptr(), blocks.shape[-1], out.data_ptr(),
-                           softmax_scale, self._stream(stream))
+                           softmax_scale, _raw_stream(stream))
         return out
 
     def sparse_decode(self, q, n_keep, keep_first=1, out=None, softmax_scale=0.0, stream=None):
@@ -663,7 +689,7 @@ class KiviPagedCache:
         c, seqs = self.cfg, list(seqs)
         _expect(k, "k", torch.float16, (len(seqs), c.n_kv_heads, c.head_dim))
         _expect(v, "v", torch.float16, (len(seqs), c.n_kv_heads, c.head_dim))
-        kivi_paged_append(self.handle, seqs, k.data_ptr(), v.data_ptr(), KiviCache._stream(stream))
+        kivi_paged_append(self.handle, seqs, k.data_ptr(), v.data_ptr(), _raw_stream(stream))
 
     def block_scores(self, seqs, q, out=None, softmax_scale=0.0, stream=None):
         """KiviCache.block_scores for the listed sequences: q [n, Hq, D] -> fp32
@@ -677,7 +703,7 @@ class KiviPagedCache:
         else:
             _expect(out, "out", torch.float32, (len(seqs), c.n_kv_heads, out.shape[-1]))
         kivi_paged_block_scores(self.handle, seqs, q.data_ptr(), softmax_scale, out.data_ptr(), out.shape[-1],
-                                KiviCache._stream(stream))
+                                _raw_stream(stream))
         return out
 
     def decode_blocks(self, seqs, q, blocks, out=None, softmax_scale=0.0, stream=None):
@@ -691,7 +717,7 @@ class KiviPagedCache:
         else:
             _expect(out, "out", torch.float16, q.shape)
         kivi_paged_decode_blocks(self.handle, seqs, q.data_ptr(), blocks.data_ptr(), blocks.shape[-1], out.data_ptr(),
-                                 softmax_scale, KiviCache._stream(stream))
+                                 softmax_scale, _raw_stream(stream))
         return out
 
     def sparse_decode(self, seqs, q, n_keep, keep_first=1, out=None, softmax_scale=0.0, stream=None):
