@@ -200,113 +200,225 @@ __device__ __forceinline__ uint32_t score_key(float x, bool always) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);   // -FLT_MAX -> 0x00800000 > 0; +inf -> 0xff800000
 }
 
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectItems = 8;
-
-// One CTA per row.  The K-th largest key is found by bisection on its bits,
-// highest first, each step one count over the CTA; the row's keys stay in
-// registers (rows of more than 8192 columns are read again at each step).
-// Then every key above it is taken and, of the keys equal to it, the first
-// ones in index order; warps own consecutive columns, so a scan of the warps'
-// counts gives each chosen column its place.
 struct SelectArgs {
     const float* scores;
-    long long cols, ld;
+    long long rows, cols, ld;
     int n_keep, keep_first;
     int* blocks;
 };
 
-__global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(const SelectArgs a) {
-    constexpr int kW = kSelectThreads / 32;
-    __shared__ int red[2][kW];
-    __shared__ int above_s[kW], equal_s[kW];
+// In both kernels: t is the least key taken, `take` the number of columns
+// taken; every key above t is taken, and of those equal to t the first ones in
+// index order.  A chosen column's place is the number of chosen ones before it.
+
+// Rows of up to 256 columns: one warp each, its keys in registers, no
+// barriers.  t is found by bisection on its bits, highest first, each step one
+// count over the warp, until as many keys as wanted are at least t.
+constexpr int kWarpItems = 8;
+constexpr int kWarpRows = 4;         // rows (warps) per CTA
+
+__global__ void __launch_bounds__(32 * kWarpRows) select_blocks_warp_kernel(const SelectArgs a) {
+    const int lane = threadIdx.x & 31;
+    const long long r = (long long)blockIdx.x * kWarpRows + (threadIdx.x >> 5);
+    griddepcontrol_wait();
+    griddepcontrol_launch_dependents();
+    if (r >= a.rows) return;
+    const float* row = a.scores + r * a.ld;
+    int* out = a.blocks + r * a.n_keep;
+    const int cols = (int)a.cols, K = a.n_keep;
+    float x[kWarpItems];
+#pragma unroll
+    for (int j = 0; j < kWarpItems; ++j) x[j] = 32 * j + lane < cols ? row[32 * j + lane] : -INFINITY;
+    uint32_t key[kWarpItems];
+#pragma unroll
+    for (int j = 0; j < kWarpItems; ++j) key[j] = score_key(x[j], 32 * j + lane < a.keep_first);
+    auto count = [&](uint32_t t) {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < kWarpItems; ++j) n += key[j] >= t;
+        return __reduce_add_sync(kFull, n);
+    };
+    const int valid = count(1u);
+    uint32_t t = 1u;
+    if (valid > K) {
+        uint32_t most = 0u, least = 0xffffffffu;
+#pragma unroll
+        for (int j = 0; j < kWarpItems; ++j) {
+            most = max(most, key[j]);
+            least = key[j] ? min(least, key[j]) : least;
+        }
+        most = __reduce_max_sync(kFull, most);
+        least = __reduce_min_sync(kFull, least);
+        // the bits above the highest one in which two keys differ are common to all
+        const int top = 31 - __clz(most ^ least);               // -1: all equal
+        t = top < 0 ? most : top == 31 ? 0u : most & ~((2u << top) - 1u);
+        for (int bit = top; bit >= 0; --bit) {
+            const uint32_t c = t | (1u << bit);
+            const int n = count(c);
+            if (n >= K) t = c;
+            if (n == K) break;
+        }
+    }
+    const int take = min(valid, K);
+    int above = 0;
+#pragma unroll
+    for (int j = 0; j < kWarpItems; ++j) above += key[j] > t;
+    const int ties = take - __reduce_add_sync(kFull, above);
+    const uint32_t below = (1u << lane) - 1u;
+    int before_a = 0, before_e = 0;
+#pragma unroll
+    for (int j = 0; j < kWarpItems; ++j) {
+        const uint32_t k = key[j];
+        const uint32_t ma = __ballot_sync(kFull, k > t), me = __ballot_sync(kFull, k == t);
+        const int ra = before_a + __popc(ma & below), re = before_e + __popc(me & below);
+        if (k > t || (k == t && re < ties)) out[ra + min(re, ties)] = 32 * j + lane;
+        before_a += __popc(ma);
+        before_e += __popc(me);
+    }
+    for (int j = take + lane; j < K; j += 32) out[j] = -1;
+}
+
+// Longer rows: one CTA each.  The keys between two bounds that hold the wanted
+// one are counted in 2048 equal bins of the range that they span; the bin of
+// the wanted key is the next range.  Two rounds for ordinary scores, three at
+// most; a row of equal scores needs none.  Keys stay in registers, or are read
+// again each time in rows of more than 16384 columns.  Warps own consecutive
+// columns.
+constexpr int kSelectItems = 16;
+constexpr int kBins = 2048;
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) select_blocks_kernel(const SelectArgs a) {
+    constexpr int kW = THREADS / 32;
+    constexpr int kBinsPerThread = kBins / THREADS;
+    __shared__ int hist[kBins];
+    __shared__ uint32_t lo_s[kW], hi_s[kW];
+    __shared__ int n_s[kW], m_s[kW];
+    __shared__ uint32_t found_bin;
+    __shared__ int found_above, found_count;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nw = blockDim.x / 32;
     griddepcontrol_wait();
     griddepcontrol_launch_dependents();
     const float* row = a.scores + (long long)blockIdx.x * a.ld;
     int* out = a.blocks + (long long)blockIdx.x * a.n_keep;
-    // columns of this warp: [c0, c0 + 32 * items), lane-strided
-    const long long items = (a.cols + blockDim.x - 1) / blockDim.x;
-    const long long c0 = warp * items * 32 + lane;
+    const int cols = (int)a.cols, K = a.n_keep;
+    const int items = (cols + THREADS - 1) / THREADS;      // per thread, 32 apart
+    const long long c0 = (long long)warp * items * 32 + lane;
     const bool held = items <= kSelectItems;
-    auto load = [&](long long c) {
-        return c < a.cols ? score_key(row[c], c < a.keep_first) : 0u;
-    };
+    auto load = [&](long long c) { return c < cols ? score_key(row[c], c < a.keep_first) : 0u; };
     uint32_t key[kSelectItems];
 #pragma unroll
-    for (int j = 0; j < kSelectItems; ++j) key[j] = j < items ? load(c0 + 32 * j) : 0u;
-    int flip = 0;
-    // columns of the row whose key is at least t
-    auto count = [&](uint32_t t) {
-        int n = 0;
+    for (int j = 0; j < kSelectItems; ++j) key[j] = held && j < items ? load(c0 + 32 * j) : 0u;
+    auto each = [&](auto f) {                              // f(key, column) of this thread's columns, in order
         if (held) {
 #pragma unroll
-            for (int j = 0; j < kSelectItems; ++j) n += key[j] >= t;
+            for (int j = 0; j < kSelectItems; ++j)
+                if (j < items) f(key[j], c0 + 32 * j);
         } else {
-            for (long long j = 0; j < items; ++j) n += load(c0 + 32 * j) >= t;
+            for (int j = 0; j < items; ++j) f(load(c0 + 32LL * j), c0 + 32LL * j);
         }
-        n = __reduce_add_sync(kFull, n);
-        if (lane == 0) red[flip][warp] = n;
-        __syncthreads();
-        int s = lane < nw ? red[flip][lane] : 0;
-        s = __reduce_add_sync(kFull, s);
-        flip ^= 1;                 // the next count writes the other half: no second barrier
-        return s;
     };
-    const int K = a.n_keep;
-    uint32_t t = 1u;               // least key taken
-    const int valid = count(1u);
-    int take = valid < K ? valid : K;
-    if (valid > K) {
-        t = 0u;
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t c = t | (1u << bit);
-            const int n = count(c);
-            if (n >= K) {
-                t = c;
-                if (n == K) break;
+    // the wanted key is among those in [lo, hi]: `above` keys are greater than hi
+    uint32_t lo = 1u, hi = 0xffffffffu;
+    int above = 0, valid = 0;
+    uint32_t t = 1u;
+    for (int round = 0;; ++round) {
+        // the span of the keys left, and (first round) how many there are
+        uint32_t least = 0xffffffffu, most = 0u;
+        int n = 0;
+        each([&](uint32_t k, long long) {
+            if (k >= lo && k <= hi) {
+                least = min(least, k);
+                most = max(most, k);
+                ++n;
             }
+        });
+        least = __reduce_min_sync(kFull, least);
+        most = __reduce_max_sync(kFull, most);
+        n = __reduce_add_sync(kFull, n);
+        if (lane == 0) {
+            lo_s[warp] = least;
+            hi_s[warp] = most;
+            n_s[warp] = n;
         }
-    }
-    // every key above t is taken, and of those equal to t the first `ties`
-    auto key_at = [&](long long j) { return held ? 0u : load(c0 + 32 * j); };
-    int na = 0, ne = 0;
-    auto tally = [&](uint32_t k) {
-        na += __popc(__ballot_sync(kFull, k > t));
-        ne += __popc(__ballot_sync(kFull, k == t));
-    };
-    if (held) {
+        for (int j = tid; j < kBins; j += THREADS) hist[j] = 0;
+        __syncthreads();
+        least = __reduce_min_sync(kFull, lane < kW ? lo_s[lane] : 0xffffffffu);
+        most = __reduce_max_sync(kFull, lane < kW ? hi_s[lane] : 0u);
+        n = __reduce_add_sync(kFull, lane < kW ? n_s[lane] : 0);
+        if (round == 0) {
+            valid = n;
+            if (valid <= K) break;                         // everything that may be taken
+        }
+        lo = least;
+        hi = most;
+        t = lo;
+        if (above + n == K || lo == hi) break;             // all of them, or equal ones
+        const int shift = max(0, 21 - __clz(hi - lo));     // (hi - lo) >> shift < 2048
+        each([&](uint32_t k, long long) {
+            if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> shift], 1);
+        });
+        __syncthreads();
+        // the bin of the (K - above)-th greatest: counts of the bins above each thread's
+        int mine[kBinsPerThread], sum = 0;
 #pragma unroll
-        for (int j = 0; j < kSelectItems; ++j) tally(key[j]);
-    } else {
-        for (long long j = 0; j < items; ++j) tally(key_at(j));
+        for (int j = 0; j < kBinsPerThread; ++j) {
+            mine[j] = hist[kBins - 1 - (tid * kBinsPerThread + j)];
+            sum += mine[j];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) m_s[warp] = incl;
+        __syncthreads();
+        int over = above + incl - sum + __reduce_add_sync(kFull, lane < warp ? m_s[lane] : 0);
+#pragma unroll
+        for (int j = 0; j < kBinsPerThread; ++j) {
+            if (over < K && over + mine[j] >= K) {
+                found_bin = kBins - 1 - (tid * kBinsPerThread + j);
+                found_above = over;
+                found_count = mine[j];
+            }
+            over += mine[j];
+        }
+        __syncthreads();
+        above = found_above;
+        hi = lo + min(hi - lo, ((found_bin + 1u) << shift) - 1u);   // (by offsets: lo plus a bin's end may pass 2^32)
+        lo = lo + (found_bin << shift);
+        t = lo;
+        if (shift == 0 || above + found_count == K) break;
     }
+    const int take = min(valid, K);
+    int na = 0, ne = 0;
+    each([&](uint32_t k, long long) {
+        na += k > t;
+        ne += k == t;
+    });
+    na = __reduce_add_sync(kFull, na);
+    ne = __reduce_add_sync(kFull, ne);
+    __syncthreads();
     if (lane == 0) {
-        above_s[warp] = na;
-        equal_s[warp] = ne;
+        n_s[warp] = na;
+        m_s[warp] = ne;
     }
     __syncthreads();
-    const int wa = lane < nw ? above_s[lane] : 0, we = lane < nw ? equal_s[lane] : 0;
-    const int total_above = __reduce_add_sync(kFull, wa);
-    const int ties = take - total_above;
+    const int wa = lane < kW ? n_s[lane] : 0, we = lane < kW ? m_s[lane] : 0;
+    const int ties = take - __reduce_add_sync(kFull, wa);
     int before_a = __reduce_add_sync(kFull, lane < warp ? wa : 0);
     int before_e = __reduce_add_sync(kFull, lane < warp ? we : 0);
     const uint32_t below = (1u << lane) - 1u;
-    auto place = [&](uint32_t k, long long c) {
-        const uint32_t ma = __ballot_sync(kFull, k > t), me = __ballot_sync(kFull, k == t && t != 0u);
+    each([&](uint32_t k, long long c) {
+        const uint32_t ma = __ballot_sync(kFull, k > t), me = __ballot_sync(kFull, k == t);
+        if ((ma | me) == 0u) return;
         const int ra = before_a + __popc(ma & below), re = before_e + __popc(me & below);
-        if (k > t || (k == t && t != 0u && re < ties)) out[ra + min(re, ties)] = (int)c;
+        if (k > t || (k == t && re < ties)) out[ra + min(re, ties)] = (int)c;
         before_a += __popc(ma);
         before_e += __popc(me);
-    };
-    if (held) {
-#pragma unroll
-        for (int j = 0; j < kSelectItems; ++j) place(key[j], c0 + 32 * j);
-    } else {
-        for (long long j = 0; j < items; ++j) place(key_at(j), c0 + 32 * j);
-    }
-    for (int j = take + tid; j < K; j += blockDim.x) out[j] = -1;
+    });
+    for (int j = take + tid; j < K; j += THREADS) out[j] = -1;
 }
 
 // A token appended to each of n sequences: residual rows of keys and values.
@@ -356,10 +468,15 @@ cudaError_t launch_block_scores(const BlockRows& r, const __half* q, float scale
 
 cudaError_t launch_select_blocks(const float* scores, long long rows, long long cols, long long ld, int n_keep,
                                  int keep_first, int* blocks, cudaStream_t st) {
-    const long long warps = (cols + 31) / 32;
-    const int threads = warps >= kSelectThreads / 32 ? kSelectThreads : warps < 1 ? 32 : (int)warps * 32;
-    const SelectArgs a{scores, cols, ld, n_keep, keep_first, blocks};
-    return launch_dependent(select_blocks_kernel, dim3((unsigned)rows), threads, st, a);
+    const SelectArgs a{scores, rows, cols, ld, n_keep, keep_first, blocks};
+    if (cols <= 32 * kWarpItems)
+        return launch_dependent(select_blocks_warp_kernel, dim3((unsigned)((rows + kWarpRows - 1) / kWarpRows)),
+                                32 * kWarpRows, st, a);
+    const dim3 grid((unsigned)rows);
+    // as few threads as hold the row: each barrier costs by the warps that meet there
+    if (cols <= 256 * kSelectItems) return launch_dependent(select_blocks_kernel<256>, grid, 256, st, a);
+    if (cols <= 512 * kSelectItems) return launch_dependent(select_blocks_kernel<512>, grid, 512, st, a);
+    return launch_dependent(select_blocks_kernel<1024>, grid, 1024, st, a);
 }
 
 cudaError_t launch_decode_blocks(const BlockRows& r, const __half* q, const int* list, int n_list, float scale_log2,
