@@ -473,8 +473,9 @@ cudaError_t launch_select_blocks(const float* scores, long long rows, long long 
         return launch_dependent(select_blocks_warp_kernel, dim3((unsigned)((rows + kWarpRows - 1) / kWarpRows)),
                                 32 * kWarpRows, st, a);
     const dim3 grid((unsigned)rows);
-    // as few threads as hold the row: each barrier costs by the warps that meet there
-    if (cols <= 256 * kSelectItems) return launch_dependent(select_blocks_kernel<256>, grid, 256, st, a);
+    // 8 to 16 keys a thread: more threads wait longer at each barrier, fewer count
+    // longer (64 x 4092: 256 threads 8.9 us, 512 8.0, 1024 9.0)
+    if (cols <= 128 * kSelectItems) return launch_dependent(select_blocks_kernel<256>, grid, 256, st, a);
     if (cols <= 512 * kSelectItems) return launch_dependent(select_blocks_kernel<512>, grid, 512, st, a);
     return launch_dependent(select_blocks_kernel<1024>, grid, 1024, st, a);
 }

@@ -38,8 +38,9 @@ kivi_status failf(kivi_status st, const char* fmt, ...) {
     return report_error(st, msg);
 }
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kAhead = 2;     // groups of heads computed together, with the next ones' loads in flight
 
 struct Part {                 // one of q, k, v
     const void* src;
@@ -48,7 +49,7 @@ struct Part {                 // one of q, k, v
     long long d_slot;         // elements between (batch row, head) slots
     const float* w;           // null: no norm
     int heads;
-    int chunks;               // grid.y entries of this tensor
+    int chunks, passes;       // grid.y entries of this tensor, and the groups of heads each takes
     int turn;                 // rotated
 };
 struct Args {
@@ -58,30 +59,27 @@ struct Args {
     const void* positions;
     long long first_position, n_positions;
     int rot, wide;            // rotated channels; positions are 64-bit
-    int passes;               // groups of heads a warp takes
     float eps;
 };
 
+// four channels as loaded, and as fp32
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, float (&x)[4]) {
-    if constexpr (sizeof(T) == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        if constexpr (sizeof(T) == sizeof(__half)) {
-            float2 a, b;
-            if constexpr (__is_same(T, __half)) {
-                a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
-                b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-            } else {
-                a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-                b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-            }
-            x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-        }
-    }
+struct Raw { using type = uint2; };
+template <>
+struct Raw<float> { using type = uint4; };
+__device__ __forceinline__ void widen(const uint4& v, float (&x)[4], float) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
 }
+__device__ __forceinline__ void widen(const uint2& v, float (&x)[4], __half) {
+    const float2 a = mma_detail::unpack_f16x2(v.x), b = mma_detail::unpack_f16x2(v.y);
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+}
+__device__ __forceinline__ void widen(const uint2& v, float (&x)[4], __nv_bfloat16) {   // bf16: fp32's upper half
+    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ uint2 ldg_raw(const void* p, uint2) { return mma_detail::ldg_stream2(p); }
+__device__ __forceinline__ uint4 ldg_raw(const void* p, uint4) { return mma_detail::ldg_stream(p); }
 __device__ __forceinline__ void store4(__half* p, const float (&x)[4]) {
     uint2 v;
     v.x = mma_detail::pack_f16x2(x[0], x[1]);
@@ -118,6 +116,25 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const __grid_
         cb = ca + (D - rot) / 2;
     }
     const bool turned = 8 * lr < rot;
+    const T* src = reinterpret_cast<const T*>(p.src) + b * p.s_batch + t * p.s_token;
+    __half* dst = p.dst + b * p.heads * p.d_slot + t * D;
+    const int h0 = chunk * p.passes * RPW + sub;
+    // kAhead groups at a time, the next ones' loads before the present ones'
+    // work; the first ones' go out ahead of the token's position and table row
+    using V = typename Raw<T>::type;
+    V xa[kAhead], xb[kAhead];
+    auto fetch = [&](int it, V (&ya)[kAhead], V (&yb)[kAhead]) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int h = h0 + (it + u) * RPW;
+            ya[u] = yb[u] = V{};
+            if (it + u < p.passes && h < p.heads) {
+                ya[u] = ldg_raw(src + h * p.s_head + ca, V{});
+                yb[u] = ldg_raw(src + h * p.s_head + cb, V{});
+            }
+        }
+    };
+    fetch(0, xa, xb);
     float cs[4], sn[4];                   // interleaved: the four pairs of the eight channels
     if (turned) {
         long long pos = a.first_position + t;
@@ -137,58 +154,58 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const __grid_
     }
     float wa[4], wb[4];
     if (p.w) {
-        load4(p.w + ca, wa);
-        load4(p.w + cb, wb);
+        widen(*reinterpret_cast<const uint4*>(p.w + ca), wa, 0.f);
+        widen(*reinterpret_cast<const uint4*>(p.w + cb), wb, 0.f);
     }
-    const T* src = reinterpret_cast<const T*>(p.src) + b * p.s_batch + t * p.s_token;
-    __half* dst = p.dst + b * p.heads * p.d_slot + t * D;
-    const int h0 = chunk * a.passes * RPW + sub;
-#pragma unroll 4
-    for (int it = 0; it < a.passes; ++it) {
-        const int h = h0 + it * RPW;
-        const bool there = h < p.heads;
-        float xa[4] = {0.f, 0.f, 0.f, 0.f}, xb[4] = {0.f, 0.f, 0.f, 0.f};
-        if (there) {
-            load4(src + h * p.s_head + ca, xa);
-            load4(src + h * p.s_head + cb, xb);
-        }
-        if (p.w) {
-            float s = 0.f;
+    for (int it = 0; it < p.passes; it += kAhead) {
+        V na[kAhead], nb[kAhead];
+        fetch(it + kAhead, na, nb);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], s));
+        for (int u = 0; u < kAhead; ++u) {
+            const int h = h0 + (it + u) * RPW;
+            float ya[4], yb[4];
+            widen(xa[u], ya, T{});
+            widen(xb[u], yb, T{});
+            if (p.w) {
+                float s = 0.f;
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-            const float r = 1.0f / sqrtf(s * (1.0f / D) + a.eps);
+                for (int j = 0; j < 4; ++j) s = fmaf(ya[j], ya[j], fmaf(yb[j], yb[j], s));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                xa[j] = xa[j] * r * wa[j];
-                xb[j] = xb[j] * r * wb[j];
-            }
-        }
-        if (turned) {
-            if (INTERLEAVED) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float u = xa[2 * j], v = xa[2 * j + 1];
-                    xa[2 * j] = u * cs[j] - v * sn[j];
-                    xa[2 * j + 1] = v * cs[j] + u * sn[j];
-                    const float y = xb[2 * j], z = xb[2 * j + 1];
-                    xb[2 * j] = y * cs[2 + j] - z * sn[2 + j];
-                    xb[2 * j + 1] = z * cs[2 + j] + y * sn[2 + j];
-                }
-            } else {
+                for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+                const float r = 1.0f / sqrtf(s * (1.0f / D) + a.eps);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float u = xa[j], v = xb[j];
-                    xa[j] = u * cs[j] - v * sn[j];
-                    xb[j] = v * cs[j] + u * sn[j];
+                    ya[j] = ya[j] * r * wa[j];
+                    yb[j] = yb[j] * r * wb[j];
                 }
             }
-        }
-        if (there) {
-            __half* row = dst + h * p.d_slot;
-            store4(row + ca, xa);
-            store4(row + cb, xb);
+            if (turned) {
+                if (INTERLEAVED) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float x0 = ya[2 * j], x1 = ya[2 * j + 1];
+                        ya[2 * j] = x0 * cs[j] - x1 * sn[j];
+                        ya[2 * j + 1] = x1 * cs[j] + x0 * sn[j];
+                        const float x2 = yb[2 * j], x3 = yb[2 * j + 1];
+                        yb[2 * j] = x2 * cs[2 + j] - x3 * sn[2 + j];
+                        yb[2 * j + 1] = x3 * cs[2 + j] + x2 * sn[2 + j];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x0 = ya[j], x1 = yb[j];
+                        ya[j] = x0 * cs[j] - x1 * sn[j];
+                        yb[j] = x1 * cs[j] + x0 * sn[j];
+                    }
+                }
+            }
+            if (it + u < p.passes && h < p.heads) {
+                __half* row = dst + h * p.d_slot;
+                store4(row + ca, ya);
+                store4(row + cb, yb);
+            }
+            xa[u] = na[u];
+            xb[u] = nb[u];
         }
     }
 }
@@ -196,15 +213,20 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const __grid_
 template <typename T, int D>
 cudaError_t launch_t(Args& a, int interleaved, cudaStream_t st) {
     constexpr int RPW = 256 / D;
-    // heads a warp walks over: enough to spread the token's table row and
-    // weights, unless the call has too few tokens to fill the GPU that way
+    // Groups of heads a warp walks over: as many as leave about 8192 warps (one
+    // wave of the GPU), 2 to 16, the same number in all chunks of a tensor.  A
+    // long walk spreads the token's table row and keeps loads in flight (7B prompt,
+    // 96 heads x 32768 tokens: 2 groups 371 us, 16 groups 252 us); a short one
+    // fills the GPU (2331 tokens of 32 heads: 2 groups 7.1 us, 16 groups 15.6 us).
     long long groups = 0;
     for (const Part& p : a.part) groups += (p.heads + RPW - 1) / RPW;
-    const long long warps = groups * a.total;
-    a.passes = warps >= 8LL * 152 * 64 ? 8 : warps >= 4LL * 152 * 64 ? 4 : 1;
+    const long long fit = groups * a.total / 8192;
+    const int most = fit < 2 ? 2 : fit > 16 ? 16 : (int)fit;
     int chunks = 0;
     for (Part& p : a.part) {
-        p.chunks = ((p.heads + RPW - 1) / RPW + a.passes - 1) / a.passes;
+        const int n = (p.heads + RPW - 1) / RPW;
+        p.chunks = (n + most - 1) / most;
+        p.passes = p.chunks ? (n + p.chunks - 1) / p.chunks : 0;
         chunks += p.chunks;
     }
     const long long ctas = (a.total + kWarps - 1) / kWarps;
@@ -256,7 +278,7 @@ cudaError_t launch_qk_norm_rope(const kivi_qkv& q, const QkvDest& d, cudaStream_
     Args a{};
     const bool turn = q.cos_sin != nullptr;
     auto part = [](const void* src, const long long* s, __half* dst, long long slot, const float* w, int heads, int t) {
-        return Part{src, s[0], s[1], s[2], dst, slot, w, src ? heads : 0, 0, t};
+        return Part{src, s[0], s[1], s[2], dst, slot, w, src ? heads : 0, 0, 0, t};
     };
     a.part[0] = part(q.q, q.q_stride, d.q, d.q_slot, q.q_weight, q.n_q_heads, turn);
     a.part[1] = part(q.k, q.k_stride, d.k, d.k_slot, q.k_weight, q.n_kv_heads, turn);
