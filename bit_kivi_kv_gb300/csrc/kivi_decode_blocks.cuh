@@ -161,10 +161,8 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     // the residual's query: fp16 hi and lo parts of each head, a padded row each
     __shared__ __align__(16) __half qres[2 * NQ][D + 8];
     // partial results: (m, l, status) per query head of each warp's residual
-    // tiles and of its listed blocks, the merge's weights, the CTA's merged heads
+    // tiles and of its listed blocks
     __shared__ __align__(16) float4 head_s[2 * kMaxRowWarps][NQ];
-    __shared__ float wgt_s[NQ][2 * kMaxRowWarps];
-    __shared__ __align__(16) float4 cta_head[NQ];
     // from the cluster's CTAs: their value sums of this CTA's outputs, and their heads
     __shared__ __align__(16) float recv_s[NQ * D];
     __shared__ __align__(16) float4 recv_head[kMaxCluster][NQ];
@@ -333,11 +331,18 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         }
         __syncwarp();
     };
-    if (k < we) read_part();
-    __half2 qv = __half2half2(__ushort_as_half(0));                // a channel pair of the query
-    const __half2* qp = reinterpret_cast<const __half2*>(a.q + ((long long)b * a.Hq + hk * NQ) * D);
-    if (tid < NQ * D / 2) qv = qp[tid];
-    if (k < we) begin_part();
+    // channel pair idx of the query (volatile: on its way while the list is read)
+    const __half* qp = a.q + ((long long)b * a.Hq + hk * NQ) * D;
+    auto query = [&](int idx) {
+        uint32_t x = 0u;
+        if (idx < NQ * D / 2) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(x) : "l"(qp + 2 * idx));
+        return x;
+    };
+    const uint32_t qv = query(tid);
+    if (k < we) {
+        read_part();
+        begin_part();
+    }
     if (lane == 0 && tb < te) {                   // the residual rows into L2 behind the first copies
         const uint32_t bytes = (uint32_t)((min(16 * te, n_res) - 16 * tb) * D * 2);
         prefetch_l2(kr + 16LL * tb * D, bytes);
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     }
     for (int idx = tid; idx < NQ * D / 2; idx += blockDim.x) {
         const int j = idx / (D / 2), cp = idx % (D / 2);
-        const float2 f = __half22float2(idx == tid ? qv : qp[idx]);
+        const float2 f = unpack_f16x2(idx == tid ? qv : query(idx));
         const float x0 = f.x * a.scale_log2, x1 = f.y * a.scale_log2;
         qf[j][2 * cp] = x0;
         qf[j][2 * cp + 1] = x1;
@@ -382,26 +387,28 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     float beta = 0.f;
 
     // Online softmax step over two tiles: sc * unit = logits of tokens g, g+8
-    // of tile A and of tile B (head i); p receives their probabilities.
+    // of tile A and of tile B (head i); p receives their probabilities.  The
+    // maximum over the lanes is taken only when some lane's logit passes the
+    // running one, which happens ever more rarely.
     auto softmax = [&](const float (&sc)[4], float (&p)[4], float unit) {
-        float mt = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 4));
-        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 8));
-        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 16));
-        const float mn = fmaxf(m, mt * unit);
-        if (fresh) {
+        float mt = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])) * unit;
+        if (__any_sync(kFull, mt > m)) {
+            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 4));
+            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 8));
+            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 16));
+            const float mn = fmaxf(m, mt);
+            if (!fresh) {                         // (before the first tiles o, zeta and l are zero)
+                const float alpha = m == mn ? 1.f : fast_exp2(m - mn);
+                l *= alpha;
+                const float ao = __shfl_sync(kFull, alpha, (lane & ~3) | (hO < NQ ? hO : 0));
+#pragma unroll
+                for (int t = 0; t < KS; ++t) { o[t][0] *= ao; o[t][1] *= ao; o[t][2] *= ao; o[t][3] *= ao; }
+                const float az = __shfl_sync(kFull, alpha, col_ok ? hP : 0);
+#pragma unroll
+                for (int f = 0; f < NBF; ++f) zeta[f] *= az;
+            }
             m = mn;
             fresh = false;
-        } else if (__any_sync(kFull, mn > m)) {
-            const float alpha = fast_exp2(m - mn);
-            l *= alpha;
-            const float ao = __shfl_sync(kFull, alpha, (lane & ~3) | (hO < NQ ? hO : 0));
-#pragma unroll
-            for (int t = 0; t < KS; ++t) { o[t][0] *= ao; o[t][1] *= ao; o[t][2] *= ao; o[t][3] *= ao; }
-            const float az = __shfl_sync(kFull, alpha, col_ok ? hP : 0);
-#pragma unroll
-            for (int f = 0; f < NBF; ++f) zeta[f] *= az;
-            m = mn;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) p[j] = fast_exp2(fmaf(sc[j], unit, -m));
@@ -435,6 +442,13 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
             const uint2 x = lds64(src + lane_words);
             w[0] = x.x; w[1] = x.y;
         }
+    };
+    auto sum_l = [&]() {                          // l over the lanes of a head
+        float lt = l;
+        lt += __shfl_xor_sync(kFull, lt, 4);
+        lt += __shfl_xor_sync(kFull, lt, 8);
+        lt += __shfl_xor_sync(kFull, lt, 16);
+        return lt;
     };
     // ---- the listed blocks ----
     while (k < we) {
@@ -506,10 +520,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
                 }
             }
             __syncwarp();                                      // every lane is done with this stage
-            if (lane == 0 && k + C::STAGES < kend) {
-                fence_proxy_async();
-                issue(k + C::STAGES, item + C::STAGES);
-            }
+            if (lane == 0 && k + C::STAGES < kend) issue(k + C::STAGES, item + C::STAGES);
         }
         if (failed) {
             // a copy timed out: wait (bounded) for the copies in flight, issue no more
@@ -528,13 +539,6 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         const float s1 = pow2i(24 - BITS * ((2 * mt + 1) % (8 / BITS)));
         o[mt][0] *= s0; o[mt][1] *= s0; o[mt][2] *= s1; o[mt][3] *= s1;
     }
-    auto sum_l = [&]() {                          // l over the lanes of a head
-        float lt = l;
-        lt += __shfl_xor_sync(kFull, lt, 4);
-        lt += __shfl_xor_sync(kFull, lt, 8);
-        lt += __shfl_xor_sync(kFull, lt, 16);
-        return lt;
-    };
     // ---- the listed blocks' partial result ----
 #pragma unroll
     for (int f = 0; f < NBF; ++f) {
@@ -620,51 +624,41 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     }
 
     // ---- the log-sum-exp merge: the CTA's partials, then the cluster's CTAs ----
-    // weights 2^(m - M) and the sum L over the lanes' (m, l, status)
-    auto weigh = [&](float4 x, float& M, float& L, bool& bad) {
-        M = x.x;
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, s));
-        const float e = x.x == -INFINITY ? 0.f : fast_exp2(x.x - M);
-        L = x.y * e;
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(kFull, L, s);
-        bad = __any_sync(kFull, x.z != 0.f);
-        return e;
-    };
-    const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    __syncthreads();
-    for (int h = warp; h < NQ; h += warps) {
-        float M, L;
-        bool bad;
-        const float e = weigh(lane < 2 * warps ? head_s[lane][h] : none, M, L, bad);
-        if (lane < 2 * warps) wgt_s[h][lane] = csize > 1 ? e : bad ? NAN : e / L;
-        if (lane == 0) cta_head[h] = make_float4(M, L, bad ? 1.f : 0.f, 0.f);
-    }
-    __syncthreads();
-    // a warp's value sums: of its residual tiles and of its blocks; a partial
-    // without tokens has weight 0 (and, of the residual, no sums)
-    __half* out = a.out + ((long long)b * a.Hq + hk * NQ) * D;
+    // every thread weighs the partials of its outputs' heads for itself: reads
+    // of one address by many threads, and one barrier instead of two
     const int span = NQ * D / (int)csize;         // the outputs a CTA of the cluster writes
+    __half* out = a.out + ((long long)b * a.Hq + hk * NQ) * D;
     if (csize > 1) cluster_wait();                // (every CTA has started: its shared memory may be written)
+    __syncthreads();
     for (int idx = tid; idx < NQ * D; idx += blockDim.x) {
-        const float* w = wgt_s[idx / D];
-        float s = 0.f;
+        const int h = idx / D;
+        float M = -INFINITY, L = 0.f, s = 0.f, bad = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < 2 * warps; ++j) M = fmaxf(M, head_s[j][h].x);
 #pragma unroll 4
         for (int j = 0; j < warps; ++j) {
+            const float4 xr = head_s[j][h], xb = head_s[warps + j][h];
             const float* mine = reinterpret_cast<const float*>(dyn_smem + j * S::WARP) + idx;
-            const float vr = mine[S::SUMS / 4], vb = mine[0], er = w[j], eb = w[warps + j];
+            const float vr = mine[S::SUMS / 4], vb = mine[0];
+            // a partial without tokens has weight 0 (and, of the residual, no sums)
+            const float er = xr.x == -INFINITY ? 0.f : fast_exp2(xr.x - M);
+            const float eb = xb.x == -INFINITY ? 0.f : fast_exp2(xb.x - M);
+            L = fmaf(xr.y, er, fmaf(xb.y, eb, L));
             s = er == 0.f ? s : fmaf(vr, er, s);
             s = eb == 0.f ? s : fmaf(vb, eb, s);
+            bad += xb.z;
         }
-        if (csize > 1) stc32(cluster_map(smem_u32(&recv_s[(int)crank * span + idx % span]), idx / span), s);
-        else out[idx] = __float2half_rn(s);
+        if (csize > 1) {
+            stc32(cluster_map(smem_u32(&recv_s[(int)crank * span + idx % span]), idx / span), s);
+            if (idx % D < (int)csize)             // (csize <= 8 < D) the head's (M, L, status) to each CTA
+                stc128(cluster_map(smem_u32(&recv_head[crank][h]), idx % D), make_float4(M, L, bad, 0.f));
+        } else {
+            out[idx] = __float2half_rn(bad != 0.f ? NAN : s / L);
+        }
     }
     if (csize == 1) return;
     // each CTA has sent the owner of every output its sum, and all of them its
-    // heads' (M, L, status); nothing is read from afar, so a CTA may leave first
-    for (int idx = tid; idx < NQ * (int)csize; idx += blockDim.x)
-        stc128(cluster_map(smem_u32(&recv_head[crank][idx % NQ]), idx / NQ), cta_head[idx % NQ]);
+    // heads; nothing is read from afar, so a CTA may leave first
     __syncwarp();
     cluster_arrive();
     cluster_wait();
