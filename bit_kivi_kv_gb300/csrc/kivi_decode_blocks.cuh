@@ -134,6 +134,13 @@ __device__ __forceinline__ void value_mma(const uint32_t (&w)[W], const B& bfrag
     }
 }
 
+// Whether odd warps take their residual tiles before their blocks, which spreads
+// the tiles' plain loads over the call.  It costs registers: with four heads of
+// 128 channels, which have 168, 44.7 -> 43.9 us (512 rows); with one head, which
+// has 128, 11.6 -> 12.4 us (256 rows).
+template <int D, int NQ>
+constexpr bool kAlternate = D == 128 && NQ == 4;
+
 // Dynamic shared memory of a CTA: per warp its copy ring (which later takes the
 // listed blocks' value sums [NQ][D] fp32), the key fragment table, the list's
 // offsets and the residual tiles' value sums [NQ][D] fp32.
@@ -141,7 +148,8 @@ template <int D, int BITS, int NQ, int G>
 struct Smem {
     using C = Cfg<D, BITS, NQ, G>;
     static constexpr int RING = C::STAGES * C::STAGE_BYTES;
-    static constexpr int FRAG = RING, OFFS = FRAG + 32 * C::QSTRIDE * 4, SUMS = OFFS + kListCache * 8;
+    static constexpr int ROWS = NQ > 1 ? 32 : 8 * NQ + 1;      // rows of the key fragment table
+    static constexpr int FRAG = RING, OFFS = FRAG + ROWS * C::QSTRIDE * 4, SUMS = OFFS + kListCache * 8;
     static constexpr int WARP = (SUMS + NQ * D * 4 + 127) / 128 * 128;
     static_assert(NQ * D * 4 <= RING, "the value sums reuse the copy ring");
 };
@@ -178,7 +186,9 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     uint32_t* qfrag = reinterpret_cast<uint32_t*>(ring + S::FRAG);
     long long* offs = reinterpret_cast<long long*>(ring + S::OFFS);
     uint64_t* bars = full_bar[warp];
-    for (int idx = lane; idx < 32 * C::QSTRIDE; idx += 32) qfrag[idx] = 0u;   // unused columns stay 0
+    // B columns from 2 NQ on are zero: with the fragments in registers each lane
+    // has its row of the table, else those lanes share the row behind the others'
+    for (int idx = 8 * NQ * C::QSTRIDE + lane; idx < S::ROWS * C::QSTRIDE; idx += 32) qfrag[idx] = 0u;
     if (lane == 0) {
 #pragma unroll
         for (int st = 0; st < C::STAGES; ++st) mbar_init(&bars[st], 1);
@@ -220,19 +230,19 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     // to w leaves beside the tiles before it.
     const int P = min(a.n_list, nblk) * PPB, T = (n_res + 15) / 16;
     const int workers = (int)csize * warps, worker = (int)crank * warps + warp;
-    const int tb = (int)((long long)worker * T / workers), te = (int)((long long)(worker + 1) * T / workers);
-    const long long wt = (long long)T * a.wr + (long long)P * a.wq;
-    auto pairs_upto = [&](auto w) {
-        using I = decltype(w);                    // 32-bit unless the list is very long
-        int most = 0;
-        for (I v = lane; v <= w; v += 32) {
-            const I y = v * (I)wt / (I)workers - v * (I)T / (I)workers * (I)a.wr;
-            most = max(most, (int)min((I)P, (max((I)0, y) + (I)a.wq - 1) / (I)a.wq));
-        }
-        return __reduce_max_sync(kFull, most);
+    const int tb = (int)((unsigned)worker * (unsigned)T / (unsigned)workers);
+    const int te = (int)(((unsigned)worker + 1u) * (unsigned)T / (unsigned)workers);
+    // (Every warp computes the same fp32 values, so the shares fit together
+    // whatever their rounding.)
+    const float per_worker = ((float)T * a.wr + (float)P * a.wq) / workers, per_tile = (float)T / workers;
+    const float inv_wq = 1.0f / a.wq;
+    auto pairs_before = [&](int w) {
+        float most = 0.f;
+        for (int v = lane; v <= w; v += 32)
+            most = fmaxf(most, (v * per_worker - floorf(v * per_tile) * a.wr) * inv_wq);
+        return min(P, __reduce_max_sync(kFull, (int)ceilf(most)));
     };
-    auto pairs_before = [&](int w) { return wt < (1 << 22) ? pairs_upto(w) : pairs_upto((long long)w); };
-    const int wb = pairs_before(worker), we = worker + 1 == workers ? P : pairs_before(worker + 1);
+    const int wb = worker == 0 ? 0 : pairs_before(worker), we = worker + 1 == workers ? P : pairs_before(worker + 1);
 
     // everything below reads what earlier kernels on the stream may have written
     griddepcontrol_wait();
@@ -343,11 +353,6 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         read_part();
         begin_part();
     }
-    if (lane == 0 && tb < te) {                   // the residual rows into L2 behind the first copies
-        const uint32_t bytes = (uint32_t)((min(16 * te, n_res) - 16 * tb) * D * 2);
-        prefetch_l2(kr + 16LL * tb * D, bytes);
-        prefetch_l2(vr + 16LL * tb * D, bytes);
-    }
     for (int idx = tid; idx < NQ * D / 2; idx += blockDim.x) {
         const int j = idx / (D / 2), cp = idx % (D / 2);
         const float2 f = unpack_f16x2(idx == tid ? qv : query(idx));
@@ -373,8 +378,6 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     float o[KS][4];
     float zeta[NBF];
 #pragma unroll
-    for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-#pragma unroll
     for (int f = 0; f < NBF; ++f) zeta[f] = 0.f;
     constexpr bool QB_REGS = NQ > 1;
     uint32_t qb[2 * KS] = {};
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         if constexpr (QB_REGS)
             return make_uint2(qb[2 * kk], qb[2 * kk + 1]);
         else
-            return *reinterpret_cast<const uint2*>(qfrag + lane * C::QSTRIDE + 2 * kk);
+            return *reinterpret_cast<const uint2*>(qfrag + min(lane, 8 * NQ) * C::QSTRIDE + 2 * kk);
     };
     float beta = 0.f;
 
@@ -450,210 +453,230 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         lt += __shfl_xor_sync(kFull, lt, 16);
         return lt;
     };
-    // ---- the listed blocks ----
-    while (k < we) {
-        if (k >= kend) {
-            read_part();
-            begin_part();
-        }
-        bool failed = false;
-        bool skip = offs[k / PPB - j0] < 0;
-        for (; k < kend; ++k, ++item) {
-            const uint32_t st = item % C::STAGES;
-            if (!__all_sync(kFull, mbar_wait(&bars[st], (item / C::STAGES) & 1u))) { failed = true; break; }
-            const uint8_t* stage = ring + st * C::STAGE_BYTES;
-            const uint32_t stage_u32 = ring_u32 + st * C::STAGE_BYTES;
-            const bool first_of_block = k % PPB == 0 || k == wb;
-            if (first_of_block) skip = offs[k / PPB - j0] < 0;
-            if (!skip) {
-                if (first_of_block)
-                    build_q_frags<C, D, NQ, QB_REGS>(stage + C::KE, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);
-                float ca[4] = {0.f, 0.f, 0.f, 0.f}, cb[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t wa[W], wc[W];
-                lds_words(stage_u32 + C::KT, wa);
-                if constexpr (BITS == 8) {                     // one tile at a time: the words of two do not fit
-                    key_mma<BITS, W, KS>(wa, qbk, ca);
-                    lds_words(stage_u32 + C::KT + C::TILE, wc);
-                    key_mma<BITS, W, KS>(wc, qbk, cb);
-                } else {                                       // two chains of sums side by side
-                    lds_words(stage_u32 + C::KT + C::TILE, wc);
-                    key_mma2<BITS, W, KS>(wa, wc, qbk, ca, cb);
-                }
-                const float sc[4] = {ca[0] + (ca[1] + beta), ca[2] + (ca[3] + beta), cb[0] + (cb[1] + beta),
-                                     cb[2] + (cb[3] + beta)};
-                constexpr bool HOIST = BITS != 8 && W <= 4;   // as in the dense kernel
-                uint32_t wvh[2][W];
-                if constexpr (HOIST) {
-                    lds_words(stage_u32 + C::VT, wvh[0]);
-                    lds_words(stage_u32 + C::VT + C::TILE, wvh[1]);
-                }
-                float p[4];
-                softmax(sc, p, 0x1p24f);                       // scores are in units of 2^-24
+    // A warp's two parts, each with a partial result of its own.
+    auto clear = [&]() {
+        m = -INFINITY;
+        l = 0.f;
+        fresh = true;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    float prb[4];
-                    gather(p[2 * t], p[2 * t + 1], prb);
-                    uint32_t ph01, ph89, pl01, pl89;
-                    split_p(prb, ph01, ph89, pl01, pl89);
-                    const uint32_t ve = stage_u32 + C::VE + t * C::ENT + eoff;
-                    uint32_t pb[NBF][2];
-#pragma unroll
-                    for (int f = 0; f < NBF; ++f) {            // B fragments of p * step, and p . zero
-                        const uint2 sv = lds64(ve + 32u * GB * f), zv = lds64(ve + 32u * (NGRP + GB * f));
-                        const uint32_t h01 = hmul2(ph01, sv.x), h89 = hmul2(ph89, sv.y);
-                        const uint32_t l01 = hfma2(pl01, sv.x, hfma2(ph01, sv.x, neg_f16x2(h01)));
-                        const uint32_t l89 = hfma2(pl89, sv.y, hfma2(ph89, sv.y, neg_f16x2(h89)));
-                        pb[f][0] = lo_col ? l01 : h01;
-                        pb[f][1] = lo_col ? l89 : h89;
-                        const float2 z01 = unpack_f16x2(zv.x), z89 = unpack_f16x2(zv.y);
-                        zeta[f] = fmaf(prb[0], z01.x, fmaf(prb[1], z01.y, fmaf(prb[2], z89.x, fmaf(prb[3], z89.y, zeta[f]))));
-                    }
-                    uint32_t wv[W];
-                    if constexpr (HOIST) {
-#pragma unroll
-                        for (int x = 0; x < W; ++x) wv[x] = wvh[t][x];
-                    } else {
-                        lds_words(stage_u32 + C::VT + t * C::TILE, wv);
-                    }
-                    auto pbk = [&](int mt) { return make_uint2(pb[(16 * mt / G) / GB][0], pb[(16 * mt / G) / GB][1]); };
-                    value_mma<BITS, W, KS>(wv, pbk, o);
-                }
+        for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    };
+    auto block_part = [&]() {
+        // ---- the listed blocks ----
+        while (k < we) {
+            if (k >= kend) {
+                read_part();
+                begin_part();
             }
-            __syncwarp();                                      // every lane is done with this stage
-            if (lane == 0 && k + C::STAGES < kend) issue(k + C::STAGES, item + C::STAGES);
+            bool failed = false;
+            bool skip = offs[k / PPB - j0] < 0;
+            for (; k < kend; ++k, ++item) {
+                const uint32_t st = item % C::STAGES;
+                if (!__all_sync(kFull, mbar_wait(&bars[st], (item / C::STAGES) & 1u))) { failed = true; break; }
+                const uint8_t* stage = ring + st * C::STAGE_BYTES;
+                const uint32_t stage_u32 = ring_u32 + st * C::STAGE_BYTES;
+                const bool first_of_block = k % PPB == 0 || k == wb;
+                if (first_of_block) skip = offs[k / PPB - j0] < 0;
+                if (!skip) {
+                    if (first_of_block)
+                        build_q_frags<C, D, NQ, QB_REGS>(stage + C::KE, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);
+                    float ca[4] = {0.f, 0.f, 0.f, 0.f}, cb[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t wa[W], wc[W];
+                    lds_words(stage_u32 + C::KT, wa);
+                    if constexpr (BITS == 8) {                     // one tile at a time: the words of two do not fit
+                        key_mma<BITS, W, KS>(wa, qbk, ca);
+                        lds_words(stage_u32 + C::KT + C::TILE, wc);
+                        key_mma<BITS, W, KS>(wc, qbk, cb);
+                    } else {                                       // two chains of sums side by side
+                        lds_words(stage_u32 + C::KT + C::TILE, wc);
+                        key_mma2<BITS, W, KS>(wa, wc, qbk, ca, cb);
+                    }
+                    const float sc[4] = {ca[0] + (ca[1] + beta), ca[2] + (ca[3] + beta), cb[0] + (cb[1] + beta),
+                                         cb[2] + (cb[3] + beta)};
+                    constexpr bool HOIST = BITS != 8 && W <= 4;   // as in the dense kernel
+                    uint32_t wvh[2][W];
+                    if constexpr (HOIST) {
+                        lds_words(stage_u32 + C::VT, wvh[0]);
+                        lds_words(stage_u32 + C::VT + C::TILE, wvh[1]);
+                    }
+                    float p[4];
+                    softmax(sc, p, 0x1p24f);                       // scores are in units of 2^-24
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        float prb[4];
+                        gather(p[2 * t], p[2 * t + 1], prb);
+                        uint32_t ph01, ph89, pl01, pl89;
+                        split_p(prb, ph01, ph89, pl01, pl89);
+                        const uint32_t ve = stage_u32 + C::VE + t * C::ENT + eoff;
+                        uint32_t pb[NBF][2];
+#pragma unroll
+                        for (int f = 0; f < NBF; ++f) {            // B fragments of p * step, and p . zero
+                            const uint2 sv = lds64(ve + 32u * GB * f), zv = lds64(ve + 32u * (NGRP + GB * f));
+                            const uint32_t h01 = hmul2(ph01, sv.x), h89 = hmul2(ph89, sv.y);
+                            const uint32_t l01 = hfma2(pl01, sv.x, hfma2(ph01, sv.x, neg_f16x2(h01)));
+                            const uint32_t l89 = hfma2(pl89, sv.y, hfma2(ph89, sv.y, neg_f16x2(h89)));
+                            pb[f][0] = lo_col ? l01 : h01;
+                            pb[f][1] = lo_col ? l89 : h89;
+                            const float2 z01 = unpack_f16x2(zv.x), z89 = unpack_f16x2(zv.y);
+                            zeta[f] = fmaf(prb[0], z01.x, fmaf(prb[1], z01.y, fmaf(prb[2], z89.x, fmaf(prb[3], z89.y, zeta[f]))));
+                        }
+                        uint32_t wv[W];
+                        if constexpr (HOIST) {
+#pragma unroll
+                            for (int x = 0; x < W; ++x) wv[x] = wvh[t][x];
+                        } else {
+                            lds_words(stage_u32 + C::VT + t * C::TILE, wv);
+                        }
+                        auto pbk = [&](int mt) { return make_uint2(pb[(16 * mt / G) / GB][0], pb[(16 * mt / G) / GB][1]); };
+                        value_mma<BITS, W, KS>(wv, pbk, o);
+                    }
+                }
+                __syncwarp();                                      // every lane is done with this stage
+                if (lane == 0 && k + C::STAGES < kend) issue(k + C::STAGES, item + C::STAGES);
+            }
+            if (failed) {
+                // a copy timed out: wait (bounded) for the copies in flight, issue no more
+                status |= 1u;
+                for (int u = 0; u < C::STAGES && k + u < kend; ++u)
+                    mbar_wait(&bars[(item + u) % C::STAGES], ((item + u) / C::STAGES) & 1u);
+                break;
+            }
         }
-        if (failed) {
-            // a copy timed out: wait (bounded) for the copies in flight, issue no more
-            status |= 1u;
-            for (int u = 0; u < C::STAGES && k + u < kend; ++u)
-                mbar_wait(&bars[(item + u) % C::STAGES], ((item + u) / C::STAGES) & 1u);
-            break;
-        }
-    }
-    // the quantized tiles' value sums are in units of 2^(BITS*pos - 24),
-    // pos = (channel / 8) % (8 / BITS): rows g and g+8 of m-tile mt have
-    // classes 2mt and 2mt+1
-#pragma unroll
-    for (int mt = 0; mt < KS; ++mt) {
-        const float s0 = pow2i(24 - BITS * ((2 * mt) % (8 / BITS)));
-        const float s1 = pow2i(24 - BITS * ((2 * mt + 1) % (8 / BITS)));
-        o[mt][0] *= s0; o[mt][1] *= s0; o[mt][2] *= s1; o[mt][3] *= s1;
-    }
-    // ---- the listed blocks' partial result ----
-#pragma unroll
-    for (int f = 0; f < NBF; ++f) {
-        zeta[f] += __shfl_xor_sync(kFull, zeta[f], 1);
-        zeta[f] += __shfl_xor_sync(kFull, zeta[f], 2);
-    }
-    float zo[NBF];
-#pragma unroll
-    for (int f = 0; f < NBF; ++f) zo[f] = __shfl_sync(kFull, zeta[f], 8 * i);
-    float* sums = reinterpret_cast<float*>(ring);
-    if (hO < NQ) {
+        // the quantized tiles' value sums are in units of 2^(BITS*pos - 24),
+        // pos = (channel / 8) % (8 / BITS): rows g and g+8 of m-tile mt have
+        // classes 2mt and 2mt+1
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
-            const int gr = 16 * mt / G;
-            if (gr % GB == jO) {
-                const float z = zo[gr / GB];
-                sums[hO * D + 16 * mt + g] = o[mt][0] + o[mt][1] + z;
-                sums[hO * D + 16 * mt + g + 8] = o[mt][2] + o[mt][3] + z;
-            }
+            const float s0 = pow2i(24 - BITS * ((2 * mt) % (8 / BITS)));
+            const float s1 = pow2i(24 - BITS * ((2 * mt + 1) % (8 / BITS)));
+            o[mt][0] *= s0; o[mt][1] *= s0; o[mt][2] *= s1; o[mt][3] *= s1;
         }
-    }
-    {
-        const uint32_t st_all = __reduce_or_sync(kFull, status);
-        const float lt = sum_l();
-        if (g == 0 && i < NQ) head_s[warps + warp][i] = make_float4(m, lt, (float)st_all, 0.f);
-    }
-
-    // ---- the residual tiles: 16 fp16 rows each, straight from memory.  The
-    // 16-byte loads hand lane i eight consecutive channels, so the MMAs' k
-    // (keys) and m (values) indices run over the channels in another order than
-    // the tiles': k-steps 2j, 2j+1 hold channels 32 j + 8 i + 0..3, + 4..7, and
-    // m-tile 2j+u has row g at channel 32 j + 8 (g / 2) + 4 u + g % 2, row g + 8
-    // two further.  Their partial result is kept apart from the blocks'. ----
-    m = -INFINITY;
-    l = 0.f;
-    fresh = true;
+        // ---- the listed blocks' partial result ----
 #pragma unroll
-    for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-    for (int tile = tb; tile < te; ++tile) {
-        load_rows(tile);
-        const bool okg = 16 * tile + g < n_res, okg8 = 16 * tile + g + 8 < n_res;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < DJ; ++j) {
-            uint4 bq = make_uint4(0, 0, 0, 0);
-            if (g < 2 * NQ) bq = *reinterpret_cast<const uint4*>(&qres[g < 2 * NQ ? g : 0][32 * j + 8 * i]);
-            const uint32_t f0[4] = {kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y};
-            const uint32_t f1[4] = {kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w};
-            mma16816(c, f0, bq.x, bq.y);
-            mma16816(c, f1, bq.z, bq.w);
+        for (int f = 0; f < NBF; ++f) {
+            zeta[f] += __shfl_xor_sync(kFull, zeta[f], 1);
+            zeta[f] += __shfl_xor_sync(kFull, zeta[f], 2);
         }
-        const float sc[4] = {okg ? c[0] + c[1] : -INFINITY, okg8 ? c[2] + c[3] : -INFINITY, -INFINITY, -INFINITY};
-        float p[4];
-        softmax(sc, p, 1.f);
-        float prb[4];
-        gather(p[0], p[1], prb);
-        uint32_t ph01, ph89, pl01, pl89;
-        split_p(prb, ph01, ph89, pl01, pl89);
-        const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
+        float zo[NBF];
 #pragma unroll
-        for (int j = 0; j < DJ; ++j) {
-            const uint32_t f0[4] = {movmatrix_trans(vx[0][j].x), movmatrix_trans(vx[0][j].y),
-                                    movmatrix_trans(vx[1][j].x), movmatrix_trans(vx[1][j].y)};
-            mma16816(o[2 * j], f0, pb0, pb1);
-            const uint32_t f1[4] = {movmatrix_trans(vx[0][j].z), movmatrix_trans(vx[0][j].w),
-                                    movmatrix_trans(vx[1][j].z), movmatrix_trans(vx[1][j].w)};
-            mma16816(o[2 * j + 1], f1, pb0, pb1);
-        }
-    }
-    {
-        float* rsum = reinterpret_cast<float*>(ring + S::SUMS);
-        const float lt = sum_l();
-        if (g == 0 && i < NQ) head_s[warp][i] = make_float4(m, lt, 0.f, 0.f);
-        if (tb < te && hO < NQ) {                 // every group slot's columns hold the same sums: each writes some
+        for (int f = 0; f < NBF; ++f) zo[f] = __shfl_sync(kFull, zeta[f], 8 * i);
+        float* sums = reinterpret_cast<float*>(ring);
+        if (hO < NQ) {
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt) {
-                if (mt % GB != jO) continue;
-                const int ch = 32 * (mt / 2) + 8 * (g / 2) + 4 * (mt % 2) + g % 2;
-                rsum[hO * D + ch] = o[mt][0] + o[mt][1];
-                rsum[hO * D + ch + 2] = o[mt][2] + o[mt][3];
+                const int gr = 16 * mt / G;
+                if (gr % GB == jO) {
+                    const float z = zo[gr / GB];
+                    sums[hO * D + 16 * mt + g] = o[mt][0] + o[mt][1] + z;
+                    sums[hO * D + 16 * mt + g + 8] = o[mt][2] + o[mt][3] + z;
+                }
             }
         }
+        {
+            const uint32_t st_all = __reduce_or_sync(kFull, status);
+            const float lt = sum_l();
+            if (g == 0 && i < NQ) head_s[warps + warp][i] = make_float4(m, lt, (float)st_all, 0.f);
+        }
+    };
+    auto tile_part = [&]() {
+        // ---- the residual tiles: 16 fp16 rows each, straight from memory.  The
+        // 16-byte loads hand lane i eight consecutive channels, so the MMAs' k
+        // (keys) and m (values) indices run over the channels in another order than
+        // the tiles': k-steps 2j, 2j+1 hold channels 32 j + 8 i + 0..3, + 4..7, and
+        // m-tile 2j+u has row g at channel 32 j + 8 (g / 2) + 4 u + g % 2, row g + 8
+        // two further.  Their partial result is kept apart from the blocks'. ----
+        // (Prefetching the rows into L2 at the start of the call, or a few pairs
+        // ahead, took the bandwidth that the first copies wait for: 7B 12.3 and 11.9
+        // us against 11.6.)
+        for (int tile = tb; tile < te; ++tile) {
+            load_rows(tile);
+            const bool okg = 16 * tile + g < n_res, okg8 = 16 * tile + g + 8 < n_res;
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < DJ; ++j) {
+                uint4 bq = make_uint4(0, 0, 0, 0);
+                if (g < 2 * NQ) bq = *reinterpret_cast<const uint4*>(&qres[g < 2 * NQ ? g : 0][32 * j + 8 * i]);
+                const uint32_t f0[4] = {kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y};
+                const uint32_t f1[4] = {kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w};
+                mma16816(c, f0, bq.x, bq.y);
+                mma16816(c, f1, bq.z, bq.w);
+            }
+            const float sc[4] = {okg ? c[0] + c[1] : -INFINITY, okg8 ? c[2] + c[3] : -INFINITY, -INFINITY, -INFINITY};
+            float p[4];
+            softmax(sc, p, 1.f);
+            float prb[4];
+            gather(p[0], p[1], prb);
+            uint32_t ph01, ph89, pl01, pl89;
+            split_p(prb, ph01, ph89, pl01, pl89);
+            const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
+#pragma unroll
+            for (int j = 0; j < DJ; ++j) {
+                const uint32_t f0[4] = {movmatrix_trans(vx[0][j].x), movmatrix_trans(vx[0][j].y),
+                                        movmatrix_trans(vx[1][j].x), movmatrix_trans(vx[1][j].y)};
+                mma16816(o[2 * j], f0, pb0, pb1);
+                const uint32_t f1[4] = {movmatrix_trans(vx[0][j].z), movmatrix_trans(vx[0][j].w),
+                                        movmatrix_trans(vx[1][j].z), movmatrix_trans(vx[1][j].w)};
+                mma16816(o[2 * j + 1], f1, pb0, pb1);
+            }
+        }
+        {
+            float* rsum = reinterpret_cast<float*>(ring + S::SUMS);
+            const float lt = sum_l();
+            if (g == 0 && i < NQ) head_s[warp][i] = make_float4(m, lt, 0.f, 0.f);
+            if (hO < NQ) {                            // every group slot's columns hold the same sums: each writes some
+#pragma unroll
+                for (int mt = 0; mt < KS; ++mt) {
+                    if (mt % GB != jO) continue;
+                    const int ch = 32 * (mt / 2) + 8 * (g / 2) + 4 * (mt % 2) + g % 2;
+                    rsum[hO * D + ch] = o[mt][0] + o[mt][1];
+                    rsum[hO * D + ch + 2] = o[mt][2] + o[mt][3];
+                }
+            }
+        }
+    };
+    if constexpr (kAlternate<D, NQ>) {
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            clear();
+            if (part == (warp & 1)) block_part();
+            else tile_part();
+        }
+    } else {
+        clear();
+        block_part();
+        clear();
+        tile_part();
     }
 
     // ---- the log-sum-exp merge: the CTA's partials, then the cluster's CTAs ----
-    // every thread weighs the partials of its outputs' heads for itself: reads
-    // of one address by many threads, and one barrier instead of two
+    // Every warp weighs the partials of its outputs' head for itself, one a
+    // lane, and hands the weights round by shuffles.
     const int span = NQ * D / (int)csize;         // the outputs a CTA of the cluster writes
     __half* out = a.out + ((long long)b * a.Hq + hk * NQ) * D;
     if (csize > 1) cluster_wait();                // (every CTA has started: its shared memory may be written)
     __syncthreads();
-    for (int idx = tid; idx < NQ * D; idx += blockDim.x) {
-        const int h = idx / D;
-        float M = -INFINITY, L = 0.f, s = 0.f, bad = 0.f;
-#pragma unroll 4
-        for (int j = 0; j < 2 * warps; ++j) M = fmaxf(M, head_s[j][h].x);
+    for (int base = 32 * warp; base < NQ * D; base += blockDim.x) {
+        const int idx = base + lane, h = base / D;
+        const float4 x = lane < 2 * warps ? head_s[lane][h] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        float M = x.x;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, s));
+        const float e = x.x == -INFINITY ? 0.f : fast_exp2(x.x - M);   // (a partial without tokens: weight 0)
+        float L = x.y * e, sum = 0.f;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(kFull, L, s);
+        const bool bad = __any_sync(kFull, x.z != 0.f);
 #pragma unroll 4
         for (int j = 0; j < warps; ++j) {
-            const float4 xr = head_s[j][h], xb = head_s[warps + j][h];
             const float* mine = reinterpret_cast<const float*>(dyn_smem + j * S::WARP) + idx;
-            const float vr = mine[S::SUMS / 4], vb = mine[0];
-            // a partial without tokens has weight 0 (and, of the residual, no sums)
-            const float er = xr.x == -INFINITY ? 0.f : fast_exp2(xr.x - M);
-            const float eb = xb.x == -INFINITY ? 0.f : fast_exp2(xb.x - M);
-            L = fmaf(xr.y, er, fmaf(xb.y, eb, L));
-            s = er == 0.f ? s : fmaf(vr, er, s);
-            s = eb == 0.f ? s : fmaf(vb, eb, s);
-            bad += xb.z;
+            sum = fmaf(mine[S::SUMS / 4], __shfl_sync(kFull, e, j), fmaf(mine[0], __shfl_sync(kFull, e, warps + j), sum));
         }
         if (csize > 1) {
-            stc32(cluster_map(smem_u32(&recv_s[(int)crank * span + idx % span]), idx / span), s);
+            stc32(cluster_map(smem_u32(&recv_s[(int)crank * span + idx % span]), idx / span), sum);
             if (idx % D < (int)csize)             // (csize <= 8 < D) the head's (M, L, status) to each CTA
-                stc128(cluster_map(smem_u32(&recv_head[crank][h]), idx % D), make_float4(M, L, bad, 0.f));
+                stc128(cluster_map(smem_u32(&recv_head[crank][h]), idx % D), make_float4(M, L, bad ? 1.f : 0.f, 0.f));
         } else {
-            out[idx] = __float2half_rn(bad != 0.f ? NAN : s / L);
+            out[idx] = __float2half_rn(bad ? NAN : sum / L);
         }
     }
     if (csize == 1) return;

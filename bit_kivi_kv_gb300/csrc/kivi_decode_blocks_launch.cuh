@@ -33,15 +33,20 @@ struct InstanceSetup {
 
 // A row's CTAs (a power of two, at most 8: a cluster) and their warps: the shape
 // with the most warps per row among those whose whole grid is resident at
-// once, a larger cluster only for at least half as many warps again.  Where
-// none gives a row two warps, CTAs of four warps in several waves.
+// once.  A cluster costs about 1 us of merging, so it has to bring half as many
+// warps again (256 rows of 32 blocks: 1 x 8 warps 11.6 us, 2 x 4 12.9); once
+// there is one, more and smaller CTAs spread over more SMs (64 rows of 128
+// blocks: 2 x 16 warps 12.5 us, 4 x 8 11.7, 8 x 4 11.7).  Where no shape gives a
+// row two warps, CTAs of four warps in several waves.
 struct Shape { int ctas, warps; };
 inline Shape row_shape(long long rows, long long units, int num_sms, const SmRoom& room) {
     Shape best{1, 0};
     for (int c = 1; c <= blocks_detail::kMaxCluster; c *= 2) {
         long long w = room.warps((rows * c + num_sms - 1) / num_sms);
         if (w * c > units) w = (units + c - 1) / c;
-        if (w >= 1 && (best.warps == 0 || 2 * w * c >= 3LL * best.ctas * best.warps)) best = Shape{c, (int)w};
+        const long long n = w * c, most = (long long)best.ctas * best.warps;
+        if (w >= 1 && (most == 0 || (best.ctas == 1 ? 2 * n >= 3 * most : n >= most && w >= 4)))
+            best = Shape{c, (int)w};
     }
     if (best.ctas * best.warps < 2 && units >= 2)
         best = Shape{1, (int)SmRoom::min2(SmRoom::min2(units, 4), room.warps(1))};

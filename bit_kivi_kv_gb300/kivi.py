@@ -9,6 +9,7 @@ missing (build it with ``python -m bit_kivi_kv_gb300.build``).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 
@@ -368,25 +369,21 @@ def select_blocks(scores, n_keep, keep_first=0, out=None, stream=None):
     evenly strided), as int32 [..., n_keep] in ascending order with -1 behind; the
     first keep_first columns always among them (kivi_select_blocks)."""
     import torch
-    cols, lead = scores.shape[-1], tuple(scores.shape[:-1])
-    if scores.dtype != torch.float32 or not scores.is_cuda:
-        raise KiviError(KIVI_ERR_INVALID_ARG, "scores must be a CUDA float32 tensor")
-    if scores.device.index != torch.cuda.current_device():
-        raise KiviError(KIVI_ERR_INVALID_ARG, f"scores are on {scores.device}, not on the current device")
-    if scores.is_contiguous():
-        ld = cols
-    elif scores.dim() == 2 and scores.stride(1) == 1:
+    shape = scores.shape
+    device = torch.cuda.current_device()
+    if scores.dtype is not torch.float32 or scores.get_device() != device:
+        raise KiviError(KIVI_ERR_INVALID_ARG, "scores must be a float32 tensor on the current CUDA device")
+    cols = ld = shape[-1]
+    if not scores.is_contiguous():
+        if scores.dim() != 2 or scores.stride(1) != 1:
+            raise KiviError(KIVI_ERR_INVALID_ARG, "scores must be contiguous, or a matrix with dense rows")
         ld = scores.stride(0)
-    else:
-        raise KiviError(KIVI_ERR_INVALID_ARG, "scores must be contiguous, or a matrix with dense rows")
-    rows = 1
-    for n in lead:
-        rows *= n
     if out is None:
-        out = torch.empty(lead + (n_keep,), dtype=torch.int32, device=scores.device)
+        out = torch.empty(shape[:-1] + (max(n_keep, 0),), dtype=torch.int32, device=scores.device)
     else:
-        _expect(out, "out", torch.int32, lead + (n_keep,))
-    kivi_select_blocks(scores.data_ptr(), rows, cols, ld, n_keep, keep_first, out.data_ptr(), _raw_stream(stream))
+        _expect(out, "out", torch.int32, shape[:-1] + (n_keep,), device)
+    kivi_select_blocks(scores.data_ptr(), math.prod(shape[:-1]), cols, ld, n_keep, keep_first, out.data_ptr(),
+                       _raw_stream(stream))
     return out
 
 
@@ -426,45 +423,58 @@ class QKNormRope:
                        else 0, eps, table, n_positions, rot_dim, bool(interleaved))
         self._dtypes = {torch.float16: KIVI_F16, torch.bfloat16: KIVI_BF16, torch.float32: KIVI_F32}
         self._positions = {torch.int32: 0, torch.int64: 1}
+        self._layouts = {}      # what _layout found out about shapes, strides and types seen before
 
-    def _args(self, q, k, v, positions, first_position, outs):
-        """The C call's arguments for inputs [batch, tokens, heads, head_dim] (or
-        [batch, heads, head_dim]: one token a row); outs(batch, tokens or None, device) gives
-        the outputs and the addresses of the three."""
-        import torch
-        lead = q.shape[:-2]
+    def _layout(self, key):
+        """Checks the inputs' types, shapes and strides (key); the packed fields that
+        follow from them, the leading sizes, and the shapes of the outputs."""
+        dtypes, shapes, all_strides = key[:3], key[3:6], key[6:]
+        lead = tuple(shapes[0][:-2])
         n = len(lead)
         if n != 1 and n != 2:
             raise KiviError(KIVI_ERR_INVALID_ARG, "q, k and v have 3 or 4 dimensions")
-        code = self._dtypes.get(q.dtype)
+        code = self._dtypes.get(dtypes[0])
         if code is None:
-            raise KiviError(KIVI_ERR_INVALID_ARG, f"no input type {q.dtype}")
+            raise KiviError(KIVI_ERR_INVALID_ARG, f"no input type {dtypes[0]}")
+        strides, D = (), self.head_dim
+        heads = (self.n_q_heads, self.n_kv_heads, self.n_kv_heads)
+        for dtype, shape, s, h, what in zip(dtypes, shapes, all_strides, heads, "qkv"):
+            if dtype is not dtypes[0]:
+                raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be of q's type")
+            if tuple(shape) != lead + (h, D) or s[-1] != 1:
+                raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be [..., {h}, {D}] with dense channels and q's "
+                                                      f"leading sizes, got {tuple(shape)}")
+            strides += (s[0], 0, s[1]) if n == 1 else s[:3]
+        head = (lead[0], self.n_q_heads, self.n_kv_heads, D, 1 if n == 1 else lead[1], code)
+        outs = tuple((lead[0], h) + lead[1:] + (D,) for h in heads)
+        if len(self._layouts) >= 256:
+            self._layouts.clear()
+        found = self._layouts[key] = (head, strides, lead, outs)
+        return found
+
+    def _args(self, q, k, v, positions, first_position, outs):
+        """The C call's arguments for inputs [batch, tokens, heads, head_dim] (or
+        [batch, heads, head_dim]: one token a row); outs(shapes, device) gives the
+        outputs and the addresses of the three."""
+        import torch
         device = torch.cuda.current_device()
+        if q.get_device() != device or k.get_device() != device or v.get_device() != device:
+            raise KiviError(KIVI_ERR_INVALID_ARG, "q, k and v must be on the current device")
         if self._device is not None and self._device != device:
             raise KiviError(KIVI_ERR_INVALID_ARG, f"the weights are on cuda:{self._device}, not on the current device")
-        strides, D = [], self.head_dim
-        for x, heads, what in ((q, self.n_q_heads, "q"), (k, self.n_kv_heads, "k"), (v, self.n_kv_heads, "v")):
-            if x.dtype is not q.dtype or x.get_device() != device:
-                raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be of q's type and on the current device")
-            s = x.stride()
-            if x.shape != lead + (heads, D) or s[-1] != 1:
-                raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be [..., {heads}, {D}] with dense channels and "
-                                                      f"q's leading sizes, got {tuple(x.shape)}")
-            strides += (s[0], 0, s[1]) if n == 1 else s[:3]
-        wide, pos = 0, 0
+        key = (q.dtype, k.dtype, v.dtype, q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride())
+        head, strides, lead, shapes = self._layouts.get(key) or self._layout(key)
+        wide = pos = 0
         if positions is not None:
             wide = self._positions.get(positions.dtype)
             if wide is None:
                 raise KiviError(KIVI_ERR_INVALID_ARG, "positions must be int32 or int64")
             _expect(positions, "positions", positions.dtype, lead, device)
             pos = positions.data_ptr()
-        tokens = 1 if n == 1 else lead[1]
-        out, ptrs = outs(lead[0], None if n == 1 else tokens, device)
-        qw, kw, eps, table, n_positions, rot_dim, interleaved = self._fixed
+        out, ptrs = outs(shapes, device)
         # (the fields of kivi_qkv in order, packed at once: a few times faster than one by one)
-        a = kivi_qkv.from_buffer_copy(_QKV.pack(
-            lead[0], self.n_q_heads, self.n_kv_heads, D, tokens, code, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            *strides, qw, kw, eps, table, n_positions, rot_dim, interleaved, pos, wide, first_position, *ptrs))
+        a = kivi_qkv.from_buffer_copy(_QKV.pack(*head, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
+                                                *self._fixed, pos, wide, first_position, *ptrs))
         return a, out
 
     def __call__(self, q, k, v, positions=None, first_position=0, out=None, stream=None):
@@ -475,16 +485,15 @@ class QKNormRope:
         inputs have none."""
         import torch
 
-        def outs(B, L, device):
-            shapes = [(B, h, self.head_dim) if L is None else (B, h, L, self.head_dim)
-                      for h in (self.n_q_heads, self.n_kv_heads, self.n_kv_heads)]
+        def outs(shapes, device):
             if out is None:
                 o = tuple(torch.empty(s, dtype=torch.float16, device=q.device) for s in shapes)
             else:
                 o = out
-                for t, s, what in zip(o, shapes, ("out[0]", "out[1]", "out[2]")):
-                    _expect(t, what, torch.float16, s, device)
-            return o, [t.data_ptr() for t in o]
+                for t, s in zip(o, shapes):
+                    _expect(t, "out", torch.float16, s, device)
+            a, b, c = o
+            return o, (a.data_ptr(), b.data_ptr(), c.data_ptr())
 
         a, out = self._args(q, k, v, positions, first_position, outs)
         kivi_qk_norm_rope(a, _raw_stream(stream))
@@ -571,13 +580,12 @@ class KiviCache:
         q [B, Hq, D], k, v [B, Hkv, D]; returns the query, fp16 [B, Hq, D]."""
         import torch
 
-        def outs(B, L, device):
-            shape = (B, norm_rope.n_q_heads, norm_rope.head_dim)
+        def outs(shapes, device):
             o = q_out
             if o is None:
-                o = torch.empty(shape, dtype=torch.float16, device=q.device)
+                o = torch.empty(shapes[0], dtype=torch.float16, device=q.device)
             else:
-                _expect(o, "q_out", torch.float16, shape, device)
+                _expect(o, "q_out", torch.float16, shapes[0], device)
             return o, (o.data_ptr(), 0, 0)
 
         a, q_out = norm_rope._args(q, k, v, positions, first_position, outs)
