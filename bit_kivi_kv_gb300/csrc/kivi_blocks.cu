@@ -90,13 +90,39 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
     if constexpr (PAGED) nblk = a.seqs[b].n_blocks;
     griddepcontrol_wait();
     griddepcontrol_launch_dependents();
+    float* out = a.scores + row * a.ld;
+    const long long n0 = ((long long)blockIdx.x * kScoreWarps + warp) * a.iters * BPI;
+    // a group's loads; a page outside the pool is read as page 0 and marked
+    uint4 x[kScoreLoads];
+    uint32_t bad = 0u;
+    auto load_group = [&](long long first) {
+        bad = 0u;
+#pragma unroll
+        for (int u = 0; u < kScoreLoads; ++u) {
+            const long long n = first + u * BPL + sub;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (n < nblk) {
+                const uint8_t* kp;
+                if constexpr (PAGED) {
+                    const int pg = __ldg(a.table + (long long)a.seqs[b].seq * a.max_blocks + n);
+                    const bool out_of_pool = (unsigned)pg >= (unsigned)a.n_pages;
+                    if (out_of_pool) bad |= 1u << u;
+                    kp = a.cache + ((long long)(out_of_pool ? 0 : pg) * a.Hkv + hk) * 2 * a.part_bytes;
+                } else {
+                    kp = a.cache + row * a.slot_bytes + n * a.part_bytes;
+                }
+                x[u] = mma_detail::ldg_stream(kp + a.entries_off + 16 * lb);
+            }
+        }
+    };
+    if (n0 < a.ld) load_group(n0);           // on its way before the query
     // the lane's coefficients: channels 8 (lb % (D/8)) .. of steps (first half of the lanes) or zeros
     const bool steps = lb < LPB / 2;
     float coef[NQ][8];
 #pragma unroll
     for (int h = 0; h < NQ; ++h) {
-        const uint4 x = *reinterpret_cast<const uint4*>(a.q + ((long long)b * a.Hq + hk * NQ + h) * D + 8 * (lb % (D / 8)));
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const uint4 qx = *reinterpret_cast<const uint4*>(a.q + ((long long)b * a.Hq + hk * NQ + h) * D + 8 * (lb % (D / 8)));
+        const uint32_t w[4] = {qx.x, qx.y, qx.z, qx.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 f = mma_detail::unpack_f16x2(w[j]);
@@ -104,30 +130,10 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
             coef[h][2 * j + 1] = steps ? fmaxf(f.y, 0.f) * a.levels * a.scale : f.y * a.scale;
         }
     }
-    float* out = a.scores + row * a.ld;
-    const long long n0 = ((long long)blockIdx.x * kScoreWarps + warp) * a.iters * BPI;
     for (int it = 0; it < a.iters; ++it) {
         const long long first = n0 + (long long)it * BPI;
         if (first >= a.ld) break;
-        uint4 x[kScoreLoads];
-        bool bad[kScoreLoads];
-#pragma unroll
-        for (int u = 0; u < kScoreLoads; ++u) {
-            const long long n = first + u * BPL + sub;
-            x[u] = make_uint4(0, 0, 0, 0);
-            bad[u] = false;
-            if (n < nblk) {
-                const uint8_t* kp;
-                if constexpr (PAGED) {
-                    const int pg = __ldg(a.table + (long long)a.seqs[b].seq * a.max_blocks + n);
-                    bad[u] = (unsigned)pg >= (unsigned)a.n_pages;
-                    kp = a.cache + ((long long)(bad[u] ? 0 : pg) * a.Hkv + hk) * 2 * a.part_bytes;
-                } else {
-                    kp = a.cache + row * a.slot_bytes + n * a.part_bytes;
-                }
-                x[u] = mma_detail::ldg_stream(kp + a.entries_off + 16 * lb);
-            }
-        }
+        if (it) load_group(first);
         float best = -INFINITY;
 #pragma unroll
         for (int h = 0; h < NQ; ++h) {
@@ -141,7 +147,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
                     const float2 f = mma_detail::unpack_f16x2(w[j]);
                     t = fmaf(coef[h][2 * j], f.x, fmaf(coef[h][2 * j + 1], f.y, t));
                 }
-                s[u] = PAGED && bad[u] ? NAN : t;
+                s[u] = PAGED && (bad >> u & 1u) ? NAN : t;
             }
             // sums over the block's LPB lanes; lane bits LPB/2, LPB/4, LPB/8 pick the load
 #pragma unroll
@@ -166,11 +172,12 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
 template <int D, int NQ, bool PAGED>
 cudaError_t launch_scores_t(typename ScoreArgsOf<PAGED>::type& a, long long rows, int num_sms, cudaStream_t st) {
     constexpr int BPI = kScoreLoads * 128 / D;
-    // a warp's coefficients cost about one group of blocks: more groups a warp
-    // only when the grid still gives every SM several CTAs
+    // a warp's coefficients cost about one group of blocks: two groups a warp
+    // where the grid still gives every SM eight CTAs (131k tokens: 2 groups 21.5
+    // us, 4 groups 22.2)
     const long long groups = (a.ld + (long long)kScoreWarps * BPI - 1) / (kScoreWarps * BPI);
     long long iters = groups * rows / (8LL * (num_sms > 0 ? num_sms : 1));
-    iters = iters < 1 ? 1 : iters > 4 ? 4 : iters;
+    iters = iters < 1 ? 1 : iters > 2 ? 2 : iters;
     a.iters = (int)iters;
     const long long ctas = (groups + iters - 1) / iters;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;

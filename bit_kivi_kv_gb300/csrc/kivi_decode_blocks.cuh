@@ -26,7 +26,7 @@ namespace blocks_detail {
 
 using namespace mma_detail;
 
-constexpr int kListCache = 64;      // list entries a warp keeps as byte offsets
+constexpr int kListCache = 32;      // list entries a warp keeps as byte offsets, one a lane
 constexpr int kMaxCluster = 8;      // CTAs that share a row, at most (the portable cluster size)
 constexpr int kMaxRowWarps = 16;    // warps of a CTA, at most: two partials each, one a lane in the merge
 
@@ -143,15 +143,18 @@ constexpr bool kAlternate = D == 128 && NQ == 4;
 
 // Dynamic shared memory of a CTA: per warp its copy ring (which later takes the
 // listed blocks' value sums [NQ][D] fp32), the key fragment table, the list's
-// offsets and the residual tiles' value sums [NQ][D] fp32.
+// offsets and the residual tiles' value sums [NQ][D] fp32 (in the table's place
+// where the tiles come last).
 template <int D, int BITS, int NQ, int G>
 struct Smem {
     using C = Cfg<D, BITS, NQ, G>;
     static constexpr int RING = C::STAGES * C::STAGE_BYTES;
     static constexpr int ROWS = NQ > 1 ? 32 : 8 * NQ + 1;      // rows of the key fragment table
-    static constexpr int FRAG = RING, OFFS = FRAG + ROWS * C::QSTRIDE * 4, SUMS = OFFS + kListCache * 8;
-    static constexpr int WARP = (SUMS + NQ * D * 4 + 127) / 128 * 128;
+    static constexpr int FRAG = RING, OFFS = FRAG + ROWS * C::QSTRIDE * 4, END = OFFS + kListCache * 8;
+    static constexpr int SUMS = kAlternate<D, NQ> ? END : FRAG;
+    static constexpr int WARP = (END + (kAlternate<D, NQ> ? NQ * D * 4 : 0) + 127) / 128 * 128;
     static_assert(NQ * D * 4 <= RING, "the value sums reuse the copy ring");
+    static_assert(kAlternate<D, NQ> || NQ * D * 4 <= ROWS * C::QSTRIDE * 4, "the tiles' sums reuse the table");
 };
 
 template <int D, int BITS, int NQ, int G, bool PAGED>
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     };
     const int* list = a.list + row * a.n_list;
     uint32_t status = 0;       // 1: a bulk copy did not complete in time; 2: an entry outside the cache
-    // entries j0 + lane, j0 + 32 + lane of the n entries from j0 on (as `none` past them)
+    // list entry j, none past the n-th
     auto list_entry = [&](int j, int n) {
         int e = -1;                               // (volatile: not moved behind the loads that follow it)
         if (j < n) asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(e) : "l"(list + j));
@@ -320,20 +323,18 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
             tma_1d_u32(dst + C::VE, vp + tiles_bytes + t * C::ENT, 2 * C::ENT, bar);
         }
     };
-    // the part of the list from pair k on: its entries (two a lane), ...
-    static_assert(kListCache == 64, "two entries a lane");
-    int e0 = -1, e1 = -1;
+    // the part of the list from pair k on: its entries, ...
+    static_assert(kListCache == 32, "one entry a lane");
+    int entry = -1;
     auto read_part = [&]() {
         j0 = k / PPB;
         const int end = min((we - 1) / PPB + 1, j0 + kListCache);
         kend = min(we, end * PPB);
-        e0 = list_entry(j0 + lane, end);
-        e1 = list_entry(j0 + 32 + lane, end);
+        entry = list_entry(j0 + lane, end);
     };
     // ... then their offsets, and the part's first copies
     auto begin_part = [&]() {
-        offs[lane] = offset_of(e0);
-        offs[32 + lane] = offset_of(e1);
+        offs[lane] = offset_of(entry);
         __syncwarp();
         if (lane == 0) {
             fence_proxy_async();
@@ -453,6 +454,29 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         lt += __shfl_xor_sync(kFull, lt, 16);
         return lt;
     };
+    // a value tile of the stage at stage_u32: the probabilities of its tokens g
+    // and g + 8, its words
+    auto value_tile = [&](uint32_t stage_u32, int t, float p0, float p1, const uint32_t (&wv)[W]) {
+        float prb[4];
+        gather(p0, p1, prb);
+        uint32_t ph01, ph89, pl01, pl89;
+        split_p(prb, ph01, ph89, pl01, pl89);
+        const uint32_t ve = stage_u32 + C::VE + t * C::ENT + eoff;
+        uint32_t pb[NBF][2];
+#pragma unroll
+        for (int f = 0; f < NBF; ++f) {            // B fragments of p * step, and p . zero
+            const uint2 sv = lds64(ve + 32u * GB * f), zv = lds64(ve + 32u * (NGRP + GB * f));
+            const uint32_t h01 = hmul2(ph01, sv.x), h89 = hmul2(ph89, sv.y);
+            const uint32_t l01 = hfma2(pl01, sv.x, hfma2(ph01, sv.x, neg_f16x2(h01)));
+            const uint32_t l89 = hfma2(pl89, sv.y, hfma2(ph89, sv.y, neg_f16x2(h89)));
+            pb[f][0] = lo_col ? l01 : h01;
+            pb[f][1] = lo_col ? l89 : h89;
+            const float2 z01 = unpack_f16x2(zv.x), z89 = unpack_f16x2(zv.y);
+            zeta[f] = fmaf(prb[0], z01.x, fmaf(prb[1], z01.y, fmaf(prb[2], z89.x, fmaf(prb[3], z89.y, zeta[f]))));
+        }
+        auto pbk = [&](int mt) { return make_uint2(pb[(16 * mt / G) / GB][0], pb[(16 * mt / G) / GB][1]); };
+        value_mma<BITS, W, KS>(wv, pbk, o);
+    };
     // A warp's two parts, each with a partial result of its own.
     auto clear = [&]() {
         m = -INFINITY;
@@ -469,7 +493,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
                 begin_part();
             }
             bool failed = false;
-            bool skip = offs[k / PPB - j0] < 0;
+            bool skip = false;
             for (; k < kend; ++k, ++item) {
                 const uint32_t st = item % C::STAGES;
                 if (!__all_sync(kFull, mbar_wait(&bars[st], (item / C::STAGES) & 1u))) { failed = true; break; }
@@ -503,23 +527,6 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
                     softmax(sc, p, 0x1p24f);                       // scores are in units of 2^-24
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        float prb[4];
-                        gather(p[2 * t], p[2 * t + 1], prb);
-                        uint32_t ph01, ph89, pl01, pl89;
-                        split_p(prb, ph01, ph89, pl01, pl89);
-                        const uint32_t ve = stage_u32 + C::VE + t * C::ENT + eoff;
-                        uint32_t pb[NBF][2];
-#pragma unroll
-                        for (int f = 0; f < NBF; ++f) {            // B fragments of p * step, and p . zero
-                            const uint2 sv = lds64(ve + 32u * GB * f), zv = lds64(ve + 32u * (NGRP + GB * f));
-                            const uint32_t h01 = hmul2(ph01, sv.x), h89 = hmul2(ph89, sv.y);
-                            const uint32_t l01 = hfma2(pl01, sv.x, hfma2(ph01, sv.x, neg_f16x2(h01)));
-                            const uint32_t l89 = hfma2(pl89, sv.y, hfma2(ph89, sv.y, neg_f16x2(h89)));
-                            pb[f][0] = lo_col ? l01 : h01;
-                            pb[f][1] = lo_col ? l89 : h89;
-                            const float2 z01 = unpack_f16x2(zv.x), z89 = unpack_f16x2(zv.y);
-                            zeta[f] = fmaf(prb[0], z01.x, fmaf(prb[1], z01.y, fmaf(prb[2], z89.x, fmaf(prb[3], z89.y, zeta[f]))));
-                        }
                         uint32_t wv[W];
                         if constexpr (HOIST) {
 #pragma unroll
@@ -527,8 +534,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
                         } else {
                             lds_words(stage_u32 + C::VT + t * C::TILE, wv);
                         }
-                        auto pbk = [&](int mt) { return make_uint2(pb[(16 * mt / G) / GB][0], pb[(16 * mt / G) / GB][1]); };
-                        value_mma<BITS, W, KS>(wv, pbk, o);
+                        value_tile(stage_u32, t, p[2 * t], p[2 * t + 1], wv);
                     }
                 }
                 __syncwarp();                                      // every lane is done with this stage
