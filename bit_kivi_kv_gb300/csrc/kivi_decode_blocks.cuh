@@ -134,27 +134,19 @@ __device__ __forceinline__ void value_mma(const uint32_t (&w)[W], const B& bfrag
     }
 }
 
-// Whether odd warps take their residual tiles before their blocks, which spreads
-// the tiles' plain loads over the call.  It costs registers: with four heads of
-// 128 channels, which have 168, 44.7 -> 43.9 us (512 rows); with one head, which
-// has 128, 11.6 -> 12.4 us (256 rows).
-template <int D, int NQ>
-constexpr bool kAlternate = D == 128 && NQ == 4;
-
 // Dynamic shared memory of a CTA: per warp its copy ring (which later takes the
 // listed blocks' value sums [NQ][D] fp32), the key fragment table, the list's
-// offsets and the residual tiles' value sums [NQ][D] fp32 (in the table's place
-// where the tiles come last).
+// offsets; the residual tiles' value sums [NQ][D] fp32 take the table's place.
 template <int D, int BITS, int NQ, int G>
 struct Smem {
     using C = Cfg<D, BITS, NQ, G>;
     static constexpr int RING = C::STAGES * C::STAGE_BYTES;
     static constexpr int ROWS = NQ > 1 ? 32 : 8 * NQ + 1;      // rows of the key fragment table
     static constexpr int FRAG = RING, OFFS = FRAG + ROWS * C::QSTRIDE * 4, END = OFFS + kListCache * 8;
-    static constexpr int SUMS = kAlternate<D, NQ> ? END : FRAG;
-    static constexpr int WARP = (END + (kAlternate<D, NQ> ? NQ * D * 4 : 0) + 127) / 128 * 128;
+    static constexpr int SUMS = FRAG;
+    static constexpr int WARP = (END + 127) / 128 * 128;
     static_assert(NQ * D * 4 <= RING, "the value sums reuse the copy ring");
-    static_assert(kAlternate<D, NQ> || NQ * D * 4 <= ROWS * C::QSTRIDE * 4, "the tiles' sums reuse the table");
+    static_assert(NQ * D * 4 <= ROWS * C::QSTRIDE * 4, "the tiles' sums reuse the table");
 };
 
 template <int D, int BITS, int NQ, int G, bool PAGED>
@@ -379,6 +371,8 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     float o[KS][4];
     float zeta[NBF];
 #pragma unroll
+    for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+#pragma unroll
     for (int f = 0; f < NBF; ++f) zeta[f] = 0.f;
     constexpr bool QB_REGS = NQ > 1;
     uint32_t qb[2 * KS] = {};
@@ -477,181 +471,163 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         auto pbk = [&](int mt) { return make_uint2(pb[(16 * mt / G) / GB][0], pb[(16 * mt / G) / GB][1]); };
         value_mma<BITS, W, KS>(wv, pbk, o);
     };
-    // A warp's two parts, each with a partial result of its own.
-    auto clear = [&]() {
-        m = -INFINITY;
-        l = 0.f;
-        fresh = true;
-#pragma unroll
-        for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-    };
-    auto block_part = [&]() {
-        // ---- the listed blocks ----
-        while (k < we) {
-            if (k >= kend) {
-                read_part();
-                begin_part();
-            }
-            bool failed = false;
-            bool skip = false;
-            for (; k < kend; ++k, ++item) {
-                const uint32_t st = item % C::STAGES;
-                if (!__all_sync(kFull, mbar_wait(&bars[st], (item / C::STAGES) & 1u))) { failed = true; break; }
-                const uint8_t* stage = ring + st * C::STAGE_BYTES;
-                const uint32_t stage_u32 = ring_u32 + st * C::STAGE_BYTES;
-                const bool first_of_block = k % PPB == 0 || k == wb;
-                if (first_of_block) skip = offs[k / PPB - j0] < 0;
-                if (!skip) {
-                    if (first_of_block)
-                        build_q_frags<C, D, NQ, QB_REGS>(stage + C::KE, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);
-                    float ca[4] = {0.f, 0.f, 0.f, 0.f}, cb[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t wa[W], wc[W];
-                    lds_words(stage_u32 + C::KT, wa);
-                    if constexpr (BITS == 8) {                     // one tile at a time: the words of two do not fit
-                        key_mma<BITS, W, KS>(wa, qbk, ca);
-                        lds_words(stage_u32 + C::KT + C::TILE, wc);
-                        key_mma<BITS, W, KS>(wc, qbk, cb);
-                    } else {                                       // two chains of sums side by side
-                        lds_words(stage_u32 + C::KT + C::TILE, wc);
-                        key_mma2<BITS, W, KS>(wa, wc, qbk, ca, cb);
-                    }
-                    const float sc[4] = {ca[0] + (ca[1] + beta), ca[2] + (ca[3] + beta), cb[0] + (cb[1] + beta),
-                                         cb[2] + (cb[3] + beta)};
-                    constexpr bool HOIST = BITS != 8 && W <= 4;   // as in the dense kernel
-                    uint32_t wvh[2][W];
-                    if constexpr (HOIST) {
-                        lds_words(stage_u32 + C::VT, wvh[0]);
-                        lds_words(stage_u32 + C::VT + C::TILE, wvh[1]);
-                    }
-                    float p[4];
-                    softmax(sc, p, 0x1p24f);                       // scores are in units of 2^-24
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        uint32_t wv[W];
-                        if constexpr (HOIST) {
-#pragma unroll
-                            for (int x = 0; x < W; ++x) wv[x] = wvh[t][x];
-                        } else {
-                            lds_words(stage_u32 + C::VT + t * C::TILE, wv);
-                        }
-                        value_tile(stage_u32, t, p[2 * t], p[2 * t + 1], wv);
-                    }
-                }
-                __syncwarp();                                      // every lane is done with this stage
-                if (lane == 0 && k + C::STAGES < kend) issue(k + C::STAGES, item + C::STAGES);
-            }
-            if (failed) {
-                // a copy timed out: wait (bounded) for the copies in flight, issue no more
-                status |= 1u;
-                for (int u = 0; u < C::STAGES && k + u < kend; ++u)
-                    mbar_wait(&bars[(item + u) % C::STAGES], ((item + u) / C::STAGES) & 1u);
-                break;
-            }
+    // ---- the listed blocks ----
+    while (k < we) {
+        if (k >= kend) {
+            read_part();
+            begin_part();
         }
-        // the quantized tiles' value sums are in units of 2^(BITS*pos - 24),
-        // pos = (channel / 8) % (8 / BITS): rows g and g+8 of m-tile mt have
-        // classes 2mt and 2mt+1
+        bool failed = false;
+        bool skip = false;
+        for (; k < kend; ++k, ++item) {
+            const uint32_t st = item % C::STAGES;
+            if (!__all_sync(kFull, mbar_wait(&bars[st], (item / C::STAGES) & 1u))) { failed = true; break; }
+            const uint8_t* stage = ring + st * C::STAGE_BYTES;
+            const uint32_t stage_u32 = ring_u32 + st * C::STAGE_BYTES;
+            const bool first_of_block = k % PPB == 0 || k == wb;
+            if (first_of_block) skip = offs[k / PPB - j0] < 0;
+            if (!skip) {
+                if (first_of_block)
+                    build_q_frags<C, D, NQ, QB_REGS>(stage + C::KE, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);
+                float ca[4] = {0.f, 0.f, 0.f, 0.f}, cb[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t wa[W], wc[W];
+                lds_words(stage_u32 + C::KT, wa);
+                if constexpr (BITS == 8) {                     // one tile at a time: the words of two do not fit
+                    key_mma<BITS, W, KS>(wa, qbk, ca);
+                    lds_words(stage_u32 + C::KT + C::TILE, wc);
+                    key_mma<BITS, W, KS>(wc, qbk, cb);
+                } else {                                       // two chains of sums side by side
+                    lds_words(stage_u32 + C::KT + C::TILE, wc);
+                    key_mma2<BITS, W, KS>(wa, wc, qbk, ca, cb);
+                }
+                const float sc[4] = {ca[0] + (ca[1] + beta), ca[2] + (ca[3] + beta), cb[0] + (cb[1] + beta),
+                                     cb[2] + (cb[3] + beta)};
+                constexpr bool HOIST = BITS != 8 && W <= 4;   // as in the dense kernel
+                uint32_t wvh[2][W];
+                if constexpr (HOIST) {
+                    lds_words(stage_u32 + C::VT, wvh[0]);
+                    lds_words(stage_u32 + C::VT + C::TILE, wvh[1]);
+                }
+                float p[4];
+                softmax(sc, p, 0x1p24f);                       // scores are in units of 2^-24
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t wv[W];
+                    if constexpr (HOIST) {
+#pragma unroll
+                        for (int x = 0; x < W; ++x) wv[x] = wvh[t][x];
+                    } else {
+                        lds_words(stage_u32 + C::VT + t * C::TILE, wv);
+                    }
+                    value_tile(stage_u32, t, p[2 * t], p[2 * t + 1], wv);
+                }
+            }
+            __syncwarp();                                      // every lane is done with this stage
+            if (lane == 0 && k + C::STAGES < kend) issue(k + C::STAGES, item + C::STAGES);
+        }
+        if (failed) {
+            // a copy timed out: wait (bounded) for the copies in flight, issue no more
+            status |= 1u;
+            for (int u = 0; u < C::STAGES && k + u < kend; ++u)
+                mbar_wait(&bars[(item + u) % C::STAGES], ((item + u) / C::STAGES) & 1u);
+            break;
+        }
+    }
+    // the quantized tiles' value sums are in units of 2^(BITS*pos - 24),
+    // pos = (channel / 8) % (8 / BITS): rows g and g+8 of m-tile mt have
+    // classes 2mt and 2mt+1
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt) {
+        const float s0 = pow2i(24 - BITS * ((2 * mt) % (8 / BITS)));
+        const float s1 = pow2i(24 - BITS * ((2 * mt + 1) % (8 / BITS)));
+        o[mt][0] *= s0; o[mt][1] *= s0; o[mt][2] *= s1; o[mt][3] *= s1;
+    }
+    // ---- the listed blocks' partial result ----
+#pragma unroll
+    for (int f = 0; f < NBF; ++f) {
+        zeta[f] += __shfl_xor_sync(kFull, zeta[f], 1);
+        zeta[f] += __shfl_xor_sync(kFull, zeta[f], 2);
+    }
+    float zo[NBF];
+#pragma unroll
+    for (int f = 0; f < NBF; ++f) zo[f] = __shfl_sync(kFull, zeta[f], 8 * i);
+    float* sums = reinterpret_cast<float*>(ring);
+    if (hO < NQ) {
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
-            const float s0 = pow2i(24 - BITS * ((2 * mt) % (8 / BITS)));
-            const float s1 = pow2i(24 - BITS * ((2 * mt + 1) % (8 / BITS)));
-            o[mt][0] *= s0; o[mt][1] *= s0; o[mt][2] *= s1; o[mt][3] *= s1;
+            const int gr = 16 * mt / G;
+            if (gr % GB == jO) {
+                const float z = zo[gr / GB];
+                sums[hO * D + 16 * mt + g] = o[mt][0] + o[mt][1] + z;
+                sums[hO * D + 16 * mt + g + 8] = o[mt][2] + o[mt][3] + z;
+            }
         }
-        // ---- the listed blocks' partial result ----
+    }
+    {
+        const uint32_t st_all = __reduce_or_sync(kFull, status);
+        const float lt = sum_l();
+        if (g == 0 && i < NQ) head_s[warps + warp][i] = make_float4(m, lt, (float)st_all, 0.f);
+    }
+
+    // ---- the residual tiles: 16 fp16 rows each, straight from memory.  The
+    // 16-byte loads hand lane i eight consecutive channels, so the MMAs' k
+    // (keys) and m (values) indices run over the channels in another order than
+    // the tiles': k-steps 2j, 2j+1 hold channels 32 j + 8 i + 0..3, + 4..7, and
+    // m-tile 2j+u has row g at channel 32 j + 8 (g / 2) + 4 u + g % 2, row g + 8
+    // two further.  Their partial result is kept apart from the blocks'. ----
+    m = -INFINITY;
+    l = 0.f;
+    fresh = true;
 #pragma unroll
-        for (int f = 0; f < NBF; ++f) {
-            zeta[f] += __shfl_xor_sync(kFull, zeta[f], 1);
-            zeta[f] += __shfl_xor_sync(kFull, zeta[f], 2);
+    for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    // (Prefetching the rows into L2 at the start of the call, or a few pairs
+    // ahead, took the bandwidth that the first copies wait for: 7B 12.3 and 11.9
+    // us against 11.6; spread over the pairs, 512 rows of four heads: 42.9 against
+    // 41.8.  Odd warps taking their tiles first: 44.1.)
+    for (int tile = tb; tile < te; ++tile) {
+        load_rows(tile);
+        const bool okg = 16 * tile + g < n_res, okg8 = 16 * tile + g + 8 < n_res;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < DJ; ++j) {
+            uint4 bq = make_uint4(0, 0, 0, 0);
+            if (g < 2 * NQ) bq = *reinterpret_cast<const uint4*>(&qres[g < 2 * NQ ? g : 0][32 * j + 8 * i]);
+            const uint32_t f0[4] = {kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y};
+            const uint32_t f1[4] = {kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w};
+            mma16816(c, f0, bq.x, bq.y);
+            mma16816(c, f1, bq.z, bq.w);
         }
-        float zo[NBF];
+        const float sc[4] = {okg ? c[0] + c[1] : -INFINITY, okg8 ? c[2] + c[3] : -INFINITY, -INFINITY, -INFINITY};
+        float p[4];
+        softmax(sc, p, 1.f);
+        float prb[4];
+        gather(p[0], p[1], prb);
+        uint32_t ph01, ph89, pl01, pl89;
+        split_p(prb, ph01, ph89, pl01, pl89);
+        const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
 #pragma unroll
-        for (int f = 0; f < NBF; ++f) zo[f] = __shfl_sync(kFull, zeta[f], 8 * i);
-        float* sums = reinterpret_cast<float*>(ring);
-        if (hO < NQ) {
+        for (int j = 0; j < DJ; ++j) {
+            const uint32_t f0[4] = {movmatrix_trans(vx[0][j].x), movmatrix_trans(vx[0][j].y),
+                                    movmatrix_trans(vx[1][j].x), movmatrix_trans(vx[1][j].y)};
+            mma16816(o[2 * j], f0, pb0, pb1);
+            const uint32_t f1[4] = {movmatrix_trans(vx[0][j].z), movmatrix_trans(vx[0][j].w),
+                                    movmatrix_trans(vx[1][j].z), movmatrix_trans(vx[1][j].w)};
+            mma16816(o[2 * j + 1], f1, pb0, pb1);
+        }
+    }
+    {
+        float* rsum = reinterpret_cast<float*>(ring + S::SUMS);
+        const float lt = sum_l();
+        if (g == 0 && i < NQ) head_s[warp][i] = make_float4(m, lt, 0.f, 0.f);
+        if (hO < NQ) {                            // every group slot's columns hold the same sums: each writes some
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt) {
-                const int gr = 16 * mt / G;
-                if (gr % GB == jO) {
-                    const float z = zo[gr / GB];
-                    sums[hO * D + 16 * mt + g] = o[mt][0] + o[mt][1] + z;
-                    sums[hO * D + 16 * mt + g + 8] = o[mt][2] + o[mt][3] + z;
-                }
+                if (mt % GB != jO) continue;
+                const int ch = 32 * (mt / 2) + 8 * (g / 2) + 4 * (mt % 2) + g % 2;
+                rsum[hO * D + ch] = o[mt][0] + o[mt][1];
+                rsum[hO * D + ch + 2] = o[mt][2] + o[mt][3];
             }
         }
-        {
-            const uint32_t st_all = __reduce_or_sync(kFull, status);
-            const float lt = sum_l();
-            if (g == 0 && i < NQ) head_s[warps + warp][i] = make_float4(m, lt, (float)st_all, 0.f);
-        }
-    };
-    auto tile_part = [&]() {
-        // ---- the residual tiles: 16 fp16 rows each, straight from memory.  The
-        // 16-byte loads hand lane i eight consecutive channels, so the MMAs' k
-        // (keys) and m (values) indices run over the channels in another order than
-        // the tiles': k-steps 2j, 2j+1 hold channels 32 j + 8 i + 0..3, + 4..7, and
-        // m-tile 2j+u has row g at channel 32 j + 8 (g / 2) + 4 u + g % 2, row g + 8
-        // two further.  Their partial result is kept apart from the blocks'. ----
-        // (Prefetching the rows into L2 at the start of the call, or a few pairs
-        // ahead, took the bandwidth that the first copies wait for: 7B 12.3 and 11.9
-        // us against 11.6.)
-        for (int tile = tb; tile < te; ++tile) {
-            load_rows(tile);
-            const bool okg = 16 * tile + g < n_res, okg8 = 16 * tile + g + 8 < n_res;
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < DJ; ++j) {
-                uint4 bq = make_uint4(0, 0, 0, 0);
-                if (g < 2 * NQ) bq = *reinterpret_cast<const uint4*>(&qres[g < 2 * NQ ? g : 0][32 * j + 8 * i]);
-                const uint32_t f0[4] = {kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y};
-                const uint32_t f1[4] = {kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w};
-                mma16816(c, f0, bq.x, bq.y);
-                mma16816(c, f1, bq.z, bq.w);
-            }
-            const float sc[4] = {okg ? c[0] + c[1] : -INFINITY, okg8 ? c[2] + c[3] : -INFINITY, -INFINITY, -INFINITY};
-            float p[4];
-            softmax(sc, p, 1.f);
-            float prb[4];
-            gather(p[0], p[1], prb);
-            uint32_t ph01, ph89, pl01, pl89;
-            split_p(prb, ph01, ph89, pl01, pl89);
-            const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
-#pragma unroll
-            for (int j = 0; j < DJ; ++j) {
-                const uint32_t f0[4] = {movmatrix_trans(vx[0][j].x), movmatrix_trans(vx[0][j].y),
-                                        movmatrix_trans(vx[1][j].x), movmatrix_trans(vx[1][j].y)};
-                mma16816(o[2 * j], f0, pb0, pb1);
-                const uint32_t f1[4] = {movmatrix_trans(vx[0][j].z), movmatrix_trans(vx[0][j].w),
-                                        movmatrix_trans(vx[1][j].z), movmatrix_trans(vx[1][j].w)};
-                mma16816(o[2 * j + 1], f1, pb0, pb1);
-            }
-        }
-        {
-            float* rsum = reinterpret_cast<float*>(ring + S::SUMS);
-            const float lt = sum_l();
-            if (g == 0 && i < NQ) head_s[warp][i] = make_float4(m, lt, 0.f, 0.f);
-            if (hO < NQ) {                            // every group slot's columns hold the same sums: each writes some
-#pragma unroll
-                for (int mt = 0; mt < KS; ++mt) {
-                    if (mt % GB != jO) continue;
-                    const int ch = 32 * (mt / 2) + 8 * (g / 2) + 4 * (mt % 2) + g % 2;
-                    rsum[hO * D + ch] = o[mt][0] + o[mt][1];
-                    rsum[hO * D + ch + 2] = o[mt][2] + o[mt][3];
-                }
-            }
-        }
-    };
-    if constexpr (kAlternate<D, NQ>) {
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-            clear();
-            if (part == (warp & 1)) block_part();
-            else tile_part();
-        }
-    } else {
-        clear();
-        block_part();
-        clear();
-        tile_part();
     }
 
     // ---- the log-sum-exp merge: the CTA's partials, then the cluster's CTAs ----
