@@ -12,7 +12,7 @@
 #include <atomic>
 #include <new>
 
-#include "kivi_common.cuh"
+#include "kivi_blocks.cuh"
 
 struct kivi_cache {
     kivi::Geometry geo;

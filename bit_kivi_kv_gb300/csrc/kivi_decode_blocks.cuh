@@ -19,6 +19,7 @@
 // the list at a time.
 #pragma once
 
+#include "kivi_blocks.cuh"
 #include "kivi_decode_mma.cuh"
 
 namespace kivi {

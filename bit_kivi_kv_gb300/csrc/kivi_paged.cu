@@ -14,7 +14,7 @@
 #include <new>
 #include <vector>
 
-#include "kivi_common.cuh"
+#include "kivi_blocks.cuh"
 
 namespace {
 

@@ -21,6 +21,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include "kivi_blocks.cuh"
 #include "kivi_decode_mma.cuh"
 
 namespace kivi {
