@@ -343,10 +343,7 @@ kivi_status decode_launch(kivi_cache_t c, const void* q, void* out, float softma
     plan.max_ctas = c->max_ctas;
     int launches = 0;
     kivi::FusedAppend f2 = fa;
-    if (variant == KIVI_DECODE_TENSOR_CORE && c->fault == KIVI_FAULT_COPY_STALL) {
-        f2.stall_bytes = 16;
-        c->fault = KIVI_FAULT_NONE;   // one call
-    }
+    if (variant == KIVI_DECODE_TENSOR_CORE) f2.stall_bytes = kivi::take_stall(c);
     const cudaError_t e = kivi::launch_decode(g, c->buf, c->n_quant, n_resid, static_cast<const __half*>(q),
                                               static_cast<__half*>(out), scale_log2, static_cast<float*>(workspace),
                                               plan, variant, reinterpret_cast<cudaStream_t>(stream), &launches, f2);
@@ -481,6 +478,12 @@ kivi_status cache_device(kivi_cache* c) { return ensure_device(c); }
 
 CacheView cache_view(const kivi_cache* c) {
     return CacheView{&c->geo, c->buf, c->n_quant, c->n_resid, c->value_queue, c->num_sms};
+}
+
+int take_stall(kivi_cache* c) {
+    const bool stall = c->fault == KIVI_FAULT_COPY_STALL;
+    c->fault = KIVI_FAULT_NONE;   // one call
+    return stall ? 16 : 0;
 }
 
 size_t decode_workspace_need(const kivi_cache* c) {

@@ -495,7 +495,7 @@ cudaError_t launch_decode_blocks(const BlockRows& r, const __half* q, const int*
     // weights: bytes of a quantized pair / 32, and 40 D bytes / 32 for a residual tile
     const blocks_detail::Args base{r.buf, q, out, list, g.NB, g.part_bytes, g.slot_bytes, g.tile_bytes,
                                    g.k_resid_off, g.v_resid_off, g.R, g.Hq, g.Hkv, n_list, r.n_blocks, r.n_resid,
-                                   g.D * g.bits / 4 + 8 * g.D / g.G, 5 * g.D / 4, scale_log2};
+                                   g.D * g.bits / 4 + 8 * g.D / g.G, 5 * g.D / 4, scale_log2, r.stall_bytes};
     auto units = [&](int nblk, int nres) {
         return (long long)(n_list < nblk ? n_list : nblk) * (g.G / 32) + (nres + 15) / 16;
     };
@@ -581,7 +581,7 @@ kivi_status kivi_block_scores(kivi_cache_t c, const void* q, float softmax_scale
     const kivi_status sa = check_scores_args(q, softmax_scale, scores, ld);
     if (sa != KIVI_OK) return sa;
     CacheView v = cache_view(c);
-    BlockRows r{v.g, v.buf, v.g->B, (int)(v.n_quant / v.g->G), (int)v.n_resid, nullptr, 0, nullptr, 0};
+    BlockRows r{v.g, v.buf, v.g->B, (int)(v.n_quant / v.g->G), (int)v.n_resid, nullptr, 0, nullptr, 0, 0};
     if (ld < r.n_blocks)
         return failf(KIVI_ERR_CAPACITY, "scores have %lld columns, the cache holds %d blocks", ld, r.n_blocks);
     if (ld == 0) return report_error(KIVI_OK, "");
@@ -597,7 +597,8 @@ kivi_status kivi_select_blocks(const float* scores, long long rows, long long co
     if (rows < 0 || cols < 0 || n_keep < 0 || keep_first < 0) return failf(KIVI_ERR_INVALID_ARG, "negative size");
     if (ld < cols) return failf(KIVI_ERR_INVALID_ARG, "ld must be at least cols");
     if (keep_first > n_keep) return failf(KIVI_ERR_INVALID_ARG, "keep_first must be at most n_keep");
-    if (rows > 0x7fffffffLL || cols > (1LL << 30)) return failf(KIVI_ERR_UNSUPPORTED, "rows must be < 2^31 and cols <= 2^30");
+    if (rows > 0x7fffffffLL || cols > (1LL << 30) || n_keep > (1 << 30))
+        return failf(KIVI_ERR_UNSUPPORTED, "rows must be < 2^31, cols and n_keep <= 2^30");
     if (rows == 0 || n_keep == 0) return report_error(KIVI_OK, "");
     if (!blocks || (!scores && cols > 0)) return failf(KIVI_ERR_INVALID_ARG, "null scores or blocks");
     if (!aligned(scores, 4) || !aligned(blocks, 4)) return failf(KIVI_ERR_INVALID_ARG, "scores and blocks must be 4-byte aligned");
@@ -617,7 +618,8 @@ kivi_status kivi_decode_blocks(kivi_cache_t c, const void* q, const int* blocks,
     const kivi_status sd = cache_device(c);
     if (sd != KIVI_OK) return sd;
     v = cache_view(c);
-    const BlockRows r{v.g, v.buf, v.g->B, (int)(v.n_quant / v.g->G), (int)v.n_resid, nullptr, 0, nullptr, v.num_sms};
+    const BlockRows r{v.g, v.buf, v.g->B, (int)(v.n_quant / v.g->G), (int)v.n_resid, nullptr, 0, nullptr, v.num_sms,
+                      take_stall(c)};
     return decode_blocks_call(r, q, blocks, n_list, out, softmax_scale, stream);
 }
 

@@ -28,6 +28,7 @@ struct BlockRows {
     long long n_pages;
     const RowSeq* seqs;         // paged: n entries (host memory)
     int num_sms;
+    int stall_bytes;            // failure-detection test hook (dense)
 };
 
 // scores [n * Hkv][ld]: the bound of each block, -inf from a row's last block on.
@@ -94,5 +95,8 @@ struct CacheView {
     int value_queue, num_sms;
 };
 CacheView cache_view(const struct ::kivi_cache* c);
+// The cache's fault for its next decode call (kivi_cache_set_fault), taken: the
+// bytes that a copy stage waits for in vain, or 0.
+int take_stall(struct ::kivi_cache* c);
 
 }  // namespace kivi

@@ -47,6 +47,7 @@ struct Args {
     int n_blocks, n_resid;          // dense: quantized blocks and residual rows of every row
     int wq, wr;                     // weights of a tile pair and of a residual tile
     float scale_log2;
+    int stall_bytes;                // failure-detection test hook, as in the dense decode kernel
 };
 
 struct PagedArgs : Args {
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     if (lane == 0) {
 #pragma unroll
         for (int st = 0; st < C::STAGES; ++st) mbar_init(&bars[st], 1);
+        if (a.stall_bytes && blockIdx.x == 0 && warp == 0) mbar_expect_tx_only(smem_u32(&bars[0]), (uint32_t)a.stall_bytes);
         fence_mbar_init();
     }
     __syncwarp();
@@ -228,14 +230,18 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     const int workers = (int)csize * warps, worker = (int)crank * warps + warp;
     const int tb = (int)((unsigned)worker * (unsigned)T / (unsigned)workers);
     const int te = (int)(((unsigned)worker + 1u) * (unsigned)T / (unsigned)workers);
-    // (Every warp computes the same fp32 values, so the shares fit together
-    // whatever their rounding.)
-    const float per_worker = ((float)T * a.wr + (float)P * a.wq) / workers, per_tile = (float)T / workers;
-    const float inv_wq = 1.0f / a.wq;
+    // (Every warp has to find the same bounds: separately rounded operations
+    // give the same fp32 values wherever the expression is compiled.)
+    const float per_worker = __fdiv_rn(__fadd_rn(__fmul_rn((float)T, (float)a.wr), __fmul_rn((float)P, (float)a.wq)),
+                                       (float)workers);
+    const float per_tile = __fdiv_rn((float)T, (float)workers);
     auto pairs_before = [&](int w) {
         float most = 0.f;
-        for (int v = lane; v <= w; v += 32)
-            most = fmaxf(most, (v * per_worker - floorf(v * per_tile) * a.wr) * inv_wq);
+        for (int v = lane; v <= w; v += 32) {
+            const float tiles = floorf(__fmul_rn((float)v, per_tile));
+            const float left = __fsub_rn(__fmul_rn((float)v, per_worker), __fmul_rn(tiles, (float)a.wr));
+            most = fmaxf(most, __fdiv_rn(left, (float)a.wq));
+        }
         return min(P, __reduce_max_sync(kFull, (int)ceilf(most)));
     };
     const int wb = worker == 0 ? 0 : pairs_before(worker), we = worker + 1 == workers ? P : pairs_before(worker + 1);

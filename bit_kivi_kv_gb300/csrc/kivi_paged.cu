@@ -207,7 +207,7 @@ kivi_status read_rows(kivi_paged* c, const int* seqs, int n, kivi::RowSeq* out, 
         out[i] = kivi::RowSeq{seqs[i], (int)(sq.n_quant / g.G), sq.n_resid};
     }
     *r = kivi::BlockRows{&g, c->buf, n, 0, 0, reinterpret_cast<const int*>(c->buf + c->pg.table_off),
-                         c->pg.n_pages, out, c->num_sms};
+                         c->pg.n_pages, out, c->num_sms, 0};
     return KIVI_OK;
 }
 

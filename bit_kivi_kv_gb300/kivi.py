@@ -364,6 +364,16 @@ def _raw_stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _new(shape, dtype, device, stream):
+    """An output of a call that runs on stream: its memory has to come from that
+    stream's pool, where no earlier work of another stream may still use it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def select_blocks(scores, n_keep, keep_first=0, out=None, stream=None):
     """The n_keep best columns of each row of scores (fp32 [..., cols], rows dense or
     evenly strided), as int32 [..., n_keep] in ascending order with -1 behind; the
@@ -379,7 +389,7 @@ def select_blocks(scores, n_keep, keep_first=0, out=None, stream=None):
             raise KiviError(KIVI_ERR_INVALID_ARG, "scores must be contiguous, or a matrix with dense rows")
         ld = scores.stride(0)
     if out is None:
-        out = torch.empty(shape[:-1] + (max(n_keep, 0),), dtype=torch.int32, device=scores.device)
+        out = _new(shape[:-1] + (max(n_keep, 0),), torch.int32, scores.device, stream)
     else:
         _expect(out, "out", torch.int32, shape[:-1] + (n_keep,), device)
     kivi_select_blocks(scores.data_ptr(), math.prod(shape[:-1]), cols, ld, n_keep, keep_first, out.data_ptr(),
@@ -487,7 +497,7 @@ class QKNormRope:
 
         def outs(shapes, device):
             if out is None:
-                o = tuple(torch.empty(s, dtype=torch.float16, device=q.device) for s in shapes)
+                o = tuple(_new(s, torch.float16, q.device, stream) for s in shapes)
             else:
                 o = out
                 for t, s in zip(o, shapes):
@@ -583,7 +593,7 @@ class KiviCache:
         def outs(shapes, device):
             o = q_out
             if o is None:
-                o = torch.empty(shapes[0], dtype=torch.float16, device=q.device)
+                o = _new(shapes[0], torch.float16, q.device, stream)
             else:
                 _expect(o, "q_out", torch.float16, shapes[0], device)
             return o, (o.data_ptr(), 0, 0)
@@ -599,7 +609,7 @@ class KiviCache:
         c = self.cfg
         _expect(q, "q", torch.float16, (c.batch, c.n_q_heads, c.head_dim))
         if out is None:
-            out = torch.empty(c.batch, c.n_kv_heads, self.counts()[0] // c.group, dtype=torch.float32, device=q.device)
+            out = _new((c.batch, c.n_kv_heads, self.counts()[0] // c.group), torch.float32, q.device, stream)
         else:
             _expect(out, "out", torch.float32, (c.batch, c.n_kv_heads, out.shape[-1]))
         kivi_block_scores(self.handle, q.data_ptr(), softmax_scale, out.data_ptr(), out.shape[-1], _raw_stream(stream))
@@ -613,7 +623,7 @@ class KiviCache:
         _expect(q, "q", torch.float16, (c.batch, c.n_q_heads, c.head_dim))
         _expect(blocks, "blocks", torch.int32, (c.batch, c.n_kv_heads, blocks.shape[-1]))
         if out is None:
-            out = torch.empty_like(q)
+            out = _new(q.shape, torch.float16, q.device, stream)
         else:
             _expect(out, "out", torch.float16, q.shape)
         kivi_decode_blocks(self.handle, q.data_ptr(), blocks.data_ptr(), blocks.shape[-1], out.data_ptr(),
@@ -707,7 +717,7 @@ class KiviPagedCache:
         _expect(q, "q", torch.float16, (len(seqs), c.n_q_heads, c.head_dim))
         if out is None:
             cols = max((self.counts(s)[0] // c.group for s in seqs), default=0)
-            out = torch.empty(len(seqs), c.n_kv_heads, cols, dtype=torch.float32, device=q.device)
+            out = _new((len(seqs), c.n_kv_heads, cols), torch.float32, q.device, stream)
         else:
             _expect(out, "out", torch.float32, (len(seqs), c.n_kv_heads, out.shape[-1]))
         kivi_paged_block_scores(self.handle, seqs, q.data_ptr(), softmax_scale, out.data_ptr(), out.shape[-1],
@@ -721,7 +731,7 @@ class KiviPagedCache:
         _expect(q, "q", torch.float16, (len(seqs), c.n_q_heads, c.head_dim))
         _expect(blocks, "blocks", torch.int32, (len(seqs), c.n_kv_heads, blocks.shape[-1]))
         if out is None:
-            out = torch.empty_like(q)
+            out = _new(q.shape, torch.float16, q.device, stream)
         else:
             _expect(out, "out", torch.float16, q.shape)
         kivi_paged_decode_blocks(self.handle, seqs, q.data_ptr(), blocks.data_ptr(), blocks.shape[-1], out.data_ptr(),

@@ -483,7 +483,8 @@ kivi_status kivi_block_scores(kivi_cache_t cache, const void* q, float softmax_s
  * their scores (the first blocks, where attention sinks sit).  -inf and NaN
  * are never chosen, not in those columns either; every other value is.
  * blocks: int32 [rows][n_keep], each row its chosen columns in ascending
- * order, then -1 for the places that no column fills.  cols may be 0.  Runs on
+ * order, then -1 for the places that no column fills.  cols may be 0 (at most 2^30, as
+ * n_keep).  Runs on
  * the current device; scores and blocks need only their natural alignment.
  */
 kivi_status kivi_select_blocks(const float* scores, long long rows, long long cols, long long ld, int n_keep,
@@ -498,7 +499,9 @@ kivi_status kivi_select_blocks(const float* scores, long long rows, long long co
  * summation, and a block listed twice counts twice.  An entry of Lq / G or
  * more (or, paged, whose page lies outside the pool) is not read from; it makes
  * the outputs of the row's heads NaN, as a copy that times out does.
- * n_list may be 0 (the residual alone).  One launch, no workspace.
+ * n_list may be 0 (the residual alone).  One launch, no workspace; tensor cores
+ * whatever kivi_cache_set_decode_kernel selects, and the grid follows the
+ * rows, not kivi_cache_set_max_ctas.
  * KIVI_ERR_STATE on an empty cache; KIVI_ERR_UNSUPPORTED with the value queue.
  */
 kivi_status kivi_decode_blocks(kivi_cache_t cache, const void* q, const int* blocks, int n_list, void* out,
@@ -595,8 +598,10 @@ kivi_status kivi_append_qkv(kivi_cache_t cache, const kivi_qkv* args, kivi_strea
  * finishes and returns; the context stays usable).  The paged kernel also
  * marks a block-table entry outside the pool the same way.
  *
+ * kivi_decode_blocks' waits and marks are the same.
+ *
  * Test hook: KIVI_FAULT_COPY_STALL makes the next tensor-core decode call on
- * this cache (kivi_decode_attn or kivi_append_decode) expect 16 bytes more on
+ * this cache (kivi_decode_attn, kivi_append_decode or kivi_decode_blocks) expect 16 bytes more on
  * the first copy stage of CTA 0, warp 0 than its copies bring, so that wait
  * runs out: that call takes about 4 s more and returns NaN for the heads of the
  * slots that warp covers, correct outputs elsewhere.  One call only; host-only.

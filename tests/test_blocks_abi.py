@@ -65,6 +65,7 @@ def test_select(K):
         refuses(K, K.KIVI_ERR_INVALID_ARG, f, *args)
     refuses(K, K.KIVI_ERR_UNSUPPORTED, f, FAKE, 1 << 31, 4, 4, 2, 0, FAKE, 0)
     refuses(K, K.KIVI_ERR_UNSUPPORTED, f, FAKE, 1, (1 << 30) + 1, 1 << 31, 2, 0, FAKE, 0)
+    refuses(K, K.KIVI_ERR_UNSUPPORTED, f, FAKE, 1, 4, 4, (1 << 30) + 1, 0, FAKE, 0)
     f(0, 0, 4, 4, 2, 0, 0, 0)            # no rows, nothing kept: nothing to do
     f(0, 5, 4, 4, 0, 0, 0, 0)
 

@@ -21,22 +21,39 @@ from oracle.attention import decode_attention  # noqa: E402
 from oracle.cache import OracleCache  # noqa: E402
 
 
+class Lazy(dict):
+    """Oracles of the slots asked for."""
+
+    def __init__(self, make):
+        self.make = make
+
+    def __missing__(self, key):
+        self[key] = self.make(*key)
+        return self[key]
+
+
 def dense(B, Hq, Hkv, D, bits, G, R, L, seed, n_app=0, sink=True):
     """A dense cache of prompt L and n_app appends, the oracle of each slot, and a next query."""
     syn = SynthKV(B, Hq, Hkv, D, seed, sink=sink, device="cuda")
     Kp, Vp = syn.prompt(L)
     cache = GuardedCache(B, Hq, Hkv, D, bits, G, R, max(L + n_app, 1) + 8)
     cache.prefill(Kp, Vp)
-    oc = {}
-    for b in range(B):
-        for h in range(Hkv):
-            oc[b, h] = OracleCache(1, 1, D, bits, G, R)
-            oc[b, h].prefill(Kp[b, h][None, None].cpu().numpy(), Vp[b, h][None, None].cpu().numpy())
-    for s in range(n_app):
-        _, k, v = syn.step(s)
+    new = [syn.step(s)[1:] for s in range(n_app)]
+    for k, v in new:
         cache.append(k, v)
-        for (b, h), o in oc.items():
+
+    def oracle(b, h):
+        o = OracleCache(1, 1, D, bits, G, R)
+        o.prefill(Kp[b, h][None, None].cpu().numpy(), Vp[b, h][None, None].cpu().numpy())
+        for k, v in new:
             o.append(k[b, h][None, None].cpu().numpy(), v[b, h][None, None].cpu().numpy())
+        return o
+
+    oc = Lazy(oracle)
+    if B * Hkv <= 64:
+        for b in range(B):
+            for h in range(Hkv):
+                oc[b, h]
     return cache, oc, syn.step(1000)[0]
 
 
@@ -243,6 +260,25 @@ def test_many_rows():
     check_decode(cache.decode_blocks(q, torch.from_numpy(blocks).cuda()), some, q, blocks, 32, 1)
 
 
+@pytest.mark.parametrize("B,Hkv,nq,bits,G,L,keep", [
+    (1, 1, 1, 2, 32, 900, 20), (1, 3, 2, 4, 64, 1200, 9), (1, 8, 1, 2, 32, 4000, 100), (2, 32, 1, 2, 32, 1500, 40),
+    (8, 19, 1, 2, 32, 700, 12), (9, 17, 4, 4, 64, 700, 5), (16, 19, 1, 8, 32, 600, 12), (38, 16, 2, 2, 32, 400, 6),
+    (61, 25, 1, 2, 32, 300, 4)])
+def test_row_counts(B, Hkv, nq, bits, G, L, keep):
+    """From one row to ten times what the GPU's SMs hold: clusters of 8 CTAs down to
+    several waves of small ones, one or more than one row an SM."""
+    cache, oc, q = dense(B, Hkv * nq, Hkv, 128 if B < 30 else 64, bits, G, G, L, B + Hkv)
+    nb = cache.counts()[0] // G
+    rng = random.Random(B)
+    blocks = lists(rng, B * Hkv, lambda r: nb, keep).reshape(B, Hkv, keep)
+    got = cache.decode_blocks(q, torch.from_numpy(blocks).cuda(), out=cache.bands.like(q))
+    cache.bands.check("after a decode over blocks")
+    rows = {(0, 0), (B - 1, Hkv - 1)} | {(rng.randrange(B), rng.randrange(Hkv)) for _ in range(6)}
+    some = {r: oc[r] for r in rows}
+    check_decode(got, some, q, blocks, G, nq)
+    check_scores(cache.block_scores(q), some, q, bits, Hkv, nq)
+
+
 def test_block_listed_twice_counts_twice():
     cache, oc, q = dense(1, 2, 2, 64, 2, 32, 32, 300, 9)
     blocks = np.array([[[2, 2, 5, 2], [0, 1, 1, 7]]], np.int32)
@@ -443,6 +479,41 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for j in range(2):
         assert all(torch.equal(o, want[j]) for o in outs[j])
+
+
+def test_outputs_allocated_on_a_side_stream():
+    """Calls on a side stream take their outputs from that stream's memory: work of the
+    current stream that is still running cannot meet them."""
+    cache, oc, q = dense(2, 4, 4, 128, 2, 32, 64, 2000, 12)
+    want_s, want_o = cache.block_scores(q), cache.sparse_decode(q, 6)
+    want_b = select_blocks(want_s, 6, 1)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        big = torch.full((want_s.numel() * 4,), 7.0, device="cuda")
+        for _ in range(20):
+            big = big * 1.0001
+        del big                                             # its memory is free again while it is still written
+        s = cache.block_scores(q, stream=side)
+        b = select_blocks(s, 6, 1, stream=side)
+        o = cache.decode_blocks(q, b, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(s, want_s) and torch.equal(b, want_b) and torch.equal(o, want_o)
+
+
+def test_copy_wait_runs_out_marks_its_row():
+    """The failure-detection hook: the wait of one warp runs out (about 2 s), the heads
+    of its row are NaN, the others and the next call are right."""
+    cache, oc, q = dense(2, 4, 2, 64, 2, 32, 64, 600, 8)
+    blocks = torch.arange(6, dtype=torch.int32, device="cuda").expand(2, 2, 6).contiguous()
+    want = cache.decode_blocks(q, blocks)
+    K.kivi_cache_set_fault(cache.handle, K.KIVI_FAULT_COPY_STALL)
+    out = cache.decode_blocks(q, blocks)
+    torch.cuda.synchronize()
+    assert out[0, :2].isnan().all()
+    out[0, :2] = want[0, :2]
+    assert torch.equal(out, want)
+    assert torch.equal(cache.decode_blocks(q, blocks), want)
 
 
 def test_refusals_with_tensors():
