@@ -492,10 +492,13 @@ cudaError_t launch_decode_blocks(const BlockRows& r, const __half* q, const int*
     const Geometry& g = *r.g;
     const int nq = g.Hq / g.Hkv;
     const long long rows = (long long)r.n * g.Hkv;
-    // weights: bytes of a quantized pair / 32, and 40 D bytes / 32 for a residual tile
+    // weights: bytes of a quantized pair / 32; a residual tile, whose loads overlap
+    // other warps' work, as 24 of its 64 D bytes (one head of 64 channels, 4 blocks
+    // and 2 tiles: 3.15 us, weighted as 40 D bytes 3.7; the 7B layer and 131k
+    // tokens do not change between 16 and 64 D)
     const blocks_detail::Args base{r.buf, q, out, list, g.NB, g.part_bytes, g.slot_bytes, g.tile_bytes,
                                    g.k_resid_off, g.v_resid_off, g.R, g.Hq, g.Hkv, n_list, r.n_blocks, r.n_resid,
-                                   g.D * g.bits / 4 + 8 * g.D / g.G, 5 * g.D / 4, scale_log2, r.stall_bytes};
+                                   g.D * g.bits / 4 + 8 * g.D / g.G, 3 * g.D / 4, scale_log2, r.stall_bytes};
     auto units = [&](int nblk, int nres) {
         return (long long)(n_list < nblk ? n_list : nblk) * (g.G / 32) + (nres + 15) / 16;
     };

@@ -177,8 +177,9 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     const int g = lane >> 2, i = lane & 3;
     const int warps = blockDim.x >> 5;
     const uint32_t crank = cluster_rank(), csize = cluster_size();
-    const long long row = blockIdx.x / csize;
-    const int b = (int)(row / a.Hkv), hk = (int)(row % a.Hkv);
+    const unsigned row32 = blockIdx.x / csize;    // (rows are at most 65535)
+    const int b = (int)(row32 / (unsigned)a.Hkv), hk = (int)(row32 % (unsigned)a.Hkv);
+    const long long row = row32;
     uint8_t* ring = dyn_smem + warp * S::WARP;
     uint32_t* qfrag = reinterpret_cast<uint32_t*>(ring + S::FRAG);
     long long* offs = reinterpret_cast<long long*>(ring + S::OFFS);
@@ -232,19 +233,19 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     const int te = (int)(((unsigned)worker + 1u) * (unsigned)T / (unsigned)workers);
     // (Every warp has to find the same bounds: separately rounded operations
     // give the same fp32 values wherever the expression is compiled.)
-    const float per_worker = __fdiv_rn(__fadd_rn(__fmul_rn((float)T, (float)a.wr), __fmul_rn((float)P, (float)a.wq)),
-                                       (float)workers);
-    const float per_tile = __fdiv_rn((float)T, (float)workers);
-    auto pairs_before = [&](int w) {
-        float most = 0.f;
-        for (int v = lane; v <= w; v += 32) {
-            const float tiles = floorf(__fmul_rn((float)v, per_tile));
-            const float left = __fsub_rn(__fmul_rn((float)v, per_worker), __fmul_rn(tiles, (float)a.wr));
-            most = fmaxf(most, __fdiv_rn(left, (float)a.wq));
-        }
-        return min(P, __reduce_max_sync(kFull, (int)ceilf(most)));
+    const float per_one = __frcp_rn((float)workers), inv_wq = __frcp_rn((float)a.wq);
+    const float per_worker =
+        __fmul_rn(__fadd_rn(__fmul_rn((float)T, (float)a.wr), __fmul_rn((float)P, (float)a.wq)), per_one);
+    const float per_tile = __fmul_rn((float)T, per_one);
+    auto pairs_at = [&](int v) {                  // pairs that fit before worker v beside the tiles before it
+        const float tiles = floorf(__fmul_rn((float)v, per_tile));
+        const float left = __fsub_rn(__fmul_rn((float)v, per_worker), __fmul_rn(tiles, (float)a.wr));
+        return min(P, max(0, (int)ceilf(__fmaf_rn(left, inv_wq, -0.02f))));   // (whole counts stay whole)
     };
-    const int wb = worker == 0 ? 0 : pairs_before(worker), we = worker + 1 == workers ? P : pairs_before(worker + 1);
+    int wb = 0;
+    for (int v = lane; v <= worker; v += 32) wb = max(wb, pairs_at(v));
+    wb = worker == 0 ? 0 : __reduce_max_sync(kFull, wb);
+    const int we = worker + 1 == workers ? P : max(wb, pairs_at(worker + 1));
 
     // everything below reads what earlier kernels on the stream may have written
     griddepcontrol_wait();
@@ -658,7 +659,8 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
 #pragma unroll 4
         for (int j = 0; j < warps; ++j) {
             const float* mine = reinterpret_cast<const float*>(dyn_smem + j * S::WARP) + idx;
-            sum = fmaf(mine[S::SUMS / 4], __shfl_sync(kFull, e, j), fmaf(mine[0], __shfl_sync(kFull, e, warps + j), sum));
+            const float er = __shfl_sync(kFull, e, j), eb = __shfl_sync(kFull, e, warps + j);
+            sum = fmaf(mine[S::SUMS / 4], er, fmaf(mine[0], eb, sum));
         }
         if (csize > 1) {
             stc32(cluster_map(smem_u32(&recv_s[(int)crank * span + idx % span]), idx / span), sum);
