@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     const int g = lane >> 2, i = lane & 3;
     const int warps = blockDim.x >> 5;
     const uint32_t crank = cluster_rank(), csize = cluster_size();
-    const unsigned row32 = blockIdx.x / csize;    // (rows are at most 65535)
+    const int cshift = 31 - __clz((int)csize);    // (a power of two)
+    const unsigned row32 = blockIdx.x >> cshift;  // (rows are at most 65535)
     const int b = (int)(row32 / (unsigned)a.Hkv), hk = (int)(row32 % (unsigned)a.Hkv);
     const long long row = row32;
     uint8_t* ring = dyn_smem + warp * S::WARP;
@@ -224,23 +225,22 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         rslot = row;
     }
     // Every worker (a warp) gets its share of the tiles, and pairs up to its
-    // share of the weight: tiles [w T / n, (w + 1) T / n), pairs from
-    // pairs_before(w), the largest count that the weight position of a worker up
-    // to w leaves beside the tiles before it.
+    // share of the weight: tiles from w T / n on, pairs from the largest count on
+    // that the weight position of a worker up to w leaves beside the tiles
+    // before it.
     const int P = min(a.n_list, nblk) * PPB, T = (n_res + 15) / 16;
     const int workers = (int)csize * warps, worker = (int)crank * warps + warp;
-    const int tb = (int)((unsigned)worker * (unsigned)T / (unsigned)workers);
-    const int te = (int)(((unsigned)worker + 1u) * (unsigned)T / (unsigned)workers);
     // (Every warp has to find the same bounds: separately rounded operations
     // give the same fp32 values wherever the expression is compiled.)
     const float per_one = __frcp_rn((float)workers), inv_wq = __frcp_rn((float)a.wq);
     const float per_worker =
         __fmul_rn(__fadd_rn(__fmul_rn((float)T, (float)a.wr), __fmul_rn((float)P, (float)a.wq)), per_one);
     const float per_tile = __fmul_rn((float)T, per_one);
+    auto tiles_at = [&](int v) { return floorf(__fmaf_rn((float)v, per_tile, 0.02f)); };   // (whole counts stay whole)
+    const int tb = (int)tiles_at(worker), te = worker + 1 == workers ? T : (int)tiles_at(worker + 1);
     auto pairs_at = [&](int v) {                  // pairs that fit before worker v beside the tiles before it
-        const float tiles = floorf(__fmul_rn((float)v, per_tile));
-        const float left = __fsub_rn(__fmul_rn((float)v, per_worker), __fmul_rn(tiles, (float)a.wr));
-        return min(P, max(0, (int)ceilf(__fmaf_rn(left, inv_wq, -0.02f))));   // (whole counts stay whole)
+        const float left = __fsub_rn(__fmul_rn((float)v, per_worker), __fmul_rn(tiles_at(v), (float)a.wr));
+        return min(P, max(0, (int)ceilf(__fmaf_rn(left, inv_wq, -0.02f))));
     };
     int wb = 0;
     for (int v = lane; v <= worker; v += 32) wb = max(wb, pairs_at(v));
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     int k = wb;                // next pair to process
     int j0 = 0, kend = wb;     // the part of the list in offs: entries from j0, pairs below kend
     uint32_t item = 0;         // ring item of pair k
-    auto issue = [&](int kk, uint32_t it) {       // lane 0: pair kk -> ring stage of item it
+    auto issue = [&](int kk, uint32_t it) {       // one lane: pair kk -> ring stage of item it
         const uint32_t st = it % C::STAGES;
         const uint32_t dst = ring_u32 + st * C::STAGE_BYTES, bar = bars_u32 + 8 * st;
         const long long off = offs[kk / PPB - j0];
@@ -336,9 +336,9 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     auto begin_part = [&]() {
         offs[lane] = offset_of(entry);
         __syncwarp();
-        if (lane == 0) {
+        if (lane < C::STAGES && k + lane < kend) {   // the part's first copies, a lane each
             fence_proxy_async();
-            for (int u = 0; u < C::STAGES && k + u < kend; ++u) issue(k + u, item + u);
+            issue(k + lane, item + lane);
         }
         __syncwarp();
     };
@@ -541,15 +541,6 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
             break;
         }
     }
-    // the quantized tiles' value sums are in units of 2^(BITS*pos - 24),
-    // pos = (channel / 8) % (8 / BITS): rows g and g+8 of m-tile mt have
-    // classes 2mt and 2mt+1
-#pragma unroll
-    for (int mt = 0; mt < KS; ++mt) {
-        const float s0 = pow2i(24 - BITS * ((2 * mt) % (8 / BITS)));
-        const float s1 = pow2i(24 - BITS * ((2 * mt + 1) % (8 / BITS)));
-        o[mt][0] *= s0; o[mt][1] *= s0; o[mt][2] *= s1; o[mt][3] *= s1;
-    }
     // ---- the listed blocks' partial result ----
 #pragma unroll
     for (int f = 0; f < NBF; ++f) {
@@ -565,9 +556,13 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         for (int mt = 0; mt < KS; ++mt) {
             const int gr = 16 * mt / G;
             if (gr % GB == jO) {
+                // the sums are in units of 2^(BITS*pos - 24), pos = (channel / 8) % (8 / BITS):
+                // rows g and g+8 of m-tile mt have classes 2mt and 2mt+1
+                const float u0 = pow2i(24 - BITS * ((2 * mt) % (8 / BITS)));
+                const float u1 = pow2i(24 - BITS * ((2 * mt + 1) % (8 / BITS)));
                 const float z = zo[gr / GB];
-                sums[hO * D + 16 * mt + g] = o[mt][0] + o[mt][1] + z;
-                sums[hO * D + 16 * mt + g + 8] = o[mt][2] + o[mt][3] + z;
+                sums[hO * D + 16 * mt + g] = fmaf(o[mt][0] + o[mt][1], u0, z);
+                sums[hO * D + 16 * mt + g + 8] = fmaf(o[mt][2] + o[mt][3], u1, z);
             }
         }
     }
@@ -583,48 +578,48 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     // the tiles': k-steps 2j, 2j+1 hold channels 32 j + 8 i + 0..3, + 4..7, and
     // m-tile 2j+u has row g at channel 32 j + 8 (g / 2) + 4 u + g % 2, row g + 8
     // two further.  Their partial result is kept apart from the blocks'. ----
-    m = -INFINITY;
-    l = 0.f;
-    fresh = true;
+    float* rsum = reinterpret_cast<float*>(ring + S::SUMS);
+    if (tb < te) {
+        m = -INFINITY;
+        l = 0.f;
+        fresh = true;
 #pragma unroll
-    for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-    // (Prefetching the rows into L2 at the start of the call, or a few pairs
-    // ahead, took the bandwidth that the first copies wait for: 7B 12.3 and 11.9
-    // us against 11.6; spread over the pairs, 512 rows of four heads: 42.9 against
-    // 41.8.  Odd warps taking their tiles first: 44.1.)
-    for (int tile = tb; tile < te; ++tile) {
-        load_rows(tile);
-        const bool okg = 16 * tile + g < n_res, okg8 = 16 * tile + g + 8 < n_res;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+        // (Prefetching the rows into L2 at the start of the call, or a few pairs
+        // ahead, took the bandwidth that the first copies wait for: 7B 12.3 and 11.9
+        // us against 11.6; spread over the pairs, 512 rows of four heads: 42.9 against
+        // 41.8.  Odd warps taking their tiles first: 44.1.)
+        for (int tile = tb; tile < te; ++tile) {
+            load_rows(tile);
+            const bool okg = 16 * tile + g < n_res, okg8 = 16 * tile + g + 8 < n_res;
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < DJ; ++j) {
-            uint4 bq = make_uint4(0, 0, 0, 0);
-            if (g < 2 * NQ) bq = *reinterpret_cast<const uint4*>(&qres[g < 2 * NQ ? g : 0][32 * j + 8 * i]);
-            const uint32_t f0[4] = {kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y};
-            const uint32_t f1[4] = {kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w};
-            mma16816(c, f0, bq.x, bq.y);
-            mma16816(c, f1, bq.z, bq.w);
+            for (int j = 0; j < DJ; ++j) {
+                uint4 bq = make_uint4(0, 0, 0, 0);
+                if (g < 2 * NQ) bq = *reinterpret_cast<const uint4*>(&qres[g < 2 * NQ ? g : 0][32 * j + 8 * i]);
+                const uint32_t f0[4] = {kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y};
+                const uint32_t f1[4] = {kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w};
+                mma16816(c, f0, bq.x, bq.y);
+                mma16816(c, f1, bq.z, bq.w);
+            }
+            const float sc[4] = {okg ? c[0] + c[1] : -INFINITY, okg8 ? c[2] + c[3] : -INFINITY, -INFINITY, -INFINITY};
+            float p[4];
+            softmax(sc, p, 1.f);
+            float prb[4];
+            gather(p[0], p[1], prb);
+            uint32_t ph01, ph89, pl01, pl89;
+            split_p(prb, ph01, ph89, pl01, pl89);
+            const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
+#pragma unroll
+            for (int j = 0; j < DJ; ++j) {
+                const uint32_t f0[4] = {movmatrix_trans(vx[0][j].x), movmatrix_trans(vx[0][j].y),
+                                        movmatrix_trans(vx[1][j].x), movmatrix_trans(vx[1][j].y)};
+                mma16816(o[2 * j], f0, pb0, pb1);
+                const uint32_t f1[4] = {movmatrix_trans(vx[0][j].z), movmatrix_trans(vx[0][j].w),
+                                        movmatrix_trans(vx[1][j].z), movmatrix_trans(vx[1][j].w)};
+                mma16816(o[2 * j + 1], f1, pb0, pb1);
+            }
         }
-        const float sc[4] = {okg ? c[0] + c[1] : -INFINITY, okg8 ? c[2] + c[3] : -INFINITY, -INFINITY, -INFINITY};
-        float p[4];
-        softmax(sc, p, 1.f);
-        float prb[4];
-        gather(p[0], p[1], prb);
-        uint32_t ph01, ph89, pl01, pl89;
-        split_p(prb, ph01, ph89, pl01, pl89);
-        const uint32_t pb0 = lo_col ? pl01 : ph01, pb1 = lo_col ? pl89 : ph89;
-#pragma unroll
-        for (int j = 0; j < DJ; ++j) {
-            const uint32_t f0[4] = {movmatrix_trans(vx[0][j].x), movmatrix_trans(vx[0][j].y),
-                                    movmatrix_trans(vx[1][j].x), movmatrix_trans(vx[1][j].y)};
-            mma16816(o[2 * j], f0, pb0, pb1);
-            const uint32_t f1[4] = {movmatrix_trans(vx[0][j].z), movmatrix_trans(vx[0][j].w),
-                                    movmatrix_trans(vx[1][j].z), movmatrix_trans(vx[1][j].w)};
-            mma16816(o[2 * j + 1], f1, pb0, pb1);
-        }
-    }
-    {
-        float* rsum = reinterpret_cast<float*>(ring + S::SUMS);
         const float lt = sum_l();
         if (g == 0 && i < NQ) head_s[warp][i] = make_float4(m, lt, 0.f, 0.f);
         if (hO < NQ) {                            // every group slot's columns hold the same sums: each writes some
@@ -636,12 +631,18 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
                 rsum[hO * D + ch + 2] = o[mt][2] + o[mt][3];
             }
         }
+    } else {                                      // no tiles: no weight, zero sums
+        if (lane < NQ) head_s[warp][lane] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        for (int idx = 4 * lane; idx < NQ * D; idx += 128)
+            *reinterpret_cast<float4*>(rsum + idx) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 
     // ---- the log-sum-exp merge: the CTA's partials, then the cluster's CTAs ----
     // Every warp weighs the partials of its outputs' head for itself, one a
     // lane, and hands the weights round by shuffles.
-    const int span = NQ * D / (int)csize;         // the outputs a CTA of the cluster writes
+    constexpr int kOutShift = NQ * D == 64 ? 6 : NQ * D == 128 ? 7 : NQ * D == 256 ? 8 : 9;
+    static_assert(NQ * D == 1 << kOutShift, "outputs of a row");
+    const int span = NQ * D >> cshift;            // the outputs a CTA of the cluster writes
     __half* out = a.out + ((long long)b * a.Hq + hk * NQ) * D;
     if (csize > 1) cluster_wait();                // (every CTA has started: its shared memory may be written)
     __syncthreads();
@@ -663,7 +664,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
             sum = fmaf(mine[S::SUMS / 4], er, fmaf(mine[0], eb, sum));
         }
         if (csize > 1) {
-            stc32(cluster_map(smem_u32(&recv_s[(int)crank * span + idx % span]), idx / span), sum);
+            stc32(cluster_map(smem_u32(&recv_s[(int)crank * span + (idx & (span - 1))]), (unsigned)idx >> (kOutShift - cshift)), sum);
             if (idx % D < (int)csize)             // (csize <= 8 < D) the head's (M, L, status) to each CTA
                 stc128(cluster_map(smem_u32(&recv_head[crank][h]), idx % D), make_float4(M, L, bad ? 1.f : 0.f, 0.f));
         } else {
