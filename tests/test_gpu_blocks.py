@@ -279,6 +279,33 @@ def test_row_counts(B, Hkv, nq, bits, G, L, keep):
     check_scores(cache.block_scores(q), some, q, bits, Hkv, nq)
 
 
+def test_offsets_past_4_gib():
+    """A dense cache and a page pool of more than 4 GiB: the last rows' blocks, scores and tables."""
+    B, H, D, bits, G, R, L = 8, 32, 128, 8, 32, 32, 60000
+    syn = SynthKV(B, H, H, D, 3, device="cuda")
+    Kp, Vp = syn.prompt(L)
+    q = syn.step(0)[0]
+    some = {}
+    for r in [(0, 0), (7, 31), (7, 0)]:
+        some[r] = OracleCache(1, 1, D, bits, G, R)
+        some[r].prefill(Kp[r][None, None].cpu().numpy(), Vp[r][None, None].cpu().numpy())
+    nb = some[0, 0].n_quant // G
+    blocks = np.sort(np.random.default_rng(1).integers(0, nb, (B, H, 9)).astype(np.int32), axis=-1)
+    blocks[..., -1] = nb - 1
+    bt = torch.from_numpy(blocks).cuda()
+    cache = KiviCache(B, H, H, D, bits, G, R, L + 1)
+    assert cache.buffer.numel() > 1 << 32
+    cache.prefill(Kp, Vp)
+    check_scores(cache.block_scores(q), some, q, bits, H, 1)
+    check_decode(cache.decode_blocks(q, bt), some, q, blocks, G, 1, "dense")
+    del cache
+    pool = KiviPagedCache(B, H, H, D, bits, G, R, nb + 1, B * nb + 3)
+    assert pool.buffer.numel() > 1 << 32
+    seqs = [pool.add(Kp[b], Vp[b]) for b in range(B)]
+    check_scores(pool.block_scores(seqs, q), some, q, bits, H, 1)
+    check_decode(pool.decode_blocks(seqs, q, bt), some, q, blocks, G, 1, "paged")
+
+
 def test_block_listed_twice_counts_twice():
     cache, oc, q = dense(1, 2, 2, 64, 2, 32, 32, 300, 9)
     blocks = np.array([[[2, 2, 5, 2], [0, 1, 1, 7]]], np.int32)

@@ -112,6 +112,23 @@ def test_strided_sources_and_wide_values():
     assert all((o == 0).all() for o in out)
 
 
+def test_more_than_2_31_values():
+    """A query tensor of 2.2 billion values: 64-bit offsets on both sides."""
+    B, L, Hq, Hkv, D = 17, 32768, 32, 1, 128
+    nr, w, table = op(Hq, Hkv, D, True, D, False, L, 6)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.empty(B, L, Hq, D, dtype=torch.bfloat16, device="cuda")
+    for b in range(B):
+        q[b] = torch.randn(L, Hq, D, generator=g, device="cuda").bfloat16()
+    k = torch.randn(B, L, Hkv, D, generator=g, device="cuda").bfloat16()
+    assert q.numel() > 1 << 31
+    got = nr(q, k, k)
+    at = torch.tensor([0, 1, L // 2, L - 1], device="cuda")
+    for b in (0, B // 2, B - 1):
+        check(got[0][b:b + 1, :, at], q[b:b + 1, at], w[0], 1e-5, table, at[None], False, f"row {b}")
+        check(got[1][b:b + 1, :, at], k[b:b + 1, at], w[1], 1e-5, table, at[None], False, f"row {b}")
+
+
 def test_positions_outside_the_table():
     """No table row is read for them; the rotated channels of the token's q and k become NaN."""
     B, L, H, D = 1, 6, 2, 128
