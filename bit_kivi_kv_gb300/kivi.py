@@ -116,8 +116,8 @@ def _load():
         "kivi_paged_block_scores": (I, [P, IP, I, P, F, P, LL, P]),
         "kivi_paged_decode_blocks": (I, [P, IP, I, P, P, I, P, F, P]),
         "kivi_paged_append": (I, [P, IP, I, P, P, P]),
-        "kivi_qk_norm_rope": (I, [ctypes.POINTER(kivi_qkv), P]),
-        "kivi_append_qkv": (I, [P, ctypes.POINTER(kivi_qkv), P]),
+        "kivi_qk_norm_rope": (I, [P, P]),     # a kivi_qkv by reference, or its packed bytes
+        "kivi_append_qkv": (I, [P, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -340,11 +340,19 @@ def kivi_launch_count() -> int:
 
 
 # ---- torch convenience wrapper -----------------------------------------------
-def _device():
-    """The current device (what torch.cuda.current_device() is, without its set-up
-    check: 0.1 against 0.3 us)."""
+# torch, and its lookups of the current device and of a device's current stream (what
+# torch.cuda.current_device() and current_stream().cuda_stream are, without their set-up
+# checks and objects: 0.1 us each against 0.3 and 2.9).  Bound when the first wrapper is
+# made, since the C calls need no torch.
+_torch = _device = _current_stream = None
+
+
+def _bind():
+    global _torch, _device, _current_stream
     import torch
-    return torch._C._cuda_getDevice()
+    _torch = torch
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
 def _expect(t, what, dtype, shape, device):
@@ -358,45 +366,36 @@ def _expect(t, what, dtype, shape, device):
     raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current device")
 
 
-def _raw_stream(stream, device):
-    """The handle of stream (None: the device's current one)."""
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    # (what torch.cuda.current_stream().cuda_stream is, without the stream object: 0.1 against 2.9 us)
-    return torch._C._cuda_getCurrentRawStream(device)
-
-
 def _new(shape, dtype, device, stream):
     """An output of a call that runs on stream: its memory has to come from that
     stream's pool, where no earlier work of another stream may still use it."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 def select_blocks(scores, n_keep, keep_first=0, out=None, stream=None):
     """The n_keep best columns of each row of scores (fp32 [..., cols], rows dense or
     evenly strided), as int32 [..., n_keep] in ascending order with -1 behind; the
     first keep_first columns always among them (kivi_select_blocks)."""
-    import torch
-    shape = scores.shape
-    device = _device()
-    if scores.dtype is not torch.float32 or scores.get_device() != device:
+    if _torch is None:
+        _bind()
+    shape, device = scores.shape, _device()
+    if scores.dtype is not _torch.float32 or scores.get_device() != device:
         raise KiviError(KIVI_ERR_INVALID_ARG, "scores must be a float32 tensor on the current CUDA device")
-    cols = ld = shape[-1]
+    *lead, cols = shape
+    ld = cols
     if not scores.is_contiguous():
-        if scores.dim() != 2 or scores.stride(1) != 1:
+        if len(lead) != 1 or scores.stride(1) != 1:
             raise KiviError(KIVI_ERR_INVALID_ARG, "scores must be contiguous, or a matrix with dense rows")
         ld = scores.stride(0)
     if out is None:
-        out = _new(shape[:-1] + (max(n_keep, 0),), torch.int32, scores.device, stream)
+        out = _new((*lead, max(n_keep, 0)), _torch.int32, scores.device, stream)
     else:
-        _expect(out, "out", torch.int32, shape[:-1] + (n_keep,), device)
-    kivi_select_blocks(scores.data_ptr(), math.prod(shape[:-1]), cols, ld, n_keep, keep_first, out.data_ptr(),
-                       _raw_stream(stream, device))
+        _expect(out, "out", _torch.int32, (*lead, n_keep), device)
+    _check(lib.kivi_select_blocks(scores.data_ptr(), math.prod(lead), cols, ld, n_keep, keep_first, out.data_ptr(),
+                                  _current_stream(device) if stream is None else stream.cuda_stream))
     return out
 
 
@@ -419,23 +418,24 @@ class QKNormRope:
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, q_weight=None, k_weight=None, cos_sin=None, eps=1e-6,
                  interleaved=False):
-        import torch
+        _bind()
+        f32 = _torch.float32
         for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
             if w is not None:
-                _expect(w, what, torch.float32, (head_dim,), _device())
+                _expect(w, what, f32, (head_dim,), _device())
         rot_dim = n_positions = table = 0
         if cos_sin is not None:
             if cos_sin.dim() != 2:
                 raise KiviError(KIVI_ERR_INVALID_ARG, "cos_sin must be [n_positions, rot_dim]")
-            _expect(cos_sin, "cos_sin", torch.float32, cos_sin.shape, _device())
+            _expect(cos_sin, "cos_sin", f32, cos_sin.shape, _device())
             table, (n_positions, rot_dim) = cos_sin.data_ptr(), cos_sin.shape
         self._keep = (q_weight, k_weight, cos_sin)
         self._device = next((t.get_device() for t in self._keep if t is not None), None)
         self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
         self._fixed = (q_weight.data_ptr() if q_weight is not None else 0, k_weight.data_ptr() if k_weight is not None
                        else 0, eps, table, n_positions, rot_dim, bool(interleaved))
-        self._dtypes = {torch.float16: KIVI_F16, torch.bfloat16: KIVI_BF16, torch.float32: KIVI_F32}
-        self._positions = {torch.int32: 0, torch.int64: 1}
+        self._dtypes = {_torch.float16: KIVI_F16, _torch.bfloat16: KIVI_BF16, f32: KIVI_F32}
+        self._positions = {_torch.int32: 0, _torch.int64: 1}
         self._layouts = {}      # what _layout found out about shapes, strides and types seen before
 
     def _layout(self, key):
@@ -465,12 +465,10 @@ class QKNormRope:
         found = self._layouts[key] = (head, strides, lead, outs)
         return found
 
-    def _args(self, q, k, v, positions, first_position, outs):
-        """The C call's arguments for inputs [batch, tokens, heads, head_dim] (or
-        [batch, heads, head_dim]: one token a row); outs(shapes, device) gives the
-        outputs and the addresses of the three."""
-        import torch
-        device = _device()
+    def _inputs(self, q, k, v, positions, device):
+        """Checks the inputs [batch, tokens, heads, head_dim] (or [batch, heads,
+        head_dim]: one token a row): the packed fields up to the strides, the address and
+        width of the positions, and the shapes of the outputs."""
         if q.get_device() != device or k.get_device() != device or v.get_device() != device:
             raise KiviError(KIVI_ERR_INVALID_ARG, "q, k and v must be on the current device")
         if self._device is not None and self._device != device:
@@ -484,11 +482,7 @@ class QKNormRope:
                 raise KiviError(KIVI_ERR_INVALID_ARG, "positions must be int32 or int64")
             _expect(positions, "positions", positions.dtype, lead, device)
             pos = positions.data_ptr()
-        out, ptrs = outs(shapes, device)
-        # (the fields of kivi_qkv in order, packed at once: a few times faster than one by one)
-        a = kivi_qkv.from_buffer_copy(_QKV.pack(*head, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
-                                                *self._fixed, pos, wide, first_position, *ptrs))
-        return a, out
+        return (*head, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, *self._fixed, pos, wide), shapes
 
     def __call__(self, q, k, v, positions=None, first_position=0, out=None, stream=None):
         """q [B, L, Hq, D], k and v [B, L, Hkv, D] (fp16, bf16 or fp32; any strides with
@@ -496,20 +490,18 @@ class QKNormRope:
         a row), positions [B, L] int32 or int64 (None: first_position + token).
         Returns fp16 (q [B, Hq, L, D], k [B, Hkv, L, D], v), without L where the
         inputs have none."""
-        import torch
-
-        def outs(shapes, device):
-            if out is None:
-                o = tuple(_new(s, torch.float16, q.device, stream) for s in shapes)
-            else:
-                o = out
-                for t, s in zip(o, shapes):
-                    _expect(t, "out", torch.float16, s, device)
-            a, b, c = o
-            return o, (a.data_ptr(), b.data_ptr(), c.data_ptr())
-
-        a, out = self._args(q, k, v, positions, first_position, outs)
-        kivi_qk_norm_rope(a, _raw_stream(stream, _device()))
+        device, f16 = _device(), _torch.float16
+        fields, (sq, sk, sv) = self._inputs(q, k, v, positions, device)
+        if out is None:
+            out = oq, ok, ov = tuple(_new(s, f16, q.device, stream) for s in (sq, sk, sv))
+        else:
+            oq, ok, ov = out
+            _expect(oq, "out[0]", f16, sq, device)
+            _expect(ok, "out[1]", f16, sk, device)
+            _expect(ov, "out[2]", f16, sv, device)
+        # (the fields of kivi_qkv in order, packed at once: a few times faster than one by one)
+        _check(lib.kivi_qk_norm_rope(_QKV.pack(*fields, first_position, oq.data_ptr(), ok.data_ptr(), ov.data_ptr()),
+                                     _current_stream(device) if stream is None else stream.cuda_stream))
         return out
 
 
@@ -518,6 +510,7 @@ class KiviCache:
 
     def __init__(self, batch, n_q_heads, n_kv_heads, head_dim, bits, group, residual, max_tokens,
                  device="cuda"):
+        _bind()
         self.cfg = make_config(batch, n_q_heads, n_kv_heads, head_dim, bits, group, residual, max_tokens)
         nbytes = kivi_cache_bytes(self.cfg)
         if nbytes == 0:
@@ -592,55 +585,50 @@ class KiviCache:
         """Append one token a row from a projection's output: norm and rotation by
         norm_rope (QKNormRope), k and v stored in the cache by the same kernel.
         q [B, Hq, D], k, v [B, Hkv, D]; returns the query, fp16 [B, Hq, D]."""
-        import torch
-
-        def outs(shapes, device):
-            o = q_out
-            if o is None:
-                o = _new(shapes[0], torch.float16, q.device, stream)
-            else:
-                _expect(o, "q_out", torch.float16, shapes[0], device)
-            return o, (o.data_ptr(), 0, 0)
-
-        a, q_out = norm_rope._args(q, k, v, positions, first_position, outs)
-        kivi_append_qkv(self.handle, a, _raw_stream(stream, _device()))
+        device, f16 = _device(), _torch.float16
+        fields, (shape, _, _) = norm_rope._inputs(q, k, v, positions, device)
+        if q_out is None:
+            q_out = _new(shape, f16, q.device, stream)
+        else:
+            _expect(q_out, "q_out", f16, shape, device)
+        _check(lib.kivi_append_qkv(self.handle, _QKV.pack(*fields, first_position, q_out.data_ptr(), 0, 0),
+                                   _current_stream(device) if stream is None else stream.cuda_stream))
         return q_out
 
     def block_scores(self, q, out=None, softmax_scale=0.0, stream=None):
         """A bound on the logits of each quantized block for q [B, Hq, D]: fp32
         [B, Hkv, blocks] (kivi_block_scores); out may have more columns (-inf there)."""
-        import torch
-        device = _device()
-        _expect(q, "q", torch.float16, self._q_shape, device)
+        device, f32 = _device(), _torch.float32
+        _expect(q, "q", _torch.float16, self._q_shape, device)
         if out is None:
-            out = _new(self._rows + (self.counts()[0] // self.cfg.group,), torch.float32, q.device, stream)
+            cols = self.counts()[0] // self.cfg.group
+            out = _new((*self._rows, cols), f32, q.device, stream)
         else:
-            _expect(out, "out", torch.float32, self._rows + out.shape[-1:], device)
-        kivi_block_scores(self.handle, q.data_ptr(), softmax_scale, out.data_ptr(), out.shape[-1],
-                          _raw_stream(stream, device))
+            cols = out.shape[-1]
+            _expect(out, "out", f32, (*self._rows, cols), device)
+        _check(lib.kivi_block_scores(self.handle, q.data_ptr(), softmax_scale, out.data_ptr(), cols,
+                                     _current_stream(device) if stream is None else stream.cuda_stream))
         return out
 
     def decode_blocks(self, q, blocks, out=None, softmax_scale=0.0, stream=None):
         """Decode attention of q [B, Hq, D] over the listed blocks (int32
         [B, Hkv, n], negative: none) and the residual (kivi_decode_blocks)."""
-        import torch
-        device = _device()
-        _expect(q, "q", torch.float16, self._q_shape, device)
-        _expect(blocks, "blocks", torch.int32, self._rows + blocks.shape[-1:], device)
+        device, f16, n = _device(), _torch.float16, blocks.shape[-1]
+        _expect(q, "q", f16, self._q_shape, device)
+        _expect(blocks, "blocks", _torch.int32, (*self._rows, n), device)
         if out is None:
-            out = _new(q.shape, torch.float16, q.device, stream)
+            out = _new(self._q_shape, f16, q.device, stream)
         else:
-            _expect(out, "out", torch.float16, self._q_shape, device)
-        kivi_decode_blocks(self.handle, q.data_ptr(), blocks.data_ptr(), blocks.shape[-1], out.data_ptr(),
-                           softmax_scale, _raw_stream(stream, device))
+            _expect(out, "out", f16, self._q_shape, device)
+        _check(lib.kivi_decode_blocks(self.handle, q.data_ptr(), blocks.data_ptr(), n, out.data_ptr(), softmax_scale,
+                                      _current_stream(device) if stream is None else stream.cuda_stream))
         return out
 
     def sparse_decode(self, q, n_keep, keep_first=1, out=None, softmax_scale=0.0, stream=None):
         """Decode attention over the n_keep blocks of the largest scores (the first
         keep_first always) and the residual: block_scores, select_blocks and
         decode_blocks in sequence."""
-        import torch
-        with torch.cuda.stream(stream):
+        with _torch.cuda.stream(stream):
             scores = self.block_scores(q, softmax_scale=softmax_scale)
             n_keep = min(n_keep, scores.shape[-1])
             blocks = select_blocks(scores, n_keep, min(keep_first, n_keep))
@@ -653,6 +641,7 @@ class KiviPagedCache:
 
     def __init__(self, max_seqs, n_q_heads, n_kv_heads, head_dim, bits, group, residual, max_blocks_per_seq,
                  n_pages, device="cuda"):
+        _bind()
         self.cfg = make_paged_config(max_seqs, n_q_heads, n_kv_heads, head_dim, bits, group, residual,
                                      max_blocks_per_seq, n_pages)
         nbytes = kivi_paged_bytes(self.cfg)
@@ -663,6 +652,7 @@ class KiviPagedCache:
         self.workspace = self._alloc(kivi_paged_workspace_bytes(self.cfg, min(max_seqs, KIVI_PAGED_MAX_CALL_SEQS)),
                                      device)
         self.handle = kivi_paged_create(self.cfg, self.buffer.data_ptr(), nbytes)
+        self._heads = (n_q_heads, n_kv_heads, head_dim)
 
     def _alloc(self, nbytes, device):
         """Device bytes for the buffer and the workspace (see KiviCache._alloc)."""
@@ -708,48 +698,45 @@ class KiviPagedCache:
 
     def append(self, seqs, k, v, stream=None):
         """For each listed sequence: append k[i], v[i] ([n][Hkv][D])."""
-        import torch
-        c, device = self.cfg, _device()
-        shape = (len(seqs), c.n_kv_heads, c.head_dim)
-        _expect(k, "k", torch.float16, shape, device)
-        _expect(v, "v", torch.float16, shape, device)
-        kivi_paged_append(self.handle, seqs, k.data_ptr(), v.data_ptr(), _raw_stream(stream, device))
+        n, (_, hkv, d), device = len(seqs), self._heads, _device()
+        _expect(k, "k", _torch.float16, (n, hkv, d), device)
+        _expect(v, "v", _torch.float16, (n, hkv, d), device)
+        _check(lib.kivi_paged_append(self.handle, _seq_array(seqs), n, k.data_ptr(), v.data_ptr(),
+                                     _current_stream(device) if stream is None else stream.cuda_stream))
 
     def block_scores(self, seqs, q, out=None, softmax_scale=0.0, stream=None):
         """KiviCache.block_scores for the listed sequences: q [n, Hq, D] -> fp32
         [n, Hkv, the longest sequence's blocks], -inf behind a sequence's last."""
-        import torch
-        c, device = self.cfg, _device()
-        _expect(q, "q", torch.float16, (len(seqs), c.n_q_heads, c.head_dim), device)
+        n, (hq, hkv, d), device = len(seqs), self._heads, _device()
+        _expect(q, "q", _torch.float16, (n, hq, d), device)
         if out is None:
-            cols = max((self.counts(s)[0] // c.group for s in seqs), default=0)
-            out = _new((len(seqs), c.n_kv_heads, cols), torch.float32, q.device, stream)
+            cols = max((self.counts(s)[0] // self.cfg.group for s in seqs), default=0)
+            out = _new((n, hkv, cols), _torch.float32, q.device, stream)
         else:
-            _expect(out, "out", torch.float32, (len(seqs), c.n_kv_heads, out.shape[-1]), device)
-        kivi_paged_block_scores(self.handle, seqs, q.data_ptr(), softmax_scale, out.data_ptr(), out.shape[-1],
-                                _raw_stream(stream, device))
+            cols = out.shape[-1]
+            _expect(out, "out", _torch.float32, (n, hkv, cols), device)
+        _check(lib.kivi_paged_block_scores(self.handle, _seq_array(seqs), n, q.data_ptr(), softmax_scale, out.data_ptr(),
+                                           cols, _current_stream(device) if stream is None else stream.cuda_stream))
         return out
 
     def decode_blocks(self, seqs, q, blocks, out=None, softmax_scale=0.0, stream=None):
         """KiviCache.decode_blocks for the listed sequences: blocks int32 [n, Hkv, m]."""
-        import torch
-        c, device = self.cfg, _device()
-        shape = (len(seqs), c.n_q_heads, c.head_dim)
-        _expect(q, "q", torch.float16, shape, device)
-        _expect(blocks, "blocks", torch.int32, (len(seqs), c.n_kv_heads, blocks.shape[-1]), device)
+        n, (hq, hkv, d), device, m = len(seqs), self._heads, _device(), blocks.shape[-1]
+        _expect(q, "q", _torch.float16, (n, hq, d), device)
+        _expect(blocks, "blocks", _torch.int32, (n, hkv, m), device)
         if out is None:
-            out = _new(shape, torch.float16, q.device, stream)
+            out = _new((n, hq, d), _torch.float16, q.device, stream)
         else:
-            _expect(out, "out", torch.float16, shape, device)
-        kivi_paged_decode_blocks(self.handle, seqs, q.data_ptr(), blocks.data_ptr(), blocks.shape[-1], out.data_ptr(),
-                                 softmax_scale, _raw_stream(stream, device))
+            _expect(out, "out", _torch.float16, (n, hq, d), device)
+        _check(lib.kivi_paged_decode_blocks(self.handle, _seq_array(seqs), n, q.data_ptr(), blocks.data_ptr(), m,
+                                            out.data_ptr(), softmax_scale,
+                                            _current_stream(device) if stream is None else stream.cuda_stream))
         return out
 
     def sparse_decode(self, seqs, q, n_keep, keep_first=1, out=None, softmax_scale=0.0, stream=None):
         """KiviCache.sparse_decode for the listed sequences."""
-        import torch
         seqs = list(seqs)
-        with torch.cuda.stream(stream):
+        with _torch.cuda.stream(stream):
             scores = self.block_scores(seqs, q, softmax_scale=softmax_scale)
             n_keep = min(n_keep, scores.shape[-1])
             blocks = select_blocks(scores, n_keep, min(keep_first, n_keep))
