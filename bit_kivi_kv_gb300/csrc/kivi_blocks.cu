@@ -287,12 +287,16 @@ __global__ void __launch_bounds__(32 * kWarpRows) select_blocks_warp_kernel(cons
 
 // Longer rows: one CTA each.  The keys between two bounds that hold the wanted
 // one are counted in 2048 equal bins of the range that they span; the bin of
-// the wanted key is the next range.  Two rounds for ordinary scores, three at
-// most; a row of equal scores needs none.  Keys stay in registers, or are read
-// again each time in rows of more than 16384 columns.  Warps own consecutive
-// columns.
-constexpr int kSelectItems = 16;
+// the wanted key is the next range, and once it holds few keys each of them is
+// ranked against the others.  One round for ordinary scores, three at most; a
+// row of equal scores needs none (64 x 4092: rounds alone 8.0 us, so 6.2).  The columns
+// that are always kept stay out of the range.  Keys stay in shared memory (in
+// registers every pass over them has to be unrolled, and code that runs once
+// costs its way into the instruction cache: 64 x 4092 7.0 us), or are read again
+// each time in rows of more than 8192 columns.  Warps own consecutive columns.
+constexpr int kHeldKeys = 8192;      // 32 KB, beside 9 KB of counts: no opt-in to more shared memory
 constexpr int kBins = 2048;
+constexpr int kRanked = 128;         // keys of a bin that are ranked, at most: four a lane
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) select_blocks_kernel(const SelectArgs a) {
@@ -301,7 +305,9 @@ __global__ void __launch_bounds__(THREADS) select_blocks_kernel(const SelectArgs
     __shared__ int hist[kBins];
     __shared__ uint32_t lo_s[kW], hi_s[kW];
     __shared__ int n_s[kW], m_s[kW];
-    __shared__ uint32_t found_bin;
+    __shared__ __align__(16) uint32_t list[kRanked];
+    __shared__ uint32_t found_bin, found_key;
+    __shared__ int a_s[kW], e_s[kW];
     __shared__ int found_above, found_count;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddepcontrol_wait();
@@ -311,42 +317,58 @@ __global__ void __launch_bounds__(THREADS) select_blocks_kernel(const SelectArgs
     const int cols = (int)a.cols, K = a.n_keep;
     const int items = (cols + THREADS - 1) / THREADS;      // per thread, 32 apart
     const long long c0 = (long long)warp * items * 32 + lane;
-    const bool held = items <= kSelectItems;
+    const bool held = cols <= kHeldKeys;
+    extern __shared__ uint32_t keys[];                     // [items * THREADS] if held; a thread reads its own
     auto load = [&](long long c) { return c < cols ? score_key(row[c], c < a.keep_first) : 0u; };
-    uint32_t key[kSelectItems];
+    if (held) {
+        for (int j0 = 0; j0 < items; j0 += 8) {            // eight loads in flight
+            float x[8];
 #pragma unroll
-    for (int j = 0; j < kSelectItems; ++j) key[j] = held && j < items ? load(c0 + 32 * j) : 0u;
+            for (int j = 0; j < 8; ++j) {
+                const int c = (int)c0 + 32 * (j0 + j);
+                x[j] = j0 + j < items && c < cols ? row[c] : -INFINITY;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = (int)c0 + 32 * (j0 + j);
+                if (j0 + j < items) keys[c] = score_key(x[j], c < a.keep_first);
+            }
+        }
+    }
     auto each = [&](auto f) {                              // f(key, column) of this thread's columns, in order
         if (held) {
-#pragma unroll
-            for (int j = 0; j < kSelectItems; ++j)
-                if (j < items) f(key[j], c0 + 32 * j);
+#pragma unroll 4
+            for (int j = 0; j < items; ++j) f(keys[(int)c0 + 32 * j], (int)c0 + 32 * j);
         } else {
-            for (int j = 0; j < items; ++j) f(load(c0 + 32LL * j), c0 + 32LL * j);
+            for (int j = 0; j < items; ++j) f(load(c0 + 32LL * j), (int)(c0 + 32LL * j));
         }
     };
     // the wanted key is among those in [lo, hi]: `above` keys are greater than hi
-    uint32_t lo = 1u, hi = 0xffffffffu;
+    uint32_t lo = 1u, hi = 0xfffffffeu;
     int above = 0, valid = 0;
     uint32_t t = 1u;
+    if (tid < kRanked) list[tid] = 0u;
     for (int round = 0;; ++round) {
         // the span of the keys left, and (first round) how many there are
         uint32_t least = 0xffffffffu, most = 0u;
-        int n = 0;
-        each([&](uint32_t k, long long) {
+        int n = 0, always = 0;
+        each([&](uint32_t k, int) {
             if (k >= lo && k <= hi) {
                 least = min(least, k);
                 most = max(most, k);
                 ++n;
             }
+            always += k == 0xffffffffu;
         });
         least = __reduce_min_sync(kFull, least);
         most = __reduce_max_sync(kFull, most);
         n = __reduce_add_sync(kFull, n);
+        if (round == 0) always = __reduce_add_sync(kFull, always);
         if (lane == 0) {
             lo_s[warp] = least;
             hi_s[warp] = most;
             n_s[warp] = n;
+            if (round == 0) m_s[warp] = always;
         }
         for (int j = tid; j < kBins; j += THREADS) hist[j] = 0;
         __syncthreads();
@@ -354,15 +376,20 @@ __global__ void __launch_bounds__(THREADS) select_blocks_kernel(const SelectArgs
         most = __reduce_max_sync(kFull, lane < kW ? hi_s[lane] : 0u);
         n = __reduce_add_sync(kFull, lane < kW ? n_s[lane] : 0);
         if (round == 0) {
-            valid = n;
+            above = __reduce_add_sync(kFull, lane < kW ? m_s[lane] : 0);
+            valid = n + above;
             if (valid <= K) break;                         // everything that may be taken
+            if (above >= K) {                              // the always kept ones fill the places
+                t = 0xffffffffu;
+                break;
+            }
         }
         lo = least;
         hi = most;
         t = lo;
         if (above + n == K || lo == hi) break;             // all of them, or equal ones
         const int shift = max(0, 21 - __clz(hi - lo));     // (hi - lo) >> shift < 2048
-        each([&](uint32_t k, long long) {
+        each([&](uint32_t k, int) {
             if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> shift], 1);
         });
         __syncthreads();
@@ -397,31 +424,63 @@ __global__ void __launch_bounds__(THREADS) select_blocks_kernel(const SelectArgs
         lo = lo + (found_bin << shift);
         t = lo;
         if (shift == 0 || above + found_count == K) break;
+        if (found_count <= kRanked) {
+            // the bin's keys into a list; each is ranked by a warp, whose lanes hold
+            // four of the list's keys each (places past the last hold 0, less than any)
+            // (their places from the warps' counts: atomics on one address take turns)
+            const int c = found_count;
+            int mine_n = 0;
+            each([&](uint32_t k, int) { mine_n += k >= lo && k <= hi; });
+            mine_n = __reduce_add_sync(kFull, mine_n);
+            if (lane == 0) a_s[warp] = mine_n;
+            __syncthreads();
+            int at = __reduce_add_sync(kFull, lane < warp ? a_s[lane] : 0);
+            if (mine_n)
+                each([&](uint32_t k, int) {
+                    const bool in = k >= lo && k <= hi;
+                    const uint32_t m = __ballot_sync(kFull, in);
+                    if (in) list[at + __popc(m & ((1u << lane) - 1u))] = k;
+                    at += __popc(m);
+                });
+            __syncthreads();
+            const uint4 x = *reinterpret_cast<const uint4*>(&list[4 * lane]);
+            for (int j = warp; j < c; j += kW) {
+                const uint32_t mine = list[j];
+                // greater keys in the low half, equal ones in the high half (both at most 128)
+                const int n = (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine) +
+                              (((x.x == mine) + (x.y == mine) + (x.z == mine) + (x.w == mine)) << 16);
+                const int r = __reduce_add_sync(kFull, n);
+                const int greater = above + (r & 0xffff);
+                if (lane == 0 && greater < K && greater + (r >> 16) >= K) found_key = mine;
+            }
+            __syncthreads();
+            t = found_key;
+            break;
+        }
     }
     const int take = min(valid, K);
     int na = 0, ne = 0;
-    each([&](uint32_t k, long long) {
+    each([&](uint32_t k, int) {
         na += k > t;
         ne += k == t;
     });
     na = __reduce_add_sync(kFull, na);
     ne = __reduce_add_sync(kFull, ne);
-    __syncthreads();
     if (lane == 0) {
-        n_s[warp] = na;
-        m_s[warp] = ne;
+        a_s[warp] = na;
+        e_s[warp] = ne;
     }
     __syncthreads();
-    const int wa = lane < kW ? n_s[lane] : 0, we = lane < kW ? m_s[lane] : 0;
+    const int wa = lane < kW ? a_s[lane] : 0, we = lane < kW ? e_s[lane] : 0;
     const int ties = take - __reduce_add_sync(kFull, wa);
     int before_a = __reduce_add_sync(kFull, lane < warp ? wa : 0);
     int before_e = __reduce_add_sync(kFull, lane < warp ? we : 0);
     const uint32_t below = (1u << lane) - 1u;
-    each([&](uint32_t k, long long c) {
+    each([&](uint32_t k, int c) {
         const uint32_t ma = __ballot_sync(kFull, k > t), me = __ballot_sync(kFull, k == t);
         if ((ma | me) == 0u) return;
         const int ra = before_a + __popc(ma & below), re = before_e + __popc(me & below);
-        if (k > t || (k == t && re < ties)) out[ra + min(re, ties)] = (int)c;
+        if (k > t || (k == t && re < ties)) out[ra + min(re, ties)] = c;
         before_a += __popc(ma);
         before_e += __popc(me);
     });
@@ -473,18 +532,32 @@ cudaError_t launch_block_scores(const BlockRows& r, const __half* q, float scale
     return launch_scores<true>(a, r, st);
 }
 
+static cudaError_t launch_select(void (*kernel)(const SelectArgs), int threads, const SelectArgs& a, cudaStream_t st) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3((unsigned)a.rows);
+    lc.blockDim = dim3((unsigned)threads);
+    lc.dynamicSmemBytes = a.cols <= kHeldKeys ? (size_t)((a.cols + threads - 1) / threads) * threads * 4 : 0;
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, a);
+}
+
 cudaError_t launch_select_blocks(const float* scores, long long rows, long long cols, long long ld, int n_keep,
                                  int keep_first, int* blocks, cudaStream_t st) {
     const SelectArgs a{scores, rows, cols, ld, n_keep, keep_first, blocks};
     if (cols <= 32 * kWarpItems)
         return launch_dependent(select_blocks_warp_kernel, dim3((unsigned)((rows + kWarpRows - 1) / kWarpRows)),
                                 32 * kWarpRows, st, a);
-    const dim3 grid((unsigned)rows);
-    // 8 to 16 keys a thread: more threads wait longer at each barrier, fewer count
-    // longer (64 x 4092: 256 threads 8.9 us, 512 8.0, 1024 9.0)
-    if (cols <= 128 * kSelectItems) return launch_dependent(select_blocks_kernel<256>, grid, 256, st, a);
-    if (cols <= 512 * kSelectItems) return launch_dependent(select_blocks_kernel<512>, grid, 512, st, a);
-    return launch_dependent(select_blocks_kernel<1024>, grid, 1024, st, a);
+    // 4 to 8 keys a thread: fewer threads take longer over their keys, more wait
+    // longer at the barriers and leave room for fewer rows (64 and 512 rows of 4092:
+    // 256 threads 8.0, 18.8 us; 512: 6.2, 14.8; 1024: 6.3, 20.9; 64 x 8000: 512 8.7, 1024 7.4)
+    if (cols <= 1024) return launch_select(select_blocks_kernel<256>, 256, a, st);
+    if (cols <= 4096) return launch_select(select_blocks_kernel<512>, 512, a, st);
+    return launch_select(select_blocks_kernel<1024>, 1024, a, st);
 }
 
 cudaError_t launch_decode_blocks(const BlockRows& r, const __half* q, const int* list, int n_list, float scale_log2,

@@ -127,7 +127,8 @@ IDS = [f"D{c[0]}b{c[1]}nq{c[2]}G{c[3]}" for c in COMBOS]
 @pytest.mark.parametrize("rows,cols,keep,first", [
     (1, 1, 1, 0), (1, 1, 1, 1), (3, 5, 5, 0), (3, 5, 8, 2), (7, 31, 4, 1), (5, 32, 31, 0), (4, 33, 16, 4),
     (256, 124, 32, 1), (64, 257, 100, 3), (9, 1000, 1, 0), (9, 1023, 1023, 0), (3, 4092, 128, 1), (2, 8192, 512, 2),
-    (2, 8193, 77, 0), (2, 20011, 3000, 5), (1, 70000, 64, 1), (600, 40, 8, 8)])
+    (2, 8193, 77, 0), (2, 20011, 3000, 5), (1, 70000, 64, 1), (600, 40, 8, 8), (5, 2000, 300, 300), (3, 9500, 128, 1),
+    (2, 12000, 200, 2), (2, 16384, 16384, 0), (40, 700, 130, 129)])
 def test_select_against_sort(rows, cols, keep, first):
     """Spread values, many equal values, masked tails, special values, in every row layout."""
     g = np.random.default_rng(rows * 1000003 + cols)
@@ -162,6 +163,21 @@ def test_select_strided_rows_and_odd_offsets():
     assert select_blocks(three, 0).shape == (4, 3, 0)
     empty = select_blocks(torch.empty(5, 0, device="cuda"), 3)
     assert (empty == -1).all()
+
+
+def test_select_crowded_bins():
+    """Rows whose wanted score sits among many near ones: bins that hold more keys than
+    are ranked, ranges that shrink by rounds, outliers that stretch the first range."""
+    g = np.random.default_rng(9)
+    rows = [np.concatenate([np.full(2, 3e38), 5 + 1e-4 * g.random(4000), np.full(98, -3e38)]),
+            np.concatenate([np.full(50, 7.0), 5 + 1e-6 * g.integers(0, 3, 4050)]),
+            5 + 1e-6 * g.random(4100), np.concatenate([-g.random(2000) * 1e-30, g.random(2100) * 1e-30]),
+            np.concatenate([np.full(4000, 1.0), np.full(100, np.inf)])]
+    s = np.stack([g.permutation(r) for r in rows]).astype(np.float32)
+    for cols in (4100, 600, 200):
+        for keep in (1, 60, 150):
+            got = select_blocks(torch.from_numpy(s[:, :cols].copy()).cuda(), keep, 1)
+            assert np.array_equal(got.cpu().numpy(), ref_select(s[:, :cols], keep, 1)), (cols, keep)
 
 
 def test_select_bits_that_differ_low_down():
