@@ -4,6 +4,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <mutex>
+
 #include "kivi_decode_blocks.cuh"
 
 namespace kivi {
@@ -293,8 +295,9 @@ __global__ void __launch_bounds__(32 * kWarpRows) select_blocks_warp_kernel(cons
 // that are always kept stay out of the range.  Keys stay in shared memory (in
 // registers every pass over them has to be unrolled, and code that runs once
 // costs its way into the instruction cache: 64 x 4092 7.0 us), or are read again
-// each time in rows of more than 8192 columns.  Warps own consecutive columns.
-constexpr int kHeldKeys = 8192;      // 32 KB, beside 9 KB of counts: no opt-in to more shared memory
+// each time in rows of more than 49152 columns.  Warps own consecutive columns.
+constexpr int kHeldKeys = 49152;
+constexpr int kPlainKeys = 8192;     // 32 KB, beside 9 KB of counts: no opt-in to more shared memory
 constexpr int kBins = 2048;
 constexpr int kRanked = 128;         // keys of a bin that are ranked, at most: four a lane
 
@@ -537,6 +540,21 @@ static cudaError_t launch_select(void (*kernel)(const SelectArgs), int threads, 
     lc.gridDim = dim3((unsigned)a.rows);
     lc.blockDim = dim3((unsigned)threads);
     lc.dynamicSmemBytes = a.cols <= kHeldKeys ? (size_t)((a.cols + threads - 1) / threads) * threads * 4 : 0;
+    if (lc.dynamicSmemBytes > 4 * kPlainKeys) {
+        // (only the kernel of the longest rows; once per device)
+        static std::mutex mu;
+        static bool set_up[64];
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!set_up[dev]) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kHeldKeys);
+            if (e != cudaSuccess) return e;
+            set_up[dev] = true;
+        }
+    }
     lc.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -128,7 +128,7 @@ IDS = [f"D{c[0]}b{c[1]}nq{c[2]}G{c[3]}" for c in COMBOS]
     (1, 1, 1, 0), (1, 1, 1, 1), (3, 5, 5, 0), (3, 5, 8, 2), (7, 31, 4, 1), (5, 32, 31, 0), (4, 33, 16, 4),
     (256, 124, 32, 1), (64, 257, 100, 3), (9, 1000, 1, 0), (9, 1023, 1023, 0), (3, 4092, 128, 1), (2, 8192, 512, 2),
     (2, 8193, 77, 0), (2, 20011, 3000, 5), (1, 70000, 64, 1), (600, 40, 8, 8), (5, 2000, 300, 300), (3, 9500, 128, 1),
-    (2, 12000, 200, 2), (2, 16384, 16384, 0), (40, 700, 130, 129)])
+    (2, 12000, 200, 2), (2, 16384, 16384, 0), (3, 32768, 512, 1), (2, 49152, 40, 0), (2, 49153, 40, 1), (40, 700, 130, 129)])
 def test_select_against_sort(rows, cols, keep, first):
     """Spread values, many equal values, masked tails, special values, in every row layout."""
     g = np.random.default_rng(rows * 1000003 + cols)
