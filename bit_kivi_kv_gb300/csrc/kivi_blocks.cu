@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lb = lane % LPB, sub = lane / LPB;
     const long long row = blockIdx.y;
-    const int b = (int)(row / a.Hkv), hk = (int)(row % a.Hkv);
+    const int b = (int)blockIdx.y / a.Hkv, hk = (int)blockIdx.y % a.Hkv;
     int nblk = a.n_blocks;
     if constexpr (PAGED) nblk = a.seqs[b].n_blocks;
     griddepcontrol_wait();
