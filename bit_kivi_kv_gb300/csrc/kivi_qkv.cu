@@ -245,8 +245,8 @@ kivi_status check_qkv(const kivi_qkv* a) {
     if (a->n_q_heads < 1 || a->n_kv_heads < 1) return failf(KIVI_ERR_INVALID_ARG, "head counts must be positive");
     if (a->head_dim != 64 && a->head_dim != 128) return failf(KIVI_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
     if (a->n_q_heads > 8192 || a->n_kv_heads > 8192) return failf(KIVI_ERR_UNSUPPORTED, "head counts must be <= 8192");
-    if (a->batch > 0 && a->n_tokens > (1LL << 33) / a->batch)
-        return failf(KIVI_ERR_UNSUPPORTED, "batch * n_tokens must be <= 2^33");
+    if (a->batch > 0 && a->n_tokens > (1LL << 32) / a->batch)
+        return failf(KIVI_ERR_UNSUPPORTED, "batch * n_tokens must be <= 2^32");
     if (a->dtype != KIVI_F16 && a->dtype != KIVI_BF16 && a->dtype != KIVI_F32)
         return failf(KIVI_ERR_INVALID_ARG, "unknown input type %d", a->dtype);
     if (a->batch > 0 && a->n_tokens > 0 && !a->q && !a->k && !a->v)   // (empty tensors have null addresses)
