@@ -37,7 +37,8 @@ struct InstanceSetup {
 // warps again (256 rows of 32 blocks: 1 x 8 warps 11.6 us, 2 x 4 12.9); once
 // there is one, more and smaller CTAs spread over more SMs (64 rows of 128
 // blocks: 2 x 16 warps 12.5 us, 4 x 8 11.7, 8 x 4 11.7).  Where no shape gives a
-// row two warps, CTAs of four warps in several waves.
+// row two warps, CTAs of up to four warps in several waves; a row with nothing
+// to read still has a warp, which writes its outputs.
 struct Shape { int ctas, warps; };
 inline Shape row_shape(long long rows, long long units, int num_sms, const SmRoom& room) {
     Shape best{1, 0};
@@ -48,8 +49,10 @@ inline Shape row_shape(long long rows, long long units, int num_sms, const SmRoo
         if (w >= 1 && (most == 0 || (best.ctas == 1 ? 2 * n >= 3 * most : n >= most && w >= 4)))
             best = Shape{c, (int)w};
     }
-    if (best.ctas * best.warps < 2 && units >= 2)
-        best = Shape{1, (int)SmRoom::min2(SmRoom::min2(units, 4), room.warps(1))};
+    if (best.ctas * best.warps < 2) {
+        const long long w = SmRoom::min2(SmRoom::min2(units, 4), room.warps(1));
+        best = Shape{1, w < 1 ? 1 : (int)w};
+    }
     return best;
 }
 

@@ -295,6 +295,28 @@ def test_row_counts(B, Hkv, nq, bits, G, L, keep):
     check_scores(cache.block_scores(q), some, q, bits, Hkv, nq)
 
 
+@pytest.mark.parametrize("B,Hkv,nq,D,L", [(330, 8, 1, 64, 5), (90, 32, 2, 128, 40), (1040, 63, 1, 64, 16)])
+def test_many_rows_with_one_tile_each(B, Hkv, nq, D, L):
+    """Thousands of rows that have at most one residual tile to read: more rows
+    than the SMs hold warps, none with work for two of them."""
+    cache, oc, q = dense(B, Hkv * nq, Hkv, D, 2, 32, 32, L, B)
+    some = {r: oc[r] for r in [(0, 0), (B // 2, Hkv // 3), (B - 1, Hkv - 1)]}
+    nothing = torch.empty(B, Hkv, 0, dtype=torch.int32, device="cuda")
+    got = cache.decode_blocks(q, nothing, out=cache.bands.like(q))
+    cache.bands.check("after a decode of one tile a row")
+    check_decode(got, some, q, nothing.cpu().numpy(), 32, nq)
+
+
+def test_many_paged_rows_with_one_tile_each():
+    lengths = [1 + i % 16 for i in range(46)]
+    cache, seqs, oc, q = paged(lengths, 64, 64, 64, 2, 32, 32, 31)
+    none = np.full((46, 64, 2), -1, np.int32)
+    got = cache.decode_blocks(seqs, q, torch.from_numpy(none).cuda())
+    cache.bands.check("after a paged decode of one tile a row")
+    some = {r: oc[r] for r in [(0, 0), (15, 63), (30, 7), (45, 40)]}
+    check_decode(got, some, q, none, 32, 1)
+
+
 def test_offsets_past_4_gib():
     """A dense cache and a page pool of more than 4 GiB: the last rows' blocks, scores and tables."""
     B, H, D, bits, G, R, L = 8, 32, 128, 8, 32, 32, 60000
