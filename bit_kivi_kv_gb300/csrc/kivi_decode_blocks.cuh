@@ -644,6 +644,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     static_assert(NQ * D == 1 << kOutShift, "outputs of a row");
     const int span = NQ * D >> cshift;            // the outputs a CTA of the cluster writes
     __half* out = a.out + ((long long)b * a.Hq + hk * NQ) * D;
+    __syncwarp();                                 // (the cluster's barrier wants whole warps)
     if (csize > 1) cluster_wait();                // (every CTA has started: its shared memory may be written)
     __syncthreads();
     for (int base = 32 * warp; base < NQ * D; base += blockDim.x) {
