@@ -31,25 +31,44 @@ struct InstanceSetup {
     SmRoom room[kMaxDevices];
 };
 
-// A row's CTAs (a power of two, at most 8: a cluster) and their warps: the shape
-// with the most warps per row among those whose whole grid is resident at
-// once.  A cluster costs about 1 us of merging, so it has to bring half as many
-// warps again (256 rows of 32 blocks: 1 x 8 warps 11.6 us, 2 x 4 12.9); once
-// there is one, more and smaller CTAs spread over more SMs (64 rows of 128
-// blocks: 2 x 16 warps 12.5 us, 4 x 8 11.7, 8 x 4 11.7).  Where no shape gives a
-// row two warps, CTAs of up to four warps in several waves; a row with nothing
-// to read still has a warp, which writes its outputs.
+// A row's CTAs (a power of two, at most 8: a cluster) and their warps, of the
+// shapes whose whole grid is resident at once.  Each is charged with the units
+// (tile pairs and residual tiles) of a warp, the mean of the busiest one's and
+// of an even split, and a cluster with what its merge costs besides: 0.7 unit,
+// 0.9 with four query heads, whose merge is larger.  (256 rows of 32 blocks: 1 x 8
+// warps 11.6 us, 2 x 4 12.9; 192 rows of 128 blocks: 1 x 8 29.5, 2 x 5 25.9; 32
+// rows of 16 blocks at head_dim 64: 1 x 16 4.9, 4 x 6 3.9; four query heads, 64
+// rows of 2 blocks of 128: 1 x 12 6.2, 2 x 8 7.2.)  Of clusters that cost the
+// same, the one with more warps, then the one with smaller CTAs, which spread
+// over more SMs (64 rows of 128 blocks: 2 x 16 warps 12.5 us, 4 x 8 11.7).
+//
+// Small CTAs are placed unevenly while the kernel before still runs, if an SM
+// holds more of them than its share: where that leaves a row of 64 KB and more
+// two warps, and wherever it leaves one, CTAs of up to four warps in several
+// waves (768 rows of 128 blocks: 2 warps 103.4 us, 4 in waves 84.1; with 4 bits
+// 127.2 and 97.6, 8 bits at 512 rows 74.8 and 63.7; but 1024 rows of 8 blocks
+// 20.1 and 21.8; with three warps, 640 rows, 71.6 and 77.3; no room for more, 8
+// bits at 640 rows, 76.0 and 85.8).  A row with nothing to read still has a warp,
+// which writes its outputs.
 struct Shape { int ctas, warps; };
-inline Shape row_shape(long long rows, long long units, int num_sms, const SmRoom& room) {
+inline Shape row_shape(long long rows, long long units, int num_sms, const SmRoom& room, int nq,
+                       long long row_bytes) {
     Shape best{1, 0};
+    long long least = 0;                 // in 1/20 of a unit
+    auto share = [&](int c) { return (rows * c + num_sms - 1) / num_sms; };   // CTAs of an SM
     for (int c = 1; c <= blocks_detail::kMaxCluster; c *= 2) {
-        long long w = room.warps((rows * c + num_sms - 1) / num_sms);
+        long long w = room.warps(share(c));
         if (w * c > units) w = (units + c - 1) / c;
+        if (w < 1) continue;
         const long long n = w * c, most = (long long)best.ctas * best.warps;
-        if (w >= 1 && (most == 0 || (best.ctas == 1 ? 2 * n >= 3 * most : n >= most && w >= 4)))
+        const long long t = 10 * ((units + n - 1) / n) + 10 * units / n + (c == 1 ? 0 : nq == 4 ? 18 : 14);
+        if (most == 0 || t < least || (t == least && best.ctas > 1 && (n > most || (n == most && w >= 4)))) {
+            least = t;
             best = Shape{c, (int)w};
+        }
     }
-    if (best.ctas * best.warps < 2) {
+    const bool uneven = row_bytes >= 65536 && room.warps(share(1) + 1) >= best.warps;
+    if (best.ctas == 1 && best.warps < (uneven ? 3 : 2)) {
         const long long w = SmRoom::min2(SmRoom::min2(units, 4), room.warps(1));
         best = Shape{1, w < 1 ? 1 : (int)w};
     }
@@ -89,7 +108,8 @@ cudaError_t launch_one(const typename blocks_detail::ArgsOf<PAGED>::type& a, lon
         }
         room = r;
     }
-    const Shape sh = row_shape(rows, units, num_sms, room);
+    // (bytes as if all units were tile pairs)
+    const Shape sh = row_shape(rows, units, num_sms, room, NN, units * 32 * a.wq);
     const int c = sh.ctas;
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3((unsigned)(rows * c));
