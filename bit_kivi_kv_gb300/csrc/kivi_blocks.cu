@@ -220,12 +220,12 @@ struct SelectArgs {
 // taken; every key above t is taken, and of those equal to t the first ones in
 // index order.  A chosen column's place is the number of chosen ones before it.
 
-// Rows of up to 256 columns: one warp each, its keys in registers, no
-// barriers.  t is found by bisection on its bits, highest first, each step one
-// count over the warp, until as many keys as wanted are at least t.
-constexpr int kWarpItems = 8;
+// Rows of up to 256 columns, and many of up to 1024: one warp each, its keys in
+// registers, no barriers.  t is found by bisection on its bits, highest first,
+// each step one count over the warp, until as many keys as wanted are at least t.
 constexpr int kWarpRows = 4;         // rows (warps) per CTA
 
+template <int kWarpItems>            // keys a lane
 __global__ void __launch_bounds__(32 * kWarpRows) select_blocks_warp_kernel(const SelectArgs a) {
     const int lane = threadIdx.x & 31;
     const long long r = (long long)blockIdx.x * kWarpRows + (threadIdx.x >> 5);
@@ -567,9 +567,15 @@ static cudaError_t launch_select(void (*kernel)(const SelectArgs), int threads, 
 cudaError_t launch_select_blocks(const float* scores, long long rows, long long cols, long long ld, int n_keep,
                                  int keep_first, int* blocks, cudaStream_t st) {
     const SelectArgs a{scores, rows, cols, ld, n_keep, keep_first, blocks};
-    if (cols <= 32 * kWarpItems)
-        return launch_dependent(select_blocks_warp_kernel, dim3((unsigned)((rows + kWarpRows - 1) / kWarpRows)),
-                                32 * kWarpRows, st, a);
+    const dim3 by_warp((unsigned)((rows + kWarpRows - 1) / kWarpRows));
+    if (cols <= 256) return launch_dependent(select_blocks_warp_kernel<8>, by_warp, 32 * kWarpRows, st, a);
+    // many rows of up to 1024 columns too: the CTAs of two rows an SM take turns
+    // (400 columns, CTA and warp a row: 256 rows 4.5, 5.0 us, 512 rows 8.1, 5.0, 2048
+    // rows 16.7, 7.9; 800 columns: 5.6, 8.0 and 10.6, 8.1 and 21.9, 19.1)
+    if (rows >= 384 && cols <= 512)
+        return launch_dependent(select_blocks_warp_kernel<16>, by_warp, 32 * kWarpRows, st, a);
+    if (rows >= 384 && cols <= 1024)
+        return launch_dependent(select_blocks_warp_kernel<32>, by_warp, 32 * kWarpRows, st, a);
     // 4 to 8 keys a thread: fewer threads take longer over their keys, more wait
     // longer at the barriers and leave room for fewer rows (64 and 512 rows of 4092:
     // 256 threads 8.0, 18.8 us; 512: 6.2, 14.8; 1024: 6.3, 20.9; 64 x 8000: 512 8.7, 1024 7.4)

@@ -150,6 +150,14 @@ def test_select_against_sort(rows, cols, keep, first):
     assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("rows,cols,keep,first", [
+    (384, 257, 30, 1), (383, 300, 30, 1), (401, 511, 511, 0), (390, 512, 64, 64), (385, 513, 1, 1), (402, 800, 799, 2),
+    (400, 1023, 128, 1), (387, 1024, 900, 0), (386, 1025, 100, 3)])
+def test_select_many_rows(rows, cols, keep, first):
+    """Rows of a warp's 16 and 32 keys a lane, and the sizes beside them."""
+    test_select_against_sort(rows, cols, keep, first)
+
+
 def test_select_strided_rows_and_odd_offsets():
     g = torch.Generator(device="cuda").manual_seed(3)
     big = torch.randn(11, 301, generator=g, device="cuda")
