@@ -158,10 +158,11 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     using S = Smem<D, BITS, NQ, G>;
     constexpr int KS = C::KSTEPS, W = C::W, NGRP = C::NGRP, GB = C::GB, NBF = C::NBF;
     constexpr int PPB = C::TPB / 2;                   // tile pairs per block
-    // the row's scaled query (fp32) and the fp16 hi / lo parts of it times the
-    // code scale 2^-(BITS*pos), shared by the CTA's warps
+    // the row's scaled query times 2^query_exponent (fp32), and the fp16 hi / lo parts
+    // of it times the code scale 2^-(BITS*pos), shared by the CTA's warps
     __shared__ __align__(16) float qf[NQ][D];
     __shared__ uint32_t qhc_s[NQ][D / 2], qlc_s[NQ][D / 2];
+    __shared__ float qunit_s[NQ];                 // 2^-query_exponent
     __shared__ __align__(8) uint64_t full_bar[kMaxRowWarps][C::STAGES];
     // the residual's query: fp16 hi and lo parts of each head, a padded row each
     __shared__ __align__(16) __half qres[2 * NQ][D + 8];
@@ -342,38 +343,51 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         }
         __syncwarp();
     };
-    // channel pair idx of the query (volatile: on its way while the list is read)
+    // a lane's channel pairs (D / 64 of them) of query head j, one warp a head
+    // (volatile: on its way while the list is read)
     const __half* qp = a.q + ((long long)b * a.Hq + hk * NQ) * D;
-    auto query = [&](int idx) {
-        uint32_t x = 0u;
-        if (idx < NQ * D / 2) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(x) : "l"(qp + 2 * idx));
-        return x;
+    constexpr int CPL = D / 64;
+    auto query = [&](int j, uint32_t (&x)[CPL]) {
+        const __half* p = qp + j * D + 2 * CPL * lane;
+        if constexpr (CPL == 2) asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[CPL - 1]) : "l"(p));
+        else asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(x[0]) : "l"(p));
     };
-    const uint32_t qv = query(tid);
+    uint32_t qv[CPL] = {};
+    if (warp < NQ) query(warp, qv);
     if (k < we) {
         read_part();
         begin_part();
     }
-    for (int idx = tid; idx < NQ * D / 2; idx += blockDim.x) {
-        const int j = idx / (D / 2), cp = idx % (D / 2);
-        const float2 f = unpack_f16x2(idx == tid ? qv : query(idx));
-        const float x0 = f.x * a.scale_log2, x1 = f.y * a.scale_log2;
-        qf[j][2 * cp] = x0;
-        qf[j][2 * cp + 1] = x1;
-        const uint32_t hi = pack_f16x2(x0, x1);
-        const float2 hf = unpack_f16x2(hi);
-        *reinterpret_cast<uint32_t*>(&qres[2 * j][2 * cp]) = hi;
-        *reinterpret_cast<uint32_t*>(&qres[2 * j + 1][2 * cp]) = pack_f16x2(x0 - hf.x, x1 - hf.y);
-        // channels 2cp, 2cp+1 have class cp / 4: their codes read as code * 2^(BITS*pos - 24)
-        const float cs = pow2i(-BITS * ((cp >> 2) % (8 / BITS)));
-        const float y0 = x0 * cs, y1 = x1 * cs;
-        const uint32_t hic = pack_f16x2(y0, y1);
-        const float2 hcf = unpack_f16x2(hic);
-        qhc_s[j][cp] = hic;
-        qlc_s[j][cp] = pack_f16x2(y0 - hcf.x, y1 - hcf.y);
+    for (int j = warp; j < NQ; j += warps) {
+        if (j != warp) query(j, qv);
+        const uint32_t most = max(abs_max_f16x2(qv[0]), abs_max_f16x2(qv[CPL - 1]));
+        const int ex = query_exponent(unpack_f16x2(__reduce_max_sync(kFull, most)).x * a.scale_log2);
+        if (lane == 0) qunit_s[j] = pow2i(-ex);
+#pragma unroll
+        for (int u = 0; u < CPL; ++u) {
+            const int cp = CPL * lane + u;
+            const float2 f = unpack_f16x2(qv[u]);
+            const float x0 = f.x * a.scale_log2 * pow2i(ex), x1 = f.y * a.scale_log2 * pow2i(ex);
+            qf[j][2 * cp] = x0;
+            qf[j][2 * cp + 1] = x1;
+            const uint32_t hi = pack_f16x2(x0, x1);
+            const float2 hf = unpack_f16x2(hi);
+            *reinterpret_cast<uint32_t*>(&qres[2 * j][2 * cp]) = hi;
+            *reinterpret_cast<uint32_t*>(&qres[2 * j + 1][2 * cp]) = pack_f16x2(x0 - hf.x, x1 - hf.y);
+            // channels 2cp, 2cp+1 have class cp / 4: their codes read as code * 2^(BITS*pos - 24)
+            const float cs = pow2i(-BITS * ((cp >> 2) % (8 / BITS)));
+            const float y0 = x0 * cs, y1 = x1 * cs;
+            const uint32_t hic = pack_f16x2(y0, y1);
+            const float2 hcf = unpack_f16x2(hic);
+            qhc_s[j][cp] = hic;
+            qlc_s[j][cp] = pack_f16x2(y0 - hcf.x, y1 - hcf.y);
+        }
     }
     __syncthreads();
 
+    // this lane's head: the logits' unit of the fp16 rows, and of the block at hand
+    const float qunit = qunit_s[i < NQ ? i : 0];
+    float unit = 0.f;
     float m = -INFINITY, l = 0.f;
     bool fresh = true;                            // no tile counted yet
     float o[KS][4];
@@ -392,33 +406,11 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     };
     float beta = 0.f;
 
-    // Online softmax step over two tiles: sc * unit = logits of tokens g, g+8
-    // of tile A and of tile B (head i); p receives their probabilities.  The
-    // maximum over the lanes is taken only when some lane's logit passes the
-    // running one, which happens ever more rarely.
-    auto softmax = [&](const float (&sc)[4], float (&p)[4], float unit) {
-        float mt = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])) * unit;
-        if (__any_sync(kFull, mt > m)) {
-            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 4));
-            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 8));
-            mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 16));
-            const float mn = fmaxf(m, mt);
-            if (!fresh) {                         // (before the first tiles o, zeta and l are zero)
-                const float alpha = m == mn ? 1.f : fast_exp2(m - mn);
-                l *= alpha;
-                const float ao = __shfl_sync(kFull, alpha, (lane & ~3) | (hO < NQ ? hO : 0));
-#pragma unroll
-                for (int t = 0; t < KS; ++t) { o[t][0] *= ao; o[t][1] *= ao; o[t][2] *= ao; o[t][3] *= ao; }
-                const float az = __shfl_sync(kFull, alpha, col_ok ? hP : 0);
-#pragma unroll
-                for (int f = 0; f < NBF; ++f) zeta[f] *= az;
-            }
-            m = mn;
-            fresh = false;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = fast_exp2(fmaf(sc[j], unit, -m));
-        l += (p[0] + p[1]) + (p[2] + p[3]);
+    ValueRange range;
+    KeyRange krange;
+    const int ao_lane = (lane & ~3) | (hO < NQ ? hO : 0), az_lane = col_ok ? hP : 0;
+    auto softmax = [&](const float (&sc)[4], float (&p)[4], float unit, uint32_t steps) {
+        softmax_pair(sc, p, unit, steps, range, m, l, fresh, o, zeta, ao_lane, az_lane);
     };
     // probabilities of tokens 2i, 2i+1, 2i+8, 2i+9 of head hP, and their fp16 hi / lo parts
     auto gather = [&](float p0, float p1, float (&pr)[4]) {
@@ -468,9 +460,9 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
 #pragma unroll
         for (int f = 0; f < NBF; ++f) {            // B fragments of p * step, and p . zero
             const uint2 sv = lds64(ve + 32u * GB * f), zv = lds64(ve + 32u * (NGRP + GB * f));
-            const uint32_t h01 = hmul2(ph01, sv.x), h89 = hmul2(ph89, sv.y);
-            const uint32_t l01 = hfma2(pl01, sv.x, hfma2(ph01, sv.x, neg_f16x2(h01)));
-            const uint32_t l89 = hfma2(pl89, sv.y, hfma2(ph89, sv.y, neg_f16x2(h89)));
+            uint32_t h01, h89, l01, l89;
+            product_parts(ph01, pl01, sv.x, range.grid, h01, l01);
+            product_parts(ph89, pl89, sv.y, range.grid, h89, l89);
             pb[f][0] = lo_col ? l01 : h01;
             pb[f][1] = lo_col ? l89 : h89;
             const float2 z01 = unpack_f16x2(zv.x), z89 = unpack_f16x2(zv.y);
@@ -496,7 +488,8 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
             if (first_of_block) skip = offs[k / PPB - j0] < 0;
             if (!skip) {
                 if (first_of_block)
-                    build_q_frags<C, D, NQ, QB_REGS>(stage + C::KE, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);
+                    build_q_frags<C, D, NQ, QB_REGS>(stage + C::KE, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta,
+                                                     &qunit, krange, unit, fresh);
                 float ca[4] = {0.f, 0.f, 0.f, 0.f}, cb[4] = {0.f, 0.f, 0.f, 0.f};
                 uint32_t wa[W], wc[W];
                 lds_words(stage_u32 + C::KT, wa);
@@ -517,7 +510,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
                     lds_words(stage_u32 + C::VT + C::TILE, wvh[1]);
                 }
                 float p[4];
-                softmax(sc, p, 0x1p24f);                       // scores are in units of 2^-24
+                softmax(sc, p, unit, pair_steps<C, NGRP>(stage_u32, lane));
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     uint32_t wv[W];
@@ -583,6 +576,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         m = -INFINITY;
         l = 0.f;
         fresh = true;
+        range = ValueRange{};
 #pragma unroll
         for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
         // (Prefetching the rows into L2 at the start of the call, or a few pairs
@@ -604,7 +598,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
             }
             const float sc[4] = {okg ? c[0] + c[1] : -INFINITY, okg8 ? c[2] + c[3] : -INFINITY, -INFINITY, -INFINITY};
             float p[4];
-            softmax(sc, p, 1.f);
+            softmax(sc, p, qunit, 0u);
             float prb[4];
             gather(p[0], p[1], prb);
             uint32_t ph01, ph89, pl01, pl89;

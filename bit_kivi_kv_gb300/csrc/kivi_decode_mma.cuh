@@ -25,6 +25,12 @@
 // query side once per slot and the 2^-24 into the softmax; for values it is
 // the output row, so the accumulators are rescaled once after the quantized
 // tiles.  The integer pipe, the busiest one, does one mask per code pair.
+// What subnormal codes cost is the tensor cores' alignment: they multiply without
+// normalizing, and cut a step's 16 products and running sum at 2^-25 of
+// the largest product that a code of 1024 would give, 2^-15 of the largest B
+// operand per unit of code (measured with single products).  So the hi parts are
+// rounded to multiples of that (product_parts): nothing of them is cut, and what
+// is left is in the lo parts, which are 2^-16 of the largest at most.
 // Online softmax per warp in the log2 domain.  Each warp of a persistent grid
 // owns a balanced, weight-proportional share of the call's work (tile pairs of
 // 32 tokens, then fp16 residual pairs, per (batch row, kv head) slot) and
@@ -148,6 +154,23 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// one of the two halves of a is greater than its counterpart in b (or not a number)
+__device__ __forceinline__ bool above_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("{\n .reg .pred p, q;\n setp.gtu.f16x2 p|q, %1, %2;\n or.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(d) : "r"(a), "r"(b));
+    return d != 0u;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t d;   // low 16 bits <- lo
@@ -363,6 +386,7 @@ __device__ __forceinline__ void load_tile_words(const uint8_t* p, uint32_t (&w)[
 
 template <int D, int BITS, int NQ, int G>
 struct Cfg {
+    static constexpr int BITS_ = BITS;
     static constexpr int KSTEPS = D / 16;             // k-steps (keys) = m-tiles (values)
     static constexpr int W = D * BITS / 64;           // words per lane per tile
     static constexpr int NGRP = D / G;                // value channel groups per token
@@ -384,16 +408,54 @@ struct Cfg {
     static constexpr bool WHOLE = TPB == 2;
 };
 
+// (hi + lo) * s as two fp16 parts that the MMAs add up without loss: h the
+// product rounded to a multiple of 2^-10 of the power of two `grid` (half of that
+// if the product is negative), or to its own 11 bits where those end above; l
+// what is left, to 11 bits.
+__device__ __forceinline__ void product_parts(uint32_t hi, uint32_t lo, uint32_t s, uint32_t grid, uint32_t& h,
+                                              uint32_t& l) {
+    h = hsub2(hfma2(hi, s, grid), grid);
+    l = hfma2(lo, s, hfma2(hi, s, neg_f16x2(h)));
+}
+
+// Where a query head and a block's key steps stand in fp16's range.  x = scale
+// log2(e) q is held times 2^query_exponent(max |x|), which puts the largest |x| into
+// [2^8, 2^9), as fp16 hi + lo parts times each channel's code scale (2^-6 at least):
+// both parts have all their bits, where those of |x| around 0.01 would be lost to
+// fp16's last one (against keys around 1000, logits off by 3%).  A block's steps are
+// taken times 2^-f, the largest then mostly between 16 and 64, so that the products
+// stay below 2^15 and the largest ones near it; the logits are in units of
+// 2^(24 + f - exponent).  f comes from the warp's first block, with one doubling of
+// room, and goes up when a block brings a step above 64 2^f.  The first block's
+// products are made twice, from f = -15, unless build_q_frags is told that it is
+// the first: 0.1 to 0.5 us less for calls over listed blocks, while the
+// whole-cache kernel, at its register limit, lost 1 to 3% to that.  A maximum
+// of 0, infinity or NaN gets an exponent like any other: the products are then 0
+// or NaN whatever it is.
+__device__ __forceinline__ int query_exponent(float xmax) {
+    return max(-80, min(80, 135 - (int)(__float_as_uint(xmax) >> 23 & 0xffu)));
+}
+// the larger one of two fp16 magnitudes
+__device__ __forceinline__ uint32_t abs_max_f16x2(uint32_t x) {
+    return max(x & 0x7fffu, x >> 16 & 0x7fffu);
+}
+struct KeyRange {
+    uint32_t mul = 0x78007800u;                   // 2^-f as two fp16
+    __device__ __forceinline__ uint32_t lim() const { return 0x90009000u - mul; }   // 64 2^f (2^16 and more: infinity)
+};
+
 // Build this warp's Qt B fragments (fp16 hi + lo parts of q_h * step) and
 // its beta = sum_c q_h[c] * zero_c, from the block's key steps and zeros
 // (D fp16 steps, then D fp16 zeros); entries == nullptr means step 1, zero 0
-// (the fp16 residual: the parts are split from the fp32 query qf).  qh/ql hold
+// (the fp16 residual: the parts are split from the fp32 query qf).  qf, qh and
+// ql are in units of 2^-query_exponent; qh/ql hold
 // the fp16 hi/lo parts of the scaled query per channel pair, already
-// multiplied by the channel's code scale 2^-(BITS*pos); with s exact in fp16, hi = rn(qh*s)
-// and lo = rn(ql*s + (qh*s - hi)), the inner residual exact, so hi + lo =
-// q*s to about 22 bits.  Lane l handles channel pairs CPL*l + j; off[j] is
-// the table offset of pair CPL*l + j (head 0, hi column).  With entries,
-// beta is returned times 2^-24, the unit of the masked codes.  KEEP: the
+// multiplied by the channel's code scale 2^-(BITS*pos), which the products' grid
+// (product_parts) carries too.  Lane l handles channel pairs CPL*l + j; off[j] is
+// the table offset of pair CPL*l + j (head 0, hi column).  With entries, beta is
+// returned in the unit of the masked codes' sums, and the logits of this lane's head
+// are those sums times unit = qunit 2^(24 + f), qunit = 2^-query_exponent; without,
+// unit = qunit.  KEEP: the
 // fragments are also loaded into qb; otherwise they stay in the table and the
 // MMAs read each k-step's pair from it.  Measured per instance: with one query
 // head per kv head, reading from the table (fewer registers held across the
@@ -404,7 +466,8 @@ template <class C, int D, int NQ, bool KEEP>
 __device__ __forceinline__ void build_q_frags(const uint8_t* entries, const float (*qf)[D],
                                               const uint32_t (*qh)[D / 2], const uint32_t (*ql)[D / 2],
                                               const int (&off)[D / 64], uint32_t* qfrag, int lane,
-                                              uint32_t (&qb)[2 * C::KSTEPS], float& beta) {
+                                              uint32_t (&qb)[2 * C::KSTEPS], float& beta, const float* qunit,
+                                              KeyRange& range, float& unit, bool first) {
     constexpr int CPL = D / 64;               // channel pairs per lane
     constexpr int HEAD = 8 * C::QSTRIDE;      // table distance between heads' hi columns
     constexpr int LOC = 4 * C::QSTRIDE;       // hi column -> lo column
@@ -422,22 +485,46 @@ __device__ __forceinline__ void build_q_frags(const uint8_t* entries, const floa
             sw[0] = *reinterpret_cast<const uint32_t*>(entries + 4 * lane);
             zw[0] = *reinterpret_cast<const uint32_t*>(entries + 2 * D + 4 * lane);
         }
+        // (a lane's channels are of one code class)
+        const uint32_t grid = 0x68006800u - (uint32_t)(C::BITS_ * ((CPL * lane >> 2) % (8 / C::BITS_))) * 0x04000400u;
+        auto fold = [&]() {
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                const int cp = CPL * lane + j;
+                const uint32_t st = hmul2(sw[j], range.mul);
+#pragma unroll
+                for (int h = 0; h < NQ; ++h)
+                    product_parts(qh[h][cp], ql[h][cp], st, grid, qfrag[off[j] + h * HEAD],
+                                  qfrag[off[j] + h * HEAD + LOC]);
+            }
+        };
+        const uint32_t smax = CPL == 2 ? hmax2(sw[0], sw[CPL - 1]) : sw[0];
+        auto set_range = [&]() {
+            // the largest step is below 2^(field - 14); one doubling of room
+            const int field = (int)(__reduce_max_sync(kFull, abs_max_f16x2(smax)) >> 10);
+            const int f = max(-15, min(10, field - 19));
+            range.mul = (uint32_t)(15 - f) * 0x04000400u;
+            unit = *qunit * pow2i(24 + f);
+        };
+        if (first) set_range();
+        fold();
 #pragma unroll
         for (int j = 0; j < CPL; ++j) {
-            const int cp = CPL * lane + j;
             const float2 z = unpack_f16x2(zw[j]);
 #pragma unroll
             for (int h = 0; h < NQ; ++h) {
-                const uint32_t hi = hmul2(qh[h][cp], sw[j]);
-                const uint32_t lo = hfma2(ql[h][cp], sw[j], hfma2(qh[h][cp], sw[j], neg_f16x2(hi)));
-                const float2 q2 = *reinterpret_cast<const float2*>(&qf[h][2 * cp]);
+                const float2 q2 = *reinterpret_cast<const float2*>(&qf[h][2 * (CPL * lane + j)]);
                 bp[h] = fmaf(q2.x, z.x, fmaf(q2.y, z.y, bp[h]));
-                qfrag[off[j] + h * HEAD] = hi;
-                qfrag[off[j] + h * HEAD + LOC] = lo;
             }
+        }
+        // (asked for behind the products, so that they do not wait for the answer)
+        if (__any_sync(kFull, above_f16x2(smax, range.lim()))) {
+            set_range();
+            fold();
         }
     } else {
         // the fp16 residual: hi / lo parts of the scaled query itself
+        unit = *qunit;
 #pragma unroll
         for (int j = 0; j < CPL; ++j) {
             const int cp = CPL * lane + j;
@@ -454,11 +541,12 @@ __device__ __forceinline__ void build_q_frags(const uint8_t* entries, const floa
     const int i = lane & 3;
     beta = 0.f;
     if (entries) {
+        const float bunit = unpack_f16x2(range.mul).x * 0x1p-24f;
 #pragma unroll
         for (int h = 0; h < NQ; ++h) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) bp[h] += __shfl_xor_sync(kFull, bp[h], o);
-            if (i == h) beta = bp[h] * 0x1p-24f;
+            if (i == h) beta = bp[h] * bunit;
         }
     }
     __syncwarp();
@@ -470,6 +558,80 @@ __device__ __forceinline__ void build_q_frags(const uint8_t* entries, const floa
             qb[4 * v] = x.x; qb[4 * v + 1] = x.y; qb[4 * v + 2] = x.z; qb[4 * v + 3] = x.w;
         }
     }
+}
+
+// Largest value steps of a staged tile pair as this lane sees them (two fp16):
+// the lanes' words together cover the 16 NGRP steps of both entry tiles.
+template <class C, int NGRP>
+__device__ __forceinline__ uint32_t pair_steps(uint32_t stage_u32, int lane) {
+    if constexpr (NGRP == 4) {
+        const uint2 x = lds64(stage_u32 + C::VE + (lane >> 4) * C::ENT + 8 * (lane & 15));
+        return hmax2(x.x, x.y);
+    } else {
+        constexpr int WPT = 8 * NGRP;             // words of steps per tile
+        return lds32(stage_u32 + C::VE + ((lane / WPT) & 1) * C::ENT + 4 * (lane % WPT));
+    }
+}
+
+// Where a warp's probabilities stand in fp16's range.  A probability is held as
+// p 2^k, and p 2^k times a value's step as two fp16 numbers, whose last bit is
+// worth 2^-24 at least: what the codes (up to 2^BITS - 1) make of half of that has
+// to stay below the output's one rounding to fp16, for small values too.  So k is as
+// large as p 2^k and p 2^k step allow (both at most 2^15): 15 for steps up to
+// 1/2, one less for each doubling.  It comes from the warp's first pair, with one
+// doubling of room, and goes down when a pair brings a step above `lim`, through the
+// rescaling that a new maximum needs anyway.  The running reference m is the
+// maximum logit less k; l and o are in units of 2^m, so nothing after the loop
+// knows k.  (With k = 0 and 8 bits, values around 0.01 were off by 2% of the
+// output, values around 0.001 by 80%.)
+struct ValueRange {
+    float k = 15.f;
+    uint32_t lim = 0u;            // as two fp16: the largest step that k allows,
+    uint32_t grid = 0x64006400u;  // and 2^-5 of the largest p 2^k step then (product_parts)
+};
+
+// Online softmax step over two tiles: sc * unit = logits of tokens g, g+8 of
+// tile A and of tile B (head i); p receives their probabilities times 2^k.
+// steps: pair_steps of the pair (0 for fp16 rows, which have none).  The maximum
+// over the lanes is taken only when some lane's logit passes the running one,
+// which happens ever more rarely.  ao_lane, az_lane: lanes that hold the logits of the
+// heads of this lane's sums o and zeta.
+template <int KS, int NBF>
+__device__ __forceinline__ void softmax_pair(const float (&sc)[4], float (&p)[4], float unit, uint32_t steps,
+                                             ValueRange& r, float& m, float& l, bool& fresh, float (&o)[KS][4],
+                                             float (&zeta)[NBF], int ao_lane, int az_lane) {
+    float mt = fmaf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), unit, -r.k);
+    const bool large = above_f16x2(steps, r.lim);
+    if (__any_sync(kFull, mt > m || large)) {
+        if (__any_sync(kFull, large)) {
+            const uint32_t most = __reduce_max_sync(kFull, max(steps & 0xffffu, steps >> 16));
+            const int field = (int)((most + 0x3ffu) >> 10);          // most <= 2^(field - 15)
+            const float k = (float)min(15, 29 - field);
+            mt = fmaxf(mt, m) + (r.k - k);        // (l and the sums follow below)
+            r.k = k;
+            r.lim = (uint32_t)min(field + 1, 31) * 0x04000400u;
+            r.grid = (uint32_t)min(field + 11, 25) * 0x04000400u;
+        }
+        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 4));
+        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 8));
+        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 16));
+        const float mn = fmaxf(m, mt);
+        if (!fresh) {                             // (before the first tiles o, zeta and l are zero)
+            const float alpha = m == mn ? 1.f : fast_exp2(m - mn);
+            l *= alpha;
+            const float ao = __shfl_sync(kFull, alpha, ao_lane);
+#pragma unroll
+            for (int t = 0; t < KS; ++t) { o[t][0] *= ao; o[t][1] *= ao; o[t][2] *= ao; o[t][3] *= ao; }
+            const float az = __shfl_sync(kFull, alpha, az_lane);
+#pragma unroll
+            for (int f = 0; f < NBF; ++f) zeta[f] *= az;
+        }
+        m = mn;
+        fresh = false;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = fast_exp2(fmaf(sc[j], unit, -m));
+    l += (p[0] + p[1]) + (p[2] + p[3]);
 }
 
 template <bool B>
@@ -582,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
     // the code scale 2^-(BITS*pos), for the slot the warp works on
     __shared__ __align__(16) float qf_all[kWarps][NQ][D];
     __shared__ uint32_t qhc_all[kWarps][NQ][D / 2], qlc_all[kWarps][NQ][D / 2];
+    __shared__ float qunit_all[kWarps][NQ];       // 2^-query_exponent
     __shared__ __align__(16) uint32_t qfrag_all[kWarps][32 * C::QSTRIDE];
     __shared__ __align__(8) uint64_t full_bar[kWarps][C::STAGES];
     // paged, per warp: the segment's block-table entries as byte offsets of the
@@ -654,34 +817,17 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
             return *reinterpret_cast<const uint2*>(qfrag + lane * C::QSTRIDE + 2 * kk);
     };
     float beta = 0.f;
+    // this lane's head: the logits' unit of the fp16 rows, and of the block at hand
+    const float* qunit = &qunit_all[warp][i < NQ ? i : 0];
+    float unit = 1.f;
     uint32_t status = 0;  // 1: a bulk copy did not complete in time (sticky)
     uint32_t item = 0;    // ring stages this warp has consumed (stage index and phase)
 
-    // Online softmax step over two tiles: sc * unit = logits of tokens g, g+8
-    // of tile A and of tile B (head i); p receives their probabilities.
-    auto softmax = [&](const float (&sc)[4], float (&p)[4], float unit) {
-        float mt = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 4));
-        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 8));
-        mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 16));
-        const float mn = fmaxf(m, mt * unit);
-        if (fresh) {
-            m = mn;          // the segment's first tiles: o, zeta and l are still zero
-            fresh = false;
-        } else if (__any_sync(kFull, mn > m)) {
-            const float alpha = fast_exp2(m - mn);
-            l *= alpha;
-            const float ao = __shfl_sync(kFull, alpha, (lane & ~3) | (hO < NQ ? hO : 0));
-#pragma unroll
-            for (int t = 0; t < KS; ++t) { o[t][0] *= ao; o[t][1] *= ao; o[t][2] *= ao; o[t][3] *= ao; }
-            const float az = __shfl_sync(kFull, alpha, col_ok ? hP : 0);
-#pragma unroll
-            for (int f = 0; f < NBF; ++f) zeta[f] *= az;
-            m = mn;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = fast_exp2(fmaf(sc[j], unit, -m));
-        l += (p[0] + p[1]) + (p[2] + p[3]);
+    ValueRange range;
+    KeyRange krange;
+    const int ao_lane = (lane & ~3) | (hO < NQ ? hO : 0), az_lane = col_ok ? hP : 0;
+    auto softmax = [&](const float (&sc)[4], float (&p)[4], float unit, uint32_t steps) {
+        softmax_pair(sc, p, unit, steps, range, m, l, fresh, o, zeta, ao_lane, az_lane);
     };
     // probabilities of tokens 2i, 2i+1, 2i+8, 2i+9 of head hP from (p0, p1) =
     // the probabilities of tokens g, g+8 held by every lane
@@ -697,9 +843,9 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
     auto p_frag = [&](const float (&pr)[4], uint32_t ph01, uint32_t ph89, uint32_t pl01, uint32_t pl89,
                       uint2 sv, uint2 zv, uint32_t& b0, uint32_t& b1, float& z) {
         const uint32_t s01 = sv.x, s89 = sv.y;
-        const uint32_t h01 = hmul2(ph01, s01), h89 = hmul2(ph89, s89);
-        const uint32_t l01 = hfma2(pl01, s01, hfma2(ph01, s01, neg_f16x2(h01)));
-        const uint32_t l89 = hfma2(pl89, s89, hfma2(ph89, s89, neg_f16x2(h89)));
+        uint32_t h01, h89, l01, l89;
+        product_parts(ph01, pl01, s01, range.grid, h01, l01);
+        product_parts(ph89, pl89, s89, range.grid, h89, l89);
         b0 = lo_col ? l01 : h01;
         b1 = lo_col ? l89 : h89;
         const float2 z01 = unpack_f16x2(zv.x);
@@ -969,20 +1115,33 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
             }
         }
         __syncwarp();
-        for (int idx = lane; idx < NQ * D / 2; idx += 32) {
-            const int j = idx / (D / 2), cp = idx % (D / 2);
-            const float2 qv = __half22float2(
-                *reinterpret_cast<const __half2*>(a.q + ((long long)b * a.Hq + hk * NQ + j) * D + 2 * cp));
-            const float x0 = qv.x * a.scale_log2, x1 = qv.y * a.scale_log2;
-            qf[j][2 * cp] = x0;
-            qf[j][2 * cp + 1] = x1;
-            // channels 2cp, 2cp+1 have class cp / 4: their codes read as code * 2^(BITS*pos - 24)
-            const float cs = pow2i(-BITS * ((cp >> 2) % (8 / BITS)));
-            const float y0 = x0 * cs, y1 = x1 * cs;
-            const uint32_t hic = pack_f16x2(y0, y1);
-            const float2 hcf = unpack_f16x2(hic);
-            qhc_s[j][cp] = hic;
-            qlc_s[j][cp] = pack_f16x2(y0 - hcf.x, y1 - hcf.y);
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            uint32_t qw[D / 64], most = 0u;
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) {
+                qw[u] = *reinterpret_cast<const uint32_t*>(a.q + ((long long)b * a.Hq + hk * NQ + j) * D +
+                                                           2 * (32 * u + lane));
+                most = max(most, abs_max_f16x2(qw[u]));
+            }
+            most = __reduce_max_sync(kFull, most);
+            const int ex = query_exponent(unpack_f16x2(most).x * a.scale_log2);
+            if (lane == 0) qunit_all[warp][j] = pow2i(-ex);
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) {
+                const int cp = 32 * u + lane;
+                const float2 qv = unpack_f16x2(qw[u]);
+                const float x0 = qv.x * a.scale_log2 * pow2i(ex), x1 = qv.y * a.scale_log2 * pow2i(ex);
+                qf[j][2 * cp] = x0;
+                qf[j][2 * cp + 1] = x1;
+                // channels 2cp, 2cp+1 have class cp / 4: their codes read as code * 2^(BITS*pos - 24)
+                const float cs = pow2i(-BITS * ((cp >> 2) % (8 / BITS)));
+                const float y0 = x0 * cs, y1 = x1 * cs;
+                const uint32_t hic = pack_f16x2(y0, y1);
+                const float2 hcf = unpack_f16x2(hic);
+                qhc_s[j][cp] = hic;
+                qlc_s[j][cp] = pack_f16x2(y0 - hcf.x, y1 - hcf.y);
+            }
         }
         if constexpr (FIFO) {
             if (tpop >= 0) {
@@ -1000,6 +1159,9 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
 
         m = -INFINITY; l = 0.f;
         fresh = true;
+        range = ValueRange{};
+        krange = KeyRange{};
+        unit = *qunit * 0x1p9f;
 #pragma unroll
         for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 #pragma unroll
@@ -1034,7 +1196,8 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
                 }
             }
             if (need_ksz(pr))
-                build_q_frags<C, D, NQ, QB_REGS>(stage + C::KE, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);
+                build_q_frags<C, D, NQ, QB_REGS>(stage + C::KE, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta,
+                                                 qunit, krange, unit, false);
             // keys: logits of tokens g, g+8 of both tiles for head i
             float sc[4];
             if constexpr (BITS == 8) {
@@ -1099,7 +1262,8 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
                 if (t0 + 32 > a.lqv) {
                     // keys quantized, some values still in the queue: keep the logits
                     // for the second pass; here only the value-quantized tokens count
-                    *mixbuf((pr - mix_first()) * 32 + lane) = make_float4(sc[0], sc[1], sc[2], sc[3]);
+                    *mixbuf((pr - mix_first()) * 32 + lane) =
+                        make_float4(sc[0] * unit, sc[1] * unit, sc[2] * unit, sc[3] * unit);
                     if (t0 + g >= a.lqv) sc[0] = -INFINITY;
                     if (t0 + g + 8 >= a.lqv) sc[1] = -INFINITY;
                     if (t0 + 16 + g >= a.lqv) sc[2] = -INFINITY;
@@ -1132,7 +1296,7 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
                     }
                 }
                 float p[4];
-                softmax(sc, p, 0x1p24f);                   // scores are in units of 2^-24
+                softmax(sc, p, unit, pair_steps<C, NGRP>(stage_u32, lane));
                 // values, tile by tile
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -1243,7 +1407,7 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
                 if (t0 + 16 + g < a.lqv) sc[2] = -INFINITY;
                 if (t0 + 24 + g < a.lqv) sc[3] = -INFINITY;
                 float p[4];
-                softmax(sc, p, 0x1p24f);
+                softmax(sc, p, 1.f, 0u);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     float prb[4];
@@ -1279,7 +1443,8 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
                     return rr == nrow ? a.new_v + islot * D : vr + (long long)(((int)(32 * P) + rr) % a.R) * D;
                 return FUSED && rr == nrow ? a.new_v + islot * D : vr + (long long)rr * D;
             };
-            build_q_frags<C, D, NQ, QB_REGS>(nullptr, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta);   // step 1, zero 0
+            build_q_frags<C, D, NQ, QB_REGS>(nullptr, qf, qhc_s, qlc_s, qoff, qfrag, lane, qb, beta, qunit,
+                                             krange, unit, false);   // step 1, zero 0
             for (int rp = rb; rp < re; ++rp) {
                 float sc[4];
 #pragma unroll
@@ -1304,7 +1469,7 @@ __global__ void __launch_bounds__(kThreads, MinCtas<D, NQ>::value)
                     sc[2 * t + 1] = okg8 ? c[2] + c[3] : -INFINITY;
                 }
                 float p[4];
-                softmax(sc, p, 1.f);
+                softmax(sc, p, unit, 0u);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     float prb[4];
