@@ -662,6 +662,7 @@ kivi_status check_scores_args(const void* q, float softmax_scale, const float* s
 kivi_status check_decode_blocks_args(const void* q, const int* blocks, int n_list, const void* out, float softmax_scale) {
     if (!q || !out) return failf(KIVI_ERR_INVALID_ARG, "null q or out");
     if (n_list < 0) return failf(KIVI_ERR_INVALID_ARG, "negative list length");
+    if (n_list > (1 << 28)) return failf(KIVI_ERR_UNSUPPORTED, "lists hold at most 2^28 entries");
     if (n_list > 0 && !blocks) return failf(KIVI_ERR_INVALID_ARG, "null block list");
     if (!aligned(q, 16) || !aligned(out, 16)) return failf(KIVI_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
     if (!aligned(blocks, 4)) return failf(KIVI_ERR_INVALID_ARG, "blocks must be 4-byte aligned");

@@ -246,7 +246,15 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     int wb = 0;
     for (int v = lane; v <= worker; v += 32) wb = max(wb, pairs_at(v));
     wb = worker == 0 ? 0 : __reduce_max_sync(kFull, wb);
-    const int we = worker + 1 == workers ? P : max(wb, pairs_at(worker + 1));
+    int we = worker + 1 == workers ? P : max(wb, pairs_at(worker + 1));
+    // A list with more places than the row has blocks (mostly a short sequence's in a
+    // ragged call: its blocks, then -1) is dealt out place by place, so that every
+    // warp gets its part of the blocks wherever they stand.
+    const bool dealt = a.n_list > nblk;
+    if (dealt) {
+        wb = 0;
+        we = nblk > 0 && a.n_list > worker ? ((a.n_list - worker - 1) / workers + 1) * PPB : 0;
+    }
 
     // everything below reads what earlier kernels on the stream may have written
     griddepcontrol_wait();
@@ -273,10 +281,12 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
     };
     const int* list = a.list + row * a.n_list;
     uint32_t status = 0;       // 1: a bulk copy did not complete in time; 2: an entry outside the cache
-    // list entry j, none past the n-th
+    // entry j of the warp's, none past the n-th
     auto list_entry = [&](int j, int n) {
         int e = -1;                               // (volatile: not moved behind the loads that follow it)
-        if (j < n) asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(e) : "l"(list + j));
+        const bool ok = j < n;
+        if (dealt) j = worker + j * workers;
+        if (ok) asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(e) : "l"(list + j));
         return e;
     };
     // entry e as the byte offset of its block's key part; -1: no block
@@ -333,8 +343,13 @@ __global__ void __launch_bounds__(32 * kCtaWarps<D, NQ>, 1)
         kend = min(we, end * PPB);
         entry = list_entry(j0 + lane, end);
     };
-    // ... then their offsets, and the part's first copies
+    // ... then their offsets, and the part's first copies.  The part ends behind its last
+    // block; entries without one from there on are read again, or passed over if
+    // the part has none.
     auto begin_part = [&]() {
+        const uint32_t some = __ballot_sync(kFull, entry >= 0);
+        if (some == 0u) k = kend;
+        kend = min(kend, (j0 + 32 - __clz(some)) * PPB);
         offs[lane] = offset_of(entry);
         __syncwarp();
         if (lane < C::STAGES && k + lane < kend) {   // the part's first copies, a lane each

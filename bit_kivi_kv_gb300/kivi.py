@@ -612,7 +612,7 @@ class KiviCache:
 
     def decode_blocks(self, q, blocks, out=None, softmax_scale=0.0, stream=None):
         """Decode attention of q [B, Hq, D] over the listed blocks (int32
-        [B, Hkv, n], negative: none) and the residual (kivi_decode_blocks)."""
+        [B, Hkv, n], negative anywhere: none) and the residual (kivi_decode_blocks)."""
         device, f16, n = _device(), _torch.float16, blocks.shape[-1]
         _expect(q, "q", f16, self._q_shape, device)
         _expect(blocks, "blocks", _torch.int32, (*self._rows, n), device)

@@ -493,13 +493,13 @@ kivi_status kivi_select_blocks(const float* scores, long long rows, long long co
 /*
  * Decode attention over chosen blocks: as kivi_decode_attn, over the tokens of
  * each row's listed blocks and all residual rows.  blocks: int32
- * [rows][n_list], 4-byte aligned, on the device.  Of a row's entries the
- * first min(n_list, Lq / G) are read; a negative entry is no block (so a
- * selection's -1 may stand anywhere), the order has no meaning beyond fp32
+ * [rows][n_list], 4-byte aligned, on the device.  A negative entry is no
+ * block, wherever it stands; the order has no meaning beyond fp32
  * summation, and a block listed twice counts twice.  An entry of Lq / G or
  * more (or, paged, whose page lies outside the pool) is not read from; it makes
- * the outputs of the row's heads NaN, as a copy that times out does.
- * n_list may be 0 (the residual alone).  One launch, no workspace; tensor cores
+ * the outputs of the row's heads NaN, as a copy that times out does.  The
+ * list of a row that has no block (Lq = 0) is not looked at.
+ * n_list may be 0 (the residual alone) and is at most 2^28.  One launch, no workspace; tensor cores
  * whatever kivi_cache_set_decode_kernel selects, and the grid follows the
  * rows, not kivi_cache_set_max_ctas.
  * KIVI_ERR_STATE on an empty cache; KIVI_ERR_UNSUPPORTED with the value queue.
