@@ -21,6 +21,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <type_traits>
+
 #include "kivi_blocks.cuh"
 #include "kivi_decode_mma.cuh"
 
@@ -173,7 +175,31 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const __grid_
                 for (int j = 0; j < 4; ++j) s = fmaf(ya[j], ya[j], fmaf(yb[j], yb[j], s));
 #pragma unroll
                 for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-                const float r = 1.0f / sqrtf(s * (1.0f / D) + a.eps);
+                const float ms = s * (1.0f / D) + a.eps;
+                float r = 1.0f / sqrtf(ms);
+                // squares that leave fp32's range (values above 2^63, or below 2^-50
+                // with next to no eps; not fp16's): the row times a power of two of its
+                // largest value.  One unsigned comparison: not in [2^-100, 2^126).
+                const bool far = !std::is_same<T, __half>::value && __float_as_uint(ms) - 0x0d800000u >= 0x71000000u;
+                if (__any_sync(kFull, far)) {
+                    float most = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) most = fmaxf(most, fmaxf(fabsf(ya[j]), fabsf(yb[j])));
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+                    const int e = max(-126, min(126, (int)(__float_as_uint(most) >> 23) - 127));
+                    const float c = far ? mma_detail::pow2i(-e) : 1.f;
+                    s = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        ya[j] *= c;
+                        yb[j] *= c;
+                        s = fmaf(ya[j], ya[j], fmaf(yb[j], yb[j], s));
+                    }
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+                    if (far) r = 1.0f / sqrtf(s * (1.0f / D) + a.eps * c * c);
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     ya[j] = ya[j] * r * wa[j];
