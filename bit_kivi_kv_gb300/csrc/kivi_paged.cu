@@ -178,6 +178,16 @@ cudaError_t launch_flushes(kivi_paged* c, const int* seqs, int n, long long page
     return e;
 }
 
+// launch_flushes as the C calls need it: nothing thrown, nothing changed on failure.
+kivi_status flush(kivi_paged* c, const int* seqs, int n, long long pages, cudaStream_t st) {
+    try {
+        const cudaError_t e = launch_flushes(c, seqs, n, pages, st);
+        return e == cudaSuccess ? KIVI_OK : cuda_fail(e, "residual flush launch");
+    } catch (const std::bad_alloc&) {
+        return failf(KIVI_ERR_INVALID_ARG, "out of host memory");
+    }
+}
+
 // The enqueued flushes' pages belong to their sequences.
 void take_flushed(kivi_paged* c, const int* seqs, int n) {
     const kivi::Geometry& g = c->pg.g;
@@ -300,8 +310,13 @@ kivi_status kivi_paged_add(kivi_paged_t c, const void* K, const void* V, long lo
     const int s = c->free_seqs.back();
     SeqState& sq = c->seqs[(size_t)s];
     sq.pages.clear();
-    sq.pages.reserve((size_t)nblk);
-    std::vector<kivi::QJob> jobs((size_t)nblk);
+    std::vector<kivi::QJob> jobs;
+    try {
+        sq.pages.reserve((size_t)nblk);
+        jobs.resize((size_t)nblk);
+    } catch (const std::bad_alloc&) {
+        return failf(KIVI_ERR_INVALID_ARG, "out of host memory");
+    }
     for (long long j = 0; j < nblk; ++j) {
         const int page = c->free_pages[c->free_pages.size() - 1 - (size_t)j];
         sq.pages.push_back(page);
@@ -404,48 +419,38 @@ kivi_status kivi_paged_append_decode(kivi_paged_t c, const int* seqs, int n, con
     const size_t need = paged_ws_need(g, n);
     if (ws_bytes < need) return failf(KIVI_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, need);
     // every check before any launch or state change
-    if (++c->stamp == 0) {   // stamp wrapped: clear the marks
-        c->mark.assign(c->mark.size(), 0u);
-        c->stamp = 1;
-    }
+    const kivi_status sm = mark_seqs(c, seqs, n);
+    if (sm != KIVI_OK) return sm;
     long long flush_pages = 0;
-    for (int i = 0; i < n; ++i) {
-        const int s = seqs[i];
-        if (!live_seq(c, s)) return failf(KIVI_ERR_INVALID_ARG, "sequence %d (entry %d) is not live", s, i);
-        if (c->mark[(size_t)s] == c->stamp) return failf(KIVI_ERR_INVALID_ARG, "sequence %d is listed twice", s);
-        c->mark[(size_t)s] = c->stamp;
-        const SeqState& sq = c->seqs[(size_t)s];
-        if (append && sq.n_resid == g.R) {
-            if (sq.n_quant / g.G + g.R / g.G > g.NB)
-                return failf(KIVI_ERR_CAPACITY, "sequence %d is full (%lld tokens)", s, sq.n_quant + sq.n_resid);
-            flush_pages += g.R / g.G;
-        }
-        if (!append && sq.n_quant + sq.n_resid == 0)
-            return failf(KIVI_ERR_STATE, "decode of sequence %d, which holds no token", s);
+    if (append) {
+        const kivi_status sf = flush_room(c, seqs, n, &flush_pages);
+        if (sf != KIVI_OK) return sf;
+    } else {
+        for (int i = 0; i < n; ++i)
+            if (c->seqs[(size_t)seqs[i]].n_quant + c->seqs[(size_t)seqs[i]].n_resid == 0)
+                return failf(KIVI_ERR_STATE, "decode of sequence %d, which holds no token", seqs[i]);
     }
-    if (flush_pages > (long long)c->free_pages.size())
-        return failf(KIVI_ERR_CAPACITY, "flushes need %lld pages, %zu are free", flush_pages, c->free_pages.size());
     const kivi_status sdev = paged_device(c);
     if (sdev != KIVI_OK) return sdev;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
 
     // flushes: the R residual rows of each full sequence become R / G blocks in new pages
-    std::vector<kivi::PagedSeq> call((size_t)n);
     if (flush_pages) {
-        const cudaError_t e = launch_flushes(c, seqs, n, flush_pages, st);
-        if (e != cudaSuccess) return cuda_fail(e, "residual flush launch");
+        const kivi_status sl = flush(c, seqs, n, flush_pages, st);
+        if (sl != KIVI_OK) return sl;
     }
+    kivi::PagedSeq call[kivi::kMaxCallSeqs];
     for (int i = 0; i < n; ++i) {
         const SeqState& sq = c->seqs[(size_t)seqs[i]];
         const bool fl = append && sq.n_resid == g.R;
         const long long lq = sq.n_quant + (fl ? g.R : 0);
         const int r = fl ? 0 : sq.n_resid;
-        call[(size_t)i] = kivi::PagedSeq{0, seqs[i], (int)(lq / 32), r + (append ? 1 : 0), append ? r : -1};
+        call[i] = kivi::PagedSeq{0, seqs[i], (int)(lq / 32), r + (append ? 1 : 0), append ? r : -1};
     }
     const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)g.D);
     int nl = 0;
     const cudaError_t e = kivi::launch_decode_paged(
-        c->pg, c->buf, call.data(), n, static_cast<const __half*>(q), static_cast<__half*>(out),
+        c->pg, c->buf, call, n, static_cast<const __half*>(q), static_cast<__half*>(out),
         scale * 1.4426950408889634f, static_cast<float*>(workspace), static_cast<const __half*>(k),
         static_cast<const __half*>(v), flush_pages ? 0 : 1, c->num_sms, c->max_ctas, st, &nl);
     kivi::count_launches(nl);
@@ -472,14 +477,10 @@ kivi_status kivi_paged_append(kivi_paged_t c, const int* seqs, int n, const void
     const kivi_status sdev = paged_device(c);
     if (sdev != KIVI_OK) return sdev;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    try {
-        if (pages) {
-            const cudaError_t e = launch_flushes(c, seqs, n, pages, st);
-            if (e != cudaSuccess) return cuda_fail(e, "residual flush launch");
-            take_flushed(c, seqs, n);
-        }
-    } catch (const std::bad_alloc&) {
-        return failf(KIVI_ERR_INVALID_ARG, "out of host memory");
+    if (pages) {
+        const kivi_status sl = flush(c, seqs, n, pages, st);
+        if (sl != KIVI_OK) return sl;
+        take_flushed(c, seqs, n);
     }
     kivi::AppendRow rows[kivi::kMaxCallSeqs];
     for (int i = 0; i < n; ++i) rows[i] = kivi::AppendRow{seqs[i], c->seqs[(size_t)seqs[i]].n_resid};
