@@ -30,8 +30,8 @@ significant bits, and a last bit worth 2^-24 at least):
            allowed, top = max(4 S, 2^-13) of the largest p, or of its own last bit: l is off by 2^-11 of its
            size, so a product per unit of code by 2^-27 top or 2^-11 of itself, whichever
            is less, and 2^-22 of itself.  The MMAs cut 17 2^-27 top a tile off the l.
-  sums     n tokens in n / 16 steps a warp at most, and the merge: (32 + n / 16) 2^-23 of
-           sum w (|v| + |z|).
+  sums     n tokens in n / 16 steps, shared by `warps` warps at least, and the merge:
+           (32 + n / 16 / warps) 2^-23 of sum w (|v| + |z|).
   output   one rounding to fp16: 2^-11 of it, 2^-25 below 2^-14.
 
 An error d of a token's logit moves the output by w (exp(d) - 1) (v - o).
@@ -63,7 +63,7 @@ class Slot:
             return np.arange(self.K.shape[0])
         return np.concatenate([block_tokens(blocks, self.G), np.arange(self.n_quant, self.K.shape[0])])
 
-    def decode(self, q, at, scale):
+    def decode(self, q, at, scale, warps=1):
         """(out, bound), both [nq][D], of attention of q [nq][D] over tokens at (of self.tokens)."""
         q, bits = np.asarray(q, np.float64), self.bits
         K, V, zk, sk, zv, sv = (t[at] for t in (self.K, self.V, self.zk, self.sk, self.zv, self.sv))
@@ -91,7 +91,7 @@ class Slot:
         lost += n * (2.0 ** -25 * wmax * max(2.0 ** -15, 2.0 ** -13 * S) * L * S + 17 / 16 * 2.0 ** -27 * top)
         tail = np.maximum(np.abs(V), 2.0 ** -14) * (sv == 0)
         lost += 17 * 2.0 ** -24 * (w @ tail) + n * 2.0 ** -25 * wmax * max(2.0 ** -15, 2.0 ** -13 * S) * tail.max(0)
-        sums = (32 + n / 16) * 2.0 ** -23 * (w @ (np.abs(V) + np.abs(zv)))
+        sums = (32 + n / 16 / warps) * 2.0 ** -23 * (w @ (np.abs(V) + np.abs(zv)))
         return o, 2.0 ** -11 * np.abs(o) + 2.0 ** -25 + 1.01 * moved + lost + sums
 
 
