@@ -366,6 +366,15 @@ def _expect(t, what, dtype, shape, device):
     raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} is on {t.device}, not on the current device")
 
 
+def _on(cache):
+    """The current device, which has to be the one that holds the cache's buffer (the
+    kernels run on the current device, whatever the buffer's)."""
+    device = _device()
+    if device != cache._device:
+        raise KiviError(KIVI_ERR_INVALID_ARG, f"the cache is on cuda:{cache._device}, not on the current device")
+    return device
+
+
 def _new(shape, dtype, device, stream):
     """An output of a call that runs on stream: its memory has to come from that
     stream's pool, where no earlier work of another stream may still use it."""
@@ -520,6 +529,7 @@ class KiviCache:
         self.workspace = self._alloc(kivi_decode_workspace_bytes(self.cfg), device)
         self.handle = kivi_cache_create(self.cfg, self.buffer.data_ptr(), nbytes)
         self._q_shape, self._rows = (batch, n_q_heads, head_dim), (batch, n_kv_heads)
+        self._device = self.buffer.get_device()
 
     def _alloc(self, nbytes, device):
         """Device bytes for the cache buffer and the workspace (256-byte aligned);
@@ -585,7 +595,7 @@ class KiviCache:
         """Append one token a row from a projection's output: norm and rotation by
         norm_rope (QKNormRope), k and v stored in the cache by the same kernel.
         q [B, Hq, D], k, v [B, Hkv, D]; returns the query, fp16 [B, Hq, D]."""
-        device, f16 = _device(), _torch.float16
+        device, f16 = _on(self), _torch.float16
         fields, (shape, _, _) = norm_rope._inputs(q, k, v, positions, device)
         if q_out is None:
             q_out = _new(shape, f16, q.device, stream)
@@ -598,7 +608,7 @@ class KiviCache:
     def block_scores(self, q, out=None, softmax_scale=0.0, stream=None):
         """A bound on the logits of each quantized block for q [B, Hq, D]: fp32
         [B, Hkv, blocks] (kivi_block_scores); out may have more columns (-inf there)."""
-        device, f32 = _device(), _torch.float32
+        device, f32 = _on(self), _torch.float32
         _expect(q, "q", _torch.float16, self._q_shape, device)
         if out is None:
             cols = self.counts()[0] // self.cfg.group
@@ -613,7 +623,7 @@ class KiviCache:
     def decode_blocks(self, q, blocks, out=None, softmax_scale=0.0, stream=None):
         """Decode attention of q [B, Hq, D] over the listed blocks (int32
         [B, Hkv, n], negative anywhere: none) and the residual (kivi_decode_blocks)."""
-        device, f16, n = _device(), _torch.float16, blocks.shape[-1]
+        device, f16, n = _on(self), _torch.float16, blocks.shape[-1]
         _expect(q, "q", f16, self._q_shape, device)
         _expect(blocks, "blocks", _torch.int32, (*self._rows, n), device)
         if out is None:
@@ -653,6 +663,7 @@ class KiviPagedCache:
                                      device)
         self.handle = kivi_paged_create(self.cfg, self.buffer.data_ptr(), nbytes)
         self._heads = (n_q_heads, n_kv_heads, head_dim)
+        self._device = self.buffer.get_device()
 
     def _alloc(self, nbytes, device):
         """Device bytes for the buffer and the workspace (see KiviCache._alloc)."""
@@ -698,7 +709,7 @@ class KiviPagedCache:
 
     def append(self, seqs, k, v, stream=None):
         """For each listed sequence: append k[i], v[i] ([n][Hkv][D])."""
-        n, (_, hkv, d), device = len(seqs), self._heads, _device()
+        n, (_, hkv, d), device = len(seqs), self._heads, _on(self)
         _expect(k, "k", _torch.float16, (n, hkv, d), device)
         _expect(v, "v", _torch.float16, (n, hkv, d), device)
         _check(lib.kivi_paged_append(self.handle, _seq_array(seqs), n, k.data_ptr(), v.data_ptr(),
@@ -707,7 +718,7 @@ class KiviPagedCache:
     def block_scores(self, seqs, q, out=None, softmax_scale=0.0, stream=None):
         """KiviCache.block_scores for the listed sequences: q [n, Hq, D] -> fp32
         [n, Hkv, the longest sequence's blocks], -inf behind a sequence's last."""
-        n, (hq, hkv, d), device = len(seqs), self._heads, _device()
+        n, (hq, hkv, d), device = len(seqs), self._heads, _on(self)
         _expect(q, "q", _torch.float16, (n, hq, d), device)
         if out is None:
             cols = max((self.counts(s)[0] // self.cfg.group for s in seqs), default=0)
@@ -721,7 +732,7 @@ class KiviPagedCache:
 
     def decode_blocks(self, seqs, q, blocks, out=None, softmax_scale=0.0, stream=None):
         """KiviCache.decode_blocks for the listed sequences: blocks int32 [n, Hkv, m]."""
-        n, (hq, hkv, d), device, m = len(seqs), self._heads, _device(), blocks.shape[-1]
+        n, (hq, hkv, d), device, m = len(seqs), self._heads, _on(self), blocks.shape[-1]
         _expect(q, "q", _torch.float16, (n, hq, d), device)
         _expect(blocks, "blocks", _torch.int32, (n, hkv, m), device)
         if out is None:
