@@ -291,10 +291,10 @@ __global__ void __launch_bounds__(32 * kWarpRows) select_blocks_warp_kernel(cons
 // one are counted in 2048 equal bins of the range that they span; the bin of
 // the wanted key is the next range, and once it holds few keys each of them is
 // ranked against the others.  One round for ordinary scores, three at most; a
-// row of equal scores needs none (64 x 4092: rounds alone 8.0 us, so 6.2).  The columns
+// row of equal scores needs none (64 x 4092: rounds alone 8.0 us, so 6.7).  The columns
 // that are always kept stay out of the range.  Keys stay in shared memory (in
 // registers every pass over them has to be unrolled, and code that runs once
-// costs its way into the instruction cache: 64 x 4092 7.0 us), or are read again
+// costs its way into the instruction cache), or are read again
 // each time in rows of more than 49152 columns.  Warps own consecutive columns.
 constexpr int kHeldKeys = 49152;
 constexpr int kPlainKeys = 8192;     // 32 KB, beside 9 KB of counts: no opt-in to more shared memory
@@ -578,7 +578,7 @@ cudaError_t launch_select_blocks(const float* scores, long long rows, long long 
         return launch_dependent(select_blocks_warp_kernel<32>, by_warp, 32 * kWarpRows, st, a);
     // 4 to 8 keys a thread: fewer threads take longer over their keys, more wait
     // longer at the barriers and leave room for fewer rows (64 and 512 rows of 4092:
-    // 256 threads 8.0, 18.8 us; 512: 6.2, 14.8; 1024: 6.3, 20.9; 64 x 8000: 512 8.7, 1024 7.4)
+    // 256 threads 8.6, 19.0 us; 512: 6.7, 15.3; 1024: 6.5, 21.1; 64 x 8000: 512 9.6, 1024 8.1)
     if (cols <= 1024) return launch_select(select_blocks_kernel<256>, 256, a, st);
     if (cols <= 4096) return launch_select(select_blocks_kernel<512>, 512, a, st);
     return launch_select(select_blocks_kernel<1024>, 1024, a, st);

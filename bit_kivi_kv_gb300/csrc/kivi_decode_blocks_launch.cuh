@@ -35,7 +35,7 @@ struct InstanceSetup {
 // shapes whose whole grid is resident at once.  Each is charged with the units
 // (tile pairs and residual tiles) of a warp, the mean of the busiest one's and
 // of an even split, and a cluster with what its merge costs besides: 0.7 unit,
-// 0.9 with four query heads, whose merge is larger.  (256 rows of 32 blocks: 1 x 8
+// 0.9 with four query heads, whose merge is larger.  (Of one version of the kernel: 256 rows of 32 blocks: 1 x 8
 // warps 11.6 us, 2 x 4 12.9; 192 rows of 128 blocks: 1 x 8 29.5, 2 x 5 25.9; 32
 // rows of 16 blocks at head_dim 64: 1 x 16 4.9, 4 x 6 3.9; four query heads, 64
 // rows of 2 blocks of 128: 1 x 12 6.2, 2 x 8 7.2.)  Of clusters that cost the
