@@ -144,14 +144,3 @@ def test_reference_selection():
     assert ref_select(s, 3, 1).tolist() == [[0, 1, 2], [2, 3, 4], [-1, -1, -1], [2, 3, 4]]
     assert ref_select(s, 3, 2).tolist() == [[0, 1, 2], [2, 3, 4], [-1, -1, -1], [1, 3, 4]]
     assert ref_select(s, 6, 0)[0].tolist() == [0, 1, 2, 3, 4, -1]
-
-
-def test_list_length_limit(K):
-    """A longer list than the kernel counts is refused."""
-    cfg = K.make_config(1, 2, 2, 64, 2, 32, 32, 64)
-    h = K.kivi_cache_create(cfg, FAKE, K.kivi_cache_bytes(cfg))
-    try:
-        refuses(K, K.KIVI_ERR_UNSUPPORTED, K.kivi_decode_blocks, h, FAKE, FAKE, (1 << 28) + 1, FAKE, 0.0, 0)
-        refuses(K, K.KIVI_ERR_STATE, K.kivi_decode_blocks, h, FAKE, FAKE, 1 << 28, FAKE, 0.0, 0)   # (an empty cache)
-    finally:
-        K.kivi_cache_destroy(h)
