@@ -1,0 +1,225 @@
+// Internal declarations of the calls that bring several tokens of a sequence at
+// once to the paged cache: attention of a chunk, its append, branches, reading back.
+#pragma once
+
+#include "kivi_blocks.cuh"
+
+namespace kivi {
+
+// ---- attention of a chunk (kivi.h, kivi_paged_chunk_attn) ----
+//
+// Work of a call.  Per (sequence, kv head) the queries of the chunk are rows,
+// row = token * nq + query head of the group, in items of kRows rows; an item
+// reads its keys in tiles of kTile tokens, from the first one that any of its
+// rows sees to the last.  An item of more than kHalf rows does two MMAs of
+// kHalf rows a tile (weight 2), one of fewer rows one (weight 1).  Items are in
+// the order sequence, item of the chunk, kv head; CTA c of n takes the tiles
+// that start in weights [c W / n, (c + 1) W / n).  A CTA that holds all of an item's
+// tiles writes its outputs, others partial results, which a merge joins.
+constexpr int kRows = 256, kHalf = 128, kTile = 128;
+constexpr int kMaxChunkCtas = 192;       // most CTAs of a call (one per SM)
+
+struct ChunkSeq {
+    long long start;    // weight of the sequences before it
+    int seq;            // sequence slot: residual rows and block-table row
+    int n;              // new tokens
+    int tok0;           // its first new token in the packed inputs
+    int n_quant;        // quantized tokens
+    int n_resid;        // residual rows
+    int pad;
+};
+
+struct ChunkPlan {
+    int nq, Hkv;        // query heads per kv head, kv heads
+    int window;         // 0: none
+};
+
+__host__ __device__ inline long long floor_div64(long long x) { return x >> 6; }
+
+// Tokens an item's rows cover: kRows / nq, 64 w4.
+__host__ __device__ inline int item_tokens(const ChunkPlan& p) { return kRows / p.nq; }
+__host__ __device__ inline int item_count(const ChunkPlan& p, int n) {
+    return (int)(((long long)n * p.nq + kRows - 1) / kRows);
+}
+// first and one-past-last key tile of the tokens [t0, t1) of a chunk after c cached tokens
+__host__ __device__ inline int first_tile(const ChunkPlan& p, long long c, long long t0) {
+    const long long x = c + t0 - p.window + 1;
+    return p.window && x > 0 ? (int)(x / kTile) : 0;
+}
+__host__ __device__ inline int last_tile(long long c, long long t1) { return (int)((c + t1 + kTile - 1) / kTile); }
+
+// One item: its rows, tiles and weight.
+struct ChunkItem {
+    int t0, t1;         // its tokens of the chunk
+    int lo, hi;         // key tiles
+    int both;           // more than kHalf rows
+    __host__ __device__ int weight() const { return both ? 2 : 1; }
+    __host__ __device__ long long total() const { return (long long)weight() * (hi - lo); }
+};
+__host__ __device__ inline ChunkItem chunk_item(const ChunkPlan& p, const ChunkSeq& s, int m) {
+    ChunkItem it;
+    const int tpm = item_tokens(p);
+    const long long c = (long long)s.n_quant + s.n_resid;
+    it.t0 = m * tpm;
+    it.t1 = s.n - it.t0 < tpm ? s.n : it.t0 + tpm;
+    it.lo = first_tile(p, c, it.t0);
+    it.hi = last_tile(c, it.t1);
+    it.both = (it.t1 - it.t0) * p.nq > kHalf;
+    return it;
+}
+
+// Tiles of the first m items of a chunk after c tokens, all of them whole: the sum
+// over j < m of ceil((c + (j + 1) T) / 128) less the first tiles, T = 64 w.
+__host__ __device__ inline long long whole_tiles(const ChunkPlan& p, long long c, long long m) {
+    const long long w = item_tokens(p) / 64;
+    const long long a = (c + 63) / 64;
+    // sum over j of ceil((a + (j + 1) w) / 2)
+    long long sum;
+    auto F = [](long long x) { return (x + 1) * (x + 1) / 4; };       // ceil(1/2) + ... + ceil(x/2)
+    auto H = [](long long x) { return x * x / 4; };                   // floor(1/2) + ... + floor(x/2), x >= -1
+    if (w == 1) sum = F(a + m) - F(a);
+    else sum = m * ((a + 1) / 2) + (w / 2) * (m * (m + 1) / 2);
+    if (p.window) {
+        const long long b = floor_div64(c - p.window + 1);            // floor
+        const long long m0 = b >= 0 ? 0 : (-b + w - 1) / w;           // first item whose first key is not below 0
+        if (m > m0) {
+            const long long b0 = b + w * m0, n = m - m0;
+            if (w == 1) sum -= H(b0 + n - 1) - (b0 > 0 ? H(b0 - 1) : 0);
+            else sum -= n * (b0 / 2) + (w / 2) * (n * (n - 1) / 2);
+        }
+    }
+    return sum;
+}
+// weight of the items before item m of a sequence (all heads); m == item_count: the sequence's
+__host__ __device__ inline long long items_weight(const ChunkPlan& p, const ChunkSeq& s, int m) {
+    const int n = item_count(p, s.n);
+    const long long c = (long long)s.n_quant + s.n_resid;
+    const int whole = m < n ? m : n - 1;
+    long long w = 2 * whole_tiles(p, c, whole);
+    if (m == n) w += chunk_item(p, s, n - 1).total();
+    return w * p.Hkv;
+}
+
+// The tiles [first, last) of item (seq, m, head) that a CTA takes.
+struct ChunkSpan {
+    int seq, m, head;
+    ChunkItem it;
+    int first, last;    // relative to it.lo
+    __host__ __device__ bool whole() const { return first == 0 && last == it.hi - it.lo; }
+};
+// Walks over a CTA's spans.
+struct ChunkWalk {
+    const ChunkPlan* p;
+    const ChunkSeq* seqs;
+    int n_seqs;
+    long long x, end;   // weights left to take
+    ChunkSpan s;
+    long long item0;    // weight where the present item starts
+    // Start at weight x0; the item that holds it (an item's tiles that start below x0 are skipped).
+    __host__ __device__ void start(const ChunkPlan* plan, const ChunkSeq* sq, int n, long long x0, long long x1) {
+        p = plan;
+        seqs = sq;
+        n_seqs = n;
+        x = x0;
+        end = x1;
+        int lo = 0, hi = n - 1;
+        while (lo < hi) {                       // the last sequence that starts at or below x0
+            const int mid = (lo + hi + 1) / 2;
+            if (sq[mid].start <= x0) lo = mid; else hi = mid - 1;
+        }
+        s.seq = lo;
+        const long long off = x0 - sq[lo].start;
+        int ml = 0, mh = item_count(*p, sq[lo].n) - 1;
+        while (ml < mh) {
+            const int mid = (ml + mh + 1) / 2;
+            if (items_weight(*p, sq[lo], mid) <= off) ml = mid; else mh = mid - 1;
+        }
+        s.m = ml;
+        s.it = chunk_item(*p, sq[lo], ml);
+        const long long in = off - items_weight(*p, sq[lo], ml);
+        s.head = (int)(in / s.it.total());
+        item0 = x0 - in % s.it.total();
+    }
+    // The next span with a tile; false when the range is used up.
+    __host__ __device__ bool next() {
+        while (x < end) {
+            const long long w = s.it.weight(), tot = s.it.total();
+            const long long from = x - item0, to = end - item0 < tot ? end - item0 : tot;
+            s.first = (int)((from + w - 1) / w);
+            s.last = (int)((to + w - 1) / w);
+            x = item0 + tot;                    // (beyond end: the loop ends with the next call)
+            if (s.first < s.last) return true;
+            advance();
+        }
+        return false;
+    }
+    __host__ __device__ void advance() {
+        item0 += s.it.total();
+        if (++s.head == p->Hkv) {
+            s.head = 0;
+            if (++s.m == item_count(*p, seqs[s.seq].n)) {
+                s.m = 0;
+                if (++s.seq == n_seqs) { x = end; s.seq = 0; return; }
+            }
+            s.it = chunk_item(*p, seqs[s.seq], s.m);
+        }
+    }
+};
+
+struct ChunkArgs {
+    const uint8_t* buf;
+    const int* table;
+    const __half *q, *k, *v;
+    __half* out;
+    long long q_stride[2], k_stride[2], v_stride[2], out_stride[2];   // token, head (elements)
+    long long page_bytes, part_bytes, k_resid_off, v_resid_off;
+    int R, G, Hq, max_blocks, n_pages, n_seqs, n_ctas;
+    float scale_log2;   // scores to base-2 logits
+    float cap;          // > 0: scores are capped at it
+    float scale;        // softmax_scale
+    const float* slopes;
+    ChunkPlan plan;
+    long long weight;   // of the whole call
+    float* ws;          // partial results: [n_ctas][2][kRows][D + 2]
+    ChunkSeq seqs[kMaxCallSeqs];
+};
+// The weights [x0, x1) of CTA c.
+__host__ __device__ inline long long chunk_begin(long long weight, int n_ctas, long long c) { return c * weight / n_ctas; }
+constexpr int chunk_partial_stride(int D) { return D + 2; }      // o[D], m, l of a row
+
+cudaError_t launch_chunk_attn_d64(const ChunkArgs& a, int bits, cudaStream_t st);
+cudaError_t launch_chunk_attn_d128(const ChunkArgs& a, int bits, cudaStream_t st);
+cudaError_t launch_chunk_merge(const ChunkArgs& a, int D, cudaStream_t st);
+
+// ---- append of a chunk, branches, reading back (kivi_pages.cu) ----
+
+// A new block of a chunk: rows [row0, row0 + G) of the sequence's virtual rows
+// (its residual rows, then its new tokens) quantized into page.
+struct ChunkJob {
+    int seq, row0, n_resid, tok0;
+    int page, tbl_idx;
+};
+constexpr int kMaxChunkJobs = 1024;      // per launch
+cudaError_t launch_quantize_chunk(const PagedGeometry& pg, uint8_t* buf, const __half* k, const long long* k_stride,
+                                  const __half* v, const long long* v_stride, const ChunkJob* jobs, int n,
+                                  cudaStream_t st, int* launches);
+
+// The residual after a chunk: virtual rows [shift, shift + keep) become residual rows [0, keep).
+struct ChunkTail {
+    int seq, n_resid, tok0, shift, keep;
+};
+cudaError_t launch_store_tail(const PagedGeometry& pg, uint8_t* buf, const __half* k, const long long* k_stride,
+                              const __half* v, const long long* v_stride, const ChunkTail* tails, int n,
+                              cudaStream_t st);
+
+// Branch i: sequence slot to[i] gets the first n_blocks[i] table entries and n_resid[i] residual rows of from[i].
+struct ForkJob {
+    int from, to, n_blocks, n_resid;
+};
+cudaError_t launch_fork(const PagedGeometry& pg, uint8_t* buf, const ForkJob* jobs, int n, cudaStream_t st);
+
+// Tokens [first, first + count) of each sequence as fp16 [n][Hkv][count][D].
+cudaError_t launch_read(const PagedGeometry& pg, const uint8_t* buf, const RowSeq* seqs, int n, long long first,
+                        long long count, __half* k, __half* v, cudaStream_t st);
+
+}  // namespace kivi

@@ -1,0 +1,808 @@
+// Attention of a chunk of new tokens over the paged cache and over the chunk
+// itself (include/kivi.h, kivi_paged_chunk_attn).
+//
+//   o_i = sum_t softmax_t(f(q_i . k_t)) v_t      over t <= c + i (and t > c + i - window),
+//
+// c cached tokens, f(x) = scale x, capped: cap tanh(scale x / cap), plus
+// slope_h (t - (c + i)).  The query heads of a kv head are rows beside each
+// other, so that they share its keys.
+//
+// The two products run on the fifth-generation tensor cores: a tile is 128 rows
+// by 128 keys, S = Q K^T and O += P V, operands in shared memory (128-byte
+// swizzle, the contracted index contiguous), P in tensor memory over S, sums
+// in tensor memory.  A CTA (one per SM) holds up to 256 rows as two tiles A and
+// B that take turns: while one's softmax runs, the other's products do.  With
+// at most 128 rows A and B are the same rows and take alternate key tiles,
+// joined at the end.
+//
+// Roles (warps):
+//   0-3, 4-7   softmax of tile A / B, a row a lane: logits from tensor memory, running
+//              maximum, exponentials, probabilities back as fp16; epilogue
+//   8-11       keys: 32 tokens of a tile each, from codes to fp16 in shared memory
+//   12-15      values, the same, transposed ([channel][token])
+//   16         issues the MMAs
+//   17         copies the quantized bytes (bulk copies into a ring of 32-token units)
+//
+// Dequantization: a code pair masked in place and OR-ed with fp16 1024 is
+// 1024 + code * 2^pos, exact; one FMA makes it the code, a second one
+// fp16(code * step + zero), rounded once.  The cache's tiles are fragments of
+// 8x8 matrices, so stmatrix puts them where the MMA's swizzle wants them.
+// Rows that are still fp16 (residual and chunk) go the same way unchanged.
+//
+// Roundings: keys and values to fp16 (half a step of 2^-11), probabilities to
+// fp16, scaled so that the largest is between 2^8 and 2^15: what falls below
+// fp16's range is under 2^-32 of the row's largest.  Everything else is fp32.
+// The running maximum is only raised when a tile exceeds it by 2^7 (the sums in tensor
+// memory are then scaled), which leaves the result the same.
+//
+// A value row that is not finite would reach rows that do not see it
+// through the product (0 * inf): it is taken as zeros, and its key as NaN, so that
+// exactly the rows that see it become NaN.
+#pragma once
+
+#include <math.h>
+
+#include "kivi_dequant.cuh"
+
+namespace kivi {
+namespace chunk_detail {
+
+using namespace mma_detail;
+
+constexpr int kChunkWarps = 18, kChunkThreads = 32 * kChunkWarps;
+constexpr float kRaise = 7.f;      // base-2 logits above the reference that a tile may have
+constexpr float kLift = 8.f;       // probabilities are held times 2^8
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D, int BITS>
+struct Shape {
+    static constexpr int KCH = D / 8;                     // 8-channel groups of a token
+    static constexpr int W = D * BITS / 64;               // words of a lane in a 16-token code tile
+    static constexpr int TILE = 2 * D * BITS;             // bytes of a code tile
+    // one 32-token unit in the ring: key codes, key steps and zeros, value codes, value steps and zeros
+    static constexpr int KC = 0, KE = 2 * TILE, VC = KE + 4 * D, VE = VC + 2 * TILE, UNIT = VE + 4 * D;
+    static constexpr int UNITS = BITS == 2 || D == 64 ? 8 : BITS == 4 ? 6 : 3;
+    // Barriers of the copies: a multiple of UNITS and of the four units of a tile, eight at least.  A warp that
+    // waits for a unit knows then that the one before it on its barrier has come (it is of the warp's
+    // last tile, or of one whose stage has been freed), so that the parity says which of the two is meant.
+    static constexpr int FULLS = UNITS == 8 ? 8 : 12;
+    static constexpr int Q_BYTES = kHalf * D * 2;         // one tile of queries
+    static constexpr int K_BYTES = kTile * D * 2;         // one stage of keys (values: the same)
+    static constexpr int OFF_Q = 0, OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + 2 * K_BYTES, OFF_RING = OFF_V + 2 * K_BYTES;
+    static constexpr int OFF_BAR = OFF_RING + UNITS * UNIT;
+    static constexpr int OFF_XCH = OFF_BAR + 512;         // (m, l) of tile B's rows
+    static constexpr int BYTES = OFF_XCH + kHalf * 8 + 1024;   // (base aligned to 1024)
+    // one CTA per SM, also where less shared memory is needed: it takes all of the SM's tensor memory
+    static constexpr int SMEM = BYTES < 117 * 1024 ? 117 * 1024 : BYTES;
+    static constexpr int COL_S = 0, COL_O = 256;          // tensor memory columns: S of A and B, O of A and B
+    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(UNIT % 16 == 0, "bulk copies");
+    static_assert(FULLS % UNITS == 0 && FULLS % 4 == 0 && FULLS >= 8 && FULLS <= 12 && UNITS <= 8, "ring barriers");
+};
+
+struct Bars {
+    uint64_t ring_full[12], ring_empty[8];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t drained;
+    uint32_t tmem;
+    int failed;         // a wait ran out: the outputs from here on are NaN
+    unsigned bad;       // spans with a block-table entry outside the pool: bit number % 32
+};
+static_assert(sizeof(Bars) <= 512, "barriers");
+
+// ---- tensor memory and tcgen05 ----
+__device__ __forceinline__ void tmem_alloc(uint32_t* out) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(out)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(at));
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void ld32(uint32_t at, float (&x)[32]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void st32(uint32_t at, const float (&x)[32]) {
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand, contracted index contiguous, 128-byte swizzle: rows of 128 bytes in
+// groups of eight (1024 bytes); the descriptor's fields in 16-byte units.
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// fp16 x fp16 -> fp32, M = 128, N columns, both operands K-major
+__host__ __device__ constexpr uint32_t mma_kind(int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <int ID, int N>
+__device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
+
+// Wait for an mbarrier's phase, about two seconds at most; a wait that runs out marks the CTA,
+// and no wait of a marked CTA waits.
+__device__ __forceinline__ bool wait_for(Bars& b, uint64_t* bar, uint32_t parity) {
+    const uint32_t addr = smem_u32(bar);
+    if (mbar_try(addr, parity)) return true;
+    volatile int* failed = &b.failed;
+    const uint64_t t0 = global_ns();
+    for (uint32_t it = 0; it < (1u << 26); ++it) {
+        if (mbar_try(addr, parity)) return true;
+        if (*failed) return false;
+        if ((it & 63u) == 63u && global_ns() - t0 > 2000000000ull) break;
+    }
+    *failed = 1;
+    return false;
+}
+
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[W]) {
+    if constexpr (W == 2) {
+        const uint2 v = lds64(at);
+        w[0] = v.x; w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) {
+            const uint4 v = lds128(at + 16 * j);
+            w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+        }
+    }
+}
+
+// Keys of a 16-token code tile: fp16(code * step + zero) into rows row0 .. row0 + 15 of the operand at dst.
+// The channel group C's step and zero pair of the lane is at ent + 16 C + 4 i (zeros 2 D bytes on).
+template <int D, int BITS, int C, int W>
+__device__ __forceinline__ void key_groups(const uint32_t (&w)[W], uint32_t ent, uint32_t dst, int row0, int lane) {
+    if constexpr (C < D / 8) {
+        const int i = lane & 3;
+        const uint32_t s0 = lds32(ent + 16 * C + 4 * i), z0 = lds32(ent + 2 * D + 16 * C + 4 * i);
+        const uint32_t s1 = lds32(ent + 16 * C + 16 + 4 * i), z1 = lds32(ent + 2 * D + 16 * C + 16 + 4 * i);
+        // matrices: (C, tokens 0-7), (C, 8-15), (C + 1, 0-7), (C + 1, 8-15); this lane gives a row's address
+        const int row = row0 + (lane & 15), chunk = C + (lane >> 4);
+        stmatrix4(dst + operand_at<kTile>(row, chunk), hfma2(code_of<BITS, C, 0>(w), s0, z0),
+                  hfma2(code_of<BITS, C, 1>(w), s0, z0), hfma2(code_of<BITS, C + 1, 0>(w), s1, z1),
+                  hfma2(code_of<BITS, C + 1, 1>(w), s1, z1));
+        key_groups<D, BITS, C + 2>(w, ent, dst, row0, lane);
+    }
+}
+// Values of a 16-token code tile into columns (tokens) tok0 .. tok0 + 15 of the operand [D channels][tokens] at dst.
+// ent: the tile's steps, channel group j's at 32 j (this lane's four tokens at 8 i), zeros 32 D/G bytes on.
+template <int D, int BITS, int C, int W>
+__device__ __forceinline__ void value_groups(const uint32_t (&w)[W], uint32_t ent, int G, uint2 s, uint2 z, uint32_t dst,
+                                             int tok0, int lane) {
+    if constexpr (C < D / 8) {
+        if constexpr (8 * C % 32 == 0) {
+            if ((8 * C & (G - 1)) == 0) {
+                const uint32_t at = ent + 32 * (8 * C / G) + 8 * (lane & 3);
+                s = lds64(at);
+                z = lds64(at + 32 * (D / G));
+            }
+        }
+        const int row = 8 * (C + (lane >> 4)) + (lane & 7), chunk = (tok0 >> 3) + ((lane >> 3) & 1);
+        stmatrix4(dst + operand_at<D>(row, chunk), hfma2(code_of<BITS, C, 0>(w), s.x, z.x),
+                  hfma2(code_of<BITS, C, 1>(w), s.y, z.y), hfma2(code_of<BITS, C + 1, 0>(w), s.x, z.x),
+                  hfma2(code_of<BITS, C + 1, 1>(w), s.y, z.y));
+        value_groups<D, BITS, C + 2>(w, ent, G, s, z, dst, tok0, lane);
+    }
+}
+
+// (asm volatile: not moved ahead of the wait for the preceding kernel, as __ldg may be)
+__device__ __forceinline__ uint4 ldg_row(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int ldg_int(const int* p) {
+    int v;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ bool pair_not_finite(uint32_t v) {
+    const uint32_t a = v & 0x7fff7fffu;
+    return (a & 0xffffu) >= 0x7c00u || a >= 0x7c000000u;
+}
+__device__ __forceinline__ bool not_finite(const uint4& v) {
+    return pair_not_finite(v.x) || pair_not_finite(v.y) || pair_not_finite(v.z) || pair_not_finite(v.w);
+}
+
+// Where the fp16 rows of a span are: row f of [residual | chunk].
+struct Rows {
+    const __half *resid, *chunk;      // kv head's first residual row, its first new token
+    long long step;                   // elements between new tokens
+    int n_resid, n;                   // residual rows, all rows
+    __device__ __forceinline__ const __half* at(int f, int D) const {
+        return f < n_resid ? resid + (long long)f * D : chunk + (long long)(f - n_resid) * step;
+    }
+};
+// 32 fp16 rows [f0, f0 + 32) (zeros behind the last) as keys; rows whose values are not finite become NaN.
+template <int D>
+__device__ __forceinline__ void key_rows(const Rows& k, const Rows& v, int f0, uint32_t dst, int row0, int lane) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, N = 32 / RPI;   // lanes a row, rows an instruction
+    const int lr = lane % LPR, sub = lane / LPR;
+#pragma unroll
+    for (int h = 0; h < N; h += 4) {
+        uint4 x[4], y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int f = f0 + (h + j) * RPI + sub;
+            x[j] = y[j] = uint4{0, 0, 0, 0};
+            if (f < k.n) {
+                x[j] = ldg_row(k.at(f, D) + 8 * lr);
+                y[j] = ldg_row(v.at(f, D) + 8 * lr);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const unsigned odd = __ballot_sync(kFull, not_finite(y[j]));
+            if (odd) {
+                const unsigned mine = LPR == 16 ? (0xffffu << (16 * sub)) : (0xffu << (8 * sub));
+                if (odd & mine) x[j] = uint4{0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu};
+            }
+            sts128(dst + operand_at<kTile>(row0 + (h + j) * RPI + sub, lr), x[j]);
+        }
+    }
+}
+// The same rows as values, transposed.  A lane loads 8 channels of a token; as matrices of
+// (8 tokens) x (channel pairs of four lanes) they are stored transposed, each row of a matrix to its channel.
+template <int D>
+__device__ __forceinline__ void value_rows(const Rows& v, int f0, uint32_t dst, int tok0, int lane) {
+    const int g = lane >> 2, i = lane & 3;
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+        uint4 x[D / 32];
+        const int f = f0 + 8 * tt + g;
+        bool odd = false;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            x[j] = uint4{0, 0, 0, 0};
+            if (f < v.n) x[j] = ldg_row(v.at(f, D) + 8 * (4 * j + i));
+            odd |= not_finite(x[j]);
+        }
+        const unsigned who = __ballot_sync(kFull, odd);
+        if (who >> (4 * g) & 15u) {
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) x[j] = uint4{0, 0, 0, 0};
+        }
+        // matrix m of an instruction: register m, channels 32 j + 8 (r / 2) + 2 m + r % 2 for its rows r
+        const int m = lane >> 3, r = lane & 7;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            const int ch = 32 * j + 8 * (r >> 1) + 2 * m + (r & 1);
+            stmatrix4_trans(dst + operand_at<D>(ch, (tok0 >> 3) + tt), x[j].x, x[j].y, x[j].z, x[j].w);
+        }
+    }
+}
+
+// What every role knows of a span.
+struct Span {
+    int nt;             // tiles
+    int na, nb;         // of tile A, of tile B
+    bool both;          // A and B are different rows (else the same, alternate tiles)
+    int tile0;          // first key tile
+    __device__ __forceinline__ int tiles(int x) const { return x ? nb : na; }
+    __device__ __forceinline__ int tile(int x, int i) const { return both ? i : 2 * i + x; }   // of x's step i
+};
+__device__ __forceinline__ Span span_of(const ChunkArgs& a, const ChunkSpan& s) {
+    Span o;
+    const ChunkSeq& q = a.seqs[s.seq];
+    o.nt = s.last - s.first;
+    o.both = s.it.both;
+    o.tile0 = s.it.lo + s.first;
+    if (o.both) {
+        // tile A's rows end at kHalf: its own last key tile
+        const int ta = last_tile((long long)q.n_quant + q.n_resid, s.it.t0 + kHalf / a.plan.nq) - o.tile0;
+        o.na = ta < 0 ? 0 : ta < o.nt ? ta : o.nt;
+        o.nb = o.nt;
+    } else {
+        o.na = (o.nt + 1) / 2;
+        o.nb = o.nt / 2;
+    }
+    return o;
+}
+
+// ---- loader: quantized bytes of the spans' tiles into the ring ----
+template <int D, int BITS>
+__device__ void load_units(const ChunkArgs& a, Bars& b, uint32_t ring, ChunkWalk& walk, int lane) {
+    using S = Shape<D, BITS>;
+    uint32_t uc = 0;
+    unsigned number = 0;                                                         // of spans with quantized tiles
+    while (walk.next()) {
+        const ChunkSeq& q = a.seqs[walk.s.seq];
+        const int first = (walk.s.it.lo + walk.s.first) * kTile;                 // token
+        const int end = min(q.n_quant, (walk.s.it.lo + walk.s.last) * kTile);
+        const int* trow = a.table + (long long)q.seq * a.max_blocks;
+        int have = -1, entry = 0;                                                // 32 table entries, one a lane
+        if (first >= end) continue;
+        ++number;
+        // (the ring lets this warp be 8 such spans ahead of the others at most)
+        if (lane == 0) atomicAnd(&b.bad, ~(1u << ((number + 16) % 32)));
+        for (int t = first; t < end; t += 32, ++uc) {
+            const int blk = t / a.G;
+            if (have < 0 || blk >= have + 32) {
+                have = blk;
+                entry = blk + lane < a.max_blocks ? ldg_int(trow + blk + lane) : 0;
+            }
+            int page = __shfl_sync(kFull, entry, blk - have);
+            if ((unsigned)page >= (unsigned)a.n_pages) {
+                page = 0;
+                if (lane == 0) atomicOr(&b.bad, 1u << (number % 32));
+            }
+            const uint32_t slot = uc % S::UNITS, ph = (uc / S::UNITS) & 1;
+            if (!wait_for(b, &b.ring_empty[slot], ph ^ 1)) break;
+            const uint8_t* kp = a.buf + (long long)page * a.page_bytes + (long long)walk.s.head * 2 * a.part_bytes;
+            const uint8_t* vp = kp + a.part_bytes;
+            const int tile = (t % a.G) / 16, tiles = a.G / 16;
+            const int ve = 64 * (D / a.G);                                       // value entries of a code tile
+            const uint32_t bar = smem_u32(&b.ring_full[uc % S::FULLS]), dst = ring + slot * S::UNIT;
+            if (lane == 0) mbar_expect_tx_u32(bar, 4 * S::TILE + 4 * D + 2 * ve);
+            __syncwarp();
+            if (lane == 0) tma_1d_u32(dst + S::KC, kp + tile * S::TILE, 2 * S::TILE, bar);
+            if (lane == 1) tma_1d_u32(dst + S::KE, kp + tiles * S::TILE, 4 * D, bar);
+            if (lane == 2) tma_1d_u32(dst + S::VC, vp + tile * S::TILE, 2 * S::TILE, bar);
+            if (lane == 3) tma_1d_u32(dst + S::VE, vp + tiles * S::TILE + tile * ve, 2 * ve, bar);
+        }
+    }
+    // no copy is in flight when the CTA ends: those that a failed CTA did not wait for
+    const uint32_t n = uc < (uint32_t)S::UNITS ? uc : (uint32_t)S::UNITS;
+    if (*(volatile int*)&b.failed)
+        for (uint32_t u = uc - n; u < uc; ++u) mbar_wait(&b.ring_full[u % S::FULLS], (u / S::FULLS) & 1);
+}
+
+// ---- producers: warp w of 4 fills tokens 32 w .. 32 w + 31 of each tile, keys or values ----
+template <int D, int BITS, bool VALUES>
+__device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t smem, ChunkWalk& walk, int w, int lane) {
+    using S = Shape<D, BITS>;
+    uint32_t tc = 0, uc = 0;
+    uint64_t* full = VALUES ? b.v_full : b.k_full;
+    uint64_t* empty = VALUES ? b.v_empty : b.k_empty;
+    while (walk.next()) {
+        const ChunkSeq& q = a.seqs[walk.s.seq];
+        Rows kr, vr;
+        const long long rrow = ((long long)q.seq * a.plan.Hkv + walk.s.head) * a.R * D;
+        kr.resid = reinterpret_cast<const __half*>(a.buf + a.k_resid_off) + rrow;
+        vr.resid = reinterpret_cast<const __half*>(a.buf + a.v_resid_off) + rrow;
+        kr.chunk = a.k + q.tok0 * a.k_stride[0] + walk.s.head * a.k_stride[1];
+        vr.chunk = a.v + q.tok0 * a.v_stride[0] + walk.s.head * a.v_stride[1];
+        kr.step = a.k_stride[0];
+        vr.step = a.v_stride[0];
+        kr.n_resid = vr.n_resid = q.n_resid;
+        kr.n = vr.n = q.n_resid + walk.s.it.t1;
+        for (int t = walk.s.it.lo + walk.s.first; t < walk.s.it.lo + walk.s.last; ++t, ++tc) {
+            const uint32_t stage = tc & 1, ph = (tc >> 1) & 1;
+            const int key0 = t * kTile + 32 * w;
+            const int units = min(4, max(0, (q.n_quant - t * kTile) >> 5));      // quantized units of the tile
+            const uint32_t dst = smem + (VALUES ? S::OFF_V : S::OFF_K) + stage * S::K_BYTES;
+            bool ok = wait_for(b, &empty[stage], ph ^ 1);
+            if (w < units) {
+                const uint32_t u = uc + w, slot = u % S::UNITS;
+                ok = ok && wait_for(b, &b.ring_full[u % S::FULLS], (u / S::FULLS) & 1);
+                if (ok) {
+                    const uint32_t src = smem + S::OFF_RING + slot * S::UNIT;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t words[S::W];
+                        lds_words(src + (VALUES ? S::VC : S::KC) + j * S::TILE + lane * (4 * S::W), words);
+                        if constexpr (VALUES)
+                            value_groups<D, BITS, 0>(words, src + S::VE + j * 64 * (D / a.G), a.G, uint2{}, uint2{}, dst,
+                                                     32 * w + 16 * j, lane);
+                        else
+                            key_groups<D, BITS, 0>(words, src + S::KE, dst, 32 * w + 16 * j, lane);
+                    }
+                    __syncwarp();
+                    if (lane == 0) arrive(&b.ring_empty[slot]);
+                }
+            } else if (ok) {
+                if constexpr (VALUES) value_rows<D>(vr, key0 - q.n_quant, dst, 32 * w, lane);
+                else key_rows<D>(kr, vr, key0 - q.n_quant, dst, 32 * w, lane);
+            }
+            uc += units;
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) arrive(&full[stage]);
+        }
+    }
+}
+
+// ---- MMA issue (one lane) ----
+template <int D, int BITS>
+__device__ void issue_mmas(const ChunkArgs& a, Bars& b, uint32_t smem, uint32_t tmem, ChunkWalk& walk) {
+    using S = Shape<D, BITS>;
+    uint32_t tc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+    const uint32_t kind_s = mma_kind(kTile), kind_o = mma_kind(D);
+    bool ok = true;
+    auto scores = [&](const Span& sp, int x, int t) {        // S_x = Q_x K_t^T
+        const uint32_t c = tc + t, stage = c & 1;
+        ok = ok && wait_for(b, &b.k_full[stage], (c >> 1) & 1);
+        if (!ok) return;
+        fence_after();
+        const uint32_t qa = smem + S::OFF_Q + (sp.both ? x : 0) * S::Q_BYTES, ka = smem + S::OFF_K + stage * S::K_BYTES;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
+            mma_ss(tmem + S::COL_S + x * kTile, operand(qa + off), operand(ka + off), kind_s, k > 0);
+        }
+        commit(&b.s_full[x]);
+        if (!sp.both || x == 1) commit(&b.k_empty[stage]);
+    };
+    while (walk.next()) {
+        const Span sp = span_of(a, walk.s);
+        for (int x = 0; x < 2; ++x) {
+            if (sp.both || x == 0) {
+                ok = ok && wait_for(b, &b.q_full[x], qc[x] & 1);
+                ++qc[x];
+            }
+            if (sp.tiles(x)) scores(sp, x, sp.tile(x, 0));
+        }
+        const int steps = max(sp.na, sp.nb);
+        for (int i = 0; i < steps; ++i) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (i >= sp.tiles(x)) {
+                    // (both: B always has the tile; alternate: the tile is nobody's)
+                    continue;
+                }
+                const int t = sp.tile(x, i);
+                const uint32_t c = tc + t, stage = c & 1;
+                ok = ok && wait_for(b, &b.p_full[x], pc[x] & 1);
+                ++pc[x];
+                ok = ok && wait_for(b, &b.v_full[stage], (c >> 1) & 1);
+                if (ok) {
+                    fence_after();
+                    const uint32_t va = smem + S::OFF_V + stage * S::K_BYTES;
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(tmem + S::COL_O + x * D, tmem + S::COL_S + x * kTile + 8 * k,
+                               operand(va + (k >> 2) * (D * 128) + (k & 3) * 32), kind_o, i > 0 || k > 0);
+                    if (!sp.both || x == 1) commit(&b.v_empty[stage]);
+                    if (i + 1 == sp.tiles(x)) commit(&b.o_full[x]);
+                }
+                if (i + 1 < sp.tiles(x)) scores(sp, x, sp.tile(x, i + 1));
+            }
+        }
+        tc += sp.nt;
+    }
+    commit(&b.drained);            // no MMA is in flight when the CTA ends
+    mbar_wait(&b.drained, 0);
+}
+
+// ---- softmax of tile X (four warps, a row a lane) ----
+template <int D, int BITS, bool MOD>
+__device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2* xch, uint32_t tmem, ChunkWalk& walk, int x,
+                             int warp, int lane) {
+    using S = Shape<D, BITS>;
+    const int row = 32 * (warp & 3) + lane;                    // of tile X
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t ts = lanes + S::COL_S + x * kTile, to = lanes + S::COL_O + x * D;
+    const int nq = a.plan.nq;
+    uint32_t sc = 0, oc = 0;
+    unsigned number = 0;
+    while (walk.next()) {
+        const Span sp = span_of(a, walk.s);
+        const ChunkSeq& q = a.seqs[walk.s.seq];
+        const bool quantized = sp.tile0 * kTile < q.n_quant;
+        number += quantized;
+        const ChunkItem& it = walk.s.it;
+        const int n_rows = (it.t1 - it.t0) * nq;
+        const int r = sp.both ? x * kHalf + row : row;         // row of the item
+        const bool valid = r < n_rows;
+        const int tok = it.t0 + r / nq, head = walk.s.head * nq + r % nq;
+        const int steps = sp.tiles(x);
+        // queries into the operand
+        if (sp.both || x == 0) {
+            const __half* src = a.q + (long long)(q.tok0 + tok) * a.q_stride[0] + head * a.q_stride[1];
+            const uint32_t dst = smem + S::OFF_Q + x * S::Q_BYTES;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                sts128(dst + operand_at<kHalf>(row, c),
+                       valid ? ldg_row(src + 8 * c) : uint4{0, 0, 0, 0});
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) arrive(&b.q_full[x]);
+        }
+        const long long pos = (long long)q.n_quant + q.n_resid + tok;       // the row's position
+        const int hi = (int)pos;                                            // last and first key that it sees
+        const int lo = a.plan.window ? max(0, (int)(pos - a.plan.window + 1)) : 0;
+        // rows of the warp: the first one sees least, the last one (that exists) starts last
+        const int w_hi = __shfl_sync(kFull, hi, 0), w_lo = __shfl_sync(kFull, lo, 31);
+        const bool any = __any_sync(kFull, valid);
+        const float slope = MOD && a.slopes && valid ? __ldg(a.slopes + head) * kLog2e : 0.f;
+        const float mul = MOD ? 1.f : a.scale_log2;
+        float m = -INFINITY, l = 0.f;
+        for (int i = 0; i < steps; ++i) {
+            const int key0 = (sp.tile0 + sp.tile(x, i)) * kTile;
+            const bool ok = wait_for(b, &b.s_full[x], sc & 1);
+            ++sc;
+            fence_after();
+            if (ok && any) {
+                const bool cut = key0 + kTile - 1 > w_hi || key0 < w_lo;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    ld32(ts + 32 * c, v);
+                    wait_ld();
+                    if (MOD) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            if (a.cap > 0.f) {
+                                // cap tanh(y), tanh(y) = 1 - 2 / (exp(2 y) + 1)
+                                const float e = exp2_ftz(v[j] * (a.scale * (2.f * kLog2e) / a.cap));
+                                v[j] = a.cap * kLog2e * (1.f - __fdividef(2.f, e + 1.f));
+                            } else {
+                                v[j] *= a.scale_log2;
+                            }
+                            v[j] = fmaf(slope, (float)(key0 + 32 * c + j - hi), v[j]);
+                        }
+                    }
+                    if (cut) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int key = key0 + 32 * c + j;
+                            if (key > hi || key < lo) v[j] = -INFINITY;
+                        }
+                    }
+                    if (MOD || cut) st32(ts + 32 * c, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, v[j]);
+                }
+                if (MOD || cut) wait_st();
+                mx *= mul;
+                // the reference is raised, and what is summed so far scaled, where a row needs it
+                if (__any_sync(kFull, mx > m + kRaise)) {
+                    const float top = fmaxf(m, mx);
+                    const float f = m == -INFINITY ? 0.f : exp2_ftz(m - top);
+                    if (i > 0) {
+                        l *= f;
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            ld32(to + 32 * c, o);
+                            wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] *= f;
+                            st32(to + 32 * c, o);
+                        }
+                    }
+                    m = top;
+                }
+                const float ref = m == -INFINITY ? 0.f : m - kLift;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    ld32(ts + 32 * c, v);
+                    wait_ld();
+                    uint32_t p[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float p0 = exp2_ftz(fmaf(v[j], mul, -ref)), p1 = exp2_ftz(fmaf(v[j + 1], mul, -ref));
+                        sum[j & 2] += p0;
+                        sum[(j & 2) + 1] += p1;
+                        p[j / 2] = pack_f16x2(p0, p1);
+                    }
+                    st16(ts + 16 * c, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                wait_st();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&b.p_full[x]);
+        }
+        // ---- epilogue ----
+        bool fine = true;
+        if (steps) {
+            fine = wait_for(b, &b.o_full[x], oc & 1);
+            ++oc;
+        }
+        fence_after();
+        float wa = 1.f, wb = 0.f;                              // weights of A's and B's sums
+        const bool join = !sp.both && sp.nb > 0;
+        if (!sp.both) {
+            if (x == 1) {
+                xch[row] = make_float2(m, l);
+                fence_before();
+                named_sync<1, 256>();
+                named_sync<2, 256>();                          // A has read B's sums
+                continue;
+            }
+            named_sync<1, 256>();
+            fence_after();
+            if (join) {
+                const float2 o = xch[row];
+                const float top = fmaxf(m, o.x);
+                const float base = top == -INFINITY ? 0.f : top;
+                wa = exp2_ftz(m - base);
+                wb = exp2_ftz(o.x - base);
+                l = l * wa + o.y * wb;
+                m = top;
+            }
+        }
+        if (!fine || *(volatile int*)&b.failed || (quantized && (*(volatile unsigned*)&b.bad >> (number % 32) & 1u)))
+            m = l = NAN;
+        const bool whole = walk.s.whole();
+        float* part = a.ws + (((long long)blockIdx.x * 2 + (walk.s.first == 0)) * kRows + r) * chunk_partial_stride(D);
+        __half* out = a.out + (long long)(q.tok0 + tok) * a.out_stride[0] + head * a.out_stride[1];
+        const float inv = 1.f / l;
+        if (any) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                __syncwarp();
+                if (steps) {
+                    ld32(to + 32 * c, o);
+                    wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0.f;
+                }
+                if (join) {
+                    float p[32];
+                    ld32(lanes + S::COL_O + D + 32 * c, p);
+                    wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = o[j] * wa + p[j] * wb;
+                }
+                if (valid && whole) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        uint4 v;
+                        v.x = pack_f16x2(o[j] * inv, o[j + 1] * inv);
+                        v.y = pack_f16x2(o[j + 2] * inv, o[j + 3] * inv);
+                        v.z = pack_f16x2(o[j + 4] * inv, o[j + 5] * inv);
+                        v.w = pack_f16x2(o[j + 6] * inv, o[j + 7] * inv);
+                        *reinterpret_cast<uint4*>(out + 32 * c + j) = v;
+                    }
+                } else if (valid) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) *reinterpret_cast<float2*>(part + 32 * c + j) = make_float2(o[j], o[j + 1]);
+                }
+            }
+            if (valid && !whole) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
+        }
+        if (!sp.both) {
+            fence_before();
+            named_sync<2, 256>();
+        }
+    }
+}
+
+template <int D, int BITS, bool MOD>
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __grid_constant__ ChunkArgs a) {
+    using S = Shape<D, BITS>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t smem = smem_u32(base);
+    Bars& b = *reinterpret_cast<Bars*>(base + S::OFF_BAR);
+    float2* xch = reinterpret_cast<float2*>(base + S::OFF_XCH);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int j = 0; j < S::FULLS; ++j) mbar_init(&b.ring_full[j], 1);
+        for (int j = 0; j < S::UNITS; ++j) mbar_init(&b.ring_empty[j], 2);
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(&b.k_full[j], 4);
+            mbar_init(&b.v_full[j], 4);
+            mbar_init(&b.k_empty[j], 1);
+            mbar_init(&b.v_empty[j], 1);
+            mbar_init(&b.q_full[j], 4);
+            mbar_init(&b.s_full[j], 1);
+            mbar_init(&b.p_full[j], 4);
+            mbar_init(&b.o_full[j], 1);
+        }
+        mbar_init(&b.drained, 1);
+        b.failed = b.bad = 0;
+        fence_mbar_init();
+    }
+    if (warp == 16) tmem_alloc(&b.tmem);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    griddepcontrol_wait();
+    griddepcontrol_launch_dependents();
+    const uint32_t tmem = b.tmem;
+    ChunkWalk walk;
+    walk.start(&a.plan, a.seqs, a.n_seqs, chunk_begin(a.weight, a.n_ctas, blockIdx.x),
+               chunk_begin(a.weight, a.n_ctas, blockIdx.x + 1LL));
+    if (warp < 8) {
+        softmax_rows<D, BITS, MOD>(a, b, smem, xch, tmem, walk, warp >> 2, warp, lane);
+    } else if (warp < 12) {
+        fill_tiles<D, BITS, false>(a, b, smem, walk, warp - 8, lane);
+    } else if (warp < 16) {
+        fill_tiles<D, BITS, true>(a, b, smem, walk, warp - 12, lane);
+    } else if (warp == 16) {
+        if (lane == 0) issue_mmas<D, BITS>(a, b, smem, tmem, walk);
+        __syncwarp();
+    } else {
+        load_units<D, BITS>(a, b, smem + S::OFF_RING, walk, lane);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 16) tmem_free(tmem);
+}
+
+template <int D, int BITS, bool MOD>
+cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t st) {
+    using S = Shape<D, BITS>;
+    auto kernel = chunk_attn_kernel<D, BITS, MOD>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3((unsigned)a.n_ctas);
+    lc.blockDim = dim3(kChunkThreads);
+    lc.dynamicSmemBytes = S::SMEM;
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, a);
+}
+template <int D>
+cudaError_t launch_chunk_bits(const ChunkArgs& a, int bits, cudaStream_t st) {
+    const bool mod = a.cap > 0.f || a.slopes;
+#define KIVI_C(B) \
+    if (bits == B) return mod ? launch_chunk<D, B, true>(a, st) : launch_chunk<D, B, false>(a, st);
+    KIVI_C(2) KIVI_C(4) KIVI_C(8)
+#undef KIVI_C
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace chunk_detail
+}  // namespace kivi

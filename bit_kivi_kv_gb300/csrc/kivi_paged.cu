@@ -14,7 +14,7 @@
 #include <new>
 #include <vector>
 
-#include "kivi_blocks.cuh"
+#include "kivi_chunk.cuh"
 
 namespace {
 
@@ -84,6 +84,7 @@ struct kivi_paged {
     kivi::PagedGeometry pg;
     uint8_t* buf;
     std::vector<int> free_pages;   // stack: the next page handed out is at the back
+    std::vector<int> refs;         // sequences that hold each page
     std::vector<int> free_seqs;
     std::vector<SeqState> seqs;
     std::vector<unsigned> mark;    // call stamp per sequence (duplicate check)
@@ -195,11 +196,54 @@ void take_flushed(kivi_paged* c, const int* seqs, int n) {
     for (int i = 0; i < n; ++i) {
         SeqState& sq = c->seqs[(size_t)seqs[i]];
         if (sq.n_resid != g.R) continue;
-        for (int jj = 0; jj < g.R / g.G; ++jj) sq.pages.push_back(c->free_pages[c->free_pages.size() - 1 - used++]);
+        for (int jj = 0; jj < g.R / g.G; ++jj) {
+            const int page = c->free_pages[c->free_pages.size() - 1 - used++];
+            sq.pages.push_back(page);
+            c->refs[(size_t)page] = 1;
+        }
         sq.n_quant += g.R;
         sq.n_resid = 0;
     }
     c->free_pages.resize(c->free_pages.size() - used);
+}
+
+// The sequence's pages from block `first` on are no longer its own; those that no other sequence holds are free.
+void drop_pages(kivi_paged* c, SeqState& sq, size_t first) {
+    for (size_t j = sq.pages.size(); j-- > first;)
+        if (--c->refs[(size_t)sq.pages[j]] == 0) c->free_pages.push_back(sq.pages[j]);   // (room since create)
+    sq.pages.resize(first);
+}
+
+// The entries of a chunk call: distinct live sequences, lengths >= 0, the tokens in all.
+kivi_status check_chunks(kivi_paged* c, const int* seqs, const int* lens, int n, long long* tokens) {
+    if (!seqs || !lens) return failf(KIVI_ERR_INVALID_ARG, "null sequence or length list");
+    if (n < 1 || n > kivi::kMaxCallSeqs) return failf(KIVI_ERR_INVALID_ARG, "n must be in [1, %d]", kivi::kMaxCallSeqs);
+    *tokens = 0;
+    for (int i = 0; i < n; ++i) {
+        if (lens[i] < 0) return failf(KIVI_ERR_INVALID_ARG, "negative length (entry %d)", i);
+        *tokens += lens[i];
+    }
+    if (*tokens > (1LL << 30)) return failf(KIVI_ERR_UNSUPPORTED, "more than 2^30 new tokens");
+    return mark_seqs(c, seqs, n);
+}
+
+kivi_status check_rows(const char* what, const void* p, const long long* stride) {
+    if (!p) return failf(KIVI_ERR_INVALID_ARG, "null %s", what);
+    if (!aligned(p, 16)) return failf(KIVI_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+    if (stride[0] % 8 || stride[1] % 8) return failf(KIVI_ERR_INVALID_ARG, "%s's strides must be multiples of 16 bytes", what);
+    return KIVI_OK;
+}
+
+// Blocks that a chunk of n tokens completes: as many as a prompt of all the tokens would have quantized
+// beyond those that are.
+long long fresh_blocks(const kivi::Geometry& g, const SeqState& sq, int n) {
+    const long long over = sq.n_quant + sq.n_resid + n - g.R;
+    const long long quant = over > 0 ? (over + g.G - 1) / g.G : 0, have = sq.n_quant / g.G;
+    return quant > have ? quant - have : 0;
+}
+
+size_t chunk_ws_need(const kivi::Geometry& g) {
+    return (size_t)kivi::kMaxChunkCtas * 2 * kivi::kRows * kivi::chunk_partial_stride(g.D) * sizeof(float);
 }
 
 // The rows of a call that only reads the cache: n distinct live sequences,
@@ -269,6 +313,7 @@ kivi_status kivi_paged_create(const kivi_paged_config* cfg, void* dev_buf, size_
         for (long long p = 0; p < pg.n_pages; ++p) c->free_pages[(size_t)p] = (int)(pg.n_pages - 1 - p);
         c->free_seqs.resize((size_t)pg.g.B);
         for (int s = 0; s < pg.g.B; ++s) c->free_seqs[(size_t)s] = pg.g.B - 1 - s;
+        c->refs.assign((size_t)pg.n_pages, 0);
         c->seqs.resize((size_t)pg.g.B);
         c->mark.assign((size_t)pg.g.B, 0u);
     } catch (const std::bad_alloc&) {
@@ -337,6 +382,7 @@ kivi_status kivi_paged_add(kivi_paged_t c, const void* K, const void* V, long lo
         kivi::count_launches(1);
         if (e != cudaSuccess) { sq.pages.clear(); return cuda_fail(e, "prompt residual copy launch"); }
     }
+    for (int page : sq.pages) c->refs[(size_t)page] = 1;
     c->free_pages.resize(c->free_pages.size() - (size_t)nblk);
     c->free_seqs.pop_back();
     sq.live = true;
@@ -350,8 +396,7 @@ kivi_status kivi_paged_release(kivi_paged_t c, int s) {
     if (!c) return failf(KIVI_ERR_INVALID_ARG, "null handle");
     if (!live_seq(c, s)) return failf(KIVI_ERR_INVALID_ARG, "sequence %d is not live", s);
     SeqState& sq = c->seqs[(size_t)s];
-    for (size_t j = sq.pages.size(); j-- > 0;) c->free_pages.push_back(sq.pages[j]);
-    sq.pages.clear();
+    drop_pages(c, sq, 0);
     sq.live = false;
     sq.n_quant = 0;
     sq.n_resid = 0;
@@ -525,6 +570,254 @@ kivi_status kivi_paged_decode_blocks(kivi_paged_t c, const int* seqs, int n, con
     if (sdev != KIVI_OK) return sdev;
     r.num_sms = c->num_sms;
     return kivi::decode_blocks_call(r, q, blocks, n_list, out, softmax_scale, stream);
+}
+
+size_t kivi_paged_chunk_workspace_bytes(const kivi_paged_config* cfg) {
+    kivi::PagedGeometry pg;
+    const char* why;
+    if (derive_paged(cfg, &pg, &why) != KIVI_OK) { failf(KIVI_ERR_INVALID_ARG, "%s", why); return 0; }
+    return chunk_ws_need(pg.g);
+}
+
+kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* lens, int n, const kivi_chunk* x,
+                                  void* workspace, size_t ws_bytes, kivi_stream_t stream) {
+    if (!c || !x) return failf(KIVI_ERR_INVALID_ARG, "null handle or arguments");
+    long long tokens;
+    kivi_status st = check_chunks(c, seqs, lens, n, &tokens);
+    if (st != KIVI_OK) return st;
+    if (!(x->softmax_scale == x->softmax_scale) || isinf(x->softmax_scale))
+        return failf(KIVI_ERR_INVALID_ARG, "softmax_scale must be finite");
+    if (!(x->cap >= 0.f) || isinf(x->cap)) return failf(KIVI_ERR_INVALID_ARG, "cap must be finite and >= 0");
+    if (x->window < 0) return failf(KIVI_ERR_INVALID_ARG, "negative window");
+    if (!aligned(x->slopes, 4)) return failf(KIVI_ERR_INVALID_ARG, "slopes must be 4-byte aligned");
+    if (tokens == 0) return ok();
+    if ((st = check_rows("q", x->q, x->q_stride)) != KIVI_OK) return st;
+    if ((st = check_rows("k", x->k, x->k_stride)) != KIVI_OK) return st;
+    if ((st = check_rows("v", x->v, x->v_stride)) != KIVI_OK) return st;
+    if ((st = check_rows("out", x->out, x->out_stride)) != KIVI_OK) return st;
+    if (!workspace || !aligned(workspace, 256)) return failf(KIVI_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    const kivi::Geometry& g = c->pg.g;
+    if (ws_bytes < chunk_ws_need(g))
+        return failf(KIVI_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, chunk_ws_need(g));
+    const kivi_status sdev = paged_device(c);
+    if (sdev != KIVI_OK) return sdev;
+    kivi::ChunkArgs a;
+    a.buf = c->buf;
+    a.table = reinterpret_cast<const int*>(c->buf + c->pg.table_off);
+    a.q = static_cast<const __half*>(x->q);
+    a.k = static_cast<const __half*>(x->k);
+    a.v = static_cast<const __half*>(x->v);
+    a.out = static_cast<__half*>(x->out);
+    for (int j = 0; j < 2; ++j) {
+        a.q_stride[j] = x->q_stride[j];
+        a.k_stride[j] = x->k_stride[j];
+        a.v_stride[j] = x->v_stride[j];
+        a.out_stride[j] = x->out_stride[j];
+    }
+    a.page_bytes = c->pg.page_bytes;
+    a.part_bytes = g.part_bytes;
+    a.k_resid_off = g.k_resid_off;
+    a.v_resid_off = g.v_resid_off;
+    a.R = g.R;
+    a.G = g.G;
+    a.Hq = g.Hq;
+    a.max_blocks = (int)g.NB;
+    a.n_pages = (int)c->pg.n_pages;
+    a.scale = x->softmax_scale > 0.f ? x->softmax_scale : 1.0f / sqrtf((float)g.D);
+    a.scale_log2 = a.scale * 1.4426950408889634f;
+    a.cap = x->cap;
+    a.slopes = x->slopes;
+    a.plan = kivi::ChunkPlan{g.Hq / g.Hkv, g.Hkv, x->window};
+    a.ws = static_cast<float*>(workspace);
+    a.n_seqs = 0;
+    a.weight = 0;
+    int tok0 = 0;
+    for (int i = 0; i < n; ++i) {
+        if (!lens[i]) continue;
+        const SeqState& sq = c->seqs[(size_t)seqs[i]];
+        if (sq.n_quant + sq.n_resid + lens[i] > (1LL << 30))
+            return failf(KIVI_ERR_UNSUPPORTED, "sequence %d: more than 2^30 tokens", seqs[i]);
+        kivi::ChunkSeq& s = a.seqs[a.n_seqs++];
+        s = kivi::ChunkSeq{a.weight, seqs[i], lens[i], tok0, (int)sq.n_quant, sq.n_resid, 0};
+        a.weight += kivi::items_weight(a.plan, s, kivi::item_count(a.plan, s.n));
+        tok0 += lens[i];
+    }
+    // every CTA gets a tile: a range of two weights holds the start of one
+    const long long most = a.weight / 2 < 1 ? 1 : a.weight / 2;
+    const long long ctas = c->num_sms < kivi::kMaxChunkCtas ? c->num_sms : kivi::kMaxChunkCtas;
+    a.n_ctas = (int)(most < ctas ? most : ctas);
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = g.D == 128 ? kivi::launch_chunk_attn_d128(a, g.bits, cs) : kivi::launch_chunk_attn_d64(a, g.bits, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+    kivi::count_launches(1);
+    if (a.n_ctas > 1) {
+        e = kivi::launch_chunk_merge(a, g.D, cs);
+        if (e != cudaSuccess) return cuda_fail(e, "chunk merge launch");
+        kivi::count_launches(1);
+    }
+    return ok();
+}
+
+kivi_status kivi_paged_append_chunk(kivi_paged_t c, const int* seqs, const int* lens, int n, const void* k,
+                                    const long long* k_stride, const void* v, const long long* v_stride,
+                                    kivi_stream_t stream) {
+    if (!c) return failf(KIVI_ERR_INVALID_ARG, "null handle");
+    if (!k_stride || !v_stride) return failf(KIVI_ERR_INVALID_ARG, "null strides");
+    long long tokens;
+    kivi_status st = check_chunks(c, seqs, lens, n, &tokens);
+    if (st != KIVI_OK) return st;
+    if (tokens == 0) return ok();
+    if ((st = check_rows("k", k, k_stride)) != KIVI_OK) return st;
+    if ((st = check_rows("v", v, v_stride)) != KIVI_OK) return st;
+    const kivi::Geometry& g = c->pg.g;
+    long long pages = 0;
+    for (int i = 0; i < n; ++i) {
+        const long long blocks = fresh_blocks(g, c->seqs[(size_t)seqs[i]], lens[i]);
+        if (c->seqs[(size_t)seqs[i]].n_quant / g.G + blocks > g.NB)
+            return failf(KIVI_ERR_CAPACITY, "sequence %d has no room for %d tokens", seqs[i], lens[i]);
+        pages += blocks;
+    }
+    if (pages > (long long)c->free_pages.size())
+        return failf(KIVI_ERR_CAPACITY, "the chunk needs %lld pages, %zu are free", pages, c->free_pages.size());
+    const kivi_status sdev = paged_device(c);
+    if (sdev != KIVI_OK) return sdev;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    kivi::ChunkTail tails[kivi::kMaxCallSeqs];
+    int n_tails = 0, tok0 = 0;
+    std::vector<kivi::ChunkJob> jobs;
+    try {
+        jobs.reserve((size_t)pages);
+        for (int i = 0; i < n; ++i) {
+            SeqState& sq = c->seqs[(size_t)seqs[i]];
+            const int blocks = (int)fresh_blocks(g, sq, lens[i]);
+            // room in the page list now, so that nothing can fail after the launch
+            const size_t need = sq.pages.size() + (size_t)blocks;
+            if (sq.pages.capacity() < need) sq.pages.reserve(need > 2 * sq.pages.size() ? need : 2 * sq.pages.size());
+            for (int j = 0; j < blocks; ++j) {
+                const int page = c->free_pages[c->free_pages.size() - 1 - jobs.size()];
+                jobs.push_back(kivi::ChunkJob{seqs[i], j * g.G, sq.n_resid, tok0, page,
+                                              (int)((long long)seqs[i] * g.NB + sq.n_quant / g.G + j)});
+            }
+            if (lens[i])
+                tails[n_tails++] = kivi::ChunkTail{seqs[i], sq.n_resid, tok0, blocks * g.G, sq.n_resid + lens[i] - blocks * g.G};
+            tok0 += lens[i];
+        }
+    } catch (const std::bad_alloc&) {
+        return failf(KIVI_ERR_INVALID_ARG, "out of host memory");
+    }
+    const __half* kh = static_cast<const __half*>(k);
+    const __half* vh = static_cast<const __half*>(v);
+    if (pages) {
+        int nl = 0;
+        const cudaError_t e = kivi::launch_quantize_chunk(c->pg, c->buf, kh, k_stride, vh, v_stride, jobs.data(), (int)pages,
+                                                          cs, &nl);
+        kivi::count_launches(nl);
+        if (e != cudaSuccess) return cuda_fail(e, "chunk quantize launch");
+    }
+    const cudaError_t e = kivi::launch_store_tail(c->pg, c->buf, kh, k_stride, vh, v_stride, tails, n_tails, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "chunk copy launch");
+    kivi::count_launches(1);
+    size_t used = 0;
+    for (int i = 0; i < n; ++i) {
+        SeqState& sq = c->seqs[(size_t)seqs[i]];
+        const int blocks = (int)fresh_blocks(g, sq, lens[i]);
+        for (int j = 0; j < blocks; ++j) {
+            const int page = jobs[used++].page;
+            sq.pages.push_back(page);
+            c->refs[(size_t)page] = 1;
+        }
+        sq.n_quant += (long long)blocks * g.G;
+        sq.n_resid += lens[i] - blocks * g.G;
+    }
+    c->free_pages.resize(c->free_pages.size() - used);
+    return ok();
+}
+
+kivi_status kivi_paged_fork(kivi_paged_t c, const int* seqs, int n, int* out, kivi_stream_t stream) {
+    if (!c || !seqs || !out) return failf(KIVI_ERR_INVALID_ARG, "null argument");
+    if (n < 1 || n > kivi::kMaxCallSeqs) return failf(KIVI_ERR_INVALID_ARG, "n must be in [1, %d]", kivi::kMaxCallSeqs);
+    bool any = false;
+    for (int i = 0; i < n; ++i) {
+        if (!live_seq(c, seqs[i])) return failf(KIVI_ERR_INVALID_ARG, "sequence %d (entry %d) is not live", seqs[i], i);
+        any |= c->seqs[(size_t)seqs[i]].n_quant + c->seqs[(size_t)seqs[i]].n_resid > 0;
+    }
+    if ((size_t)n > c->free_seqs.size())
+        return failf(KIVI_ERR_CAPACITY, "%d branches, %zu sequence slots are free", n, c->free_seqs.size());
+    if (any) {
+        const kivi_status sdev = paged_device(c);
+        if (sdev != KIVI_OK) return sdev;
+    }
+    kivi::ForkJob jobs[kivi::kMaxCallSeqs];
+    try {
+        for (int i = 0; i < n; ++i) {
+            const SeqState& from = c->seqs[(size_t)seqs[i]];
+            const int to = c->free_seqs[c->free_seqs.size() - 1 - (size_t)i];
+            c->seqs[(size_t)to].pages = from.pages;
+            jobs[i] = kivi::ForkJob{seqs[i], to, (int)from.pages.size(), from.n_resid};
+        }
+    } catch (const std::bad_alloc&) {
+        return failf(KIVI_ERR_INVALID_ARG, "out of host memory");
+    }
+    if (any) {
+        const cudaError_t e = kivi::launch_fork(c->pg, c->buf, jobs, n, reinterpret_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_fail(e, "fork launch");
+        kivi::count_launches(1);
+    }
+    for (int i = 0; i < n; ++i) {
+        SeqState& to = c->seqs[(size_t)jobs[i].to];
+        const SeqState& from = c->seqs[(size_t)seqs[i]];
+        to.live = true;
+        to.n_quant = from.n_quant;
+        to.n_resid = from.n_resid;
+        for (int page : to.pages) ++c->refs[(size_t)page];
+        out[i] = jobs[i].to;
+    }
+    c->free_seqs.resize(c->free_seqs.size() - (size_t)n);
+    return ok();
+}
+
+kivi_status kivi_paged_truncate(kivi_paged_t c, int s, long long n_tokens) {
+    if (!c) return failf(KIVI_ERR_INVALID_ARG, "null handle");
+    if (!live_seq(c, s)) return failf(KIVI_ERR_INVALID_ARG, "sequence %d is not live", s);
+    SeqState& sq = c->seqs[(size_t)s];
+    const kivi::Geometry& g = c->pg.g;
+    if (n_tokens < 0 || n_tokens > sq.n_quant + sq.n_resid)
+        return failf(KIVI_ERR_INVALID_ARG, "sequence %d holds %lld tokens", s, sq.n_quant + sq.n_resid);
+    if (n_tokens >= sq.n_quant) {
+        sq.n_resid = (int)(n_tokens - sq.n_quant);
+        return ok();
+    }
+    if (n_tokens % g.G)
+        return failf(KIVI_ERR_UNSUPPORTED, "token %lld is inside a quantized block of %d", n_tokens, g.G);
+    drop_pages(c, sq, (size_t)(n_tokens / g.G));
+    sq.n_quant = n_tokens;
+    sq.n_resid = 0;
+    return ok();
+}
+
+kivi_status kivi_paged_read(kivi_paged_t c, const int* seqs, int n, long long first, long long count, void* K, void* V,
+                            kivi_stream_t stream) {
+    if (!c || !seqs) return failf(KIVI_ERR_INVALID_ARG, "null handle or sequence list");
+    if (n < 1 || n > kivi::kMaxCallSeqs) return failf(KIVI_ERR_INVALID_ARG, "n must be in [1, %d]", kivi::kMaxCallSeqs);
+    if (first < 0 || count < 0) return failf(KIVI_ERR_INVALID_ARG, "negative token range");
+    kivi::RowSeq rows[kivi::kMaxCallSeqs];
+    for (int i = 0; i < n; ++i) {
+        if (!live_seq(c, seqs[i])) return failf(KIVI_ERR_INVALID_ARG, "sequence %d (entry %d) is not live", seqs[i], i);
+        const SeqState& sq = c->seqs[(size_t)seqs[i]];
+        if (count > sq.n_quant + sq.n_resid - first)
+            return failf(KIVI_ERR_INVALID_ARG, "sequence %d holds %lld tokens", seqs[i], sq.n_quant + sq.n_resid);
+        rows[i] = kivi::RowSeq{seqs[i], (int)(sq.n_quant / c->pg.g.G), sq.n_resid};
+    }
+    if (count == 0) return ok();
+    if (!K || !V) return failf(KIVI_ERR_INVALID_ARG, "null K or V");
+    if (!aligned(K, 16) || !aligned(V, 16)) return failf(KIVI_ERR_INVALID_ARG, "K and V must be 16-byte aligned");
+    const kivi_status sdev = paged_device(c);
+    if (sdev != KIVI_OK) return sdev;
+    const cudaError_t e = kivi::launch_read(c->pg, c->buf, rows, n, first, count, static_cast<__half*>(K),
+                                            static_cast<__half*>(V), reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "read launch");
+    kivi::count_launches(1);
+    return ok();
 }
 
 }  // extern "C"

@@ -6,7 +6,7 @@
 // grouped per channel over G tokens, values per token over G channels (same
 // guide, keys and values sections; KIVI explainer, discosf.com, 3.1).  The
 // arithmetic is the fixed fp32 formula written out in kivi.h.
-#include "kivi_common.cuh"
+#include "kivi_chunk.cuh"
 
 namespace kivi {
 namespace {
@@ -143,10 +143,26 @@ struct PagedQuantArgs {
     QJob jobs[kMaxQJobs];
 };
 
-template <bool PAGED>
+// Chunk form (paged): job j's rows are virtual rows of its sequence, its residual
+// rows and then its new tokens (strides in elements).
+struct ChunkQuantArgs {
+    uint8_t* pool;
+    int* table;
+    const __half *resid_k, *resid_v;
+    const __half *new_k, *new_v;
+    long long k_stride[2], v_stride[2];   // token, head
+    long long part_bytes, tile_bytes;
+    int Hkv, G, R;
+    ChunkJob jobs[kMaxChunkJobs];
+};
+
+constexpr int kDense = 0, kPaged = 1, kChunk = 2;   // where a block's rows are and where it goes
+template <int MODE>
 struct QuantArgsOf { using type = QuantArgs; };
 template <>
-struct QuantArgsOf<true> { using type = PagedQuantArgs; };
+struct QuantArgsOf<kPaged> { using type = PagedQuantArgs; };
+template <>
+struct QuantArgsOf<kChunk> { using type = ChunkQuantArgs; };
 
 // One CTA quantizes one block (G tokens x D channels) of keys and of values.
 // The block's rows are staged in shared memory with a stride of D + 8 halves,
@@ -154,9 +170,9 @@ struct QuantArgsOf<true> { using type = PagedQuantArgs; };
 // thread packs the same word position of every 16-token tile, so the
 // coordinates of its codes (and, for keys, their steps and zeros) are fixed
 // once per block.
-template <int D, int BITS, int G, bool PAGED>
+template <int D, int BITS, int G, int MODE>
 __global__ void __launch_bounds__(kQuantThreads)
-    quantize_blocks_kernel(const __grid_constant__ typename QuantArgsOf<PAGED>::type a) {
+    quantize_blocks_kernel(const __grid_constant__ typename QuantArgsOf<MODE>::type a) {
     constexpr int L = (1 << BITS) - 1;
     constexpr int W = D * BITS / 64;        // words per lane per tile
     constexpr int PER = 16 / BITS;          // code pairs per word
@@ -176,7 +192,24 @@ __global__ void __launch_bounds__(kQuantThreads)
     const __half* blk_v;
     uint8_t* part_k;
     uint8_t* part_v;
-    if constexpr (PAGED) {
+    long long new_k = 0, new_v = 0;                          // kChunk: elements between rows from row `split` on
+    int split = G;                                           // (blk_k and blk_v as if all rows were new)
+    const __half *old_k = nullptr, *old_v = nullptr;         // rows before it, D elements apart
+    if constexpr (MODE == kChunk) {
+        const ChunkJob& jb = a.jobs[blockIdx.x];
+        const int h = blockIdx.y;
+        const long long slot = ((long long)jb.seq * a.Hkv + h) * a.R + jb.row0;
+        old_k = a.resid_k + slot * D;
+        old_v = a.resid_v + slot * D;
+        split = jb.n_resid - jb.row0;
+        new_k = a.k_stride[0];
+        new_v = a.v_stride[0];
+        blk_k = a.new_k + ((long long)jb.tok0 - split) * new_k + h * a.k_stride[1];
+        blk_v = a.new_v + ((long long)jb.tok0 - split) * new_v + h * a.v_stride[1];
+        part_k = a.pool + ((long long)jb.page * a.Hkv + h) * 2 * a.part_bytes;
+        part_v = part_k + a.part_bytes;
+        if (h == 0 && tid == 0) a.table[jb.tbl_idx] = jb.page;
+    } else if constexpr (MODE == kPaged) {
         const QJob& jb = a.jobs[blockIdx.x];
         const int h = blockIdx.y;
         const long long off = jb.src_off + h * a.src_head_elems;
@@ -195,16 +228,17 @@ __global__ void __launch_bounds__(kQuantThreads)
         part_v = part_k + a.NB * a.part_bytes;
     }
     const long long tiles_bytes = (long long)TPB * a.tile_bytes;
-    auto stage_rows = [&](const __half* src) {
+    auto stage_rows = [&](const __half* src, const __half* old, long long step) {
         const uint4* s4 = reinterpret_cast<const uint4*>(src);
         for (int v = tid; v < G * D / 8; v += kQuantThreads) {
             const int row = v / (D / 8), c8 = v - row * (D / 8);
-            *reinterpret_cast<uint4*>(xs + row * DP + 8 * c8) = s4[v];
+            if constexpr (MODE == kChunk) s4 = reinterpret_cast<const uint4*>(row < split ? old + row * D : src + row * step);
+            *reinterpret_cast<uint4*>(xs + row * DP + 8 * c8) = s4[MODE == kChunk ? c8 : v];
         }
     };
 
     // ---------------- keys: per channel over the block's G tokens ----------------
-    stage_rows(blk_k);
+    stage_rows(blk_k, old_k, new_k);
     __syncthreads();
     // min / max of channel pairs (2cp, 2cp+1) over the G tokens on fp16 pairs (exact);
     // adjacent threads take alternate blocks of 4 tokens (rows 4 apart fall 16
@@ -295,11 +329,11 @@ __global__ void __launch_bounds__(kQuantThreads)
     __syncthreads();
 
     // ---------------- values: per token over groups of G channels ----------------
-    stage_rows(blk_v);
+    stage_rows(blk_v, old_v, new_v);
     __syncthreads();
     const int ngrp = D / G;                 // channel groups per token; G * ngrp == D entries
     long long vfirst = 0;                   // slot position of the block's first token (value limit)
-    if constexpr (!PAGED) vfirst = (a.first_block + (long long)blockIdx.x) * G;
+    if constexpr (MODE == kDense) vfirst = (a.first_block + (long long)blockIdx.x) * G;
     for (int e = tid; e < D; e += kQuantThreads) {
         const int t = e / ngrp, gr = e % ngrp;
         const __half* row = xs + t * DP + gr * G;
@@ -315,7 +349,7 @@ __global__ void __launch_bounds__(kQuantThreads)
         }
         const float2 mnf = __half22float2(mn2), mxf = __half22float2(mx2);
         float mn = fminf(mnf.x, mnf.y), mx = fmaxf(mxf.x, mxf.y);
-        if constexpr (!PAGED) {
+        if constexpr (MODE == kDense) {
             // a value token not quantized yet: step 0 and zero point 0, so codes 0
             if (vfirst + t >= a.vlimit) mn = mx = 0.0f;
         }
@@ -492,13 +526,13 @@ __global__ void __launch_bounds__(128) copy_rows_kernel(uint8_t* cache, const __
     }
 }
 
-template <bool PAGED>
-cudaError_t launch_q(const typename QuantArgsOf<PAGED>::type& a, const Geometry& g, dim3 grid, cudaStream_t st) {
+template <int MODE>
+cudaError_t launch_q(const typename QuantArgsOf<MODE>::type& a, const Geometry& g, dim3 grid, cudaStream_t st) {
     // staged rows + (step, 1/step, zero) per group + three fp16 level thresholds per group
     const size_t smem = (size_t)g.G * (g.D + 8) * 2 + 16 * (size_t)g.D + 6 * (size_t)g.D;
 #define KIVI_Q(DD, BB, GG)                                                                      \
     if (g.D == DD && g.bits == BB && g.G == GG) {                                               \
-        quantize_blocks_kernel<DD, BB, GG, PAGED><<<grid, kQuantThreads, smem, st>>>(a);        \
+        quantize_blocks_kernel<DD, BB, GG, MODE><<<grid, kQuantThreads, smem, st>>>(a);        \
         return cudaGetLastError();                                                              \
     }
 #define KIVI_QG(DD, BB) KIVI_Q(DD, BB, 32) KIVI_Q(DD, BB, 64) if (DD >= 128) { KIVI_Q(128, BB, 128) }
@@ -516,7 +550,7 @@ cudaError_t launch_quantize_blocks(const Geometry& g, uint8_t* cache, const __ha
     QuantArgs a{cache, src_k, src_v, src_slot_elems, first_block, g.NB, g.part_bytes,
                 g.slot_bytes, g.tile_bytes, vlimit, g.G};
     const dim3 grid((unsigned)nblk, (unsigned)(g.B * g.Hkv));
-    return launch_q<false>(a, g, grid, st);
+    return launch_q<kDense>(a, g, grid, st);
 }
 
 cudaError_t launch_quantize_pages(const PagedGeometry& pg, uint8_t* buf, const __half* src_k,
@@ -537,7 +571,38 @@ cudaError_t launch_quantize_pages(const PagedGeometry& pg, uint8_t* buf, const _
     for (int j0 = 0; j0 < njobs; j0 += kMaxQJobs) {
         const int nj = njobs - j0 < kMaxQJobs ? njobs - j0 : kMaxQJobs;
         for (int j = 0; j < nj; ++j) a.jobs[j] = jobs[j0 + j];
-        const cudaError_t e = launch_q<true>(a, g, dim3((unsigned)nj, (unsigned)g.Hkv), st);
+        const cudaError_t e = launch_q<kPaged>(a, g, dim3((unsigned)nj, (unsigned)g.Hkv), st);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_quantize_chunk(const PagedGeometry& pg, uint8_t* buf, const __half* k, const long long* k_stride,
+                                  const __half* v, const long long* v_stride, const ChunkJob* jobs, int n,
+                                  cudaStream_t st, int* launches) {
+    const Geometry& g = pg.g;
+    ChunkQuantArgs a;          // ~24 KB of kernel parameters
+    a.pool = buf;
+    a.table = reinterpret_cast<int*>(buf + pg.table_off);
+    a.resid_k = reinterpret_cast<const __half*>(buf + g.k_resid_off);
+    a.resid_v = reinterpret_cast<const __half*>(buf + g.v_resid_off);
+    a.new_k = k;
+    a.new_v = v;
+    for (int j = 0; j < 2; ++j) {
+        a.k_stride[j] = k_stride[j];
+        a.v_stride[j] = v_stride[j];
+    }
+    a.part_bytes = g.part_bytes;
+    a.tile_bytes = g.tile_bytes;
+    a.Hkv = g.Hkv;
+    a.G = g.G;
+    a.R = g.R;
+    *launches = 0;
+    for (int j0 = 0; j0 < n; j0 += kMaxChunkJobs) {
+        const int nj = n - j0 < kMaxChunkJobs ? n - j0 : kMaxChunkJobs;
+        for (int j = 0; j < nj; ++j) a.jobs[j] = jobs[j0 + j];
+        const cudaError_t e = launch_q<kChunk>(a, g, dim3((unsigned)nj, (unsigned)g.Hkv), st);
         if (e != cudaSuccess) return e;
         ++*launches;
     }

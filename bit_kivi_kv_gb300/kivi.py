@@ -58,6 +58,18 @@ class kivi_qkv(ctypes.Structure):
                 ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p)]
 
 
+class kivi_chunk(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_longlong * 2), ("k_stride", ctypes.c_longlong * 2),
+                ("v_stride", ctypes.c_longlong * 2), ("out_stride", ctypes.c_longlong * 2),
+                ("softmax_scale", ctypes.c_float), ("cap", ctypes.c_float), ("window", ctypes.c_int),
+                ("slopes", ctypes.c_void_p)]
+
+
+_CHUNK = struct.Struct("@PPPPqqqqqqqqffiP")   # kivi_chunk, field by field
+assert _CHUNK.size == ctypes.sizeof(kivi_chunk)
+_PAIR = struct.Struct("@qq")                  # the strides of kivi_paged_append_chunk
+
 _QKV = struct.Struct("@iiiiqiPPPqqqqqqqqqPPfPqiiPiqPPP")   # kivi_qkv, field by field
 assert _QKV.size == ctypes.sizeof(kivi_qkv)
 
@@ -116,6 +128,12 @@ def _load():
         "kivi_paged_block_scores": (I, [P, IP, I, P, F, P, LL, P]),
         "kivi_paged_decode_blocks": (I, [P, IP, I, P, P, I, P, F, P]),
         "kivi_paged_append": (I, [P, IP, I, P, P, P]),
+        "kivi_paged_chunk_workspace_bytes": (SZ, [pcfgp]),
+        "kivi_paged_chunk_attn": (I, [P, IP, IP, I, P, P, SZ, P]),   # a kivi_chunk by reference, or its packed bytes
+        "kivi_paged_append_chunk": (I, [P, IP, IP, I, P, P, P, P, P]),   # strides: addresses, or packed bytes
+        "kivi_paged_fork": (I, [P, IP, I, IP, P]),
+        "kivi_paged_truncate": (I, [P, I, LL]),
+        "kivi_paged_read": (I, [P, IP, I, LL, LL, P, P, P]),
         "kivi_qk_norm_rope": (I, [P, P]),     # a kivi_qkv by reference, or its packed bytes
         "kivi_append_qkv": (I, [P, P, P]),
     }
@@ -320,6 +338,35 @@ def kivi_paged_decode_blocks(h: int, seqs, q: int, blocks: int, n_list: int, out
 
 def kivi_paged_append(h: int, seqs, k: int, v: int, stream: int):
     _check(lib.kivi_paged_append(h, _seq_array(seqs), len(seqs), k, v, stream))
+
+
+# ---- chunks of new tokens ---------------------------------------------------------
+def kivi_paged_chunk_workspace_bytes(cfg: kivi_paged_config) -> int:
+    return lib.kivi_paged_chunk_workspace_bytes(ctypes.byref(cfg))
+
+
+def kivi_paged_chunk_attn(h: int, seqs, lens, args: kivi_chunk, workspace: int, ws_bytes: int, stream: int):
+    _check(lib.kivi_paged_chunk_attn(h, _seq_array(seqs), _seq_array(lens), len(seqs), ctypes.byref(args), workspace,
+                                     ws_bytes, stream))
+
+
+def kivi_paged_append_chunk(h: int, seqs, lens, k: int, k_stride, v: int, v_stride, stream: int):
+    _check(lib.kivi_paged_append_chunk(h, _seq_array(seqs), _seq_array(lens), len(seqs), k, _PAIR.pack(*k_stride), v,
+                                       _PAIR.pack(*v_stride), stream))
+
+
+def kivi_paged_fork(h: int, seqs, stream: int) -> list:
+    out = (ctypes.c_int * max(len(seqs), 1))()
+    _check(lib.kivi_paged_fork(h, _seq_array(seqs), len(seqs), out, stream))
+    return list(out[:len(seqs)])
+
+
+def kivi_paged_truncate(h: int, seq: int, n_tokens: int):
+    _check(lib.kivi_paged_truncate(h, seq, n_tokens))
+
+
+def kivi_paged_read(h: int, seqs, first: int, count: int, K: int, V: int, stream: int):
+    _check(lib.kivi_paged_read(h, _seq_array(seqs), len(seqs), first, count, K, V, stream))
 
 
 # ---- norm and rotation of queries and keys -----------------------------------------
@@ -663,6 +710,7 @@ class KiviPagedCache:
                                      device)
         self.handle = kivi_paged_create(self.cfg, self.buffer.data_ptr(), nbytes)
         self._heads = (n_q_heads, n_kv_heads, head_dim)
+        self._chunk_ws = kivi_paged_chunk_workspace_bytes(self.cfg)
         self._device = self.buffer.get_device()
 
     def _alloc(self, nbytes, device):
@@ -752,3 +800,89 @@ class KiviPagedCache:
             n_keep = min(n_keep, scores.shape[-1])
             blocks = select_blocks(scores, n_keep, min(keep_first, n_keep))
             return self.decode_blocks(seqs, q, blocks, out, softmax_scale)
+
+    def _chunk(self, t, what, tokens, heads, device):
+        """Checks a chunk's tensor [tokens, heads, head_dim] (fp16, any strides with dense
+        channels); its strides over tokens and heads."""
+        shape = (tokens, heads, self._heads[2])
+        if t.dtype is not _torch.float16 or t.shape != shape or t.get_device() != device or t.stride(2) != 1:
+            raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be a float16 tensor of shape {shape} with dense channels "
+                                                  f"on the current device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.stride(0), t.stride(1)
+
+    @staticmethod
+    def _lens(seqs, lens):
+        """The lengths of a chunk call, one for each sequence."""
+        if len(lens) != len(seqs):
+            raise KiviError(KIVI_ERR_INVALID_ARG, f"{len(seqs)} sequences, {len(lens)} lengths")
+        return _seq_array(lens), sum(lens)
+
+    def chunk_attn(self, seqs, lens, q, k, v, out=None, softmax_scale=0.0, cap=0.0, window=0, slopes=None, stream=None):
+        """Attention of lens[i] new tokens of each listed sequence over its cached tokens
+        and, causally, over the new tokens themselves (kivi_paged_chunk_attn).  q
+        [T, Hq, D], k and v [T, Hkv, D] fp16, T = sum(lens), the sequences' tokens behind
+        each other, any strides with dense channels; returns [T, Hq, D].  cap: scores
+        become cap * tanh(score / cap); slopes fp32 [Hq]: a bias of slope * (t - position);
+        window: tokens that a query sees, itself included (0: all).  The new tokens are
+        not appended (append_chunk)."""
+        (hq, hkv, d), device = self._heads, _on(self)
+        n_arr, tokens = self._lens(seqs, lens)
+        qs = self._chunk(q, "q", tokens, hq, device)
+        ks = self._chunk(k, "k", tokens, hkv, device)
+        vs = self._chunk(v, "v", tokens, hkv, device)
+        if out is None:
+            out = _new((tokens, hq, d), _torch.float16, q.device, stream)
+        os_ = self._chunk(out, "out", tokens, hq, device)
+        if slopes is not None:
+            _expect(slopes, "slopes", _torch.float32, (hq,), device)
+        # scratch of this call alone, from its stream's memory: calls on other streams and in graphs share nothing
+        ws = _new((self._chunk_ws,), _torch.uint8, q.device, stream)
+        args = _CHUNK.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *qs, *ks, *vs, *os_, softmax_scale, cap,
+                           window, slopes.data_ptr() if slopes is not None else 0)
+        _check(lib.kivi_paged_chunk_attn(self.handle, _seq_array(seqs), n_arr, len(seqs), args, ws.data_ptr(), self._chunk_ws,
+                                         _current_stream(device) if stream is None else stream.cuda_stream))
+        return out
+
+    def append_chunk(self, seqs, lens, k, v, stream=None):
+        """Append lens[i] tokens to each listed sequence: k and v [T, Hkv, D] fp16 as in
+        chunk_attn (kivi_paged_append_chunk)."""
+        (_, hkv, _), device = self._heads, _on(self)
+        n_arr, tokens = self._lens(seqs, lens)
+        ks = self._chunk(k, "k", tokens, hkv, device)
+        vs = self._chunk(v, "v", tokens, hkv, device)
+        _check(lib.kivi_paged_append_chunk(self.handle, _seq_array(seqs), n_arr, len(seqs), k.data_ptr(), _PAIR.pack(*ks),
+                                           v.data_ptr(), _PAIR.pack(*vs),
+                                           _current_stream(device) if stream is None else stream.cuda_stream))
+
+    def extend(self, seqs, lens, q, k, v, out=None, softmax_scale=0.0, cap=0.0, window=0, slopes=None, stream=None):
+        """chunk_attn, then append_chunk: a piece of a prompt in one go."""
+        with _torch.cuda.stream(stream):
+            out = self.chunk_attn(seqs, lens, q, k, v, out, softmax_scale, cap, window, slopes)
+            self.append_chunk(seqs, lens, k, v)
+            return out
+
+    def fork(self, seqs, stream=None) -> list:
+        """A new sequence with the same tokens for each listed one (which may be listed
+        several times): its pages shared, its residual its own (kivi_paged_fork)."""
+        device = _on(self)
+        return kivi_paged_fork(self.handle, list(seqs),
+                               _current_stream(device) if stream is None else stream.cuda_stream)
+
+    def truncate(self, seq: int, n_tokens: int):
+        """Forget the sequence's tokens from n_tokens on (kivi_paged_truncate)."""
+        kivi_paged_truncate(self.handle, seq, n_tokens)
+
+    def read(self, seqs, first, count, out=None, stream=None):
+        """Tokens [first, first + count) of each listed sequence in fp16, dequantized:
+        (K, V), each [n, Hkv, count, D] (kivi_paged_read)."""
+        (_, hkv, d), device = self._heads, _on(self)
+        shape, f16 = (len(seqs), hkv, max(count, 0), d), _torch.float16
+        if out is None:
+            K, V = out = _new(shape, f16, self.buffer.device, stream), _new(shape, f16, self.buffer.device, stream)
+        else:
+            K, V = out
+            _expect(K, "out[0]", f16, shape, device)
+            _expect(V, "out[1]", f16, shape, device)
+        _check(lib.kivi_paged_read(self.handle, _seq_array(seqs), len(seqs), first, count, K.data_ptr(), V.data_ptr(),
+                                   _current_stream(device) if stream is None else stream.cuda_stream))
+        return out

@@ -523,6 +523,107 @@ kivi_status kivi_paged_decode_blocks(kivi_paged_t cache, const int* seqs, int n,
 kivi_status kivi_paged_append(kivi_paged_t cache, const int* seqs, int n, const void* k, const void* v,
                               kivi_stream_t stream);
 
+/* ===================== Chunks of new tokens =====================
+ *
+ * Calls that bring several tokens of a sequence at once to the paged cache: a
+ * piece of a prompt, the proposals of a draft model, several continuations of
+ * one prompt.  The method's description has no counterpart.
+ *
+ *     kivi_paged_chunk_attn     attention of the new tokens' queries over the
+ *                               cached tokens and over the new tokens
+ *     kivi_paged_append_chunk   the new tokens (or the first of them) stored
+ *     kivi_paged_fork           new sequences with another's tokens
+ *     kivi_paged_truncate       a sequence's last tokens forgotten
+ *     kivi_paged_read           cached tokens as fp16
+ *
+ * A call lists n distinct live sequences (host array) and the number of new
+ * tokens of each (host array, 0 allowed: the sequence is passed over).  The new
+ * tokens of all sequences lie behind each other, in the list's order, in tensors
+ * [tokens][heads][head_dim] with any strides (elements; multiples of 16 bytes;
+ * token, head) and dense channels, 16-byte aligned.
+ */
+typedef struct {
+    const void *q, *k, *v;    /* fp16: query heads; kv heads */
+    void* out;                /* fp16, as q; must not overlap an input */
+    long long q_stride[2], k_stride[2], v_stride[2], out_stride[2];
+    float softmax_scale;      /* <= 0: 1/sqrt(D) */
+    float cap;                /* > 0: scores are capped; 0: not */
+    int window;               /* > 0: a query sees that many tokens, itself the last; 0: all */
+    const float* slopes;      /* device, [n_q_heads], or null: no distance bias */
+} kivi_chunk;
+
+/* Bytes of workspace of a kivi_paged_chunk_attn call on any device; 0 if cfg is
+ * invalid.  Host-only. */
+size_t kivi_paged_chunk_workspace_bytes(const kivi_paged_config* cfg);
+
+/*
+ * Attention of a chunk.  With L tokens cached in a sequence, its new token i has
+ * position L + i and sees the tokens t <= L + i (with a window w, those of them
+ * with t > L + i - w): the cached ones as the cache holds them, the new ones
+ * from k and v.
+ *
+ *     x_t = scale q . k_t;  capped: x_t = cap tanh(x_t / cap)
+ *     x_t += slope_h (t - (L + i))
+ *     out = sum_t softmax_t(x) v_t
+ *
+ * The cache is not changed (the new tokens are not appended).  Dequantized keys
+ * and values are rounded to fp16, and so are the attention weights (times a
+ * power of two that keeps them in range); sums are fp32.  A dequantized value
+ * beyond fp16's range is infinite here.  A new or residual token whose value
+ * row holds a number that is not finite makes the outputs that see it NaN, and no
+ * other.  A block-table entry outside the pool, or a copy that does not complete
+ * (see "Failure detection"), makes the outputs that depend on it NaN.
+ *
+ * workspace: 256-byte aligned device scratch of
+ * ws_bytes >= kivi_paged_chunk_workspace_bytes(cfg); garbage afterwards.  Calls
+ * that may run at once need one each.  At most 2^30 tokens in a sequence, cached
+ * and new.
+ */
+kivi_status kivi_paged_chunk_attn(kivi_paged_t cache, const int* seqs, const int* lens, int n, const kivi_chunk* args,
+                                  void* workspace, size_t ws_bytes, kivi_stream_t stream);
+
+/*
+ * Append a chunk: k, v fp16 [tokens][Hkv][D].  A sequence of L tokens of which
+ * Lq are quantized gets n more, and as many whole blocks as a prompt of its
+ * L + n tokens would have are quantized:
+ * Lq <- max(Lq, G * ceil(max(L + n - R, 0) / G)); the tokens behind them are its
+ * residual.  So a prompt appended in pieces gives the cache that kivi_paged_add
+ * gives for the whole, bit for bit.  (A single token appended to a full residual
+ * quantizes one block of G here, all R tokens with kivi_paged_append.)
+ * KIVI_ERR_CAPACITY when a sequence or the pool has no room; every check runs
+ * before anything is launched.
+ */
+kivi_status kivi_paged_append_chunk(kivi_paged_t cache, const int* seqs, const int* lens, int n, const void* k,
+                                    const long long* k_stride, const void* v, const long long* v_stride,
+                                    kivi_stream_t stream);
+
+/*
+ * Branches: for each of the n live sequences seqs[i] (host array; one may be
+ * listed several times) a new sequence out[i] that holds the same tokens.  It
+ * shares the quantized pages (a page is free when the last sequence that holds it
+ * is released) and has residual rows of its own, so either may be
+ * appended to, truncated or released without the other.  KIVI_ERR_CAPACITY when
+ * fewer than n sequence slots are free.
+ */
+kivi_status kivi_paged_fork(kivi_paged_t cache, const int* seqs, int n, int* out, kivi_stream_t stream);
+
+/*
+ * Forget a sequence's tokens from n_tokens on (host only, no device work; pages
+ * that become free as with kivi_paged_release).  n_tokens is at least Lq, or a
+ * multiple of the group size (the residual is then empty);
+ * KIVI_ERR_UNSUPPORTED otherwise: a quantized block is kept or dropped whole.
+ */
+kivi_status kivi_paged_truncate(kivi_paged_t cache, int seq, long long n_tokens);
+
+/*
+ * Tokens [first, first + count) of the n live sequences seqs[i] (host array) as
+ * fp16 [n][Hkv][count][D]: quantized ones as fp16(code * s + z), residual ones
+ * as they are.  Every sequence must hold them.  A block-table entry outside the
+ * pool makes its tokens NaN.
+ */
+kivi_status kivi_paged_read(kivi_paged_t cache, const int* seqs, int n, long long first, long long count, void* K,
+                            void* V, kivi_stream_t stream);
+
 /* ===================== Norm and rotation of queries and keys =====================
  *
  * From a projection's output to the cache's inputs in one pass: each head row
