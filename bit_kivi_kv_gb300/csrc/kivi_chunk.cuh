@@ -173,7 +173,7 @@ struct ChunkArgs {
     __half* out;
     long long q_stride[2], k_stride[2], v_stride[2], out_stride[2];   // token, head (elements)
     long long page_bytes, part_bytes, k_resid_off, v_resid_off;
-    int R, G, Hq, max_blocks, n_pages, n_seqs, n_ctas;
+    int R, lgG, Hq, max_blocks, n_pages, n_seqs, n_ctas;   // lgG: log2 of the group size
     float scale_log2;   // scores to base-2 logits
     float cap;          // > 0: scores are capped at it
     float scale;        // softmax_scale

@@ -18,10 +18,12 @@
 // Roles (warps):
 //   0-3, 4-7   softmax of tile A / B, a row a lane: logits from tensor memory, running
 //              maximum, exponentials, probabilities back as fp16; epilogue
-//   8-11       keys: 32 tokens of a tile each, from codes to fp16 in shared memory
+//   8-11       keys: 32 tokens of a tile each, from codes to fp16 in shared memory; the
+//              next tile's bytes are loaded into registers as this one's are used up
 //   12-15      values, the same, transposed ([channel][token])
 //   16         issues the MMAs
-//   17         copies the quantized bytes (bulk copies into a ring of 32-token units)
+//   17         finds the spans of items that the CTA works on, ahead of the others (18, 19: idle,
+//              they fill their warpgroup for the redistribution of registers)
 //
 // Dequantization: a code pair masked in place and OR-ed with fp16 1024 is
 // 1024 + code * 2^pos, exact; one FMA makes it the code, a second one
@@ -36,8 +38,8 @@
 // memory are then scaled), which leaves the result the same.
 //
 // A value row that is not finite would reach rows that do not see it
-// through the product (0 * inf): it is taken as zeros, and its key as NaN, so that
-// exactly the rows that see it become NaN.
+// through the product (0 * inf): it is taken as zeros and noted, and the rows that
+// see it become NaN at the end.
 #pragma once
 
 #include <math.h>
@@ -49,7 +51,11 @@ namespace chunk_detail {
 
 using namespace mma_detail;
 
-constexpr int kChunkWarps = 18, kChunkThreads = 32 * kChunkWarps;
+constexpr int kChunkWarps = 20, kChunkThreads = 32 * kChunkWarps;
+// Registers a thread: the launch's, and what the five warpgroups (A, B, keys, values, the rest) make of them.
+constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsFill = 88, kRegsRest = 48;
+static_assert(2 * kRegsSoftmax + 2 * kRegsFill + kRegsRest <= 5 * kRegs, "registers of the launch");
+constexpr int kSpanRing = 4, kSpanReaders = 17;
 constexpr float kRaise = 7.f;      // base-2 logits above the reference that a tile may have
 constexpr float kLift = 8.f;       // probabilities are held times 2^8
 constexpr float kLog2e = 1.4426950408889634f;
@@ -59,37 +65,42 @@ struct Shape {
     static constexpr int KCH = D / 8;                     // 8-channel groups of a token
     static constexpr int W = D * BITS / 64;               // words of a lane in a 16-token code tile
     static constexpr int TILE = 2 * D * BITS;             // bytes of a code tile
-    // one 32-token unit in the ring: key codes, key steps and zeros, value codes, value steps and zeros
-    static constexpr int KC = 0, KE = 2 * TILE, VC = KE + 4 * D, VE = VC + 2 * TILE, UNIT = VE + 4 * D;
-    static constexpr int UNITS = BITS == 2 || D == 64 ? 8 : BITS == 4 ? 6 : 3;
-    // Barriers of the copies: a multiple of UNITS and of the four units of a tile, eight at least.  A warp that
-    // waits for a unit knows then that the one before it on its barrier has come (it is of the warp's
-    // last tile, or of one whose stage has been freed), so that the parity says which of the two is meant.
-    static constexpr int FULLS = UNITS == 8 ? 8 : 12;
     static constexpr int Q_BYTES = kHalf * D * 2;         // one tile of queries
     static constexpr int K_BYTES = kTile * D * 2;         // one stage of keys (values: the same)
-    static constexpr int OFF_Q = 0, OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + 2 * K_BYTES, OFF_RING = OFF_V + 2 * K_BYTES;
-    static constexpr int OFF_BAR = OFF_RING + UNITS * UNIT;
-    static constexpr int OFF_XCH = OFF_BAR + 512;         // (m, l) of tile B's rows
+    static constexpr int OFF_Q = 0, OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + 2 * K_BYTES, OFF_ENT = OFF_V + 2 * K_BYTES;
+    static constexpr int OFF_BAR = OFF_ENT + 8 * 4 * D;   // steps and zeros of the unit that each filling warp works on
+    static constexpr int OFF_XCH = OFF_BAR + 1024;         // (m, l) of tile B's rows
     static constexpr int BYTES = OFF_XCH + kHalf * 8 + 1024;   // (base aligned to 1024)
     // one CTA per SM, also where less shared memory is needed: it takes all of the SM's tensor memory
     static constexpr int SMEM = BYTES < 117 * 1024 ? 117 * 1024 : BYTES;
     static constexpr int COL_S = 0, COL_O = 256;          // tensor memory columns: S of A and B, O of A and B
     static_assert(SMEM <= 232448, "shared memory");
-    static_assert(UNIT % 16 == 0, "bulk copies");
-    static_assert(FULLS % UNITS == 0 && FULLS % 4 == 0 && FULLS >= 8 && FULLS <= 12 && UNITS <= 8, "ring barriers");
+};
+
+// What the roles know of a span: the tiles [tile0, tile0 + nt) of an item's keys for its rows.
+struct Span {
+    int more;                   // 0: there is none
+    int seq, tok0, n_quant, n_resid;
+    int t0, t1, head;           // the item's tokens of the chunk, kv head
+    int tile0, nt, na, nb;      // key tiles, of tile A, of tile B
+    int both;                   // A and B are different rows (else the same, alternate tiles)
+    int first, whole;           // holds the item's first tile, all of them
+    int pad;
+    __device__ __forceinline__ int tiles(int x) const { return x ? nb : na; }
+    __device__ __forceinline__ int tile(int x, int i) const { return both ? i : 2 * i + x; }   // of x's step i
 };
 
 struct Bars {
-    uint64_t ring_full[12], ring_empty[8];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t span_full[kSpanRing], span_empty[kSpanRing];
     uint64_t drained;
     uint32_t tmem;
     int failed;         // a wait ran out: the outputs from here on are NaN
-    unsigned bad;       // spans with a block-table entry outside the pool: bit number % 32
+    unsigned bad, odd;  // spans with a block-table entry outside the pool, with a value that is not finite: bit number % 32
+    alignas(16) Span spans[kSpanRing];
 };
-static_assert(sizeof(Bars) <= 512, "barriers");
+static_assert(sizeof(Bars) <= 1024, "barriers");
 
 // ---- tensor memory and tcgen05 ----
 __device__ __forceinline__ void tmem_alloc(uint32_t* out) {
@@ -101,9 +112,12 @@ __device__ __forceinline__ void tmem_free(uint32_t at) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+        "r"(one)
+        : "memory");
 }
 __device__ __forceinline__ void ld32(uint32_t at, float (&x)[32]) {
     uint32_t* r = reinterpret_cast<uint32_t*>(x);
@@ -146,18 +160,30 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr) {
 __host__ __device__ constexpr uint32_t mma_kind(int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+// (by the lane whose `one` is set)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add, uint32_t one) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add), "r"(one)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add, uint32_t one) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add), "r"(one)
         : "memory");
 }
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one;
+}
+template <int N>
+__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 __device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -174,30 +200,36 @@ template <int ID, int N>
 __device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
 
 // Wait for an mbarrier's phase, about two seconds at most; a wait that runs out marks the CTA,
-// and no wait of a marked CTA waits.
+// and no wait of a marked CTA waits, but a patient one (for spans: they keep coming).
+template <bool PATIENT = false>
 __device__ __forceinline__ bool wait_for(Bars& b, uint64_t* bar, uint32_t parity) {
     const uint32_t addr = smem_u32(bar);
     if (mbar_try(addr, parity)) return true;
     volatile int* failed = &b.failed;
-    const uint64_t t0 = global_ns();
-    for (uint32_t it = 0; it < (1u << 26); ++it) {
+    uint64_t t0 = 0;           // (reading the timer takes about a microsecond: not before 256 polls)
+    for (uint32_t it = 1; it < (1u << 26); ++it) {
         if (mbar_try(addr, parity)) return true;
-        if (*failed) return false;
-        if ((it & 63u) == 63u && global_ns() - t0 > 2000000000ull) break;
+        if (it % 256 == 0) {
+            if (!PATIENT && *failed) return false;
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > 2000000000ull) break;
+        }
     }
     *failed = 1;
     return false;
 }
 
+// a lane's words of a code tile
 template <int W>
-__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[W]) {
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[W]) {
     if constexpr (W == 2) {
-        const uint2 v = lds64(at);
+        const uint2 v = ldg_stream2(p);
         w[0] = v.x; w[1] = v.y;
     } else {
 #pragma unroll
         for (int j = 0; j < W / 4; ++j) {
-            const uint4 v = lds128(at + 16 * j);
+            const uint4 v = ldg_stream(p + 16 * j);
             w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
         }
     }
@@ -222,21 +254,21 @@ __device__ __forceinline__ void key_groups(const uint32_t (&w)[W], uint32_t ent,
 // Values of a 16-token code tile into columns (tokens) tok0 .. tok0 + 15 of the operand [D channels][tokens] at dst.
 // ent: the tile's steps, channel group j's at 32 j (this lane's four tokens at 8 i), zeros 32 D/G bytes on.
 template <int D, int BITS, int C, int W>
-__device__ __forceinline__ void value_groups(const uint32_t (&w)[W], uint32_t ent, int G, uint2 s, uint2 z, uint32_t dst,
+__device__ __forceinline__ void value_groups(const uint32_t (&w)[W], uint32_t ent, int lgG, uint2 s, uint2 z, uint32_t dst,
                                              int tok0, int lane) {
     if constexpr (C < D / 8) {
         if constexpr (8 * C % 32 == 0) {
-            if ((8 * C & (G - 1)) == 0) {
-                const uint32_t at = ent + 32 * (8 * C / G) + 8 * (lane & 3);
+            if (((8 * C) & ((1 << lgG) - 1)) == 0) {
+                const uint32_t at = ent + 32 * ((8 * C) >> lgG) + 8 * (lane & 3);
                 s = lds64(at);
-                z = lds64(at + 32 * (D / G));
+                z = lds64(at + 32 * (D >> lgG));
             }
         }
         const int row = 8 * (C + (lane >> 4)) + (lane & 7), chunk = (tok0 >> 3) + ((lane >> 3) & 1);
         stmatrix4(dst + operand_at<D>(row, chunk), hfma2(code_of<BITS, C, 0>(w), s.x, z.x),
                   hfma2(code_of<BITS, C, 1>(w), s.y, z.y), hfma2(code_of<BITS, C + 1, 0>(w), s.x, z.x),
                   hfma2(code_of<BITS, C + 1, 1>(w), s.y, z.y));
-        value_groups<D, BITS, C + 2>(w, ent, G, s, z, dst, tok0, lane);
+        value_groups<D, BITS, C + 2>(w, ent, lgG, s, z, dst, tok0, lane);
     }
 }
 
@@ -260,6 +292,11 @@ __device__ __forceinline__ bool not_finite(const uint4& v) {
     return pair_not_finite(v.x) || pair_not_finite(v.y) || pair_not_finite(v.z) || pair_not_finite(v.w);
 }
 
+// 16 bytes global -> shared, asynchronous; zeros instead where there are none
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
 // Where the fp16 rows of a span are: row f of [residual | chunk].
 struct Rows {
     const __half *resid, *chunk;      // kv head's first residual row, its first new token
@@ -269,284 +306,326 @@ struct Rows {
         return f < n_resid ? resid + (long long)f * D : chunk + (long long)(f - n_resid) * step;
     }
 };
-// 32 fp16 rows [f0, f0 + 32) (zeros behind the last) as keys; rows whose values are not finite become NaN.
+// 32 fp16 rows [f0, f0 + 32) (zeros behind the last) as keys.
 template <int D>
-__device__ __forceinline__ void key_rows(const Rows& k, const Rows& v, int f0, uint32_t dst, int row0, int lane) {
-    constexpr int LPR = D / 8, RPI = 32 / LPR, N = 32 / RPI;   // lanes a row, rows an instruction
+__device__ __forceinline__ void key_rows(const Rows& k, int f0, uint32_t dst, int row0, int lane) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR;                 // lanes a row, rows an instruction
     const int lr = lane % LPR, sub = lane / LPR;
-#pragma unroll
-    for (int h = 0; h < N; h += 4) {
-        uint4 x[4], y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int f = f0 + (h + j) * RPI + sub;
-            x[j] = y[j] = uint4{0, 0, 0, 0};
-            if (f < k.n) {
-                x[j] = ldg_row(k.at(f, D) + 8 * lr);
-                y[j] = ldg_row(v.at(f, D) + 8 * lr);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const unsigned odd = __ballot_sync(kFull, not_finite(y[j]));
-            if (odd) {
-                const unsigned mine = LPR == 16 ? (0xffffu << (16 * sub)) : (0xffu << (8 * sub));
-                if (odd & mine) x[j] = uint4{0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu};
-            }
-            sts128(dst + operand_at<kTile>(row0 + (h + j) * RPI + sub, lr), x[j]);
-        }
+#pragma unroll 4
+    for (int h = 0; h < 32; h += RPI) {
+        const int f = f0 + h + sub;
+        cp_async16_or_zero(dst + operand_at<kTile>(row0 + h + sub, lr), k.at(f < k.n ? f : 0, D) + 8 * lr, f < k.n);
     }
+    cp_async_wait_all();
 }
 // The same rows as values, transposed.  A lane loads 8 channels of a token; as matrices of
 // (8 tokens) x (channel pairs of four lanes) they are stored transposed, each row of a matrix to its channel.
+// Rows that are not finite become zeros; whether there was one.
 template <int D>
-__device__ __forceinline__ void value_rows(const Rows& v, int f0, uint32_t dst, int tok0, int lane) {
+__device__ __forceinline__ bool value_rows(const Rows& v, int f0, uint32_t dst, int tok0, int lane) {
     const int g = lane >> 2, i = lane & 3;
+    unsigned any = 0;
+#pragma unroll 1
+    for (int t2 = 0; t2 < 2; ++t2) {
+        uint4 x[2][D / 32];
 #pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-        uint4 x[D / 32];
-        const int f = f0 + 8 * tt + g;
-        bool odd = false;
+        for (int u = 0; u < 2; ++u) {
+            const int f = f0 + 16 * t2 + 8 * u + g;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-            x[j] = uint4{0, 0, 0, 0};
-            if (f < v.n) x[j] = ldg_row(v.at(f, D) + 8 * (4 * j + i));
-            odd |= not_finite(x[j]);
+            for (int j = 0; j < D / 32; ++j) {
+                x[u][j] = uint4{0, 0, 0, 0};
+                if (f < v.n) x[u][j] = ldg_row(v.at(f, D) + 8 * (4 * j + i));
+            }
         }
-        const unsigned who = __ballot_sync(kFull, odd);
-        if (who >> (4 * g) & 15u) {
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) x[j] = uint4{0, 0, 0, 0};
-        }
-        // matrix m of an instruction: register m, channels 32 j + 8 (r / 2) + 2 m + r % 2 for its rows r
-        const int m = lane >> 3, r = lane & 7;
+        for (int u = 0; u < 2; ++u) {
+            bool odd = false;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-            const int ch = 32 * j + 8 * (r >> 1) + 2 * m + (r & 1);
-            stmatrix4_trans(dst + operand_at<D>(ch, (tok0 >> 3) + tt), x[j].x, x[j].y, x[j].z, x[j].w);
+            for (int j = 0; j < D / 32; ++j) odd |= not_finite(x[u][j]);
+            const unsigned who = __ballot_sync(kFull, odd);
+            any |= who;
+            if (who >> (4 * g) & 15u) {
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) x[u][j] = uint4{0, 0, 0, 0};
+            }
+            // matrix m of an instruction: register m, channels 32 j + 8 (r / 2) + 2 m + r % 2 for its rows r
+            const int m = lane >> 3, r = lane & 7;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                const int ch = 32 * j + 8 * (r >> 1) + 2 * m + (r & 1);
+                stmatrix4_trans(dst + operand_at<D>(ch, (tok0 >> 3) + 2 * t2 + u), x[u][j].x, x[u][j].y, x[u][j].z, x[u][j].w);
+            }
         }
     }
+    return any != 0;
 }
 
-// What every role knows of a span.
-struct Span {
-    int nt;             // tiles
-    int na, nb;         // of tile A, of tile B
-    bool both;          // A and B are different rows (else the same, alternate tiles)
-    int tile0;          // first key tile
-    __device__ __forceinline__ int tiles(int x) const { return x ? nb : na; }
-    __device__ __forceinline__ int tile(int x, int i) const { return both ? i : 2 * i + x; }   // of x's step i
-};
-__device__ __forceinline__ Span span_of(const ChunkArgs& a, const ChunkSpan& s) {
-    Span o;
-    const ChunkSeq& q = a.seqs[s.seq];
-    o.nt = s.last - s.first;
-    o.both = s.it.both;
-    o.tile0 = s.it.lo + s.first;
-    if (o.both) {
-        // tile A's rows end at kHalf: its own last key tile
-        const int ta = last_tile((long long)q.n_quant + q.n_resid, s.it.t0 + kHalf / a.plan.nq) - o.tile0;
-        o.na = ta < 0 ? 0 : ta < o.nt ? ta : o.nt;
-        o.nb = o.nt;
-    } else {
-        o.na = (o.nt + 1) / 2;
-        o.nb = o.nt / 2;
+// ---- spans: one warp finds them, the others read them ----
+inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, int lane) {
+    if (lane == 0) {
+        ChunkWalk walk;
+        walk.start(&a.plan, a.seqs, a.n_seqs, chunk_begin(a.weight, a.n_ctas, blockIdx.x),
+                   chunk_begin(a.weight, a.n_ctas, blockIdx.x + 1LL));
+        uint32_t n = 0;
+        bool more = true;
+        while (more) {
+            more = walk.next();
+            const uint32_t slot = n % kSpanRing;
+            wait_for<true>(b, &b.span_empty[slot], ((n / kSpanRing) & 1) ^ 1);
+            Span o;
+            o.more = more;
+            if (more) {
+                const ChunkItem& it = walk.s.it;
+                const ChunkSeq& q = a.seqs[walk.s.seq];
+                o.seq = q.seq;
+                o.tok0 = q.tok0;
+                o.n_quant = q.n_quant;
+                o.n_resid = q.n_resid;
+                o.t0 = it.t0;
+                o.t1 = it.t1;
+                o.head = walk.s.head;
+                o.tile0 = it.lo + walk.s.first;
+                o.nt = walk.s.last - walk.s.first;
+                o.both = it.both;
+                o.first = walk.s.first == 0;
+                o.whole = walk.s.whole();
+                if (it.both) {
+                    // tile A's rows end at kHalf: its own last key tile
+                    const int ta = last_tile((long long)q.n_quant + q.n_resid, it.t0 + kHalf / a.plan.nq) - o.tile0;
+                    o.na = ta < 0 ? 0 : ta < o.nt ? ta : o.nt;
+                    o.nb = o.nt;
+                } else {
+                    o.na = (o.nt + 1) / 2;
+                    o.nb = o.nt / 2;
+                }
+            }
+            // (the roles are at spans n - 4 to n: a mark of 24 spans ago is nobody's)
+            atomicAnd(&b.bad, ~(1u << ((n + 8) % 32)));
+            atomicAnd(&b.odd, ~(1u << ((n + 8) % 32)));
+            b.spans[slot] = o;
+            arrive(&b.span_full[slot]);
+            ++n;
+        }
     }
-    return o;
+    __syncwarp();
 }
-
-// ---- loader: quantized bytes of the spans' tiles into the ring ----
-template <int D, int BITS>
-__device__ void load_units(const ChunkArgs& a, Bars& b, uint32_t ring, ChunkWalk& walk, int lane) {
-    using S = Shape<D, BITS>;
-    uint32_t uc = 0;
-    unsigned number = 0;                                                         // of spans with quantized tiles
-    while (walk.next()) {
-        const ChunkSeq& q = a.seqs[walk.s.seq];
-        const int first = (walk.s.it.lo + walk.s.first) * kTile;                 // token
-        const int end = min(q.n_quant, (walk.s.it.lo + walk.s.last) * kTile);
-        const int* trow = a.table + (long long)q.seq * a.max_blocks;
-        int have = -1, entry = 0;                                                // 32 table entries, one a lane
-        if (first >= end) continue;
-        ++number;
-        // (the ring lets this warp be 8 such spans ahead of the others at most)
-        if (lane == 0) atomicAnd(&b.bad, ~(1u << ((number + 16) % 32)));
-        for (int t = first; t < end; t += 32, ++uc) {
-            const int blk = t / a.G;
-            if (have < 0 || blk >= have + 32) {
-                have = blk;
-                entry = blk + lane < a.max_blocks ? ldg_int(trow + blk + lane) : 0;
-            }
-            int page = __shfl_sync(kFull, entry, blk - have);
-            if ((unsigned)page >= (unsigned)a.n_pages) {
-                page = 0;
-                if (lane == 0) atomicOr(&b.bad, 1u << (number % 32));
-            }
-            const uint32_t slot = uc % S::UNITS, ph = (uc / S::UNITS) & 1;
-            if (!wait_for(b, &b.ring_empty[slot], ph ^ 1)) break;
-            const uint8_t* kp = a.buf + (long long)page * a.page_bytes + (long long)walk.s.head * 2 * a.part_bytes;
-            const uint8_t* vp = kp + a.part_bytes;
-            const int tile = (t % a.G) / 16, tiles = a.G / 16;
-            const int ve = 64 * (D / a.G);                                       // value entries of a code tile
-            const uint32_t bar = smem_u32(&b.ring_full[uc % S::FULLS]), dst = ring + slot * S::UNIT;
-            if (lane == 0) mbar_expect_tx_u32(bar, 4 * S::TILE + 4 * D + 2 * ve);
+// A warp's view of them: next() gives the next span, which stays in place until the one after is asked for.
+struct SpanReader {
+    Bars& b;
+    uint32_t n;                 // of spans read; the present one is number n - 1
+    __device__ __forceinline__ unsigned mark() const { return 1u << ((n - 1) % 32); }
+    __device__ __forceinline__ explicit SpanReader(Bars& bars) : b(bars), n(0) {}
+    __device__ __forceinline__ const Span* next(int lane) {
+        if (n) {
             __syncwarp();
-            if (lane == 0) tma_1d_u32(dst + S::KC, kp + tile * S::TILE, 2 * S::TILE, bar);
-            if (lane == 1) tma_1d_u32(dst + S::KE, kp + tiles * S::TILE, 4 * D, bar);
-            if (lane == 2) tma_1d_u32(dst + S::VC, vp + tile * S::TILE, 2 * S::TILE, bar);
-            if (lane == 3) tma_1d_u32(dst + S::VE, vp + tiles * S::TILE + tile * ve, 2 * ve, bar);
+            if (lane == 0) arrive(&b.span_empty[(n - 1) % kSpanRing]);
         }
+        const uint32_t slot = n % kSpanRing;
+        const bool ok = __all_sync(kFull, wait_for<true>(b, &b.span_full[slot], (n / kSpanRing) & 1));
+        ++n;
+        const Span* s = &b.spans[slot];
+        return ok && s->more ? s : nullptr;
     }
-    // no copy is in flight when the CTA ends: those that a failed CTA did not wait for
-    const uint32_t n = uc < (uint32_t)S::UNITS ? uc : (uint32_t)S::UNITS;
-    if (*(volatile int*)&b.failed)
-        for (uint32_t u = uc - n; u < uc; ++u) mbar_wait(&b.ring_full[u % S::FULLS], (u / S::FULLS) & 1);
-}
+};
 
 // ---- producers: warp w of 4 fills tokens 32 w .. 32 w + 31 of each tile, keys or values ----
 template <int D, int BITS, bool VALUES>
-__device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t smem, ChunkWalk& walk, int w, int lane) {
+__device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t smem, int w, int lane) {
     using S = Shape<D, BITS>;
-    uint32_t tc = 0, uc = 0;
+    constexpr int W = S::W, TILE = S::TILE;
     uint64_t* full = VALUES ? b.v_full : b.k_full;
     uint64_t* empty = VALUES ? b.v_empty : b.k_empty;
-    while (walk.next()) {
-        const ChunkSeq& q = a.seqs[walk.s.seq];
-        Rows kr, vr;
-        const long long rrow = ((long long)q.seq * a.plan.Hkv + walk.s.head) * a.R * D;
-        kr.resid = reinterpret_cast<const __half*>(a.buf + a.k_resid_off) + rrow;
-        vr.resid = reinterpret_cast<const __half*>(a.buf + a.v_resid_off) + rrow;
-        kr.chunk = a.k + q.tok0 * a.k_stride[0] + walk.s.head * a.k_stride[1];
-        vr.chunk = a.v + q.tok0 * a.v_stride[0] + walk.s.head * a.v_stride[1];
-        kr.step = a.k_stride[0];
-        vr.step = a.v_stride[0];
-        kr.n_resid = vr.n_resid = q.n_resid;
-        kr.n = vr.n = q.n_resid + walk.s.it.t1;
-        for (int t = walk.s.it.lo + walk.s.first; t < walk.s.it.lo + walk.s.last; ++t, ++tc) {
-            const uint32_t stage = tc & 1, ph = (tc >> 1) & 1;
-            const int key0 = t * kTile + 32 * w;
-            const int units = min(4, max(0, (q.n_quant - t * kTile) >> 5));      // quantized units of the tile
-            const uint32_t dst = smem + (VALUES ? S::OFF_V : S::OFF_K) + stage * S::K_BYTES;
-            bool ok = wait_for(b, &empty[stage], ph ^ 1);
-            if (w < units) {
-                const uint32_t u = uc + w, slot = u % S::UNITS;
-                ok = ok && wait_for(b, &b.ring_full[u % S::FULLS], (u / S::FULLS) & 1);
-                if (ok) {
-                    const uint32_t src = smem + S::OFF_RING + slot * S::UNIT;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t words[S::W];
-                        lds_words(src + (VALUES ? S::VC : S::KC) + j * S::TILE + lane * (4 * S::W), words);
-                        if constexpr (VALUES)
-                            value_groups<D, BITS, 0>(words, src + S::VE + j * 64 * (D / a.G), a.G, uint2{}, uint2{}, dst,
-                                                     32 * w + 16 * j, lane);
-                        else
-                            key_groups<D, BITS, 0>(words, src + S::KE, dst, 32 * w + 16 * j, lane);
-                    }
-                    __syncwarp();
-                    if (lane == 0) arrive(&b.ring_empty[slot]);
-                }
-            } else if (ok) {
-                if constexpr (VALUES) value_rows<D>(vr, key0 - q.n_quant, dst, 32 * w, lane);
-                else key_rows<D>(kr, vr, key0 - q.n_quant, dst, 32 * w, lane);
-            }
-            uc += units;
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) arrive(&full[stage]);
+    const uint32_t ent = smem + S::OFF_ENT + (4 * VALUES + w) * (4 * D);
+    const int lgG = a.lgG, ve = 64 * (D >> lgG);               // bytes of value entries of a code tile
+    const int n_ent = VALUES ? 2 * ve / 16 : 4 * D / 16;       // 16-byte groups of a unit's steps and zeros
+    const long long resid = VALUES ? a.v_resid_off : a.k_resid_off;
+    const __half* chunk = VALUES ? a.v : a.k;
+    const long long step = VALUES ? a.v_stride[0] : a.k_stride[0], per_head = VALUES ? a.v_stride[1] : a.k_stride[1];
+    SpanReader reader(b);
+    // the unit ahead: its span's fields, and its bytes where it is quantized
+    int t = 0, t_end = 0, key0 = 0, n_quant = 0, seq = 0, head = 0, tok0 = 0, n_resid = 0, t1 = 0;
+    bool more = true, quantized = false;
+    int have = 0, entry = 0;                                   // table entries of tiles have .. have + 31, one a lane
+    const uint8_t* codes = nullptr;                            // of the unit ahead, this lane's
+    uint32_t words[2][W];
+    uint4 ents{};
+    auto ahead = [&]() {
+        bool fresh = false;
+        if (++t >= t_end) {
+            const Span* sp = reader.next(lane);
+            more = sp != nullptr;
+            if (!more) return;
+            t = sp->tile0;
+            t_end = t + sp->nt;
+            n_quant = sp->n_quant;
+            seq = sp->seq;
+            head = sp->head;
+            tok0 = sp->tok0;
+            n_resid = sp->n_resid;
+            t1 = sp->t1;
+            fresh = true;
         }
+        key0 = t * kTile + 32 * w;
+        quantized = key0 < n_quant;
+        if (!quantized) return;
+        if (fresh || t >= have + 32) {
+            have = t;
+            const int key = (t + lane) * kTile + 32 * w;
+            entry = key < n_quant ? ldg_int(a.table + (long long)seq * a.max_blocks + (key >> lgG)) : 0;
+        }
+        int page = __shfl_sync(kFull, entry, t - have);
+        if ((unsigned)page >= (unsigned)a.n_pages) {           // an entry outside the pool: the span's outputs are NaN
+            page = 0;
+            if (lane == 0) atomicOr(&b.bad, reader.mark());
+        }
+        const uint8_t* part = a.buf + (long long)page * a.page_bytes + (2LL * head + VALUES) * a.part_bytes;
+        const int tile = (key0 & ((1 << lgG) - 1)) >> 4, tiles = 1 << (lgG - 4);
+        codes = part + tile * TILE + lane * (4 * W);
+        if (lane < n_ent) ents = ldg_stream(part + tiles * TILE + (VALUES ? tile * ve : 0) + 16 * lane);
+    };
+    ahead();
+    if (more && quantized) {
+        load_words(codes, words[0]);
+        load_words(codes + TILE, words[1]);
+    }
+    for (uint32_t tc = 0; more; ++tc) {
+        const uint32_t stage = tc & 1, ph = (tc >> 1) & 1;
+        const uint32_t dst = smem + (VALUES ? S::OFF_V : S::OFF_K) + stage * S::K_BYTES;
+        const bool ok = __all_sync(kFull, wait_for(b, &empty[stage], ph ^ 1));
+        if (quantized) {
+            if (lane < n_ent) sts128(ent + 16 * lane, ents);
+            __syncwarp();
+            ahead();
+            const bool next = more && quantized;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if constexpr (VALUES) value_groups<D, BITS, 0>(words[j], ent + j * ve, lgG, uint2{}, uint2{}, dst, 32 * w + 16 * j, lane);
+                else key_groups<D, BITS, 0>(words[j], ent, dst, 32 * w + 16 * j, lane);
+                if (next) load_words(codes + j * TILE, words[j]);
+            }
+        } else {
+            if (ok) {
+                const Rows r{reinterpret_cast<const __half*>(a.buf + resid) + ((long long)seq * a.plan.Hkv + head) * a.R * D,
+                             chunk + tok0 * step + head * per_head, step, n_resid, n_resid + t1};
+                if constexpr (VALUES) {
+                    if (value_rows<D>(r, key0 - n_quant, dst, 32 * w, lane) && lane == 0) atomicOr(&b.odd, reader.mark());
+                } else {
+                    key_rows<D>(r, key0 - n_quant, dst, 32 * w, lane);
+                }
+            }
+            ahead();
+            if (more && quantized) {
+                load_words(codes, words[0]);
+                load_words(codes + TILE, words[1]);
+            }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive(&full[stage]);
     }
 }
 
-// ---- MMA issue (one lane) ----
+// ---- MMA issue: the warp runs as one, so that descriptors stay in uniform registers; one lane issues ----
 template <int D, int BITS>
-__device__ void issue_mmas(const ChunkArgs& a, Bars& b, uint32_t smem, uint32_t tmem, ChunkWalk& walk) {
+__device__ void issue_mmas(const ChunkArgs& a, Bars& b, uint32_t smem, uint32_t tmem, int lane) {
     using S = Shape<D, BITS>;
-    uint32_t tc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+    uint32_t tc = 0, qc = 0, pc = 0;                         // tiles; bit x: parity of the next wait for A or B
     const uint32_t kind_s = mma_kind(kTile), kind_o = mma_kind(D);
+    const uint32_t one = elect_one();
     bool ok = true;
-    auto scores = [&](const Span& sp, int x, int t) {        // S_x = Q_x K_t^T
-        const uint32_t c = tc + t, stage = c & 1;
-        ok = ok && wait_for(b, &b.k_full[stage], (c >> 1) & 1);
-        if (!ok) return;
-        fence_after();
-        const uint32_t qa = smem + S::OFF_Q + (sp.both ? x : 0) * S::Q_BYTES, ka = smem + S::OFF_K + stage * S::K_BYTES;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
-            mma_ss(tmem + S::COL_S + x * kTile, operand(qa + off), operand(ka + off), kind_s, k > 0);
-        }
-        commit(&b.s_full[x]);
-        if (!sp.both || x == 1) commit(&b.k_empty[stage]);
-    };
-    while (walk.next()) {
-        const Span sp = span_of(a, walk.s);
-        for (int x = 0; x < 2; ++x) {
-            if (sp.both || x == 0) {
-                ok = ok && wait_for(b, &b.q_full[x], qc[x] & 1);
-                ++qc[x];
-            }
-            if (sp.tiles(x)) scores(sp, x, sp.tile(x, 0));
-        }
-        const int steps = max(sp.na, sp.nb);
-        for (int i = 0; i < steps; ++i) {
-#pragma unroll
+    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(kFull, wait_for(b, bar, parity)); };
+    SpanReader reader(b);
+    while (const Span* sp = reader.next(lane)) {
+        const int both = sp->both, na = sp->na, nb = sp->nb, steps = max(na, nb);
+        for (int i = -1; i < steps; ++i) {
+#pragma unroll 1
             for (int x = 0; x < 2; ++x) {
-                if (i >= sp.tiles(x)) {
-                    // (both: B always has the tile; alternate: the tile is nobody's)
-                    continue;
-                }
-                const int t = sp.tile(x, i);
-                const uint32_t c = tc + t, stage = c & 1;
-                ok = ok && wait_for(b, &b.p_full[x], pc[x] & 1);
-                ++pc[x];
-                ok = ok && wait_for(b, &b.v_full[stage], (c >> 1) & 1);
-                if (ok) {
-                    fence_after();
-                    const uint32_t va = smem + S::OFF_V + stage * S::K_BYTES;
+                const int n = x ? nb : na;
+                if (i < 0) {
+                    if (both || x == 0) {
+                        wait(&b.q_full[x], (qc >> x) & 1);
+                        qc ^= 1u << x;
+                    }
+                } else if (i < n) {
+                    // (both: B has every tile; alternate: a tile that one lacks is nobody's)
+                    const uint32_t c = tc + (both ? i : 2 * i + x), stage = c & 1;
+                    wait(&b.p_full[x], (pc >> x) & 1);
+                    pc ^= 1u << x;
+                    wait(&b.v_full[stage], (c >> 1) & 1);
+                    if (ok) {                                // O_x += P_x V_t
+                        fence_after();
+                        const uint64_t va = operand(smem + S::OFF_V + stage * S::K_BYTES);
+                        const uint32_t o = tmem + S::COL_O + x * D, pa = tmem + S::COL_S + x * kTile;
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(tmem + S::COL_O + x * D, tmem + S::COL_S + x * kTile + 8 * k,
-                               operand(va + (k >> 2) * (D * 128) + (k & 3) * 32), kind_o, i > 0 || k > 0);
-                    if (!sp.both || x == 1) commit(&b.v_empty[stage]);
-                    if (i + 1 == sp.tiles(x)) commit(&b.o_full[x]);
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_ts(o, pa + 8 * k, va + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), kind_o, i > 0 || k > 0, one);
+                        if (!both || x == 1) commit(&b.v_empty[stage], one);
+                        if (i + 1 == n) commit(&b.o_full[x], one);
+                    }
                 }
-                if (i + 1 < sp.tiles(x)) scores(sp, x, sp.tile(x, i + 1));
+                if (i + 1 < n) {
+                    const uint32_t c = tc + (both ? i + 1 : 2 * (i + 1) + x), stage = c & 1;
+                    wait(&b.k_full[stage], (c >> 1) & 1);
+                    if (ok) {                                // S_x = Q_x K_t^T
+                        fence_after();
+                        const uint64_t qa = operand(smem + S::OFF_Q + (both ? x : 0) * S::Q_BYTES);
+                        const uint64_t ka = operand(smem + S::OFF_K + stage * S::K_BYTES);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
+                            mma_ss(tmem + S::COL_S + x * kTile, qa + off, ka + off, kind_s, k > 0, one);
+                        }
+                        commit(&b.s_full[x], one);
+                        if (!both || x == 1) commit(&b.k_empty[stage], one);
+                    }
+                }
             }
         }
-        tc += sp.nt;
+        tc += sp->nt;
     }
-    commit(&b.drained);            // no MMA is in flight when the CTA ends
+    commit(&b.drained, one);       // no MMA is in flight when the CTA ends
     mbar_wait(&b.drained, 0);
 }
 
 // ---- softmax of tile X (four warps, a row a lane) ----
+__device__ __forceinline__ float max32(const float (&v)[32]) {
+    float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int j = 4; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// Weights 2^(mul v - ref) of 32 columns, as fp16 to `at`, their sums.
+__device__ __forceinline__ void weights32(uint32_t at, const float (&v)[32], float mul, float ref, float (&sum)[4]) {
+    uint32_t p[16];
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float p0 = exp2_ftz(fmaf(v[j], mul, -ref)), p1 = exp2_ftz(fmaf(v[j + 1], mul, -ref));
+        sum[j & 2] += p0;
+        sum[(j & 2) + 1] += p1;
+        p[j / 2] = pack_f16x2(p0, p1);
+    }
+    st16(at, p);
+}
 template <int D, int BITS, bool MOD>
-__device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2* xch, uint32_t tmem, ChunkWalk& walk, int x,
-                             int warp, int lane) {
+__device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2* xch, uint32_t tmem, int x, int warp, int lane) {
     using S = Shape<D, BITS>;
     const int row = 32 * (warp & 3) + lane;                    // of tile X
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = lanes + S::COL_S + x * kTile, to = lanes + S::COL_O + x * D;
     const int nq = a.plan.nq;
     uint32_t sc = 0, oc = 0;
-    unsigned number = 0;
-    while (walk.next()) {
-        const Span sp = span_of(a, walk.s);
-        const ChunkSeq& q = a.seqs[walk.s.seq];
-        const bool quantized = sp.tile0 * kTile < q.n_quant;
-        number += quantized;
-        const ChunkItem& it = walk.s.it;
-        const int n_rows = (it.t1 - it.t0) * nq;
-        const int r = sp.both ? x * kHalf + row : row;         // row of the item
-        const bool valid = r < n_rows;
-        const int tok = it.t0 + r / nq, head = walk.s.head * nq + r % nq;
-        const int steps = sp.tiles(x);
+    SpanReader reader(b);
+    while (const Span* sp = reader.next(lane)) {
+        const bool both = sp->both;
+        const int r = both ? x * kHalf + row : row;            // row of the item
+        const bool valid = r < (sp->t1 - sp->t0) * nq;
+        const int tok = sp->t0 + r / nq, head = sp->head * nq + r % nq;
+        const int steps = sp->tiles(x);
         // queries into the operand
-        if (sp.both || x == 0) {
-            const __half* src = a.q + (long long)(q.tok0 + tok) * a.q_stride[0] + head * a.q_stride[1];
+        if (both || x == 0) {
+            const __half* src = a.q + (long long)(sp->tok0 + tok) * a.q_stride[0] + head * a.q_stride[1];
             const uint32_t dst = smem + S::OFF_Q + x * S::Q_BYTES;
-#pragma unroll
+#pragma unroll 4
             for (int c = 0; c < D / 8; ++c)
                 sts128(dst + operand_at<kHalf>(row, c),
                        valid ? ldg_row(src + 8 * c) : uint4{0, 0, 0, 0});
@@ -554,53 +633,66 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
             __syncwarp();
             if (lane == 0) arrive(&b.q_full[x]);
         }
-        const long long pos = (long long)q.n_quant + q.n_resid + tok;       // the row's position
+        const long long pos = (long long)sp->n_quant + sp->n_resid + tok;   // the row's position
         const int hi = (int)pos;                                            // last and first key that it sees
         const int lo = a.plan.window ? max(0, (int)(pos - a.plan.window + 1)) : 0;
         // rows of the warp: the first one sees least, the last one (that exists) starts last
         const int w_hi = __shfl_sync(kFull, hi, 0), w_lo = __shfl_sync(kFull, lo, 31);
         const bool any = __any_sync(kFull, valid);
         const float slope = MOD && a.slopes && valid ? __ldg(a.slopes + head) * kLog2e : 0.f;
-        const float mul = MOD ? 1.f : a.scale_log2;
+        const float cap_in = a.scale * (2.f * kLog2e) / a.cap, cap_out = a.cap * kLog2e;    // (without a cap: not used)
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < steps; ++i) {
-            const int key0 = (sp.tile0 + sp.tile(x, i)) * kTile;
+            const int key0 = (sp->tile0 + (both ? i : 2 * i + x)) * kTile;
             const bool ok = wait_for(b, &b.s_full[x], sc & 1);
+            float mul = a.scale_log2;
             ++sc;
             fence_after();
             if (ok && any) {
+                // (loops over a tile's columns stay loops: unrolled, the roles' code misses the instruction cache)
                 const bool cut = key0 + kTile - 1 > w_hi || key0 < w_lo;
-                float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    ld32(ts + 32 * c, v);
-                    wait_ld();
-                    if (MOD) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            if (a.cap > 0.f) {
-                                // cap tanh(y), tanh(y) = 1 - 2 / (exp(2 y) + 1)
-                                const float e = exp2_ftz(v[j] * (a.scale * (2.f * kLog2e) / a.cap));
-                                v[j] = a.cap * kLog2e * (1.f - __fdividef(2.f, e + 1.f));
-                            } else {
-                                v[j] *= a.scale_log2;
-                            }
-                            v[j] = fmaf(slope, (float)(key0 + 32 * c + j - hi), v[j]);
-                        }
-                    }
-                    if (cut) {
+                if (MOD || cut) {                              // logits other than mul * S: written back as such
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        ld32(ts + 32 * c, v);
+                        wait_ld();
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const int key = key0 + 32 * c + j;
+                            if (MOD) {
+                                if (a.cap > 0.f) {
+                                    // cap tanh(y), tanh(y) = 1 - 2 / (exp(2 y) + 1)
+                                    const float e = exp2_ftz(v[j] * cap_in);
+                                    v[j] = cap_out * (1.f - __fdividef(2.f, e + 1.f));
+                                } else {
+                                    v[j] *= a.scale_log2;
+                                }
+                                v[j] = fmaf(slope, (float)(key - hi), v[j]);
+                            } else {
+                                v[j] *= a.scale_log2;
+                            }
                             if (key > hi || key < lo) v[j] = -INFINITY;
                         }
+                        st32(ts + 32 * c, v);
                     }
-                    if (MOD || cut) st32(ts + 32 * c, v);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, v[j]);
+                    wait_st();
+                    mul = 1.f;
                 }
-                if (MOD || cut) wait_st();
+                float mx = -INFINITY;
+                {
+                    float v[32], u[32];
+                    ld32(ts, v);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+                        wait_ld();
+                        ld32(ts + 32 * c + 32, u);
+                        mx = fmaxf(mx, max32(v));
+                        wait_ld();
+                        if (c == 0) ld32(ts + 64, v);
+                        mx = fmaxf(mx, max32(u));
+                    }
+                }
                 mx *= mul;
                 // the reference is raised, and what is summed so far scaled, where a row needs it
                 if (__any_sync(kFull, mx > m + kRaise)) {
@@ -608,7 +700,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                     const float f = m == -INFINITY ? 0.f : exp2_ftz(m - top);
                     if (i > 0) {
                         l *= f;
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             float o[32];
                             ld32(to + 32 * c, o);
@@ -622,20 +714,18 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                 }
                 const float ref = m == -INFINITY ? 0.f : m - kLift;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    ld32(ts + 32 * c, v);
-                    wait_ld();
-                    uint32_t p[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float p0 = exp2_ftz(fmaf(v[j], mul, -ref)), p1 = exp2_ftz(fmaf(v[j + 1], mul, -ref));
-                        sum[j & 2] += p0;
-                        sum[(j & 2) + 1] += p1;
-                        p[j / 2] = pack_f16x2(p0, p1);
+                {
+                    float v[32], u[32];
+                    ld32(ts, v);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+                        wait_ld();
+                        ld32(ts + 32 * c + 32, u);
+                        weights32(ts + 16 * c, v, mul, ref, sum);
+                        wait_ld();
+                        if (c == 0) ld32(ts + 64, v);
+                        weights32(ts + 16 * c + 16, u, mul, ref, sum);
                     }
-                    st16(ts + 16 * c, p);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 wait_st();
@@ -652,8 +742,8 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
         }
         fence_after();
         float wa = 1.f, wb = 0.f;                              // weights of A's and B's sums
-        const bool join = !sp.both && sp.nb > 0;
-        if (!sp.both) {
+        const bool join = !both && sp->nb > 0;
+        if (!both) {
             if (x == 1) {
                 xch[row] = make_float2(m, l);
                 fence_before();
@@ -673,14 +763,24 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                 m = top;
             }
         }
-        if (!fine || *(volatile int*)&b.failed || (quantized && (*(volatile unsigned*)&b.bad >> (number % 32) & 1u)))
-            m = l = NAN;
-        const bool whole = walk.s.whole();
-        float* part = a.ws + (((long long)blockIdx.x * 2 + (walk.s.first == 0)) * kRows + r) * chunk_partial_stride(D);
-        __half* out = a.out + (long long)(q.tok0 + tok) * a.out_stride[0] + head * a.out_stride[1];
+        if (!fine || *(volatile int*)&b.failed || (*(volatile unsigned*)&b.bad & reader.mark())) m = l = NAN;
+        if ((*(volatile unsigned*)&b.odd & reader.mark()) && valid) {
+            // a value that is not finite: the row is NaN if it sees one (looked for again, value by value)
+            const Rows v{reinterpret_cast<const __half*>(a.buf + a.v_resid_off) +
+                             ((long long)sp->seq * a.plan.Hkv + sp->head) * a.R * D,
+                         a.v + sp->tok0 * a.v_stride[0] + sp->head * a.v_stride[1], a.v_stride[0], sp->n_resid, 0};
+            const int last = min(hi, (sp->tile0 + sp->nt) * kTile - 1);
+            for (int t = max(max(lo, sp->tile0 * kTile), sp->n_quant); t <= last && l == l; ++t)
+                for (int j = 0; j < D / 8; ++j)
+                    if (not_finite(ldg_row(v.at(t - sp->n_quant, D) + 8 * j))) m = l = NAN;
+        }
+        __syncwarp();
+        const bool whole = sp->whole;
+        float* part = a.ws + (((long long)blockIdx.x * 2 + sp->first) * kRows + r) * chunk_partial_stride(D);
+        __half* out = a.out + (long long)(sp->tok0 + tok) * a.out_stride[0] + head * a.out_stride[1];
         const float inv = 1.f / l;
         if (any) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 float o[32];
                 __syncwarp();
@@ -715,7 +815,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
             }
             if (valid && !whole) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
         }
-        if (!sp.both) {
+        if (!both) {
             fence_before();
             named_sync<2, 256>();
         }
@@ -732,8 +832,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     float2* xch = reinterpret_cast<float2*>(base + S::OFF_XCH);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int j = 0; j < S::FULLS; ++j) mbar_init(&b.ring_full[j], 1);
-        for (int j = 0; j < S::UNITS; ++j) mbar_init(&b.ring_empty[j], 2);
         for (int j = 0; j < 2; ++j) {
             mbar_init(&b.k_full[j], 4);
             mbar_init(&b.v_full[j], 4);
@@ -744,8 +842,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             mbar_init(&b.p_full[j], 4);
             mbar_init(&b.o_full[j], 1);
         }
+        for (int j = 0; j < kSpanRing; ++j) {
+            mbar_init(&b.span_full[j], 1);
+            mbar_init(&b.span_empty[j], kSpanReaders);
+        }
         mbar_init(&b.drained, 1);
-        b.failed = b.bad = 0;
+        b.failed = 0;
+        b.bad = b.odd = 0;
         fence_mbar_init();
     }
     if (warp == 16) tmem_alloc(&b.tmem);
@@ -755,20 +858,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     griddepcontrol_wait();
     griddepcontrol_launch_dependents();
     const uint32_t tmem = b.tmem;
-    ChunkWalk walk;
-    walk.start(&a.plan, a.seqs, a.n_seqs, chunk_begin(a.weight, a.n_ctas, blockIdx.x),
-               chunk_begin(a.weight, a.n_ctas, blockIdx.x + 1LL));
     if (warp < 8) {
-        softmax_rows<D, BITS, MOD>(a, b, smem, xch, tmem, walk, warp >> 2, warp, lane);
-    } else if (warp < 12) {
-        fill_tiles<D, BITS, false>(a, b, smem, walk, warp - 8, lane);
+        more_regs<kRegsSoftmax>();
+        softmax_rows<D, BITS, MOD>(a, b, smem, xch, tmem, warp >> 2, warp, lane);
     } else if (warp < 16) {
-        fill_tiles<D, BITS, true>(a, b, smem, walk, warp - 12, lane);
-    } else if (warp == 16) {
-        if (lane == 0) issue_mmas<D, BITS>(a, b, smem, tmem, walk);
-        __syncwarp();
+        fewer_regs<kRegsFill>();
+        if (warp < 12) fill_tiles<D, BITS, false>(a, b, smem, warp - 8, lane);
+        else fill_tiles<D, BITS, true>(a, b, smem, warp - 12, lane);
     } else {
-        load_units<D, BITS>(a, b, smem + S::OFF_RING, walk, lane);
+        fewer_regs<kRegsRest>();
+        if (warp == 16) issue_mmas<D, BITS>(a, b, smem, tmem, lane);
+        else if (warp == 17) plan_spans(a, b, lane);
     }
     fence_before();
     __syncthreads();

@@ -619,7 +619,7 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
     a.k_resid_off = g.k_resid_off;
     a.v_resid_off = g.v_resid_off;
     a.R = g.R;
-    a.G = g.G;
+    a.lgG = g.G == 32 ? 5 : g.G == 64 ? 6 : 7;
     a.Hq = g.Hq;
     a.max_blocks = (int)g.NB;
     a.n_pages = (int)c->pg.n_pages;
