@@ -19,7 +19,7 @@
 //   0-3, 4-7   softmax of tile A / B, a row a lane: logits from tensor memory, running
 //              maximum, exponentials, probabilities back as fp16; epilogue
 //   8-11       keys: 32 tokens of a tile each, from codes to fp16 in shared memory; the
-//              next tile's bytes are loaded into registers as this one's are used up
+//              next tile's bytes are loaded into registers while this one waits its turn
 //   12-15      values, the same, transposed ([channel][token])
 //   16         issues the MMAs
 //   17         finds the spans of items that the CTA works on, ahead of the others (18, 19: idle,
@@ -53,7 +53,7 @@ using namespace mma_detail;
 
 constexpr int kChunkWarps = 20, kChunkThreads = 32 * kChunkWarps;
 // Registers a thread: the launch's, and what the five warpgroups (A, B, keys, values, the rest) make of them.
-constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsFill = 88, kRegsRest = 48;
+constexpr int kRegs = 96, kRegsSoftmax = 120, kRegsFill = 88, kRegsRest = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsFill + kRegsRest <= 5 * kRegs, "registers of the launch");
 constexpr int kSpanRing = 4, kSpanReaders = 17;
 constexpr float kRaise = 7.f;      // base-2 logits above the reference that a tile may have
@@ -199,25 +199,21 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 template <int ID, int N>
 __device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
 
-// Wait for an mbarrier's phase, about two seconds at most; a wait that runs out marks the CTA,
+// Wait for an mbarrier's phase, 2^32 cycles (about two seconds) at most; a wait that runs out marks the CTA,
 // and no wait of a marked CTA waits, but a patient one (for spans: they keep coming).
 template <bool PATIENT = false>
 __device__ __forceinline__ bool wait_for(Bars& b, uint64_t* bar, uint32_t parity) {
     const uint32_t addr = smem_u32(bar);
-    if (mbar_try(addr, parity)) return true;
-    volatile int* failed = &b.failed;
-    uint64_t t0 = 0;           // (reading the timer takes about a microsecond: not before 256 polls)
-    for (uint32_t it = 1; it < (1u << 26); ++it) {
-        if (mbar_try(addr, parity)) return true;
-        if (it % 256 == 0) {
-            if (!PATIENT && *failed) return false;
-            const uint64_t now = global_ns();
-            if (t0 == 0) t0 = now;
-            else if (now - t0 > 2000000000ull) break;
+    const long long t0 = clock64();
+    while (!mbar_try(addr, parity)) {
+        volatile int* failed = &b.failed;
+        if (!PATIENT && *failed) return false;
+        if (clock64() - t0 >= 1LL << 32) {
+            *failed = 1;
+            return false;
         }
     }
-    *failed = 1;
-    return false;
+    return true;
 }
 
 // a lane's words of a code tile
@@ -235,40 +231,75 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[W]) {
     }
 }
 
-// Keys of a 16-token code tile: fp16(code * step + zero) into rows row0 .. row0 + 15 of the operand at dst.
-// The channel group C's step and zero pair of the lane is at ent + 16 C + 4 i (zeros 2 D bytes on).
-template <int D, int BITS, int C, int W>
-__device__ __forceinline__ void key_groups(const uint32_t (&w)[W], uint32_t ent, uint32_t dst, int row0, int lane) {
-    if constexpr (C < D / 8) {
-        const int i = lane & 3;
-        const uint32_t s0 = lds32(ent + 16 * C + 4 * i), z0 = lds32(ent + 2 * D + 16 * C + 4 * i);
-        const uint32_t s1 = lds32(ent + 16 * C + 16 + 4 * i), z1 = lds32(ent + 2 * D + 16 * C + 16 + 4 * i);
-        // matrices: (C, tokens 0-7), (C, 8-15), (C + 1, 0-7), (C + 1, 8-15); this lane gives a row's address
-        const int row = row0 + (lane & 15), chunk = C + (lane >> 4);
-        stmatrix4(dst + operand_at<kTile>(row, chunk), hfma2(code_of<BITS, C, 0>(w), s0, z0),
-                  hfma2(code_of<BITS, C, 1>(w), s0, z0), hfma2(code_of<BITS, C + 1, 0>(w), s1, z1),
-                  hfma2(code_of<BITS, C + 1, 1>(w), s1, z1));
-        key_groups<D, BITS, C + 2>(w, ent, dst, row0, lane);
+template <int W, int TILE>
+__device__ __forceinline__ void load_unit(const uint8_t* p, uint32_t (&w)[2 * W]) {
+    uint32_t x[W], y[W];
+    load_words(p, x);
+    load_words(p + TILE, y);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        w[j] = x[j];
+        w[W + j] = y[j];
     }
 }
-// Values of a 16-token code tile into columns (tokens) tok0 .. tok0 + 15 of the operand [D channels][tokens] at dst.
-// ent: the tile's steps, channel group j's at 32 j (this lane's four tokens at 8 i), zeros 32 D/G bytes on.
-template <int D, int BITS, int C, int W>
-__device__ __forceinline__ void value_groups(const uint32_t (&w)[W], uint32_t ent, int lgG, uint2 s, uint2 z, uint32_t dst,
-                                             int tok0, int lane) {
-    if constexpr (C < D / 8) {
-        if constexpr (8 * C % 32 == 0) {
-            if (((8 * C) & ((1 << lgG) - 1)) == 0) {
-                const uint32_t at = ent + 32 * ((8 * C) >> lgG) + 8 * (lane & 3);
-                s = lds64(at);
-                z = lds64(at + 32 * (D >> lgG));
-            }
+
+// A lane's words of a unit (two code tiles) are taken four channel groups (32 channels) at a time, from the front:
+// loops over them are kept loops, their bodies are small.
+template <int BITS, int N>
+__device__ __forceinline__ void take_words(uint32_t (&w)[N], uint32_t (&x)[BITS / 2]) {
+#pragma unroll
+    for (int j = 0; j < BITS / 2; ++j) x[j] = w[j];
+#pragma unroll
+    for (int j = 0; j + BITS / 2 < N; ++j) w[j] = w[j + BITS / 2];
+}
+// Keys: fp16(code * step + zero), rows row0 .. row0 + 31 of the operand at dst.  The channel group C's step and
+// zero pair of the lane is at ent + 16 C + 4 i (zeros 2 D bytes on).
+template <int D, int BITS, int N>
+__device__ __forceinline__ void key_unit(uint32_t (&w)[N], uint32_t ent, uint32_t dst, int row0, int lane) {
+    const int r7 = lane & 7;
+    uint32_t rows = dst + (row0 + (lane & 15)) * 128, e = ent + 4 * (lane & 3);
+#pragma unroll 1
+    for (int it = 0; it < D / 16; ++it) {                      // 2 tiles x D / 32
+        const int c = it % (D / 32);                           // channels 32 c ..
+        uint32_t x[BITS / 2];
+        take_words<BITS>(w, x);
+        const uint32_t at = rows + (it / (D / 32)) * 2048 + (c >> 1) * (kTile * 128);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t s0 = lds32(e + 64 * c + 32 * h), z0 = lds32(e + 64 * c + 32 * h + 2 * D);
+            const uint32_t s1 = lds32(e + 64 * c + 32 * h + 16), z1 = lds32(e + 64 * c + 32 * h + 16 + 2 * D);
+            // matrices: (group, tokens 0-7), (group, 8-15), (next group, ...); this lane gives a row's address
+            const int chunk = 4 * (c & 1) + 2 * h + (lane >> 4);
+            const uint32_t to = at + ((chunk ^ r7) << 4);
+            if (h == 0)
+                stmatrix4(to, hfma2(code_of<BITS, 0, 0>(x), s0, z0), hfma2(code_of<BITS, 0, 1>(x), s0, z0),
+                          hfma2(code_of<BITS, 1, 0>(x), s1, z1), hfma2(code_of<BITS, 1, 1>(x), s1, z1));
+            else
+                stmatrix4(to, hfma2(code_of<BITS, 2, 0>(x), s0, z0), hfma2(code_of<BITS, 2, 1>(x), s0, z0),
+                          hfma2(code_of<BITS, 3, 0>(x), s1, z1), hfma2(code_of<BITS, 3, 1>(x), s1, z1));
         }
-        const int row = 8 * (C + (lane >> 4)) + (lane & 7), chunk = (tok0 >> 3) + ((lane >> 3) & 1);
-        stmatrix4(dst + operand_at<D>(row, chunk), hfma2(code_of<BITS, C, 0>(w), s.x, z.x),
-                  hfma2(code_of<BITS, C, 1>(w), s.y, z.y), hfma2(code_of<BITS, C + 1, 0>(w), s.x, z.x),
-                  hfma2(code_of<BITS, C + 1, 1>(w), s.y, z.y));
-        value_groups<D, BITS, C + 2>(w, ent, lgG, s, z, dst, tok0, lane);
+    }
+}
+// Values into columns (tokens) tok0 .. tok0 + 31 of the operand [D channels][tokens] at dst.  ent: per code tile the
+// steps, channel group j's at 32 j (this lane's four tokens at 8 i), and the zeros.
+template <int D, int BITS, int N>
+__device__ __forceinline__ void value_unit(uint32_t (&w)[N], uint32_t ent, int lgG, uint32_t dst, int tok0, int lane) {
+    const int r7 = lane & 7, ve = 64 * (D >> lgG);
+    // (128 tokens a row in two blocks of 64; a unit lies in one)
+    const uint32_t rows = dst + (tok0 >> 6) * (D * 128) + (8 * (lane >> 4) + r7) * 128;
+    const int chunk0 = ((tok0 >> 3) & 7) + ((lane >> 3) & 1);
+#pragma unroll 1
+    for (int it = 0; it < D / 16; ++it) {
+        const int c = it % (D / 32), j = it / (D / 32);
+        uint32_t x[BITS / 2];
+        take_words<BITS>(w, x);
+        const uint32_t e = ent + j * ve + 32 * ((32 * c) >> lgG) + 8 * (lane & 3);
+        const uint2 s = lds64(e), z = lds64(e + ve / 2);
+        const uint32_t to = rows + c * 4096 + (((chunk0 + 2 * j) ^ r7) << 4);
+        stmatrix4(to, hfma2(code_of<BITS, 0, 0>(x), s.x, z.x), hfma2(code_of<BITS, 0, 1>(x), s.y, z.y),
+                  hfma2(code_of<BITS, 1, 0>(x), s.x, z.x), hfma2(code_of<BITS, 1, 1>(x), s.y, z.y));
+        stmatrix4(to + 2048, hfma2(code_of<BITS, 2, 0>(x), s.x, z.x), hfma2(code_of<BITS, 2, 1>(x), s.y, z.y),
+                  hfma2(code_of<BITS, 3, 0>(x), s.x, z.x), hfma2(code_of<BITS, 3, 1>(x), s.y, z.y));
     }
 }
 
@@ -447,7 +478,7 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t smem, int w, in
     bool more = true, quantized = false;
     int have = 0, entry = 0;                                   // table entries of tiles have .. have + 31, one a lane
     const uint8_t* codes = nullptr;                            // of the unit ahead, this lane's
-    uint32_t words[2][W];
+    uint32_t words[2 * W];
     uint4 ents{};
     auto ahead = [&]() {
         bool fresh = false;
@@ -484,10 +515,7 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t smem, int w, in
         if (lane < n_ent) ents = ldg_stream(part + tiles * TILE + (VALUES ? tile * ve : 0) + 16 * lane);
     };
     ahead();
-    if (more && quantized) {
-        load_words(codes, words[0]);
-        load_words(codes + TILE, words[1]);
-    }
+    if (more && quantized) load_unit<W, TILE>(codes, words);
     for (uint32_t tc = 0; more; ++tc) {
         const uint32_t stage = tc & 1, ph = (tc >> 1) & 1;
         const uint32_t dst = smem + (VALUES ? S::OFF_V : S::OFF_K) + stage * S::K_BYTES;
@@ -495,14 +523,8 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t smem, int w, in
         if (quantized) {
             if (lane < n_ent) sts128(ent + 16 * lane, ents);
             __syncwarp();
-            ahead();
-            const bool next = more && quantized;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if constexpr (VALUES) value_groups<D, BITS, 0>(words[j], ent + j * ve, lgG, uint2{}, uint2{}, dst, 32 * w + 16 * j, lane);
-                else key_groups<D, BITS, 0>(words[j], ent, dst, 32 * w + 16 * j, lane);
-                if (next) load_words(codes + j * TILE, words[j]);
-            }
+            if constexpr (VALUES) value_unit<D, BITS>(words, ent, lgG, dst, 32 * w, lane);
+            else key_unit<D, BITS>(words, ent, dst, 32 * w, lane);
         } else {
             if (ok) {
                 const Rows r{reinterpret_cast<const __half*>(a.buf + resid) + ((long long)seq * a.plan.Hkv + head) * a.R * D,
@@ -513,15 +535,12 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t smem, int w, in
                     key_rows<D>(r, key0 - n_quant, dst, 32 * w, lane);
                 }
             }
-            ahead();
-            if (more && quantized) {
-                load_words(codes, words[0]);
-                load_words(codes + TILE, words[1]);
-            }
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) arrive(&full[stage]);
+        ahead();
+        if (more && quantized) load_unit<W, TILE>(codes, words);
     }
 }
 
@@ -591,18 +610,41 @@ __device__ void issue_mmas(const ChunkArgs& a, Bars& b, uint32_t smem, uint32_t 
 __device__ __forceinline__ float max32(const float (&v)[32]) {
     float m[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int j = 4; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    for (int j = 4; j < 28; j += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(m[k], v[j + k]), v[j + 4 + k]);
+    return fmaxf(fmaxf(fmaxf(m[0], v[28]), fmaxf(m[1], v[29])), fmaxf(fmaxf(m[2], v[30]), fmaxf(m[3], v[31])));
 }
-// Weights 2^(mul v - ref) of 32 columns, as fp16 to `at`, their sums.
-__device__ __forceinline__ void weights32(uint32_t at, const float (&v)[32], float mul, float ref, float (&sum)[4]) {
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// Weights 2^(mul v - ref) of 32 columns, as fp16 to `at`, their sums (mul and -ref twice each).
+__device__ __forceinline__ void weights32(uint32_t at, const float (&v)[32], uint64_t mul, uint64_t ref, uint64_t (&sum)[2]) {
     uint32_t p[16];
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
-        const float p0 = exp2_ftz(fmaf(v[j], mul, -ref)), p1 = exp2_ftz(fmaf(v[j + 1], mul, -ref));
-        sum[j & 2] += p0;
-        sum[(j & 2) + 1] += p1;
-        p[j / 2] = pack_f16x2(p0, p1);
+        float2 y = unpair(fma2(pair(v[j], v[j + 1]), mul, ref));
+        y.x = exp2_ftz(y.x);
+        y.y = exp2_ftz(y.y);
+        sum[(j / 2) & 1] = add2(sum[(j / 2) & 1], pair(y.x, y.y));
+        p[j / 2] = pack_f16x2(y.x, y.y);
     }
     st16(at, p);
 }
@@ -713,7 +755,8 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                     m = top;
                 }
                 const float ref = m == -INFINITY ? 0.f : m - kLift;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t mul2 = pair(mul, mul), ref2 = pair(-ref, -ref);
+                uint64_t sum[2] = {0, 0};
                 {
                     float v[32], u[32];
                     ld32(ts, v);
@@ -721,13 +764,14 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                     for (int c = 0; c < 4; c += 2) {
                         wait_ld();
                         ld32(ts + 32 * c + 32, u);
-                        weights32(ts + 16 * c, v, mul, ref, sum);
+                        weights32(ts + 16 * c, v, mul2, ref2, sum);
                         wait_ld();
                         if (c == 0) ld32(ts + 64, v);
-                        weights32(ts + 16 * c + 16, u, mul, ref, sum);
+                        weights32(ts + 16 * c + 16, u, mul2, ref2, sum);
                     }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float2 total = unpair(add2(sum[0], sum[1]));
+                l += total.x + total.y;
                 wait_st();
             }
             fence_before();
