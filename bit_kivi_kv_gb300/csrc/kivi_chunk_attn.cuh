@@ -21,7 +21,7 @@
 //   8-11       keys: 32 tokens of a tile each, from codes to fp16 in shared memory; the
 //              next tile's bytes are loaded into registers while this one waits its turn
 //   12-15      values, the same, transposed ([channel][token])
-//   16         issues the MMAs
+//   16         issues the MMAs (one thread)
 //   17         finds the spans of items that the CTA works on, ahead of the others (18, 19: idle,
 //              they fill their warpgroup for the redistribution of registers)
 //
@@ -43,6 +43,7 @@
 #pragma once
 
 #include <math.h>
+#include <stddef.h>
 
 #include "kivi_dequant.cuh"
 
@@ -101,6 +102,7 @@ struct Bars {
     alignas(16) Span spans[kSpanRing];
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
+#define BAR(member) (uint32_t) offsetof(Bars, member)     // (barriers are used by their 32-bit shared address)
 
 // ---- tensor memory and tcgen05 ----
 __device__ __forceinline__ void tmem_alloc(uint32_t* out) {
@@ -112,12 +114,9 @@ __device__ __forceinline__ void tmem_free(uint32_t at) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
-        "r"(one)
-        : "memory");
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ void ld32(uint32_t at, float (&x)[32]) {
     uint32_t* r = reinterpret_cast<uint32_t*>(x);
@@ -130,8 +129,15 @@ __device__ __forceinline__ void ld32(uint32_t at, float (&x)[32]) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
 }
-__device__ __forceinline__ void st32(uint32_t at, const float (&x)[32]) {
-    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+__device__ __forceinline__ void ld16(uint32_t at, float (&x)[16]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+}
+__device__ __forceinline__ void st32(uint32_t at, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
         "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
@@ -141,6 +147,9 @@ __device__ __forceinline__ void st32(uint32_t at, const float (&x)[32]) {
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void st32(uint32_t at, const float (&x)[32]) {
+    st32(at, reinterpret_cast<const uint32_t*>(x));
+}
 __device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
@@ -148,7 +157,27 @@ __device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Wait for the loads: what they bring passes through, so that no use of it is moved ahead of the wait.
+__device__ __forceinline__ void wait_ld(float (&x)[16]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                   "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void wait_ld(float (&x)[32]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                   "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                   "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                   "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory operand, contracted index contiguous, 128-byte swizzle: rows of 128 bytes in
@@ -160,25 +189,22 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr) {
 __host__ __device__ constexpr uint32_t mma_kind(int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-// (by the lane whose `one` is set)
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add, uint32_t one) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add), "r"(one)
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add, uint32_t one) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add), "r"(one)
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
         : "memory");
 }
-__device__ __forceinline__ uint32_t elect_one() {
+__device__ __forceinline__ bool elect_one() {
     uint32_t one;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
-    return one;
+    return one != 0;
 }
 template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -188,8 +214,8 @@ __device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync
 __device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ float exp2_ftz(float x) {
     float y;
@@ -202,49 +228,49 @@ __device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" :
 // Wait for an mbarrier's phase, 2^32 cycles (about two seconds) at most; a wait that runs out marks the CTA,
 // and no wait of a marked CTA waits, but a patient one (for spans: they keep coming).
 template <bool PATIENT = false>
-__device__ __forceinline__ bool wait_for(Bars& b, uint64_t* bar, uint32_t parity) {
-    const uint32_t addr = smem_u32(bar);
+__device__ __forceinline__ bool wait_for(uint32_t bars, uint32_t bar, uint32_t parity) {
+    if (mbar_try(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try(addr, parity)) {
-        volatile int* failed = &b.failed;
-        if (!PATIENT && *failed) return false;
+    while (!mbar_try(bar, parity)) {
+        if (!PATIENT && lds32(bars + BAR(failed))) return false;
         if (clock64() - t0 >= 1LL << 32) {
-            *failed = 1;
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(bars + BAR(failed)), "r"(1) : "memory");
             return false;
         }
     }
     return true;
 }
 
-// a lane's words of a code tile
+// A lane's words of a unit's two code tiles, as loaded.
 template <int W>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[W]) {
-    if constexpr (W == 2) {
-        const uint2 v = ldg_stream2(p);
-        w[0] = v.x; w[1] = v.y;
-    } else {
+struct Words {
+    uint4 v[2][W < 4 ? 1 : W / 4];
+};
+template <int W, int TILE>
+__device__ __forceinline__ void load_unit(const uint8_t* p, Words<W>& w) {
 #pragma unroll
-        for (int j = 0; j < W / 4; ++j) {
-            const uint4 v = ldg_stream(p + 16 * j);
-            w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+    for (int t = 0; t < 2; ++t) {
+        if constexpr (W == 2) {
+            const uint2 v = ldg_stream2(p + t * TILE);
+            w.v[t][0].x = v.x; w.v[t][0].y = v.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < W / 4; ++j) w.v[t][j] = ldg_stream(p + t * TILE + 16 * j);
         }
     }
 }
-
-template <int W, int TILE>
-__device__ __forceinline__ void load_unit(const uint8_t* p, uint32_t (&w)[2 * W]) {
-    uint32_t x[W], y[W];
-    load_words(p, x);
-    load_words(p + TILE, y);
+// Code tile t's words in registers of their own (the loops below move them; the loaded ones are not touched, so that
+// the next loads need not be waited for).
+template <int W>
+__device__ __forceinline__ void tile_words(const Words<W>& u, int t, uint32_t (&w)[W]) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        w[j] = x[j];
-        w[W + j] = y[j];
+    for (int j = 0; j < W; j += 2) {
+        const uint4& v = u.v[t][j / 4];
+        w[j] = j % 4 ? v.z : v.x;
+        w[j + 1] = j % 4 ? v.w : v.y;
     }
 }
-
-// A lane's words of a unit (two code tiles) are taken four channel groups (32 channels) at a time, from the front:
-// loops over them are kept loops, their bodies are small.
+// The words of four channel groups (32 channels), from the front: loops over them are kept loops, their bodies are small.
 template <int BITS, int N>
 __device__ __forceinline__ void take_words(uint32_t (&w)[N], uint32_t (&x)[BITS / 2]) {
 #pragma unroll
@@ -254,52 +280,59 @@ __device__ __forceinline__ void take_words(uint32_t (&w)[N], uint32_t (&x)[BITS 
 }
 // Keys: fp16(code * step + zero), rows row0 .. row0 + 31 of the operand at dst.  The channel group C's step and
 // zero pair of the lane is at ent + 16 C + 4 i (zeros 2 D bytes on).
-template <int D, int BITS, int N>
-__device__ __forceinline__ void key_unit(uint32_t (&w)[N], uint32_t ent, uint32_t dst, int row0, int lane) {
+template <int D, int BITS, int W>
+__device__ __forceinline__ void key_unit(const Words<W>& u, uint32_t ent, uint32_t dst, int row0, int lane) {
     const int r7 = lane & 7;
-    uint32_t rows = dst + (row0 + (lane & 15)) * 128, e = ent + 4 * (lane & 3);
-#pragma unroll 1
-    for (int it = 0; it < D / 16; ++it) {                      // 2 tiles x D / 32
-        const int c = it % (D / 32);                           // channels 32 c ..
-        uint32_t x[BITS / 2];
-        take_words<BITS>(w, x);
-        const uint32_t at = rows + (it / (D / 32)) * 2048 + (c >> 1) * (kTile * 128);
+    const uint32_t rows = dst + (row0 + (lane & 15)) * 128, e0 = ent + 4 * (lane & 3);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t s0 = lds32(e + 64 * c + 32 * h), z0 = lds32(e + 64 * c + 32 * h + 2 * D);
-            const uint32_t s1 = lds32(e + 64 * c + 32 * h + 16), z1 = lds32(e + 64 * c + 32 * h + 16 + 2 * D);
+    for (int t = 0; t < 2; ++t) {
+        uint32_t w[W];
+        tile_words(u, t, w);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {                     // channels 32 c ..
+            uint32_t x[BITS / 2];
+            take_words<BITS>(w, x);
+            const uint32_t at = rows + t * 2048 + (c >> 1) * (kTile * 128), e = e0 + 64 * c;
+            uint32_t s[4], z[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                s[g] = lds32(e + 16 * g);
+                z[g] = lds32(e + 16 * g + 2 * D);
+            }
             // matrices: (group, tokens 0-7), (group, 8-15), (next group, ...); this lane gives a row's address
-            const int chunk = 4 * (c & 1) + 2 * h + (lane >> 4);
-            const uint32_t to = at + ((chunk ^ r7) << 4);
-            if (h == 0)
-                stmatrix4(to, hfma2(code_of<BITS, 0, 0>(x), s0, z0), hfma2(code_of<BITS, 0, 1>(x), s0, z0),
-                          hfma2(code_of<BITS, 1, 0>(x), s1, z1), hfma2(code_of<BITS, 1, 1>(x), s1, z1));
-            else
-                stmatrix4(to, hfma2(code_of<BITS, 2, 0>(x), s0, z0), hfma2(code_of<BITS, 2, 1>(x), s0, z0),
-                          hfma2(code_of<BITS, 3, 0>(x), s1, z1), hfma2(code_of<BITS, 3, 1>(x), s1, z1));
+            const int chunk = 4 * (c & 1) + (lane >> 4);
+            stmatrix4(at + ((chunk ^ r7) << 4), hfma2(code_of<BITS, 0, 0>(x), s[0], z[0]), hfma2(code_of<BITS, 0, 1>(x), s[0], z[0]),
+                      hfma2(code_of<BITS, 1, 0>(x), s[1], z[1]), hfma2(code_of<BITS, 1, 1>(x), s[1], z[1]));
+            stmatrix4(at + (((chunk + 2) ^ r7) << 4), hfma2(code_of<BITS, 2, 0>(x), s[2], z[2]),
+                      hfma2(code_of<BITS, 2, 1>(x), s[2], z[2]), hfma2(code_of<BITS, 3, 0>(x), s[3], z[3]),
+                      hfma2(code_of<BITS, 3, 1>(x), s[3], z[3]));
         }
     }
 }
 // Values into columns (tokens) tok0 .. tok0 + 31 of the operand [D channels][tokens] at dst.  ent: per code tile the
 // steps, channel group j's at 32 j (this lane's four tokens at 8 i), and the zeros.
-template <int D, int BITS, int N>
-__device__ __forceinline__ void value_unit(uint32_t (&w)[N], uint32_t ent, int lgG, uint32_t dst, int tok0, int lane) {
+template <int D, int BITS, int W>
+__device__ __forceinline__ void value_unit(const Words<W>& u, uint32_t ent, int lgG, uint32_t dst, int tok0, int lane) {
     const int r7 = lane & 7, ve = 64 * (D >> lgG);
     // (128 tokens a row in two blocks of 64; a unit lies in one)
     const uint32_t rows = dst + (tok0 >> 6) * (D * 128) + (8 * (lane >> 4) + r7) * 128;
     const int chunk0 = ((tok0 >> 3) & 7) + ((lane >> 3) & 1);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        uint32_t w[W];
+        tile_words(u, t, w);
+        const uint32_t e0 = ent + t * ve + 8 * (lane & 3), at = rows + (((chunk0 + 2 * t) ^ r7) << 4);
 #pragma unroll 1
-    for (int it = 0; it < D / 16; ++it) {
-        const int c = it % (D / 32), j = it / (D / 32);
-        uint32_t x[BITS / 2];
-        take_words<BITS>(w, x);
-        const uint32_t e = ent + j * ve + 32 * ((32 * c) >> lgG) + 8 * (lane & 3);
-        const uint2 s = lds64(e), z = lds64(e + ve / 2);
-        const uint32_t to = rows + c * 4096 + (((chunk0 + 2 * j) ^ r7) << 4);
-        stmatrix4(to, hfma2(code_of<BITS, 0, 0>(x), s.x, z.x), hfma2(code_of<BITS, 0, 1>(x), s.y, z.y),
-                  hfma2(code_of<BITS, 1, 0>(x), s.x, z.x), hfma2(code_of<BITS, 1, 1>(x), s.y, z.y));
-        stmatrix4(to + 2048, hfma2(code_of<BITS, 2, 0>(x), s.x, z.x), hfma2(code_of<BITS, 2, 1>(x), s.y, z.y),
-                  hfma2(code_of<BITS, 3, 0>(x), s.x, z.x), hfma2(code_of<BITS, 3, 1>(x), s.y, z.y));
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[BITS / 2];
+            take_words<BITS>(w, x);
+            const uint32_t e = e0 + 32 * ((32 * c) >> lgG), to = at + c * 4096;
+            const uint2 s = lds64(e), z = lds64(e + ve / 2);
+            stmatrix4(to, hfma2(code_of<BITS, 0, 0>(x), s.x, z.x), hfma2(code_of<BITS, 0, 1>(x), s.y, z.y),
+                      hfma2(code_of<BITS, 1, 0>(x), s.x, z.x), hfma2(code_of<BITS, 1, 1>(x), s.y, z.y));
+            stmatrix4(to + 2048, hfma2(code_of<BITS, 2, 0>(x), s.x, z.x), hfma2(code_of<BITS, 2, 1>(x), s.y, z.y),
+                      hfma2(code_of<BITS, 3, 0>(x), s.x, z.x), hfma2(code_of<BITS, 3, 1>(x), s.y, z.y));
+        }
     }
 }
 
@@ -392,7 +425,7 @@ __device__ __forceinline__ bool value_rows(const Rows& v, int f0, uint32_t dst, 
 }
 
 // ---- spans: one warp finds them, the others read them ----
-inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, int lane) {
+inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, uint32_t bars, int lane) {
     if (lane == 0) {
         ChunkWalk walk;
         walk.start(&a.plan, a.seqs, a.n_seqs, chunk_begin(a.weight, a.n_ctas, blockIdx.x),
@@ -402,7 +435,7 @@ inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, int lane) {
         while (more) {
             more = walk.next();
             const uint32_t slot = n % kSpanRing;
-            wait_for<true>(b, &b.span_empty[slot], ((n / kSpanRing) & 1) ^ 1);
+            wait_for<true>(bars, bars + BAR(span_empty) + 8 * (slot), ((n / kSpanRing) & 1) ^ 1);
             Span o;
             o.more = more;
             if (more) {
@@ -434,7 +467,7 @@ inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, int lane) {
             atomicAnd(&b.bad, ~(1u << ((n + 8) % 32)));
             atomicAnd(&b.odd, ~(1u << ((n + 8) % 32)));
             b.spans[slot] = o;
-            arrive(&b.span_full[slot]);
+            arrive(bars + BAR(span_full) + 8 * (slot));
             ++n;
         }
     }
@@ -442,84 +475,84 @@ inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, int lane) {
 }
 // A warp's view of them: next() gives the next span, which stays in place until the one after is asked for.
 struct SpanReader {
-    Bars& b;
+    const Bars& b;
+    uint32_t bars;
     uint32_t n;                 // of spans read; the present one is number n - 1
     __device__ __forceinline__ unsigned mark() const { return 1u << ((n - 1) % 32); }
-    __device__ __forceinline__ explicit SpanReader(Bars& bars) : b(bars), n(0) {}
-    __device__ __forceinline__ const Span* next(int lane) {
-        if (n) {
-            __syncwarp();
-            if (lane == 0) arrive(&b.span_empty[(n - 1) % kSpanRing]);
-        }
+    __device__ __forceinline__ SpanReader(const Bars& data, uint32_t at) : b(data), bars(at), n(0) {}
+    __device__ __forceinline__ void release() const { arrive(bars + BAR(span_empty) + 8 * ((n - 1) % kSpanRing)); }
+    __device__ __forceinline__ const Span* next() {              // one lane alone, or all of a warp with the same result
         const uint32_t slot = n % kSpanRing;
-        const bool ok = __all_sync(kFull, wait_for<true>(b, &b.span_full[slot], (n / kSpanRing) & 1));
+        const bool ok = wait_for<true>(bars, bars + BAR(span_full) + 8 * slot, (n / kSpanRing) & 1);
         ++n;
         const Span* s = &b.spans[slot];
         return ok && s->more ? s : nullptr;
+    }
+    __device__ __forceinline__ const Span* next(int lane) {      // a whole warp
+        if (n) {
+            __syncwarp();
+            if (lane == 0) release();
+        }
+        return next();
     }
 };
 
 // ---- producers: warp w of 4 fills tokens 32 w .. 32 w + 31 of each tile, keys or values ----
 template <int D, int BITS, bool VALUES>
-__device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t smem, int w, int lane) {
+__device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t smem, int w, int lane) {
     using S = Shape<D, BITS>;
     constexpr int W = S::W, TILE = S::TILE;
-    uint64_t* full = VALUES ? b.v_full : b.k_full;
-    uint64_t* empty = VALUES ? b.v_empty : b.k_empty;
+    const uint32_t full = bars + (VALUES ? BAR(v_full) : BAR(k_full)), empty = bars + (VALUES ? BAR(v_empty) : BAR(k_empty));
     const uint32_t ent = smem + S::OFF_ENT + (4 * VALUES + w) * (4 * D);
     const int lgG = a.lgG, ve = 64 * (D >> lgG);               // bytes of value entries of a code tile
     const int n_ent = VALUES ? 2 * ve / 16 : 4 * D / 16;       // 16-byte groups of a unit's steps and zeros
     const long long resid = VALUES ? a.v_resid_off : a.k_resid_off;
     const __half* chunk = VALUES ? a.v : a.k;
     const long long step = VALUES ? a.v_stride[0] : a.k_stride[0], per_head = VALUES ? a.v_stride[1] : a.k_stride[1];
-    SpanReader reader(b);
+    SpanReader reader(b, bars);
     // the unit ahead: its span's fields, and its bytes where it is quantized
-    int t = 0, t_end = 0, key0 = 0, n_quant = 0, seq = 0, head = 0, tok0 = 0, n_resid = 0, t1 = 0;
-    bool more = true, quantized = false;
+    const Span* sp = nullptr;
+    int t = 0, t_end = 0, n_quant = 0;
+    bool quantized = false;
     int have = 0, entry = 0;                                   // table entries of tiles have .. have + 31, one a lane
-    const uint8_t* codes = nullptr;                            // of the unit ahead, this lane's
-    uint32_t words[2 * W];
+    const uint8_t *base = nullptr, *codes = nullptr;           // page 0's part; of the unit ahead, this lane's words
+    Words<W> words;
     uint4 ents{};
     auto ahead = [&]() {
         bool fresh = false;
         if (++t >= t_end) {
-            const Span* sp = reader.next(lane);
-            more = sp != nullptr;
-            if (!more) return;
+            sp = reader.next(lane);
+            if (!sp) return;
             t = sp->tile0;
             t_end = t + sp->nt;
             n_quant = sp->n_quant;
-            seq = sp->seq;
-            head = sp->head;
-            tok0 = sp->tok0;
-            n_resid = sp->n_resid;
-            t1 = sp->t1;
+            base = a.buf + (2LL * sp->head + VALUES) * a.part_bytes;
             fresh = true;
         }
-        key0 = t * kTile + 32 * w;
+        const int key0 = t * kTile + 32 * w;
         quantized = key0 < n_quant;
         if (!quantized) return;
         if (fresh || t >= have + 32) {
             have = t;
             const int key = (t + lane) * kTile + 32 * w;
-            entry = key < n_quant ? ldg_int(a.table + (long long)seq * a.max_blocks + (key >> lgG)) : 0;
+            entry = key < n_quant ? ldg_int(a.table + (long long)sp->seq * a.max_blocks + (key >> lgG)) : 0;
         }
         int page = __shfl_sync(kFull, entry, t - have);
         if ((unsigned)page >= (unsigned)a.n_pages) {           // an entry outside the pool: the span's outputs are NaN
             page = 0;
             if (lane == 0) atomicOr(&b.bad, reader.mark());
         }
-        const uint8_t* part = a.buf + (long long)page * a.page_bytes + (2LL * head + VALUES) * a.part_bytes;
+        const uint8_t* part = base + (unsigned long long)(unsigned)page * (unsigned)a.page_bytes;   // (a page: under 2^32 bytes)
         const int tile = (key0 & ((1 << lgG) - 1)) >> 4, tiles = 1 << (lgG - 4);
         codes = part + tile * TILE + lane * (4 * W);
-        if (lane < n_ent) ents = ldg_stream(part + tiles * TILE + (VALUES ? tile * ve : 0) + 16 * lane);
+        ents = ldg_stream(part + tiles * TILE + (VALUES ? tile * ve : 0) + 16 * min(lane, n_ent - 1));
     };
     ahead();
-    if (more && quantized) load_unit<W, TILE>(codes, words);
-    for (uint32_t tc = 0; more; ++tc) {
+    if (sp && quantized) load_unit<W, TILE>(codes, words);
+    for (uint32_t tc = 0; sp; ++tc) {
         const uint32_t stage = tc & 1, ph = (tc >> 1) & 1;
         const uint32_t dst = smem + (VALUES ? S::OFF_V : S::OFF_K) + stage * S::K_BYTES;
-        const bool ok = __all_sync(kFull, wait_for(b, &empty[stage], ph ^ 1));
+        const bool ok = __all_sync(kFull, wait_for(bars, empty + 8 * stage, ph ^ 1));
         if (quantized) {
             if (lane < n_ent) sts128(ent + 16 * lane, ents);
             __syncwarp();
@@ -527,94 +560,90 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t smem, int w, in
             else key_unit<D, BITS>(words, ent, dst, 32 * w, lane);
         } else {
             if (ok) {
-                const Rows r{reinterpret_cast<const __half*>(a.buf + resid) + ((long long)seq * a.plan.Hkv + head) * a.R * D,
-                             chunk + tok0 * step + head * per_head, step, n_resid, n_resid + t1};
+                const Rows r{reinterpret_cast<const __half*>(a.buf + resid) +
+                                 ((long long)sp->seq * a.plan.Hkv + sp->head) * a.R * D,
+                             chunk + sp->tok0 * step + sp->head * per_head, step, sp->n_resid, sp->n_resid + sp->t1};
+                const int f0 = t * kTile + 32 * w - n_quant;
                 if constexpr (VALUES) {
-                    if (value_rows<D>(r, key0 - n_quant, dst, 32 * w, lane) && lane == 0) atomicOr(&b.odd, reader.mark());
+                    if (value_rows<D>(r, f0, dst, 32 * w, lane) && lane == 0) atomicOr(&b.odd, reader.mark());
                 } else {
-                    key_rows<D>(r, key0 - n_quant, dst, 32 * w, lane);
+                    key_rows<D>(r, f0, dst, 32 * w, lane);
                 }
             }
         }
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) arrive(&full[stage]);
+        if (lane == 0) arrive(full + 8 * stage);
         ahead();
-        if (more && quantized) load_unit<W, TILE>(codes, words);
+        if (sp && quantized) load_unit<W, TILE>(codes, words);
     }
 }
 
-// ---- MMA issue: the warp runs as one, so that descriptors stay in uniform registers; one lane issues ----
+// ---- MMA issue: one thread ----
+// A turn is x's product P V and its next S, over the P that the product reads: one thread's MMAs run in the order
+// of their issue.  Turns are short of time (two to a tile): every wait that is met costs some 60 cycles, a commit 130.
 template <int D, int BITS>
-__device__ void issue_mmas(const ChunkArgs& a, Bars& b, uint32_t smem, uint32_t tmem, int lane) {
+__device__ void issue_mmas(const Bars& b, uint32_t bars, uint32_t smem, uint32_t tmem) {
     using S = Shape<D, BITS>;
     uint32_t tc = 0, qc = 0, pc = 0;                         // tiles; bit x: parity of the next wait for A or B
     const uint32_t kind_s = mma_kind(kTile), kind_o = mma_kind(D);
-    const uint32_t one = elect_one();
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(kFull, wait_for(b, bar, parity)); };
-    SpanReader reader(b);
-    while (const Span* sp = reader.next(lane)) {
-        const int both = sp->both, na = sp->na, nb = sp->nb, steps = max(na, nb);
-        for (int i = -1; i < steps; ++i) {
+    auto wait = [&](uint32_t bar, uint32_t parity) { ok = ok && wait_for(bars, bar, parity); };
+    const uint64_t q0 = operand(smem + S::OFF_Q), k0 = operand(smem + S::OFF_K), v0 = operand(smem + S::OFF_V);
+    SpanReader reader(b, bars);
+    while (const Span* sp = reader.next()) {
+        const int both = sp->both, na = sp->na, nb = sp->nb, nt = sp->nt;
+        reader.release();
+        for (int i = -1; i < max(na, nb); ++i) {
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 const int n = x ? nb : na;
                 if (i < 0) {
                     if (both || x == 0) {
-                        wait(&b.q_full[x], (qc >> x) & 1);
+                        wait(bars + BAR(q_full) + 8 * x, (qc >> x) & 1);
                         qc ^= 1u << x;
                     }
                 } else if (i < n) {
                     // (both: B has every tile; alternate: a tile that one lacks is nobody's)
                     const uint32_t c = tc + (both ? i : 2 * i + x), stage = c & 1;
-                    wait(&b.p_full[x], (pc >> x) & 1);
+                    if (!both || x == 0 || i >= na) wait(bars + BAR(v_full) + 8 * stage, (c >> 1) & 1);
+                    wait(bars + BAR(p_full) + 8 * x, (pc >> x) & 1);
                     pc ^= 1u << x;
-                    wait(&b.v_full[stage], (c >> 1) & 1);
                     if (ok) {                                // O_x += P_x V_t
                         fence_after();
-                        const uint64_t va = operand(smem + S::OFF_V + stage * S::K_BYTES);
+                        const uint64_t va = v0 + stage * (S::K_BYTES >> 4);
                         const uint32_t o = tmem + S::COL_O + x * D, pa = tmem + S::COL_S + x * kTile;
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(o, pa + 8 * k, va + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), kind_o, i > 0 || k > 0, one);
-                        if (!both || x == 1) commit(&b.v_empty[stage], one);
-                        if (i + 1 == n) commit(&b.o_full[x], one);
+                            mma_ts(o, pa + 8 * k, va + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), kind_o, k > 0 || i > 0);
+                        if (i + 1 == n) commit(bars + BAR(o_full) + 8 * x);
+                        if (!both || x == 1) commit(bars + BAR(v_empty) + 8 * stage);
                     }
                 }
                 if (i + 1 < n) {
                     const uint32_t c = tc + (both ? i + 1 : 2 * (i + 1) + x), stage = c & 1;
-                    wait(&b.k_full[stage], (c >> 1) & 1);
+                    if (!both || x == 0 || i + 1 >= na) wait(bars + BAR(k_full) + 8 * stage, (c >> 1) & 1);
                     if (ok) {                                // S_x = Q_x K_t^T
                         fence_after();
-                        const uint64_t qa = operand(smem + S::OFF_Q + (both ? x : 0) * S::Q_BYTES);
-                        const uint64_t ka = operand(smem + S::OFF_K + stage * S::K_BYTES);
+                        const uint64_t qa = q0 + (both ? x : 0) * (S::Q_BYTES >> 4), ka = k0 + stage * (S::K_BYTES >> 4);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
                             const uint32_t off = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
-                            mma_ss(tmem + S::COL_S + x * kTile, qa + off, ka + off, kind_s, k > 0, one);
+                            mma_ss(tmem + S::COL_S + x * kTile, qa + off, ka + off, kind_s, k > 0);
                         }
-                        commit(&b.s_full[x], one);
-                        if (!both || x == 1) commit(&b.k_empty[stage], one);
+                        commit(bars + BAR(s_full) + 8 * x);
+                        if (!both || x == 1) commit(bars + BAR(k_empty) + 8 * stage);
                     }
                 }
             }
         }
-        tc += sp->nt;
+        tc += nt;
     }
-    commit(&b.drained, one);       // no MMA is in flight when the CTA ends
-    mbar_wait(&b.drained, 0);
+    commit(bars + BAR(drained));   // no MMA is in flight when the CTA ends
+    wait_for<true>(bars, bars + BAR(drained), 0);
 }
 
 // ---- softmax of tile X (four warps, a row a lane) ----
-__device__ __forceinline__ float max32(const float (&v)[32]) {
-    float m[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-    for (int j = 4; j < 28; j += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(m[k], v[j + k]), v[j + 4 + k]);
-    return fmaxf(fmaxf(fmaxf(m[0], v[28]), fmaxf(m[1], v[29])), fmaxf(fmaxf(m[2], v[30]), fmaxf(m[3], v[31])));
-}
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -635,34 +664,41 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// Weights 2^(mul v - ref) of 32 columns, as fp16 to `at`, their sums (mul and -ref twice each).
-__device__ __forceinline__ void weights32(uint32_t at, const float (&v)[32], uint64_t mul, uint64_t ref, uint64_t (&sum)[2]) {
-    uint32_t p[16];
+// Weights 2^(mul v - ref) of 16 columns as fp16 pairs, their sums (mul and -ref twice each).
+__device__ __forceinline__ void weights16(uint32_t* p, const float* v, uint64_t mul, uint64_t ref, uint64_t (&sum)[2]) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
+    for (int j = 0; j < 16; j += 2) {
         float2 y = unpair(fma2(pair(v[j], v[j + 1]), mul, ref));
         y.x = exp2_ftz(y.x);
         y.y = exp2_ftz(y.y);
         sum[(j / 2) & 1] = add2(sum[(j / 2) & 1], pair(y.x, y.y));
         p[j / 2] = pack_f16x2(y.x, y.y);
     }
-    st16(at, p);
+}
+__device__ __forceinline__ float max16(float m, const float (&v)[16]) {
+    float n = fmaxf(v[0], v[1]);
+#pragma unroll
+    for (int j = 2; j < 16; j += 4) {
+        m = fmaxf(fmaxf(m, v[j]), v[j + 1]);
+        if (j + 2 < 16) n = fmaxf(fmaxf(n, v[j + 2]), v[j + 3]);
+    }
+    return fmaxf(m, n);
 }
 template <int D, int BITS, bool MOD>
-__device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2* xch, uint32_t tmem, int x, int warp, int lane) {
+__device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t smem, float2* xch, uint32_t tmem, int x, int warp, int lane) {
     using S = Shape<D, BITS>;
     const int row = 32 * (warp & 3) + lane;                    // of tile X
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = lanes + S::COL_S + x * kTile, to = lanes + S::COL_O + x * D;
     const int nq = a.plan.nq;
     uint32_t sc = 0, oc = 0;
-    SpanReader reader(b);
+    SpanReader reader(b, bars);
     while (const Span* sp = reader.next(lane)) {
         const bool both = sp->both;
         const int r = both ? x * kHalf + row : row;            // row of the item
         const bool valid = r < (sp->t1 - sp->t0) * nq;
         const int tok = sp->t0 + r / nq, head = sp->head * nq + r % nq;
-        const int steps = sp->tiles(x);
+        const int steps = sp->tiles(x), tile0 = sp->tile0;
         // queries into the operand
         if (both || x == 0) {
             const __half* src = a.q + (long long)(sp->tok0 + tok) * a.q_stride[0] + head * a.q_stride[1];
@@ -673,7 +709,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                        valid ? ldg_row(src + 8 * c) : uint4{0, 0, 0, 0});
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) arrive(&b.q_full[x]);
+            if (lane == 0) arrive(bars + BAR(q_full) + 8 * (x));
         }
         const long long pos = (long long)sp->n_quant + sp->n_resid + tok;   // the row's position
         const int hi = (int)pos;                                            // last and first key that it sees
@@ -685,8 +721,8 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
         const float cap_in = a.scale * (2.f * kLog2e) / a.cap, cap_out = a.cap * kLog2e;    // (without a cap: not used)
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < steps; ++i) {
-            const int key0 = (sp->tile0 + (both ? i : 2 * i + x)) * kTile;
-            const bool ok = wait_for(b, &b.s_full[x], sc & 1);
+            const int key0 = (tile0 + (both ? i : 2 * i + x)) * kTile;
+            const bool ok = wait_for(bars, bars + BAR(s_full) + 8 * (x), sc & 1);
             float mul = a.scale_log2;
             ++sc;
             fence_after();
@@ -698,7 +734,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                     for (int c = 0; c < 4; ++c) {
                         float v[32];
                         ld32(ts + 32 * c, v);
-                        wait_ld();
+                        wait_ld(v);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const int key = key0 + 32 * c + j;
@@ -721,23 +757,40 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                     wait_st();
                     mul = 1.f;
                 }
+                // One walk over the logits: the weights by the present reference are kept in registers until the
+                // tile's maximum has shown that they are in range (S stays as it is until then).
+                const uint64_t mul2 = pair(mul, mul);
                 float mx = -INFINITY;
+                bool high;
                 {
-                    float v[32], u[32];
-                    ld32(ts, v);
-#pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        wait_ld();
-                        ld32(ts + 32 * c + 32, u);
-                        mx = fmaxf(mx, max32(v));
-                        wait_ld();
-                        if (c == 0) ld32(ts + 64, v);
-                        mx = fmaxf(mx, max32(u));
+                    const float ref = m == -INFINITY ? 0.f : m - kLift;
+                    const uint64_t ref2 = pair(-ref, -ref);
+                    uint64_t sum[2] = {0, 0};
+                    uint32_t p[64];
+                    float v[16], u[16];
+                    ld16(ts, v);
+#pragma unroll
+                    for (int c = 0; c < 8; c += 2) {
+                        wait_ld(v);
+                        ld16(ts + 16 * c + 16, u);
+                        mx = max16(mx, v);
+                        weights16(p + 8 * c, v, mul2, ref2, sum);
+                        wait_ld(u);
+                        if (c < 6) ld16(ts + 16 * c + 32, v);
+                        mx = max16(mx, u);
+                        weights16(p + 8 * c + 8, u, mul2, ref2, sum);
+                    }
+                    mx *= mul;
+                    high = __any_sync(kFull, mx > m + kRaise);
+                    if (!high) {
+                        st32(ts, p);
+                        st32(ts + 32, p + 32);
+                        const float2 total = unpair(add2(sum[0], sum[1]));
+                        l += total.x + total.y;
                     }
                 }
-                mx *= mul;
-                // the reference is raised, and what is summed so far scaled, where a row needs it
-                if (__any_sync(kFull, mx > m + kRaise)) {
+                if (high) {
+                    // the reference is raised, what is summed so far scaled, the weights taken again
                     const float top = fmaxf(m, mx);
                     const float f = m == -INFINITY ? 0.f : exp2_ftz(m - top);
                     if (i > 0) {
@@ -746,42 +799,39 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                         for (int c = 0; c < D / 32; ++c) {
                             float o[32];
                             ld32(to + 32 * c, o);
-                            wait_ld();
+                            wait_ld(o);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) o[j] *= f;
                             st32(to + 32 * c, o);
                         }
                     }
                     m = top;
-                }
-                const float ref = m == -INFINITY ? 0.f : m - kLift;
-                const uint64_t mul2 = pair(mul, mul), ref2 = pair(-ref, -ref);
-                uint64_t sum[2] = {0, 0};
-                {
-                    float v[32], u[32];
-                    ld32(ts, v);
+                    const float ref = m == -INFINITY ? 0.f : m - kLift;
+                    const uint64_t ref2 = pair(-ref, -ref);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        wait_ld();
-                        ld32(ts + 32 * c + 32, u);
-                        weights32(ts + 16 * c, v, mul2, ref2, sum);
-                        wait_ld();
-                        if (c == 0) ld32(ts + 64, v);
-                        weights32(ts + 16 * c + 16, u, mul2, ref2, sum);
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        uint32_t p[16];
+                        ld32(ts + 32 * c, v);
+                        wait_ld(v);
+                        weights16(p, v, mul2, ref2, sum);
+                        weights16(p + 8, v + 16, mul2, ref2, sum);
+                        st16(ts + 16 * c, p);
                     }
+                    const float2 total = unpair(add2(sum[0], sum[1]));
+                    l += total.x + total.y;
                 }
-                const float2 total = unpair(add2(sum[0], sum[1]));
-                l += total.x + total.y;
                 wait_st();
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) arrive(&b.p_full[x]);
+            if (lane == 0) arrive(bars + BAR(p_full) + 8 * (x));
         }
         // ---- epilogue ----
         bool fine = true;
         if (steps) {
-            fine = wait_for(b, &b.o_full[x], oc & 1);
+            fine = wait_for(bars, bars + BAR(o_full) + 8 * (x), oc & 1);
             ++oc;
         }
         fence_after();
@@ -830,7 +880,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                 __syncwarp();
                 if (steps) {
                     ld32(to + 32 * c, o);
-                    wait_ld();
+                    wait_ld(o);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = 0.f;
@@ -838,7 +888,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t smem, float2*
                 if (join) {
                     float p[32];
                     ld32(lanes + S::COL_O + D + 32 * c, p);
-                    wait_ld();
+                    wait_ld(p);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = o[j] * wa + p[j] * wb;
                 }
@@ -871,7 +921,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     using S = Shape<D, BITS>;
     extern __shared__ uint8_t raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t smem = smem_u32(base);
+    const uint32_t smem = smem_u32(base), bars = smem + S::OFF_BAR;
     Bars& b = *reinterpret_cast<Bars*>(base + S::OFF_BAR);
     float2* xch = reinterpret_cast<float2*>(base + S::OFF_XCH);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -904,15 +954,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     const uint32_t tmem = b.tmem;
     if (warp < 8) {
         more_regs<kRegsSoftmax>();
-        softmax_rows<D, BITS, MOD>(a, b, smem, xch, tmem, warp >> 2, warp, lane);
+        softmax_rows<D, BITS, MOD>(a, b, bars, smem, xch, tmem, warp >> 2, warp, lane);
     } else if (warp < 16) {
         fewer_regs<kRegsFill>();
-        if (warp < 12) fill_tiles<D, BITS, false>(a, b, smem, warp - 8, lane);
-        else fill_tiles<D, BITS, true>(a, b, smem, warp - 12, lane);
+        if (warp < 12) fill_tiles<D, BITS, false>(a, b, bars, smem, warp - 8, lane);
+        else fill_tiles<D, BITS, true>(a, b, bars, smem, warp - 12, lane);
     } else {
         fewer_regs<kRegsRest>();
-        if (warp == 16) issue_mmas<D, BITS>(a, b, smem, tmem, lane);
-        else if (warp == 17) plan_spans(a, b, lane);
+        if (warp == 16) {
+            if (elect_one()) issue_mmas<D, BITS>(b, bars, smem, tmem);
+            __syncwarp();
+        }
+        if (warp == 17) plan_spans(a, b, bars, lane);
     }
     fence_before();
     __syncthreads();
