@@ -265,9 +265,9 @@ template <int W>
 __device__ __forceinline__ void tile_words(const Words<W>& u, int t, uint32_t (&w)[W]) {
 #pragma unroll
     for (int j = 0; j < W; j += 2) {
-        const uint4& v = u.v[t][j / 4];
-        w[j] = j % 4 ? v.z : v.x;
-        w[j + 1] = j % 4 ? v.w : v.y;
+        const uint4 &p = u.v[0][j / 4], &q = u.v[1][j / 4];
+        w[j] = j % 4 ? (t ? q.z : p.z) : (t ? q.x : p.x);
+        w[j + 1] = j % 4 ? (t ? q.w : p.w) : (t ? q.y : p.y);
     }
 }
 // The words of four channel groups (32 channels), from the front: loops over them are kept loops, their bodies are small.
@@ -284,7 +284,7 @@ template <int D, int BITS, int W>
 __device__ __forceinline__ void key_unit(const Words<W>& u, uint32_t ent, uint32_t dst, int row0, int lane) {
     const int r7 = lane & 7;
     const uint32_t rows = dst + (row0 + (lane & 15)) * 128, e0 = ent + 4 * (lane & 3);
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
         uint32_t w[W];
         tile_words(u, t, w);
@@ -317,7 +317,7 @@ __device__ __forceinline__ void value_unit(const Words<W>& u, uint32_t ent, int 
     // (128 tokens a row in two blocks of 64; a unit lies in one)
     const uint32_t rows = dst + (tok0 >> 6) * (D * 128) + (8 * (lane >> 4) + r7) * 128;
     const int chunk0 = ((tok0 >> 3) & 7) + ((lane >> 3) & 1);
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
         uint32_t w[W];
         tile_words(u, t, w);
@@ -498,24 +498,23 @@ struct SpanReader {
 };
 
 // ---- producers: warp w of 4 fills tokens 32 w .. 32 w + 31 of each tile, keys or values ----
-template <int D, int BITS, bool VALUES>
-__device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t smem, int w, int lane) {
+// (one body for both: the instruction cache)
+template <int D, int BITS>
+__device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t smem, bool values, int w, int lane) {
     using S = Shape<D, BITS>;
     constexpr int W = S::W, TILE = S::TILE;
-    const uint32_t full = bars + (VALUES ? BAR(v_full) : BAR(k_full)), empty = bars + (VALUES ? BAR(v_empty) : BAR(k_empty));
-    const uint32_t ent = smem + S::OFF_ENT + (4 * VALUES + w) * (4 * D);
+    const uint32_t full = bars + (values ? BAR(v_full) : BAR(k_full)), empty = bars + (values ? BAR(v_empty) : BAR(k_empty));
+    const uint32_t ent = smem + S::OFF_ENT + (4 * values + w) * (4 * D);
+    const uint32_t stages = smem + (values ? S::OFF_V : S::OFF_K);
     const int lgG = a.lgG, ve = 64 * (D >> lgG);               // bytes of value entries of a code tile
-    const int n_ent = VALUES ? 2 * ve / 16 : 4 * D / 16;       // 16-byte groups of a unit's steps and zeros
-    const long long resid = VALUES ? a.v_resid_off : a.k_resid_off;
-    const __half* chunk = VALUES ? a.v : a.k;
-    const long long step = VALUES ? a.v_stride[0] : a.k_stride[0], per_head = VALUES ? a.v_stride[1] : a.k_stride[1];
+    const int last_ent = (values ? 2 * ve / 16 : 4 * D / 16) - 1;   // 16-byte groups of a unit's steps and zeros, less one
     SpanReader reader(b, bars);
-    // the unit ahead: its span's fields, and its bytes where it is quantized
+    // the unit ahead: its bytes where it is quantized
     const Span* sp = nullptr;
     int t = 0, t_end = 0, n_quant = 0;
     bool quantized = false;
     int have = 0, entry = 0;                                   // table entries of tiles have .. have + 31, one a lane
-    const uint8_t *base = nullptr, *codes = nullptr;           // page 0's part; of the unit ahead, this lane's words
+    const uint8_t* base = nullptr;                             // page 0's part
     Words<W> words;
     uint4 ents{};
     auto ahead = [&]() {
@@ -526,7 +525,7 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
             t = sp->tile0;
             t_end = t + sp->nt;
             n_quant = sp->n_quant;
-            base = a.buf + (2LL * sp->head + VALUES) * a.part_bytes;
+            base = a.buf + (2 * sp->head + values) * a.part_bytes;
             fresh = true;
         }
         const int key0 = t * kTile + 32 * w;
@@ -543,39 +542,33 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
             if (lane == 0) atomicOr(&b.bad, reader.mark());
         }
         const uint8_t* part = base + (unsigned long long)(unsigned)page * (unsigned)a.page_bytes;   // (a page: under 2^32 bytes)
-        const int tile = (key0 & ((1 << lgG) - 1)) >> 4, tiles = 1 << (lgG - 4);
-        codes = part + tile * TILE + lane * (4 * W);
-        ents = ldg_stream(part + tiles * TILE + (VALUES ? tile * ve : 0) + 16 * min(lane, n_ent - 1));
+        const int tile = (key0 & ((1 << lgG) - 1)) >> 4;
+        ents = ldg_stream(part + (TILE << (lgG - 4)) + (values ? tile * ve : 0) + 16 * min(lane, last_ent));
+        load_unit<W, TILE>(part + tile * TILE + lane * (4 * W), words);
     };
     ahead();
-    if (sp && quantized) load_unit<W, TILE>(codes, words);
     for (uint32_t tc = 0; sp; ++tc) {
         const uint32_t stage = tc & 1, ph = (tc >> 1) & 1;
-        const uint32_t dst = smem + (VALUES ? S::OFF_V : S::OFF_K) + stage * S::K_BYTES;
+        const uint32_t dst = stages + stage * S::K_BYTES;
         const bool ok = __all_sync(kFull, wait_for(bars, empty + 8 * stage, ph ^ 1));
         if (quantized) {
-            if (lane < n_ent) sts128(ent + 16 * lane, ents);
+            if (lane <= last_ent) sts128(ent + 16 * lane, ents);
             __syncwarp();
-            if constexpr (VALUES) value_unit<D, BITS>(words, ent, lgG, dst, 32 * w, lane);
+            if (values) value_unit<D, BITS>(words, ent, lgG, dst, 32 * w, lane);
             else key_unit<D, BITS>(words, ent, dst, 32 * w, lane);
-        } else {
-            if (ok) {
-                const Rows r{reinterpret_cast<const __half*>(a.buf + resid) +
-                                 ((long long)sp->seq * a.plan.Hkv + sp->head) * a.R * D,
-                             chunk + sp->tok0 * step + sp->head * per_head, step, sp->n_resid, sp->n_resid + sp->t1};
-                const int f0 = t * kTile + 32 * w - n_quant;
-                if constexpr (VALUES) {
-                    if (value_rows<D>(r, f0, dst, 32 * w, lane) && lane == 0) atomicOr(&b.odd, reader.mark());
-                } else {
-                    key_rows<D>(r, f0, dst, 32 * w, lane);
-                }
-            }
+        } else if (ok) {
+            const long long resid = values ? a.v_resid_off : a.k_resid_off;
+            const long long step = values ? a.v_stride[0] : a.k_stride[0], per_head = values ? a.v_stride[1] : a.k_stride[1];
+            const Rows r{reinterpret_cast<const __half*>(a.buf + resid) + ((long long)sp->seq * a.plan.Hkv + sp->head) * a.R * D,
+                         (values ? a.v : a.k) + sp->tok0 * step + sp->head * per_head, step, sp->n_resid, sp->n_resid + sp->t1};
+            const int f0 = t * kTile + 32 * w - n_quant;
+            if (!values) key_rows<D>(r, f0, dst, 32 * w, lane);
+            else if (value_rows<D>(r, f0, dst, 32 * w, lane) && lane == 0) atomicOr(&b.odd, reader.mark());
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) arrive(full + 8 * stage);
         ahead();
-        if (sp && quantized) load_unit<W, TILE>(codes, words);
     }
 }
 
@@ -664,60 +657,61 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// Weights 2^(mul v - ref) of 16 columns as fp16 pairs, their sums (mul and -ref twice each).
-__device__ __forceinline__ void weights16(uint32_t* p, const float* v, uint64_t mul, uint64_t ref, uint64_t (&sum)[2]) {
+// Weights 2^(mul v - ref) of 32 columns, as fp16 to `at`, their sums (mul and -ref twice each).
+__device__ __forceinline__ void weights32(uint32_t at, const float (&v)[32], uint64_t mul, uint64_t ref, uint64_t (&sum)[2]) {
+    uint32_t p[16];
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
+    for (int j = 0; j < 32; j += 2) {
         float2 y = unpair(fma2(pair(v[j], v[j + 1]), mul, ref));
         y.x = exp2_ftz(y.x);
         y.y = exp2_ftz(y.y);
         sum[(j / 2) & 1] = add2(sum[(j / 2) & 1], pair(y.x, y.y));
         p[j / 2] = pack_f16x2(y.x, y.y);
     }
+    st16(at, p);
 }
-__device__ __forceinline__ float max16(float m, const float (&v)[16]) {
-    float n = fmaxf(v[0], v[1]);
+__device__ __forceinline__ float max32(const float (&v)[32]) {
+    float m[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int j = 2; j < 16; j += 4) {
-        m = fmaxf(fmaxf(m, v[j]), v[j + 1]);
-        if (j + 2 < 16) n = fmaxf(fmaxf(n, v[j + 2]), v[j + 3]);
-    }
-    return fmaxf(m, n);
+    for (int j = 4; j < 28; j += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(m[k], v[j + k]), v[j + 4 + k]);
+    return fmaxf(fmaxf(fmaxf(m[0], v[28]), fmaxf(m[1], v[29])), fmaxf(fmaxf(m[2], v[30]), fmaxf(m[3], v[31])));
 }
+
 template <int D, int BITS, bool MOD>
 __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t smem, float2* xch, uint32_t tmem, int x, int warp, int lane) {
     using S = Shape<D, BITS>;
     const int row = 32 * (warp & 3) + lane;                    // of tile X
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = lanes + S::COL_S + x * kTile, to = lanes + S::COL_O + x * D;
-    const int nq = a.plan.nq;
+    const int lgq = a.plan.nq >> 1;                            // log2 of 1, 2 or 4 query heads
     uint32_t sc = 0, oc = 0;
     SpanReader reader(b, bars);
     while (const Span* sp = reader.next(lane)) {
         const bool both = sp->both;
         const int r = both ? x * kHalf + row : row;            // row of the item
-        const bool valid = r < (sp->t1 - sp->t0) * nq;
-        const int tok = sp->t0 + r / nq, head = sp->head * nq + r % nq;
+        const int n_rows = (sp->t1 - sp->t0) << lgq;
         const int steps = sp->tiles(x), tile0 = sp->tile0;
         // queries into the operand
         if (both || x == 0) {
-            const __half* src = a.q + (long long)(sp->tok0 + tok) * a.q_stride[0] + head * a.q_stride[1];
+            const __half* src = a.q + (long long)(sp->tok0 + sp->t0 + (r >> lgq)) * a.q_stride[0] +
+                                ((sp->head << lgq) + (r & ((1 << lgq) - 1))) * a.q_stride[1];
             const uint32_t dst = smem + S::OFF_Q + x * S::Q_BYTES;
 #pragma unroll 4
             for (int c = 0; c < D / 8; ++c)
-                sts128(dst + operand_at<kHalf>(row, c),
-                       valid ? ldg_row(src + 8 * c) : uint4{0, 0, 0, 0});
+                sts128(dst + operand_at<kHalf>(row, c), r < n_rows ? ldg_row(src + 8 * c) : uint4{0, 0, 0, 0});
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) arrive(bars + BAR(q_full) + 8 * (x));
+            if (lane == 0) arrive(bars + BAR(q_full) + 8 * x);
         }
-        const long long pos = (long long)sp->n_quant + sp->n_resid + tok;   // the row's position
-        const int hi = (int)pos;                                            // last and first key that it sees
-        const int lo = a.plan.window ? max(0, (int)(pos - a.plan.window + 1)) : 0;
-        // rows of the warp: the first one sees least, the last one (that exists) starts last
-        const int w_hi = __shfl_sync(kFull, hi, 0), w_lo = __shfl_sync(kFull, lo, 31);
-        const bool any = __any_sync(kFull, valid);
-        const float slope = MOD && a.slopes && valid ? __ldg(a.slopes + head) * kLog2e : 0.f;
+        // A row's position is p0 + (r >> lgq): the last key that it sees.  Of the warp's rows the first one sees
+        // least, the last one starts last.
+        const int p0 = sp->n_quant + sp->n_resid + sp->t0, r0 = r - lane;
+        const int w_hi = p0 + (r0 >> lgq), w_lo = a.plan.window ? p0 + ((r0 + 31) >> lgq) - a.plan.window + 1 : 0;
+        const bool any = r0 < n_rows;
+        const float slope = MOD && a.slopes && r < n_rows
+                                ? __ldg(a.slopes + (sp->head << lgq) + (r & ((1 << lgq) - 1))) * kLog2e : 0.f;
         const float cap_in = a.scale * (2.f * kLog2e) / a.cap, cap_out = a.cap * kLog2e;    // (without a cap: not used)
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < steps; ++i) {
@@ -730,6 +724,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                 // (loops over a tile's columns stay loops: unrolled, the roles' code misses the instruction cache)
                 const bool cut = key0 + kTile - 1 > w_hi || key0 < w_lo;
                 if (MOD || cut) {                              // logits other than mul * S: written back as such
+                    const int hi = p0 + (r >> lgq), lo = a.plan.window ? hi - a.plan.window + 1 : 0;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         float v[32];
@@ -757,71 +752,65 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                     wait_st();
                     mul = 1.f;
                 }
-                // One walk over the logits: the weights by the present reference are kept in registers until the
-                // tile's maximum has shown that they are in range (S stays as it is until then).
+                // One walk over the logits, with the weights by the present reference.
                 const uint64_t mul2 = pair(mul, mul);
-                float mx = -INFINITY;
-                bool high;
-                {
+                uint64_t ref2, sum[2] = {0, 0};
+                auto refer = [&]() {
                     const float ref = m == -INFINITY ? 0.f : m - kLift;
-                    const uint64_t ref2 = pair(-ref, -ref);
-                    uint64_t sum[2] = {0, 0};
-                    uint32_t p[64];
-                    float v[16], u[16];
-                    ld16(ts, v);
-#pragma unroll
-                    for (int c = 0; c < 8; c += 2) {
-                        wait_ld(v);
-                        ld16(ts + 16 * c + 16, u);
-                        mx = max16(mx, v);
-                        weights16(p + 8 * c, v, mul2, ref2, sum);
-                        wait_ld(u);
-                        if (c < 6) ld16(ts + 16 * c + 32, v);
-                        mx = max16(mx, u);
-                        weights16(p + 8 * c + 8, u, mul2, ref2, sum);
-                    }
-                    mx *= mul;
-                    high = __any_sync(kFull, mx > m + kRaise);
-                    if (!high) {
-                        st32(ts, p);
-                        st32(ts + 32, p + 32);
-                        const float2 total = unpair(add2(sum[0], sum[1]));
-                        l += total.x + total.y;
-                    }
-                }
-                if (high) {
-                    // the reference is raised, what is summed so far scaled, the weights taken again
-                    const float top = fmaxf(m, mx);
+                    ref2 = pair(-ref, -ref);
+                };
+                // Columns 32 c .. exceed it: it is raised by a whole number (so that all scaling is exact), and what
+                // has been summed and written so far is scaled.
+                auto raise = [&](float mx, int c) {
+                    if (!__any_sync(kFull, mx > m + kRaise)) return;
+                    const float top = m == -INFINITY ? mx : m + fmaxf(0.f, ceilf(mx - m));
                     const float f = m == -INFINITY ? 0.f : exp2_ftz(m - top);
-                    if (i > 0) {
-                        l *= f;
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            float o[32];
-                            ld32(to + 32 * c, o);
-                            wait_ld(o);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] *= f;
-                            st32(to + 32 * c, o);
-                        }
-                    }
+                    const float2 sums = unpair(add2(sum[0], sum[1]));
+                    l = (l + sums.x + sums.y) * f;
+                    sum[0] = sum[1] = 0;
                     m = top;
-                    const float ref = m == -INFINITY ? 0.f : m - kLift;
-                    const uint64_t ref2 = pair(-ref, -ref);
-                    uint64_t sum[2] = {0, 0};
+                    refer();
+                    wait_st();
+                    const uint32_t f2 = pack_f16x2(f, f);
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        uint32_t p[16];
-                        ld32(ts + 32 * c, v);
-                        wait_ld(v);
-                        weights16(p, v, mul2, ref2, sum);
-                        weights16(p + 8, v + 16, mul2, ref2, sum);
-                        st16(ts + 16 * c, p);
+                    for (int k = 0; k < c; ++k) {
+                        float p[16];
+                        ld16(ts + 16 * k, p);
+                        wait_ld(p);
+                        uint32_t y[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) y[j] = hmul2(__float_as_uint(p[j]), f2);
+                        st16(ts + 16 * k, y);
                     }
-                    const float2 total = unpair(add2(sum[0], sum[1]));
-                    l += total.x + total.y;
+                    if (i == 0) return;                        // (no product yet)
+#pragma unroll 1
+                    for (int k = 0; k < D / 32; ++k) {
+                        float o[32];
+                        ld32(to + 32 * k, o);
+                        wait_ld(o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] *= f;
+                        st32(to + 32 * k, o);
+                    }
+                };
+                refer();
+                {
+                    float v[32], u[32];
+                    ld32(ts, v);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+                        wait_ld(v);
+                        ld32(ts + 32 * c + 32, u);
+                        raise(max32(v) * mul, c);
+                        weights32(ts + 16 * c, v, mul2, ref2, sum);
+                        wait_ld(u);
+                        if (c == 0) ld32(ts + 64, v);
+                        raise(max32(u) * mul, c + 1);
+                        weights32(ts + 16 * c + 16, u, mul2, ref2, sum);
+                    }
                 }
+                const float2 sums = unpair(add2(sum[0], sum[1]));
+                l += sums.x + sums.y;
                 wait_st();
             }
             fence_before();
@@ -858,20 +847,24 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
             }
         }
         if (!fine || *(volatile int*)&b.failed || (*(volatile unsigned*)&b.bad & reader.mark())) m = l = NAN;
+        const bool valid = r < n_rows;
         if ((*(volatile unsigned*)&b.odd & reader.mark()) && valid) {
             // a value that is not finite: the row is NaN if it sees one (looked for again, value by value)
             const Rows v{reinterpret_cast<const __half*>(a.buf + a.v_resid_off) +
                              ((long long)sp->seq * a.plan.Hkv + sp->head) * a.R * D,
                          a.v + sp->tok0 * a.v_stride[0] + sp->head * a.v_stride[1], a.v_stride[0], sp->n_resid, 0};
+            const int hi = p0 + (r >> lgq), lo = a.plan.window ? hi - a.plan.window + 1 : 0;
             const int last = min(hi, (sp->tile0 + sp->nt) * kTile - 1);
             for (int t = max(max(lo, sp->tile0 * kTile), sp->n_quant); t <= last && l == l; ++t)
+#pragma unroll 1
                 for (int j = 0; j < D / 8; ++j)
                     if (not_finite(ldg_row(v.at(t - sp->n_quant, D) + 8 * j))) m = l = NAN;
         }
         __syncwarp();
         const bool whole = sp->whole;
         float* part = a.ws + (((long long)blockIdx.x * 2 + sp->first) * kRows + r) * chunk_partial_stride(D);
-        __half* out = a.out + (long long)(sp->tok0 + tok) * a.out_stride[0] + head * a.out_stride[1];
+        __half* out = a.out + (long long)(sp->tok0 + sp->t0 + (r >> lgq)) * a.out_stride[0] +
+                      ((sp->head << lgq) + (r & ((1 << lgq) - 1))) * a.out_stride[1];
         const float inv = 1.f / l;
         if (any) {
 #pragma unroll 1
@@ -957,8 +950,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         softmax_rows<D, BITS, MOD>(a, b, bars, smem, xch, tmem, warp >> 2, warp, lane);
     } else if (warp < 16) {
         fewer_regs<kRegsFill>();
-        if (warp < 12) fill_tiles<D, BITS, false>(a, b, bars, smem, warp - 8, lane);
-        else fill_tiles<D, BITS, true>(a, b, bars, smem, warp - 12, lane);
+        fill_tiles<D, BITS>(a, b, bars, smem, warp >= 12, warp & 3, lane);
     } else {
         fewer_regs<kRegsRest>();
         if (warp == 16) {
