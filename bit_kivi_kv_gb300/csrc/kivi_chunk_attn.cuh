@@ -16,14 +16,17 @@
 // joined at the end.
 //
 // Roles (warps):
-//   0-3, 4-7   softmax of tile A / B, a row a lane: logits from tensor memory, running
-//              maximum, exponentials, probabilities back as fp16; epilogue
+//   0-3, 4-7   tile A / B: softmax, a row a lane (logits from tensor memory, running maximum,
+//              exponentials, probabilities back as fp16), then one lane issues the tile's
+//              next MMAs; epilogue
 //   8-11       keys: 32 tokens of a tile each, from codes to fp16 in shared memory; the
 //              next tile's bytes are loaded into registers while this one waits its turn
 //   12-15      values, the same, transposed ([channel][token])
-//   16         issues the MMAs (one thread)
-//   17         finds the spans of items that the CTA works on, ahead of the others (18, 19: idle,
+//   16         finds the spans of items that the CTA works on, ahead of the others (17-19: idle,
 //              they fill their warpgroup for the redistribution of registers)
+// A warp of its own for the MMAs was slower: its code, some 250 instructions a turn, is run
+// once in a thousand cycles and has left the instruction cache each time (a turn took 2000
+// cycles with nothing to wait for).  For the same reason the loops are kept small.
 //
 // Dequantization: a code pair masked in place and OR-ed with fp16 1024 is
 // 1024 + code * 2^pos, exact; one FMA makes it the code, a second one
@@ -53,10 +56,15 @@ namespace chunk_detail {
 using namespace mma_detail;
 
 constexpr int kChunkWarps = 20, kChunkThreads = 32 * kChunkWarps;
-// Registers a thread: the launch's, and what the five warpgroups (A, B, keys, values, the rest) make of them.
-constexpr int kRegs = 96, kRegsSoftmax = 120, kRegsFill = 88, kRegsRest = 64;
-static_assert(2 * kRegsSoftmax + 2 * kRegsFill + kRegsRest <= 5 * kRegs, "registers of the launch");
-constexpr int kSpanRing = 4, kSpanReaders = 17;
+// Registers a thread: the launch's, and what the five warpgroups (A, B, keys, values, the rest) make of them: none
+// of the roles spills (8 bits: a unit's words alone take 32, a few values of the filling warps do).
+constexpr int kRegs = 96;
+template <int BITS>
+struct Regs {
+    static constexpr int SOFTMAX = BITS == 8 ? 120 : 128, FILL = BITS == 8 ? 96 : 88, REST = 48;
+    static_assert(2 * SOFTMAX + 2 * FILL + REST <= 5 * kRegs, "registers of the launch");
+};
+constexpr int kSpanRing = 4, kSpanReaders = 16;
 constexpr float kRaise = 7.f;      // base-2 logits above the reference that a tile may have
 constexpr float kLift = 8.f;       // probabilities are held times 2^8
 constexpr float kLog2e = 1.4426950408889634f;
@@ -93,9 +101,8 @@ struct Span {
 
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], o_full[2], drained[2];      // of A, B
     uint64_t span_full[kSpanRing], span_empty[kSpanRing];
-    uint64_t drained;
     uint32_t tmem;
     int failed;         // a wait ran out: the outputs from here on are NaN
     unsigned bad, odd;  // spans with a block-table entry outside the pool, with a value that is not finite: bit number % 32
@@ -222,21 +229,19 @@ __device__ __forceinline__ float exp2_ftz(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ void tile_sync(int x) { asm volatile("bar.sync %0, 128;" ::"r"(3 + x) : "memory"); }
 template <int ID, int N>
 __device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
 
-// Wait for an mbarrier's phase, 2^32 cycles (about two seconds) at most; a wait that runs out marks the CTA,
+// Wait for an mbarrier's phase, 2^31 cycles (about a second) at most; a wait that runs out marks the CTA,
 // and no wait of a marked CTA waits, but a patient one (for spans: they keep coming).
 template <bool PATIENT = false>
 __device__ __forceinline__ bool wait_for(uint32_t bars, uint32_t bar, uint32_t parity) {
-    if (mbar_try(bar, parity)) return true;
-    const long long t0 = clock64();
+    const unsigned t0 = (unsigned)clock();
     while (!mbar_try(bar, parity)) {
-        if (!PATIENT && lds32(bars + BAR(failed))) return false;
-        if (clock64() - t0 >= 1LL << 32) {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(bars + BAR(failed)), "r"(1) : "memory");
-            return false;
-        }
+        if ((unsigned)clock() - t0 < 1u << 31 && (PATIENT || !lds32(bars + BAR(failed)))) continue;
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(bars + BAR(failed)), "r"(1) : "memory");
+        return false;
     }
     return true;
 }
@@ -572,71 +577,45 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
     }
 }
 
-// ---- MMA issue: one thread ----
-// A turn is x's product P V and its next S, over the P that the product reads: one thread's MMAs run in the order
-// of their issue.  Turns are short of time (two to a tile): every wait that is met costs some 60 cycles, a commit 130.
+// ---- MMAs of tile X, by one warp: it runs as one (descriptors stay in uniform registers), one lane issues ----
+// The product P V of tile number cv (of the CTA) and then S of tile number ck, over the P that the product
+// reads: one thread's MMAs run in the order of their issue.  A stage is free when both tiles have said so
+// (`times`: a tile that the other one has no use for is let go twice).
 template <int D, int BITS>
-__device__ void issue_mmas(const Bars& b, uint32_t bars, uint32_t smem, uint32_t tmem) {
+__device__ __forceinline__ void issue_mmas(uint32_t bars, uint32_t smem, uint32_t tmem, int x, int q_tile, bool product, bool add,
+                                           uint32_t cv, int times_v, bool next, uint32_t ck, int times_k) {
     using S = Shape<D, BITS>;
-    uint32_t tc = 0, qc = 0, pc = 0;                         // tiles; bit x: parity of the next wait for A or B
-    const uint32_t kind_s = mma_kind(kTile), kind_o = mma_kind(D);
     bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t parity) { ok = ok && wait_for(bars, bar, parity); };
-    const uint64_t q0 = operand(smem + S::OFF_Q), k0 = operand(smem + S::OFF_K), v0 = operand(smem + S::OFF_V);
-    SpanReader reader(b, bars);
-    while (const Span* sp = reader.next()) {
-        const int both = sp->both, na = sp->na, nb = sp->nb, nt = sp->nt;
-        reader.release();
-        for (int i = -1; i < max(na, nb); ++i) {
-#pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
-                const int n = x ? nb : na;
-                if (i < 0) {
-                    if (both || x == 0) {
-                        wait(bars + BAR(q_full) + 8 * x, (qc >> x) & 1);
-                        qc ^= 1u << x;
-                    }
-                } else if (i < n) {
-                    // (both: B has every tile; alternate: a tile that one lacks is nobody's)
-                    const uint32_t c = tc + (both ? i : 2 * i + x), stage = c & 1;
-                    if (!both || x == 0 || i >= na) wait(bars + BAR(v_full) + 8 * stage, (c >> 1) & 1);
-                    wait(bars + BAR(p_full) + 8 * x, (pc >> x) & 1);
-                    pc ^= 1u << x;
-                    if (ok) {                                // O_x += P_x V_t
-                        fence_after();
-                        const uint64_t va = v0 + stage * (S::K_BYTES >> 4);
-                        const uint32_t o = tmem + S::COL_O + x * D, pa = tmem + S::COL_S + x * kTile;
+    if (product) ok = wait_for(bars, bars + BAR(v_full) + 8 * (cv & 1), (cv >> 1) & 1);
+    if (next) ok = wait_for(bars, bars + BAR(k_full) + 8 * (ck & 1), (ck >> 1) & 1) && ok;
+    ok = __all_sync(kFull, ok);
+    fence_after();
+    if (!ok || !elect_one()) return;
+    const uint32_t s_at = tmem + S::COL_S + x * kTile;
+    if (product) {                                           // O_x += P_x V_t
+        const uint64_t va = operand(smem + S::OFF_V + (cv & 1) * S::K_BYTES);
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(o, pa + 8 * k, va + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), kind_o, k > 0 || i > 0);
-                        if (i + 1 == n) commit(bars + BAR(o_full) + 8 * x);
-                        if (!both || x == 1) commit(bars + BAR(v_empty) + 8 * stage);
-                    }
-                }
-                if (i + 1 < n) {
-                    const uint32_t c = tc + (both ? i + 1 : 2 * (i + 1) + x), stage = c & 1;
-                    if (!both || x == 0 || i + 1 >= na) wait(bars + BAR(k_full) + 8 * stage, (c >> 1) & 1);
-                    if (ok) {                                // S_x = Q_x K_t^T
-                        fence_after();
-                        const uint64_t qa = q0 + (both ? x : 0) * (S::Q_BYTES >> 4), ka = k0 + stage * (S::K_BYTES >> 4);
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
-                            mma_ss(tmem + S::COL_S + x * kTile, qa + off, ka + off, kind_s, k > 0);
-                        }
-                        commit(bars + BAR(s_full) + 8 * x);
-                        if (!both || x == 1) commit(bars + BAR(k_empty) + 8 * stage);
-                    }
-                }
-            }
-        }
-        tc += nt;
+        for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(tmem + S::COL_O + x * D, s_at + 8 * k, va + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), mma_kind(D), k > 0 || add);
     }
-    commit(bars + BAR(drained));   // no MMA is in flight when the CTA ends
-    wait_for<true>(bars, bars + BAR(drained), 0);
+    if (next) {                                              // S_x = Q_x K_t^T
+        const uint64_t qa = operand(smem + S::OFF_Q + q_tile * S::Q_BYTES);
+        const uint64_t ka = operand(smem + S::OFF_K + (ck & 1) * S::K_BYTES);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
+            mma_ss(s_at, qa + off, ka + off, mma_kind(kTile), k > 0);
+        }
+        commit(bars + BAR(s_full) + 8 * x);
+        for (int j = 0; j < times_k; ++j) commit(bars + BAR(k_empty) + 8 * (ck & 1));
+    } else {
+        commit(bars + BAR(o_full) + 8 * x);
+    }
+    if (product)
+        for (int j = 0; j < times_v; ++j) commit(bars + BAR(v_empty) + 8 * (cv & 1));
 }
 
-// ---- softmax of tile X (four warps, a row a lane) ----
+// ---- tile X: softmax (four warps, a row a lane), and the issue of its MMAs ----
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -657,26 +636,25 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// Weights 2^(mul v - ref) of 32 columns, as fp16 to `at`, their sums (mul and -ref twice each).
-__device__ __forceinline__ void weights32(uint32_t at, const float (&v)[32], uint64_t mul, uint64_t ref, uint64_t (&sum)[2]) {
-    uint32_t p[16];
+// Weights 2^(mul v - ref) of 16 columns as fp16 pairs, their sums (mul and -ref twice each).
+__device__ __forceinline__ void weights16(uint32_t* p, const float* v, uint64_t mul, uint64_t ref, uint64_t (&sum)[2]) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
+    for (int j = 0; j < 16; j += 2) {
         float2 y = unpair(fma2(pair(v[j], v[j + 1]), mul, ref));
         y.x = exp2_ftz(y.x);
         y.y = exp2_ftz(y.y);
         sum[(j / 2) & 1] = add2(sum[(j / 2) & 1], pair(y.x, y.y));
         p[j / 2] = pack_f16x2(y.x, y.y);
     }
-    st16(at, p);
 }
-__device__ __forceinline__ float max32(const float (&v)[32]) {
-    float m[4] = {v[0], v[1], v[2], v[3]};
+__device__ __forceinline__ float max16(float m, const float (&v)[16]) {
+    float n = fmaxf(v[0], v[1]);
 #pragma unroll
-    for (int j = 4; j < 28; j += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(m[k], v[j + k]), v[j + 4 + k]);
-    return fmaxf(fmaxf(fmaxf(m[0], v[28]), fmaxf(m[1], v[29])), fmaxf(fmaxf(m[2], v[30]), fmaxf(m[3], v[31])));
+    for (int j = 2; j < 16; j += 4) {
+        m = fmaxf(fmaxf(m, v[j]), v[j + 1]);
+        if (j + 2 < 16) n = fmaxf(fmaxf(n, v[j + 2]), v[j + 3]);
+    }
+    return fmaxf(m, n);
 }
 
 template <int D, int BITS, bool MOD>
@@ -686,14 +664,14 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = lanes + S::COL_S + x * kTile, to = lanes + S::COL_O + x * D;
     const int lgq = a.plan.nq >> 1;                            // log2 of 1, 2 or 4 query heads
-    uint32_t sc = 0, oc = 0;
+    uint32_t sc = 0, oc = 0, tc = 0;                           // S, last products and key tiles so far
     SpanReader reader(b, bars);
     while (const Span* sp = reader.next(lane)) {
         const bool both = sp->both;
         const int r = both ? x * kHalf + row : row;            // row of the item
         const int n_rows = (sp->t1 - sp->t0) << lgq;
         const int steps = sp->tiles(x), tile0 = sp->tile0;
-        // queries into the operand
+        // queries into the operand (the same rows: A loads them, for both)
         if (both || x == 0) {
             const __half* src = a.q + (long long)(sp->tok0 + sp->t0 + (r >> lgq)) * a.q_stride[0] +
                                 ((sp->head << lgq) + (r & ((1 << lgq) - 1))) * a.q_stride[1];
@@ -702,9 +680,13 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
             for (int c = 0; c < D / 8; ++c)
                 sts128(dst + operand_at<kHalf>(row, c), r < n_rows ? ldg_row(src + 8 * c) : uint4{0, 0, 0, 0});
             fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) arrive(bars + BAR(q_full) + 8 * x);
         }
+        if (both) tile_sync(x);
+        else named_sync<1, 256>();
+        // the tile of step i, by its number in the CTA; how often it is let go
+        auto tile = [&](int i) { return tc + (both ? i : 2 * i + x); };
+        auto times = [&](int i) { return both && i < sp->na ? 1 : 2; };
+        if ((warp & 3) == 0 && steps) issue_mmas<D, BITS>(bars, smem, tmem, x, both ? x : 0, false, false, 0, 0, true, tile(0), times(0));
         // A row's position is p0 + (r >> lgq): the last key that it sees.  Of the warp's rows the first one sees
         // least, the last one starts last.
         const int p0 = sp->n_quant + sp->n_resid + sp->t0, r0 = r - lane;
@@ -752,71 +734,74 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                     wait_st();
                     mul = 1.f;
                 }
-                // One walk over the logits, with the weights by the present reference.
+                // Half a tile at a time: the weights by the present reference are kept in registers until their
+                // maximum has shown that they are in range; a half that is not raises it and is taken again.
                 const uint64_t mul2 = pair(mul, mul);
-                uint64_t ref2, sum[2] = {0, 0};
-                auto refer = [&]() {
-                    const float ref = m == -INFINITY ? 0.f : m - kLift;
-                    ref2 = pair(-ref, -ref);
-                };
-                // Columns 32 c .. exceed it: it is raised by a whole number (so that all scaling is exact), and what
-                // has been summed and written so far is scaled.
-                auto raise = [&](float mx, int c) {
-                    if (!__any_sync(kFull, mx > m + kRaise)) return;
-                    const float top = m == -INFINITY ? mx : m + fmaxf(0.f, ceilf(mx - m));
-                    const float f = m == -INFINITY ? 0.f : exp2_ftz(m - top);
-                    const float2 sums = unpair(add2(sum[0], sum[1]));
-                    l = (l + sums.x + sums.y) * f;
-                    sum[0] = sum[1] = 0;
-                    m = top;
-                    refer();
-                    wait_st();
-                    const uint32_t f2 = pack_f16x2(f, f);
 #pragma unroll 1
-                    for (int k = 0; k < c; ++k) {
-                        float p[16];
-                        ld16(ts + 16 * k, p);
-                        wait_ld(p);
-                        uint32_t y[16];
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t from = ts + 64 * h;
+                    while (true) {
+                        const float ref = m == -INFINITY ? 0.f : m - kLift;
+                        const uint64_t ref2 = pair(-ref, -ref);
+                        uint64_t sum[2] = {0, 0};
+                        uint32_t p[32];
+                        float v[16], u[16], mx = -INFINITY;
+                        ld16(from, v);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) y[j] = hmul2(__float_as_uint(p[j]), f2);
-                        st16(ts + 16 * k, y);
-                    }
-                    if (i == 0) return;                        // (no product yet)
-#pragma unroll 1
-                    for (int k = 0; k < D / 32; ++k) {
-                        float o[32];
-                        ld32(to + 32 * k, o);
-                        wait_ld(o);
+                        for (int c = 0; c < 4; c += 2) {
+                            wait_ld(v);
+                            ld16(from + 16 * c + 16, u);
+                            mx = max16(mx, v);
+                            weights16(p + 8 * c, v, mul2, ref2, sum);
+                            wait_ld(u);
+                            if (c < 2) ld16(from + 32, v);
+                            mx = max16(mx, u);
+                            weights16(p + 8 * c + 8, u, mul2, ref2, sum);
+                        }
+                        mx *= mul;
+                        if (!__any_sync(kFull, mx > m + kRaise)) {
+                            st32(ts + 32 * h, p);
+                            const float2 total = unpair(add2(sum[0], sum[1]));
+                            l += total.x + total.y;
+                            break;
+                        }
+                        // raised by a whole number, so that scaling what is there (sums, the first half's weights) is exact
+                        const float top = m == -INFINITY ? mx : m + fmaxf(0.f, ceilf(mx - m));
+                        const float f = m == -INFINITY ? 0.f : exp2_ftz(m - top);
+                        m = top;
+                        l *= f;
+                        if (h) {
+                            wait_st();
+                            const uint32_t f2 = pack_f16x2(f, f);
+                            float y[32];
+                            ld32(ts, y);
+                            wait_ld(y);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] *= f;
-                        st32(to + 32 * k, o);
-                    }
-                };
-                refer();
-                {
-                    float v[32], u[32];
-                    ld32(ts, v);
+                            for (int j = 0; j < 32; ++j) p[j] = hmul2(__float_as_uint(y[j]), f2);
+                            st32(ts, p);
+                        }
+                        if (i > 0) {
 #pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        wait_ld(v);
-                        ld32(ts + 32 * c + 32, u);
-                        raise(max32(v) * mul, c);
-                        weights32(ts + 16 * c, v, mul2, ref2, sum);
-                        wait_ld(u);
-                        if (c == 0) ld32(ts + 64, v);
-                        raise(max32(u) * mul, c + 1);
-                        weights32(ts + 16 * c + 16, u, mul2, ref2, sum);
+                            for (int c = 0; c < D / 32; ++c) {
+                                float o[32];
+                                ld32(to + 32 * c, o);
+                                wait_ld(o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] *= f;
+                                st32(to + 32 * c, o);
+                            }
+                        }
                     }
                 }
-                const float2 sums = unpair(add2(sum[0], sum[1]));
-                l += sums.x + sums.y;
                 wait_st();
             }
             fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(bars + BAR(p_full) + 8 * (x));
+            tile_sync(x);
+            if ((warp & 3) == 0)
+                issue_mmas<D, BITS>(bars, smem, tmem, x, both ? x : 0, true, i > 0, tile(i), times(i), i + 1 < steps, tile(i + 1),
+                                    times(i + 1));
         }
+        tc += sp->nt;
         // ---- epilogue ----
         bool fine = true;
         if (steps) {
@@ -907,6 +892,11 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
             named_sync<2, 256>();
         }
     }
+    if ((warp & 3) == 0) {         // no MMA is in flight when the CTA ends (after a wait that ran out; else none is)
+        if (elect_one()) commit(bars + BAR(drained) + 8 * x);
+        __syncwarp();
+        wait_for<true>(bars, bars + BAR(drained) + 8 * x, 0);
+    }
 }
 
 template <int D, int BITS, bool MOD>
@@ -922,23 +912,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         for (int j = 0; j < 2; ++j) {
             mbar_init(&b.k_full[j], 4);
             mbar_init(&b.v_full[j], 4);
-            mbar_init(&b.k_empty[j], 1);
-            mbar_init(&b.v_empty[j], 1);
-            mbar_init(&b.q_full[j], 4);
+            mbar_init(&b.k_empty[j], 2);
+            mbar_init(&b.v_empty[j], 2);
             mbar_init(&b.s_full[j], 1);
-            mbar_init(&b.p_full[j], 4);
             mbar_init(&b.o_full[j], 1);
+            mbar_init(&b.drained[j], 1);
         }
         for (int j = 0; j < kSpanRing; ++j) {
             mbar_init(&b.span_full[j], 1);
             mbar_init(&b.span_empty[j], kSpanReaders);
         }
-        mbar_init(&b.drained, 1);
         b.failed = 0;
         b.bad = b.odd = 0;
         fence_mbar_init();
     }
-    if (warp == 16) tmem_alloc(&b.tmem);
+    if (warp == 0) tmem_alloc(&b.tmem);
     fence_before();
     __syncthreads();
     fence_after();
@@ -946,23 +934,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     griddepcontrol_launch_dependents();
     const uint32_t tmem = b.tmem;
     if (warp < 8) {
-        more_regs<kRegsSoftmax>();
+        more_regs<Regs<BITS>::SOFTMAX>();
         softmax_rows<D, BITS, MOD>(a, b, bars, smem, xch, tmem, warp >> 2, warp, lane);
     } else if (warp < 16) {
-        fewer_regs<kRegsFill>();
+        fewer_regs<Regs<BITS>::FILL>();
         fill_tiles<D, BITS>(a, b, bars, smem, warp >= 12, warp & 3, lane);
     } else {
-        fewer_regs<kRegsRest>();
-        if (warp == 16) {
-            if (elect_one()) issue_mmas<D, BITS>(b, bars, smem, tmem);
-            __syncwarp();
-        }
-        if (warp == 17) plan_spans(a, b, bars, lane);
+        fewer_regs<Regs<BITS>::REST>();
+        if (warp == 16) plan_spans(a, b, bars, lane);
     }
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == 16) tmem_free(tmem);
+    if (warp == 0) tmem_free(tmem);
 }
 
 template <int D, int BITS, bool MOD>
