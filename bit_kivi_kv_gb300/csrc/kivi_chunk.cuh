@@ -17,6 +17,7 @@ namespace kivi {
 // that start in weights [c W / n, (c + 1) W / n).  A CTA that holds all of an item's
 // tiles writes its outputs, others partial results, which a merge joins.
 constexpr int kRows = 256, kHalf = 128, kTile = 128;
+constexpr int kBothWeight = 4, kHalfWeight = 3;
 constexpr int kMaxChunkCtas = 192;       // most CTAs of a call (one per SM)
 
 struct ChunkSeq {
@@ -53,7 +54,7 @@ struct ChunkItem {
     int t0, t1;         // its tokens of the chunk
     int lo, hi;         // key tiles
     int both;           // more than kHalf rows
-    __host__ __device__ int weight() const { return both ? 2 : 1; }
+    __host__ __device__ int weight() const { return both ? kBothWeight : kHalfWeight; }
     __host__ __device__ long long total() const { return (long long)weight() * (hi - lo); }
 };
 __host__ __device__ inline ChunkItem chunk_item(const ChunkPlan& p, const ChunkSeq& s, int m) {
@@ -95,7 +96,7 @@ __host__ __device__ inline long long items_weight(const ChunkPlan& p, const Chun
     const int n = item_count(p, s.n);
     const long long c = (long long)s.n_quant + s.n_resid;
     const int whole = m < n ? m : n - 1;
-    long long w = 2 * whole_tiles(p, c, whole);
+    long long w = kBothWeight * whole_tiles(p, c, whole);
     if (m == n) w += chunk_item(p, s, n - 1).total();
     return w * p.Hkv;
 }

@@ -19,9 +19,9 @@
 //   0-3, 4-7   tile A / B: softmax, a row a lane (logits from tensor memory, running maximum,
 //              exponentials, probabilities back as fp16), then one lane issues the tile's
 //              next MMAs; epilogue
-//   8-11       keys: 32 tokens of a tile each, from codes to fp16 in shared memory; the
-//              next tile's bytes are loaded into registers while this one waits its turn
-//   12-15      values, the same, transposed ([channel][token])
+//   8-15       four the keys, 32 tokens of a tile each, from codes to fp16 in shared memory;
+//              the next tile's bytes are loaded into registers while this one waits its
+//              turn; four the values, the same, transposed ([channel][token])
 //   16         finds the spans of items that the CTA works on, ahead of the others (17-19: idle,
 //              they fill their warpgroup for the redistribution of registers)
 // A warp of its own for the MMAs was slower: its code, some 250 instructions a turn, is run
@@ -264,54 +264,54 @@ __device__ __forceinline__ void load_unit(const uint8_t* p, Words<W>& w) {
         }
     }
 }
-// Code tile t's words in registers of their own (the loops below move them; the loaded ones are not touched, so that
-// the next loads need not be waited for).
+// Words J .. J + BITS / 2 - 1 of tile t, from the front of what is left of them (the loops below are kept loops, their
+// bodies are small): x[t]; the loaded registers themselves are not touched, so that the next loads need not be waited for.
 template <int W>
-__device__ __forceinline__ void tile_words(const Words<W>& u, int t, uint32_t (&w)[W]) {
+__device__ __forceinline__ void tile_words(const Words<W>& u, uint32_t (&w)[2][W]) {
 #pragma unroll
-    for (int j = 0; j < W; j += 2) {
-        const uint4 &p = u.v[0][j / 4], &q = u.v[1][j / 4];
-        w[j] = j % 4 ? (t ? q.z : p.z) : (t ? q.x : p.x);
-        w[j + 1] = j % 4 ? (t ? q.w : p.w) : (t ? q.y : p.y);
-    }
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < W; j += 2) {
+            const uint4& v = u.v[t][j / 4];
+            w[t][j] = j % 4 ? v.z : v.x;
+            w[t][j + 1] = j % 4 ? v.w : v.y;
+        }
 }
-// The words of four channel groups (32 channels), from the front: loops over them are kept loops, their bodies are small.
 template <int BITS, int N>
-__device__ __forceinline__ void take_words(uint32_t (&w)[N], uint32_t (&x)[BITS / 2]) {
+__device__ __forceinline__ void next_words(uint32_t (&w)[2][N]) {
 #pragma unroll
-    for (int j = 0; j < BITS / 2; ++j) x[j] = w[j];
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int j = 0; j + BITS / 2 < N; ++j) w[j] = w[j + BITS / 2];
+        for (int j = 0; j + BITS / 2 < N; ++j) w[t][j] = w[t][j + BITS / 2];
 }
 // Keys: fp16(code * step + zero), rows row0 .. row0 + 31 of the operand at dst.  The channel group C's step and
-// zero pair of the lane is at ent + 16 C + 4 i (zeros 2 D bytes on).
+// zero pair of the lane is at ent + 16 C + 4 i (zeros 2 D bytes on); it holds for both code tiles.
 template <int D, int BITS, int W>
 __device__ __forceinline__ void key_unit(const Words<W>& u, uint32_t ent, uint32_t dst, int row0, int lane) {
     const int r7 = lane & 7;
     const uint32_t rows = dst + (row0 + (lane & 15)) * 128, e0 = ent + 4 * (lane & 3);
+    uint32_t x[2][W];
+    tile_words(u, x);
 #pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-        uint32_t w[W];
-        tile_words(u, t, w);
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {                     // channels 32 c ..
-            uint32_t x[BITS / 2];
-            take_words<BITS>(w, x);
-            const uint32_t at = rows + t * 2048 + (c >> 1) * (kTile * 128), e = e0 + 64 * c;
-            uint32_t s[4], z[4];
+    for (int c = 0; c < D / 32; ++c) {                         // channels 32 c ..
+        const uint32_t at = rows + (c >> 1) * (kTile * 128), e = e0 + 64 * c;
+        uint32_t s[4], z[4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                s[g] = lds32(e + 16 * g);
-                z[g] = lds32(e + 16 * g + 2 * D);
-            }
-            // matrices: (group, tokens 0-7), (group, 8-15), (next group, ...); this lane gives a row's address
-            const int chunk = 4 * (c & 1) + (lane >> 4);
-            stmatrix4(at + ((chunk ^ r7) << 4), hfma2(code_of<BITS, 0, 0>(x), s[0], z[0]), hfma2(code_of<BITS, 0, 1>(x), s[0], z[0]),
-                      hfma2(code_of<BITS, 1, 0>(x), s[1], z[1]), hfma2(code_of<BITS, 1, 1>(x), s[1], z[1]));
-            stmatrix4(at + (((chunk + 2) ^ r7) << 4), hfma2(code_of<BITS, 2, 0>(x), s[2], z[2]),
-                      hfma2(code_of<BITS, 2, 1>(x), s[2], z[2]), hfma2(code_of<BITS, 3, 0>(x), s[3], z[3]),
-                      hfma2(code_of<BITS, 3, 1>(x), s[3], z[3]));
+        for (int g = 0; g < 4; ++g) {
+            s[g] = lds32(e + 16 * g);
+            z[g] = lds32(e + 16 * g + 2 * D);
         }
+        // matrices: (group, tokens 0-7), (group, 8-15), (next group, ...); this lane gives a row's address
+        const int chunk = 4 * (c & 1) + (lane >> 4);
+        const uint32_t to0 = at + ((chunk ^ r7) << 4), to1 = at + (((chunk + 2) ^ r7) << 4);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            stmatrix4(to0 + t * 2048, hfma2(code_of<BITS, 0, 0>(x[t]), s[0], z[0]), hfma2(code_of<BITS, 0, 1>(x[t]), s[0], z[0]),
+                      hfma2(code_of<BITS, 1, 0>(x[t]), s[1], z[1]), hfma2(code_of<BITS, 1, 1>(x[t]), s[1], z[1]));
+            stmatrix4(to1 + t * 2048, hfma2(code_of<BITS, 2, 0>(x[t]), s[2], z[2]), hfma2(code_of<BITS, 2, 1>(x[t]), s[2], z[2]),
+                      hfma2(code_of<BITS, 3, 0>(x[t]), s[3], z[3]), hfma2(code_of<BITS, 3, 1>(x[t]), s[3], z[3]));
+        }
+        next_words<BITS>(x);
     }
 }
 // Values into columns (tokens) tok0 .. tok0 + 31 of the operand [D channels][tokens] at dst.  ent: per code tile the
@@ -320,24 +320,29 @@ template <int D, int BITS, int W>
 __device__ __forceinline__ void value_unit(const Words<W>& u, uint32_t ent, int lgG, uint32_t dst, int tok0, int lane) {
     const int r7 = lane & 7, ve = 64 * (D >> lgG);
     // (128 tokens a row in two blocks of 64; a unit lies in one)
-    const uint32_t rows = dst + (tok0 >> 6) * (D * 128) + (8 * (lane >> 4) + r7) * 128;
+    const uint32_t rows = dst + (tok0 >> 6) * (D * 128) + (8 * (lane >> 4) + r7) * 128, e0 = ent + 8 * (lane & 3);
     const int chunk0 = ((tok0 >> 3) & 7) + ((lane >> 3) & 1);
+    const uint32_t col[2] = {(uint32_t)((chunk0 ^ r7) << 4), (uint32_t)(((chunk0 + 2) ^ r7) << 4)};
+    uint32_t x[2][W];
+    tile_words(u, x);
 #pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-        uint32_t w[W];
-        tile_words(u, t, w);
-        const uint32_t e0 = ent + t * ve + 8 * (lane & 3), at = rows + (((chunk0 + 2 * t) ^ r7) << 4);
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-            uint32_t x[BITS / 2];
-            take_words<BITS>(w, x);
-            const uint32_t e = e0 + 32 * ((32 * c) >> lgG), to = at + c * 4096;
-            const uint2 s = lds64(e), z = lds64(e + ve / 2);
-            stmatrix4(to, hfma2(code_of<BITS, 0, 0>(x), s.x, z.x), hfma2(code_of<BITS, 0, 1>(x), s.y, z.y),
-                      hfma2(code_of<BITS, 1, 0>(x), s.x, z.x), hfma2(code_of<BITS, 1, 1>(x), s.y, z.y));
-            stmatrix4(to + 2048, hfma2(code_of<BITS, 2, 0>(x), s.x, z.x), hfma2(code_of<BITS, 2, 1>(x), s.y, z.y),
-                      hfma2(code_of<BITS, 3, 0>(x), s.x, z.x), hfma2(code_of<BITS, 3, 1>(x), s.y, z.y));
+    for (int c = 0; c < D / 32; ++c) {
+        const uint32_t e = e0 + 32 * ((32 * c) >> lgG), at = rows + c * 4096;
+        uint2 s[2], z[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t] = lds64(e + t * ve);
+            z[t] = lds64(e + t * ve + ve / 2);
         }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t to = at + col[t];
+            stmatrix4(to, hfma2(code_of<BITS, 0, 0>(x[t]), s[t].x, z[t].x), hfma2(code_of<BITS, 0, 1>(x[t]), s[t].y, z[t].y),
+                      hfma2(code_of<BITS, 1, 0>(x[t]), s[t].x, z[t].x), hfma2(code_of<BITS, 1, 1>(x[t]), s[t].y, z[t].y));
+            stmatrix4(to + 2048, hfma2(code_of<BITS, 2, 0>(x[t]), s[t].x, z[t].x), hfma2(code_of<BITS, 2, 1>(x[t]), s[t].y, z[t].y),
+                      hfma2(code_of<BITS, 3, 0>(x[t]), s[t].x, z[t].x), hfma2(code_of<BITS, 3, 1>(x[t]), s[t].y, z[t].y));
+        }
+        next_words<BITS>(x);
     }
 }
 
@@ -938,7 +943,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         softmax_rows<D, BITS, MOD>(a, b, bars, smem, xch, tmem, warp >> 2, warp, lane);
     } else if (warp < 16) {
         fewer_regs<Regs<BITS>::FILL>();
-        fill_tiles<D, BITS>(a, b, bars, smem, warp >= 12, warp & 3, lane);
+        // keys on two of the SM's four schedulers, values on the others: each has the code of one to hold
+        fill_tiles<D, BITS>(a, b, bars, smem, warp & 2, (warp & 1) + 2 * (warp >= 12), lane);
     } else {
         fewer_regs<Regs<BITS>::REST>();
         if (warp == 16) plan_spans(a, b, bars, lane);

@@ -642,8 +642,8 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
         a.weight += kivi::items_weight(a.plan, s, kivi::item_count(a.plan, s.n));
         tok0 += lens[i];
     }
-    // every CTA gets a tile: a range of two weights holds the start of one
-    const long long most = a.weight / 2 < 1 ? 1 : a.weight / 2;
+    // every CTA gets a tile: a range of the largest weight holds the start of one
+    const long long most = a.weight < kivi::kBothWeight ? 1 : a.weight / kivi::kBothWeight;
     const long long ctas = c->num_sms < kivi::kMaxChunkCtas ? c->num_sms : kivi::kMaxChunkCtas;
     a.n_ctas = (int)(most < ctas ? most : ctas);
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

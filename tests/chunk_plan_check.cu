@@ -53,7 +53,7 @@ int main() {
             w += sum * p.Hkv;
         }
         // (as the call sizes its grid)
-        const long long most = w / 2 < 1 ? 1 : w / 2;
+        const long long most = w < kBothWeight ? 1 : w / kBothWeight;
         const int ctas = (int)std::min(most, pick(0, 1) ? pick(1, 40) : 152LL);
         size_t at = 0;
         long long seen_parts = 0;
