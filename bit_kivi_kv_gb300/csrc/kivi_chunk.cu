@@ -1,4 +1,4 @@
-// Chunk attention: the merge of items that several CTAs worked on.
+// Chunk attention: the merge of items that several CTAs worked on; the rows of sequences with few of them.
 #include "kivi_chunk.cuh"
 #include "kivi_decode_mma.cuh"
 
@@ -87,6 +87,116 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_merge_kernel(const __gr
         *reinterpret_cast<uint32_t*>(out + 64 * d + 2 * lane) = pack_f16x2(o[d].x * inv, o[d].y * inv);
 }
 
+// Rows of the groups as the query heads of a single-token call; rows that a group lacks are zeros.
+template <int D>
+__global__ void __launch_bounds__(256) gather_rows_kernel(const __grid_constant__ GroupArgs a) {
+    griddepcontrol_wait();
+    griddepcontrol_launch_dependents();
+    const long long x = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int c = (int)(x % (D / 8)), j = (int)(x / (D / 8) % a.nv), h = (int)(x / (D / 8) / a.nv % a.Hkv);
+    const long long g = x / (D / 8) / a.nv / a.Hkv;
+    if (g >= a.n) return;
+    uint4 v{0, 0, 0, 0};
+    const ChunkGroup& p = a.groups[g];
+    if (j < p.rows) {
+        const int r = p.row0 + j;
+        const __half* src = a.q + (long long)(p.tok0 + r / a.nq) * a.q_stride[0] + (h * a.nq + r % a.nq) * a.q_stride[1];
+        v = *reinterpret_cast<const uint4*>(src + 8 * c);
+    }
+    reinterpret_cast<uint4*>(a.gathered)[x] = v;
+}
+
+// A warp per row: the partial results over the cached tokens, and the row's new tokens up to its own.
+template <int D>
+__global__ void __launch_bounds__(128) group_merge_kernel(const __grid_constant__ GroupArgs a) {
+    constexpr int S = partial_stride(D), C = D / 32;           // channels a lane holds
+    griddepcontrol_wait();
+    griddepcontrol_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const long long at = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int j = (int)(at % a.nv), h = (int)(at / a.nv % a.Hkv);
+    const long long g = at / a.nv / a.Hkv;
+    if (g >= a.n) return;
+    const ChunkGroup& p = a.groups[g];
+    if (j >= p.rows) return;
+    const PagedSeq& sq = a.seqs[g];
+    const long long P = sq.P, PR = (sq.n_resid + 31) / 32;
+    const long long w0 = sq.start + h * (a.wm.S0 + slot_weight(a.wm, P, 0, PR));
+    const long long last = w0 + unit_start_p(a.wm, P, 0, P + PR - 1);
+    const int n = (int)(map_owner(a.wm, last) - map_owner(a.wm, w0 + a.wm.S0) + 1);
+    const float* base = a.ws + at * kPartialSlots * S;
+    const int r = p.row0 + j, tok = r / a.nq, head = h * a.nq + r % a.nq;
+    auto widen = [&](const __half* src, float (&x)[C]) {
+        if constexpr (C == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(src + 4 * lane);
+            const float2 lo = unpack_f16x2(v.x), hi = unpack_f16x2(v.y);
+            x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+        } else {
+            const float2 v = unpack_f16x2(*reinterpret_cast<const uint32_t*>(src + 2 * lane));
+            x[0] = v.x; x[1] = v.y;
+        }
+    };
+    float q[C];
+    widen(a.q + (long long)(p.tok0 + tok) * a.q_stride[0] + head * a.q_stride[1], q);
+#pragma unroll
+    for (int c = 0; c < C; ++c) q[c] *= a.scale_log2;
+    // weights of the partials, three a lane
+    float w[3], top = -INFINITY, l = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int i = lane + 32 * k;
+        w[k] = -INFINITY;
+        if (i < n) {
+            w[k] = base[i * S];
+            bad |= base[i * S + 2] != 0.f;
+        }
+        top = fmaxf(top, w[k]);
+    }
+    top = warp_max(top);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int i = lane + 32 * k;
+        w[k] = w[k] == -INFINITY ? 0.f : exp2f(w[k] - top);
+        if (w[k] != 0.f) l += w[k] * base[i * S + 1];
+    }
+    l = warp_sum(l);
+    float o[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float f = __shfl_sync(kFull, i < 32 ? w[0] : i < 64 ? w[1] : w[2], i & 31);
+        const float* src = base + i * S + 4 + C * lane;
+        if (f == 0.f) continue;                                // (an empty partial's values are not written)
+#pragma unroll
+        for (int c = 0; c < C; c += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(src + c);
+            o[c] = fmaf(f, x.x, o[c]);
+            o[c + 1] = fmaf(f, x.y, o[c + 1]);
+        }
+    }
+    const __half* kp = a.k + p.tok0 * a.k_stride[0] + h * a.k_stride[1];
+    const __half* vp = a.v + p.tok0 * a.v_stride[0] + h * a.v_stride[1];
+    for (int t = 0; t <= tok; ++t) {
+        float x[C], v[C], s = 0.f;
+        widen(kp + t * a.k_stride[0], x);
+        widen(vp + t * a.v_stride[0], v);
+#pragma unroll
+        for (int c = 0; c < C; ++c) s = fmaf(q[c], x[c], s);
+        s = warp_sum(s);
+        const float m = fmaxf(top, s), f = exp2f(top - m), e = exp2f(s - m);
+        top = m;
+        l = l * f + e;
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[c] = o[c] * f + e * v[c];
+    }
+    const float inv = __any_sync(kFull, bad) ? NAN : 1.f / l;
+    __half* out = a.out + (long long)(p.tok0 + tok) * a.out_stride[0] + head * a.out_stride[1] + C * lane;
+#pragma unroll
+    for (int c = 0; c < C; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack_f16x2(o[c] * inv, o[c + 1] * inv);
+}
+
 }  // namespace
 
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int D, cudaStream_t st) {
@@ -96,6 +206,19 @@ cudaError_t launch_chunk_merge(const ChunkArgs& a, int D, cudaStream_t st) {
     const dim3 grid((unsigned)(a.n_ctas - 1), (unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
     return D == 128 ? launch_dependent(chunk_merge_kernel<128>, grid, 32 * kJoinWarps, st, a)
                     : launch_dependent(chunk_merge_kernel<64>, grid, 32 * kJoinWarps, st, a);
+}
+
+cudaError_t launch_gather_rows(const GroupArgs& a, int D, cudaStream_t st) {
+    const long long n = (long long)a.n * a.Hkv * a.nv * (D / 8);
+    const dim3 grid((unsigned)((n + 255) / 256));
+    return D == 128 ? launch_dependent(gather_rows_kernel<128>, grid, 256, st, a)
+                    : launch_dependent(gather_rows_kernel<64>, grid, 256, st, a);
+}
+
+cudaError_t launch_group_merge(const GroupArgs& a, int D, cudaStream_t st) {
+    const dim3 grid((unsigned)(((long long)a.n * a.Hkv * a.nv + 3) / 4));
+    return D == 128 ? launch_dependent(group_merge_kernel<128>, grid, 128, st, a)
+                    : launch_dependent(group_merge_kernel<64>, grid, 128, st, a);
 }
 
 }  // namespace kivi

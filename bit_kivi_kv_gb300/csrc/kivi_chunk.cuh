@@ -192,6 +192,29 @@ cudaError_t launch_chunk_attn_d64(const ChunkArgs& a, int bits, cudaStream_t st)
 cudaError_t launch_chunk_attn_d128(const ChunkArgs& a, int bits, cudaStream_t st);
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int D, cudaStream_t st);
 
+// Sequences with few rows (new tokens x query heads per kv head) that see all
+// cached tokens: up to kGroupRows rows of a kv head are taken as the query heads
+// of a single-token call, whose decode kernel reads the cache for them; the merge adds
+// the new tokens.  A sequence of more rows makes several groups, each reads the cache again.
+constexpr int kGroupRows = 4, kFewRows = 16;
+struct ChunkGroup {
+    int tok0;           // the sequence's first new token in the packed inputs
+    int row0, rows;     // its rows of each kv head
+};
+struct GroupArgs {
+    const __half *q, *k, *v;
+    __half *out, *gathered;                                           // gathered: [groups][Hkv][nv][D]
+    long long q_stride[2], k_stride[2], v_stride[2], out_stride[2];
+    const float* ws;    // partial results of the decode kernel
+    float scale_log2;
+    int Hkv, nq, nv, n; // query heads per kv head, rows per group, groups
+    WorkMap wm;
+    PagedSeq seqs[kMaxCallSeqs];
+    ChunkGroup groups[kMaxCallSeqs];
+};
+cudaError_t launch_gather_rows(const GroupArgs& a, int D, cudaStream_t st);
+cudaError_t launch_group_merge(const GroupArgs& a, int D, cudaStream_t st);
+
 // ---- append of a chunk, branches, reading back (kivi_pages.cu) ----
 
 // A new block of a chunk: rows [row0, row0 + G) of the sequence's virtual rows

@@ -269,6 +269,13 @@ cudaError_t launch_decode_paged(const PagedGeometry& pg, const uint8_t* buf, con
                                 const __half* new_k, const __half* new_v, int early_ok, int num_sms, int max_ctas,
                                 cudaStream_t st, int* launches);
 
+// The decode kernel of such a call without its merge: the partial results of
+// sequence i's head h are at workspace + (i * Hq + h) * kPartialSlots *
+// partial_stride(D); their number follows from *wm and seqs[i] (start filled in).
+cudaError_t launch_decode_paged_parts(const PagedGeometry& pg, const uint8_t* buf, PagedSeq* seqs, int n,
+                                      const __half* q, float scale_log2, float* workspace, int num_sms, int max_ctas,
+                                      cudaStream_t st, WorkMap* wm);
+
 // Host-side helpers of the C ABI (kivi_api.cu): set the calling thread's
 // error string and return st; the decode workspace bytes a handle needs.
 kivi_status report_error(kivi_status st, const char* msg);

@@ -372,12 +372,12 @@ cudaError_t launch_finish(K kernel, const A& f, long long ctas, cudaStream_t st)
 
 }  // namespace
 
-cudaError_t launch_decode_paged(const PagedGeometry& pg, const uint8_t* buf, const PagedSeq* seqs, int n,
-                                const __half* q, __half* out, float scale_log2, float* workspace,
-                                const __half* new_k, const __half* new_v, int early_ok, int num_sms, int max_ctas,
-                                cudaStream_t st, int* launches) {
+namespace {
+// The decode kernel of a paged call alone: m.wm and m.seqs say where its partial results are.
+cudaError_t paged_parts(const PagedGeometry& pg, const uint8_t* buf, const PagedSeq* seqs, int n, const __half* q,
+                        float scale_log2, float* workspace, const __half* new_k, const __half* new_v, int early_ok,
+                        int num_sms, int max_ctas, cudaStream_t st, mma_detail::PagedArgs& m) {
     const Geometry& g = pg.g;
-    *launches = 0;
     if (n < 1 || n > kMaxCallSeqs) return cudaErrorInvalidValue;
     const int nq = g.Hq / g.Hkv;
     WorkMap wm{};
@@ -391,7 +391,6 @@ cudaError_t launch_decode_paged(const PagedGeometry& pg, const uint8_t* buf, con
         if (ws_min < 0 || w < ws_min) ws_min = w;
     }
     wm.S0 = segment_lead(wm.wq, ws_min, wt0, num_sms);
-    mma_detail::PagedArgs m;   // ~12 KB of kernel parameters
     long long start = 0, ws_max = 0;
     for (int i = 0; i < n; ++i) {
         PagedSeq s = seqs[i];
@@ -411,7 +410,29 @@ cudaError_t launch_decode_paged(const PagedGeometry& pg, const uint8_t* buf, con
     m.max_blocks = (int)g.NB;
     m.n_pages = (int)pg.n_pages;
     m.n_seqs = n;
-    cudaError_t e = (g.D == 128 ? launch_decode_mma_d128p : launch_decode_mma_d64p)(m, g.bits, nq, g.G, num_sms, st);
+    return (g.D == 128 ? launch_decode_mma_d128p : launch_decode_mma_d64p)(m, g.bits, nq, g.G, num_sms, st);
+}
+}  // namespace
+
+cudaError_t launch_decode_paged_parts(const PagedGeometry& pg, const uint8_t* buf, PagedSeq* seqs, int n,
+                                      const __half* q, float scale_log2, float* workspace, int num_sms, int max_ctas,
+                                      cudaStream_t st, WorkMap* wm) {
+    mma_detail::PagedArgs m;
+    const cudaError_t e = paged_parts(pg, buf, seqs, n, q, scale_log2, workspace, nullptr, nullptr, 1, num_sms, max_ctas, st, m);
+    if (e != cudaSuccess) return e;
+    for (int i = 0; i < n; ++i) seqs[i] = m.seqs[i];
+    *wm = m.wm;
+    return cudaSuccess;
+}
+
+cudaError_t launch_decode_paged(const PagedGeometry& pg, const uint8_t* buf, const PagedSeq* seqs, int n,
+                                const __half* q, __half* out, float scale_log2, float* workspace,
+                                const __half* new_k, const __half* new_v, int early_ok, int num_sms, int max_ctas,
+                                cudaStream_t st, int* launches) {
+    const Geometry& g = pg.g;
+    *launches = 0;
+    mma_detail::PagedArgs m;   // ~12 KB of kernel parameters
+    cudaError_t e = paged_parts(pg, buf, seqs, n, q, scale_log2, workspace, new_k, new_v, early_ok, num_sms, max_ctas, st, m);
     if (e != cudaSuccess) return e;
     *launches = 1;
     mma_detail::PagedFinishArgs f;
@@ -419,7 +440,7 @@ cudaError_t launch_decode_paged(const PagedGeometry& pg, const uint8_t* buf, con
     f.out = out;
     f.Hq = g.Hq;
     f.Hkv = g.Hkv;
-    f.nq = nq;
+    f.nq = g.Hq / g.Hkv;
     f.wm = m.wm;   // with the grid size the launch chose
     f.heads = (long long)n * g.Hq;
     f.n_seqs = n;

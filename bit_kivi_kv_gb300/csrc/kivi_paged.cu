@@ -242,8 +242,25 @@ long long fresh_blocks(const kivi::Geometry& g, const SeqState& sq, int n) {
     return quant > have ? quant - have : 0;
 }
 
-size_t chunk_ws_need(const kivi::Geometry& g) {
+// Workspace of a chunk attention call: the wide kernel's partial results, then the gathered rows and the partial
+// results of the groups that the sequences with few rows make (kMaxCallSeqs at most).
+size_t wide_ws_need(const kivi::Geometry& g) {
     return (size_t)kivi::kMaxChunkCtas * 2 * kivi::kRows * kivi::chunk_partial_stride(g.D) * sizeof(float);
+}
+int groups_of(const kivi::Geometry& g, int len) {
+    const long long rows = (long long)len * (g.Hq / g.Hkv);
+    return rows < 1 || rows > kivi::kFewRows ? 0 : (int)((rows + kivi::kGroupRows - 1) / kivi::kGroupRows);
+}
+size_t group_rows_bytes(const kivi::Geometry& g, int groups) {
+    return (size_t)groups * g.Hkv * kivi::kGroupRows * g.D * sizeof(__half);
+}
+size_t chunk_ws_need(const kivi::Geometry& g, const int* lens, int n) {
+    int groups = 0;
+    for (int i = 0; i < n; ++i)
+        if (groups + groups_of(g, lens[i]) <= kivi::kMaxCallSeqs) groups += groups_of(g, lens[i]);
+    kivi::Geometry v = g;
+    v.Hq = g.Hkv * kivi::kGroupRows;
+    return wide_ws_need(g) + group_rows_bytes(g, groups) + paged_ws_need(v, groups);
 }
 
 // The rows of a call that only reads the cache: n distinct live sequences,
@@ -572,11 +589,15 @@ kivi_status kivi_paged_decode_blocks(kivi_paged_t c, const int* seqs, int n, con
     return kivi::decode_blocks_call(r, q, blocks, n_list, out, softmax_scale, stream);
 }
 
-size_t kivi_paged_chunk_workspace_bytes(const kivi_paged_config* cfg) {
+size_t kivi_paged_chunk_workspace_bytes(const kivi_paged_config* cfg, const int* lens, int n) {
     kivi::PagedGeometry pg;
     const char* why;
     if (derive_paged(cfg, &pg, &why) != KIVI_OK) { failf(KIVI_ERR_INVALID_ARG, "%s", why); return 0; }
-    return chunk_ws_need(pg.g);
+    if (!lens || n < 1 || n > kivi::kMaxCallSeqs) {
+        failf(KIVI_ERR_INVALID_ARG, "null lengths, or n outside [1, %d]", kivi::kMaxCallSeqs);
+        return 0;
+    }
+    return chunk_ws_need(pg.g, lens, n);
 }
 
 kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* lens, int n, const kivi_chunk* x,
@@ -597,63 +618,116 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
     if ((st = check_rows("out", x->out, x->out_stride)) != KIVI_OK) return st;
     if (!workspace || !aligned(workspace, 256)) return failf(KIVI_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     const kivi::Geometry& g = c->pg.g;
-    if (ws_bytes < chunk_ws_need(g))
-        return failf(KIVI_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, chunk_ws_need(g));
+    const size_t need = chunk_ws_need(g, lens, n);
+    if (ws_bytes < need) return failf(KIVI_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+    for (int i = 0; i < n; ++i)
+        if (c->seqs[(size_t)seqs[i]].n_quant + c->seqs[(size_t)seqs[i]].n_resid + lens[i] > (1LL << 30))
+            return failf(KIVI_ERR_UNSUPPORTED, "sequence %d: more than 2^30 tokens", seqs[i]);
     const kivi_status sdev = paged_device(c);
     if (sdev != KIVI_OK) return sdev;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const float scale = x->softmax_scale > 0.f ? x->softmax_scale : 1.0f / sqrtf((float)g.D);
+    const float scale_log2 = scale * 1.4426950408889634f;
+    const bool plain = x->cap == 0.f && !x->slopes;
+    // sequences with few rows, that see all their tokens, go in groups to the decode kernel; the others to the wide one
+    kivi::GroupArgs few;
     kivi::ChunkArgs a;
-    a.buf = c->buf;
-    a.table = reinterpret_cast<const int*>(c->buf + c->pg.table_off);
-    a.q = static_cast<const __half*>(x->q);
-    a.k = static_cast<const __half*>(x->k);
-    a.v = static_cast<const __half*>(x->v);
-    a.out = static_cast<__half*>(x->out);
-    for (int j = 0; j < 2; ++j) {
-        a.q_stride[j] = x->q_stride[j];
-        a.k_stride[j] = x->k_stride[j];
-        a.v_stride[j] = x->v_stride[j];
-        a.out_stride[j] = x->out_stride[j];
-    }
-    a.page_bytes = c->pg.page_bytes;
-    a.part_bytes = g.part_bytes;
-    a.k_resid_off = g.k_resid_off;
-    a.v_resid_off = g.v_resid_off;
-    a.R = g.R;
-    a.lgG = g.G == 32 ? 5 : g.G == 64 ? 6 : 7;
-    a.Hq = g.Hq;
-    a.max_blocks = (int)g.NB;
-    a.n_pages = (int)c->pg.n_pages;
-    a.scale = x->softmax_scale > 0.f ? x->softmax_scale : 1.0f / sqrtf((float)g.D);
-    a.scale_log2 = a.scale * 1.4426950408889634f;
-    a.cap = x->cap;
-    a.slopes = x->slopes;
-    a.plan = kivi::ChunkPlan{g.Hq / g.Hkv, g.Hkv, x->window};
-    a.ws = static_cast<float*>(workspace);
-    a.n_seqs = 0;
+    few.n = a.n_seqs = 0;
     a.weight = 0;
-    int tok0 = 0;
+    a.plan = kivi::ChunkPlan{g.Hq / g.Hkv, g.Hkv, x->window};
+    int tok0 = 0, most_rows = 0;
+    bool as_they_lie = true;             // every group is one token's heads, where the decode kernel would look for them
     for (int i = 0; i < n; ++i) {
         if (!lens[i]) continue;
         const SeqState& sq = c->seqs[(size_t)seqs[i]];
-        if (sq.n_quant + sq.n_resid + lens[i] > (1LL << 30))
-            return failf(KIVI_ERR_UNSUPPORTED, "sequence %d: more than 2^30 tokens", seqs[i]);
-        kivi::ChunkSeq& s = a.seqs[a.n_seqs++];
-        s = kivi::ChunkSeq{a.weight, seqs[i], lens[i], tok0, (int)sq.n_quant, sq.n_resid, 0};
-        a.weight += kivi::items_weight(a.plan, s, kivi::item_count(a.plan, s.n));
+        const long long cached = sq.n_quant + sq.n_resid;
+        const int groups = groups_of(g, lens[i]);
+        if (groups && plain && cached > 0 && (x->window == 0 || x->window >= cached + lens[i]) &&
+            few.n + groups <= kivi::kMaxCallSeqs) {
+            const int rows = lens[i] * a.plan.nq;
+            as_they_lie = as_they_lie && lens[i] == 1 && tok0 == few.n;
+            for (int r = 0; r < rows; r += kivi::kGroupRows) {
+                const int left = rows - r < kivi::kGroupRows ? rows - r : kivi::kGroupRows;
+                if (left > most_rows) most_rows = left;
+                few.seqs[few.n] = kivi::PagedSeq{0, seqs[i], (int)(sq.n_quant / 32), sq.n_resid, -1};
+                few.groups[few.n++] = kivi::ChunkGroup{tok0, r, left};
+            }
+        } else {
+            kivi::ChunkSeq& s = a.seqs[a.n_seqs++];
+            s = kivi::ChunkSeq{a.weight, seqs[i], lens[i], tok0, (int)sq.n_quant, sq.n_resid, 0};
+            a.weight += kivi::items_weight(a.plan, s, kivi::item_count(a.plan, s.n));
+        }
         tok0 += lens[i];
     }
-    // every CTA gets a tile: a range of the largest weight holds the start of one
-    const long long most = a.weight < kivi::kBothWeight ? 1 : a.weight / kivi::kBothWeight;
-    const long long ctas = c->num_sms < kivi::kMaxChunkCtas ? c->num_sms : kivi::kMaxChunkCtas;
-    a.n_ctas = (int)(most < ctas ? most : ctas);
-    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = g.D == 128 ? kivi::launch_chunk_attn_d128(a, g.bits, cs) : kivi::launch_chunk_attn_d64(a, g.bits, cs);
-    if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
-    kivi::count_launches(1);
-    if (a.n_ctas > 1) {
-        e = kivi::launch_chunk_merge(a, g.D, cs);
-        if (e != cudaSuccess) return cuda_fail(e, "chunk merge launch");
+    auto inputs = [&](auto& p) {
+        p.q = static_cast<const __half*>(x->q);
+        p.k = static_cast<const __half*>(x->k);
+        p.v = static_cast<const __half*>(x->v);
+        p.out = static_cast<__half*>(x->out);
+        for (int j = 0; j < 2; ++j) {
+            p.q_stride[j] = x->q_stride[j];
+            p.k_stride[j] = x->k_stride[j];
+            p.v_stride[j] = x->v_stride[j];
+            p.out_stride[j] = x->out_stride[j];
+        }
+    };
+    cudaError_t e = cudaSuccess;
+    if (few.n) {
+        inputs(few);
+        few.Hkv = g.Hkv;
+        few.nq = a.plan.nq;
+        few.nv = most_rows > 2 ? 4 : most_rows;
+        few.scale_log2 = scale_log2;
+        uint8_t* at = static_cast<uint8_t*>(workspace) + wide_ws_need(g);
+        few.gathered = reinterpret_cast<__half*>(at);
+        float* parts = reinterpret_cast<float*>(at + group_rows_bytes(g, few.n));
+        few.ws = parts;
+        const __half* rows = few.q;
+        if (!as_they_lie || few.nv != few.nq || x->q_stride[1] != g.D || x->q_stride[0] != (long long)g.Hq * g.D) {
+            e = kivi::launch_gather_rows(few, g.D, cs);
+            if (e != cudaSuccess) return cuda_fail(e, "chunk gather launch");
+            kivi::count_launches(1);
+            rows = few.gathered;
+        }
+        kivi::PagedGeometry vg = c->pg;          // the groups' rows are its query heads
+        vg.g.Hq = g.Hkv * few.nv;
+        e = kivi::launch_decode_paged_parts(vg, c->buf, few.seqs, few.n, rows, scale_log2, parts, c->num_sms, c->max_ctas, cs,
+                                            &few.wm);
+        if (e != cudaSuccess) return cuda_fail(e, "chunk decode launch");
+        e = kivi::launch_group_merge(few, g.D, cs);
+        if (e != cudaSuccess) return cuda_fail(e, "chunk group merge launch");
+        kivi::count_launches(2);
+    }
+    if (a.n_seqs) {
+        inputs(a);
+        a.buf = c->buf;
+        a.table = reinterpret_cast<const int*>(c->buf + c->pg.table_off);
+        a.page_bytes = c->pg.page_bytes;
+        a.part_bytes = g.part_bytes;
+        a.k_resid_off = g.k_resid_off;
+        a.v_resid_off = g.v_resid_off;
+        a.R = g.R;
+        a.lgG = g.G == 32 ? 5 : g.G == 64 ? 6 : 7;
+        a.Hq = g.Hq;
+        a.max_blocks = (int)g.NB;
+        a.n_pages = (int)c->pg.n_pages;
+        a.scale = scale;
+        a.scale_log2 = scale_log2;
+        a.cap = x->cap;
+        a.slopes = x->slopes;
+        a.ws = static_cast<float*>(workspace);
+        // every CTA gets a tile: a range of the largest weight holds the start of one
+        const long long most = a.weight < kivi::kBothWeight ? 1 : a.weight / kivi::kBothWeight;
+        const long long ctas = c->num_sms < kivi::kMaxChunkCtas ? c->num_sms : kivi::kMaxChunkCtas;
+        a.n_ctas = (int)(most < ctas ? most : ctas);
+        e = g.D == 128 ? kivi::launch_chunk_attn_d128(a, g.bits, cs) : kivi::launch_chunk_attn_d64(a, g.bits, cs);
+        if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
         kivi::count_launches(1);
+        if (a.n_ctas > 1) {
+            e = kivi::launch_chunk_merge(a, g.D, cs);
+            if (e != cudaSuccess) return cuda_fail(e, "chunk merge launch");
+            kivi::count_launches(1);
+        }
     }
     return ok();
 }

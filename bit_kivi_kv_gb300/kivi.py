@@ -128,7 +128,7 @@ def _load():
         "kivi_paged_block_scores": (I, [P, IP, I, P, F, P, LL, P]),
         "kivi_paged_decode_blocks": (I, [P, IP, I, P, P, I, P, F, P]),
         "kivi_paged_append": (I, [P, IP, I, P, P, P]),
-        "kivi_paged_chunk_workspace_bytes": (SZ, [pcfgp]),
+        "kivi_paged_chunk_workspace_bytes": (SZ, [pcfgp, IP, I]),
         "kivi_paged_chunk_attn": (I, [P, IP, IP, I, P, P, SZ, P]),   # a kivi_chunk by reference, or its packed bytes
         "kivi_paged_append_chunk": (I, [P, IP, IP, I, P, P, P, P, P]),   # strides: addresses, or packed bytes
         "kivi_paged_fork": (I, [P, IP, I, IP, P]),
@@ -341,8 +341,8 @@ def kivi_paged_append(h: int, seqs, k: int, v: int, stream: int):
 
 
 # ---- chunks of new tokens ---------------------------------------------------------
-def kivi_paged_chunk_workspace_bytes(cfg: kivi_paged_config) -> int:
-    return lib.kivi_paged_chunk_workspace_bytes(ctypes.byref(cfg))
+def kivi_paged_chunk_workspace_bytes(cfg: kivi_paged_config, lens) -> int:
+    return lib.kivi_paged_chunk_workspace_bytes(ctypes.byref(cfg), _seq_array(lens), len(lens))
 
 
 def kivi_paged_chunk_attn(h: int, seqs, lens, args: kivi_chunk, workspace: int, ws_bytes: int, stream: int):
@@ -710,7 +710,6 @@ class KiviPagedCache:
                                      device)
         self.handle = kivi_paged_create(self.cfg, self.buffer.data_ptr(), nbytes)
         self._heads = (n_q_heads, n_kv_heads, head_dim)
-        self._chunk_ws = kivi_paged_chunk_workspace_bytes(self.cfg)
         self._device = self.buffer.get_device()
 
     def _alloc(self, nbytes, device):
@@ -836,10 +835,11 @@ class KiviPagedCache:
         if slopes is not None:
             _expect(slopes, "slopes", _torch.float32, (hq,), device)
         # scratch of this call alone, from its stream's memory: calls on other streams and in graphs share nothing
-        ws = _new((self._chunk_ws,), _torch.uint8, q.device, stream)
+        ws_bytes = lib.kivi_paged_chunk_workspace_bytes(ctypes.byref(self.cfg), n_arr, len(seqs))
+        ws = _new((ws_bytes,), _torch.uint8, q.device, stream)
         args = _CHUNK.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *qs, *ks, *vs, *os_, softmax_scale, cap,
                            window, slopes.data_ptr() if slopes is not None else 0)
-        _check(lib.kivi_paged_chunk_attn(self.handle, _seq_array(seqs), n_arr, len(seqs), args, ws.data_ptr(), self._chunk_ws,
+        _check(lib.kivi_paged_chunk_attn(self.handle, _seq_array(seqs), n_arr, len(seqs), args, ws.data_ptr(), ws_bytes,
                                          _current_stream(device) if stream is None else stream.cuda_stream))
         return out
 

@@ -552,9 +552,9 @@ typedef struct {
     const float* slopes;      /* device, [n_q_heads], or null: no distance bias */
 } kivi_chunk;
 
-/* Bytes of workspace of a kivi_paged_chunk_attn call on any device; 0 if cfg is
- * invalid.  Host-only. */
-size_t kivi_paged_chunk_workspace_bytes(const kivi_paged_config* cfg);
+/* Bytes of workspace of a kivi_paged_chunk_attn call over n sequences with lens[i]
+ * new tokens (host array), on any device; 0 if cfg or n is invalid.  Host-only. */
+size_t kivi_paged_chunk_workspace_bytes(const kivi_paged_config* cfg, const int* lens, int n);
 
 /*
  * Attention of a chunk.  With L tokens cached in a sequence, its new token i has
@@ -566,16 +566,18 @@ size_t kivi_paged_chunk_workspace_bytes(const kivi_paged_config* cfg);
  *     x_t += slope_h (t - (L + i))
  *     out = sum_t softmax_t(x) v_t
  *
- * The cache is not changed (the new tokens are not appended).  Dequantized keys
- * and values are rounded to fp16, and so are the attention weights (times a
- * power of two that keeps them in range); sums are fp32.  A dequantized value
- * beyond fp16's range is infinite here.  A new or residual token whose value
+ * The cache is not changed (the new tokens are not appended).  Sequences with
+ * few rows (new tokens x query heads per kv head, 16 at most) that see all their
+ * tokens are read by the kernel of the single-token calls, with its accuracy.
+ * For the others dequantized keys and values are rounded to fp16, and so are the
+ * attention weights (times a power of two that keeps them in range); sums are
+ * fp32.  A dequantized value beyond fp16's range is infinite there.  A new or residual token whose value
  * row holds a number that is not finite makes the outputs that see it NaN, and no
  * other.  A block-table entry outside the pool, or a copy that does not complete
  * (see "Failure detection"), makes the outputs that depend on it NaN.
  *
  * workspace: 256-byte aligned device scratch of
- * ws_bytes >= kivi_paged_chunk_workspace_bytes(cfg); garbage afterwards.  Calls
+ * ws_bytes >= kivi_paged_chunk_workspace_bytes(cfg, lens, n); garbage afterwards.  Calls
  * that may run at once need one each.  At most 2^30 tokens in a sequence, cached
  * and new.
  */

@@ -160,7 +160,7 @@ class ChunkRun:
         bands = Banded()
         out = bands.like(q)
         out.fill_(float("nan"))
-        ws = bands.bytes(K.kivi_paged_chunk_workspace_bytes(self.cache.cfg), "cuda")
+        ws = bands.bytes(K.kivi_paged_chunk_workspace_bytes(self.cache.cfg, lens), "cuda")
         a = K.kivi_chunk()
         for name, t in (("q", qs), ("k", ks), ("v", vs), ("out", out)):
             setattr(a, name, t.data_ptr())

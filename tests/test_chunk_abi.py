@@ -41,13 +41,18 @@ def chunk(K, **kw):
 
 def test_workspace_size(K):
     cfg = K.make_paged_config(6, 8, 4, 64, 2, 32, 64, 16, 32)
-    assert K.kivi_paged_chunk_workspace_bytes(cfg) == 192 * 2 * 256 * 66 * 4
-    assert K.kivi_paged_chunk_workspace_bytes(K.make_paged_config(6, 8, 4, 96, 2, 32, 64, 16, 32)) == 0
+    wide, group = 192 * 2 * 256 * 66 * 4, 4 * 4 * 64 * 2 + 4 * 4 * 65 * 68 * 4
+    # (2 query heads per kv head: 16 rows are 8 tokens, 4 rows a group)
+    for lens, groups in (([9], 0), ([1], 1), ([2], 1), ([3, 8], 6), ([0, 100, 5], 3), ([8] * 200, 512)):
+        assert K.kivi_paged_chunk_workspace_bytes(cfg, lens) == wide + groups * group
+    assert K.kivi_paged_chunk_workspace_bytes(cfg, []) == 0 and K.kivi_paged_chunk_workspace_bytes(cfg, [1] * 513) == 0
+    assert K.kivi_paged_chunk_workspace_bytes(K.make_paged_config(6, 8, 4, 96, 2, 32, 64, 16, 32), [1]) == 0
 
 
 def test_attention_refusals(K, h):
     a, b = (K.kivi_paged_add(h, 0, 0, 0, 0) for _ in range(2))
-    ws, n = 1 << 20, 192 * 2 * 256 * 66 * 4
+    cfg = K.make_paged_config(6, 8, 4, 64, 2, 32, 64, 16, 32)
+    ws, n = 1 << 20, K.kivi_paged_chunk_workspace_bytes(cfg, [1])
     call = lambda seqs, lens, x, w=ws, m=n: K.kivi_paged_chunk_attn(h, seqs, lens, x, w, m, 0)  # noqa: E731
     bad = K.KIVI_ERR_INVALID_ARG
     assert status(K, call, [], [], chunk(K)) == bad

@@ -36,6 +36,24 @@ def test_lengths(past, n):
     run.attend([run.add(past)], [n])
 
 
+@pytest.mark.parametrize("nq,lens", [(1, [1, 2, 3, 4, 5, 16, 17]), (2, [1, 2, 3, 8, 9, 0, 4]), (4, [1, 2, 4, 5, 1, 3, 1])])
+@pytest.mark.parametrize("D,bits", [(128, 2), (64, 8), (128, 4)])
+def test_few_rows(nq, lens, D, bits):
+    """Sequences of 16 rows at most go to the single-token decode kernel in groups, others beside them do not."""
+    run = ChunkRun(2 * nq, 2, D, bits, 64, 128, max_seqs=7, n_pages=400, seed=nq + D)
+    seqs = [run.add(L) for L in (1, 130, 700, 64, 3000, 400, 0)]
+    data = run.chunk(lens)
+    a = run.attend(seqs, lens, data)
+    run.attend(seqs, lens, data, fit=in_wider)
+    assert torch.equal(a, run.attend(seqs, lens, data, window=5000))      # (cuts nothing)
+    run.attend(seqs, lens, data, window=300)
+    run.attend(seqs, lens, data, cap=20.0, scale=0.2)
+    ones = [1] * 7
+    data = run.chunk(ones)
+    run.attend(seqs[:6], ones[:6], tuple(x[:6].contiguous() for x in data))      # single tokens: read where they lie
+    run.attend(seqs[:6], ones[:6], tuple(x[:6].contiguous() for x in data), fit=head_strided)
+
+
 @pytest.mark.parametrize("window", [1, 2, 31, 128, 129, 300, 5000])
 @pytest.mark.parametrize("nq", [1, 4])
 def test_windows(window, nq):
@@ -197,6 +215,15 @@ def test_values_that_are_not_finite_reach_only_those_that_see_them():
             out = run.attend([s], [300], (q, bad, v) if x is k else (q, k, bad), check=False)
             assert torch.equal(out[:t], clean[:t]), (t, value)
             assert torch.isnan(out[t:]).any(-1).all() or x is k
+    for n in (3, 8):                                            # few rows: the other kernels
+        few = [x[:n].contiguous() for x in (q, k, v)]
+        clean_few = run.attend([s], [n], tuple(few))
+        for x in (1, 2):
+            bad = [y.clone() for y in few]
+            bad[x][n - 2, 0, 7] = float("inf")
+            out = run.attend([s], [n], tuple(bad), check=False)
+            assert torch.equal(out[:n - 2], clean_few[:n - 2])
+            assert x == 1 or not torch.isfinite(out[n - 2:]).all(-1).any()
     bad = q.clone()
     bad[9, 1] = float("nan")
     out = run.attend([s], [300], (bad, k, v), check=False)
@@ -268,8 +295,7 @@ def test_serving_run():
     both = [torch.cat([x, x]) for x in (q, k, v)]
     out = c.chunk_attn(draft, [5, 5], *both)
     torch.cuda.synchronize()
-    run.check_out(draft, [5, 5], *both, out)
-    assert torch.equal(out[:5], out[5:])
+    run.check_out(draft, [5, 5], *both, out)                    # (split over the CTAs as they come: not the same bits)
     c.append_chunk([s], [3], k[:3], v[:3])                      # three of the five are accepted
     oracle_chunk(run.live[s], k[:3].transpose(0, 1).cpu().numpy(), v[:3].transpose(0, 1).cpu().numpy())
     for d in draft:
