@@ -21,43 +21,26 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// Block (c, y): where CTA c + 1's first span continues the item that CTA c began, 8 of that item's rows, a
-// warp each: o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over its parts, p in order.
+// Row r of an item that CTAs c - 1 .. worked on, by a warp: o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over its
+// parts, p in order.
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) chunk_merge_kernel(const __grid_constant__ ChunkArgs a) {
+__device__ __forceinline__ void merge_row(const ChunkArgs& a, const MergeJob& job, int c, int r, int lane) {
     constexpr int S = chunk_partial_stride(D);
-    griddepcontrol_wait();
-    griddepcontrol_launch_dependents();
-    const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
-    ChunkWalk walk;
-    walk.start(&a.plan, a.seqs, a.n_seqs, chunk_begin(a.weight, a.n_ctas, c), chunk_begin(a.weight, a.n_ctas, c + 1LL));
-    if (!walk.next()) return;
-    const ChunkSpan s = walk.s;
-    const ChunkSeq& q = a.seqs[s.seq];
-    if (s.first == 0 || chunk_begin(a.weight, a.n_ctas, c - 1LL) > walk.item0) return;
-    const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), nq = a.plan.nq;
-    if (r >= (s.it.t1 - s.it.t0) * nq) return;
-    // the parts: CTA c - 1's last span, then the first ones of CTAs c .. c + n - 2
-    const long long last = walk.item0 + (long long)(s.it.hi - s.it.lo - 1) * s.it.weight();
-    int n = 2;
-    while (c - 1 + n < a.n_ctas && chunk_begin(a.weight, a.n_ctas, c - 1LL + n) <= last) ++n;
-    auto part = [&](int p) {
-        return a.ws + (((long long)(c - 1 + p) * 2 + (p == 0)) * kRows + r) * S;
-    };
+    const int n = job.parts, nq = a.plan.nq;
+    auto part = [&](int p) { return a.ws + (((long long)(c - 1 + p) * 2 + (p == 0)) * kRows + r) * S; };
     float w[kPartRegs], top = -INFINITY, l = 0.f;
 #pragma unroll
     for (int j = 0; j < kPartRegs; ++j) {
         const int p = 32 * j + lane;
         w[j] = -INFINITY;
         if (32 * j < n && p < n) w[j] = part(p)[D];
-        top = w[j] != w[j] ? w[j] : fmaxf(top, w[j]);
+        top = fmaxf(top, w[j]);
     }
-    const bool bad = __any_sync(kFull, top != top);
     top = warp_max(top);
 #pragma unroll
     for (int j = 0; j < kPartRegs; ++j) {
         const int p = 32 * j + lane;
-        w[j] = w[j] == -INFINITY ? 0.f : exp2f(w[j] - top);
+        w[j] = w[j] == -INFINITY ? 0.f : exp2f(w[j] - top);    // (a part that is marked: NaN, and so is the row)
         if (32 * j < n && p < n) l += w[j] * part(p)[D + 1];
     }
     l = warp_sum(l);
@@ -79,12 +62,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_merge_kernel(const __gr
             }
         }
     }
-    const float inv = bad ? NAN : 1.f / l;
-    const int tok = s.it.t0 + r / nq, head = s.head * nq + r % nq;
-    __half* out = a.out + (long long)(q.tok0 + tok) * a.out_stride[0] + head * a.out_stride[1];
+    const float inv = 1.f / l;
+    __half* out = a.out + (long long)(job.tok + r / nq) * a.out_stride[0] + (job.head * nq + r % nq) * a.out_stride[1];
 #pragma unroll
     for (int d = 0; d < D / 64; ++d)
         *reinterpret_cast<uint32_t*>(out + 64 * d + 2 * lane) = pack_f16x2(o[d].x * inv, o[d].y * inv);
+}
+
+// Block (x, y): the item that CTA x + 1's first span continues, if CTA x began it; every gridDim.y-th eight of its
+// rows.  (The main kernel leaves the jobs: found anew in each block, by division and search, they took 33 us of a call
+// of 75.)
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) chunk_merge_kernel(const __grid_constant__ ChunkArgs a) {
+    griddepcontrol_wait();
+    griddepcontrol_launch_dependents();
+    const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const MergeJob job = a.jobs[c];
+    if (!job.parts) return;
+    for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < job.rows; r += gridDim.y * kJoinWarps)
+        merge_row<D>(a, job, c, r, lane);
 }
 
 // Rows of the groups as the query heads of a single-token call; rows that a group lacks are zeros.
@@ -178,18 +174,27 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const __grid_constant_
     }
     const __half* kp = a.k + p.tok0 * a.k_stride[0] + h * a.k_stride[1];
     const __half* vp = a.v + p.tok0 * a.v_stride[0] + h * a.v_stride[1];
-    for (int t = 0; t <= tok; ++t) {
-        float x[C], v[C], s = 0.f;
-        widen(kp + t * a.k_stride[0], x);
-        widen(vp + t * a.v_stride[0], v);
+    for (int t0 = 0; t0 <= tok; t0 += 4) {                     // four new tokens' loads at a time
+        float x[4][C], v[4][C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) s = fmaf(q[c], x[c], s);
-        s = warp_sum(s);
-        const float m = fmaxf(top, s), f = exp2f(top - m), e = exp2f(s - m);
-        top = m;
-        l = l * f + e;
+        for (int u = 0; u < 4; ++u) {
+            const long long t = min(t0 + u, tok);
+            widen(kp + t * a.k_stride[0], x[u]);
+            widen(vp + t * a.v_stride[0], v[u]);
+        }
 #pragma unroll
-        for (int c = 0; c < C; ++c) o[c] = o[c] * f + e * v[c];
+        for (int u = 0; u < 4; ++u) {
+            if (t0 + u > tok) break;
+            float s = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) s = fmaf(q[c], x[u][c], s);
+            s = warp_sum(s);
+            const float m = fmaxf(top, s), f = exp2f(top - m), e = exp2f(s - m);
+            top = m;
+            l = l * f + e;
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[c] = o[c] * f + e * v[u][c];
+        }
     }
     const float inv = __any_sync(kFull, bad) ? NAN : 1.f / l;
     __half* out = a.out + (long long)(p.tok0 + tok) * a.out_stride[0] + head * a.out_stride[1] + C * lane;
@@ -203,7 +208,9 @@ cudaError_t launch_chunk_merge(const ChunkArgs& a, int D, cudaStream_t st) {
     int most = 0;
     for (int i = 0; i < a.n_seqs; ++i) most = a.seqs[i].n > most ? a.seqs[i].n : most;
     const long long rows = (long long)most * a.plan.nq < kRows ? (long long)most * a.plan.nq : kRows;
-    const dim3 grid((unsigned)(a.n_ctas - 1), (unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
+    // (blocks for one wave: eight of 256 threads an SM)
+    const long long blocks = (rows + kJoinWarps - 1) / kJoinWarps;
+    const dim3 grid((unsigned)(a.n_ctas - 1), (unsigned)(blocks < 8 ? blocks : 8));
     return D == 128 ? launch_dependent(chunk_merge_kernel<128>, grid, 32 * kJoinWarps, st, a)
                     : launch_dependent(chunk_merge_kernel<64>, grid, 32 * kJoinWarps, st, a);
 }

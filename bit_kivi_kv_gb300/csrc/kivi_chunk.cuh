@@ -182,11 +182,31 @@ struct ChunkArgs {
     ChunkPlan plan;
     long long weight;   // of the whole call
     float* ws;          // partial results: [n_ctas][2][kRows][D + 2]
+    struct MergeJob* jobs;   // [n_ctas]: what each CTA's first span leaves to be joined
     ChunkSeq seqs[kMaxCallSeqs];
+};
+// An item whose first tiles CTA c - 1 did and whose others CTAs c .. c + parts - 2 did, written by CTA c
+// (parts 0: its first span continues no item, or CTA c - 1 did not begin it).
+struct MergeJob {
+    int parts, rows;    // rows of the item
+    int tok, head;      // its first new token in the packed tensors, kv head
 };
 // The weights [x0, x1) of CTA c.
 __host__ __device__ inline long long chunk_begin(long long weight, int n_ctas, long long c) { return c * weight / n_ctas; }
 constexpr int chunk_partial_stride(int D) { return D + 2; }      // o[D], m, l of a row
+
+// (the first span that the walk gives; called after next())
+__host__ __device__ inline MergeJob merge_job(const ChunkWalk& w, long long weight, int n_ctas, int c) {
+    MergeJob j{0, 0, 0, 0};
+    if (w.s.first == 0 || chunk_begin(weight, n_ctas, c - 1LL) > w.item0) return j;
+    const long long last = w.item0 + (long long)(w.s.it.hi - w.s.it.lo - 1) * w.s.it.weight();
+    j.parts = 2;
+    while (c - 1 + j.parts < n_ctas && chunk_begin(weight, n_ctas, c - 1LL + j.parts) <= last) ++j.parts;
+    j.rows = (w.s.it.t1 - w.s.it.t0) * w.p->nq;
+    j.tok = w.seqs[w.s.seq].tok0 + w.s.it.t0;
+    j.head = w.s.head;
+    return j;
+}
 
 cudaError_t launch_chunk_attn_d64(const ChunkArgs& a, int bits, cudaStream_t st);
 cudaError_t launch_chunk_attn_d128(const ChunkArgs& a, int bits, cudaStream_t st);

@@ -32,7 +32,8 @@
 // 1024 + code * 2^pos, exact; one FMA makes it the code, a second one
 // fp16(code * step + zero), rounded once.  The cache's tiles are fragments of
 // 8x8 matrices, so stmatrix puts them where the MMA's swizzle wants them.
-// Rows that are still fp16 (residual and chunk) go the same way unchanged.
+// Rows that are still fp16 (residual and chunk) are copied; values of tiles
+// that hold nothing else stay token by token (the MMA takes both orders).
 //
 // Roundings: keys and values to fp16 (half a step of 2^-11), probabilities to
 // fp16, scaled so that the largest is between 2^8 and 2^15: what falls below
@@ -105,6 +106,7 @@ struct Bars {
     uint64_t span_full[kSpanRing], span_empty[kSpanRing];
     uint32_t tmem;
     int failed;         // a wait ran out: the outputs from here on are NaN
+    int busy;           // a tile's MMAs are being issued
     unsigned bad, odd;  // spans with a block-table entry outside the pool, with a value that is not finite: bit number % 32
     alignas(16) Span spans[kSpanRing];
 };
@@ -192,9 +194,14 @@ __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.
 __device__ __forceinline__ uint64_t operand(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
-// fp16 x fp16 -> fp32, M = 128, N columns, both operands K-major
-__host__ __device__ constexpr uint32_t mma_kind(int n) {
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+// The same memory as an operand of [64-column blocks][rows][128 bytes] whose rows are the contracted index: rows in
+// groups of eight 1024 bytes apart, blocks of 64 columns kTile * 128 bytes.
+__device__ __forceinline__ uint64_t operand_rows(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(kTile * 128 / 16) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// fp16 x fp16 -> fp32, M = 128, N columns, the contracted index contiguous in both operands (or, rows: not in B)
+__host__ __device__ constexpr uint32_t mma_kind(int n, bool rows = false) {
+    return (1u << 4) | ((uint32_t)rows << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
     asm volatile(
@@ -358,12 +365,10 @@ __device__ __forceinline__ int ldg_int(const int* p) {
     return v;
 }
 
-__device__ __forceinline__ bool pair_not_finite(uint32_t v) {
-    const uint32_t a = v & 0x7fff7fffu;
-    return (a & 0xffffu) >= 0x7c00u || a >= 0x7c000000u;
-}
+// (an exponent of ones carries into the sign's place)
+__device__ __forceinline__ uint32_t odd_bits(uint32_t v) { return (v & 0x7c007c00u) + 0x04000400u; }
 __device__ __forceinline__ bool not_finite(const uint4& v) {
-    return pair_not_finite(v.x) || pair_not_finite(v.y) || pair_not_finite(v.z) || pair_not_finite(v.w);
+    return ((odd_bits(v.x) | odd_bits(v.y) | odd_bits(v.z) | odd_bits(v.w)) & 0x80008000u) != 0u;
 }
 
 // 16 bytes global -> shared, asynchronous; zeros instead where there are none
@@ -380,17 +385,48 @@ struct Rows {
         return f < n_resid ? resid + (long long)f * D : chunk + (long long)(f - n_resid) * step;
     }
 };
-// 32 fp16 rows [f0, f0 + 32) (zeros behind the last) as keys.
+// 32 fp16 rows [f0, f0 + 32) (zeros behind the last) as they lie, token by token: keys, and values of a tile that
+// holds nothing but rows.
 template <int D>
-__device__ __forceinline__ void key_rows(const Rows& k, int f0, uint32_t dst, int row0, int lane) {
+__device__ __forceinline__ void plain_rows(const Rows& k, int f0, uint32_t dst, int row0, int lane) {
     constexpr int LPR = D / 8, RPI = 32 / LPR;                 // lanes a row, rows an instruction
     const int lr = lane % LPR, sub = lane / LPR;
+    const uint32_t to = dst + (uint32_t)((lr >> 3) * (kTile * 128) + (row0 + sub) * 128);
+    if (f0 >= k.n_resid && f0 + 32 <= k.n) {                   // all of them new tokens: evenly spaced
+        const __half* src = k.chunk + (f0 + sub - k.n_resid) * k.step + 8 * lr;
+        const long long step = RPI * k.step;
 #pragma unroll 4
-    for (int h = 0; h < 32; h += RPI) {
-        const int f = f0 + h + sub;
-        cp_async16_or_zero(dst + operand_at<kTile>(row0 + h + sub, lr), k.at(f < k.n ? f : 0, D) + 8 * lr, f < k.n);
+        for (int h = 0; h < 32; h += RPI, src += step)
+            cp_async16_or_zero(to + h * 128 + (((lr & 7) ^ ((sub + h) & 7)) << 4), src, true);
+    } else {
+#pragma unroll 1
+        for (int h = 0; h < 32; h += RPI) {
+            const int f = f0 + h + sub;
+            cp_async16_or_zero(to + h * 128 + (((lr & 7) ^ ((sub + h) & 7)) << 4), k.at(f < k.n ? f : 0, D) + 8 * lr, f < k.n);
+        }
     }
     cp_async_wait_all();
+}
+// Of rows that plain_rows has brought: those that are not finite become zeros; whether there was one.
+template <int D>
+__device__ __forceinline__ bool clear_odd_rows(uint32_t dst, int row0, int lane) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR;
+    const int lr = lane % LPR, sub = lane / LPR;
+    const uint32_t at = dst + (uint32_t)((lr >> 3) * (kTile * 128) + (row0 + sub) * 128);
+    uint32_t odd = 0;
+#pragma unroll 4
+    for (int h = 0; h < 32; h += RPI) {
+        const uint4 v = lds128(at + h * 128 + (((lr & 7) ^ ((sub + h) & 7)) << 4));
+        odd |= odd_bits(v.x) | odd_bits(v.y) | odd_bits(v.z) | odd_bits(v.w);
+    }
+    if (!__any_sync(kFull, (odd & 0x80008000u) != 0u)) return false;
+#pragma unroll 1
+    for (int h = 0; h < 32; h += RPI) {
+        const uint32_t x = at + h * 128 + (((lr & 7) ^ ((sub + h) & 7)) << 4);
+        const unsigned who = __ballot_sync(kFull, not_finite(lds128(x)));
+        if (who >> (LPR * sub) & (LPR == 16 ? 0xffffu : 0xffu)) sts128(x, uint4{0, 0, 0, 0});
+    }
+    return true;
 }
 // The same rows as values, transposed.  A lane loads 8 channels of a token; as matrices of
 // (8 tokens) x (channel pairs of four lanes) they are stored transposed, each row of a matrix to its channel.
@@ -444,6 +480,7 @@ inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, uint32_t bars, in
         bool more = true;
         while (more) {
             more = walk.next();
+            if (n == 0) a.jobs[blockIdx.x] = merge_job(walk, a.weight, a.n_ctas, blockIdx.x);   // (every CTA has a span)
             const uint32_t slot = n % kSpanRing;
             wait_for<true>(bars, bars + BAR(span_empty) + 8 * (slot), ((n / kSpanRing) & 1) ^ 1);
             Span o;
@@ -572,8 +609,14 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
             const Rows r{reinterpret_cast<const __half*>(a.buf + resid) + ((long long)sp->seq * a.plan.Hkv + sp->head) * a.R * D,
                          (values ? a.v : a.k) + sp->tok0 * step + sp->head * per_head, step, sp->n_resid, sp->n_resid + sp->t1};
             const int f0 = t * kTile + 32 * w - n_quant;
-            if (!values) key_rows<D>(r, f0, dst, 32 * w, lane);
-            else if (value_rows<D>(r, f0, dst, 32 * w, lane) && lane == 0) atomicOr(&b.odd, reader.mark());
+            bool odd = false;
+            if (!values || t * kTile >= n_quant) {
+                plain_rows<D>(r, f0, dst, 32 * w, lane);
+                if (values) odd = clear_odd_rows<D>(dst, 32 * w, lane);
+            } else {
+                odd = value_rows<D>(r, f0, dst, 32 * w, lane);
+            }
+            if (odd && lane == 0) atomicOr(&b.odd, reader.mark());
         }
         fence_proxy_async();
         __syncwarp();
@@ -582,13 +625,29 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
     }
 }
 
+// The tensor core takes MMAs in the order of their issue and makes the thread that issues wait.  A tile's run of
+// them is kept together: mixed with the other tile's, both would be done when the second one is (in step, A and B took
+// 5000 cycles a tile).
+__device__ __forceinline__ void take_turn(uint32_t bars) {
+    const uint32_t at = bars + BAR(busy);
+    const unsigned t0 = (unsigned)clock();
+    while (true) {
+        uint32_t old;
+        asm volatile("atom.shared.cas.b32 %0, [%1], 0, 1;" : "=r"(old) : "r"(at) : "memory");
+        if (!old || (unsigned)clock() - t0 >= 1u << 31) return;   // (a lost turn costs time only)
+    }
+}
+__device__ __forceinline__ void pass_turn(uint32_t bars) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(bars + BAR(busy)), "r"(0) : "memory");
+}
+
 // ---- MMAs of tile X, by one warp: it runs as one (descriptors stay in uniform registers), one lane issues ----
 // The product P V of tile number cv (of the CTA) and then S of tile number ck, over the P that the product
 // reads: one thread's MMAs run in the order of their issue.  A stage is free when both tiles have said so
 // (`times`: a tile that the other one has no use for is let go twice).
 template <int D, int BITS>
 __device__ __forceinline__ void issue_mmas(uint32_t bars, uint32_t smem, uint32_t tmem, int x, int q_tile, bool product, bool add,
-                                           uint32_t cv, int times_v, bool next, uint32_t ck, int times_k) {
+                                           bool rows, uint32_t cv, int times_v, bool next, uint32_t ck, int times_k) {
     using S = Shape<D, BITS>;
     bool ok = true;
     if (product) ok = wait_for(bars, bars + BAR(v_full) + 8 * (cv & 1), (cv >> 1) & 1);
@@ -597,11 +656,22 @@ __device__ __forceinline__ void issue_mmas(uint32_t bars, uint32_t smem, uint32_
     fence_after();
     if (!ok || !elect_one()) return;
     const uint32_t s_at = tmem + S::COL_S + x * kTile;
+    take_turn(bars);
     if (product) {                                           // O_x += P_x V_t
-        const uint64_t va = operand(smem + S::OFF_V + (cv & 1) * S::K_BYTES);
+        const uint32_t v_at = smem + S::OFF_V + (cv & 1) * S::K_BYTES;
+        if (rows) {                                          // values token by token
+            const uint64_t va = operand_rows(v_at);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tmem + S::COL_O + x * D, s_at + 8 * k, va + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), mma_kind(D), k > 0 || add);
+            for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(tmem + S::COL_O + x * D, s_at + 8 * k, va + k * (16 * 128 / 16), mma_kind(D, true), k > 0 || add);
+        } else {
+            const uint64_t va = operand(v_at);
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(tmem + S::COL_O + x * D, s_at + 8 * k, va + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), mma_kind(D),
+                       k > 0 || add);
+        }
+        for (int j = 0; j < times_v; ++j) commit(bars + BAR(v_empty) + 8 * (cv & 1));
     }
     if (next) {                                              // S_x = Q_x K_t^T
         const uint64_t qa = operand(smem + S::OFF_Q + q_tile * S::Q_BYTES);
@@ -612,12 +682,12 @@ __device__ __forceinline__ void issue_mmas(uint32_t bars, uint32_t smem, uint32_
             mma_ss(s_at, qa + off, ka + off, mma_kind(kTile), k > 0);
         }
         commit(bars + BAR(s_full) + 8 * x);
+        pass_turn(bars);
         for (int j = 0; j < times_k; ++j) commit(bars + BAR(k_empty) + 8 * (ck & 1));
     } else {
         commit(bars + BAR(o_full) + 8 * x);
+        pass_turn(bars);
     }
-    if (product)
-        for (int j = 0; j < times_v; ++j) commit(bars + BAR(v_empty) + 8 * (cv & 1));
 }
 
 // ---- tile X: softmax (four warps, a row a lane), and the issue of its MMAs ----
@@ -691,7 +761,8 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
         // the tile of step i, by its number in the CTA; how often it is let go
         auto tile = [&](int i) { return tc + (both ? i : 2 * i + x); };
         auto times = [&](int i) { return both && i < sp->na ? 1 : 2; };
-        if ((warp & 3) == 0 && steps) issue_mmas<D, BITS>(bars, smem, tmem, x, both ? x : 0, false, false, 0, 0, true, tile(0), times(0));
+        if ((warp & 3) == 0 && steps) issue_mmas<D, BITS>(bars, smem, tmem, x, both ? x : 0, false, false, false, 0, 0, true, tile(0),
+                                                     times(0));
         // A row's position is p0 + (r >> lgq): the last key that it sees.  Of the warp's rows the first one sees
         // least, the last one starts last.
         const int p0 = sp->n_quant + sp->n_resid + sp->t0, r0 = r - lane;
@@ -803,7 +874,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
             fence_before();
             tile_sync(x);
             if ((warp & 3) == 0)
-                issue_mmas<D, BITS>(bars, smem, tmem, x, both ? x : 0, true, i > 0, tile(i), times(i), i + 1 < steps, tile(i + 1),
+                issue_mmas<D, BITS>(bars, smem, tmem, x, both ? x : 0, true, i > 0, key0 >= sp->n_quant, tile(i), times(i), i + 1 < steps, tile(i + 1),
                                     times(i + 1));
         }
         tc += sp->nt;
@@ -927,7 +998,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             mbar_init(&b.span_full[j], 1);
             mbar_init(&b.span_empty[j], kSpanReaders);
         }
-        b.failed = 0;
+        b.failed = b.busy = 0;
         b.bad = b.odd = 0;
         fence_mbar_init();
     }

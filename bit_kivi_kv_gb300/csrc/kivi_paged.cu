@@ -245,7 +245,8 @@ long long fresh_blocks(const kivi::Geometry& g, const SeqState& sq, int n) {
 // Workspace of a chunk attention call: the wide kernel's partial results, then the gathered rows and the partial
 // results of the groups that the sequences with few rows make (kMaxCallSeqs at most).
 size_t wide_ws_need(const kivi::Geometry& g) {
-    return (size_t)kivi::kMaxChunkCtas * 2 * kivi::kRows * kivi::chunk_partial_stride(g.D) * sizeof(float);
+    return (size_t)kivi::kMaxChunkCtas *
+           (2 * kivi::kRows * kivi::chunk_partial_stride(g.D) * sizeof(float) + sizeof(kivi::MergeJob));
 }
 int groups_of(const kivi::Geometry& g, int len) {
     const long long rows = (long long)len * (g.Hq / g.Hkv);
@@ -716,6 +717,8 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
         a.cap = x->cap;
         a.slopes = x->slopes;
         a.ws = static_cast<float*>(workspace);
+        a.jobs = reinterpret_cast<kivi::MergeJob*>(a.ws + (size_t)kivi::kMaxChunkCtas * 2 * kivi::kRows *
+                                                               kivi::chunk_partial_stride(g.D));
         // every CTA gets a tile: a range of the largest weight holds the start of one
         const long long most = a.weight < kivi::kBothWeight ? 1 : a.weight / kivi::kBothWeight;
         const long long ctas = c->num_sms < kivi::kMaxChunkCtas ? c->num_sms : kivi::kMaxChunkCtas;

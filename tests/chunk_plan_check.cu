@@ -80,11 +80,9 @@ int main() {
         for (int c = 1; c < ctas; ++c) {
             ChunkWalk walk;
             walk.start(&p, s.data(), n, chunk_begin(w, ctas, c), chunk_begin(w, ctas, c + 1));
-            if (!walk.next() || walk.s.first == 0 || chunk_begin(w, ctas, c - 1) > walk.item0) continue;
-            const long long last = walk.item0 + (long long)(walk.s.it.hi - walk.s.it.lo - 1) * walk.s.it.weight();
-            int k = 2;
-            while (c - 1 + k < ctas && chunk_begin(w, ctas, c - 1 + k) <= last) ++k;
-            parts += k - 1;
+            if (!walk.next()) return fail("a CTA without a span");
+            const MergeJob j = merge_job(walk, w, ctas, c);
+            if (j.parts) parts += j.parts - 1;
         }
         if (parts != seen_parts) return fail("parts of the merge");
     }
