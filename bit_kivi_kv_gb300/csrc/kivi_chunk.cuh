@@ -11,13 +11,16 @@ namespace kivi {
 // Work of a call.  Per (sequence, kv head) the queries of the chunk are rows,
 // row = token * nq + query head of the group, in items of kRows rows; an item
 // reads its keys in tiles of kTile tokens, from the first one that any of its
-// rows sees to the last.  An item of more than kHalf rows does two MMAs of
-// kHalf rows a tile (weight 2), one of fewer rows one (weight 1).  Items are in
-// the order sequence, item of the chunk, kv head; CTA c of n takes the tiles
-// that start in weights [c W / n, (c + 1) W / n).  A CTA that holds all of an item's
+// rows sees to the last.  An item of more than kHalf rows does the MMAs of two halves a
+// tile, one of fewer rows of one; both dequantize it, so their tiles weigh 4 and 3 (with 2
+// and 1, of a chunk of 5 whole items and 52 rows over 131072 tokens of 8 heads the CTAs that
+// held the 52 rows took twice as long as the others: 929 us, 798 with 4 and 3).  An item's
+// tiles come after a lead of weight 5, for what a CTA does once for it (queries in, outputs
+// out).  Items are in the order sequence, item of the chunk, kv head; CTA c of n takes
+// the tiles that start in weights [c W / n, (c + 1) W / n).  A CTA that holds all of an item's
 // tiles writes its outputs, others partial results, which a merge joins.
 constexpr int kRows = 256, kHalf = 128, kTile = 128;
-constexpr int kBothWeight = 4, kHalfWeight = 3;
+constexpr int kBothWeight = 4, kHalfWeight = 3, kItemLead = 5;
 constexpr int kMaxChunkCtas = 192;       // most CTAs of a call (one per SM)
 
 struct ChunkSeq {
@@ -55,7 +58,12 @@ struct ChunkItem {
     int lo, hi;         // key tiles
     int both;           // more than kHalf rows
     __host__ __device__ int weight() const { return both ? kBothWeight : kHalfWeight; }
-    __host__ __device__ long long total() const { return (long long)weight() * (hi - lo); }
+    __host__ __device__ long long start(int tile) const { return kItemLead + (long long)weight() * tile; }
+    __host__ __device__ long long total() const { return start(hi - lo); }
+    // the first tile that starts at weight x or behind it
+    __host__ __device__ int tile_at(long long x) const {
+        return x <= kItemLead ? 0 : (int)((x - kItemLead + weight() - 1) / weight());
+    }
 };
 __host__ __device__ inline ChunkItem chunk_item(const ChunkPlan& p, const ChunkSeq& s, int m) {
     ChunkItem it;
@@ -96,7 +104,7 @@ __host__ __device__ inline long long items_weight(const ChunkPlan& p, const Chun
     const int n = item_count(p, s.n);
     const long long c = (long long)s.n_quant + s.n_resid;
     const int whole = m < n ? m : n - 1;
-    long long w = kBothWeight * whole_tiles(p, c, whole);
+    long long w = kBothWeight * whole_tiles(p, c, whole) + (long long)kItemLead * whole;
     if (m == n) w += chunk_item(p, s, n - 1).total();
     return w * p.Hkv;
 }
@@ -144,10 +152,9 @@ struct ChunkWalk {
     // The next span with a tile; false when the range is used up.
     __host__ __device__ bool next() {
         while (x < end) {
-            const long long w = s.it.weight(), tot = s.it.total();
-            const long long from = x - item0, to = end - item0 < tot ? end - item0 : tot;
-            s.first = (int)((from + w - 1) / w);
-            s.last = (int)((to + w - 1) / w);
+            const long long tot = s.it.total();
+            s.first = s.it.tile_at(x - item0);
+            s.last = s.it.tile_at(end - item0 < tot ? end - item0 : tot);
             x = item0 + tot;                    // (beyond end: the loop ends with the next call)
             if (s.first < s.last) return true;
             advance();
@@ -198,8 +205,8 @@ constexpr int chunk_partial_stride(int D) { return D + 2; }      // o[D], m, l o
 // (the first span that the walk gives; called after next())
 __host__ __device__ inline MergeJob merge_job(const ChunkWalk& w, long long weight, int n_ctas, int c) {
     MergeJob j{0, 0, 0, 0};
-    if (w.s.first == 0 || chunk_begin(weight, n_ctas, c - 1LL) > w.item0) return j;
-    const long long last = w.item0 + (long long)(w.s.it.hi - w.s.it.lo - 1) * w.s.it.weight();
+    if (w.s.first == 0 || chunk_begin(weight, n_ctas, c - 1LL) > w.item0 + w.s.it.start(0)) return j;
+    const long long last = w.item0 + w.s.it.start(w.s.it.hi - w.s.it.lo - 1);
     j.parts = 2;
     while (c - 1 + j.parts < n_ctas && chunk_begin(weight, n_ctas, c - 1LL + j.parts) <= last) ++j.parts;
     j.rows = (w.s.it.t1 - w.s.it.t0) * w.p->nq;

@@ -480,7 +480,7 @@ inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, uint32_t bars, in
         bool more = true;
         while (more) {
             more = walk.next();
-            if (n == 0) a.jobs[blockIdx.x] = merge_job(walk, a.weight, a.n_ctas, blockIdx.x);   // (every CTA has a span)
+            if (n == 0) a.jobs[blockIdx.x] = more ? merge_job(walk, a.weight, a.n_ctas, blockIdx.x) : MergeJob{0, 0, 0, 0};
             const uint32_t slot = n % kSpanRing;
             wait_for<true>(bars, bars + BAR(span_empty) + 8 * (slot), ((n / kSpanRing) & 1) ^ 1);
             Span o;

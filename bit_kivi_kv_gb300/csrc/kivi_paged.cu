@@ -719,7 +719,7 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
         a.ws = static_cast<float*>(workspace);
         a.jobs = reinterpret_cast<kivi::MergeJob*>(a.ws + (size_t)kivi::kMaxChunkCtas * 2 * kivi::kRows *
                                                                kivi::chunk_partial_stride(g.D));
-        // every CTA gets a tile: a range of the largest weight holds the start of one
+        // a tile's weight for every CTA at least
         const long long most = a.weight < kivi::kBothWeight ? 1 : a.weight / kivi::kBothWeight;
         const long long ctas = c->num_sms < kivi::kMaxChunkCtas ? c->num_sms : kivi::kMaxChunkCtas;
         a.n_ctas = (int)(most < ctas ? most : ctas);

@@ -1,6 +1,6 @@
 // The plan of a chunk attention call (kivi_chunk.cuh) against counting one by one: the
 // weights of a sequence's items in closed form, and the CTAs' spans, which must
-// hold every tile of every item once, in order, each CTA at least one.
+// hold every tile of every item once, in order.
 #include <cstdio>
 #include <cstdlib>
 #include <random>
@@ -57,6 +57,7 @@ int main() {
         const int ctas = (int)std::min(most, pick(0, 1) ? pick(1, 40) : 152LL);
         size_t at = 0;
         long long seen_parts = 0;
+        int empty = 0;
         for (int c = 0; c < ctas; ++c) {
             ChunkWalk walk;
             walk.start(&p, s.data(), n, chunk_begin(w, ctas, c), chunk_begin(w, ctas, c + 1));
@@ -72,15 +73,17 @@ int main() {
                     if (y.seq != x.seq || y.m != x.m || y.head != x.head || y.tile != x.it.lo + t) return fail("order of tiles");
                 }
             }
-            if (!tiles) return fail("a CTA without a tile");
+            empty += !tiles;
         }
         if (at != want.size()) return fail("tiles left over");
+        // (a CTA without a tile lies between two items)
+        if (empty > 2 * (long long)want.size()) return fail("empty CTAs");
         // the merge's parts of each split item are the spans that continue it
         long long parts = 0;
         for (int c = 1; c < ctas; ++c) {
             ChunkWalk walk;
             walk.start(&p, s.data(), n, chunk_begin(w, ctas, c), chunk_begin(w, ctas, c + 1));
-            if (!walk.next()) return fail("a CTA without a span");
+            if (!walk.next()) continue;
             const MergeJob j = merge_job(walk, w, ctas, c);
             if (j.parts) parts += j.parts - 1;
         }
