@@ -15,12 +15,12 @@ namespace kivi {
 // tile, one of fewer rows of one; both dequantize it, so their tiles weigh 4 and 3 (with 2
 // and 1, of a chunk of 5 whole items and 52 rows over 131072 tokens of 8 heads the CTAs that
 // held the 52 rows took twice as long as the others: 929 us, 798 with 4 and 3).  An item's
-// tiles come after a lead of weight 5, for what a CTA does once for it (queries in, outputs
+// tiles come after a lead of weight 16, for what a CTA does once for it (queries in, outputs
 // out).  Items are in the order sequence, item of the chunk, kv head; CTA c of n takes
 // the tiles that start in weights [c W / n, (c + 1) W / n).  A CTA that holds all of an item's
 // tiles writes its outputs, others partial results, which a merge joins.
 constexpr int kRows = 256, kHalf = 128, kTile = 128;
-constexpr int kBothWeight = 4, kHalfWeight = 3, kItemLead = 5;
+constexpr int kBothWeight = 4, kHalfWeight = 3, kItemLead = 16;
 constexpr int kMaxChunkCtas = 192;       // most CTAs of a call (one per SM)
 
 struct ChunkSeq {
@@ -188,7 +188,7 @@ struct ChunkArgs {
     const float* slopes;
     ChunkPlan plan;
     long long weight;   // of the whole call
-    float* ws;          // partial results: [n_ctas][2][kRows][D + 2]
+    float* ws;          // partial results: [n_ctas][2][kRows][chunk_partial_stride(D)]
     struct MergeJob* jobs;   // [n_ctas]: what each CTA's first span leaves to be joined
     ChunkSeq seqs[kMaxCallSeqs];
 };
@@ -200,7 +200,7 @@ struct MergeJob {
 };
 // The weights [x0, x1) of CTA c.
 __host__ __device__ inline long long chunk_begin(long long weight, int n_ctas, long long c) { return c * weight / n_ctas; }
-constexpr int chunk_partial_stride(int D) { return D + 2; }      // o[D], m, l of a row
+constexpr int chunk_partial_stride(int D) { return D + 4; }      // o[D], m, l of a row (16-byte aligned)
 
 // (the first span that the walk gives; called after next())
 __host__ __device__ inline MergeJob merge_job(const ChunkWalk& w, long long weight, int n_ctas, int c) {

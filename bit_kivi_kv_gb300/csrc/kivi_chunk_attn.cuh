@@ -38,8 +38,8 @@
 // Roundings: keys and values to fp16 (half a step of 2^-11), probabilities to
 // fp16, scaled so that the largest is between 2^8 and 2^15: what falls below
 // fp16's range is under 2^-32 of the row's largest.  Everything else is fp32.
-// The running maximum is only raised when a tile exceeds it by 2^7 (the sums in tensor
-// memory are then scaled), which leaves the result the same.
+// The reference is the maximum of some tile so far, raised (and the sums in tensor memory
+// scaled) when the weights of 64 keys reach 2^15 together, which leaves the result the same.
 //
 // A value row that is not finite would reach rows that do not see it
 // through the product (0 * inf): it is taken as zeros and noted, and the rows that
@@ -66,8 +66,8 @@ struct Regs {
     static_assert(2 * SOFTMAX + 2 * FILL + REST <= 5 * kRegs, "registers of the launch");
 };
 constexpr int kSpanRing = 4, kSpanReaders = 16;
-constexpr float kRaise = 7.f;      // base-2 logits above the reference that a tile may have
-constexpr float kLift = 8.f;       // probabilities are held times 2^8
+constexpr float kLift = 8.f;       // weights are held times 2^8
+constexpr float kMostSum = 32768.f;   // of 64 weights: each is in fp16's range then
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int BITS>
@@ -751,9 +751,11 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
             const __half* src = a.q + (long long)(sp->tok0 + sp->t0 + (r >> lgq)) * a.q_stride[0] +
                                 ((sp->head << lgq) + (r & ((1 << lgq) - 1))) * a.q_stride[1];
             const uint32_t dst = smem + S::OFF_Q + x * S::Q_BYTES;
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c)
-                sts128(dst + operand_at<kHalf>(row, c), r < n_rows ? ldg_row(src + 8 * c) : uint4{0, 0, 0, 0});
+            uint4 v[D / 8];                                    // (all loads in flight)
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) v[c] = r < n_rows ? ldg_row(src + 8 * c) : uint4{0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) sts128(dst + operand_at<kHalf>(row, c), v[c]);
             fence_proxy_async();
         }
         if (both) tile_sync(x);
@@ -810,37 +812,46 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                     wait_st();
                     mul = 1.f;
                 }
-                // Half a tile at a time: the weights by the present reference are kept in registers until their
-                // maximum has shown that they are in range; a half that is not raises it and is taken again.
+                // Half a tile at a time: the weights by the present reference are kept in registers until their sum
+                // has shown that each is in range (the sum of 64 weights by a fitting reference is 2^14 at
+                // most); a reference that is too low, or none yet, is raised and the half taken again.
                 const uint64_t mul2 = pair(mul, mul);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t from = ts + 64 * h;
+                    bool again = true;
                     while (true) {
                         const float ref = m == -INFINITY ? 0.f : m - kLift;
                         const uint64_t ref2 = pair(-ref, -ref);
                         uint64_t sum[2] = {0, 0};
                         uint32_t p[32];
-                        float v[16], u[16], mx = -INFINITY;
+                        float v[16], u[16];
                         ld16(from, v);
 #pragma unroll
                         for (int c = 0; c < 4; c += 2) {
                             wait_ld(v);
                             ld16(from + 16 * c + 16, u);
-                            mx = max16(mx, v);
                             weights16(p + 8 * c, v, mul2, ref2, sum);
                             wait_ld(u);
                             if (c < 2) ld16(from + 32, v);
-                            mx = max16(mx, u);
                             weights16(p + 8 * c + 8, u, mul2, ref2, sum);
                         }
-                        mx *= mul;
-                        if (!__any_sync(kFull, mx > m + kRaise)) {
+                        const float2 total = unpair(add2(sum[0], sum[1]));
+                        const float all = total.x + total.y;
+                        if (!again || !__any_sync(kFull, all >= kMostSum || m == -INFINITY)) {
                             st32(ts + 32 * h, p);
-                            const float2 total = unpair(add2(sum[0], sum[1]));
-                            l += total.x + total.y;
+                            l += all;
                             break;
                         }
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            ld16(from + 16 * c, v);
+                            wait_ld(v);
+                            mx = max16(mx, v);
+                        }
+                        mx *= mul;
+                        again = false;                         // (the weights by the maximum fit, if there is one)
                         // raised by a whole number, so that scaling what is there (sums, the first half's weights) is exact
                         const float top = m == -INFINITY ? mx : m + fmaxf(0.f, ceilf(mx - m));
                         const float f = m == -INFINITY ? 0.f : exp2_ftz(m - top);
@@ -958,7 +969,8 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                     }
                 } else if (valid) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) *reinterpret_cast<float2*>(part + 32 * c + j) = make_float2(o[j], o[j + 1]);
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<float4*>(part + 32 * c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 }
             }
             if (valid && !whole) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
