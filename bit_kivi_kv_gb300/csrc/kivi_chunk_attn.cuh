@@ -35,11 +35,11 @@
 // Rows that are still fp16 (residual and chunk) are copied; values of tiles
 // that hold nothing else stay token by token (the MMA takes both orders).
 //
-// Roundings: keys and values to fp16 (half a step of 2^-11), probabilities to
-// fp16, scaled so that the largest is between 2^8 and 2^15: what falls below
-// fp16's range is under 2^-32 of the row's largest.  Everything else is fp32.
-// The reference is the maximum of some tile so far, raised (and the sums in tensor memory
-// scaled) when the weights of 64 keys reach 2^15 together, which leaves the result the same.
+// Roundings: keys and values to fp16 (half a step of 2^-10), probabilities to
+// fp16, scaled so that 2^4 at least stands for the row's largest: what falls below fp16's
+// range is under 2^-29 of it.  Everything else is fp32.  The reference is the
+// maximum of some tile so far, raised (and the sums in tensor memory scaled) when the
+// weights of 64 keys reach 2^15 together, which leaves the result the same.
 //
 // A value row that is not finite would reach rows that do not see it
 // through the product (0 * inf): it is taken as zeros and noted, and the rows that
@@ -66,7 +66,7 @@ struct Regs {
     static_assert(2 * SOFTMAX + 2 * FILL + REST <= 5 * kRegs, "registers of the launch");
 };
 constexpr int kSpanRing = 4, kSpanReaders = 16;
-constexpr float kLift = 8.f;       // weights are held times 2^8
+constexpr float kLift = 4.f;       // weights are held times 2^4
 constexpr float kMostSum = 32768.f;   // of 64 weights: each is in fp16's range then
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -813,8 +813,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                     mul = 1.f;
                 }
                 // Half a tile at a time: the weights by the present reference are kept in registers until their sum
-                // has shown that each is in range (the sum of 64 weights by a fitting reference is 2^14 at
-                // most); a reference that is too low, or none yet, is raised and the half taken again.
+                // has shown that each is in range (64 weights by the maximum are 2^10 at most); a reference that is too low, or none yet, is raised and the half taken again.
                 const uint64_t mul2 = pair(mul, mul);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {

@@ -13,7 +13,7 @@ The bound, from the kernel's arithmetic:
            each, of numbers up to 1); its slope is at most 1.  A bias: 2^-22 of itself.
   weights  2^y to 2^-21; rounded to fp16 for the product with the values (2^-11) but not in the
            sum that they are divided by; a weight below fp16's range is off by 2^-25 where the
-           largest one is held as 2^8 at least: 2^-33 of it.
+           largest one is held as 2^4 at least: 2^-29 of it.
   values   dequantized ones rounded to fp16 (2^-11, 2^-25 below 2^-14).
   sums     n tokens in n / 16 steps cut to 2^-23, over two halves of a tile, parts and tiles:
            (64 + n / 16) 2^-23 of sum w |v|.
@@ -91,7 +91,7 @@ def ref_attend(keys, vals, n_quant, q, past, scale=None, cap=0.0, window=0, slop
     d = a * (2.0 ** -11 * deq + 2.0 ** -18) + scale * q.abs().sum(1, keepdim=True) * 2.0 ** -25 * deq
     size = x.masked_fill(hidden, 0.0).abs()
     d = d + 2.0 ** -22 * (size + top.abs() + bias.abs()) + 2.0 ** -20 * cap + 2.0 ** -21
-    move = w * (torch.expm1(d) + 2.0 ** -11) + 2.0 ** -33 * (~hidden) / torch.exp(x - top).sum(1, keepdim=True)
+    move = w * (torch.expm1(d) + 2.0 ** -11) + 2.0 ** -29 * (~hidden) / torch.exp(x - top).sum(1, keepdim=True)
     av = vals.abs()
     verr = (2.0 ** -11 * av + 2.0 ** -25) * deq[:, None]
     bound = (move @ av + o.abs() * (w * torch.expm1(d)).sum(1, keepdim=True) + w @ verr
