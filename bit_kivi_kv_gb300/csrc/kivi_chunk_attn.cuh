@@ -49,6 +49,8 @@
 #include <math.h>
 #include <stddef.h>
 
+#include <atomic>
+
 #include "kivi_dequant.cuh"
 
 namespace kivi {
@@ -237,6 +239,11 @@ __device__ __forceinline__ float exp2_ftz(float x) {
     return y;
 }
 __device__ __forceinline__ void tile_sync(int x) { asm volatile("bar.sync %0, 128;" ::"r"(3 + x) : "memory"); }
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 template <int ID, int N>
 __device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
 
@@ -790,22 +797,25 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                         float v[32];
                         ld32(ts + 32 * c, v);
                         wait_ld(v);
+                        const int d = key0 + 32 * c - hi;      // key less position of the first column
+                        if (MOD && a.cap > 0.f) {
+                            // cap tanh(y), tanh(y) = 1 - 2 / (exp(2 y) + 1)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int key = key0 + 32 * c + j;
-                            if (MOD) {
-                                if (a.cap > 0.f) {
-                                    // cap tanh(y), tanh(y) = 1 - 2 / (exp(2 y) + 1)
-                                    const float e = exp2_ftz(v[j] * cap_in);
-                                    v[j] = cap_out * (1.f - __fdividef(2.f, e + 1.f));
-                                } else {
-                                    v[j] *= a.scale_log2;
-                                }
-                                v[j] = fmaf(slope, (float)(key - hi), v[j]);
-                            } else {
-                                v[j] *= a.scale_log2;
-                            }
-                            if (key > hi || key < lo) v[j] = -INFINITY;
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = fmaf(-2.f * cap_out, rcp_ftz(exp2_ftz(v[j] * cap_in) + 1.f), cap_out);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] *= a.scale_log2;
+                        }
+                        if (MOD && a.slopes) {
+                            const float first = slope * (float)d;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = fmaf(slope, (float)j, v[j] + first);
+                        }
+                        if (cut) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j > -d || j < lo - hi - d) v[j] = -INFINITY;
                         }
                         st32(ts + 32 * c, v);
                     }
@@ -813,7 +823,8 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                     mul = 1.f;
                 }
                 // Half a tile at a time: the weights by the present reference are kept in registers until their sum
-                // has shown that each is in range (64 weights by the maximum are 2^10 at most); a reference that is too low, or none yet, is raised and the half taken again.
+                // has shown that each is in range (64 weights by the maximum are 2^10 at most); a reference that is
+                // too low, or none yet, is raised and the half taken again.
                 const uint64_t mul2 = pair(mul, mul);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -1041,8 +1052,17 @@ template <int D, int BITS, bool MOD>
 cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t st) {
     using S = Shape<D, BITS>;
     auto kernel = chunk_attn_kernel<D, BITS, MOD>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    // the opt-in to its shared memory is a property of the kernel on a device: made once for each
+    static std::atomic<unsigned long long> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev > 63 || !(ready.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev <= 63) ready.fetch_or(bit, std::memory_order_release);
+    }
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3((unsigned)a.n_ctas);
     lc.blockDim = dim3(kChunkThreads);

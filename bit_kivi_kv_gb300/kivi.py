@@ -807,7 +807,9 @@ class KiviPagedCache:
         if t.dtype is not _torch.float16 or t.shape != shape or t.get_device() != device or t.stride(2) != 1:
             raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be a float16 tensor of shape {shape} with dense channels "
                                                   f"on the current device, got {t.dtype} {tuple(t.shape)} on {t.device}")
-        return t.stride(0), t.stride(1)
+        # (the stride of a single token or head says nothing: it may be any number)
+        d = shape[2]
+        return t.stride(0) if tokens > 1 else heads * d, t.stride(1) if heads > 1 else d
 
     @staticmethod
     def _lens(seqs, lens):
