@@ -128,12 +128,12 @@ def _load():
         "kivi_paged_block_scores": (I, [P, IP, I, P, F, P, LL, P]),
         "kivi_paged_decode_blocks": (I, [P, IP, I, P, P, I, P, F, P]),
         "kivi_paged_append": (I, [P, IP, I, P, P, P]),
-        "kivi_paged_chunk_workspace_bytes": (SZ, [pcfgp, IP, I]),
-        "kivi_paged_chunk_attn": (I, [P, IP, IP, I, P, P, SZ, P]),   # a kivi_chunk by reference, or its packed bytes
-        "kivi_paged_append_chunk": (I, [P, IP, IP, I, P, P, P, P, P]),   # strides: addresses, or packed bytes
+        "kivi_paged_chunk_workspace_bytes": (SZ, [pcfgp, P, I]),   # (int lists: ctypes arrays, or packed bytes)
+        "kivi_paged_chunk_attn": (I, [P, P, P, I, P, P, SZ, P]),   # a kivi_chunk by reference, or its packed bytes
+        "kivi_paged_append_chunk": (I, [P, P, P, I, P, P, P, P, P]),   # strides: addresses, or packed bytes
         "kivi_paged_fork": (I, [P, IP, I, IP, P]),
         "kivi_paged_truncate": (I, [P, I, LL]),
-        "kivi_paged_read": (I, [P, IP, I, LL, LL, P, P, P]),
+        "kivi_paged_read": (I, [P, P, I, LL, LL, P, P, P]),
         "kivi_qk_norm_rope": (I, [P, P]),     # a kivi_qkv by reference, or its packed bytes
         "kivi_append_qkv": (I, [P, P, P]),
     }
@@ -320,6 +320,11 @@ def kivi_select_blocks(scores: int, rows: int, cols: int, ld: int, n_keep: int, 
 
 def kivi_decode_blocks(h: int, q: int, blocks: int, n_list: int, out: int, softmax_scale: float, stream: int):
     _check(lib.kivi_decode_blocks(h, q, blocks, n_list, out, softmax_scale, stream))
+
+
+def _ints(values):
+    """values as the bytes of an int array (faster to make than a ctypes array)."""
+    return struct.pack(f"@{len(values)}i", *values)
 
 
 def _seq_array(seqs):
@@ -710,6 +715,7 @@ class KiviPagedCache:
                                      device)
         self.handle = kivi_paged_create(self.cfg, self.buffer.data_ptr(), nbytes)
         self._heads = (n_q_heads, n_kv_heads, head_dim)
+        self._ws_bytes = {}     # workspace of chunk_attn by its lengths
         self._device = self.buffer.get_device()
 
     def _alloc(self, nbytes, device):
@@ -803,20 +809,20 @@ class KiviPagedCache:
     def _chunk(self, t, what, tokens, heads, device):
         """Checks a chunk's tensor [tokens, heads, head_dim] (fp16, any strides with dense
         channels); its strides over tokens and heads."""
-        shape = (tokens, heads, self._heads[2])
-        if t.dtype is not _torch.float16 or t.shape != shape or t.get_device() != device or t.stride(2) != 1:
-            raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be a float16 tensor of shape {shape} with dense channels "
+        d = self._heads[2]
+        s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
+        if t.dtype is not _torch.float16 or t.shape != (tokens, heads, d) or t.get_device() != device or s2 != 1:
+            raise KiviError(KIVI_ERR_INVALID_ARG, f"{what} must be a float16 tensor of shape {(tokens, heads, d)} with dense channels "
                                                   f"on the current device, got {t.dtype} {tuple(t.shape)} on {t.device}")
         # (the stride of a single token or head says nothing: it may be any number)
-        d = shape[2]
-        return t.stride(0) if tokens > 1 else heads * d, t.stride(1) if heads > 1 else d
+        return s0 if tokens > 1 else heads * d, s1 if heads > 1 else d
 
     @staticmethod
     def _lens(seqs, lens):
         """The lengths of a chunk call, one for each sequence."""
         if len(lens) != len(seqs):
             raise KiviError(KIVI_ERR_INVALID_ARG, f"{len(seqs)} sequences, {len(lens)} lengths")
-        return _seq_array(lens), sum(lens)
+        return _ints(lens), sum(lens)
 
     def chunk_attn(self, seqs, lens, q, k, v, out=None, softmax_scale=0.0, cap=0.0, window=0, slopes=None, stream=None):
         """Attention of lens[i] new tokens of each listed sequence over its cached tokens
@@ -837,11 +843,15 @@ class KiviPagedCache:
         if slopes is not None:
             _expect(slopes, "slopes", _torch.float32, (hq,), device)
         # scratch of this call alone, from its stream's memory: calls on other streams and in graphs share nothing
-        ws_bytes = lib.kivi_paged_chunk_workspace_bytes(ctypes.byref(self.cfg), n_arr, len(seqs))
+        ws_bytes = self._ws_bytes.get(n_arr)
+        if ws_bytes is None:
+            if len(self._ws_bytes) >= 256:
+                self._ws_bytes.clear()
+            ws_bytes = self._ws_bytes[n_arr] = lib.kivi_paged_chunk_workspace_bytes(ctypes.byref(self.cfg), n_arr, len(seqs))
         ws = _new((ws_bytes,), _torch.uint8, q.device, stream)
         args = _CHUNK.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *qs, *ks, *vs, *os_, softmax_scale, cap,
                            window, slopes.data_ptr() if slopes is not None else 0)
-        _check(lib.kivi_paged_chunk_attn(self.handle, _seq_array(seqs), n_arr, len(seqs), args, ws.data_ptr(), ws_bytes,
+        _check(lib.kivi_paged_chunk_attn(self.handle, _ints(seqs), n_arr, len(seqs), args, ws.data_ptr(), ws_bytes,
                                          _current_stream(device) if stream is None else stream.cuda_stream))
         return out
 
@@ -852,7 +862,7 @@ class KiviPagedCache:
         n_arr, tokens = self._lens(seqs, lens)
         ks = self._chunk(k, "k", tokens, hkv, device)
         vs = self._chunk(v, "v", tokens, hkv, device)
-        _check(lib.kivi_paged_append_chunk(self.handle, _seq_array(seqs), n_arr, len(seqs), k.data_ptr(), _PAIR.pack(*ks),
+        _check(lib.kivi_paged_append_chunk(self.handle, _ints(seqs), n_arr, len(seqs), k.data_ptr(), _PAIR.pack(*ks),
                                            v.data_ptr(), _PAIR.pack(*vs),
                                            _current_stream(device) if stream is None else stream.cuda_stream))
 
@@ -885,6 +895,6 @@ class KiviPagedCache:
             K, V = out
             _expect(K, "out[0]", f16, shape, device)
             _expect(V, "out[1]", f16, shape, device)
-        _check(lib.kivi_paged_read(self.handle, _seq_array(seqs), len(seqs), first, count, K.data_ptr(), V.data_ptr(),
+        _check(lib.kivi_paged_read(self.handle, _ints(seqs), len(seqs), first, count, K.data_ptr(), V.data_ptr(),
                                    _current_stream(device) if stream is None else stream.cuda_stream))
         return out
