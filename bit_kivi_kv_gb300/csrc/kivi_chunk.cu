@@ -66,7 +66,7 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& a, const MergeJob& jo
     __half* out = a.out + (long long)(job.tok + r / nq) * a.out_stride[0] + (job.head * nq + r % nq) * a.out_stride[1];
 #pragma unroll
     for (int d = 0; d < D / 64; ++d)
-        *reinterpret_cast<uint32_t*>(out + 64 * d + 2 * lane) = pack_f16x2(o[d].x * inv, o[d].y * inv);
+        *reinterpret_cast<uint32_t*>(out + 64 * d + 2 * lane) = pack_out(o[d].x * inv, o[d].y * inv);
 }
 
 // Block (x, y): the item that CTA x + 1's first span continues, if CTA x began it; every gridDim.y-th eight of its

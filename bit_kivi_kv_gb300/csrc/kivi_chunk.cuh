@@ -198,6 +198,11 @@ struct MergeJob {
     int parts, rows;    // rows of the item
     int tok, head;      // its first new token in the packed tensors, kv head
 };
+// CTAs of a call whose items are `items` (of all heads): a whole tile's weight for each at least, leads not counted.
+__host__ __device__ inline int chunk_ctas(long long weight, long long items, int most) {
+    const long long n = (weight - kItemLead * items) / kBothWeight;
+    return (int)(n < 1 ? 1 : n < most ? n : most);
+}
 // The weights [x0, x1) of CTA c.
 __host__ __device__ inline long long chunk_begin(long long weight, int n_ctas, long long c) { return c * weight / n_ctas; }
 constexpr int chunk_partial_stride(int D) { return D + 4; }      // o[D], m, l of a row (16-byte aligned)
@@ -213,6 +218,15 @@ __host__ __device__ inline MergeJob merge_job(const ChunkWalk& w, long long weig
     j.tok = w.seqs[w.s.seq].tok0 + w.s.it.t0;
     j.head = w.s.head;
     return j;
+}
+
+// Outputs: finite weights of finite values, which the weights' own roundings may take past the largest fp16 number (by
+// 2^-11 of it): such a one is the largest.  NaN stays.
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
+    uint32_t v;
+    asm("{\n .reg .b32 t;\n cvt.rn.f16x2.f32 t, %2, %1;\n min.NaN.f16x2 t, t, %3;\n max.NaN.f16x2 %0, t, %4;\n}"
+        : "=r"(v) : "f"(lo), "f"(hi), "r"(0x7bff7bffu), "r"(0xfbfffbffu));
+    return v;
 }
 
 cudaError_t launch_chunk_attn_d64(const ChunkArgs& a, int bits, cudaStream_t st);

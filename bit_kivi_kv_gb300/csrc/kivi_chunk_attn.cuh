@@ -41,9 +41,11 @@
 // maximum of some tile so far, raised (and the sums in tensor memory scaled) when the
 // weights of 64 keys reach 2^15 together, which leaves the result the same.
 //
-// A value row that is not finite would reach rows that do not see it
-// through the product (0 * inf): it is taken as zeros and noted, and the rows that
-// see it become NaN at the end.
+// A value that is not finite would reach rows that do not see it
+// through the product (0 * inf): it is taken as zero and noted, and the rows that
+// see it become NaN at the end.  A dequantized number beyond fp16's range whose step and zero
+// are finite is held as the largest fp16 number: off by 2^-10 of it at most, since a block's
+// extremes are fp16 numbers and its step is off by 2^-11.
 #pragma once
 
 #include <math.h>
@@ -109,7 +111,8 @@ struct Bars {
     uint32_t tmem;
     int failed;         // a wait ran out: the outputs from here on are NaN
     int busy;           // a tile's MMAs are being issued
-    unsigned bad, odd;  // spans with a block-table entry outside the pool, with a value that is not finite: bit number % 32
+    unsigned bad, odd;  // spans with a block-table entry outside the pool, with an fp16 value that is not finite: bit number % 32
+    int last_odd[2 * kSpanRing];   // of a span (number % 8): the last quantized token whose value is not finite, or -1
     alignas(16) Span spans[kSpanRing];
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
@@ -360,6 +363,38 @@ __device__ __forceinline__ void value_unit(const Words<W>& u, uint32_t ent, int 
     }
 }
 
+__device__ __forceinline__ uint32_t lds16(uint32_t at) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)v) : "memory");
+}
+// Of a unit some of whose steps or zeros are large: numbers beyond fp16's range become the largest one; values whose step
+// or zero is not finite become zeros (keys like that stay: they reach their own column of the logits alone).  A token a
+// lane; whether its value was one of those.
+template <int D>
+__device__ __forceinline__ bool mend_unit(bool values, uint32_t ent, int lgG, uint32_t dst, int tok, int lane) {
+    const int ve = 64 * (D >> lgG);
+    bool odd = false;
+#pragma unroll 1
+    for (int ch = 0; ch < D; ++ch) {
+        const uint32_t at = dst + (values ? operand_at<D>(ch, tok >> 3) + 2 * (tok & 7) : operand_at<kTile>(tok, ch >> 3) + 2 * (ch & 7));
+        const uint32_t x = lds16(at);
+        if ((x & 0x7c00u) != 0x7c00u) continue;
+        const uint32_t s = ent + (values ? (lane >> 4) * ve + 32 * (ch >> lgG) + 8 * ((lane >> 1) & 3) + 4 * ((lane >> 3) & 1) + 2 * (lane & 1)
+                                         : 2 * ch);
+        if ((lds16(s) & 0x7c00u) != 0x7c00u && (lds16(s + (values ? ve / 2 : 2 * D)) & 0x7c00u) != 0x7c00u) {
+            sts16(at, (x & 0x8000u) | 0x7bffu);
+        } else if (values) {
+            sts16(at, 0u);
+            odd = true;
+        }
+    }
+    return odd;
+}
+
 // (asm volatile: not moved ahead of the wait for the preceding kernel, as __ldg may be)
 __device__ __forceinline__ uint4 ldg_row(const void* p) {
     uint4 v;
@@ -520,6 +555,7 @@ inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, uint32_t bars, in
             // (the roles are at spans n - 4 to n: a mark of 24 spans ago is nobody's)
             atomicAnd(&b.bad, ~(1u << ((n + 8) % 32)));
             atomicAnd(&b.odd, ~(1u << ((n + 8) % 32)));
+            b.last_odd[n % (2 * kSpanRing)] = -1;              // (of span n - 8: nobody's)
             b.spans[slot] = o;
             arrive(bars + BAR(span_full) + 8 * (slot));
             ++n;
@@ -533,6 +569,7 @@ struct SpanReader {
     uint32_t bars;
     uint32_t n;                 // of spans read; the present one is number n - 1
     __device__ __forceinline__ unsigned mark() const { return 1u << ((n - 1) % 32); }
+    __device__ __forceinline__ uint32_t place() const { return (n - 1) % (2 * kSpanRing); }
     __device__ __forceinline__ SpanReader(const Bars& data, uint32_t at) : b(data), bars(at), n(0) {}
     __device__ __forceinline__ void release() const { arrive(bars + BAR(span_empty) + 8 * ((n - 1) % kSpanRing)); }
     __device__ __forceinline__ const Span* next() {              // one lane alone, or all of a warp with the same result
@@ -562,6 +599,10 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
     const uint32_t stages = smem + (values ? S::OFF_V : S::OFF_K);
     const int lgG = a.lgG, ve = 64 * (D >> lgG);               // bytes of value entries of a code tile
     const int last_ent = (values ? 2 * ve / 16 : 4 * D / 16) - 1;   // 16-byte groups of a unit's steps and zeros, less one
+    // A step of 2^(15 - BITS) or a zero of 2^15 and more (a bit 15 after the addition), without which no number of a unit
+    // is beyond fp16's range.
+    const int run = values ? ve / 16 : 4 * D / 16;             // 16-byte groups: half of them steps, half zeros, ..
+    const uint32_t large = (0x0800u + (min(lane, last_ent) % run < run / 2 ? BITS * 0x0400u : 0u)) * 0x00010001u;
     SpanReader reader(b, bars);
     // the unit ahead: its bytes where it is quantized
     const Span* sp = nullptr;
@@ -606,10 +647,17 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
         const uint32_t dst = stages + stage * S::K_BYTES;
         const bool ok = __all_sync(kFull, wait_for(bars, empty + 8 * stage, ph ^ 1));
         if (quantized) {
+            auto over = [&](uint32_t v) { return (v & 0x7fff7fffu) + large; };
+            const bool mend = __any_sync(kFull, ((over(ents.x) | over(ents.y) | over(ents.z) | over(ents.w)) & 0x80008000u) != 0u);
             if (lane <= last_ent) sts128(ent + 16 * lane, ents);
             __syncwarp();
             if (values) value_unit<D, BITS>(words, ent, lgG, dst, 32 * w, lane);
             else key_unit<D, BITS>(words, ent, dst, 32 * w, lane);
+            if (mend) {
+                __syncwarp();
+                const unsigned who = __ballot_sync(kFull, mend_unit<D>(values, ent, lgG, dst, 32 * w + lane, lane));
+                if (who && lane == 0) atomicMax(&b.last_odd[reader.place()], t * kTile + 32 * w + 31 - __clz(who));
+            }
         } else if (ok) {
             const long long resid = values ? a.v_resid_off : a.k_resid_off;
             const long long step = values ? a.v_stride[0] : a.k_stride[0], per_head = values ? a.v_stride[1] : a.k_stride[1];
@@ -823,7 +871,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                     mul = 1.f;
                 }
                 // Half a tile at a time: the weights by the present reference are kept in registers until their sum
-                // has shown that each is in range (64 weights by the maximum are 2^10 at most); a reference that is
+                // has shown that each is in range (64 of 2^5 are 2^11); a reference that is
                 // too low, or none yet, is raised and the half taken again.
                 const uint64_t mul2 = pair(mul, mul);
 #pragma unroll 1
@@ -863,18 +911,21 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                         mx *= mul;
                         again = false;                         // (the weights by the maximum fit, if there is one)
                         // raised by a whole number, so that scaling what is there (sums, the first half's weights) is exact
-                        const float top = m == -INFINITY ? mx : m + fmaxf(0.f, ceilf(mx - m));
+                        // (down: the largest weight is 2^4 at least then, and under 2^5)
+                        const float top = m == -INFINITY ? mx : m + fmaxf(0.f, floorf(mx - m));
                         const float f = m == -INFINITY ? 0.f : exp2_ftz(m - top);
                         m = top;
                         l *= f;
                         if (h) {
                             wait_st();
-                            const uint32_t f2 = pack_f16x2(f, f);
+                            // (two factors: weights of up to 2^15 outlast a factor that fp16 does not hold)
+                            const float g1 = fmaxf(f, 0x1p-15f), g2 = fminf(f * 0x1p15f, 1.f);
+                            const uint32_t f1 = pack_f16x2(g1, g1), f2 = pack_f16x2(g2, g2);
                             float y[32];
                             ld32(ts, y);
                             wait_ld(y);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) p[j] = hmul2(__float_as_uint(y[j]), f2);
+                            for (int j = 0; j < 32; ++j) p[j] = hmul2(hmul2(__float_as_uint(y[j]), f1), f2);
                             st32(ts, p);
                         }
                         if (i > 0) {
@@ -930,6 +981,9 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
         }
         if (!fine || *(volatile int*)&b.failed || (*(volatile unsigned*)&b.bad & reader.mark())) m = l = NAN;
         const bool valid = r < n_rows;
+        // (all rows are behind the quantized tokens)
+        if (const int t = *(volatile int*)&b.last_odd[reader.place()]; t >= 0 && (!a.plan.window || t > p0 + (r >> lgq) - a.plan.window))
+            m = l = NAN;
         if ((*(volatile unsigned*)&b.odd & reader.mark()) && valid) {
             // a value that is not finite: the row is NaN if it sees one (looked for again, value by value)
             const Rows v{reinterpret_cast<const __half*>(a.buf + a.v_resid_off) +
@@ -971,10 +1025,10 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
                         uint4 v;
-                        v.x = pack_f16x2(o[j] * inv, o[j + 1] * inv);
-                        v.y = pack_f16x2(o[j + 2] * inv, o[j + 3] * inv);
-                        v.z = pack_f16x2(o[j + 4] * inv, o[j + 5] * inv);
-                        v.w = pack_f16x2(o[j + 6] * inv, o[j + 7] * inv);
+                        v.x = pack_out(o[j] * inv, o[j + 1] * inv);
+                        v.y = pack_out(o[j + 2] * inv, o[j + 3] * inv);
+                        v.z = pack_out(o[j + 4] * inv, o[j + 5] * inv);
+                        v.w = pack_out(o[j + 6] * inv, o[j + 7] * inv);
                         *reinterpret_cast<uint4*>(out + 32 * c + j) = v;
                     }
                 } else if (valid) {

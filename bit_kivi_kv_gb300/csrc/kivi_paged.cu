@@ -255,10 +255,14 @@ int groups_of(const kivi::Geometry& g, int len) {
 size_t group_rows_bytes(const kivi::Geometry& g, int groups) {
     return (size_t)groups * g.Hkv * kivi::kGroupRows * g.D * sizeof(__half);
 }
-size_t chunk_ws_need(const kivi::Geometry& g, const int* lens, int n) {
+// Most groups of a call: the workspace holds no more, whichever sequences make them.
+int most_groups(const kivi::Geometry& g, const int* lens, int n) {
     int groups = 0;
-    for (int i = 0; i < n; ++i)
-        if (groups + groups_of(g, lens[i]) <= kivi::kMaxCallSeqs) groups += groups_of(g, lens[i]);
+    for (int i = 0; i < n; ++i) groups += groups_of(g, lens[i]);
+    return groups < kivi::kMaxCallSeqs ? groups : kivi::kMaxCallSeqs;
+}
+size_t chunk_ws_need(const kivi::Geometry& g, const int* lens, int n) {
+    const int groups = most_groups(g, lens, n);
     kivi::Geometry v = g;
     v.Hq = g.Hkv * kivi::kGroupRows;
     return wide_ws_need(g) + group_rows_bytes(g, groups) + paged_ws_need(v, groups);
@@ -636,7 +640,9 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
     few.n = a.n_seqs = 0;
     a.weight = 0;
     a.plan = kivi::ChunkPlan{g.Hq / g.Hkv, g.Hkv, x->window};
+    const int budget = most_groups(g, lens, n);
     int tok0 = 0, most_rows = 0;
+    long long items = 0;
     bool as_they_lie = true;             // every group is one token's heads, where the decode kernel would look for them
     for (int i = 0; i < n; ++i) {
         if (!lens[i]) continue;
@@ -644,7 +650,7 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
         const long long cached = sq.n_quant + sq.n_resid;
         const int groups = groups_of(g, lens[i]);
         if (groups && plain && cached > 0 && (x->window == 0 || x->window >= cached + lens[i]) &&
-            few.n + groups <= kivi::kMaxCallSeqs) {
+            few.n + groups <= budget) {
             const int rows = lens[i] * a.plan.nq;
             as_they_lie = as_they_lie && lens[i] == 1 && tok0 == few.n;
             for (int r = 0; r < rows; r += kivi::kGroupRows) {
@@ -657,6 +663,7 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
             kivi::ChunkSeq& s = a.seqs[a.n_seqs++];
             s = kivi::ChunkSeq{a.weight, seqs[i], lens[i], tok0, (int)sq.n_quant, sq.n_resid, 0};
             a.weight += kivi::items_weight(a.plan, s, kivi::item_count(a.plan, s.n));
+            items += kivi::item_count(a.plan, s.n);
         }
         tok0 += lens[i];
     }
@@ -719,10 +726,9 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
         a.ws = static_cast<float*>(workspace);
         a.jobs = reinterpret_cast<kivi::MergeJob*>(a.ws + (size_t)kivi::kMaxChunkCtas * 2 * kivi::kRows *
                                                                kivi::chunk_partial_stride(g.D));
-        // a tile's weight for every CTA at least
-        const long long most = a.weight < kivi::kBothWeight ? 1 : a.weight / kivi::kBothWeight;
-        const long long ctas = c->num_sms < kivi::kMaxChunkCtas ? c->num_sms : kivi::kMaxChunkCtas;
-        a.n_ctas = (int)(most < ctas ? most : ctas);
+        int most = c->num_sms < kivi::kMaxChunkCtas ? c->num_sms : kivi::kMaxChunkCtas;
+        if (c->max_ctas > 0 && c->max_ctas < most) most = c->max_ctas;
+        a.n_ctas = kivi::chunk_ctas(a.weight, items * g.Hkv, most);
         e = g.D == 128 ? kivi::launch_chunk_attn_d128(a, g.bits, cs) : kivi::launch_chunk_attn_d64(a, g.bits, cs);
         if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
         kivi::count_launches(1);

@@ -399,7 +399,8 @@ kivi_status kivi_paged_add(kivi_paged_t cache, const void* K, const void* V, lon
 
 /* Release a sequence: its slot and pages return to the free lists (host only,
  * no device work; work already enqueued that reads them must finish before the
- * next call that reuses them is enqueued on another stream). */
+ * next call that reuses them is enqueued on another stream).  A page that a
+ * branch shares (kivi_paged_fork) returns with the last sequence that holds it. */
 kivi_status kivi_paged_release(kivi_paged_t cache, int seq);
 
 /* Token counts of one live sequence. */
@@ -412,7 +413,8 @@ kivi_status kivi_paged_seq_pages(kivi_paged_t cache, int seq, int* pages, int ca
 /* Free pages and free sequence slots. */
 kivi_status kivi_paged_free(kivi_paged_t cache, long long* free_pages, int* free_seqs);
 
-/* Cap the decode kernel's persistent grid at max_ctas CTAs for this cache's
+/* Cap the decode kernel's persistent grid, and that of kivi_paged_chunk_attn's
+ * kernel, at max_ctas CTAs for this cache's
  * calls (0, the default: SMs x resident CTAs per SM); as
  * kivi_cache_set_max_ctas.  Host-only; KIVI_ERR_INVALID_ARG for a negative cap. */
 kivi_status kivi_paged_set_max_ctas(kivi_paged_t cache, int max_ctas);
@@ -571,8 +573,9 @@ size_t kivi_paged_chunk_workspace_bytes(const kivi_paged_config* cfg, const int*
  * tokens are read by the kernel of the single-token calls, with its accuracy.
  * For the others dequantized keys and values are rounded to fp16, and so are the
  * attention weights (times a power of two that keeps them in range); sums are
- * fp32.  A dequantized value beyond fp16's range is infinite there.  A new or residual token whose value
- * row holds a number that is not finite makes the outputs that see it NaN, and no
+ * fp32.  A dequantized number beyond fp16's range (a block that reaches from -65504
+ * to 65504 may have some) is taken as the largest fp16 number there.  A token whose
+ * value holds a number that is not finite makes the outputs that see it NaN, and no
  * other.  A block-table entry outside the pool, or a copy that does not complete
  * (see "Failure detection"), makes the outputs that depend on it NaN.
  *
@@ -701,7 +704,9 @@ kivi_status kivi_append_qkv(kivi_cache_t cache, const kivi_qkv* args, kivi_strea
  * finishes and returns; the context stays usable).  The paged kernel also
  * marks a block-table entry outside the pool the same way.
  *
- * kivi_decode_blocks' waits and marks are the same.
+ * kivi_decode_blocks' waits and marks are the same.  Every wait of
+ * kivi_paged_chunk_attn's kernel is bounded too (2^31 cycles, about 1 s): one that
+ * runs out makes the outputs that its CTA still has to write NaN.
  *
  * Test hook: KIVI_FAULT_COPY_STALL makes the next tensor-core decode call on
  * this cache (kivi_decode_attn, kivi_append_decode or kivi_decode_blocks) expect 16 bytes more on

@@ -4,7 +4,9 @@ reference of the attention and an error bound per output that follows the inputs
 The bound, from the kernel's arithmetic:
 
   keys     dequantized ones are rounded to fp16, half a step of 2^-10: each channel is off by
-           2^-11 of itself (2^-25 below 2^-14); fp16 rows are exact.
+           2^-11 of itself (2^-25 below 2^-14); fp16 rows are exact.  A number beyond fp16's
+           range is taken as 65504: it is at most z + 2 * 65504 (1 + 2^-11) with z >= -65504, so
+           65568, off by 64: 2^-10 of itself (deq_step).
   logits   products of fp16 numbers are exact, the sum over D channels in D / 16 tensor-core
            steps of fp32 sums, which may be cut (2^-23 of the largest partial sum each) after
            alignment of 17 terms: below 2^-18 of A = scale sum |q_c k_c|.  The softmax works on
@@ -13,7 +15,9 @@ The bound, from the kernel's arithmetic:
            each, of numbers up to 1); its slope is at most 1.  A bias: 2^-22 of itself.
   weights  2^y to 2^-21; rounded to fp16 for the product with the values (2^-11) but not in the
            sum that they are divided by; a weight below fp16's range is off by 2^-25 where the
-           largest one is held as 2^4 at least: 2^-29 of it.
+           largest one is held as 2^4 at least: 2^-29 of it.  A reference raised within a tile
+           scales its first half's weights, by f = 2^-1 at most and rounded again: 2^-25 (1 + f +
+           f / 2^-15) where f < 2^-15 is made of two factors, else 2^-25 (1 + f): below 2^-28 in all.
   values   dequantized ones rounded to fp16 (2^-11, 2^-25 below 2^-14).
   sums     n tokens in n / 16 steps cut to 2^-23, over two halves of a tile, parts and tiles:
            (64 + n / 16) 2^-23 of sum w |v|.
@@ -68,7 +72,7 @@ def oracle_truncate(oc, n):
     oc.k_res, oc.v_res = (x[:, :, :max(0, n - oc.n_quant)] for x in (oc.k_res, oc.v_res))
 
 
-def ref_attend(keys, vals, n_quant, q, past, scale=None, cap=0.0, window=0, slope=0.0):
+def ref_attend(keys, vals, n_quant, q, past, scale=None, cap=0.0, window=0, slope=0.0, deq_step=2.0 ** -11):
     """(out, bound) [n][D] of one query head: q [n][D] (fp64) at positions past .. past + n - 1 over keys and
     vals [past + n][D] (fp64, exact), the first n_quant of them dequantized."""
     n, D = q.shape
@@ -88,12 +92,12 @@ def ref_attend(keys, vals, n_quant, q, past, scale=None, cap=0.0, window=0, slop
     o = w @ vals
     deq = (t < n_quant).double()
     a = scale * (q.abs() @ keys.abs().T)
-    d = a * (2.0 ** -11 * deq + 2.0 ** -18) + scale * q.abs().sum(1, keepdim=True) * 2.0 ** -25 * deq
+    d = a * (deq_step * deq + 2.0 ** -18) + scale * q.abs().sum(1, keepdim=True) * 2.0 ** -25 * deq
     size = x.masked_fill(hidden, 0.0).abs()
     d = d + 2.0 ** -22 * (size + top.abs() + bias.abs()) + 2.0 ** -20 * cap + 2.0 ** -21
-    move = w * (torch.expm1(d) + 2.0 ** -11) + 2.0 ** -29 * (~hidden) / torch.exp(x - top).sum(1, keepdim=True)
+    move = w * (torch.expm1(d) + 2.0 ** -11) + 2.0 ** -28 * (~hidden) / torch.exp(x - top).sum(1, keepdim=True)
     av = vals.abs()
-    verr = (2.0 ** -11 * av + 2.0 ** -25) * deq[:, None]
+    verr = (deq_step * av + 2.0 ** -25) * deq[:, None]
     bound = (move @ av + o.abs() * (w * torch.expm1(d)).sum(1, keepdim=True) + w @ verr
              + (64 + (past + n) / 16) * 2.0 ** -23 * (w @ av) + 2.0 ** -11 * o.abs() + 2.0 ** -25)
     return o, bound
@@ -135,8 +139,8 @@ class ChunkRun:
         return SynthKV(1, self.Hq, self.Hkv, self.D, self.seed * 7919 + self.made, outliers=RANGE_2_6_X10_50,
                        sink=self.sink, device="cuda")
 
-    def add(self, L):
-        Kp, Vp, _ = self.draw(L)
+    def add(self, L, kv=None):
+        Kp, Vp = kv or self.draw(L)[:2]
         s = self.cache.add(Kp, Vp)
         oc = OracleCache(1, self.Hkv, self.D, self.bits, self.G, self.R)
         oc.prefill(Kp.cpu().numpy()[None], Vp.cpu().numpy()[None])
@@ -154,7 +158,7 @@ class ChunkRun:
         return torch.cat([p[2] for p in parts]).contiguous(), k, v
 
     # -- calls ----------------------------------------------------------------------
-    def attend(self, seqs, lens, data=None, scale=0.0, cap=0.0, window=0, slopes=None, check=True, fit=lambda x: x):
+    def attend(self, seqs, lens, data=None, scale=0.0, cap=0.0, window=0, slopes=None, check=True, fit=lambda x: x, **bound):
         q, k, v = data or self.chunk(lens)
         qs, ks, vs = fit(q), fit(k), fit(v)
         bands = Banded()
@@ -175,10 +179,10 @@ class ChunkRun:
         self.cache.bands.check("after attention")
         assert torch.equal(before, self.cache.buffer), "attention changed the cache"
         if check:
-            self.check_out(seqs, lens, q, k, v, out, scale, cap, window, slopes)
+            self.check_out(seqs, lens, q, k, v, out, scale, cap, window, slopes, **bound)
         return out
 
-    def check_out(self, seqs, lens, q, k, v, out, scale=0.0, cap=0.0, window=0, slopes=None):
+    def check_out(self, seqs, lens, q, k, v, out, scale=0.0, cap=0.0, window=0, slopes=None, **bound):
         first, rep = 0, self.Hq // self.Hkv
         for s, n in zip(seqs, lens):
             oc = self.live[s]
@@ -189,12 +193,12 @@ class ChunkRun:
             for h in range(self.Hq if n else 0):
                 keys = torch.cat([kc[h // rep], k[part, h // rep].double()])
                 vals = torch.cat([vc[h // rep], v[part, h // rep].double()])
-                ref, bound = ref_attend(keys, vals, oc.n_quant, q[part, h].double(), past, scale or None, cap, window,
-                                        float(slopes[h]) if slopes is not None else 0.0)
+                ref, most = ref_attend(keys, vals, oc.n_quant, q[part, h].double(), past, scale or None, cap, window,
+                                        float(slopes[h]) if slopes is not None else 0.0, **bound)
                 got = out[part, h].double()
                 what = f"sequence {s} ({past} + {n} tokens) head {h}"
                 assert torch.isfinite(got).all(), f"{what}: {int((~torch.isfinite(got)).sum())} values not finite"
-                over = ((got - ref).abs() / bound).max().item()
+                over = ((got - ref).abs() / most).max().item()
                 self.worst = max(self.worst, over)
                 assert over <= 1.0, f"{what}: {over:.2f} of the bound, off by {(got - ref).abs().max().item():.3e}"
             first += n

@@ -24,7 +24,7 @@ int main() {
         ChunkPlan p{nqs[pick(0, 2)], (int)pick(1, 5), windows[pick(0, 5)]};
         const int n = (int)pick(1, 6);
         std::vector<ChunkSeq> s(n);
-        long long w = 0;
+        long long w = 0, n_items = 0;
         struct Tile { int seq, m, head, tile; };
         std::vector<Tile> want;
         for (int i = 0; i < n; ++i) {
@@ -51,10 +51,10 @@ int main() {
                 sum += it.total();
             }
             w += sum * p.Hkv;
+            n_items += items;
         }
         // (as the call sizes its grid)
-        const long long most = w < kBothWeight ? 1 : w / kBothWeight;
-        const int ctas = (int)std::min(most, pick(0, 1) ? pick(1, 40) : 152LL);
+        const int ctas = chunk_ctas(w, n_items * p.Hkv, (int)(pick(0, 1) ? pick(1, 40) : 152));
         size_t at = 0;
         long long seen_parts = 0;
         int empty = 0;

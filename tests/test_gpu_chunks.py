@@ -9,7 +9,8 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover - collected on CPU hosts too
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
-from bit_kivi_kv_gb300.kivi import KiviError, KiviPagedCache, QKNormRope, rope_table  # noqa: E402
+from bit_kivi_kv_gb300.kivi import (KiviError, KiviPagedCache, QKNormRope, kivi_paged_set_max_ctas,  # noqa: E402
+                                    rope_table)
 from chunk_harness import ChunkRun, head_strided, in_wider, oracle_chunk  # noqa: E402
 from oracle.cache import OracleCache  # noqa: E402
 
@@ -230,6 +231,111 @@ def test_values_that_are_not_finite_reach_only_those_that_see_them():
     keep = torch.ones(300, 2, dtype=torch.bool, device="cuda")
     keep[9, 1] = False
     assert torch.equal(out[keep], clean[keep]) and torch.isnan(out[9, 1]).all()
+
+
+@pytest.mark.parametrize("cached", [0, 3])
+@pytest.mark.parametrize("jump", [12, 17, 24, 25, 26, 29, 33, 40])
+def test_logits_that_jump_within_a_tile(jump, cached):
+    """Weights of up to 2^9 times the reference, then in the same tile one that raises it by 2^jump."""
+    run = ChunkRun(1, 1, 64, 2, 32, 32, max_seqs=1, seed=jump)
+    s = run.add(cached)
+    q, k, v = run.chunk([300])
+    q.zero_()
+    k.zero_()
+    q[:, :, 0] = 1.0
+    k[150, 0, 0], k[200, 0, 0] = 9.0, float(jump)              # base-2 logits: scale ln 2
+    v[150], v[200] = 60000.0, 0.0
+    run.attend([s], [300], (q, k, v), scale=0.6931471805599453)
+
+
+@pytest.mark.parametrize("D,bits,G", [(128, 2, 32), (64, 4, 64), (128, 8, 128), (128, 4, 32), (64, 2, 32)])
+def test_numbers_up_to_the_largest_fp16(D, bits, G):
+    """Blocks that reach from -65504 to 65504: a step's rounding takes some numbers beyond fp16's range."""
+    run = ChunkRun(4, 2, D, bits, G, G, max_seqs=2, seed=D + bits + G)
+    g = torch.Generator(device="cuda").manual_seed(7)
+
+    def wide(*shape):
+        x = (30000 * torch.randn(*shape, generator=g, device="cuda")).clamp(-65504, 65504)
+        ends = torch.rand(*shape, generator=g, device="cuda")
+        return torch.where(ends < 0.05, -65504.0, torch.where(ends > 0.95, 65504.0, x)).half()
+
+    s = run.add(700, (wide(2, 700, D), wide(2, 700, D)))
+    t = run.add(300, (wide(2, 300, D), torch.full((2, 300, D), 65504.0, device="cuda").half()))
+    hat = run.live[s].keys_hat()
+    assert hat.max() >= 65520 and torch.isinf(torch.from_numpy(hat).half()).any()
+    for n in (1, 70, 300):
+        q = torch.randn(n + 5, 4, D, generator=g, device="cuda").half()
+        v = torch.cat([wide(n, 2, D), torch.full((5, 2, D), 65504.0, device="cuda").half()])
+        run.attend([s, t], [n, 5], (q, wide(n + 5, 2, D), v), scale=2.0 ** -17, deq_step=2.0 ** -10)
+        run.attend([t, s], [n, 5], (q, wide(n + 5, 2, D), v), scale=2.0 ** -17, window=250, deq_step=2.0 ** -10)
+
+
+@pytest.mark.parametrize("bits,G,nq", [(2, 32, 1), (4, 64, 4), (8, 128, 2)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_quantized_values_that_are_not_finite_outside_the_window(bits, G, nq, value):
+    run = ChunkRun(2 * nq, 2, 128, bits, G, G, max_seqs=3, seed=bits)
+    K, V, _ = run.draw(1000)
+    seqs = [run.cache.add(K, V)]
+    for x in (K, V):
+        bad = x.clone()
+        bad[:, 500, 3] = value
+        seqs.append(run.cache.add(bad if x is K else K, bad if x is V else V))
+    data = run.chunk([300])
+    # row i sees the tokens behind 1000 + i - 600
+    clean, by_key, by_value = (run.attend([s], [300], data, window=600, check=False) for s in seqs)
+    assert torch.isfinite(clean).all()
+    # (a NaN leaves no trace in a quantized block: its extremes are taken over the numbers)
+    lost_key = not torch.isfinite(run.cache.read([seqs[1]], 500, 1)[0]).all()
+    lost_value = not torch.isfinite(run.cache.read([seqs[2]], 500, 1)[1]).all()
+    assert lost_key == lost_value == (value == float("inf"))
+    seen = by_value[:100]
+    assert (torch.isnan(seen) if lost_value else torch.isfinite(seen)).all() and torch.equal(by_value[100:], clean[100:])
+    block = 500 // G * G + G                                    # (a key's step is its block's)
+    seen = torch.isfinite(by_key[:100])
+    assert seen.all() if not lost_key else not seen.all(-1).any()
+    assert torch.equal(by_key[block - 400:], clean[block - 400:])
+    assert torch.isnan(run.attend([seqs[2]], [300], data, check=False)).all() == lost_value
+
+
+def test_more_groups_of_few_rows_than_a_call_takes():
+    """A sequence without tokens goes to the wide kernel: what it would have had of the groups is another's."""
+    run = ChunkRun(2, 2, 64, 2, 32, 32, max_seqs=67, n_pages=200, seed=6)
+    seqs = [run.add(0)] + [run.add(70) for _ in range(66)]
+    run.attend(seqs, [1] + [16] * 64 + [3, 16])
+
+
+def test_capped_grid():
+    run = ChunkRun(8, 2, 128, 2, 32, 128, max_seqs=3, seed=12)
+    seqs = [run.add(L) for L in (400, 1000, 90)]
+    data = run.chunk([30, 400, 2])
+    for most in (1, 3, 7, 0):
+        kivi_paged_set_max_ctas(run.cache.handle, most)
+        run.attend(seqs, [30, 400, 2], data)
+
+
+def test_captured_few_rows_and_appends():
+    """Single tokens and a few rows, captured and replayed twice on one workspace of each graph; between the replays the
+    cache goes on as the calls outside the graphs leave it."""
+    run = ChunkRun(8, 2, 128, 4, 64, 64, max_seqs=3, seed=13)
+    c = run.cache
+    seqs = [run.add(L) for L in (400, 1000, 1)]
+    sets = [(lens, run.chunk(lens)) for lens in ([1, 1, 1], [2, 4, 3], [1, 40, 2])]
+    refs = [run.attend(seqs, lens, data) for lens, data in sets]
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in sets], []
+    for graph, (lens, data) in zip(graphs, sets):
+        with torch.cuda.graph(graph):
+            outs.append(c.chunk_attn(seqs, lens, *data))
+    side = [torch.cuda.Stream() for _ in sets]
+    for _ in range(2):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for stream, graph in zip(side, graphs):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for o, ref in zip(outs, refs):
+            assert torch.equal(o, ref)
 
 
 def test_wrapper_streams_graphs_and_extend():
