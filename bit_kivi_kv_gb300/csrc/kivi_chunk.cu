@@ -69,6 +69,57 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& a, const MergeJob& jo
         *reinterpret_cast<uint32_t*>(out + 64 * d + 2 * lane) = pack_out(o[d].x * inv, o[d].y * inv);
 }
 
+// The same for rows r and r + step of an item of kFewParts parts at most, the commonest: everything is loaded at once,
+// whatever its weight.
+constexpr int kFewParts = 4;
+template <int D>
+__device__ __forceinline__ void merge_rows(const ChunkArgs& a, const MergeJob& job, int c, int r0, int step, int lane) {
+    constexpr int S = chunk_partial_stride(D);
+    const int n = job.parts, nq = a.plan.nq;
+    float2 ml[2][kFewParts], x[2][kFewParts][D / 64];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int p = 0; p < kFewParts; ++p) {
+            ml[k][p] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d) x[k][p][d] = make_float2(0.f, 0.f);
+            const int r = r0 + k * step;
+            if (p < n && r < job.rows) {
+                const float* src = a.ws + (((long long)(c - 1 + p) * 2 + (p == 0)) * kRows + r) * S;
+                ml[k][p] = *reinterpret_cast<const float2*>(src + D);
+#pragma unroll
+                for (int d = 0; d < D / 64; ++d) x[k][p][d] = *reinterpret_cast<const float2*>(src + 64 * d + 2 * lane);
+            }
+        }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = r0 + k * step;
+        float top = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int p = 0; p < kFewParts; ++p) top = fmaxf(top, ml[k][p].x);
+        float2 o[D / 64];
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d) o[d] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < kFewParts; ++p) {
+            const float w = ml[k][p].x == -INFINITY ? 0.f : exp2f(ml[k][p].x - top);   // (a part that is marked: NaN)
+            l = fmaf(w, ml[k][p].y, l);
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d) {
+                o[d].x = fmaf(w, x[k][p][d].x, o[d].x);
+                o[d].y = fmaf(w, x[k][p][d].y, o[d].y);
+            }
+        }
+        if (r >= job.rows) return;
+        const float inv = 1.f / l;
+        __half* out = a.out + (long long)(job.tok + r / nq) * a.out_stride[0] + (job.head * nq + r % nq) * a.out_stride[1];
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d)
+            *reinterpret_cast<uint32_t*>(out + 64 * d + 2 * lane) = pack_out(o[d].x * inv, o[d].y * inv);
+    }
+}
+
 // Block (x, y): the item that CTA x + 1's first span continues, if CTA x began it; every gridDim.y-th eight of its
 // rows.  (The main kernel leaves the jobs: found anew in each block, by division and search, they took 33 us of a call
 // of 75.)
@@ -79,8 +130,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_merge_kernel(const __gr
     const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
     const MergeJob job = a.jobs[c];
     if (!job.parts) return;
-    for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < job.rows; r += gridDim.y * kJoinWarps)
-        merge_row<D>(a, job, c, r, lane);
+    const int step = gridDim.y * kJoinWarps;
+    int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+    if (job.parts <= kFewParts)
+        for (; r < job.rows; r += 2 * step) merge_rows<D>(a, job, c, r, step, lane);
+    else
+        for (; r < job.rows; r += step) merge_row<D>(a, job, c, r, lane);
 }
 
 // Rows of the groups as the query heads of a single-token call; rows that a group lacks are zeros.

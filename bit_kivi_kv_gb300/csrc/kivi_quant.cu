@@ -157,6 +157,10 @@ struct ChunkQuantArgs {
 };
 
 constexpr int kDense = 0, kPaged = 1, kChunk = 2;   // where a block's rows are and where it goes
+// A chunk completes few blocks, whose CTAs run at once: a block's keys and its values are CTAs of their own (blockIdx.z).
+constexpr int kChunkQuantThreads = 256;
+template <int MODE>
+constexpr int quant_threads = MODE == kChunk ? kChunkQuantThreads : kQuantThreads;
 template <int MODE>
 struct QuantArgsOf { using type = QuantArgs; };
 template <>
@@ -171,8 +175,9 @@ struct QuantArgsOf<kChunk> { using type = ChunkQuantArgs; };
 // coordinates of its codes (and, for keys, their steps and zeros) are fixed
 // once per block.
 template <int D, int BITS, int G, int MODE>
-__global__ void __launch_bounds__(kQuantThreads)
+__global__ void __launch_bounds__(quant_threads<MODE>)
     quantize_blocks_kernel(const __grid_constant__ typename QuantArgsOf<MODE>::type a) {
+    constexpr int kThreads = quant_threads<MODE>;
     constexpr int L = (1 << BITS) - 1;
     constexpr int W = D * BITS / 64;        // words per lane per tile
     constexpr int PER = 16 / BITS;          // code pairs per word
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(kQuantThreads)
         blk_v = a.new_v + ((long long)jb.tok0 - split) * new_v + h * a.v_stride[1];
         part_k = a.pool + ((long long)jb.page * a.Hkv + h) * 2 * a.part_bytes;
         part_v = part_k + a.part_bytes;
-        if (h == 0 && tid == 0) a.table[jb.tbl_idx] = jb.page;
+        if (h == 0 && tid == 0 && blockIdx.z == 0) a.table[jb.tbl_idx] = jb.page;
     } else if constexpr (MODE == kPaged) {
         const QJob& jb = a.jobs[blockIdx.x];
         const int h = blockIdx.y;
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     const long long tiles_bytes = (long long)TPB * a.tile_bytes;
     auto stage_rows = [&](const __half* src, const __half* old, long long step) {
         const uint4* s4 = reinterpret_cast<const uint4*>(src);
-        for (int v = tid; v < G * D / 8; v += kQuantThreads) {
+        for (int v = tid; v < G * D / 8; v += kThreads) {
             const int row = v / (D / 8), c8 = v - row * (D / 8);
             if constexpr (MODE == kChunk) s4 = reinterpret_cast<const uint4*>(row < split ? old + row * D : src + row * step);
             *reinterpret_cast<uint4*>(xs + row * DP + 8 * c8) = s4[MODE == kChunk ? c8 : v];
@@ -238,12 +243,13 @@ __global__ void __launch_bounds__(kQuantThreads)
     };
 
     // ---------------- keys: per channel over the block's G tokens ----------------
+    if (MODE != kChunk || blockIdx.z == 0) {
     stage_rows(blk_k, old_k, new_k);
     __syncthreads();
     // min / max of channel pairs (2cp, 2cp+1) over the G tokens on fp16 pairs (exact);
     // adjacent threads take alternate blocks of 4 tokens (rows 4 apart fall 16
     // banks apart, so the pair's reads do not conflict) and combine
-    for (int idx = tid; idx < D; idx += kQuantThreads) {
+    for (int idx = tid; idx < D; idx += kThreads) {
         const int cp = idx >> 1, half = idx & 1;
         __half2 mn2 = __half2half2(__ushort_as_half(0x7C00)), mx2 = __half2half2(__ushort_as_half(0xFC00));
         for (int jt = 0; jt < G / 2; ++jt) {
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(kQuantThreads)
         // warp takes one word column (wl) of all 32 lanes, so its rows (tokens g,
         // g + 8) and channel pairs fall in distinct banks.
         using PP = PairPlace<BITS, false>;
-        for (int wt = tid; wt < TILE_WORDS; wt += kQuantThreads) {
+        for (int wt = tid; wt < TILE_WORDS; wt += kThreads) {
             const int lane = wt & 31, wl = wt >> 5;
             const int g = lane >> 2, i = lane & 3;
             int off[PER];
@@ -298,7 +304,7 @@ __global__ void __launch_bounds__(kQuantThreads)
             }
         }
     } else
-    for (int wt = tid; wt < TILE_WORDS; wt += kQuantThreads) {
+    for (int wt = tid; wt < TILE_WORDS; wt += kThreads) {
         using PP = PairPlace<BITS, false>;
         const int lane = wt / W, wl = wt - lane * W;
         const int g = lane >> 2, i = lane & 3;
@@ -326,7 +332,9 @@ __global__ void __launch_bounds__(kQuantThreads)
             reinterpret_cast<uint32_t*>(part_k)[tt * TILE_WORDS + wt] = word;
         }
     }
+    if (MODE == kChunk) return;
     __syncthreads();
+    }
 
     // ---------------- values: per token over groups of G channels ----------------
     stage_rows(blk_v, old_v, new_v);
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     const int ngrp = D / G;                 // channel groups per token; G * ngrp == D entries
     long long vfirst = 0;                   // slot position of the block's first token (value limit)
     if constexpr (MODE == kDense) vfirst = (a.first_block + (long long)blockIdx.x) * G;
-    for (int e = tid; e < D; e += kQuantThreads) {
+    for (int e = tid; e < D; e += kThreads) {
         const int t = e / ngrp, gr = e % ngrp;
         const __half* row = xs + t * DP + gr * G;
         __half2 mn2 = __half2half2(__ushort_as_half(0x7C00)), mx2 = __half2half2(__ushort_as_half(0xFC00));
@@ -371,7 +379,7 @@ __global__ void __launch_bounds__(kQuantThreads)
         // one channel of two consecutive tokens, compared with the tokens'
         // thresholds; a warp takes one word column of all 32 lanes
         using PP = PairPlace<BITS, true>;
-        for (int wt = tid; wt < TILE_WORDS; wt += kQuantThreads) {
+        for (int wt = tid; wt < TILE_WORDS; wt += kThreads) {
             const int lane = wt & 31, wl = wt >> 5;
             const int g = lane >> 2, i = lane & 3;
             // the word's channels 16k + g (+8), k in {2wl, 2wl+1}, lie in one group of
@@ -406,7 +414,7 @@ __global__ void __launch_bounds__(kQuantThreads)
             }
         }
     } else
-    for (int wt = tid; wt < TILE_WORDS; wt += kQuantThreads) {
+    for (int wt = tid; wt < TILE_WORDS; wt += kThreads) {
         using PP = PairPlace<BITS, true>;
         const int lane = wt / W, wl = wt - lane * W;
         const int g = lane >> 2, i = lane & 3;
@@ -532,7 +540,7 @@ cudaError_t launch_q(const typename QuantArgsOf<MODE>::type& a, const Geometry& 
     const size_t smem = (size_t)g.G * (g.D + 8) * 2 + 16 * (size_t)g.D + 6 * (size_t)g.D;
 #define KIVI_Q(DD, BB, GG)                                                                      \
     if (g.D == DD && g.bits == BB && g.G == GG) {                                               \
-        quantize_blocks_kernel<DD, BB, GG, MODE><<<grid, kQuantThreads, smem, st>>>(a);        \
+        quantize_blocks_kernel<DD, BB, GG, MODE><<<grid, quant_threads<MODE>, smem, st>>>(a);  \
         return cudaGetLastError();                                                              \
     }
 #define KIVI_QG(DD, BB) KIVI_Q(DD, BB, 32) KIVI_Q(DD, BB, 64) if (DD >= 128) { KIVI_Q(128, BB, 128) }
@@ -602,7 +610,7 @@ cudaError_t launch_quantize_chunk(const PagedGeometry& pg, uint8_t* buf, const _
     for (int j0 = 0; j0 < n; j0 += kMaxChunkJobs) {
         const int nj = n - j0 < kMaxChunkJobs ? n - j0 : kMaxChunkJobs;
         for (int j = 0; j < nj; ++j) a.jobs[j] = jobs[j0 + j];
-        const cudaError_t e = launch_q<kChunk>(a, g, dim3((unsigned)nj, (unsigned)g.Hkv), st);
+        const cudaError_t e = launch_q<kChunk>(a, g, dim3((unsigned)nj, (unsigned)g.Hkv, 2), st);
         if (e != cudaSuccess) return e;
         ++*launches;
     }
