@@ -157,10 +157,23 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const __grid_constant_
     reinterpret_cast<uint4*>(a.gathered)[x] = v;
 }
 
+template <int C>
+__device__ __forceinline__ void load_row(const float* src, float (&x)[C]) {
+    if constexpr (C == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        x[0] = v.x; x[1] = v.y;
+    }
+}
+
 // A warp per row: the partial results over the cached tokens, and the row's new tokens up to its own.
 template <int D>
 __global__ void __launch_bounds__(128) group_merge_kernel(const __grid_constant__ GroupArgs a) {
     constexpr int S = partial_stride(D), C = D / 32;           // channels a lane holds
+    constexpr int kAhead = 8;
+    static_assert(S % 4 == 0, "16-byte loads");
     griddepcontrol_wait();
     griddepcontrol_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -192,39 +205,44 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const __grid_constant_
 #pragma unroll
     for (int c = 0; c < C; ++c) q[c] *= a.scale_log2;
     // weights of the partials, three a lane
-    float w[3], top = -INFINITY, l = 0.f;
+    float w[3], lw[3], top = -INFINITY, l = 0.f;
     bool bad = false;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         const int i = lane + 32 * k;
         w[k] = -INFINITY;
+        lw[k] = 0.f;
         if (i < n) {
-            w[k] = base[i * S];
-            bad |= base[i * S + 2] != 0.f;
+            const float4 head = *reinterpret_cast<const float4*>(base + i * S);
+            w[k] = head.x;
+            lw[k] = head.y;
+            bad |= head.z != 0.f;
         }
         top = fmaxf(top, w[k]);
     }
     top = warp_max(top);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        const int i = lane + 32 * k;
         w[k] = w[k] == -INFINITY ? 0.f : exp2f(w[k] - top);
-        if (w[k] != 0.f) l += w[k] * base[i * S + 1];
+        if (w[k] != 0.f) l += w[k] * lw[k];
     }
     l = warp_sum(l);
     float o[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) o[c] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float f = __shfl_sync(kFull, i < 32 ? w[0] : i < 64 ? w[1] : w[2], i & 31);
-        const float* src = base + i * S + 4 + C * lane;
-        if (f == 0.f) continue;                                // (an empty partial's values are not written)
+    for (int i0 = 0; i0 < n; i0 += kAhead) {                   // (loads that wait for no weight)
+        float x[kAhead][C];
 #pragma unroll
-        for (int c = 0; c < C; c += 2) {
-            const float2 x = *reinterpret_cast<const float2*>(src + c);
-            o[c] = fmaf(f, x.x, o[c]);
-            o[c + 1] = fmaf(f, x.y, o[c + 1]);
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u < n) load_row<C>(base + (i0 + u) * S + 4 + C * lane, x[u]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u;
+            if (i >= n) break;
+            const float f = __shfl_sync(kFull, i < 32 ? w[0] : i < 64 ? w[1] : w[2], i & 31);
+            if (f == 0.f) continue;                            // (an empty partial's values are not written)
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[c] = fmaf(f, x[u][c], o[c]);
         }
     }
     const __half* kp = a.k + p.tok0 * a.k_stride[0] + h * a.k_stride[1];
