@@ -70,7 +70,7 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& a, const MergeJob& jo
 }
 
 // The same for rows r and r + step of an item of kFewParts parts at most, the commonest: everything is loaded at once,
-// whatever its weight.
+// whatever its weight (three chunks of up to 777 tokens of 16 heads, a call of 108 us: 100).
 constexpr int kFewParts = 4;
 template <int D>
 __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const MergeJob& job, int c, int r0, int step, int lane) {

@@ -157,7 +157,8 @@ struct ChunkQuantArgs {
 };
 
 constexpr int kDense = 0, kPaged = 1, kChunk = 2;   // where a block's rows are and where it goes
-// A chunk completes few blocks, whose CTAs run at once: a block's keys and its values are CTAs of their own (blockIdx.z).
+// A chunk completes few blocks, whose CTAs run at once: a block's keys and its values are CTAs of their own (blockIdx.z),
+// of more threads (64 blocks of 128 tokens of 8 heads: a call of 72 us takes 67.9 with 128 threads, 54.5 with 256, 53.5 with 512).
 constexpr int kChunkQuantThreads = 256;
 template <int MODE>
 constexpr int quant_threads = MODE == kChunk ? kChunkQuantThreads : kQuantThreads;
