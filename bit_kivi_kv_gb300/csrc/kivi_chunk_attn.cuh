@@ -807,14 +807,17 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
         const int steps = sp->tiles(x), tile0 = sp->tile0;
         // queries into the operand (the same rows: A loads them, for both)
         if (both || x == 0) {
-            const __half* src = a.q + (long long)(sp->tok0 + sp->t0 + (r >> lgq)) * a.q_stride[0] +
-                                ((sp->head << lgq) + (r & ((1 << lgq) - 1))) * a.q_stride[1];
+            constexpr int LPR = D / 8, RPI = 32 / LPR;         // lanes a row, rows an instruction
+            const int lr = lane % LPR, sub = lane / LPR;
+            const __half* first = a.q + (long long)(sp->tok0 + sp->t0) * a.q_stride[0] + (sp->head << lgq) * a.q_stride[1] + 8 * lr;
             const uint32_t dst = smem + S::OFF_Q + x * S::Q_BYTES;
-            uint4 v[D / 8];                                    // (all loads in flight)
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) v[c] = r < n_rows ? ldg_row(src + 8 * c) : uint4{0, 0, 0, 0};
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) sts128(dst + operand_at<kHalf>(row, c), v[c]);
+#pragma unroll 4
+            for (int h = 0; h < 32; h += RPI) {
+                const int to_row = row - lane + h + sub, from = r - lane + h + sub;
+                const long long at = (long long)(from >> lgq) * a.q_stride[0] + (from & ((1 << lgq) - 1)) * a.q_stride[1];
+                cp_async16_or_zero(dst + operand_at<kHalf>(to_row, lr), first + (from < n_rows ? at : 0), from < n_rows);
+            }
+            cp_async_wait_all();
             fence_proxy_async();
         }
         if (both) tile_sync(x);
@@ -842,11 +845,12 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
             if (ok && any) {
                 // (loops over a tile's columns stay loops: unrolled, the roles' code misses the instruction cache)
                 const bool cut = key0 + kTile - 1 > w_hi || key0 < w_lo;
-                if (MOD || cut) {                              // logits other than mul * S: written back as such
+                if (MOD || cut) {                              // logits other than mul * S, hidden ones: written back as such
                     const int hi = p0 + (r >> lgq), lo = a.plan.window ? hi - a.plan.window + 1 : 0;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         float v[32];
+                        if (!MOD && key0 + 32 * c + 31 <= w_hi && key0 + 32 * c >= w_lo) continue;   // (all rows see all)
                         ld32(ts + 32 * c, v);
                         wait_ld(v);
                         const int d = key0 + 32 * c - hi;      // key less position of the first column
@@ -855,7 +859,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
                                 v[j] = fmaf(-2.f * cap_out, rcp_ftz(exp2_ftz(v[j] * cap_in) + 1.f), cap_out);
-                        } else {
+                        } else if (MOD) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v[j] *= a.scale_log2;
                         }
@@ -872,7 +876,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                         st32(ts + 32 * c, v);
                     }
                     wait_st();
-                    mul = 1.f;
+                    if (MOD) mul = 1.f;
                 }
                 // Half a tile at a time: the weights by the present reference are kept in registers until their sum
                 // has shown that each is in range (64 of 2^5 are 2^11); a reference that is
