@@ -598,7 +598,9 @@ template <int D, int BITS>
 __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t smem, bool values, int w, int lane) {
     using S = Shape<D, BITS>;
     constexpr int W = S::W, TILE = S::TILE;
-    const uint32_t full = bars + (values ? BAR(v_full) : BAR(k_full)), empty = bars + (values ? BAR(v_empty) : BAR(k_empty));
+    const uint32_t full = bars + (values ? BAR(v_full) : BAR(k_full));
+    constexpr uint32_t kEmpty = BAR(k_empty) - BAR(k_full);
+    static_assert(kEmpty == BAR(v_empty) - BAR(v_full), "the same for both");
     const uint32_t ent = smem + S::OFF_ENT + (4 * values + w) * (4 * D);
     const uint32_t stages = smem + (values ? S::OFF_V : S::OFF_K);
     const int lgG = a.lgG, ve = 64 * (D >> lgG);               // bytes of value entries of a code tile
@@ -606,14 +608,13 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
     // A step of 2^(15 - BITS) or a zero of 2^15 and more (a bit 15 after the addition), without which no number of a unit
     // is beyond fp16's range.
     const int run = values ? ve / 16 : 4 * D / 16;             // 16-byte groups: half of them steps, half zeros, ..
-    const uint32_t large = (0x0800u + (min(lane, last_ent) % run < run / 2 ? BITS * 0x0400u : 0u)) * 0x00010001u;
+    const bool steps_lane = min(lane, last_ent) % run < run / 2;
     SpanReader reader(b, bars);
     // the unit ahead: its bytes where it is quantized
     const Span* sp = nullptr;
-    int t = 0, t_end = 0, n_quant = 0;
+    int t = 0, t_end = 0;                                      // (of the span the rest is read again: registers)
     bool quantized = false;
     int have = 0, entry = 0;                                   // table entries of tiles have .. have + 31, one a lane
-    const uint8_t* base = nullptr;                             // page 0's part
     Words<W> words;
     uint4 ents{};
     auto ahead = [&]() {
@@ -623,11 +624,9 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
             if (!sp) return;
             t = sp->tile0;
             t_end = t + sp->nt;
-            n_quant = sp->n_quant;
-            base = a.buf + (2 * sp->head + values) * a.part_bytes;
             fresh = true;
         }
-        const int key0 = t * kTile + 32 * w;
+        const int key0 = t * kTile + 32 * w, n_quant = sp->n_quant;
         quantized = key0 < n_quant;
         if (!quantized) return;
         if (fresh || t >= have + 32) {
@@ -640,7 +639,8 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
             page = 0;
             if (lane == 0) atomicOr(&b.bad, reader.mark());
         }
-        const uint8_t* part = base + (unsigned long long)(unsigned)page * (unsigned)a.page_bytes;   // (a page: under 2^32 bytes)
+        const uint8_t* part = a.buf + (unsigned long long)(unsigned)page * (unsigned)a.page_bytes +   // (a page: under 2^32 bytes)
+                              (unsigned)(2 * sp->head + values) * (unsigned)a.part_bytes;
         const int tile = (key0 & ((1 << lgG) - 1)) >> 4;
         ents = ldg_stream(part + (TILE << (lgG - 4)) + (values ? tile * ve : 0) + 16 * min(lane, last_ent));
         load_unit<W, TILE>(part + tile * TILE + lane * (4 * W), words);
@@ -649,8 +649,9 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
     for (uint32_t tc = 0; sp; ++tc) {
         const uint32_t stage = tc & 1, ph = (tc >> 1) & 1;
         const uint32_t dst = stages + stage * S::K_BYTES;
-        const bool ok = __all_sync(kFull, wait_for(bars, empty + 8 * stage, ph ^ 1));
+        const bool ok = __all_sync(kFull, wait_for(bars, full + kEmpty + 8 * stage, ph ^ 1));
         if (quantized) {
+            const uint32_t large = steps_lane ? (0x0800u + BITS * 0x0400u) * 0x00010001u : 0x08000800u;
             auto over = [&](uint32_t v) { return (v & 0x7fff7fffu) + large; };
             const bool mend = __any_sync(kFull, ((over(ents.x) | over(ents.y) | over(ents.z) | over(ents.w)) & 0x80008000u) != 0u);
             if (lane <= last_ent) sts128(ent + 16 * lane, ents);
@@ -667,7 +668,7 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
             const long long step = values ? a.v_stride[0] : a.k_stride[0], per_head = values ? a.v_stride[1] : a.k_stride[1];
             const Rows r{reinterpret_cast<const __half*>(a.buf + resid) + ((long long)sp->seq * a.plan.Hkv + sp->head) * a.R * D,
                          (values ? a.v : a.k) + sp->tok0 * step + sp->head * per_head, step, sp->n_resid, sp->n_resid + sp->t1};
-            const int f0 = t * kTile + 32 * w - n_quant;
+            const int n_quant = sp->n_quant, f0 = t * kTile + 32 * w - n_quant;
             bool odd = false;
             if (!values || t * kTile >= n_quant) {
                 plain_rows<D>(r, f0, dst, 32 * w, lane);
