@@ -15,13 +15,13 @@ namespace kivi {
 // tile, one of fewer rows of one; both dequantize it, so their tiles weigh 4 and 3 (with 2
 // and 1, of a chunk of 5 whole items and 52 rows over 131072 tokens of 8 heads the CTAs that
 // held the 52 rows took twice as long as the others: 929 us, 798 with 4 and 3).  An item's
-// tiles come after a lead of weight 16, for what a CTA does once for it (queries in, outputs
-// out; a prompt of 8192 tokens of 32 heads over 8: 1134 us without a lead, 679 with 6, 650 with 10, 599 with 14, 576 with
-// 16, 580 with 20, 583 with 28).  Items are in the order sequence, item of the chunk, kv head; CTA c of n takes
+// tiles come after a lead of weight 14, for what a CTA does once for it (queries in, outputs
+// out; a prompt of 8192 tokens of 32 heads over 8: 618 us with a lead of 8, 556 with 11, 533 with 14, 534 with 16, 535 with
+// 19; chunks of 777 tokens of 16 heads at most, 64 channels: 96, 99, 98, 98, 106).  Items are in the order sequence, item of the chunk, kv head; CTA c of n takes
 // the tiles that start in weights [c W / n, (c + 1) W / n).  A CTA that holds all of an item's
 // tiles writes its outputs, others partial results, which a merge joins.
 constexpr int kRows = 256, kHalf = 128, kTile = 128;
-constexpr int kBothWeight = 4, kHalfWeight = 3, kItemLead = 16;
+constexpr int kBothWeight = 4, kHalfWeight = 3, kItemLead = 14;
 constexpr int kMaxChunkCtas = 192;       // most CTAs of a call (one per SM)
 
 struct ChunkSeq {

@@ -37,7 +37,7 @@
 //
 // Bound by the warps' instructions: a tile of 128 keys by 256 rows takes some 4400 cycles (2650 warp instructions a
 // scheduler), its 32 MMAs 2050 of them.  512 new tokens of each of 8 sequences over 4096 (32 heads of 128, 2 bits):
-// 342 us, 854 TFLOP/s; a prompt of 8192 tokens: 563 us, 976.
+// 328 us, 889 TFLOP/s; a prompt of 8192 tokens: 533 us, 1030.
 //
 // Roundings: keys and values to fp16 (half a step of 2^-10), probabilities to
 // fp16, scaled so that 2^4 at least stands for the row's largest: what falls below fp16's
