@@ -65,8 +65,9 @@ namespace chunk_detail {
 using namespace mma_detail;
 
 constexpr int kChunkWarps = 20, kChunkThreads = 32 * kChunkWarps;
-// Registers a thread: the launch's, and what the five warpgroups (A, B, keys, values, the rest) make of them: none
-// of the roles spills (8 bits: a unit's words alone take 32, a few values of the filling warps do).
+// Registers a thread: the launch's, and what the five warpgroups (A, B, keys, values, the rest) make of them.  2 bits:
+// none of the roles that repeat spills; 4 bits: one value of the filling warps; 8 bits, whose words of a unit alone take
+// 32: a few.
 constexpr int kRegs = 96;
 template <int BITS>
 struct Regs {
