@@ -43,7 +43,7 @@ def test_workspace_size(K):
     cfg = K.make_paged_config(6, 8, 4, 64, 2, 32, 64, 16, 32)
     wide, group = 192 * (2 * 256 * 68 * 4 + 16), 4 * 4 * 64 * 2 + 4 * 4 * 65 * 68 * 4
     # (2 query heads per kv head: 16 rows are 8 tokens, 4 rows a group)
-    for lens, groups in (([9], 0), ([1], 1), ([2], 1), ([3, 8], 6), ([0, 100, 5], 3), ([8] * 200, 512)):
+    for lens, groups in (([9], 0), ([1], 1), ([2], 1), ([3, 8], 6), ([0, 100, 5], 3), ([8] * 200, 512), ([1] + [8] * 128, 512)):
         assert K.kivi_paged_chunk_workspace_bytes(cfg, lens) == wide + groups * group
     assert K.kivi_paged_chunk_workspace_bytes(cfg, []) == 0 and K.kivi_paged_chunk_workspace_bytes(cfg, [1] * 513) == 0
     assert K.kivi_paged_chunk_workspace_bytes(K.make_paged_config(6, 8, 4, 96, 2, 32, 64, 16, 32), [1]) == 0

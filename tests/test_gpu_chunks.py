@@ -299,9 +299,9 @@ def test_quantized_values_that_are_not_finite_outside_the_window(bits, G, nq, va
 
 def test_more_groups_of_few_rows_than_a_call_takes():
     """A sequence without tokens goes to the wide kernel: what it would have had of the groups is another's."""
-    run = ChunkRun(2, 2, 64, 2, 32, 32, max_seqs=67, n_pages=200, seed=6)
-    seqs = [run.add(0)] + [run.add(70) for _ in range(66)]
-    run.attend(seqs, [1] + [16] * 64 + [3, 16])
+    run = ChunkRun(2, 2, 64, 2, 32, 32, max_seqs=131, n_pages=300, seed=6)
+    seqs = [run.add(0)] + [run.add(70) for _ in range(130)]
+    run.attend(seqs, [1] + [16] * 128 + [3, 16])              # (four groups each: 512 in all)
 
 
 def test_capped_grid():
