@@ -282,7 +282,7 @@ cudaError_t launch_store_tail(const PagedGeometry& pg, uint8_t* buf, const __hal
 struct ForkJob {
     int from, to, n_blocks, n_resid;
 };
-cudaError_t launch_fork(const PagedGeometry& pg, uint8_t* buf, const ForkJob* jobs, int n, cudaStream_t st);
+cudaError_t launch_fork(const PagedGeometry& pg, uint8_t* buf, const ForkJob* jobs, int n, cudaStream_t st, int* launches);
 
 // Tokens [first, first + count) of each sequence as fp16 [n][Hkv][count][D].
 cudaError_t launch_read(const PagedGeometry& pg, const uint8_t* buf, const RowSeq* seqs, int n, long long first,

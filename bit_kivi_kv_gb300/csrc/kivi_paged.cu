@@ -842,9 +842,10 @@ kivi_status kivi_paged_fork(kivi_paged_t c, const int* seqs, int n, int* out, ki
         return failf(KIVI_ERR_INVALID_ARG, "out of host memory");
     }
     if (any) {
-        const cudaError_t e = kivi::launch_fork(c->pg, c->buf, jobs, n, reinterpret_cast<cudaStream_t>(stream));
+        int nl = 0;
+        const cudaError_t e = kivi::launch_fork(c->pg, c->buf, jobs, n, reinterpret_cast<cudaStream_t>(stream), &nl);
+        kivi::count_launches(nl);
         if (e != cudaSuccess) return cuda_fail(e, "fork launch");
-        kivi::count_launches(1);
     }
     for (int i = 0; i < n; ++i) {
         SeqState& to = c->seqs[(size_t)jobs[i].to];

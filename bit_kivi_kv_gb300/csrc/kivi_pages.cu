@@ -61,11 +61,24 @@ struct ForkArgs {
     ForkJob jobs[kMaxCallSeqs];
 };
 
-// CTA (h, i): kv head h of branch i: its residual rows, and every Hkv-th run of 256 table entries.
-// Launched in stream order, and it lets no dependent start early: a decode call reads the table
-// before it waits for the kernel ahead of it.
+// The block-table entries of branch i, by the CTAs (x, i).  It gives no signal to start its dependent early: the next
+// kernel waits until these stores are there.
+__global__ void __launch_bounds__(256) fork_table_kernel(const __grid_constant__ ForkArgs a) {
+    griddepcontrol_wait();
+    const ForkJob& j = a.jobs[blockIdx.y];
+    const int* ts = a.table + (long long)j.from * a.max_blocks;
+    int* td = a.table + (long long)j.to * a.max_blocks;
+    for (int x = blockIdx.x * 256 + threadIdx.x; x < j.n_blocks; x += 256 * gridDim.x) td[x] = ts[x];
+}
+
+// CTA (h, i): kv head h of branch i: its residual rows.  A launch of its own, behind the table's: a decode call reads
+// the table ahead of its wait for the kernel before it, so that kernel may write residual rows and no table entry.
+// (One kernel for both that sends no signal is not enough: a dependent then starts when the CTAs have exited, and
+// only its wait makes their stores visible.)
 template <int D>
-__global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ ForkArgs a) {
+__global__ void __launch_bounds__(256) fork_rows_kernel(const __grid_constant__ ForkArgs a) {
+    griddepcontrol_wait();
+    griddepcontrol_launch_dependents();
     const ForkJob& j = a.jobs[blockIdx.y];
     const long long rows = (long long)gridDim.x * a.resid.R * D, head = (long long)blockIdx.x * a.resid.R * D;
     const int n = j.n_resid * (D / 8);
@@ -73,15 +86,12 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ ForkA
     const uint4* sv = reinterpret_cast<const uint4*>(a.resid.v + j.from * rows + head);
     uint4* dk = reinterpret_cast<uint4*>(a.resid.k + j.to * rows + head);
     uint4* dv = reinterpret_cast<uint4*>(a.resid.v + j.to * rows + head);
-    const int* ts = a.table + (long long)j.from * a.max_blocks;
-    int* td = a.table + (long long)j.to * a.max_blocks;
 #pragma unroll 4
     for (int x = threadIdx.x; x < n; x += 256) {
         const uint4 p = sk[x], q = sv[x];
         dk[x] = p;
         dv[x] = q;
     }
-    for (int x = blockIdx.x * 256 + threadIdx.x; x < j.n_blocks; x += 256 * gridDim.x) td[x] = ts[x];
 }
 
 // ---- reading back ----
@@ -226,17 +236,29 @@ cudaError_t launch_store_tail(const PagedGeometry& pg, uint8_t* buf, const __hal
                       : launch_dependent(store_tail_kernel<64>, grid, 256, st, a);
 }
 
-cudaError_t launch_fork(const PagedGeometry& pg, uint8_t* buf, const ForkJob* jobs, int n, cudaStream_t st) {
+cudaError_t launch_fork(const PagedGeometry& pg, uint8_t* buf, const ForkJob* jobs, int n, cudaStream_t st, int* launches) {
     const Geometry& g = pg.g;
     ForkArgs a;
     a.resid = resid_of(g, buf);
     a.table = reinterpret_cast<int*>(buf + pg.table_off);
     a.max_blocks = (int)g.NB;
-    for (int i = 0; i < n; ++i) a.jobs[i] = jobs[i];
+    int most = 0;
+    for (int i = 0; i < n; ++i) {
+        a.jobs[i] = jobs[i];
+        most = jobs[i].n_blocks > most ? jobs[i].n_blocks : most;
+    }
+    *launches = 0;
+    if (most) {
+        const int ctas = (most + 255) / 256;
+        const cudaError_t e = launch_dependent(fork_table_kernel, dim3((unsigned)(ctas < 16 ? ctas : 16), (unsigned)n), 256, st, a);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
     const dim3 grid((unsigned)g.Hkv, (unsigned)n);
-    if (g.D == 128) fork_kernel<128><<<grid, 256, 0, st>>>(a);
-    else fork_kernel<64><<<grid, 256, 0, st>>>(a);
-    return cudaGetLastError();
+    const cudaError_t e = g.D == 128 ? launch_dependent(fork_rows_kernel<128>, grid, 256, st, a)
+                                     : launch_dependent(fork_rows_kernel<64>, grid, 256, st, a);
+    if (e == cudaSuccess) ++*launches;
+    return e;
 }
 
 cudaError_t launch_read(const PagedGeometry& pg, const uint8_t* buf, const RowSeq* seqs, int n, long long first,
