@@ -793,6 +793,17 @@ __device__ __forceinline__ float max16(float m, const float (&v)[16]) {
     return fmaxf(m, n);
 }
 
+// Base-2 logit of a capped score of s = q . k: cap tanh(y) log2(e), y = scale s / cap.  From |y| = 1/4 on tanh(y) is
+// 1 - 2 / (exp(2 y) + 1), off by under 2^-21.5 there, 2^-19.5 of it; below, where that form would lose the score in the
+// one, y times its series up to y^6 (the next term is 62/2835 y^8: 2^-21.5 at 1/4).  So the logit is off by 2^-19 of itself,
+// whatever the cap, and a cap beyond all scores leaves them as they are.
+__device__ __forceinline__ float capped(float s, float y_mul, float scale_log2, float cap_out) {
+    const float y = s * y_mul, y2 = y * y;
+    const float series = fmaf(fmaf(fmaf(-17.f / 315.f, y2, 2.f / 15.f), y2, -1.f / 3.f), y2, 1.f);
+    const float far = fmaf(-2.f * cap_out, rcp_ftz(exp2_ftz(y * (2.f * kLog2e)) + 1.f), cap_out);
+    return fabsf(y) < 0.25f ? s * scale_log2 * series : far;
+}
+
 template <int D, int BITS, bool MOD>
 __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t smem, float2* xch, uint32_t tmem, int x, int warp, int lane) {
     using S = Shape<D, BITS>;
@@ -836,7 +847,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
         const bool any = r0 < n_rows;
         const float slope = MOD && a.slopes && r < n_rows
                                 ? __ldg(a.slopes + (sp->head << lgq) + (r & ((1 << lgq) - 1))) * kLog2e : 0.f;
-        const float cap_in = a.scale * (2.f * kLog2e) / a.cap, cap_out = a.cap * kLog2e;    // (without a cap: not used)
+        const float cap_in = fminf(a.scale / a.cap, 0x1.fffffep127f), cap_out = a.cap * kLog2e;    // (without a cap: not used)
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < steps; ++i) {
             const int key0 = (tile0 + (both ? i : 2 * i + x)) * kTile;
@@ -857,10 +868,8 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                         wait_ld(v);
                         const int d = key0 + 32 * c - hi;      // key less position of the first column
                         if (MOD && a.cap > 0.f) {
-                            // cap tanh(y), tanh(y) = 1 - 2 / (exp(2 y) + 1)
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = fmaf(-2.f * cap_out, rcp_ftz(exp2_ftz(v[j] * cap_in) + 1.f), cap_out);
+                            for (int j = 0; j < 32; ++j) v[j] = capped(v[j], cap_in, a.scale_log2, cap_out);
                         } else if (MOD) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v[j] *= a.scale_log2;

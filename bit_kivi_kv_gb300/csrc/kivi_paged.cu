@@ -721,7 +721,8 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
         a.n_pages = (int)c->pg.n_pages;
         a.scale = scale;
         a.scale_log2 = scale_log2;
-        a.cap = x->cap;
+        // (from 2^-100, below which all scores are 0 to the exponential as well, to 2^126, whose product with log2(e) is in range)
+        a.cap = x->cap > 0.f ? fminf(fmaxf(x->cap, 0x1p-100f), 0x1p126f) : 0.f;
         a.slopes = x->slopes;
         a.ws = static_cast<float*>(workspace);
         a.jobs = reinterpret_cast<kivi::MergeJob*>(a.ws + (size_t)kivi::kMaxChunkCtas * 2 * kivi::kRows *
