@@ -176,6 +176,13 @@ __device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// (the first eight of x)
+__device__ __forceinline__ void st8(uint32_t at, const float (&x)[16]) {
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 // Wait for the loads: what they bring passes through, so that no use of it is moved ahead of the wait.
 __device__ __forceinline__ void wait_ld(float (&x)[16]) {
     uint32_t* r = reinterpret_cast<uint32_t*>(x);
@@ -915,9 +922,28 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                         }
                         const float2 total = unpair(add2(sum[0], sum[1]));
                         const float all = total.x + total.y;
-                        if (!again || !__any_sync(kFull, all >= kMostSum || m == -INFINITY)) {
+                        if (!__any_sync(kFull, all >= kMostSum || (again && m == -INFINITY))) {
                             st32(ts + 32 * h, p);
                             l += all;
+                            break;
+                        }
+                        if (!again) {
+                            // Logits whose neighbours in fp32 are several apart (from 2^24 on): the largest may be far above its
+                            // rounded value, and its weight beyond fp16's range.  It stays 2^15.
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                ld16(from + 16 * c, v);
+                                wait_ld(v);
+#pragma unroll
+                                for (int j = 0; j < 16; j += 2) {
+                                    float y0 = fmaf(v[j], mul, -ref), y1 = fmaf(v[j + 1], mul, -ref);
+                                    y0 = exp2_ftz(y0 > 15.f ? 15.f : y0);      // (NaN stays)
+                                    y1 = exp2_ftz(y1 > 15.f ? 15.f : y1);
+                                    l += y0 + y1;
+                                    u[j / 2] = __uint_as_float(pack_f16x2(y0, y1));
+                                }
+                                st8(ts + 32 * h + 8 * c, u);                   // (over logits that have been read)
+                            }
                             break;
                         }
                         float mx = -INFINITY;
@@ -927,11 +953,13 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
                             wait_ld(v);
                             mx = max16(mx, v);
                         }
-                        mx *= mul;
+                        // (down: the largest weight is 2^4 at least, and under 2^5 where fp32 tells such logits apart)
+                        mx = __fmul_rd(mx, mul);
                         again = false;                         // (the weights by the maximum fit, if there is one)
-                        // raised by a whole number, so that scaling what is there (sums, the first half's weights) is exact
-                        // (down: the largest weight is 2^4 at least then, and under 2^5)
-                        const float top = m == -INFINITY ? mx : m + fmaxf(0.f, floorf(mx - m));
+                        // raised by a whole number, so that scaling what is there (sums, the first half's weights) is exact;
+                        // after a jump beyond fp32's exponents nothing is left of it
+                        const float rise = mx - m;
+                        const float top = m == -INFINITY || rise > 1000.f ? mx : m + fmaxf(0.f, floorf(rise));
                         const float f = m == -INFINITY ? 0.f : exp2_ftz(m - top);
                         m = top;
                         l *= f;
