@@ -115,6 +115,7 @@ struct Bars {
     uint64_t span_full[kSpanRing], span_empty[kSpanRing];
     uint32_t tmem;
     int failed;         // a wait ran out: the outputs from here on are NaN
+    int ended;          // no span comes any more, although none said so
     int busy;           // a tile's MMAs are being issued
     unsigned bad, odd;  // spans with a block-table entry outside the pool, with an fp16 value that is not finite: bit number % 32
     int last_odd[2 * kSpanRing];   // of a span (number % 8): the last quantized token whose value is not finite, or -1
@@ -263,12 +264,37 @@ template <int ID, int N>
 __device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
 
 // Wait for an mbarrier's phase, 2^31 cycles (about a second) at most; a wait that runs out marks the CTA,
-// and no wait of a marked CTA waits, but a patient one (for spans: they keep coming).
+// and no wait of a marked CTA waits, but a patient one (for MMAs in flight at its end).  Each lane has a result of
+// its own: a warp that goes on together takes them together.
 template <bool PATIENT = false>
 __device__ __forceinline__ bool wait_for(uint32_t bars, uint32_t bar, uint32_t parity) {
     const unsigned t0 = (unsigned)clock();
     while (!mbar_try(bar, parity)) {
         if ((unsigned)clock() - t0 < 1u << 31 && (PATIENT || !lds32(bars + BAR(failed)))) continue;
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(bars + BAR(failed)), "r"(1) : "memory");
+        return false;
+    }
+    return true;
+}
+// The waits for spans (a span may take long, its tiles' waits do not).  The warps of a role meet at barriers within a
+// span, so they have to agree whether there is one: the planner's wait alone runs out (2^36 cycles), it tells them that
+// no span comes any more, and a span that is there by then counts.  (Theirs, 2^37 cycles, are for form.)
+__device__ __forceinline__ bool wait_place(uint32_t bars, uint32_t bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity)) {
+        if (clock64() - t0 < 1ll << 36) continue;
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(bars + BAR(failed)), "r"(1) : "memory");
+        __threadfence_block();
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(bars + BAR(ended)), "r"(1) : "memory");
+        return false;
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_span(uint32_t bars, uint32_t bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity)) {
+        if (lds32(bars + BAR(ended))) return mbar_try(bar, parity);
+        if (clock64() - t0 < 1ll << 37) continue;
         asm volatile("st.shared.u32 [%0], %1;" ::"r"(bars + BAR(failed)), "r"(1) : "memory");
         return false;
     }
@@ -536,7 +562,7 @@ inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, uint32_t bars, in
             more = walk.next();
             if (n == 0) a.jobs[blockIdx.x] = more ? merge_job(walk, a.weight, a.n_ctas, blockIdx.x) : MergeJob{0, 0, 0, 0};
             const uint32_t slot = n % kSpanRing;
-            wait_for<true>(bars, bars + BAR(span_empty) + 8 * (slot), ((n / kSpanRing) & 1) ^ 1);
+            if (!wait_place(bars, bars + BAR(span_empty) + 8 * slot, ((n / kSpanRing) & 1) ^ 1)) break;
             Span o;
             o.more = more;
             if (more) {
@@ -584,19 +610,16 @@ struct SpanReader {
     __device__ __forceinline__ uint32_t place() const { return (n - 1) % (2 * kSpanRing); }
     __device__ __forceinline__ SpanReader(const Bars& data, uint32_t at) : b(data), bars(at), n(0) {}
     __device__ __forceinline__ void release() const { arrive(bars + BAR(span_empty) + 8 * ((n - 1) % kSpanRing)); }
-    __device__ __forceinline__ const Span* next() {              // one lane alone, or all of a warp with the same result
-        const uint32_t slot = n % kSpanRing;
-        const bool ok = wait_for<true>(bars, bars + BAR(span_full) + 8 * slot, (n / kSpanRing) & 1);
-        ++n;
-        const Span* s = &b.spans[slot];
-        return ok && s->more ? s : nullptr;
-    }
     __device__ __forceinline__ const Span* next(int lane) {      // a whole warp
         if (n) {
             __syncwarp();
             if (lane == 0) release();
         }
-        return next();
+        const uint32_t slot = n % kSpanRing;
+        const bool ok = __all_sync(kFull, wait_span(bars, bars + BAR(span_full) + 8 * slot, (n / kSpanRing) & 1));
+        ++n;
+        const Span* s = &b.spans[slot];
+        return ok && s->more ? s : nullptr;
     }
 };
 
@@ -881,7 +904,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < steps; ++i) {
             const int key0 = (tile0 + (both ? i : 2 * i + x)) * kTile;
-            const bool ok = wait_for(bars, bars + BAR(s_full) + 8 * (x), sc & 1);
+            const bool ok = __all_sync(kFull, wait_for(bars, bars + BAR(s_full) + 8 * (x), sc & 1));
             float mul = a.scale_log2;
             ++sc;
             fence_after();
@@ -1008,7 +1031,7 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
         // ---- epilogue ----
         bool fine = true;
         if (steps) {
-            fine = wait_for(bars, bars + BAR(o_full) + 8 * (x), oc & 1);
+            fine = __all_sync(kFull, wait_for(bars, bars + BAR(o_full) + 8 * (x), oc & 1));
             ++oc;
         }
         fence_after();
@@ -1129,7 +1152,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             mbar_init(&b.span_full[j], 1);
             mbar_init(&b.span_empty[j], kSpanReaders);
         }
-        b.failed = b.busy = 0;
+        b.failed = b.ended = b.busy = 0;
         b.bad = b.odd = 0;
         fence_mbar_init();
     }

@@ -705,8 +705,10 @@ kivi_status kivi_append_qkv(kivi_cache_t cache, const kivi_qkv* args, kivi_strea
  * marks a block-table entry outside the pool the same way.
  *
  * kivi_decode_blocks' waits and marks are the same.  Every wait of
- * kivi_paged_chunk_attn's kernel is bounded too (2^31 cycles, about 1 s): one that
- * runs out makes the outputs that its CTA still has to write NaN.
+ * kivi_paged_chunk_attn's kernel is bounded too: for a tile's keys, values and
+ * products 2^31 cycles, about 1 s, after which no such wait of the CTA waits any
+ * more; for the next piece of its work 2^36.  One that runs out makes the outputs that
+ * its CTA still has to write NaN.
  *
  * Test hook: KIVI_FAULT_COPY_STALL makes the next tensor-core decode call on
  * this cache (kivi_decode_attn, kivi_append_decode or kivi_decode_blocks) expect 16 bytes more on
