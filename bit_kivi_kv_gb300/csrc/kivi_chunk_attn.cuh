@@ -75,6 +75,7 @@ struct Regs {
     static_assert(2 * SOFTMAX + 2 * FILL + REST <= 5 * kRegs, "registers of the launch");
 };
 constexpr int kSpanRing = 4, kSpanReaders = 16;
+constexpr int kNoTile = 0x7fffffff;
 constexpr float kLift = 4.f;       // weights are held times 2^4
 constexpr float kMostSum = 32768.f;   // of 64 weights: each is in fp16's range then
 constexpr float kLog2e = 1.4426950408889634f;
@@ -117,8 +118,9 @@ struct Bars {
     int failed;         // a wait ran out: the outputs from here on are NaN
     int ended;          // no span comes any more, although none said so
     int busy;           // a tile's MMAs are being issued
-    unsigned bad, odd;  // spans with a block-table entry outside the pool, with an fp16 value that is not finite: bit number % 32
+    unsigned bad;       // spans with a block-table entry outside the pool: bit number % 32
     int last_odd[2 * kSpanRing];   // of a span (number % 8): the last quantized token whose value is not finite, or -1
+    int odd_tile[2][2 * kSpanRing];   // the first and the last tile with an fp16 value that is not finite, or kNoTile and -1
     alignas(16) Span spans[kSpanRing];
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
@@ -592,8 +594,8 @@ inline __device__ void plan_spans(const ChunkArgs& a, Bars& b, uint32_t bars, in
             }
             // (the roles are at spans n - 4 to n: a mark of 24 spans ago is nobody's)
             atomicAnd(&b.bad, ~(1u << ((n + 8) % 32)));
-            atomicAnd(&b.odd, ~(1u << ((n + 8) % 32)));
-            b.last_odd[n % (2 * kSpanRing)] = -1;              // (of span n - 8: nobody's)
+            b.last_odd[n % (2 * kSpanRing)] = b.odd_tile[1][n % (2 * kSpanRing)] = -1;    // (of span n - 8: nobody's)
+            b.odd_tile[0][n % (2 * kSpanRing)] = kNoTile;
             b.spans[slot] = o;
             arrive(bars + BAR(span_full) + 8 * (slot));
             ++n;
@@ -707,7 +709,10 @@ __device__ void fill_tiles(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_t 
             } else {
                 odd = value_rows<D>(r, f0, dst, 32 * w, lane);
             }
-            if (odd && lane == 0) atomicOr(&b.odd, reader.mark());
+            if (odd && lane == 0) {
+                atomicMin(&b.odd_tile[0][reader.place()], t);
+                atomicMax(&b.odd_tile[1][reader.place()], t);
+            }
         }
         fence_proxy_async();
         __syncwarp();
@@ -1062,17 +1067,27 @@ __device__ void softmax_rows(const ChunkArgs& a, Bars& b, uint32_t bars, uint32_
         // (all rows are behind the quantized tokens)
         if (const int t = *(volatile int*)&b.last_odd[reader.place()]; t >= 0 && (!a.plan.window || t > p0 + (r >> lgq) - a.plan.window))
             m = l = NAN;
-        if ((*(volatile unsigned*)&b.odd & reader.mark()) && valid) {
-            // a value that is not finite: the row is NaN if it sees one (looked for again, value by value)
+        const int odd0 = *(volatile int*)&b.odd_tile[0][reader.place()], odd1 = *(volatile int*)&b.odd_tile[1][reader.place()];
+        if (__any_sync(kFull, odd0 != kNoTile && odd1 >= 0)) {
+            // fp16 values that are not finite, in these two tiles at least: a row is NaN if it sees one.  The warp looks for them
+            // again, token by token: the first one hides from no row that sees the end of its tile, unless there is a window.
+            constexpr int LPR = D / 8, RPI = 32 / LPR;         // lanes a row, rows an instruction
             const Rows v{reinterpret_cast<const __half*>(a.buf + a.v_resid_off) +
                              ((long long)sp->seq * a.plan.Hkv + sp->head) * a.R * D,
                          a.v + sp->tok0 * a.v_stride[0] + sp->head * a.v_stride[1], a.v_stride[0], sp->n_resid, 0};
             const int hi = p0 + (r >> lgq), lo = a.plan.window ? hi - a.plan.window + 1 : 0;
-            const int last = min(hi, (sp->tile0 + sp->nt) * kTile - 1);
-            for (int t = max(max(lo, sp->tile0 * kTile), sp->n_quant); t <= last && l == l; ++t)
+            const int end = min((a.plan.window ? odd1 : odd0) * kTile + kTile, p0 + (min(r0 + 31, n_rows - 1) >> lgq) + 1);
+            int t = max(max(odd0 * kTile, sp->n_quant), a.plan.window ? p0 + (r0 >> lgq) - a.plan.window + 1 : 0);
+            if (valid && !a.plan.window && hi >= odd0 * kTile + kTile - 1) m = l = NAN;
 #pragma unroll 1
-                for (int j = 0; j < D / 8; ++j)
-                    if (not_finite(ldg_row(v.at(t - sp->n_quant, D) + 8 * j))) m = l = NAN;
+            for (; t < end && __any_sync(kFull, valid && l == l); t += RPI) {
+                const int at = t + lane / LPR;
+                unsigned who = __ballot_sync(kFull, at < end && not_finite(ldg_row(v.at(min(at, end - 1) - sp->n_quant, D) + 8 * (lane % LPR))));
+                for (; who; who &= who - 1) {
+                    const int x = t + (__ffs(who) - 1) / LPR;
+                    if (x >= lo && x <= hi) m = l = NAN;
+                }
+            }
         }
         __syncwarp();
         const bool whole = sp->whole;
@@ -1153,7 +1168,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             mbar_init(&b.span_empty[j], kSpanReaders);
         }
         b.failed = b.ended = b.busy = 0;
-        b.bad = b.odd = 0;
+        b.bad = 0;
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&b.tmem);
