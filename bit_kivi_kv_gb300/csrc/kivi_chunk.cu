@@ -222,9 +222,9 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const __grid_constant_
     }
     top = warp_max(top);
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        w[k] = w[k] == -INFINITY ? 0.f : exp2f(w[k] - top);
-        if (w[k] != 0.f) l += w[k] * lw[k];
+    for (int k = 0; k < 3; ++k) {                              // (an empty partial: -1)
+        w[k] = w[k] == -INFINITY ? -1.f : exp2f(w[k] - top);
+        if (!(w[k] < 0.f)) l += w[k] * lw[k];
     }
     l = warp_sum(l);
     float o[C];
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const __grid_constant_
             const int i = i0 + u;
             if (i >= n) break;
             const float f = __shfl_sync(kFull, i < 32 ? w[0] : i < 64 ? w[1] : w[2], i & 31);
-            if (f == 0.f) continue;                            // (an empty partial's values are not written)
+            if (f < 0.f) continue;                             // (an empty partial's values are not written)
 #pragma unroll
             for (int c = 0; c < C; ++c) o[c] = fmaf(f, x[u][c], o[c]);
         }
@@ -269,6 +269,9 @@ __global__ void __launch_bounds__(128) group_merge_kernel(const __grid_constant_
             for (int c = 0; c < C; ++c) o[c] = o[c] * f + e * v[u][c];
         }
     }
+    // (a token's value that is not finite leaves its channel so, whatever its weight: the row is NaN, as in the wide kernel)
+#pragma unroll
+    for (int c = 0; c < C; ++c) bad |= !(fabsf(o[c]) < INFINITY);
     const float inv = __any_sync(kFull, bad) ? NAN : 1.f / l;
     __half* out = a.out + (long long)(p.tok0 + tok) * a.out_stride[0] + head * a.out_stride[1] + C * lane;
 #pragma unroll

@@ -1,5 +1,5 @@
 """Values that are not finite make the outputs that see them NaN, whole rows of them, and change no other output: in long
-prompts and between the ends of a window."""
+prompts, between the ends of a window, among few rows and in the cache."""
 import pytest
 import torch
 
@@ -52,3 +52,50 @@ def test_a_long_prompt_with_a_late_one(window):
     assert torch.isnan(out[t:t + (window or n)]).all() and torch.isnan(out[5:first]).all()
     if window:
         assert same(out[t + window:], clean[t + window:]) and same(out[:5], clean[:5])
+
+
+@pytest.mark.parametrize("D,bits,G,nq", [(128, 2, 32, 1), (64, 4, 64, 2), (128, 8, 128, 4), (64, 2, 32, 4)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("weight", ["some", "none"])
+def test_few_rows_that_see_one(D, bits, G, nq, value, weight):
+    """A new token's: NaN for every channel from that token on.  A residual one's: for every row.  Whatever weight the
+    token has: with keys far from every query its exponential is 0."""
+    run = ChunkRun(2 * nq, 2, D, bits, G, 2 * G, max_seqs=2, seed=D + bits)
+    n = 16 // nq
+    L = 700
+    K, V, _ = run.draw(L)
+    q, k, v = run.chunk([n])
+    if weight == "none":
+        q = q.abs() + 1
+        k[n // 2] = -3000.0
+        K[:, L - 3] = -3000.0
+    s = run.cache.add(K, V)
+    clean = run.attend([s], [n], (q, k, v), check=False)
+    assert torch.isfinite(clean).all()
+    bad = v.clone()
+    bad[n // 2, 0, 5] = value                                     # kv head 0 alone
+    out = run.attend([s], [n], (q, k, bad), check=False)
+    assert torch.isnan(out[n // 2:, :nq]).all()
+    assert same(out[:n // 2], clean[:n // 2]) and same(out[:, nq:], clean[:, nq:])
+    run.cache.release(s)
+    V[1, L - 3, D - 1] = value                                    # kv head 1, a residual row
+    s = run.cache.add(K, V)
+    out = run.attend([s], [n], (q, k, v), check=False)
+    assert torch.isnan(out[:, nq:]).all() and same(out[:, :nq], clean[:, :nq])
+
+
+@pytest.mark.parametrize("D,bits,G,nq", [(128, 2, 32, 1), (64, 4, 64, 2), (128, 8, 128, 4)])
+def test_few_rows_over_a_quantized_one(D, bits, G, nq):
+    """An infinity in a quantized token's group: its values read back as such, and no row of that head is a number."""
+    run = ChunkRun(2 * nq, 2, D, bits, G, G, max_seqs=2, seed=D + bits)
+    L = 900
+    K, V, _ = run.draw(L)
+    data = run.chunk([16 // nq])
+    s = run.cache.add(K, V)
+    clean = run.attend([s], [16 // nq], data, check=False)
+    run.cache.release(s)
+    V[0, 333, 1] = float("inf")
+    s = run.cache.add(K, V)
+    assert not torch.isfinite(run.cache.read([s], 333, 1)[1][0, 0]).all()
+    out = run.attend([s], [16 // nq], data, check=False)
+    assert torch.isnan(out[:, :nq]).all() and same(out[:, nq:], clean[:, nq:])
