@@ -10,6 +10,7 @@
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
+#include <stdlib.h>
 
 #include <new>
 #include <vector>
@@ -232,6 +233,19 @@ kivi_status check_rows(const char* what, const void* p, const long long* stride)
     if (!aligned(p, 16)) return failf(KIVI_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
     if (stride[0] % 8 || stride[1] % 8) return failf(KIVI_ERR_INVALID_ARG, "%s's strides must be multiples of 16 bytes", what);
     return KIVI_OK;
+}
+
+// Whether some of the rows of D elements that stride leads to, over tokens and heads, share an element.
+bool rows_overlap(const long long* stride, long long tokens, long long heads, long long D) {
+    const long long st = llabs(stride[0]), sh = llabs(stride[1]);
+    if ((tokens > 1 && st < D) || (heads > 1 && sh < D)) return true;
+    if (tokens < 2 || heads < 2 || st >= (heads - 1) * sh + D || sh >= (tokens - 1) * st + D) return false;
+    for (long long h = 1; h < heads; ++h) {                    // rows of heads h apart, and of tokens t or t + 1
+        const long long t = h * sh / st, in = h * sh - t * st;
+        if (t < tokens && in < D) return true;
+        if (t + 1 < tokens && st - in < D) return true;
+    }
+    return false;
 }
 
 // Blocks that a chunk of n tokens completes: as many as a prompt of all the tokens would have quantized
@@ -621,6 +635,7 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
     if ((st = check_rows("k", x->k, x->k_stride)) != KIVI_OK) return st;
     if ((st = check_rows("v", x->v, x->v_stride)) != KIVI_OK) return st;
     if ((st = check_rows("out", x->out, x->out_stride)) != KIVI_OK) return st;
+    if (rows_overlap(x->out_stride, tokens, c->pg.g.Hq, c->pg.g.D)) return failf(KIVI_ERR_INVALID_ARG, "rows of out overlap");
     if (!workspace || !aligned(workspace, 256)) return failf(KIVI_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     const kivi::Geometry& g = c->pg.g;
     const size_t need = chunk_ws_need(g, lens, n);

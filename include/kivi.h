@@ -546,7 +546,7 @@ kivi_status kivi_paged_append(kivi_paged_t cache, const int* seqs, int n, const 
  */
 typedef struct {
     const void *q, *k, *v;    /* fp16: query heads; kv heads */
-    void* out;                /* fp16, as q; must not overlap an input */
+    void* out;                /* fp16, as q; must not overlap an input, nor its rows each other */
     long long q_stride[2], k_stride[2], v_stride[2], out_stride[2];
     float softmax_scale;      /* <= 0: 1/sqrt(D) */
     float cap;                /* > 0: scores are capped; 0: not */
