@@ -256,6 +256,22 @@ long long fresh_blocks(const kivi::Geometry& g, const SeqState& sq, int n) {
     return quant > have ? quant - have : 0;
 }
 
+// The pages that a chunk's append needs, and whether the sequences and the pool have room.
+kivi_status chunk_room(const kivi_paged* c, const int* seqs, const int* lens, int n, long long* pages) {
+    const kivi::Geometry& g = c->pg.g;
+    *pages = 0;
+    for (int i = 0; i < n; ++i) {
+        const SeqState& sq = c->seqs[(size_t)seqs[i]];
+        const long long blocks = fresh_blocks(g, sq, lens[i]);
+        if (sq.n_quant / g.G + blocks > g.NB)
+            return failf(KIVI_ERR_CAPACITY, "sequence %d has no room for %d tokens", seqs[i], lens[i]);
+        *pages += blocks;
+    }
+    if (*pages > (long long)c->free_pages.size())
+        return failf(KIVI_ERR_CAPACITY, "the chunk needs %lld pages, %zu are free", *pages, c->free_pages.size());
+    return KIVI_OK;
+}
+
 // Workspace of a chunk attention call: the wide kernel's partial results, then the gathered rows and the partial
 // results of the groups that the sequences with few rows make (kMaxCallSeqs at most).
 size_t wide_ws_need(const kivi::Geometry& g) {
@@ -757,6 +773,14 @@ kivi_status kivi_paged_chunk_attn(kivi_paged_t c, const int* seqs, const int* le
     return ok();
 }
 
+kivi_status kivi_paged_append_room(kivi_paged_t c, const int* seqs, const int* lens, int n) {
+    if (!c) return failf(KIVI_ERR_INVALID_ARG, "null handle");
+    long long tokens, pages;
+    kivi_status st = check_chunks(c, seqs, lens, n, &tokens);
+    if (st == KIVI_OK) st = chunk_room(c, seqs, lens, n, &pages);
+    return st == KIVI_OK ? ok() : st;
+}
+
 kivi_status kivi_paged_append_chunk(kivi_paged_t c, const int* seqs, const int* lens, int n, const void* k,
                                     const long long* k_stride, const void* v, const long long* v_stride,
                                     kivi_stream_t stream) {
@@ -769,15 +793,8 @@ kivi_status kivi_paged_append_chunk(kivi_paged_t c, const int* seqs, const int* 
     if ((st = check_rows("k", k, k_stride)) != KIVI_OK) return st;
     if ((st = check_rows("v", v, v_stride)) != KIVI_OK) return st;
     const kivi::Geometry& g = c->pg.g;
-    long long pages = 0;
-    for (int i = 0; i < n; ++i) {
-        const long long blocks = fresh_blocks(g, c->seqs[(size_t)seqs[i]], lens[i]);
-        if (c->seqs[(size_t)seqs[i]].n_quant / g.G + blocks > g.NB)
-            return failf(KIVI_ERR_CAPACITY, "sequence %d has no room for %d tokens", seqs[i], lens[i]);
-        pages += blocks;
-    }
-    if (pages > (long long)c->free_pages.size())
-        return failf(KIVI_ERR_CAPACITY, "the chunk needs %lld pages, %zu are free", pages, c->free_pages.size());
+    long long pages;
+    if ((st = chunk_room(c, seqs, lens, n, &pages)) != KIVI_OK) return st;
     const kivi_status sdev = paged_device(c);
     if (sdev != KIVI_OK) return sdev;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

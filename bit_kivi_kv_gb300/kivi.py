@@ -131,6 +131,7 @@ def _load():
         "kivi_paged_chunk_workspace_bytes": (SZ, [pcfgp, P, I]),   # (int lists: ctypes arrays, or packed bytes)
         "kivi_paged_chunk_attn": (I, [P, P, P, I, P, P, SZ, P]),   # a kivi_chunk by reference, or its packed bytes
         "kivi_paged_append_chunk": (I, [P, P, P, I, P, P, P, P, P]),   # strides: addresses, or packed bytes
+        "kivi_paged_append_room": (I, [P, P, P, I]),
         "kivi_paged_fork": (I, [P, IP, I, IP, P]),
         "kivi_paged_truncate": (I, [P, I, LL]),
         "kivi_paged_read": (I, [P, P, I, LL, LL, P, P, P]),
@@ -358,6 +359,10 @@ def kivi_paged_chunk_attn(h: int, seqs, lens, args: kivi_chunk, workspace: int, 
 def kivi_paged_append_chunk(h: int, seqs, lens, k: int, k_stride, v: int, v_stride, stream: int):
     _check(lib.kivi_paged_append_chunk(h, _seq_array(seqs), _seq_array(lens), len(seqs), k, _PAIR.pack(*k_stride), v,
                                        _PAIR.pack(*v_stride), stream))
+
+
+def kivi_paged_append_room(h: int, seqs, lens):
+    _check(lib.kivi_paged_append_room(h, _seq_array(seqs), _seq_array(lens), len(seqs)))
 
 
 def kivi_paged_fork(h: int, seqs, stream: int) -> list:
@@ -867,7 +872,10 @@ class KiviPagedCache:
                                            _current_stream(device) if stream is None else stream.cuda_stream))
 
     def extend(self, seqs, lens, q, k, v, out=None, softmax_scale=0.0, cap=0.0, window=0, slopes=None, stream=None):
-        """chunk_attn, then append_chunk: a piece of a prompt in one go."""
+        """chunk_attn, then append_chunk: a piece of a prompt in one go.  Without room for the
+        tokens neither is done."""
+        n_arr, _ = self._lens(seqs, lens)
+        _check(lib.kivi_paged_append_room(self.handle, _ints(seqs), n_arr, len(seqs)))
         with _torch.cuda.stream(stream):
             out = self.chunk_attn(seqs, lens, q, k, v, out, softmax_scale, cap, window, slopes)
             self.append_chunk(seqs, lens, k, v)

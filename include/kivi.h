@@ -602,6 +602,10 @@ kivi_status kivi_paged_append_chunk(kivi_paged_t cache, const int* seqs, const i
                                     const long long* k_stride, const void* v, const long long* v_stride,
                                     kivi_stream_t stream);
 
+/* What kivi_paged_append_chunk of these lengths would answer about its sequences and
+ * their room, before work whose result needs it (host only; nothing changes). */
+kivi_status kivi_paged_append_room(kivi_paged_t cache, const int* seqs, const int* lens, int n);
+
 /*
  * Branches: for each of the n live sequences seqs[i] (host array; one may be
  * listed several times) a new sequence out[i] that holds the same tokens.  It
