@@ -1,9 +1,10 @@
 """Capped scores of chunk attention at caps of every size: the bound follows the scores, not the cap.
 
-As chunk_harness.ref_attend's, but for the cap's own error.  With y = score / cap, tanh(y) is y times its series up to
-y^6 below 1/4 (the next term is 62/2835 y^8, 2^-21.5; five roundings of 2^-24) and 1 - 2 / (exp(2 y) + 1) above: the
-exponential and the division to 2^-22 each, of numbers up to 1, and y to 2^-23 of itself, are under 2^-21.5 of 1 and
-2^-19.5 of tanh(1/4).  So the capped score is off by 2^-19 of itself.
+As chunk_harness.ref_attend's, but for the cap's own error.  With y = score / cap, 1 - 2 / (exp(2 y) + 1) is off by under
+2^-21.5 of 1 at |y| = 1/4 (the exponential and the division to 2^-22 each, of numbers up to 1, and y to 2^-23 of itself),
+2^-19.5 of tanh(1/4), and 2^-20 of 1 at most.  Caps up to 64 are computed so throughout: 2^-20 of the cap.  With larger ones
+tanh(y) is y times its series up to y^6 below 1/4 (the next term is 62/2835 y^8, 2^-21.5; five roundings of 2^-24): the
+capped score is off by 2^-19 of itself.
 """
 import math
 
@@ -30,7 +31,7 @@ def reference(keys, vals, n_quant, q, past, scale, cap, window=0, slope=0.0):
     if window:
         hidden = hidden | (t <= at - window)
     size = (x.abs() + bias.abs()).masked_fill(hidden, 0.0)
-    d = 2.0 ** -19 * x.abs()
+    d = 2.0 ** -19 * x.abs() + (2.0 ** -20 * cap if cap <= 64 else 0.0)
     x = (x + bias).masked_fill(hidden, -math.inf)
     top = x.amax(1, keepdim=True)
     w = torch.softmax(x, dim=1)
@@ -65,7 +66,7 @@ def check(run, seqs, lens, data, cap, scale=0.0, window=0, slopes=None):
 
 
 # (as the kernel's argument, a float)
-CAPS = [1e-44, 1e-38, 1e-3, 0.25, 4.0, 30.0, 1e3, 1e5, 1e6, 1e8, 1e20, 1e30, 3e38]
+CAPS = [1e-44, 1e-38, 1e-3, 0.25, 4.0, 30.0, 64.0, 65.0, 1e3, 1e5, 1e6, 1e8, 1e20, 1e30, 3e38]
 
 
 @pytest.mark.parametrize("cap", [torch.tensor(c).item() for c in CAPS])
