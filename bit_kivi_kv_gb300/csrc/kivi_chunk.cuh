@@ -238,6 +238,16 @@ cudaError_t launch_chunk_merge(const ChunkArgs& a, int D, cudaStream_t st);
 // cached tokens: up to kGroupRows rows of a kv head are taken as the query heads
 // of a single-token call, whose decode kernel reads the cache for them; the merge adds
 // the new tokens.  A sequence of more rows makes several groups, each reads the cache again.
+// By groups and by the wide kernel (us a call; 2 bits but where said):
+//   rows of a kv head                            4           8           12          16          24
+//   8 sequences of 512-7680, 32 heads            51 / 102    87 / 102    123 / 103   159 / 103   236 / 104
+//   the same with 4 bits                         58 / 118    93 / 119    131 / 119   171 / 119   253 / 119
+//   the same, 32 heads over 8                    20 / 35     31 / 35     39 / 36     48 / 36     65 / 36
+//   16 sequences to 15872, 32 over 8, 4 bits     44 / 116    69 / 117    95 / 117    119 / 117   172 / 117
+//   64 sequences of 1000, 32 over 8              32 / 65     56 / 65     -           99 / 65     -
+// To 8 rows groups are faster; to 16 they cost up to half as much again and keep the decode kernel's accuracy (exact
+// dequantized operands), which a verified proposal then shares with the token that is decoded alone; beyond, they would
+// cost twice and more.
 constexpr int kGroupRows = 4, kFewRows = 16;
 struct ChunkGroup {
     int tok0;           // the sequence's first new token in the packed inputs

@@ -35,13 +35,19 @@
 // Rows that are still fp16 (residual and chunk) are copied; values of tiles
 // that hold nothing else stay token by token (the MMA takes both orders).
 //
-// Bound by the warps' instructions: a tile of 128 keys by 256 rows takes some 4400 cycles (2650 warp instructions a
-// scheduler), its 32 MMAs 2050 of them.  512 new tokens of each of 8 sequences over 4096 (32 heads of 128, 2 bits):
-// 328 us, 889 TFLOP/s; a prompt of 8192 tokens: 533 us, 1030.
+// Bound by the chain of a tile's steps (S, the walk over its logits, the four warps' meeting, P V and the next S), of which
+// two tiles overlap: no pipe is full.  A tile of 128 keys by 256 rows takes some 4400 cycles, its 32 MMAs 2050 of them, the
+// instructions 2650 issue slots a scheduler; over 512 new tokens of each of 8 sequences over 4096 (32 heads of 128, 2
+// bits) ncu shows issue active 45%, the tensor pipe 40%, exponentials 21%: 330 us, 883 TFLOP/s; a prompt of 8192
+// tokens, with nothing to dequantize, 538 us, 1020.
 //
 // Roundings: keys and values to fp16 (half a step of 2^-10), probabilities to
 // fp16, scaled so that 2^4 at least stands for the row's largest: what falls below fp16's
-// range is under 2^-29 of it.  Everything else is fp32.  The reference is the
+// range is under 2^-29 of it.  Everything else is fp32.  The keys' rounding is what shows: outputs are off by some 1e-3
+// of their size where channels are outliers, by 2.4e-4 if keys alone were exact, 2e-4 being the outputs' own rounding.  Exact
+// keys are a second operand (what is left of each number) in the same product: S twice, 64 KB more of shared memory than
+// there is beside two stages.
+// The reference is the
 // maximum of some tile so far, raised (and the sums in tensor memory scaled) when the
 // weights of 64 keys reach 2^15 together, which leaves the result the same.
 //

@@ -836,7 +836,10 @@ class KiviPagedCache:
         each other, any strides with dense channels; returns [T, Hq, D].  cap: scores
         become cap * tanh(score / cap); slopes fp32 [Hq]: a bias of slope * (t - position);
         window: tokens that a query sees, itself included (0: all).  The new tokens are
-        not appended (append_chunk)."""
+        not appended (append_chunk).  Sequences of at most 16 rows (new tokens x query heads
+        per kv head) without cap, slopes or a window that cuts have the accuracy of
+        append_decode; the others read dequantized keys and values rounded to fp16, which
+        moves outputs by some 1e-3 of their size."""
         (hq, hkv, d), device = self._heads, _on(self)
         n_arr, tokens = self._lens(seqs, lens)
         qs = self._chunk(q, "q", tokens, hq, device)
